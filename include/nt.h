@@ -363,6 +363,159 @@ nt_status nt_attention(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, in
                        const float* dev_q, const void* dev_k, const void* dev_v, float* dev_out, void* dev_workspace,
                        size_t workspace_bytes, void* stream);
 
+/* --------------------------------------------------- paged 4-bit K/V cache -- */
+
+/* A K/V cache of several sequences at 4.5 bits per value, cut into pages that
+ * sequences can share (the branches of a speculative draft, several samples of
+ * one prompt), with the attention that reads it and the operators on its pages.
+ * It stands beside the model's own f16 cache; the pages have no counterpart.
+ *
+ * Values.  Every 32 consecutive dimensions of a position and kv head are a Q4_0
+ * block, value d (q - 8), whose scale has six mantissa bits:
+ *   A = max |x|, h = the bits of f16(A / 7) (both roundings to nearest),
+ *   d = the f16 of bits (h + 8) & 0xfff0,
+ *   q = min(max(round(x / d) + 8, 0), 15), halves away from zero; 8 where d = 0.
+ * A block that holds a NaN or an infinity, or whose d is above 896, is stored as
+ * d = NaN and reads as NaN.
+ * Six mantissa bits make every value, and the products the attention forms on
+ * the way to it, exact in f16.
+ *
+ * Pages.  A page holds page_len positions of one layer: for each kv head its
+ * page_len / 16 chunks of 16 positions, 18 head_dim bytes each.  With NG =
+ * head_dim / 32, a chunk is
+ *   K codes  [i 2][n 8][tg 4][j NG] words: position 8i + n, dimensions 32j + 8tg + 0..7
+ *   V codes  [r 2][gi 8][tg 4][j NG] words: low half position 8r + 2tg, high half
+ *            the next one, each of dimensions 32j + 4gi + 0..3
+ *   K scales [position 16][j NG] f16
+ *   V scales [r 2][tg 4][j NG][2] f16: positions 8r + 2tg and the next one
+ * with the lowest dimension in the lowest bits of a word or half.
+ *
+ * The caller owns every buffer.  page p of layer l starts at pool +
+ * (l * n_pages + p) * page bytes.  table[s][j] is the page of positions
+ * [j page_len, (j + 1) page_len) of sequence s in every layer, for j <
+ * ceil(len[s] / page_len), and -1 beyond; refs[p] counts the table entries that
+ * name page p (0: free).  A new cache has table -1, len 0, refs 0, error 0.
+ *
+ * What the device finds wrong (lists, tables and lengths live there) is ORed
+ * into *error as NT_KV4_* bits and never cleared by the library; each function
+ * says what it leaves undone.  No such value makes a kernel read or write out of
+ * the cache's bounds.  Calls on one cache, and calls that share a workspace,
+ * must not overlap on the GPU, but for reads (nt_kv4_read, nt_attention_kv4 with
+ * a workspace each).  All calls are asynchronous on stream, allocate nothing, can
+ * be captured into a graph, and give the same result in every run.
+ * Host checks, NT_E_INVAL: NULL or misaligned pointers (pool, workspaces, k, v, q
+ * and out 16 bytes; all int32 arrays 4), sizes outside the ranges below, a
+ * workspace too small, buffers that overlap.  NT_E_UNSUPPORTED: head_dim other
+ * than 64 or 128. */
+typedef struct {
+  int32_t n_layers;     /* 1..65535                                                      */
+  int32_t n_kv_heads;   /* 1..65535                                                      */
+  int32_t head_dim;     /* 64 or 128                                                     */
+  int32_t page_len;     /* positions per page: a multiple of 16, 16..256                 */
+  int32_t n_pages;      /* pages of each layer, at least 1                               */
+  int32_t max_seqs;     /* rows of the table, 1..65536                                   */
+  int32_t max_pages;    /* columns of the table; max_pages * page_len at most 2^31 - 256 */
+  void* pool;           /* dev: nt_kv4_pool_bytes() bytes                                */
+  int32_t* table;       /* dev [max_seqs][max_pages]                                     */
+  int32_t* len;         /* dev [max_seqs]: positions held                                */
+  int32_t* refs;        /* dev [n_pages]                                                 */
+  uint32_t* error;      /* dev [1]: NT_KV4_* bits                                        */
+} nt_kv4_cache;
+
+enum {
+  NT_KV4_BAD_SEQ = 1,   /* a sequence out of range, listed twice, or not empty where it has to be */
+  NT_KV4_BAD_LEN = 2,   /* a length, count or row range that does not fit                */
+  NT_KV4_BAD_PAGE = 4,  /* a page index out of range, or a reference count that contradicts the call */
+  NT_KV4_NO_PAGE = 8,   /* too few free pages                                            */
+  NT_KV4_TIMEOUT = 16   /* a kernel gave up waiting for its own copies                   */
+};
+
+/* Bytes of one page of one layer, and of the whole pool (either nullable). */
+nt_status nt_kv4_pool_bytes(const nt_kv4_cache* c, size_t* page_bytes, size_t* pool_bytes);
+
+/* Bytes of a workspace that serves every call below on this cache with at most n
+ * listed sequences, and nt_attention_kv4 with n_heads query heads.  Its contents
+ * on entry do not matter. */
+nt_status nt_kv4_workspace_bytes(const nt_kv4_cache* c, int32_t n_heads, int32_t n, size_t* bytes);
+
+/* Room for dev_count[i] >= 0 more positions of each listed sequence dev_seq[i], i < n
+ * (n <= max_seqs; dev_seq NULL: sequences 0..n-1): len grows by the count, and the
+ * pages that it needs beyond those held are the lowest free ones, in list order.
+ * Where the last page held is partly filled and shared (refs > 1), the sequence
+ * gets a copy of it in a page of its own.  The new positions' contents are
+ * whatever the pages held: nt_kv4_append writes them.  If any entry is invalid or
+ * the free pages do not suffice, the call changes nothing but *error. */
+nt_status nt_kv4_extend(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_count,
+                        void* dev_workspace, size_t workspace_bytes, void* stream);
+
+/* Sequence dev_dst[i], empty before, becomes the first dev_keep[i] positions of
+ * dev_src[i] (dev_keep NULL: all of them): the full pages are shared, a partly
+ * filled last one is copied into the lowest free page.  A source may be listed
+ * several times, a destination once; a destination may be no source.  If any entry
+ * is invalid or the free pages do not suffice, the call changes nothing but
+ * *error. */
+nt_status nt_kv4_fork(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
+                      const int32_t* dev_keep, void* dev_workspace, size_t workspace_bytes, void* stream);
+
+/* Listed sequences (dev_seq NULL: 0..n-1) keep their first dev_keep[i] positions (dev_keep NULL: none): the
+ * pages behind are given back (refs one lower, the table entry -1).  An invalid
+ * entry (keep outside [0, len], a sequence listed before) is passed over. */
+nt_status nt_kv4_free(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_keep, void* stream);
+
+/* Page dev_dst[i] becomes a copy of page dev_src[i] in every layer (n <= n_pages);
+ * tables and counts stay.  A pair is passed over (NT_KV4_BAD_PAGE) where a page is out of
+ * range, its destination is one of an earlier pair, or its source is the
+ * destination of another. */
+nt_status nt_kv4_copy_pages(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
+                            void* stream);
+
+/* Moves the pages in use (refs > 0), L of them, below page L, so that the pages
+ * from L on are free: the k-th free page below L takes the k-th page in use from
+ * L on, in every layer.  dev_table_out [max_seqs][max_pages] and dev_refs_out
+ * [n_pages] receive the table and counts that go with it; each is either the
+ * cache's own array or one that does not overlap it (the cache then still
+ * describes the state before: moved pages keep their old bytes until they are
+ * taken).  dev_live: L.  Table entries out of range are copied as they are. */
+nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t* dev_refs_out, int32_t* dev_live,
+                         void* dev_workspace, size_t workspace_bytes, void* stream);
+
+/* Quantizes rows of keys (already rotated) and values into layer `layer`: rows
+ * [dev_begin[i], dev_begin[i+1]) belong to the listed sequence dev_seq[i] (NULL:
+ * sequence i) and become its last positions, the last row position len - 1.
+ * dev_begin [n + 1] int32, ascending; NULL: one row each.  n_rows: rows of k and v;
+ * those outside [dev_begin[0], dev_begin[n]) are not read.  Row r of kv head g
+ * starts at element r * row_stride + g * head_stride of dev_k and of dev_v (f32 or f16 by
+ * `type`: NT_F32, NT_F16; both strides multiples of 16 bytes), head_dim elements
+ * each: a projection's [row][kv head][dim] as well as an f16 cache's [kv
+ * head][position][dim].  A row is passed over where its sequence or position is
+ * out of range, or its page is not held by this sequence alone (refs other than 1).
+ * A sequence listed twice is flagged; which of its rows are stored is not defined. */
+nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
+                        const int32_t* dev_begin, int32_t n_rows, nt_qtype type, const void* dev_k, const void* dev_v,
+                        int64_t row_stride, int64_t head_stride, void* stream);
+
+/* The inverse: the last positions of the listed sequences, as nt_kv4_append would
+ * write them, dequantized into dev_k and dev_v (f32 exactly; f16 rounded to nearest,
+ * which is exact).  A sequence may be listed several times.  Rows passed over, and
+ * rows outside [dev_begin[0], dev_begin[n]), are left as they were. */
+nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
+                      const int32_t* dev_begin, int32_t n_rows, nt_qtype type, void* dev_k, void* dev_v,
+                      int64_t row_stride, int64_t head_stride, void* stream);
+
+/* nt_attention over the paged cache: for the listed sequences (dev_seq NULL: 0..n-1;
+ * a sequence may be listed several times) and every query head j, kv head g = j /
+ * (n_heads / n_kv_heads),
+ *   out_ij = sum_t softmax_t(q_ij . K[g][t] / sqrt(head_dim)) V[g][t],  t in [0, len),
+ * and zeros where len = 0.  dev_q and dev_out: fp32, sequence i at element i * q_stride
+ * and i * out_stride (multiples of 4, at least n_heads * head_dim), [n_heads][head_dim] each.
+ * The statistics and sums are fp32; K and V enter exactly, q and the softmax
+ * weights with about 22 bits.  A sequence out of range, a length that the table
+ * cannot hold and a page index out of range give NaN in that sequence's outputs.
+ * NT_E_UNSUPPORTED: n_heads / n_kv_heads other than 1, 2, 4, 8 or 16. */
+nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
+                           const float* dev_q, int64_t q_stride, float* dev_out, int64_t out_stride,
+                           void* dev_workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------ allocation-free variant -- */
 
 /* y = W x as nt_gemv_q, then the index of the largest y (ties to the lowest

@@ -1,0 +1,763 @@
+// nt_kv4.cu -- the paged 4-bit K/V cache: rows into and out of it, and the
+// operators on its pages (include/nt.h documents each).
+#include "nt_kv4.cuh"
+
+namespace nt {
+
+nt_status kv4_check(const nt_kv4_cache* c, const char* who, bool pointers, Kv4* k) {
+  auto bad = [&](const char* what) { return fail(NT_E_INVAL, std::string(who) + ": " + what); };
+  if (!c) return bad("NULL cache");
+  if (c->n_layers < 1 || c->n_layers > 65535) return bad("n_layers outside [1, 65535]");
+  if (c->n_kv_heads < 1 || c->n_kv_heads > 65535) return bad("n_kv_heads outside [1, 65535]");
+  if (c->page_len < 16 || c->page_len > 256 || c->page_len % 16) return bad("page_len must be a multiple of 16, 16..256");
+  if (c->n_pages < 1) return bad("n_pages must be positive");
+  if (c->max_seqs < 1 || c->max_seqs > kKv4MaxSeqs) return bad("max_seqs outside [1, 65536]");
+  if (c->max_pages < 1 || int64_t(c->max_pages) * c->page_len > 0x7fffffffLL - 255)
+    return bad("max_pages must be positive and max_pages * page_len at most 2^31 - 256");
+  if (c->head_dim != 64 && c->head_dim != 128)
+    return fail(NT_E_UNSUPPORTED, std::string(who) + ": head_dim must be 64 or 128");
+  *k = Kv4{c->n_layers, c->n_kv_heads, c->head_dim, c->page_len, c->n_pages, c->max_seqs, c->max_pages,
+           static_cast<uint8_t*>(c->pool), c->table, c->len, c->refs, c->error};
+  // every byte offset into the pool fits 62 bits
+  if (double(k->page_bytes()) * c->n_pages * c->n_layers > 4e18) return bad("the pool is too large");
+  if (pointers) {
+    if (!kv4_aligned(c->pool, 16)) return bad("pool is NULL or not 16-byte aligned");
+    if (!kv4_aligned(c->table, 4) || !kv4_aligned(c->len, 4) || !kv4_aligned(c->refs, 4) || !kv4_aligned(c->error, 4))
+      return bad("table, len, refs or error is NULL or not 4-byte aligned");
+  }
+  return NT_OK;
+}
+
+bool kv4_meets_cache(const Kv4& k, const void* p, int64_t bytes) {
+  return kv4_overlap(p, bytes, k.pool, k.page_bytes() * k.n_pages * k.n_layers) ||
+         kv4_overlap(p, bytes, k.table, int64_t(k.max_seqs) * k.max_pages * 4) ||
+         kv4_overlap(p, bytes, k.len, int64_t(k.max_seqs) * 4) || kv4_overlap(p, bytes, k.refs, int64_t(k.n_pages) * 4) ||
+         kv4_overlap(p, bytes, k.error, 4);
+}
+
+// ------------------------------------------------------------ append, read --
+
+struct Kv4Rows {
+  int32_t layer, n, n_rows;
+  const int32_t* seq;
+  const int32_t* begin;
+  int64_t row_stride, head_stride;
+};
+
+// The place of row r: its page (-1: the row is passed over) and position within it.
+__device__ __forceinline__ int kv4_place(const Kv4& c, const Kv4Rows& a, int r, bool append, int* at) {
+  int i = r, behind = 1;   // entry, and rows from this one to the entry's end
+  if (a.begin) {
+    if (r < a.begin[0] || r >= a.begin[a.n]) return -1;
+    int lo = 0, hi = a.n;  // begin[lo] <= r < begin[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.begin[mid] <= r) lo = mid; else hi = mid;
+    }
+    i = lo;
+    behind = a.begin[i + 1] - r;
+  } else if (r >= a.n) {
+    return -1;
+  }
+  const int s = a.seq ? a.seq[i] : i;
+  if (s < 0 || s >= c.max_seqs) { kv4_flag(c, NT_KV4_BAD_SEQ); return -1; }
+  const int n = c.len[s], pos = n - behind;
+  if (n > c.capacity() || pos < 0 || behind < 1) { kv4_flag(c, NT_KV4_BAD_LEN); return -1; }
+  const int page = c.table[int64_t(s) * c.max_pages + pos / c.page_len];
+  if (page < 0 || page >= c.n_pages || (append && c.refs[page] != 1)) { kv4_flag(c, NT_KV4_BAD_PAGE); return -1; }
+  *at = pos % c.page_len;
+  return page;
+}
+
+template <class T> __device__ __forceinline__ void kv4_load8(const T* p, float (&x)[8]);
+template <> __device__ __forceinline__ void kv4_load8<float>(const float* p, float (&x)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+template <> __device__ __forceinline__ void kv4_load8<__half>(const __half* p, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    x[2 * i] = f.x; x[2 * i + 1] = f.y;
+  }
+}
+template <class T> __device__ __forceinline__ void kv4_store8(T* p, const float (&x)[8]);
+template <> __device__ __forceinline__ void kv4_store8<float>(float* p, const float (&x)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+template <> __device__ __forceinline__ void kv4_store8<__half>(__half* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Codes of this lane's 8 values of a 32-value block (4 neighbouring lanes hold
+// it), the first in the lowest bits, and the block's scale bits.  All 32 lanes call it.
+__device__ __forceinline__ uint32_t kv4_quantize(const float (&x)[8], uint32_t* scale) {
+  float top = 0.f;
+  bool fin = true;
+#pragma unroll
+  for (int e = 0; e < 8; e++) {
+    top = fmaxf(top, fabsf(x[e]));
+    fin = fin && fabsf(x[e]) < INFINITY;   // false for NaN too
+  }
+  if (!fin) top = INFINITY;
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  uint32_t h = (uint32_t(__half_as_ushort(__float2half_rn(__fdiv_rn(top, 7.0f)))) + 8u) & 0xfff0u;
+  const float d = __half2float(__ushort_as_half(uint16_t(h)));
+  uint32_t w = 0x88888888u;
+  if (h > 0x6300u) {   // above 896, infinite or NaN
+    h = 0x7e00u;
+  } else if (h != 0u) {
+    w = 0u;
+#pragma unroll
+    for (int e = 0; e < 8; e++) {
+      const int q = int(roundf(__fdiv_rn(x[e], d))) + 8;
+      w |= uint32_t(q < 0 ? 0 : (q > 15 ? 15 : q)) << (4 * e);
+    }
+  }
+  *scale = h;
+  return w;
+}
+
+// One lane per 8 dimensions of a row of K or V.  A row of HD/8 lanes holds whole
+// blocks of 4 lanes; the grid-stride loop keeps warps together for the shuffles.
+template <int HD, class T>
+__global__ void __launch_bounds__(256) k_kv4_append(Kv4 c, Kv4Rows a, const T* k, const T* v) {
+  using L = Kv4Chunk<HD>;
+  constexpr int LPR = HD / 8;
+  const int64_t total = int64_t(a.n_rows) * c.n_kv * 2 * LPR;
+  const int lane = threadIdx.x & 31;
+  for (int64_t w0 = int64_t(blockIdx.x) * 256 + (threadIdx.x & ~31); w0 < total; w0 += int64_t(gridDim.x) * 256) {
+    const int64_t u = w0 + lane;
+    const bool live = u < total;
+    const int part = int(u % LPR), g = int(u / (LPR * 2) % c.n_kv);
+    const bool is_v = (u / LPR) & 1;
+    const int r = int(u / (int64_t(LPR) * 2 * c.n_kv));
+    int at = 0;
+    const int page = live ? kv4_place(c, a, r, true, &at) : -1;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (page >= 0) kv4_load8((is_v ? v : k) + int64_t(r) * a.row_stride + int64_t(g) * a.head_stride + part * 8, x);
+    uint32_t scale;
+    const uint32_t w = kv4_quantize(x, &scale);
+    if (page < 0) continue;
+    uint8_t* ch = c.chunk(a.layer, page, g, at);
+    const int p = at % kKv4Chunk, j = part >> 2, tg = part & 3;
+    if (is_v) {
+      *reinterpret_cast<uint16_t*>(ch + L::v_half(p, 2 * tg, j)) = uint16_t(w);
+      *reinterpret_cast<uint16_t*>(ch + L::v_half(p, 2 * tg + 1, j)) = uint16_t(w >> 16);
+      if (tg == 0) *reinterpret_cast<uint16_t*>(ch + L::v_scale(p, j)) = uint16_t(scale);
+    } else {
+      *reinterpret_cast<uint32_t*>(ch + L::k_word(p, tg, j)) = w;
+      if (tg == 0) *reinterpret_cast<uint16_t*>(ch + L::k_scale(p, j)) = uint16_t(scale);
+    }
+  }
+}
+
+// Flags sequences listed twice.
+__global__ void __launch_bounds__(1024) k_kv4_listed_twice(Kv4 c, int n, const int32_t* seq) {
+  __shared__ uint32_t set[kKv4MaxSeqs / 32];
+  for (int i = threadIdx.x; i < kKv4MaxSeqs / 32; i += blockDim.x) set[i] = 0u;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const int s = seq[i];
+    if (s < 0 || s >= c.max_seqs) continue;
+    if (atomicOr(&set[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u) kv4_flag(c, NT_KV4_BAD_SEQ);
+  }
+}
+
+template <int HD, class T>
+__global__ void __launch_bounds__(256) k_kv4_read(Kv4 c, Kv4Rows a, T* k, T* v) {
+  using L = Kv4Chunk<HD>;
+  constexpr int LPR = HD / 8;
+  const int64_t total = int64_t(a.n_rows) * c.n_kv * 2 * LPR;
+  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < total; u += int64_t(gridDim.x) * 256) {
+    const int part = int(u % LPR), g = int(u / (LPR * 2) % c.n_kv);
+    const bool is_v = (u / LPR) & 1;
+    const int r = int(u / (int64_t(LPR) * 2 * c.n_kv));
+    int at = 0;
+    const int page = kv4_place(c, a, r, false, &at);
+    if (page < 0) continue;
+    const uint8_t* ch = c.chunk(a.layer, page, g, at);
+    const int p = at % kKv4Chunk, j = part >> 2, tg = part & 3;
+    uint32_t w;
+    if (is_v)
+      w = uint32_t(*reinterpret_cast<const uint16_t*>(ch + L::v_half(p, 2 * tg, j))) |
+          uint32_t(*reinterpret_cast<const uint16_t*>(ch + L::v_half(p, 2 * tg + 1, j))) << 16;
+    else
+      w = *reinterpret_cast<const uint32_t*>(ch + L::k_word(p, tg, j));
+    const float d = __half2float(*reinterpret_cast<const __half*>(ch + (is_v ? L::v_scale(p, j) : L::k_scale(p, j))));
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) x[e] = __fmul_rn(d, float(int((w >> (4 * e)) & 15u) - 8));
+    kv4_store8((is_v ? v : k) + int64_t(r) * a.row_stride + int64_t(g) * a.head_stride + part * 8, x);
+  }
+}
+
+// ------------------------------------------------------------ page operators --
+
+// Exclusive prefix sum of one value per thread of a 1024-thread CTA; *total: the sum.
+__device__ __forceinline__ int64_t kv4_scan(int64_t x, int64_t* total) {
+  __shared__ int64_t part[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += y;
+  }
+  __syncthreads();   // the previous call's sums have been read
+  if (lane == 31) part[warp] = s;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+  for (int w = 0; w < 32; w++) {
+    if (w < warp) before += part[w];
+    all += part[w];
+  }
+  *total = all;
+  return before + s - x;
+}
+
+__device__ __forceinline__ int kv4_pages(int len, int page_len) { return int((int64_t(len) + page_len - 1) / page_len); }
+
+struct Kv4PlanArgs {
+  int32_t n;
+  const int32_t* a;   // extend: sequences (nullable); fork: sources
+  const int32_t* b;   // extend: counts; fork: destinations
+  const int32_t* keep;
+  int32_t* go;
+  int64_t* off;
+  int2* pair;
+  int32_t* free;
+};
+
+// The plan of an extend (FORK = false) or a fork, by one CTA: checks every entry,
+// counts the pages it takes, finds that many free pages, the lowest first, and
+// (extend) writes the table, counts and lengths.  Nothing is changed unless every
+// entry is valid and the free pages suffice.  The pages to copy go to `pair`.
+template <bool FORK>
+__global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
+  __shared__ uint32_t set[kKv4MaxSeqs / 32];                  // sequences listed (fork: destinations)
+  __shared__ uint32_t s_bad;
+  const int t = threadIdx.x;
+  for (int i = t; i < kKv4MaxSeqs / 32; i += 1024) set[i] = 0u;
+  if (t == 0) s_bad = 0u;
+  __syncthreads();
+  const int32_t* listed = FORK ? a.b : a.a;
+  for (int i = t; i < a.n; i += 1024) {
+    const int s = listed ? listed[i] : i;
+    if (s < 0 || s >= c.max_seqs || (atomicOr(&set[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u))
+      atomicOr(&s_bad, NT_KV4_BAD_SEQ);
+  }
+  __syncthreads();
+  int64_t run = 0;   // pages taken by the entries before
+  for (int i0 = 0; i0 < a.n; i0 += 1024) {
+    const int i = i0 + t;
+    int64_t need = 0;
+    int2 pair = make_int2(-1, -1);
+    uint32_t bad = 0;
+    if (i < a.n) {
+      const int s = a.a ? a.a[i] : i;   // the sequence read from
+      if (s < 0 || s >= c.max_seqs) {
+        bad = NT_KV4_BAD_SEQ;
+      } else {
+        const int n = c.len[s], held = n < 0 || n > c.capacity() ? 0 : kv4_pages(n, c.page_len);
+        if (n < 0 || n > c.capacity()) bad |= NT_KV4_BAD_LEN;
+        if (FORK) {
+          const int keep = a.keep ? a.keep[i] : n, d = a.b[i];
+          if (set[s >> 5] >> (s & 31) & 1u) bad |= NT_KV4_BAD_SEQ;
+          if (d >= 0 && d < c.max_seqs && c.len[d] != 0) bad |= NT_KV4_BAD_SEQ;
+          if (keep < 0 || keep > n) bad |= NT_KV4_BAD_LEN;
+          if (!bad && keep % c.page_len) {
+            pair.x = c.table[int64_t(s) * c.max_pages + keep / c.page_len];
+            if (pair.x < 0 || pair.x >= c.n_pages) bad |= NT_KV4_BAD_PAGE;
+            need = 1;
+          }
+        } else {
+          const int count = a.b[i];
+          if (count < 0 || count > c.capacity() - n) bad |= NT_KV4_BAD_LEN;
+          if (!bad && count > 0) {
+            need = kv4_pages(n + count, c.page_len) - held;
+            if (n % c.page_len) {
+              const int p = c.table[int64_t(s) * c.max_pages + n / c.page_len];
+              if (p < 0 || p >= c.n_pages || c.refs[p] < 1) bad |= NT_KV4_BAD_PAGE;
+              else if (c.refs[p] > 1) { pair.x = p; need++; }
+            }
+          }
+        }
+      }
+      if (bad) atomicOr(&s_bad, bad);
+      a.pair[i] = pair;
+    }
+    int64_t all;
+    const int64_t before = kv4_scan(need, &all);
+    if (i < a.n) a.off[i] = run + before;
+    run += all;
+  }
+  if (t == 0) a.off[a.n] = run;
+  // the lowest `run` free pages
+  int64_t found = 0;
+  for (int64_t p0 = 0; p0 < c.n_pages && found < run; p0 += 1024) {
+    const int64_t p = p0 + t;
+    const bool is_free = p < c.n_pages && c.refs[p] == 0;
+    int64_t all;
+    const int64_t before = kv4_scan(is_free ? 1 : 0, &all);
+    if (is_free && found + before < run) a.free[found + before] = int32_t(p);
+    found += all;
+  }
+  __syncthreads();
+  if (found < run && t == 0 && !s_bad) s_bad = NT_KV4_NO_PAGE;
+  __syncthreads();
+  const uint32_t bad = s_bad;
+  if (t == 0) {
+    a.go[0] = bad == 0u;
+    a.go[1] = bad == 0u ? a.n : 0;
+    if (bad) kv4_flag(c, bad);
+  }
+  if (bad) return;
+  for (int64_t f = t; f < run; f += 1024) {   // free page f belongs to the entry with off[lo] <= f < off[lo + 1]
+    int lo = 0, hi = a.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.off[mid] <= f) lo = mid; else hi = mid;
+    }
+    const int page = a.free[f], kth = int(f - a.off[lo]);
+    c.refs[page] = 1;
+    const bool copied = a.pair[lo].x >= 0;
+    if (copied && kth == 0) a.pair[lo].y = page;
+    if (!FORK) {
+      const int s = a.a ? a.a[lo] : lo, n = c.len[s];
+      const int slot = copied ? n / c.page_len + kth : kv4_pages(n, c.page_len) + kth;
+      int32_t* e = &c.table[int64_t(s) * c.max_pages + slot];
+      if (copied && kth == 0) atomicSub(&c.refs[*e], 1);
+      *e = page;
+    }
+  }
+  __syncthreads();
+  if (!FORK)
+    for (int i = t; i < a.n; i += 1024) c.len[a.a ? a.a[i] : i] += a.b[i];
+}
+
+// Copies pages in every layer: item = (pair, layer), 16 bytes a thread.
+__device__ __forceinline__ void kv4_copy_page(const Kv4& c, int src, int dst, int layer) {
+  const int64_t pb = c.page_bytes(), n16 = pb / 16;
+  const uint4* from = reinterpret_cast<const uint4*>(c.pool + (int64_t(layer) * c.n_pages + src) * pb);
+  uint4* to = reinterpret_cast<uint4*>(c.pool + (int64_t(layer) * c.n_pages + dst) * pb);
+  for (int64_t i = threadIdx.x; i < n16; i += blockDim.x) to[i] = from[i];
+}
+
+// The pairs of a plan; FORK: also the destinations' tables, counts and lengths.
+template <bool FORK>
+__global__ void __launch_bounds__(256) k_kv4_apply(Kv4 c, Kv4PlanArgs a) {
+  if (!a.go[0]) return;
+  const int64_t items = int64_t(a.n) * c.n_layers;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = int(it % a.n), layer = int(it / a.n);
+    const int2 pair = a.pair[i];
+    if (pair.x >= 0) kv4_copy_page(c, pair.x, pair.y, layer);
+    if (FORK && layer == 0) {
+      const int s = a.a[i], d = a.b[i], keep = a.keep ? a.keep[i] : c.len[s], full = keep / c.page_len;
+      const int32_t* from = c.table + int64_t(s) * c.max_pages;
+      int32_t* to = c.table + int64_t(d) * c.max_pages;
+      for (int j = threadIdx.x; j < full; j += blockDim.x) {
+        const int p = from[j];
+        to[j] = p;
+        if (p >= 0 && p < c.n_pages) atomicAdd(&c.refs[p], 1);
+        else kv4_flag(c, NT_KV4_BAD_PAGE);
+      }
+      if (threadIdx.x == 0) {
+        if (pair.x >= 0) to[full] = pair.y;
+        c.len[d] = keep;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) k_kv4_free(Kv4 c, int n, const int32_t* seq, const int32_t* keep) {
+  __shared__ int s_again;
+  for (int i = blockIdx.x; i < n; i += gridDim.x) {
+    const int s = seq ? seq[i] : i;
+    __syncthreads();
+    if (threadIdx.x == 0) s_again = 0;
+    __syncthreads();
+    if (seq)
+      for (int e = threadIdx.x; e < i; e += blockDim.x)
+        if (seq[e] == s) s_again = 1;
+    __syncthreads();
+    if (s < 0 || s >= c.max_seqs || s_again) {
+      if (threadIdx.x == 0) kv4_flag(c, NT_KV4_BAD_SEQ);
+      continue;
+    }
+    const int len = c.len[s], left = keep ? keep[i] : 0;
+    if (len < 0 || len > c.capacity() || left < 0 || left > len) {
+      if (threadIdx.x == 0) kv4_flag(c, NT_KV4_BAD_LEN);
+      continue;
+    }
+    int32_t* row = c.table + int64_t(s) * c.max_pages;
+    for (int j = kv4_pages(left, c.page_len) + int(threadIdx.x); j < kv4_pages(len, c.page_len); j += blockDim.x) {
+      const int p = row[j];
+      row[j] = -1;
+      if (p < 0 || p >= c.n_pages) { kv4_flag(c, NT_KV4_BAD_PAGE); continue; }
+      if (atomicSub(&c.refs[p], 1) < 1) {   // nobody held it
+        atomicAdd(&c.refs[p], 1);
+        kv4_flag(c, NT_KV4_BAD_PAGE);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) c.len[s] = left;
+  }
+}
+
+__global__ void __launch_bounds__(256) k_kv4_copy_pages(Kv4 c, int n, const int32_t* src, const int32_t* dst) {
+  __shared__ int s_bad;
+  const int64_t items = int64_t(n) * c.n_layers;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = int(it / c.n_layers), layer = int(it % c.n_layers);
+    const int s = src[i], d = dst[i];
+    __syncthreads();
+    if (threadIdx.x == 0) s_bad = s < 0 || s >= c.n_pages || d < 0 || d >= c.n_pages;
+    __syncthreads();
+    for (int e = threadIdx.x; e < n; e += blockDim.x)
+      if (e != i && (dst[e] == s || (e < i && dst[e] == d))) s_bad = 1;
+    __syncthreads();
+    if (s_bad) {
+      if (threadIdx.x == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
+      continue;
+    }
+    if (s != d) kv4_copy_page(c, s, d, layer);
+  }
+}
+
+// The plan of a compaction by one CTA: L, the pages in use; `to[p]`, where page p
+// goes (itself, or -2 for a free page below L, which receives another); the moves
+// in `pair`, the k-th page in use from L on to the k-th free page below.
+__global__ void __launch_bounds__(1024) k_kv4_compact_plan(Kv4 c, int32_t* go, int2* pair, int32_t* to, int32_t* live) {
+  const int t = threadIdx.x;
+  int64_t used = 0;
+  for (int64_t p0 = 0; p0 < c.n_pages; p0 += 1024) {
+    int64_t all;
+    kv4_scan(p0 + t < c.n_pages && c.refs[p0 + t] > 0 ? 1 : 0, &all);
+    used += all;
+  }
+  int64_t holes = 0, movers = 0;
+  for (int64_t p0 = 0; p0 < c.n_pages; p0 += 1024) {
+    const int64_t p = p0 + t;
+    const bool in = p < c.n_pages, use = in && c.refs[p] > 0;
+    const bool hole = in && !use && p < used, mover = use && p >= used;
+    int64_t nh, nm;
+    const int64_t h = holes + kv4_scan(hole ? 1 : 0, &nh), m = movers + kv4_scan(mover ? 1 : 0, &nm);
+    if (hole) pair[h].y = int32_t(p);
+    if (mover) pair[m].x = int32_t(p);
+    if (in) to[p] = hole ? -2 : int32_t(p);
+    holes += nh;
+    movers += nm;
+  }
+  __syncthreads();
+  for (int64_t i = t; i < movers; i += 1024) to[pair[i].x] = pair[i].y;
+  if (t == 0) {
+    go[1] = int32_t(movers);
+    *live = int32_t(used);
+  }
+}
+
+__global__ void __launch_bounds__(256) k_kv4_compact_apply(Kv4 c, const int32_t* go, const int2* pair, const int32_t* to,
+                                                           int32_t* table_out, int32_t* refs_out) {
+  const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+  for (int64_t p = first; p < c.n_pages; p += step) {
+    const int d = to[p], r = c.refs[p];
+    if (d == -2) continue;                     // the page that moves here writes it
+    if (d != int(p)) refs_out[d] = r;
+    refs_out[p] = d == int(p) ? r : 0;
+  }
+  for (int64_t e = first; e < int64_t(c.max_seqs) * c.max_pages; e += step) {
+    int p = c.table[e];
+    if (p >= c.n_pages) kv4_flag(c, NT_KV4_BAD_PAGE);
+    else if (p >= 0) {
+      p = to[p];
+      if (p < 0) kv4_flag(c, NT_KV4_BAD_PAGE);   // an entry that names a free page: it holds nothing
+    }
+    table_out[e] = p == -2 ? -1 : p;
+  }
+  const int64_t items = int64_t(go[1]) * c.n_layers;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int2 m = pair[it / c.n_layers];
+    kv4_copy_page(c, m.x, m.y, int(it % c.n_layers));
+  }
+}
+
+static unsigned kv4_grid(int64_t blocks, int64_t most) { return unsigned(blocks < 1 ? 1 : (blocks > most ? most : blocks)); }
+constexpr int64_t kKv4Blocks = 152 * 8;
+
+static nt_status kv4_ws_check(const Kv4& k, const char* who, int64_t n, void* ws, size_t bytes, Kv4Ws* w) {
+  *w = kv4_ws(k, n);
+  if (!kv4_aligned(ws, 16)) return fail(NT_E_INVAL, std::string(who) + ": workspace is NULL or not 16-byte aligned");
+  if (bytes < w->bytes) return fail(NT_E_INVAL, std::string(who) + ": workspace too small");
+  if (kv4_meets_cache(k, ws, int64_t(w->bytes))) return fail(NT_E_INVAL, std::string(who) + ": the workspace overlaps the cache");
+  return NT_OK;
+}
+
+static nt_status kv4_list_check(const Kv4& k, const char* who, int64_t n, int64_t most) {
+  if (n < 0 || n > most) return fail(NT_E_INVAL, std::string(who) + ": more entries than the cache has, or fewer than 0");
+  return NT_OK;
+}
+
+// A list of n int32 on the device: aligned, and apart from the cache and the workspace.
+static nt_status kv4_array_check(const Kv4& k, const char* who, const void* p, int64_t n, bool nullable, const void* ws,
+                                 size_t ws_bytes) {
+  if (!p && nullable) return NT_OK;
+  if (!kv4_aligned(p, 4)) return fail(NT_E_INVAL, std::string(who) + ": a list is NULL or not 4-byte aligned");
+  if (kv4_meets_cache(k, p, n * 4) || (ws && kv4_overlap(p, n * 4, ws, int64_t(ws_bytes))))
+    return fail(NT_E_INVAL, std::string(who) + ": a list overlaps the cache or the workspace");
+  return NT_OK;
+}
+
+template <bool FORK>
+static nt_status kv4_plan_apply(const char* who, const Kv4& k, Kv4PlanArgs a, void* ws, size_t ws_bytes, void* stream) {
+  Kv4Ws w;
+  nt_status st = kv4_ws_check(k, who, a.n, ws, ws_bytes, &w);
+  if (!st) st = kv4_array_check(k, who, a.a, a.n, !FORK, ws, w.bytes);
+  if (!st) st = kv4_array_check(k, who, a.b, a.n, false, ws, w.bytes);
+  if (!st) st = kv4_array_check(k, who, a.keep, a.n, true, ws, w.bytes);
+  if (st || a.n == 0) return st;
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  a.go = reinterpret_cast<int32_t*>(base);
+  a.off = reinterpret_cast<int64_t*>(base + w.off);
+  a.pair = reinterpret_cast<int2*>(base + w.pair);
+  a.free = reinterpret_cast<int32_t*>(base + w.free);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  k_kv4_plan<FORK><<<1, 1024, 0, s>>>(k, a);
+  NT_CUDA(cudaGetLastError());
+  k_kv4_apply<FORK><<<kv4_grid(int64_t(a.n) * k.n_layers, kKv4Blocks), 256, 0, s>>>(k, a);
+  NT_CUDA(cudaGetLastError());
+  return NT_OK;
+}
+
+static nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a, nt_qtype type, const void* pk, const void* pv) {
+  auto bad = [&](const char* what) { return fail(NT_E_INVAL, std::string(who) + ": " + what); };
+  if (type != NT_F32 && type != NT_F16) return bad("type must be NT_F32 or NT_F16");
+  if (a.layer < 0 || a.layer >= k.n_layers) return bad("layer out of range");
+  if (a.n < 0 || (!a.seq && a.n > k.max_seqs)) return bad("n out of range");
+  if (a.n_rows < 0) return bad("n_rows must not be negative");
+  const int64_t es = type == NT_F32 ? 4 : 2, most = int64_t(1) << 40;
+  if (a.row_stride < 0 || a.head_stride < 0 || a.row_stride > most || a.head_stride > most || a.row_stride * es % 16 ||
+      a.head_stride * es % 16)
+    return bad("strides must be multiples of 16 bytes and not negative");
+  if (!kv4_aligned(pk, 16) || !kv4_aligned(pv, 16)) return bad("k or v is NULL or not 16-byte aligned");
+  return NT_OK;
+}
+
+// Bytes from the first to the last element of the rows (-1: beyond 2^60).
+static int64_t kv4_rows_bytes(const Kv4& k, const Kv4Rows& a, nt_qtype type) {
+  const double most = double(a.n_rows) * double(a.row_stride) + double(k.n_kv) * double(a.head_stride);
+  if (most > 1e17) return -1;
+  return ((int64_t(a.n_rows) - 1) * a.row_stride + int64_t(k.n_kv - 1) * a.head_stride + k.hd) * (type == NT_F32 ? 4 : 2);
+}
+
+// Whether a (row, kv head) vector of one tensor shares bytes with one of another
+// of the same strides that starts d bytes further (same: the tensor itself, each
+// vector apart from itself).
+static bool kv4_rows_meet(const Kv4& k, const Kv4Rows& a, int64_t es, int64_t d, bool same) {
+  const int64_t rs = a.row_stride * es, hs = a.head_stride * es, w = k.hd * es;
+  for (int64_t h = -(k.n_kv - 1); h <= k.n_kv - 1; h++) {
+    const int64_t x = d + h * hs;                 // then + r rs, r in (-n_rows, n_rows)
+    int64_t r0 = rs ? -x / rs : 0;                // near the row difference that brings it to 0
+    for (int64_t r = r0 - 1; r <= r0 + 1; r++) {
+      if (r <= -int64_t(a.n_rows) || r >= a.n_rows || (same && r == 0 && h == 0)) continue;
+      const int64_t y = x + r * rs;
+      if (y > -w && y < w) return true;
+    }
+  }
+  return false;
+}
+
+}  // namespace nt
+
+using namespace nt;
+
+extern "C" {
+
+nt_status nt_kv4_pool_bytes(const nt_kv4_cache* c, size_t* page_bytes, size_t* pool_bytes) {
+  Kv4 k;
+  const nt_status st = kv4_check(c, "nt_kv4_pool_bytes", false, &k);
+  if (st) return st;
+  if (page_bytes) *page_bytes = size_t(k.page_bytes());
+  if (pool_bytes) *pool_bytes = size_t(k.page_bytes()) * size_t(k.n_pages) * size_t(k.n_layers);
+  return NT_OK;
+}
+
+nt_status nt_kv4_workspace_bytes(const nt_kv4_cache* c, int32_t n_heads, int32_t n, size_t* bytes) {
+  Kv4 k;
+  const nt_status st = kv4_check(c, "nt_kv4_workspace_bytes", false, &k);
+  if (st) return st;
+  if (!bytes) return fail(NT_E_INVAL, "nt_kv4_workspace_bytes: NULL argument");
+  if (n < 0 || n_heads < 1) return fail(NT_E_INVAL, "nt_kv4_workspace_bytes: n or n_heads out of range");
+  if (n_heads % k.n_kv) return fail(NT_E_INVAL, "nt_kv4_workspace_bytes: n_heads must be a multiple of n_kv_heads");
+  const size_t a = kv4_ws(k, n).bytes, b = kv4_attn_ws_bytes(n_heads, k.n_kv, k.hd);
+  *bytes = a > b ? a : b;
+  return NT_OK;
+}
+
+nt_status nt_kv4_extend(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_count,
+                        void* dev_workspace, size_t workspace_bytes, void* stream) {
+  Kv4 k;
+  nt_status st = kv4_check(c, "nt_kv4_extend", true, &k);
+  if (!st) st = kv4_list_check(k, "nt_kv4_extend", n, k.max_seqs);
+  if (st) return st;
+  Kv4PlanArgs a{};
+  a.n = n;
+  a.a = dev_seq;
+  a.b = dev_count;
+  return kv4_plan_apply<false>("nt_kv4_extend", k, a, dev_workspace, workspace_bytes, stream);
+}
+
+nt_status nt_kv4_fork(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
+                      const int32_t* dev_keep, void* dev_workspace, size_t workspace_bytes, void* stream) {
+  Kv4 k;
+  nt_status st = kv4_check(c, "nt_kv4_fork", true, &k);
+  if (!st) st = kv4_list_check(k, "nt_kv4_fork", n, k.max_seqs);
+  if (st) return st;
+  Kv4PlanArgs a{};
+  a.n = n;
+  a.a = dev_src;
+  a.b = dev_dst;
+  a.keep = dev_keep;
+  return kv4_plan_apply<true>("nt_kv4_fork", k, a, dev_workspace, workspace_bytes, stream);
+}
+
+nt_status nt_kv4_free(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_keep, void* stream) {
+  Kv4 k;
+  nt_status st = kv4_check(c, "nt_kv4_free", true, &k);
+  if (!st) st = kv4_list_check(k, "nt_kv4_free", n, k.max_seqs);
+  if (!st) st = kv4_array_check(k, "nt_kv4_free", dev_seq, n, true, nullptr, 0);
+  if (!st) st = kv4_array_check(k, "nt_kv4_free", dev_keep, n, true, nullptr, 0);
+  if (st || n == 0) return st;
+  k_kv4_free<<<kv4_grid(n, kKv4Blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(k, n, dev_seq, dev_keep);
+  NT_CUDA(cudaGetLastError());
+  return NT_OK;
+}
+
+nt_status nt_kv4_copy_pages(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
+                            void* stream) {
+  Kv4 k;
+  nt_status st = kv4_check(c, "nt_kv4_copy_pages", true, &k);
+  if (!st) st = kv4_list_check(k, "nt_kv4_copy_pages", n, k.n_pages);
+  if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_src, n, false, nullptr, 0);
+  if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_dst, n, false, nullptr, 0);
+  if (st || n == 0) return st;
+  k_kv4_copy_pages<<<kv4_grid(int64_t(n) * k.n_layers, kKv4Blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(
+      k, n, dev_src, dev_dst);
+  NT_CUDA(cudaGetLastError());
+  return NT_OK;
+}
+
+nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t* dev_refs_out, int32_t* dev_live,
+                         void* dev_workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "nt_kv4_compact";
+  Kv4 k;
+  Kv4Ws w;
+  nt_status st = kv4_check(c, who, true, &k);
+  if (!st) st = kv4_ws_check(k, who, 0, dev_workspace, workspace_bytes, &w);
+  if (st) return st;
+  const int64_t tb = int64_t(k.max_seqs) * k.max_pages * 4, rb = int64_t(k.n_pages) * 4;
+  if (!kv4_aligned(dev_table_out, 4) || !kv4_aligned(dev_refs_out, 4) || !kv4_aligned(dev_live, 4))
+    return fail(NT_E_INVAL, "nt_kv4_compact: an output is NULL or not 4-byte aligned");
+  if ((dev_table_out != k.table && kv4_meets_cache(k, dev_table_out, tb)) ||
+      (dev_refs_out != k.refs && kv4_meets_cache(k, dev_refs_out, rb)) || kv4_meets_cache(k, dev_live, 4) ||
+      kv4_overlap(dev_table_out, tb, dev_refs_out, rb) || kv4_overlap(dev_table_out, tb, dev_live, 4) ||
+      kv4_overlap(dev_refs_out, rb, dev_live, 4) || kv4_overlap(dev_workspace, int64_t(w.bytes), dev_table_out, tb) ||
+      kv4_overlap(dev_workspace, int64_t(w.bytes), dev_refs_out, rb) ||
+      kv4_overlap(dev_workspace, int64_t(w.bytes), dev_live, 4))
+    return fail(NT_E_INVAL, "nt_kv4_compact: an output overlaps another buffer");
+  uint8_t* base = static_cast<uint8_t*>(dev_workspace);
+  int32_t* go = reinterpret_cast<int32_t*>(base);
+  int2* pair = reinterpret_cast<int2*>(base + w.pair);
+  int32_t* to = reinterpret_cast<int32_t*>(base + w.free);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  k_kv4_compact_plan<<<1, 1024, 0, s>>>(k, go, pair, to, dev_live);
+  NT_CUDA(cudaGetLastError());
+  k_kv4_compact_apply<<<unsigned(kKv4Blocks), 256, 0, s>>>(k, go, pair, to, dev_table_out, dev_refs_out);
+  NT_CUDA(cudaGetLastError());
+  return NT_OK;
+}
+
+nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
+                        const int32_t* dev_begin, int32_t n_rows, nt_qtype type, const void* dev_k, const void* dev_v,
+                        int64_t row_stride, int64_t head_stride, void* stream) {
+  const char* who = "nt_kv4_append";
+  Kv4 k;
+  nt_status st = kv4_check(c, who, true, &k);
+  const Kv4Rows a{layer, n, n_rows, dev_seq, dev_begin, row_stride, head_stride};
+  if (!st) st = kv4_rows_check(who, k, a, type, dev_k, dev_v);
+  if (!st && n > k.max_seqs) st = fail(NT_E_INVAL, "nt_kv4_append: n above max_seqs");
+  if (!st) st = kv4_array_check(k, who, dev_seq, n, true, nullptr, 0);
+  if (!st) st = kv4_array_check(k, who, dev_begin, int64_t(n) + 1, true, nullptr, 0);
+  if (st || n == 0 || n_rows == 0) return st;
+  const int64_t bytes = kv4_rows_bytes(k, a, type);
+  if (bytes < 0) return fail(NT_E_INVAL, "nt_kv4_append: the strides are too large");
+  if (kv4_meets_cache(k, dev_k, bytes) || kv4_meets_cache(k, dev_v, bytes))
+    return fail(NT_E_INVAL, "nt_kv4_append: k or v overlaps the cache");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t lanes = int64_t(n_rows) * k.n_kv * 2 * (k.hd / 8);
+  const unsigned grid = kv4_grid((lanes + 255) / 256, kKv4Blocks);
+  if (type == NT_F32) {
+    const float *pk = static_cast<const float*>(dev_k), *pv = static_cast<const float*>(dev_v);
+    if (k.hd == 64) k_kv4_append<64, float><<<grid, 256, 0, s>>>(k, a, pk, pv);
+    else k_kv4_append<128, float><<<grid, 256, 0, s>>>(k, a, pk, pv);
+  } else {
+    const __half *pk = static_cast<const __half*>(dev_k), *pv = static_cast<const __half*>(dev_v);
+    if (k.hd == 64) k_kv4_append<64, __half><<<grid, 256, 0, s>>>(k, a, pk, pv);
+    else k_kv4_append<128, __half><<<grid, 256, 0, s>>>(k, a, pk, pv);
+  }
+  NT_CUDA(cudaGetLastError());
+  if (dev_seq && n > 1) {
+    k_kv4_listed_twice<<<1, 1024, 0, s>>>(k, n, dev_seq);
+    NT_CUDA(cudaGetLastError());
+  }
+  return NT_OK;
+}
+
+nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq, const int32_t* dev_begin,
+                      int32_t n_rows, nt_qtype type, void* dev_k, void* dev_v, int64_t row_stride, int64_t head_stride,
+                      void* stream) {
+  const char* who = "nt_kv4_read";
+  Kv4 k;
+  nt_status st = kv4_check(c, who, true, &k);
+  const Kv4Rows a{layer, n, n_rows, dev_seq, dev_begin, row_stride, head_stride};
+  if (!st) st = kv4_rows_check(who, k, a, type, dev_k, dev_v);
+  if (!st) st = kv4_array_check(k, who, dev_seq, n, true, nullptr, 0);
+  if (!st) st = kv4_array_check(k, who, dev_begin, int64_t(n) + 1, true, nullptr, 0);
+  if (st || n == 0 || n_rows == 0) return st;
+  const int64_t bytes = kv4_rows_bytes(k, a, type), es = type == NT_F32 ? 4 : 2;
+  if (bytes < 0) return fail(NT_E_INVAL, "nt_kv4_read: the strides are too large");
+  const int64_t apart = static_cast<char*>(dev_v) - static_cast<char*>(dev_k);
+  if (kv4_rows_meet(k, a, es, 0, true) || (kv4_overlap(dev_k, bytes, dev_v, bytes) && kv4_rows_meet(k, a, es, apart, false)))
+    return fail(NT_E_INVAL, "nt_kv4_read: rows of the outputs overlap");
+  if (kv4_meets_cache(k, dev_k, bytes) || kv4_meets_cache(k, dev_v, bytes) ||
+      kv4_overlap(dev_seq, int64_t(n) * 4, dev_k, bytes) || kv4_overlap(dev_seq, int64_t(n) * 4, dev_v, bytes) ||
+      kv4_overlap(dev_begin, int64_t(n) * 4 + 4, dev_k, bytes) || kv4_overlap(dev_begin, int64_t(n) * 4 + 4, dev_v, bytes))
+    return fail(NT_E_INVAL, "nt_kv4_read: an output overlaps another buffer");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t lanes = int64_t(n_rows) * k.n_kv * 2 * (k.hd / 8);
+  const unsigned grid = kv4_grid((lanes + 255) / 256, kKv4Blocks);
+  if (type == NT_F32) {
+    float *pk = static_cast<float*>(dev_k), *pv = static_cast<float*>(dev_v);
+    if (k.hd == 64) k_kv4_read<64, float><<<grid, 256, 0, s>>>(k, a, pk, pv);
+    else k_kv4_read<128, float><<<grid, 256, 0, s>>>(k, a, pk, pv);
+  } else {
+    __half *pk = static_cast<__half*>(dev_k), *pv = static_cast<__half*>(dev_v);
+    if (k.hd == 64) k_kv4_read<64, __half><<<grid, 256, 0, s>>>(k, a, pk, pv);
+    else k_kv4_read<128, __half><<<grid, 256, 0, s>>>(k, a, pk, pv);
+  }
+  NT_CUDA(cudaGetLastError());
+  return NT_OK;
+}
+
+}  // extern "C"

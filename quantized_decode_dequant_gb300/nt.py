@@ -61,8 +61,18 @@ class nt_kernel_times(C.Structure):
                 ("step_ms", C.c_double), ("kernel_launches", C.c_int64)]
 
 
+class nt_kv4_cache(C.Structure):
+    _fields_ = [("n_layers", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("page_len", C.c_int32), ("n_pages", C.c_int32), ("max_seqs", C.c_int32), ("max_pages", C.c_int32),
+                ("pool", C.c_void_p), ("table", C.c_void_p), ("len", C.c_void_p), ("refs", C.c_void_p),
+                ("error", C.c_void_p)]
+
+
+NT_KV4_BAD_SEQ, NT_KV4_BAD_LEN, NT_KV4_BAD_PAGE, NT_KV4_NO_PAGE, NT_KV4_TIMEOUT = 1, 2, 4, 8, 16
+
 _lib = None
 _vp, _i32, _i64, _u64, _f32p = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64, C.POINTER(C.c_float)
+_kv4p = C.POINTER(nt_kv4_cache)
 _SIGS = {
     "nt_last_error": (C.c_char_p, []),
     "nt_model_create": (C.c_int, [C.POINTER(nt_config), C.POINTER(C.c_void_p)]),
@@ -96,6 +106,16 @@ _SIGS = {
     "nt_gemv_argmax_noalloc": (C.c_int, [_vp, _vp, _vp, _vp, _vp, _vp]),
     "nt_attention_workspace_bytes": (C.c_int, [_i32, _i32, _i32, _i32, C.POINTER(C.c_size_t)]),
     "nt_attention": (C.c_int, [_i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "nt_kv4_pool_bytes": (C.c_int, [_kv4p, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)]),
+    "nt_kv4_workspace_bytes": (C.c_int, [_kv4p, _i32, _i32, C.POINTER(C.c_size_t)]),
+    "nt_kv4_extend": (C.c_int, [_kv4p, _i32, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "nt_kv4_fork": (C.c_int, [_kv4p, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "nt_kv4_free": (C.c_int, [_kv4p, _i32, _vp, _vp, _vp]),
+    "nt_kv4_copy_pages": (C.c_int, [_kv4p, _i32, _vp, _vp, _vp]),
+    "nt_kv4_compact": (C.c_int, [_kv4p, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "nt_kv4_append": (C.c_int, [_kv4p, _i32, _i32, _vp, _vp, _i32, C.c_int, _vp, _vp, _i64, _i64, _vp]),
+    "nt_kv4_read": (C.c_int, [_kv4p, _i32, _i32, _vp, _vp, _i32, C.c_int, _vp, _vp, _i64, _i64, _vp]),
+    "nt_attention_kv4": (C.c_int, [_kv4p, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _vp, C.c_size_t, _vp]),
 }
 
 
@@ -351,6 +371,79 @@ def nt_attention(n_heads: int, n_kv_heads: int, head_dim: int, max_ctx: int, n_c
     """GQA attention of fp32 q over positions [0, n_ctx) of an f16 [n_kv][max_ctx][hd] K/V cache."""
     _check(lib().nt_attention(n_heads, n_kv_heads, head_dim, max_ctx, n_ctx, dev_q, dev_k, dev_v, dev_out,
                               dev_workspace, workspace_bytes, _stream(stream)), "nt_attention")
+
+
+# ------------------------------------------------------ paged 4-bit K/V cache --
+
+def make_kv4_cache(*, n_layers, n_kv_heads, head_dim, page_len, n_pages, max_seqs, max_pages, pool=0, table=0, len=0,
+                   refs=0, error=0) -> nt_kv4_cache:
+    """Description of a paged 4-bit K/V cache; pool, table, len, refs and error are device addresses."""
+    return nt_kv4_cache(n_layers, n_kv_heads, head_dim, page_len, n_pages, max_seqs, max_pages, pool, table, len, refs,
+                        error)
+
+
+def nt_kv4_pool_bytes(c: nt_kv4_cache) -> tuple[int, int]:
+    """(bytes of one page of one layer, bytes of the pool)."""
+    page, pool = C.c_size_t(), C.c_size_t()
+    _check(lib().nt_kv4_pool_bytes(c, page, pool), "nt_kv4_pool_bytes")
+    return int(page.value), int(pool.value)
+
+
+def nt_kv4_workspace_bytes(c: nt_kv4_cache, n_heads: int, n: int) -> int:
+    b = C.c_size_t()
+    _check(lib().nt_kv4_workspace_bytes(c, n_heads, n, b), "nt_kv4_workspace_bytes")
+    return int(b.value)
+
+
+def nt_kv4_extend(c: nt_kv4_cache, n: int, dev_seq, dev_count: int, dev_workspace: int, workspace_bytes: int,
+                  stream=None) -> None:
+    """Room for dev_count[i] more positions of each listed sequence."""
+    _check(lib().nt_kv4_extend(c, n, dev_seq, dev_count, dev_workspace, workspace_bytes, _stream(stream)),
+           "nt_kv4_extend")
+
+
+def nt_kv4_fork(c: nt_kv4_cache, n: int, dev_src: int, dev_dst: int, dev_keep, dev_workspace: int,
+                workspace_bytes: int, stream=None) -> None:
+    """The empty sequences dev_dst[i] become (the first dev_keep[i] positions of) dev_src[i]."""
+    _check(lib().nt_kv4_fork(c, n, dev_src, dev_dst, dev_keep, dev_workspace, workspace_bytes, _stream(stream)),
+           "nt_kv4_fork")
+
+
+def nt_kv4_free(c: nt_kv4_cache, n: int, dev_seq, dev_keep=None, stream=None) -> None:
+    """The listed sequences keep their first dev_keep[i] positions (None: nothing)."""
+    _check(lib().nt_kv4_free(c, n, dev_seq, dev_keep, _stream(stream)), "nt_kv4_free")
+
+
+def nt_kv4_copy_pages(c: nt_kv4_cache, n: int, dev_src: int, dev_dst: int, stream=None) -> None:
+    _check(lib().nt_kv4_copy_pages(c, n, dev_src, dev_dst, _stream(stream)), "nt_kv4_copy_pages")
+
+
+def nt_kv4_compact(c: nt_kv4_cache, dev_table_out: int, dev_refs_out: int, dev_live: int, dev_workspace: int,
+                   workspace_bytes: int, stream=None) -> None:
+    """The pages in use move below their number; table and counts that go with it into dev_table_out, dev_refs_out."""
+    _check(lib().nt_kv4_compact(c, dev_table_out, dev_refs_out, dev_live, dev_workspace, workspace_bytes,
+                                _stream(stream)), "nt_kv4_compact")
+
+
+def nt_kv4_append(c: nt_kv4_cache, layer: int, n: int, dev_seq, dev_begin, n_rows: int, qtype: str, dev_k: int,
+                  dev_v: int, row_stride: int, head_stride: int, stream=None) -> None:
+    """Quantizes rows of K and V ("f32" or "f16") into the last positions of the listed sequences."""
+    _check(lib().nt_kv4_append(c, layer, n, dev_seq, dev_begin, n_rows, QTYPES[qtype], dev_k, dev_v, row_stride,
+                               head_stride, _stream(stream)), "nt_kv4_append")
+
+
+def nt_kv4_read(c: nt_kv4_cache, layer: int, n: int, dev_seq, dev_begin, n_rows: int, qtype: str, dev_k: int,
+                dev_v: int, row_stride: int, head_stride: int, stream=None) -> None:
+    """Dequantizes the last positions of the listed sequences into rows of K and V ("f32" or "f16")."""
+    _check(lib().nt_kv4_read(c, layer, n, dev_seq, dev_begin, n_rows, QTYPES[qtype], dev_k, dev_v, row_stride,
+                             head_stride, _stream(stream)), "nt_kv4_read")
+
+
+def nt_attention_kv4(c: nt_kv4_cache, layer: int, n_heads: int, n: int, dev_seq, dev_q: int, q_stride: int,
+                     dev_out: int, out_stride: int, dev_workspace: int, workspace_bytes: int, stream=None) -> None:
+    """GQA attention of fp32 q over the listed sequences of a paged 4-bit cache."""
+    _check(lib().nt_attention_kv4(c, layer, n_heads, n, dev_seq, dev_q, q_stride, dev_out, out_stride, dev_workspace,
+                                  workspace_bytes, _stream(stream)), "nt_attention_kv4")
 
 
 def nt_gemv_argmax_noalloc(t: int, dev_x: int, dev_y: int, dev_index: int, dev_margin: int, stream=None) -> None:
