@@ -1,92 +1,662 @@
 // nt_kv4_attn.cu -- GQA decode attention over the paged 4-bit K/V cache.
+//
+// out_j = sum_t softmax(q_j . K_t / sqrt(hd))_t V_t for the G query heads j of a
+// kv head, in one pass over its chunks of 16 positions with a running maximum
+// and sum (flash decoding): each warp copies its chunks from the pages into a
+// ring of its own in shared memory (one bulk copy of 18 hd contiguous bytes per
+// chunk), decodes codes in registers and contracts them on the tensor cores.
+//
+// Decoding.  Four bits moved to bits 4..7 of an f16 whose upper bits are 0x5400
+// are the number 64 + q; one fused multiply-add gives the value, (64 + q) d - 72 d
+// = d (q - 8), exactly: d has seven significant bits, so 72 d has eleven.  That is
+// 3 shifts, 4 logic ops and 4 half2 multiply-adds for 8 values, the scale included.
+// The words are laid out so that what a lane decodes is its own fragment of the
+// B operand of mma.sync m16n8k16: nothing passes through shared memory twice.
+//
+// Contractions.  Scores S[h][t] = q_h . K_t and outputs O[h][d] = sum_t P[h][t]
+// V_t[d].  q (scaled by a power of two) and P are split into two f16 terms, hi =
+// f16(x) and lo = f16(x - hi), about 22 bits.  With G <= 8 hi takes rows 0..7 of
+// the 16-row A operand and lo rows 8..15; with G = 16 each has a product of its own.
+//
+// What bounds it: a byte of cache is 1.8 values, and a value costs about 2.3
+// instructions of a lane, so at 6.8 TB/s the SMs' issue slots are about 3/4 busy:
+// near the memory bound, with the arithmetic close behind.  (tcgen05 would need
+// the decoded f16 values, four times the bytes, written to shared memory first;
+// mma.sync takes them from registers, and at 16 rows its rate is not the limit.)
 #include "nt_kv4.cuh"
 
 namespace nt {
 
-size_t kv4_attn_ws_bytes(int, int, int) { return 16; }
+constexpr int kKv4Batch = 1024;        // sequences of one launch: their chunk offsets are kept in shared memory
+constexpr int kKv4AttnMaxCtas = 152;   // one CTA per SM; the workspace holds two partial results of each
+constexpr int kKv4MinChunks = 2;       // fewest chunks of a warp: below, fewer CTAs work
 
 struct Kv4AttnArgs {
-  int32_t layer, n_heads, n;
+  int32_t layer, n, G;
+  int32_t seq0;                        // sequence of entry 0 where none are listed
   const int32_t* seq;
   const float* q;
   int64_t q_stride;
   float* out;
   int64_t out_stride;
+  float scale_log2;                    // log2(e) / sqrt(hd)
+  float* part;                         // [CTA][2] partial results: see Kv4Part
+  int32_t ctas, warps;                 // of the attention kernel
 };
 
-// One CTA per (sequence, kv head): chunks of 16 positions are dequantized into
-// shared memory, scored against the G query heads, and folded into the running
-// maximum, sum and output of each head.
-template <int HD>
-__global__ void __launch_bounds__(256) k_kv4_attn(Kv4 c, Kv4AttnArgs a, int G, float scale) {
+template <int HD, int MT>
+struct Kv4AttnCfg {
+  static constexpr int NW = MT == 1 ? (HD == 128 ? 12 : 16) : (HD == 128 ? 8 : 12);   // warps: registers decide
+  static constexpr int S = HD == 128 ? 4 : 6;                                          // ring stages of a warp
+  static constexpr int kThreads = 32 * NW;
+  static constexpr int kRows = 8 * MT;                                                 // heads of a partial result
+  // partial result: o [kRows][HD], then (reference m, sum l) per head
+  static constexpr int kPartFloats = kRows * HD + 2 * kRows;
+  static constexpr int kRing = 0;
+  static constexpr int kSlots = kRing + NW * S * kv4_chunk_bytes(HD);
+  static constexpr int kPrefix = kSlots + 2 * NW * kPartFloats * 4;
+  static constexpr int kBars = kPrefix + (kKv4Batch + 1) * 8;
+  static constexpr int kItem = kBars + NW * S * 8;                                     // item of each slot (-1: none)
+  static constexpr int kSmem = kItem + 2 * NW * 8 + 64;
+  static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+};
+
+size_t kv4_attn_ws_bytes(int n_heads, int n_kv, int hd) {
+  const int rows = n_heads / n_kv > 8 ? 16 : 8;
+  return size_t(kKv4AttnMaxCtas) * 2 * (size_t(rows) * hd + 2 * rows) * 4;
+}
+
+// ------------------------------------------------------------ small pieces --
+
+__device__ __forceinline__ uint32_t kv4_smem(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ float kv4_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint4 kv4_lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 kv4_lds8(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint32_t kv4_lds4(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+// NG consecutive words
+template <int NG>
+__device__ __forceinline__ void kv4_words(uint32_t a, uint32_t (&w)[NG]) {
+  if (NG == 4) {
+    const uint4 v = kv4_lds16(a);
+    w[0] = v.x; w[1] = v.y; w[2 % NG] = v.z; w[3 % NG] = v.w;
+  } else {
+    const uint2 v = kv4_lds8(a);
+    w[0] = v.x; w[1] = v.y;
+  }
+}
+__device__ __forceinline__ uint32_t kv4_h2fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t kv4_h2mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// The four half2 of a word: value pairs (code k, code k + 4), k = 0..3, times the
+// scale pair d; d72 = -72 d.
+__device__ __forceinline__ void kv4_decode(uint32_t w, uint32_t d, uint32_t d72, uint32_t (&b)[4]) {
+  constexpr uint32_t kMask = 0x00f000f0u, k64 = 0x54005400u;
+  b[0] = kv4_h2fma(((w << 4) & kMask) | k64, d, d72);
+  b[1] = kv4_h2fma((w & kMask) | k64, d, d72);
+  b[2] = kv4_h2fma(((w >> 4) & kMask) | k64, d, d72);
+  b[3] = kv4_h2fma(((w >> 8) & kMask) | k64, d, d72);
+}
+constexpr uint32_t kMinus72 = 0xd480d480u;   // f16 -72 twice
+
+// hi and lo f16 terms of two fp32 values
+__device__ __forceinline__ void kv4_split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ void kv4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void kv4_bar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+// One chunk from global to shared memory, counted on bar.
+__device__ __forceinline__ void kv4_copy_chunk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void kv4_bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Waits for the phase of `parity` to complete, at most kKv4WaitTries tries (each
+// of which the hardware may hold for a while); false: gave up.
+constexpr int kKv4WaitTries = 1 << 20;
+__device__ __forceinline__ bool kv4_bar_wait(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < kKv4WaitTries; i++) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
+
+// Chunks of listed entry e (0: nothing to read); *bad: error bits of an entry that cannot be read.
+__device__ __forceinline__ int kv4_entry_chunks(const Kv4& c, const Kv4AttnArgs& a, int e, uint32_t* bad) {
+  const int s = a.seq ? a.seq[e] : a.seq0 + e;
+  if (s < 0 || s >= c.max_seqs) { *bad = NT_KV4_BAD_SEQ; return 0; }
+  const int n = c.len[s];
+  if (n < 0 || n > c.capacity()) { *bad = NT_KV4_BAD_LEN; return 0; }
+  *bad = 0;
+  return (n + kKv4Chunk - 1) / kKv4Chunk;
+}
+
+// Chunks of a warp when `total` are shared out.
+__device__ __forceinline__ int64_t kv4_share(int64_t total, const Kv4AttnArgs& a) {
+  const int64_t warps = int64_t(a.ctas) * a.warps, per = (total + warps - 1) / warps;
+  return per < kKv4MinChunks ? kKv4MinChunks : per;
+}
+
+// Entry of prefix (ascending, prefix[0] = 0) that holds chunk x: prefix[i] <= x < prefix[i + 1].
+__device__ __forceinline__ int kv4_find(const int64_t* prefix, int n, int64_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// Output rows of one head: lane (row, tg) holds dimensions 32 j + 8 tg + 0..7 of it.
+template <int NG>
+__device__ __forceinline__ void kv4_store_row(float* o, int tg, const float (&v)[NG][8], float f) {
+#pragma unroll
+  for (int j = 0; j < NG; j++) {
+    float4* p = reinterpret_cast<float4*>(o + 32 * j + 8 * tg);
+    p[0] = make_float4(v[j][0] * f, v[j][1] * f, v[j][2] * f, v[j][3] * f);
+    p[1] = make_float4(v[j][4] * f, v[j][5] * f, v[j][6] * f, v[j][7] * f);
+  }
+}
+
+// ------------------------------------------------------------ the kernel --
+
+// All chunks of all (entry, kv head) items in a row, item after item, are shared
+// out evenly: warp w of CTA b takes chunks [(b NW + w) C, (b NW + w + 1) C).  An
+// item that lies within a warp's share is finished by it; one that lies within a
+// CTA's is merged in shared memory; the rest leaves partial results (at most two
+// a CTA: of an item begun before it and of one that goes on behind it) to
+// k_kv4_attn_merge.  Partial results are merged in the order of the positions, so
+// the result does not depend on timing.
+template <int HD, int MT>
+__global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv4 c, Kv4AttnArgs a) {
+  using Cfg = Kv4AttnCfg<HD, MT>;
   using L = Kv4Chunk<HD>;
-  __shared__ float q[16 * HD], ks[16][HD], vs[16][HD], ps[16][16], corr[16], ml[16][2];
-  const int i = blockIdx.x, g = blockIdx.y, t = threadIdx.x;
-  const int s = a.seq ? a.seq[i] : i;
-  const float* qi = a.q + int64_t(i) * a.q_stride + int64_t(g) * G * HD;
-  float* oi = a.out + int64_t(i) * a.out_stride + int64_t(g) * G * HD;
-  const bool bad_seq = s < 0 || s >= c.max_seqs;
-  const int len = bad_seq ? 0 : c.len[s];
-  bool poison = bad_seq || len < 0 || len > c.capacity();
-  if (poison && t == 0) kv4_flag(c, bad_seq ? NT_KV4_BAD_SEQ : NT_KV4_BAD_LEN);
-  for (int e = t; e < G * HD; e += 256) q[e] = qi[e];
-  if (t < G) { ml[t][0] = -INFINITY; ml[t][1] = 0.f; }
-  float acc[16 * HD / 256];
+  constexpr int NW = Cfg::NW, S = Cfg::S, NG = HD / 32, NT = HD / 8, CB = L::kBytes, ROWS = Cfg::kRows;
+  extern __shared__ __align__(128) uint8_t sm[];
+  int64_t* prefix = reinterpret_cast<int64_t*>(sm + Cfg::kPrefix);
+  float* slots = reinterpret_cast<float*>(sm + Cfg::kSlots);
+  int64_t* slot_item = reinterpret_cast<int64_t*>(sm + Cfg::kItem);
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, gi = lane >> 2, tg = lane & 3;
+  const int G = a.G, n = a.n;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // ---- chunk offsets of the entries (an entry's chunks are counted once per kv head)
+  {
+    int64_t* sums = reinterpret_cast<int64_t*>(sm + Cfg::kSlots);   // per-warp sums, before the slots are used
+    int64_t run = 0;
+    for (int e0 = 0; e0 < n; e0 += Cfg::kThreads) {
+      const int e = e0 + t;
+      uint32_t bad = 0;
+      int64_t x = e < n ? int64_t(kv4_entry_chunks(c, a, e, &bad)) : 0;
+      if (bad && blockIdx.x == 0) kv4_flag(c, bad);
+      const int64_t mine = x;
 #pragma unroll
-  for (int e = 0; e < 16 * HD / 256; e++) acc[e] = 0.f;
-  for (int t0 = 0; t0 < len && !poison; t0 += 16) {
-    const int page = c.table[int64_t(s) * c.max_pages + t0 / c.page_len], live = min(16, len - t0);
-    if (page < 0 || page >= c.n_pages) {   // uniform over the CTA
-      poison = true;
-      if (t == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
-      break;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) sums[warp] = x;
+      __syncthreads();
+      int64_t before = 0, all = 0;
+      for (int w = 0; w < NW; w++) {
+        const int64_t y = sums[w];
+        if (w < warp) before += y;
+        all += y;
+      }
+      if (e < n) prefix[e] = (run + before + x - mine) * c.n_kv;
+      run += all;
+      __syncthreads();
     }
-    const uint8_t* ch = c.chunk(a.layer, page, g, t0 % c.page_len);
+    if (t == 0) prefix[n] = run * c.n_kv;
+    if (lane < S) kv4_bar_init(kv4_smem(sm + Cfg::kBars + (warp * S + lane) * 8));
+    if (lane < 2) slot_item[2 * warp + lane] = -1;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
-    for (int e = t; e < 16 * HD; e += 256) {
-      const int p = e / HD, d = e % HD, j = d / 32;
-      if (p < live) {
-        const uint32_t kw = *reinterpret_cast<const uint32_t*>(ch + L::k_word(p, d / 8 % 4, j));
-        const uint32_t vh = *reinterpret_cast<const uint16_t*>(ch + L::v_half(p, d / 4 % 8, j));
-        ks[p][d] = __half2float(*reinterpret_cast<const __half*>(ch + L::k_scale(p, j))) * float(int(kw >> (4 * (d % 8)) & 15u) - 8);
-        vs[p][d] = __half2float(*reinterpret_cast<const __half*>(ch + L::v_scale(p, j))) * float(int(vh >> (4 * (d % 4)) & 15u) - 8);
+  }
+  const int64_t total = prefix[n], share = kv4_share(total, a);
+  const int64_t c0 = int64_t(blockIdx.x) * NW * share;   // the CTA's first chunk
+  int64_t c1 = c0 + NW * share;
+  if (c1 > total) c1 = total;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (c0 >= total) return;   // the whole CTA
+
+  const int64_t w0 = c0 + warp * share;
+  const int count = w0 >= c1 ? 0 : int(w0 + share > c1 ? c1 - w0 : share);
+  const uint32_t ring = kv4_smem(sm + Cfg::kRing) + uint32_t(warp) * S * CB;
+  const uint32_t bars = kv4_smem(sm + Cfg::kBars) + uint32_t(warp) * S * 8;
+  const int cpp = c.page_len / kKv4Chunk;
+
+  // index of chunk x of this warp within its layer's pool (in chunks), -1: no such page
+  auto resolve = [&](int x) -> int {
+    if (x >= count) return -1;
+    const int64_t y = w0 + x;
+    const int e = kv4_find(prefix, n, y);
+    const int nch = int((prefix[e + 1] - prefix[e]) / c.n_kv), rem_g = int((y - prefix[e]) / nch);
+    const int ci = int(y - prefix[e] - int64_t(rem_g) * nch);
+    const int s = a.seq ? a.seq[e] : a.seq0 + e;
+    const int page = c.table[int64_t(s) * c.max_pages + ci / cpp];
+    if (page < 0 || page >= c.n_pages) { kv4_flag(c, NT_KV4_BAD_PAGE); return -1; }
+    return int((int64_t(page) * c.n_kv + rem_g) * cpp + ci % cpp);
+  };
+  const uint8_t* layer_pool = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes();
+
+  int addr = resolve(lane), addr_next = -1;   // of chunks 32 b + lane and the 32 behind
+  int issued = 0;
+  uint32_t missing = 0;                       // stages whose chunk has no page
+  bool dead = false;                          // a wait ran out: nothing more is copied or read
+  auto issue = [&]() {
+    if (issued < count && !dead) {
+      const int x = __shfl_sync(0xffffffffu, addr, issued & 31), st = issued % S;
+      missing = x < 0 ? missing | (1u << st) : missing & ~(1u << st);
+      if (lane == 0) {
+        if (x >= 0) kv4_copy_chunk(ring + st * CB, layer_pool + int64_t(x) * CB, CB, bars + st * 8);
+        else kv4_bar_arrive(bars + st * 8);
+      }
+      issued++;
+      if ((issued & 31) == 16) addr_next = resolve((issued & ~31) + 32 + lane);
+      if ((issued & 31) == 0) addr = addr_next;
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < S; i++) issue();
+
+  float O[NT][4];
+  uint32_t qa[MT][HD / 16][4];
+  float mref[MT], l[MT], cs[MT];
+  int k = 0;                                  // chunks read
+  while (k < count) {
+    // ---- a segment: consecutive chunks of one item
+    const int64_t y = w0 + k;
+    const int e = kv4_find(prefix, n, y);
+    const int nch = int((prefix[e + 1] - prefix[e]) / c.n_kv), g = int((y - prefix[e]) / nch);
+    const int ci0 = int(y - prefix[e] - int64_t(g) * nch);
+    const int seg = nch - ci0 < count - k ? nch - ci0 : count - k;
+    const int s = a.seq ? a.seq[e] : a.seq0 + e;
+    const int len = c.len[s];
+    bool poison = false;
+    {
+      // q of heads gi (and gi + 8), scaled so that the largest element is in [2^10, 2^11), split
+      const float* qb = a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD;
+      float x[MT][NG][8];
+#pragma unroll
+      for (int m = 0; m < MT; m++) {
+        const int h = gi + 8 * m;
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+          float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+          if (h < G) {
+            u = __ldg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg));
+            v = __ldg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg) + 1);
+          }
+          x[m][j][0] = u.x; x[m][j][1] = u.y; x[m][j][2] = u.z; x[m][j][3] = u.w;
+          x[m][j][4] = v.x; x[m][j][5] = v.y; x[m][j][6] = v.z; x[m][j][7] = v.w;
+#pragma unroll
+          for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(x[m][j][i]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int ex = int(__float_as_uint(top) >> 23);
+        ex = ex < 11 ? 11 : ex;                                  // (zeros and values below 2^-116)
+        const float up = __uint_as_float(uint32_t(264 - ex) << 23);   // 2^(137 - ex)
+        cs[m] = a.scale_log2 * __uint_as_float(uint32_t(ex - 10) << 23);
+#pragma unroll
+        for (int j = 0; j < NG; j++)
+#pragma unroll
+          for (int i = 0; i < 8; i++) x[m][j][i] *= up;
+      }
+#pragma unroll
+      for (int j = 0; j < NG; j++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {   // pair (code i, code i + 4): k-step 2 j + i / 2, half i % 2
+          const int kk = 2 * j + (i >> 1), r = 2 * (i & 1);
+          if (MT == 1) {
+            kv4_split(x[0][j][i], x[0][j][i + 4], qa[0][kk][r], qa[0][kk][r + 1]);
+          } else {
+            kv4_split(x[0][j][i], x[0][j][i + 4], qa[0][kk][r], qa[MT - 1][kk][r]);
+            kv4_split(x[MT - 1][j][i], x[MT - 1][j][i + 4], qa[0][kk][r + 1], qa[MT - 1][kk][r + 1]);
+          }
+        }
+#pragma unroll
+      for (int m = 0; m < MT; m++) { mref[m] = -INFINITY; l[m] = 0.f; }
+#pragma unroll
+      for (int i = 0; i < NT; i++) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
+    }
+
+#pragma unroll 1
+    for (int ci = ci0; ci < ci0 + seg; ci++, k++) {
+      const int st = k % S;
+      if (!dead && !kv4_bar_wait(bars + st * 8, uint32_t(k / S) & 1u)) {
+        dead = true;
+        if (lane == 0) kv4_flag(c, NT_KV4_TIMEOUT);
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      if (dead || (missing >> st & 1u)) {
+        poison = true;
+        __syncwarp();
+        issue();
+        continue;
+      }
+      const uint32_t base = ring + st * CB;
+      const int live = len - ci * kKv4Chunk;       // positions of this chunk that exist (16 or more: all)
+
+      // ---- scores of 16 positions
+      float sc[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; i++) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+      {
+        uint32_t kw[2][NG], ks[2][NG / 2];
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+          kv4_words<NG>(base + (i * 32 + lane) * (4 * NG), kw[i]);
+          if (NG == 4) {
+            const uint2 v = kv4_lds8(base + L::kKS + (8 * i + gi) * (2 * NG));
+            ks[i][0] = v.x; ks[i][NG / 2 - 1] = v.y;
+          } else {
+            ks[i][0] = kv4_lds4(base + L::kKS + (8 * i + gi) * (2 * NG));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NG; j++)
+#pragma unroll
+          for (int i = 0; i < 2; i++) {
+            const uint32_t d = __byte_perm(ks[i][j >> 1], 0u, (j & 1) ? 0x3232u : 0x1010u), d72 = kv4_h2mul(d, kMinus72);
+            uint32_t b[4];
+            kv4_decode(kw[i][j], d, d72, b);
+#pragma unroll
+            for (int m = 0; m < MT; m++) {
+              kv4_mma(sc[i], qa[m][2 * j], b[0], b[1]);
+              kv4_mma(sc[i], qa[m][2 * j + 1], b[2], b[3]);
+            }
+          }
+      }
+      // the positions' scores of this lane's heads: 2 tg, 2 tg + 1, 8 + 2 tg, 8 + 2 tg + 1
+      float p[MT][4];
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+#pragma unroll
+        for (int x = 0; x < 2; x++) {
+          if (MT == 1) {
+            p[0][2 * i + x] = sc[i][x] + sc[i][x + 2];
+          } else {
+            p[0][2 * i + x] = sc[i][x];
+            p[MT - 1][2 * i + x] = sc[i][x + 2];
+          }
+        }
+      if (live < kKv4Chunk) {
+#pragma unroll
+        for (int m = 0; m < MT; m++)
+#pragma unroll
+          for (int x = 0; x < 4; x++)
+            if (8 * (x >> 1) + 2 * tg + (x & 1) >= live) p[m][x] = -INFINITY;
+      }
+      // ---- weights 2^(s - mref).  mref stays until a score passes it by 14, then becomes the maximum less 6: the largest
+      // weight is in [2^6, 2^14], so that the lo terms of all that matter are ordinary f16 numbers
+      bool grow = false;
+      float top[MT];
+#pragma unroll
+      for (int m = 0; m < MT; m++) {
+        top[m] = fmaxf(fmaxf(p[m][0], p[m][1]), fmaxf(p[m][2], p[m][3])) * cs[m];
+        grow = grow || top[m] > mref[m] + 14.f;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        float f[MT];
+#pragma unroll
+        for (int m = 0; m < MT; m++) {
+          float x = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          const float to = x > mref[m] + 14.f ? x - 6.f : mref[m];
+          f[m] = to > mref[m] ? kv4_ex2(mref[m] - to) : 1.f;
+          mref[m] = to;
+          l[m] *= f[m];
+        }
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+          O[i][0] *= f[0]; O[i][1] *= f[0];
+          O[i][2] *= f[MT - 1]; O[i][3] *= f[MT - 1];
+        }
+      }
+      uint32_t pa[MT][4];
+#pragma unroll
+      for (int m = 0; m < MT; m++) {
+#pragma unroll
+        for (int x = 0; x < 4; x++) p[m][x] = kv4_ex2(fmaf(p[m][x], cs[m], -mref[m]));
+        l[m] += (p[m][0] + p[m][1]) + (p[m][2] + p[m][3]);
+      }
+      if (MT == 1) {      // rows gi: hi, rows gi + 8: lo
+        kv4_split(p[0][0], p[0][1], pa[0][0], pa[0][1]);
+        kv4_split(p[0][2], p[0][3], pa[0][2], pa[0][3]);
+      } else {            // product 0: hi of heads gi and gi + 8, product 1: lo
+        kv4_split(p[0][0], p[0][1], pa[0][0], pa[MT - 1][0]);
+        kv4_split(p[0][2], p[0][3], pa[0][2], pa[MT - 1][2]);
+        kv4_split(p[MT - 1][0], p[MT - 1][1], pa[0][1], pa[MT - 1][1]);
+        kv4_split(p[MT - 1][2], p[MT - 1][3], pa[0][3], pa[MT - 1][3]);
+      }
+
+      // ---- weighted values
+      {
+        uint32_t vw[2][NG], vs[2][NG];
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+          kv4_words<NG>(base + L::kV + (r * 32 + lane) * (4 * NG), vw[r]);
+          kv4_words<NG>(base + L::kVS + (r * 4 + tg) * (4 * NG), vs[r]);
+        }
+        __syncwarp();
+        issue();   // the chunk is in registers: its stage takes the next one
+        if (live < kKv4Chunk) {   // positions behind the end: scale 0, whatever the page holds there
+#pragma unroll
+          for (int r = 0; r < 2; r++) {
+            const uint32_t keep = (8 * r + 2 * tg < live ? 0xffffu : 0u) | (8 * r + 2 * tg + 1 < live ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int j = 0; j < NG; j++) vs[r][j] &= keep;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+          uint32_t b[2][4];
+#pragma unroll
+          for (int r = 0; r < 2; r++) kv4_decode(vw[r][j], vs[r][j], kv4_h2mul(vs[r][j], kMinus72), b[r]);
+#pragma unroll
+          for (int x = 0; x < 4; x++)
+#pragma unroll
+            for (int m = 0; m < MT; m++) kv4_mma(O[4 * j + x], pa[m], b[0][x], b[1][x]);
+        }
+      }
+    }
+
+    // ---- the end of the segment: this lane's rows, dimensions 32 j + 8 tg + 0..7
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      l[m] += __shfl_xor_sync(0xffffffffu, l[m], 1);
+      l[m] += __shfl_xor_sync(0xffffffffu, l[m], 2);
+      if (poison) l[m] = NAN;
+    }
+    const bool whole = ci0 == 0 && seg == nch;
+    const int slot = 2 * warp + (ci0 > 0 ? 0 : 1);
+    float* po = slots + slot * Cfg::kPartFloats;
+    if (!whole && lane == 0) slot_item[slot] = int64_t(e) * c.n_kv + g;
+#pragma unroll
+    for (int m = 0; m < MT; m++) {
+      const int h = gi + 8 * m;
+      float v[NG][8];
+#pragma unroll
+      for (int j = 0; j < NG; j++)
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+          const float* o = O[4 * j + x];
+          v[j][x] = MT == 1 ? o[0] + o[2] : o[2 * m];
+          v[j][x + 4] = MT == 1 ? o[1] + o[3] : o[2 * m + 1];
+        }
+      if (whole) {
+        if (h < G) kv4_store_row<NG>(a.out + int64_t(e) * a.out_stride + (int64_t(g) * G + h) * HD, tg, v, 1.f / l[m]);
       } else {
-        ks[p][d] = vs[p][d] = 0.f;
-      }
-    }
-    __syncthreads();
-    if (t < 16 * G) {
-      float x = 0.f;
-      for (int d = 0; d < HD; d++) x = fmaf(q[(t / 16) * HD + d], ks[t % 16][d], x);
-      ps[t / 16][t % 16] = t % 16 < live ? x * scale : -INFINITY;
-    }
-    __syncthreads();
-    if (t < G) {
-      float m = ml[t][0];
-      for (int p = 0; p < 16; p++) m = fmaxf(m, ps[t][p]);
-      const float w = expf(ml[t][0] - m);
-      float l = ml[t][1] * w;
-      for (int p = 0; p < 16; p++) l += (ps[t][p] = expf(ps[t][p] - m));
-      corr[t] = w;
-      ml[t][0] = m;
-      ml[t][1] = l;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int e = 0; e < 16 * HD / 256; e++) {
-      const int h = (t + 256 * e) / HD, d = (t + 256 * e) % HD;
-      if (h < G) {
-        acc[e] *= corr[h];
-        for (int p = 0; p < 16; p++) acc[e] = fmaf(ps[h][p], vs[p][d], acc[e]);
+        kv4_store_row<NG>(po + h * HD, tg, v, 1.f);
+        if (tg == 0) reinterpret_cast<float2*>(po + ROWS * HD)[h] = make_float2(mref[m], l[m]);
       }
     }
   }
+
+  if (dead)   // copies still in flight land before the CTA's shared memory is given up
+    for (int x = issued > S ? issued - S : 0; x < issued; x++) kv4_bar_wait(bars + (x % S) * 8, uint32_t(x / S) & 1u);
+
+  // ---- merge within the CTA: slots of the same item follow one another
   __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 16 * HD / 256; e++) {
-    const int h = (t + 256 * e) / HD, d = (t + 256 * e) % HD;
-    if (h < G) oi[h * HD + d] = poison ? NAN : (len ? acc[e] / ml[h][1] : 0.f);
+  for (int a0 = 0; a0 < 2 * NW;) {
+    const int64_t item = slot_item[a0];
+    if (item < 0) { a0++; continue; }
+    int a1 = a0 + 1;
+    while (a1 < 2 * NW && (slot_item[a1] < 0 || slot_item[a1] == item)) a1++;
+    const int e = int(item / c.n_kv), g = int(item % c.n_kv);
+    const int64_t nch = (prefix[e + 1] - prefix[e]) / c.n_kv, first = prefix[e] + g * nch;
+    const bool whole = first >= c0 && first + nch <= c1;
+    float* part = a.part + (int64_t(blockIdx.x) * 2 + (first < c0 ? 0 : 1)) * Cfg::kPartFloats;
+    for (int x = t; x < G * HD; x += Cfg::kThreads) {
+      const int h = x / HD;
+      float M = -INFINITY;
+      for (int w = a0; w < a1; w++)
+        if (slot_item[w] == item) M = fmaxf(M, slots[w * Cfg::kPartFloats + ROWS * HD + 2 * h]);
+      float sum = 0.f, o = 0.f;
+      for (int w = a0; w < a1; w++)
+        if (slot_item[w] == item) {
+          const float* ps = slots + w * Cfg::kPartFloats;
+          const float f = kv4_ex2(ps[ROWS * HD + 2 * h] - M);
+          sum = fmaf(ps[ROWS * HD + 2 * h + 1], f, sum);
+          o = fmaf(ps[x], f, o);
+        }
+      if (whole) {
+        a.out[int64_t(e) * a.out_stride + int64_t(g) * G * HD + x] = o / sum;
+      } else {
+        part[x] = o;
+        if (x % HD == 0) reinterpret_cast<float2*>(part + ROWS * HD)[h] = make_float2(M, sum);
+      }
+    }
+    a0 = a1;
   }
+}
+
+// Items that several CTAs worked on, and empty or unreadable ones: one CTA per
+// (entry, kv head, query head), a thread per dimension.
+template <int HD>
+__global__ void __launch_bounds__(HD) k_kv4_attn_merge(Kv4 c, Kv4AttnArgs a, int part_floats) {
+  __shared__ int64_t s_sum[2][HD / 32];
+  __shared__ float2 s_ml[kKv4AttnMaxCtas];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int e = blockIdx.x, g = blockIdx.y / a.G, h = blockIdx.y % a.G;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  uint32_t bad = 0;
+  const int nch = kv4_entry_chunks(c, a, e, &bad);
+  float* out = a.out + int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + t;
+  if (nch == 0) {
+    *out = bad ? NAN : 0.f;
+    return;
+  }
+  int64_t before = 0, all = 0;
+  for (int i = t; i < a.n; i += HD) {
+    uint32_t b;
+    const int x = kv4_entry_chunks(c, a, i, &b);
+    all += x;
+    if (i < e) before += x;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) { s_sum[0][warp] = before; s_sum[1][warp] = all; }
+  __syncthreads();
+  before = all = 0;
+#pragma unroll
+  for (int w = 0; w < HD / 32; w++) { before += s_sum[0][w]; all += s_sum[1][w]; }
+  const int64_t first = before * c.n_kv + int64_t(g) * nch, per = kv4_share(all * c.n_kv, a) * a.warps;
+  const int b0 = int(first / per), b1 = int((first + nch - 1) / per);   // CTAs that worked on it
+  if (b0 == b1) return;
+  auto record = [&](int b) { return a.part + (int64_t(b) * 2 + (b == b0 ? (first < b * per ? 0 : 1) : 0)) * part_floats; };
+  const int rows = (part_floats) / (HD + 2);
+  for (int b = b0 + t; b <= b1; b += HD) s_ml[b - b0] = reinterpret_cast<const float2*>(record(b) + rows * HD)[h];
+  __syncthreads();
+  float M = -INFINITY;
+  for (int b = 0; b <= b1 - b0; b++) M = fmaxf(M, s_ml[b].x);
+  float sum = 0.f, o = 0.f;
+#pragma unroll 8
+  for (int b = 0; b <= b1 - b0; b++) {
+    const float f = kv4_ex2(s_ml[b].x - M);
+    sum = fmaf(s_ml[b].y, f, sum);
+    o = fmaf(record(b + b0)[h * HD + t], f, o);
+  }
+  *out = o / sum;
+}
+
+template <int HD, int MT>
+static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_chunks, cudaStream_t s) {
+  using Cfg = Kv4AttnCfg<HD, MT>;
+  static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, MT>, Cfg::kSmem);
+  if (setup.err != cudaSuccess) return setup.err;
+  const int64_t useful = (most_chunks + Cfg::NW * kKv4MinChunks - 1) / (Cfg::NW * kKv4MinChunks);
+  int64_t ctas = setup.sms < kKv4AttnMaxCtas ? setup.sms : kKv4AttnMaxCtas;
+  if (ctas > useful) ctas = useful;
+  a.ctas = int(ctas);
+  a.warps = Cfg::NW;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(Cfg::kThreads);
+  cfg.dynamicSmemBytes = Cfg::kSmem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, MT>, k, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(unsigned(a.n), unsigned(k.n_kv * a.G));
+  cfg.blockDim = dim3(HD);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, k_kv4_attn_merge<HD>, k, a, int(Cfg::kPartFloats));
 }
 
 }  // namespace nt
@@ -105,6 +675,8 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
   const int G = n_heads / k.n_kv;
   if (G != 1 && G != 2 && G != 4 && G != 8 && G != 16)
     return fail(NT_E_UNSUPPORTED, "nt_attention_kv4: query heads per kv head must be 1, 2, 4, 8 or 16");
+  if (int64_t(k.n_pages) * k.n_kv * (k.page_len / kKv4Chunk) > 0x7fffffffLL) return bad("a layer of the pool has more than 2^31 - 1 chunks");
+  if (n_heads > 65535) return bad("n_heads above 65535");
   if (n < 0 || n > 65536 || (!dev_seq && n > k.max_seqs)) return bad("n out of range");
   const int64_t row = int64_t(n_heads) * k.hd;
   if (q_stride < row || out_stride < row || q_stride % 4 || out_stride % 4 || q_stride > (int64_t(1) << 40) ||
@@ -123,12 +695,29 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
       (dev_seq && (kv4_overlap(dev_seq, int64_t(n) * 4, dev_out, ob) ||
                    kv4_overlap(dev_seq, int64_t(n) * 4, dev_workspace, int64_t(wb)))))
     return bad("the output or the workspace overlaps another buffer");
-  const Kv4AttnArgs a{layer, n_heads, n, dev_seq, dev_q, q_stride, dev_out, out_stride};
+  Kv4AttnArgs a{};
+  a.layer = layer;
+  a.G = G;
+  a.scale_log2 = 1.4426950408889634f / sqrtf(float(k.hd));
+  a.part = static_cast<float*>(dev_workspace);
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  const int64_t entry_chunks = int64_t(k.n_kv) * ((int64_t(k.max_pages) * k.page_len) / kKv4Chunk);
+  // a launch's chunks are counted in 64 bits, a warp's share of them in 32
+  const int64_t most = int64_t(1) << 40;
+  if (entry_chunks > most) return bad("n_kv_heads * max_pages * page_len above 2^44");
+  const int32_t batch = entry_chunks * kKv4Batch <= most ? kKv4Batch : int32_t(most / entry_chunks);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid{unsigned(n), unsigned(k.n_kv)};
-  const float scale = 1.0f / sqrtf(float(k.hd));
-  if (k.hd == 64) k_kv4_attn<64><<<grid, 256, 0, s>>>(k, a, G, scale);
-  else k_kv4_attn<128><<<grid, 256, 0, s>>>(k, a, G, scale);
-  NT_CUDA(cudaGetLastError());
+  for (int32_t i = 0; i < n; i += batch) {
+    a.n = n - i < batch ? n - i : batch;
+    a.seq0 = i;
+    a.seq = dev_seq ? dev_seq + i : nullptr;
+    a.q = dev_q + int64_t(i) * q_stride;
+    a.out = dev_out + int64_t(i) * out_stride;
+    cudaError_t e;
+    if (k.hd == 64) e = G <= 8 ? kv4_launch_attn<64, 1>(k, a, a.n * entry_chunks, s) : kv4_launch_attn<64, 2>(k, a, a.n * entry_chunks, s);
+    else e = G <= 8 ? kv4_launch_attn<128, 1>(k, a, a.n * entry_chunks, s) : kv4_launch_attn<128, 2>(k, a, a.n * entry_chunks, s);
+    if (e != cudaSuccess) return cuda_fail(e, "nt_attention_kv4");
+  }
   return NT_OK;
 }
