@@ -27,9 +27,9 @@
 
 namespace nt {
 
-constexpr int kKv4Batch = 1024;        // sequences of one launch: their chunk offsets are kept in shared memory
+constexpr int kKv4Batch = 1024;        // sequences of one launch: their pair offsets are kept in shared memory
 constexpr int kKv4AttnMaxCtas = 152;   // one CTA per SM; the workspace holds two partial results of each
-constexpr int kKv4MinChunks = 2;       // fewest chunks of a warp: below, fewer CTAs work
+constexpr int kKv4MinPairs = 1;        // fewest pairs of chunks of a warp: below, fewer CTAs work
 
 struct Kv4AttnArgs {
   int32_t layer, n, G;
@@ -40,30 +40,36 @@ struct Kv4AttnArgs {
   float* out;
   int64_t out_stride;
   float scale_log2;                    // log2(e) / sqrt(hd)
-  float* part;                         // [CTA][2] partial results: see Kv4Part
-  int32_t ctas, warps;                 // of the attention kernel
+  float* part;                         // [CTA][2] partial results
 };
+
+// Partial result of one item: o [rows][HD], then (reference m, sum l) per row, then
+// a header of 4 words (used by the CTAs' slot 1: the item, -1 none, and the
+// number of CTAs that worked on it).
+__host__ __device__ constexpr int kv4_part_floats(int hd, int rows) { return rows * hd + 2 * rows + 4; }
 
 template <int HD, int MT>
 struct Kv4AttnCfg {
   static constexpr int NW = MT == 1 ? (HD == 128 ? 12 : 16) : (HD == 128 ? 8 : 12);   // warps: registers decide
-  static constexpr int S = HD == 128 ? 4 : 6;                                          // ring stages of a warp
+  static constexpr int S = HD == 128 && MT == 1 ? 3 : 4;                               // ring stages of a warp
   static constexpr int kThreads = 32 * NW;
   static constexpr int kRows = 8 * MT;                                                 // heads of a partial result
-  // partial result: o [kRows][HD], then (reference m, sum l) per head
-  static constexpr int kPartFloats = kRows * HD + 2 * kRows;
+  static constexpr int kPart = kv4_part_floats(HD, kRows);
+  static constexpr int kPair = 2 * kv4_chunk_bytes(HD);                                // a stage: two chunks
   static constexpr int kRing = 0;
-  static constexpr int kSlots = kRing + NW * S * kv4_chunk_bytes(HD);
-  static constexpr int kPrefix = kSlots + 2 * NW * kPartFloats * 4;
+  static constexpr int kSlots = kRing + NW * S * kPair;                                // a slot of each warp (see below)
+  static constexpr int kPrefix = kSlots + NW * kPart * 4;
   static constexpr int kBars = kPrefix + (kKv4Batch + 1) * 8;
   static constexpr int kItem = kBars + NW * S * 8;                                     // item of each slot (-1: none)
-  static constexpr int kSmem = kItem + 2 * NW * 8 + 64;
+  static constexpr int kWeight = kItem + 2 * NW * 4;                                   // [2 NW][kRows] merge weights
+  static constexpr int kSmem = kWeight + 2 * NW * kRows * 4;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
+  static_assert(kPart * 4 <= S * kPair && kPart % 4 == 0, "a warp's ring holds a partial result");
+  static_assert(2 * NW <= 32, "a lane per slot");
 };
 
 size_t kv4_attn_ws_bytes(int n_heads, int n_kv, int hd) {
-  const int rows = n_heads / n_kv > 8 ? 16 : 8;
-  return size_t(kKv4AttnMaxCtas) * 2 * (size_t(rows) * hd + 2 * rows) * 4;
+  return size_t(kKv4AttnMaxCtas) * 2 * size_t(kv4_part_floats(hd, n_heads / n_kv > 8 ? 16 : 8)) * 4;
 }
 
 // ------------------------------------------------------------ small pieces --
@@ -110,14 +116,30 @@ __device__ __forceinline__ uint32_t kv4_h2mul(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+__device__ __forceinline__ uint32_t kv4_h2add(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// (w & mask) | magic
+template <uint32_t mask>
+__device__ __forceinline__ uint32_t kv4_pick(uint32_t w, uint32_t magic) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(mask), "r"(magic));
+  return d;
+}
 // The four half2 of a word: value pairs (code k, code k + 4), k = 0..3, times the
-// scale pair d; d72 = -72 d.
+// scale pair d; d72 = -72 d.  Codes 1 and 3 stand (3 after a shift) in bits 4..7:
+// 64 + q, and one multiply-add.  Codes 0 and 2 stand in bits 0..3: 1024 + q, less
+// 1032, times d, three exact steps as well; two more shifts would spare one of
+// them but the logic pipe, at half the rate, is the busier one.
 __device__ __forceinline__ void kv4_decode(uint32_t w, uint32_t d, uint32_t d72, uint32_t (&b)[4]) {
-  constexpr uint32_t kMask = 0x00f000f0u, k64 = 0x54005400u;
-  b[0] = kv4_h2fma(((w << 4) & kMask) | k64, d, d72);
-  b[1] = kv4_h2fma((w & kMask) | k64, d, d72);
-  b[2] = kv4_h2fma(((w >> 4) & kMask) | k64, d, d72);
-  b[3] = kv4_h2fma(((w >> 8) & kMask) | k64, d, d72);
+  constexpr uint32_t k64 = 0x54005400u, k1024 = 0x64006400u, kMinus1032 = 0xe408e408u;
+  const uint32_t u = w >> 8;
+  b[0] = kv4_h2mul(kv4_h2add(kv4_pick<0x000f000fu>(w, k1024), kMinus1032), d);
+  b[1] = kv4_h2fma(kv4_pick<0x00f000f0u>(w, k64), d, d72);
+  b[2] = kv4_h2mul(kv4_h2add(kv4_pick<0x000f000fu>(u, k1024), kMinus1032), d);
+  b[3] = kv4_h2fma(kv4_pick<0x00f000f0u>(u, k64), d, d72);
 }
 constexpr uint32_t kMinus72 = 0xd480d480u;   // f16 -72 twice
 
@@ -140,9 +162,11 @@ __device__ __forceinline__ void kv4_mma(float (&d)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ void kv4_bar_init(uint32_t bar) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
 }
-// One chunk from global to shared memory, counted on bar.
-__device__ __forceinline__ void kv4_copy_chunk(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+__device__ __forceinline__ void kv4_bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Chunks from global to shared memory, their bytes counted on bar.
+__device__ __forceinline__ void kv4_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
                : "memory");
@@ -166,20 +190,15 @@ __device__ __forceinline__ bool kv4_bar_wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-// Chunks of listed entry e (0: nothing to read); *bad: error bits of an entry that cannot be read.
-__device__ __forceinline__ int kv4_entry_chunks(const Kv4& c, const Kv4AttnArgs& a, int e, uint32_t* bad) {
+// Pairs of chunks (32 positions) of listed entry e (0: nothing to read); *bad:
+// error bits of an entry that cannot be read.
+__device__ __forceinline__ int kv4_entry_pairs(const Kv4& c, const Kv4AttnArgs& a, int e, uint32_t* bad) {
   const int s = a.seq ? a.seq[e] : a.seq0 + e;
   if (s < 0 || s >= c.max_seqs) { *bad = NT_KV4_BAD_SEQ; return 0; }
   const int n = c.len[s];
   if (n < 0 || n > c.capacity()) { *bad = NT_KV4_BAD_LEN; return 0; }
   *bad = 0;
-  return (n + kKv4Chunk - 1) / kKv4Chunk;
-}
-
-// Chunks of a warp when `total` are shared out.
-__device__ __forceinline__ int64_t kv4_share(int64_t total, const Kv4AttnArgs& a) {
-  const int64_t warps = int64_t(a.ctas) * a.warps, per = (total + warps - 1) / warps;
-  return per < kKv4MinChunks ? kKv4MinChunks : per;
+  return (n + 2 * kKv4Chunk - 1) / (2 * kKv4Chunk);
 }
 
 // Entry of prefix (ascending, prefix[0] = 0) that holds chunk x: prefix[i] <= x < prefix[i + 1].
@@ -205,13 +224,17 @@ __device__ __forceinline__ void kv4_store_row(float* o, int tg, const float (&v)
 
 // ------------------------------------------------------------ the kernel --
 
-// All chunks of all (entry, kv head) items in a row, item after item, are shared
-// out evenly: warp w of CTA b takes chunks [(b NW + w) C, (b NW + w + 1) C).  An
-// item that lies within a warp's share is finished by it; one that lies within a
-// CTA's is merged in shared memory; the rest leaves partial results (at most two
-// a CTA: of an item begun before it and of one that goes on behind it) to
-// k_kv4_attn_merge.  Partial results are merged in the order of the positions, so
-// the result does not depend on timing.
+// The chunk pairs of all (entry, kv head) items in a row, item after item, are
+// shared out evenly: warp w of CTA b takes pairs [(b NW + w) C, (b NW + w + 1) C).
+// An item that lies within a warp's share is finished by it; one that lies within
+// a CTA's is merged in shared memory; the rest leaves partial results (at most two
+// a CTA: slot 0 of an item begun before it, slot 1 of one that goes on behind it)
+// to k_kv4_attn_merge.  Partial results are merged in the order of the positions,
+// so the result does not depend on timing.
+//
+// A warp leaves at most two partial results to the CTA: of the item it did not
+// begin (slot 2 warp, in memory of its own) and of the one it did not end (slot
+// 2 warp + 1, its last: it stands in the warp's ring, which is empty by then).
 template <int HD, int MT>
 __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv4 c, Kv4AttnArgs a) {
   using Cfg = Kv4AttnCfg<HD, MT>;
@@ -219,20 +242,22 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
   constexpr int NW = Cfg::NW, S = Cfg::S, NG = HD / 32, NT = HD / 8, CB = L::kBytes, ROWS = Cfg::kRows;
   extern __shared__ __align__(128) uint8_t sm[];
   int64_t* prefix = reinterpret_cast<int64_t*>(sm + Cfg::kPrefix);
-  float* slots = reinterpret_cast<float*>(sm + Cfg::kSlots);
-  int64_t* slot_item = reinterpret_cast<int64_t*>(sm + Cfg::kItem);
+  int* slot_item = reinterpret_cast<int*>(sm + Cfg::kItem);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, gi = lane >> 2, tg = lane & 3;
   const int G = a.G, n = a.n;
+  auto slot_ptr = [&](int w) {
+    return reinterpret_cast<float*>(w & 1 ? sm + Cfg::kRing + (w >> 1) * (S * Cfg::kPair) : sm + Cfg::kSlots + (w >> 1) * (Cfg::kPart * 4));
+  };
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // ---- chunk offsets of the entries (an entry's chunks are counted once per kv head)
+  // ---- pair offsets of the entries (an entry's pairs are counted once per kv head)
   {
     int64_t* sums = reinterpret_cast<int64_t*>(sm + Cfg::kSlots);   // per-warp sums, before the slots are used
     int64_t run = 0;
     for (int e0 = 0; e0 < n; e0 += Cfg::kThreads) {
       const int e = e0 + t;
       uint32_t bad = 0;
-      int64_t x = e < n ? int64_t(kv4_entry_chunks(c, a, e, &bad)) : 0;
+      int64_t x = e < n ? int64_t(kv4_entry_pairs(c, a, e, &bad)) : 0;
       if (bad && blockIdx.x == 0) kv4_flag(c, bad);
       const int64_t mine = x;
 #pragma unroll
@@ -258,46 +283,78 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
   }
-  const int64_t total = prefix[n], share = kv4_share(total, a);
-  const int64_t c0 = int64_t(blockIdx.x) * NW * share;   // the CTA's first chunk
+  // the entries without a position: zeros, or NaN where they cannot be read
+  for (int e = blockIdx.x; e < n; e += gridDim.x) {
+    if (prefix[e + 1] != prefix[e]) continue;
+    uint32_t bad = 0;
+    kv4_entry_pairs(c, a, e, &bad);
+    for (int x = t; x < c.n_kv * G * HD; x += Cfg::kThreads) a.out[int64_t(e) * a.out_stride + x] = bad ? NAN : 0.f;
+  }
+  const int64_t total = prefix[n], warps = int64_t(gridDim.x) * NW;
+  int64_t share = (total + warps - 1) / warps;
+  if (share < kKv4MinPairs) share = kKv4MinPairs;
+  const int64_t c0 = int64_t(blockIdx.x) * NW * share;   // the CTA's first pair
   int64_t c1 = c0 + NW * share;
   if (c1 > total) c1 = total;
+  float* part0 = a.part + int64_t(blockIdx.x) * 2 * Cfg::kPart;
+  int* header = reinterpret_cast<int*>(part0 + 2 * Cfg::kPart - 4);   // of slot 1
+  if (t == 0) header[0] = -1;
   asm volatile("griddepcontrol.launch_dependents;");
   if (c0 >= total) return;   // the whole CTA
 
   const int64_t w0 = c0 + warp * share;
   const int count = w0 >= c1 ? 0 : int(w0 + share > c1 ? c1 - w0 : share);
-  const uint32_t ring = kv4_smem(sm + Cfg::kRing) + uint32_t(warp) * S * CB;
+  const uint32_t ring = kv4_smem(sm + Cfg::kRing) + uint32_t(warp) * (S * Cfg::kPair);
   const uint32_t bars = kv4_smem(sm + Cfg::kBars) + uint32_t(warp) * S * 8;
   const int cpp = c.page_len / kKv4Chunk;
-
-  // index of chunk x of this warp within its layer's pool (in chunks), -1: no such page
-  auto resolve = [&](int x) -> int {
-    if (x >= count) return -1;
-    const int64_t y = w0 + x;
-    const int e = kv4_find(prefix, n, y);
-    const int nch = int((prefix[e + 1] - prefix[e]) / c.n_kv), rem_g = int((y - prefix[e]) / nch);
-    const int ci = int(y - prefix[e] - int64_t(rem_g) * nch);
-    const int s = a.seq ? a.seq[e] : a.seq0 + e;
-    const int page = c.table[int64_t(s) * c.max_pages + ci / cpp];
-    if (page < 0 || page >= c.n_pages) { kv4_flag(c, NT_KV4_BAD_PAGE); return -1; }
-    return int((int64_t(page) * c.n_kv + rem_g) * cpp + ci % cpp);
-  };
   const uint8_t* layer_pool = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes();
 
-  int addr = resolve(lane), addr_next = -1;   // of chunks 32 b + lane and the 32 behind
-  int issued = 0;
-  uint32_t missing = 0;                       // stages whose chunk has no page
+  // the item of pair y: entry e, kv head g, pair pi of np
+  auto locate = [&](int64_t y, int& e, int& g, int& pi, int& np) {
+    e = kv4_find(prefix, n, y);
+    np = int((prefix[e + 1] - prefix[e]) / c.n_kv);
+    const int64_t r = y - prefix[e];
+    g = int(r / np);
+    pi = int(r - int64_t(g) * np);
+  };
+  // indexes of the two chunks of pair x of this warp within the layer's pool (in
+  // chunks); -1: no page, -2: behind the sequence's end
+  auto resolve = [&](int x) -> int2 {
+    if (x >= count) return make_int2(-2, -2);
+    int e, g, pi, np;
+    locate(w0 + x, e, g, pi, np);
+    const int s = a.seq ? a.seq[e] : a.seq0 + e, len = c.len[s];
+    const int32_t* row = c.table + int64_t(s) * c.max_pages;
+    auto chunk = [&](int ci) -> int {
+      if (ci * kKv4Chunk >= len) return -2;
+      const int page = row[ci / cpp];
+      if (page < 0 || page >= c.n_pages) { kv4_flag(c, NT_KV4_BAD_PAGE); return -1; }
+      return int((int64_t(page) * c.n_kv + g) * cpp + ci % cpp);
+    };
+    return make_int2(chunk(2 * pi), chunk(2 * pi + 1));
+  };
+
+  int2 addr = resolve(lane), addr_next = make_int2(-2, -2);   // of pairs 32 b + lane and the 32 behind
+  int issued = 0, ist = 0;                    // pairs issued, stage of the next
+  uint32_t missing = 0;                       // stages that lack a page
   bool dead = false;                          // a wait ran out: nothing more is copied or read
   auto issue = [&]() {
     if (issued < count && !dead) {
-      const int x = __shfl_sync(0xffffffffu, addr, issued & 31), st = issued % S;
-      missing = x < 0 ? missing | (1u << st) : missing & ~(1u << st);
+      const int x0 = __shfl_sync(0xffffffffu, addr.x, issued & 31), x1 = __shfl_sync(0xffffffffu, addr.y, issued & 31);
+      const uint32_t dst = ring + ist * Cfg::kPair, bar = bars + ist * 8;
+      const bool lacks = x0 < 0 || x1 == -1;
+      missing = lacks ? missing | (1u << ist) : missing & ~(1u << ist);
       if (lane == 0) {
-        if (x >= 0) kv4_copy_chunk(ring + st * CB, layer_pool + int64_t(x) * CB, CB, bars + st * 8);
-        else kv4_bar_arrive(bars + st * 8);
+        if (lacks) {
+          kv4_bar_arrive(bar);
+        } else {
+          kv4_bar_expect(bar, x1 < 0 ? CB : 2 * CB);
+          kv4_copy(dst, layer_pool + int64_t(x0) * CB, x1 == x0 + 1 ? 2 * CB : CB, bar);
+          if (x1 >= 0 && x1 != x0 + 1) kv4_copy(dst + CB, layer_pool + int64_t(x1) * CB, CB, bar);
+        }
       }
       issued++;
+      ist = ist + 1 == S ? 0 : ist + 1;
       if ((issued & 31) == 16) addr_next = resolve((issued & ~31) + 32 + lane);
       if ((issued & 31) == 0) addr = addr_next;
     }
@@ -308,16 +365,16 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
   float O[NT][4];
   uint32_t qa[MT][HD / 16][4];
   float mref[MT], l[MT], cs[MT];
-  int k = 0;                                  // chunks read
+  int k = 0, st = 0;                          // pairs read, stage of the next
+  uint32_t parity = 0;
+#pragma unroll 1
   while (k < count) {
-    // ---- a segment: consecutive chunks of one item
-    const int64_t y = w0 + k;
-    const int e = kv4_find(prefix, n, y);
-    const int nch = int((prefix[e + 1] - prefix[e]) / c.n_kv), g = int((y - prefix[e]) / nch);
-    const int ci0 = int(y - prefix[e] - int64_t(g) * nch);
-    const int seg = nch - ci0 < count - k ? nch - ci0 : count - k;
+    // ---- a segment: consecutive pairs of one item
+    int e, g, pi0, np;
+    locate(w0 + k, e, g, pi0, np);
+    const int seg = np - pi0 < count - k ? np - pi0 : count - k;
     const int s = a.seq ? a.seq[e] : a.seq0 + e;
-    const int len = c.len[s];
+    int live = c.len[s] - pi0 * 2 * kKv4Chunk;   // positions from the pair on that exist
     bool poison = false;
     {
       // q of heads gi (and gi + 8), scaled so that the largest element is in [2^10, 2^11), split
@@ -331,8 +388,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
         for (int j = 0; j < NG; j++) {
           float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
           if (h < G) {
-            u = __ldg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg));
-            v = __ldg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg) + 1);
+            u = __ldcg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg));
+            v = __ldcg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg) + 1);
           }
           x[m][j][0] = u.x; x[m][j][1] = u.y; x[m][j][2] = u.z; x[m][j][3] = u.w;
           x[m][j][4] = v.x; x[m][j][5] = v.y; x[m][j][6] = v.z; x[m][j][7] = v.w;
@@ -363,42 +420,46 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
           }
         }
 #pragma unroll
-      for (int m = 0; m < MT; m++) { mref[m] = -INFINITY; l[m] = 0.f; }
+      for (int m = 0; m < MT; m++) { mref[m] = -3e38f; l[m] = 0.f; }
 #pragma unroll
       for (int i = 0; i < NT; i++) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
     }
 
 #pragma unroll 1
-    for (int ci = ci0; ci < ci0 + seg; ci++, k++) {
-      const int st = k % S;
-      if (!dead && !kv4_bar_wait(bars + st * 8, uint32_t(k / S) & 1u)) {
+    for (const int k1 = k + seg; k < k1; k++, live -= 2 * kKv4Chunk) {
+      if (!__all_sync(0xffffffffu, dead || kv4_bar_wait(bars + st * 8, parity)) && !dead) {
         dead = true;
         if (lane == 0) kv4_flag(c, NT_KV4_TIMEOUT);
+        for (int y = k; y < issued; y++) {   // copies in flight land before anything else happens to the ring
+          const int at = st + y - k;
+          kv4_bar_wait(bars + (at < S ? at : at - S) * 8, at < S ? parity : parity ^ 1u);
+        }
       }
-      dead = __any_sync(0xffffffffu, dead);
-      if (dead || (missing >> st & 1u)) {
+      const uint32_t base = ring + st * Cfg::kPair;
+      const bool lacks = dead || (missing >> st & 1u);
+      st++;
+      if (st == S) { st = 0; parity ^= 1u; }
+      if (lacks) {
         poison = true;
-        __syncwarp();
         issue();
         continue;
       }
-      const uint32_t base = ring + st * CB;
-      const int live = len - ci * kKv4Chunk;       // positions of this chunk that exist (16 or more: all)
 
-      // ---- scores of 16 positions
-      float sc[2][4];
+      // ---- scores of 32 positions
+      float sc[4][4];
 #pragma unroll
-      for (int i = 0; i < 2; i++) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
-      {
+      for (int i = 0; i < 4; i++) sc[i][0] = sc[i][1] = sc[i][2] = sc[i][3] = 0.f;
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
         uint32_t kw[2][NG], ks[2][NG / 2];
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-          kv4_words<NG>(base + (i * 32 + lane) * (4 * NG), kw[i]);
+          kv4_words<NG>(base + u * CB + (i * 32 + lane) * (4 * NG), kw[i]);
           if (NG == 4) {
-            const uint2 v = kv4_lds8(base + L::kKS + (8 * i + gi) * (2 * NG));
+            const uint2 v = kv4_lds8(base + u * CB + L::kKS + (8 * i + gi) * (2 * NG));
             ks[i][0] = v.x; ks[i][NG / 2 - 1] = v.y;
           } else {
-            ks[i][0] = kv4_lds4(base + L::kKS + (8 * i + gi) * (2 * NG));
+            ks[i][0] = kv4_lds4(base + u * CB + L::kKS + (8 * i + gi) * (2 * NG));
           }
         }
 #pragma unroll
@@ -410,48 +471,56 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
             kv4_decode(kw[i][j], d, d72, b);
 #pragma unroll
             for (int m = 0; m < MT; m++) {
-              kv4_mma(sc[i], qa[m][2 * j], b[0], b[1]);
-              kv4_mma(sc[i], qa[m][2 * j + 1], b[2], b[3]);
+              kv4_mma(sc[2 * u + i], qa[m][2 * j], b[0], b[1]);
+              kv4_mma(sc[2 * u + i], qa[m][2 * j + 1], b[2], b[3]);
             }
           }
       }
-      // the positions' scores of this lane's heads: 2 tg, 2 tg + 1, 8 + 2 tg, 8 + 2 tg + 1
-      float p[MT][4];
+      // the scores of this lane's heads at positions 8 i + 2 tg and 8 i + 2 tg + 1, i < 4
+      float x[MT][8];
 #pragma unroll
-      for (int i = 0; i < 2; i++)
+      for (int i = 0; i < 4; i++)
 #pragma unroll
-        for (int x = 0; x < 2; x++) {
+        for (int y = 0; y < 2; y++) {
           if (MT == 1) {
-            p[0][2 * i + x] = sc[i][x] + sc[i][x + 2];
+            x[0][2 * i + y] = sc[i][y] + sc[i][y + 2];
           } else {
-            p[0][2 * i + x] = sc[i][x];
-            p[MT - 1][2 * i + x] = sc[i][x + 2];
+            x[0][2 * i + y] = sc[i][y];
+            x[MT - 1][2 * i + y] = sc[i][y + 2];
           }
         }
-      if (live < kKv4Chunk) {
+      if (live < 2 * kKv4Chunk) {
 #pragma unroll
         for (int m = 0; m < MT; m++)
 #pragma unroll
-          for (int x = 0; x < 4; x++)
-            if (8 * (x >> 1) + 2 * tg + (x & 1) >= live) p[m][x] = -INFINITY;
+          for (int i = 0; i < 8; i++)
+            if (8 * (i >> 1) + 2 * tg + (i & 1) >= live) x[m][i] = -INFINITY;
       }
-      // ---- weights 2^(s - mref).  mref stays until a score passes it by 14, then becomes the maximum less 6: the largest
-      // weight is in [2^6, 2^14], so that the lo terms of all that matter are ordinary f16 numbers
-      bool grow = false;
-      float top[MT];
+      // ---- weights p = 2^(s - mref).  Only where a lane's sum passes 2^15 (at first it is infinite) is the maximum looked
+      // for; where that passes mref by 14, it less 6 becomes mref.  So weights stay below 2^15, within f16, and the largest
+      // so far is at least 2^6: the lo terms of all that matter are ordinary f16 numbers.
+      float p[MT][8], sum[MT];
+      auto weights = [&]() {
 #pragma unroll
-      for (int m = 0; m < MT; m++) {
-        top[m] = fmaxf(fmaxf(p[m][0], p[m][1]), fmaxf(p[m][2], p[m][3])) * cs[m];
-        grow = grow || top[m] > mref[m] + 14.f;
-      }
-      if (__any_sync(0xffffffffu, grow)) {
+        for (int m = 0; m < MT; m++) {
+#pragma unroll
+          for (int i = 0; i < 8; i++) p[m][i] = kv4_ex2(fmaf(x[m][i], cs[m], -mref[m]));
+          sum[m] = ((p[m][0] + p[m][1]) + (p[m][2] + p[m][3])) + ((p[m][4] + p[m][5]) + (p[m][6] + p[m][7]));
+        }
+      };
+      weights();
+      if (__any_sync(0xffffffffu, sum[0] > 32768.f || sum[MT - 1] > 32768.f)) {
         float f[MT];
 #pragma unroll
         for (int m = 0; m < MT; m++) {
-          float x = fmaxf(top[m], __shfl_xor_sync(0xffffffffu, top[m], 1));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-          const float to = x > mref[m] + 14.f ? x - 6.f : mref[m];
-          f[m] = to > mref[m] ? kv4_ex2(mref[m] - to) : 1.f;
+          float top = x[m][0];
+#pragma unroll
+          for (int i = 1; i < 8; i++) top = fmaxf(top, x[m][i]);
+          top *= cs[m];
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const float to = top > mref[m] + 14.f ? top - 6.f : mref[m];
+          f[m] = kv4_ex2(mref[m] - to);
           mref[m] = to;
           l[m] *= f[m];
         }
@@ -460,38 +529,43 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
           O[i][0] *= f[0]; O[i][1] *= f[0];
           O[i][2] *= f[MT - 1]; O[i][3] *= f[MT - 1];
         }
+        weights();
       }
-      uint32_t pa[MT][4];
+      uint32_t pa[2][MT][4];
 #pragma unroll
-      for (int m = 0; m < MT; m++) {
+      for (int m = 0; m < MT; m++) l[m] += sum[m];
 #pragma unroll
-        for (int x = 0; x < 4; x++) p[m][x] = kv4_ex2(fmaf(p[m][x], cs[m], -mref[m]));
-        l[m] += (p[m][0] + p[m][1]) + (p[m][2] + p[m][3]);
-      }
-      if (MT == 1) {      // rows gi: hi, rows gi + 8: lo
-        kv4_split(p[0][0], p[0][1], pa[0][0], pa[0][1]);
-        kv4_split(p[0][2], p[0][3], pa[0][2], pa[0][3]);
-      } else {            // product 0: hi of heads gi and gi + 8, product 1: lo
-        kv4_split(p[0][0], p[0][1], pa[0][0], pa[MT - 1][0]);
-        kv4_split(p[0][2], p[0][3], pa[0][2], pa[MT - 1][2]);
-        kv4_split(p[MT - 1][0], p[MT - 1][1], pa[0][1], pa[MT - 1][1]);
-        kv4_split(p[MT - 1][2], p[MT - 1][3], pa[0][3], pa[MT - 1][3]);
+      for (int u = 0; u < 2; u++) {
+        const int o = 4 * u;
+        if (MT == 1) {      // rows gi: hi, rows gi + 8: lo
+          kv4_split(p[0][o], p[0][o + 1], pa[u][0][0], pa[u][0][1]);
+          kv4_split(p[0][o + 2], p[0][o + 3], pa[u][0][2], pa[u][0][3]);
+        } else {            // product 0: hi of heads gi and gi + 8, product 1: lo
+          kv4_split(p[0][o], p[0][o + 1], pa[u][0][0], pa[u][MT - 1][0]);
+          kv4_split(p[0][o + 2], p[0][o + 3], pa[u][0][2], pa[u][MT - 1][2]);
+          kv4_split(p[MT - 1][o], p[MT - 1][o + 1], pa[u][0][1], pa[u][MT - 1][1]);
+          kv4_split(p[MT - 1][o + 2], p[MT - 1][o + 3], pa[u][0][3], pa[u][MT - 1][3]);
+        }
       }
 
       // ---- weighted values
-      {
+#pragma unroll
+      for (int u = 0; u < 2; u++) {
         uint32_t vw[2][NG], vs[2][NG];
 #pragma unroll
         for (int r = 0; r < 2; r++) {
-          kv4_words<NG>(base + L::kV + (r * 32 + lane) * (4 * NG), vw[r]);
-          kv4_words<NG>(base + L::kVS + (r * 4 + tg) * (4 * NG), vs[r]);
+          kv4_words<NG>(base + u * CB + L::kV + (r * 32 + lane) * (4 * NG), vw[r]);
+          kv4_words<NG>(base + u * CB + L::kVS + (r * 4 + tg) * (4 * NG), vs[r]);
         }
-        __syncwarp();
-        issue();   // the chunk is in registers: its stage takes the next one
-        if (live < kKv4Chunk) {   // positions behind the end: scale 0, whatever the page holds there
+        if (u == 1) {
+          __syncwarp();
+          issue();   // the pair is in registers: its stage takes the next one
+        }
+        if (live < 2 * kKv4Chunk) {   // positions behind the end: scale 0, whatever the page holds there
 #pragma unroll
           for (int r = 0; r < 2; r++) {
-            const uint32_t keep = (8 * r + 2 * tg < live ? 0xffffu : 0u) | (8 * r + 2 * tg + 1 < live ? 0xffff0000u : 0u);
+            const int at = 16 * u + 8 * r + 2 * tg;
+            const uint32_t keep = (at < live ? 0xffffu : 0u) | (at + 1 < live ? 0xffff0000u : 0u);
 #pragma unroll
             for (int j = 0; j < NG; j++) vs[r][j] &= keep;
           }
@@ -502,9 +576,9 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll
           for (int r = 0; r < 2; r++) kv4_decode(vw[r][j], vs[r][j], kv4_h2mul(vs[r][j], kMinus72), b[r]);
 #pragma unroll
-          for (int x = 0; x < 4; x++)
+          for (int y = 0; y < 4; y++)
 #pragma unroll
-            for (int m = 0; m < MT; m++) kv4_mma(O[4 * j + x], pa[m], b[0][x], b[1][x]);
+            for (int m = 0; m < MT; m++) kv4_mma(O[4 * j + y], pa[u][m], b[0][y], b[1][y]);
         }
       }
     }
@@ -516,10 +590,11 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
       l[m] += __shfl_xor_sync(0xffffffffu, l[m], 2);
       if (poison) l[m] = NAN;
     }
-    const bool whole = ci0 == 0 && seg == nch;
-    const int slot = 2 * warp + (ci0 > 0 ? 0 : 1);
-    float* po = slots + slot * Cfg::kPartFloats;
-    if (!whole && lane == 0) slot_item[slot] = int64_t(e) * c.n_kv + g;
+    const bool whole = pi0 == 0 && seg == np;
+    const int slot = 2 * warp + (pi0 > 0 ? 0 : 1);
+    float* po = slot_ptr(slot);
+    if (!whole && lane == 0) slot_item[slot] = e * c.n_kv + g;
+    __syncwarp();   // (slot 1 is the ring: every lane has read its last pair)
 #pragma unroll
     for (int m = 0; m < MT; m++) {
       const int h = gi + 8 * m;
@@ -527,10 +602,10 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll
       for (int j = 0; j < NG; j++)
 #pragma unroll
-        for (int x = 0; x < 4; x++) {
-          const float* o = O[4 * j + x];
-          v[j][x] = MT == 1 ? o[0] + o[2] : o[2 * m];
-          v[j][x + 4] = MT == 1 ? o[1] + o[3] : o[2 * m + 1];
+        for (int y = 0; y < 4; y++) {
+          const float* o = O[4 * j + y];
+          v[j][y] = MT == 1 ? o[0] + o[2] : o[2 * m];
+          v[j][y + 4] = MT == 1 ? o[1] + o[3] : o[2 * m + 1];
         }
       if (whole) {
         if (h < G) kv4_store_row<NG>(a.out + int64_t(e) * a.out_stride + (int64_t(g) * G + h) * HD, tg, v, 1.f / l[m]);
@@ -541,106 +616,120 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
     }
   }
 
-  if (dead)   // copies still in flight land before the CTA's shared memory is given up
-    for (int x = issued > S ? issued - S : 0; x < issued; x++) kv4_bar_wait(bars + (x % S) * 8, uint32_t(x / S) & 1u);
-
   // ---- merge within the CTA: slots of the same item follow one another
+  float* weight = reinterpret_cast<float*>(sm + Cfg::kWeight);   // [slot][row]
   __syncthreads();
   for (int a0 = 0; a0 < 2 * NW;) {
-    const int64_t item = slot_item[a0];
+    const int item = slot_item[a0];
     if (item < 0) { a0++; continue; }
-    int a1 = a0 + 1;
-    while (a1 < 2 * NW && (slot_item[a1] < 0 || slot_item[a1] == item)) a1++;
-    const int e = int(item / c.n_kv), g = int(item % c.n_kv);
-    const int64_t nch = (prefix[e + 1] - prefix[e]) / c.n_kv, first = prefix[e] + g * nch;
-    const bool whole = first >= c0 && first + nch <= c1;
-    float* part = a.part + (int64_t(blockIdx.x) * 2 + (first < c0 ? 0 : 1)) * Cfg::kPartFloats;
-    for (int x = t; x < G * HD; x += Cfg::kThreads) {
-      const int h = x / HD;
-      float M = -INFINITY;
-      for (int w = a0; w < a1; w++)
-        if (slot_item[w] == item) M = fmaxf(M, slots[w * Cfg::kPartFloats + ROWS * HD + 2 * h]);
-      float sum = 0.f, o = 0.f;
-      for (int w = a0; w < a1; w++)
-        if (slot_item[w] == item) {
-          const float* ps = slots + w * Cfg::kPartFloats;
-          const float f = kv4_ex2(ps[ROWS * HD + 2 * h] - M);
-          sum = fmaf(ps[ROWS * HD + 2 * h + 1], f, sum);
-          o = fmaf(ps[x], f, o);
-        }
-      if (whole) {
-        a.out[int64_t(e) * a.out_stride + int64_t(g) * G * HD + x] = o / sum;
-      } else {
-        part[x] = o;
-        if (x % HD == 0) reinterpret_cast<float2*>(part + ROWS * HD)[h] = make_float2(M, sum);
+    int a1 = a0 + 1, last = a0;
+    for (; a1 < 2 * NW && (slot_item[a1] < 0 || slot_item[a1] == item); a1++)
+      if (slot_item[a1] == item) last = a1;
+    const int e = item / c.n_kv, g = item % c.n_kv;
+    const int64_t np = (prefix[e + 1] - prefix[e]) / c.n_kv, first = prefix[e] + g * np;
+    const bool whole = first >= c0 && first + np <= c1;
+    float* part = part0 + (first < c0 ? 0 : Cfg::kPart);
+    for (int h = warp; h < G; h += NW) {   // a warp per head, a lane per slot
+      const bool mine = lane >= a0 && lane <= last && slot_item[lane] == item;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (mine) ml = reinterpret_cast<const float2*>(slot_ptr(lane) + ROWS * HD)[h];
+      float M = ml.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float f = mine ? kv4_ex2(ml.x - M) : 0.f;
+      float sum = ml.y * f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane < 2 * NW) weight[lane * ROWS + h] = whole ? f / sum : f;
+      if (!whole && lane == 0) reinterpret_cast<float2*>(part + ROWS * HD)[h] = make_float2(M, sum);
+    }
+    __syncthreads();
+    float* to = whole ? a.out + int64_t(e) * a.out_stride + int64_t(g) * G * HD : part;
+    for (int x = t; x < G * HD / 4; x += Cfg::kThreads) {
+      const int h = x / (HD / 4);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+      for (int w = a0; w <= last; w++) {
+        if (slot_item[w] != item) continue;
+        const float f = weight[w * ROWS + h];
+        const float4 v = reinterpret_cast<const float4*>(slot_ptr(w))[x];
+        o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
       }
+      reinterpret_cast<float4*>(to)[x] = o;
+    }
+    if (!whole && first >= c0 && t == 0) {   // begun here: k_kv4_attn_merge collects it from here
+      header[1] = int((first + np - 1) / (NW * share)) - int(blockIdx.x) + 1;
+      header[0] = item;
     }
     a0 = a1;
+    __syncthreads();
   }
 }
 
-// Items that several CTAs worked on, and empty or unreadable ones: one CTA per
-// (entry, kv head, query head), a thread per dimension.
+// Items that several CTAs worked on: CTA (b, h) merges query head h of the item that
+// CTA b of k_kv4_attn began and others ended.  A warp reads a row of partial
+// results per step, the warps' sums are added in order.
+constexpr int kKv4MergeWarps = 8;
 template <int HD>
-__global__ void __launch_bounds__(HD) k_kv4_attn_merge(Kv4 c, Kv4AttnArgs a, int part_floats) {
-  __shared__ int64_t s_sum[2][HD / 32];
-  __shared__ float2 s_ml[kKv4AttnMaxCtas];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int e = blockIdx.x, g = blockIdx.y / a.G, h = blockIdx.y % a.G;
+__global__ void __launch_bounds__(32 * kKv4MergeWarps) k_kv4_attn_merge(Kv4 c, Kv4AttnArgs a, int part_floats, int rows) {
+  constexpr int V = HD / 32;
+  __shared__ float s_o[kKv4MergeWarps][HD];
+  __shared__ float s_l[kKv4MergeWarps];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, h = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  uint32_t bad = 0;
-  const int nch = kv4_entry_chunks(c, a, e, &bad);
-  float* out = a.out + int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + t;
-  if (nch == 0) {
-    *out = bad ? NAN : 0.f;
-    return;
-  }
-  int64_t before = 0, all = 0;
-  for (int i = t; i < a.n; i += HD) {
-    uint32_t b;
-    const int x = kv4_entry_chunks(c, a, i, &b);
-    all += x;
-    if (i < e) before += x;
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-  }
-  if (lane == 0) { s_sum[0][warp] = before; s_sum[1][warp] = all; }
-  __syncthreads();
-  before = all = 0;
-#pragma unroll
-  for (int w = 0; w < HD / 32; w++) { before += s_sum[0][w]; all += s_sum[1][w]; }
-  const int64_t first = before * c.n_kv + int64_t(g) * nch, per = kv4_share(all * c.n_kv, a) * a.warps;
-  const int b0 = int(first / per), b1 = int((first + nch - 1) / per);   // CTAs that worked on it
-  if (b0 == b1) return;
-  auto record = [&](int b) { return a.part + (int64_t(b) * 2 + (b == b0 ? (first < b * per ? 0 : 1) : 0)) * part_floats; };
-  const int rows = (part_floats) / (HD + 2);
-  for (int b = b0 + t; b <= b1; b += HD) s_ml[b - b0] = reinterpret_cast<const float2*>(record(b) + rows * HD)[h];
-  __syncthreads();
+  const float* first = a.part + (int64_t(blockIdx.x) * 2 + 1) * part_floats;   // slot 1, then slot 0 of the next CTAs
+  const int* header = reinterpret_cast<const int*>(first + part_floats - 4);
+  const int item = __ldcg(header), members = __ldcg(header + 1);
+  if (item < 0) return;
+  auto record = [&](int b) { return b ? first + (int64_t(b) * 2 - 1) * part_floats : first; };
   float M = -INFINITY;
-  for (int b = 0; b <= b1 - b0; b++) M = fmaxf(M, s_ml[b].x);
-  float sum = 0.f, o = 0.f;
-#pragma unroll 8
-  for (int b = 0; b <= b1 - b0; b++) {
-    const float f = kv4_ex2(s_ml[b].x - M);
-    sum = fmaf(s_ml[b].y, f, sum);
-    o = fmaf(record(b + b0)[h * HD + t], f, o);
+  for (int b = lane; b < members; b += 32) M = fmaxf(M, __ldcg(record(b) + rows * HD + 2 * h));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float sum = 0.f, o[V];
+#pragma unroll
+  for (int v = 0; v < V; v++) o[v] = 0.f;
+#pragma unroll 4
+  for (int b = warp; b < members; b += kKv4MergeWarps) {
+    const float* r = record(b);
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(r + rows * HD) + h);
+    float x[V];
+    if (V == 4) {
+      const float4 u = __ldcg(reinterpret_cast<const float4*>(r + h * HD) + lane);
+      x[0] = u.x; x[1] = u.y; x[2 % V] = u.z; x[3 % V] = u.w;
+    } else {
+      const float2 u = __ldcg(reinterpret_cast<const float2*>(r + h * HD) + lane);
+      x[0] = u.x; x[1] = u.y;
+    }
+    const float f = kv4_ex2(ml.x - M);
+    sum = fmaf(ml.y, f, sum);
+#pragma unroll
+    for (int v = 0; v < V; v++) o[v] = fmaf(x[v], f, o[v]);
   }
-  *out = o / sum;
+#pragma unroll
+  for (int v = 0; v < V; v++) s_o[warp][lane * V + v] = o[v];
+  if (lane == 0) s_l[warp] = sum;
+  __syncthreads();
+  if (t < HD) {
+    float total = 0.f, x = 0.f;
+#pragma unroll
+    for (int w = 0; w < kKv4MergeWarps; w++) {
+      total += s_l[w];
+      x += s_o[w][t];
+    }
+    const int e = item / c.n_kv, g = item % c.n_kv;
+    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + t] = x / total;
+  }
 }
 
 template <int HD, int MT>
-static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_chunks, cudaStream_t s) {
+static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_pairs, cudaStream_t s) {
   using Cfg = Kv4AttnCfg<HD, MT>;
   static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, MT>, Cfg::kSmem);
   if (setup.err != cudaSuccess) return setup.err;
-  const int64_t useful = (most_chunks + Cfg::NW * kKv4MinChunks - 1) / (Cfg::NW * kKv4MinChunks);
+  const int64_t useful = (most_pairs + Cfg::NW * kKv4MinPairs - 1) / (Cfg::NW * kKv4MinPairs);
   int64_t ctas = setup.sms < kKv4AttnMaxCtas ? setup.sms : kKv4AttnMaxCtas;
   if (ctas > useful) ctas = useful;
-  a.ctas = int(ctas);
-  a.warps = Cfg::NW;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
@@ -651,12 +740,12 @@ static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_chu
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, MT>, k, a);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(unsigned(a.n), unsigned(k.n_kv * a.G));
-  cfg.blockDim = dim3(HD);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, MT>, k, a);
+  if (e != cudaSuccess || ctas < 2) return e;
+  cfg.gridDim = dim3(unsigned(ctas - 1), unsigned(a.G));   // the last CTA's items end with it
+  cfg.blockDim = dim3(32 * kKv4MergeWarps);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, k_kv4_attn_merge<HD>, k, a, int(Cfg::kPartFloats));
+  return cudaLaunchKernelEx(&cfg, k_kv4_attn_merge<HD>, k, a, int(Cfg::kPart), int(Cfg::kRows));
 }
 
 }  // namespace nt
@@ -702,11 +791,11 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
   a.part = static_cast<float*>(dev_workspace);
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  const int64_t entry_chunks = int64_t(k.n_kv) * ((int64_t(k.max_pages) * k.page_len) / kKv4Chunk);
-  // a launch's chunks are counted in 64 bits, a warp's share of them in 32
+  const int64_t entry_pairs = int64_t(k.n_kv) * ((int64_t(k.max_pages) * k.page_len + 31) / (2 * kKv4Chunk));
+  // a launch's pairs are counted in 64 bits, a warp's share of them in 32
   const int64_t most = int64_t(1) << 40;
-  if (entry_chunks > most) return bad("n_kv_heads * max_pages * page_len above 2^44");
-  const int32_t batch = entry_chunks * kKv4Batch <= most ? kKv4Batch : int32_t(most / entry_chunks);
+  if (entry_pairs > most) return bad("n_kv_heads * max_pages * page_len above 2^45");
+  const int32_t batch = entry_pairs * kKv4Batch <= most ? kKv4Batch : int32_t(most / entry_pairs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int32_t i = 0; i < n; i += batch) {
     a.n = n - i < batch ? n - i : batch;
@@ -715,8 +804,8 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
     a.q = dev_q + int64_t(i) * q_stride;
     a.out = dev_out + int64_t(i) * out_stride;
     cudaError_t e;
-    if (k.hd == 64) e = G <= 8 ? kv4_launch_attn<64, 1>(k, a, a.n * entry_chunks, s) : kv4_launch_attn<64, 2>(k, a, a.n * entry_chunks, s);
-    else e = G <= 8 ? kv4_launch_attn<128, 1>(k, a, a.n * entry_chunks, s) : kv4_launch_attn<128, 2>(k, a, a.n * entry_chunks, s);
+    if (k.hd == 64) e = G <= 8 ? kv4_launch_attn<64, 1>(k, a, a.n * entry_pairs, s) : kv4_launch_attn<64, 2>(k, a, a.n * entry_pairs, s);
+    else e = G <= 8 ? kv4_launch_attn<128, 1>(k, a, a.n * entry_pairs, s) : kv4_launch_attn<128, 2>(k, a, a.n * entry_pairs, s);
     if (e != cudaSuccess) return cuda_fail(e, "nt_attention_kv4");
   }
   return NT_OK;
