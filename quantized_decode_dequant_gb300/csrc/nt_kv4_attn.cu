@@ -16,7 +16,10 @@
 // Contractions.  Scores S[h][t] = q_h . K_t and outputs O[h][d] = sum_t P[h][t]
 // V_t[d].  q (scaled by a power of two) and P are split into two f16 terms, hi =
 // f16(x) and lo = f16(x - hi), about 22 bits.  With G <= 8 hi takes rows 0..7 of
-// the 16-row A operand and lo rows 8..15; with G = 16 each has a product of its own.
+// the 16-row A operand of the scores and lo rows 8..15 (G = 16: a product each); for
+// the outputs V^T is the A operand, 16 dimensions a tile, and P, as the scores'
+// accumulators hold it, the B operand of 8 heads, hi and lo a product each into
+// the same accumulators: 32 registers of them for 8 heads of 128 dimensions.
 //
 // What bounds it: a byte of cache is 1.8 values, and a value costs about 2.3
 // instructions of a lane, so at 6.8 TB/s the SMs' issue slots are about 3/4 busy:
@@ -50,8 +53,8 @@ __host__ __device__ constexpr int kv4_part_floats(int hd, int rows) { return row
 
 template <int HD, int MT>
 struct Kv4AttnCfg {
-  static constexpr int NW = MT == 1 ? (HD == 128 ? 12 : 16) : (HD == 128 ? 8 : 12);   // warps: registers decide
-  static constexpr int S = HD == 128 && MT == 1 ? 3 : 4;                               // ring stages of a warp
+  static constexpr int NW = MT == 1 ? 16 : (HD == 128 ? 8 : 12);                       // warps: registers decide
+  static constexpr int S = HD == 128 && MT == 1 ? 2 : 4;                               // ring stages of a warp
   static constexpr int kThreads = 32 * NW;
   static constexpr int kRows = 8 * MT;                                                 // heads of a partial result
   static constexpr int kPart = kv4_part_floats(HD, kRows);
@@ -211,17 +214,6 @@ __device__ __forceinline__ int kv4_find(const int64_t* prefix, int n, int64_t x)
   return lo;
 }
 
-// Output rows of one head: lane (row, tg) holds dimensions 32 j + 8 tg + 0..7 of it.
-template <int NG>
-__device__ __forceinline__ void kv4_store_row(float* o, int tg, const float (&v)[NG][8], float f) {
-#pragma unroll
-  for (int j = 0; j < NG; j++) {
-    float4* p = reinterpret_cast<float4*>(o + 32 * j + 8 * tg);
-    p[0] = make_float4(v[j][0] * f, v[j][1] * f, v[j][2] * f, v[j][3] * f);
-    p[1] = make_float4(v[j][4] * f, v[j][5] * f, v[j][6] * f, v[j][7] * f);
-  }
-}
-
 // ------------------------------------------------------------ the kernel --
 
 // The chunk pairs of all (entry, kv head) items in a row, item after item, are
@@ -362,7 +354,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll 1
   for (int i = 0; i < S; i++) issue();
 
-  float O[NT][4];
+  float O[NT / 2][MT][4];   // dimensions 32 j + 4 gi + 2 z (+ 1: the last two) of tile 2 j + z, heads 8 m + 2 tg, + 1
   uint32_t qa[MT][HD / 16][4];
   float mref[MT], l[MT], cs[MT];
   int k = 0, st = 0;                          // pairs read, stage of the next
@@ -422,7 +414,9 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll
       for (int m = 0; m < MT; m++) { mref[m] = -3e38f; l[m] = 0.f; }
 #pragma unroll
-      for (int i = 0; i < NT; i++) O[i][0] = O[i][1] = O[i][2] = O[i][3] = 0.f;
+      for (int i = 0; i < NT / 2; i++)
+#pragma unroll
+        for (int m = 0; m < MT; m++) O[i][m][0] = O[i][m][1] = O[i][m][2] = O[i][m][3] = 0.f;
     }
 
 #pragma unroll 1
@@ -525,27 +519,25 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
           l[m] *= f[m];
         }
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-          O[i][0] *= f[0]; O[i][1] *= f[0];
-          O[i][2] *= f[MT - 1]; O[i][3] *= f[MT - 1];
+        for (int m = 0; m < MT; m++) {
+          const float f0 = __shfl_sync(0xffffffffu, f[m], 8 * tg), f1 = __shfl_sync(0xffffffffu, f[m], 8 * tg + 4);
+#pragma unroll
+          for (int i = 0; i < NT / 2; i++) {
+            O[i][m][0] *= f0; O[i][m][1] *= f1;
+            O[i][m][2] *= f0; O[i][m][3] *= f1;
+          }
         }
         weights();
       }
-      uint32_t pa[2][MT][4];
+      // P of the chunk u as B operand: positions 2 tg, 2 tg + 1 and 8 + 2 tg, 8 + 2 tg + 1 of head gi (+ 8 m)
+      uint32_t hi[2][MT][2], lo[2][MT][2];
 #pragma unroll
-      for (int m = 0; m < MT; m++) l[m] += sum[m];
+      for (int m = 0; m < MT; m++) {
+        l[m] += sum[m];
 #pragma unroll
-      for (int u = 0; u < 2; u++) {
-        const int o = 4 * u;
-        if (MT == 1) {      // rows gi: hi, rows gi + 8: lo
-          kv4_split(p[0][o], p[0][o + 1], pa[u][0][0], pa[u][0][1]);
-          kv4_split(p[0][o + 2], p[0][o + 3], pa[u][0][2], pa[u][0][3]);
-        } else {            // product 0: hi of heads gi and gi + 8, product 1: lo
-          kv4_split(p[0][o], p[0][o + 1], pa[u][0][0], pa[u][MT - 1][0]);
-          kv4_split(p[0][o + 2], p[0][o + 3], pa[u][0][2], pa[u][MT - 1][2]);
-          kv4_split(p[MT - 1][o], p[MT - 1][o + 1], pa[u][0][1], pa[u][MT - 1][1]);
-          kv4_split(p[MT - 1][o + 2], p[MT - 1][o + 3], pa[u][0][3], pa[u][MT - 1][3]);
-        }
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+          for (int i = 0; i < 2; i++) kv4_split(p[m][4 * u + 2 * i], p[m][4 * u + 2 * i + 1], hi[u][m][i], lo[u][m][i]);
       }
 
       // ---- weighted values
@@ -576,14 +568,19 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll
           for (int r = 0; r < 2; r++) kv4_decode(vw[r][j], vs[r][j], kv4_h2mul(vs[r][j], kMinus72), b[r]);
 #pragma unroll
-          for (int y = 0; y < 4; y++)
+          for (int z = 0; z < 2; z++) {
+            const uint32_t v[4] = {b[0][2 * z], b[0][2 * z + 1], b[1][2 * z], b[1][2 * z + 1]};
 #pragma unroll
-            for (int m = 0; m < MT; m++) kv4_mma(O[4 * j + y], pa[u][m], b[0][y], b[1][y]);
+            for (int m = 0; m < MT; m++) {
+              kv4_mma(O[2 * j + z][m], v, hi[u][m][0], hi[u][m][1]);
+              kv4_mma(O[2 * j + z][m], v, lo[u][m][0], lo[u][m][1]);
+            }
+          }
         }
       }
     }
 
-    // ---- the end of the segment: this lane's rows, dimensions 32 j + 8 tg + 0..7
+    // ---- the end of the segment
 #pragma unroll
     for (int m = 0; m < MT; m++) {
       l[m] += __shfl_xor_sync(0xffffffffu, l[m], 1);
@@ -595,23 +592,20 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
     float* po = slot_ptr(slot);
     if (!whole && lane == 0) slot_item[slot] = e * c.n_kv + g;
     __syncwarp();   // (slot 1 is the ring: every lane has read its last pair)
+    float* to = whole ? a.out + int64_t(e) * a.out_stride + int64_t(g) * G * HD : po;
 #pragma unroll
     for (int m = 0; m < MT; m++) {
-      const int h = gi + 8 * m;
-      float v[NG][8];
+      if (!whole && tg == 0) reinterpret_cast<float2*>(po + ROWS * HD)[gi + 8 * m] = make_float2(mref[m], l[m]);
 #pragma unroll
-      for (int j = 0; j < NG; j++)
+      for (int y = 0; y < 2; y++) {   // head 8 m + 2 tg + y: dimensions 32 j + 4 gi + 0..3
+        const int h = 8 * m + 2 * tg + y;
+        const float lh = __shfl_sync(0xffffffffu, l[m], 8 * tg + 4 * y), f = whole ? 1.f / lh : 1.f;
+        if (h < G) {
 #pragma unroll
-        for (int y = 0; y < 4; y++) {
-          const float* o = O[4 * j + y];
-          v[j][y] = MT == 1 ? o[0] + o[2] : o[2 * m];
-          v[j][y + 4] = MT == 1 ? o[1] + o[3] : o[2 * m + 1];
+          for (int j = 0; j < NG; j++)
+            *reinterpret_cast<float4*>(to + h * HD + 32 * j + 4 * gi) =
+                make_float4(O[2 * j][m][y] * f, O[2 * j][m][y + 2] * f, O[2 * j + 1][m][y] * f, O[2 * j + 1][m][y + 2] * f);
         }
-      if (whole) {
-        if (h < G) kv4_store_row<NG>(a.out + int64_t(e) * a.out_stride + (int64_t(g) * G + h) * HD, tg, v, 1.f / l[m]);
-      } else {
-        kv4_store_row<NG>(po + h * HD, tg, v, 1.f);
-        if (tg == 0) reinterpret_cast<float2*>(po + ROWS * HD)[h] = make_float2(mref[m], l[m]);
       }
     }
   }
