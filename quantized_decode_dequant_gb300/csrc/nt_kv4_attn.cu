@@ -62,10 +62,10 @@ struct Kv4AttnCfg {
   static constexpr int kRing = 0;
   static constexpr int kSlots = kRing + NW * S * kPair;                                // a slot of each warp (see below)
   static constexpr int kPrefix = kSlots + NW * kPart * 4;
-  static constexpr int kBars = kPrefix + (kKv4Batch + 1) * 8;
+  static constexpr int kEntry = kPrefix + (kKv4Batch + 4) * 4;                         // {sequence, length} of each
+  static constexpr int kBars = kEntry + kKv4Batch * 8;
   static constexpr int kItem = kBars + NW * S * 8;                                     // item of each slot (-1: none)
-  static constexpr int kWeight = kItem + 2 * NW * 4;                                   // [2 NW][kRows] merge weights
-  static constexpr int kSmem = kWeight + 2 * NW * kRows * 4;
+  static constexpr int kSmem = kItem + 2 * NW * 4;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kPart * 4 <= S * kPair && kPart % 4 == 0, "a warp's ring holds a partial result");
   static_assert(2 * NW <= 32, "a lane per slot");
@@ -193,19 +193,19 @@ __device__ __forceinline__ bool kv4_bar_wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-// Pairs of chunks (32 positions) of listed entry e (0: nothing to read); *bad:
-// error bits of an entry that cannot be read.
-__device__ __forceinline__ int kv4_entry_pairs(const Kv4& c, const Kv4AttnArgs& a, int e, uint32_t* bad) {
+// Sequence and length of listed entry e (length 0 and *bad where it cannot be read).
+__device__ __forceinline__ int2 kv4_entry(const Kv4& c, const Kv4AttnArgs& a, int e, uint32_t* bad) {
   const int s = a.seq ? a.seq[e] : a.seq0 + e;
-  if (s < 0 || s >= c.max_seqs) { *bad = NT_KV4_BAD_SEQ; return 0; }
+  *bad = NT_KV4_BAD_SEQ;
+  if (s < 0 || s >= c.max_seqs) return make_int2(-1, 0);
   const int n = c.len[s];
-  if (n < 0 || n > c.capacity()) { *bad = NT_KV4_BAD_LEN; return 0; }
-  *bad = 0;
-  return (n + 2 * kKv4Chunk - 1) / (2 * kKv4Chunk);
+  *bad = n < 0 || n > c.capacity() ? NT_KV4_BAD_LEN : 0;
+  return make_int2(*bad ? -1 : s, *bad ? 0 : n);
 }
+__device__ __forceinline__ int kv4_pairs(int len) { return (len + 2 * kKv4Chunk - 1) / (2 * kKv4Chunk); }
 
 // Entry of prefix (ascending, prefix[0] = 0) that holds chunk x: prefix[i] <= x < prefix[i + 1].
-__device__ __forceinline__ int kv4_find(const int64_t* prefix, int n, int64_t x) {
+__device__ __forceinline__ int kv4_find(const int* prefix, int n, int x) {
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -233,7 +233,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
   using L = Kv4Chunk<HD>;
   constexpr int NW = Cfg::NW, S = Cfg::S, NG = HD / 32, NT = HD / 8, CB = L::kBytes, ROWS = Cfg::kRows;
   extern __shared__ __align__(128) uint8_t sm[];
-  int64_t* prefix = reinterpret_cast<int64_t*>(sm + Cfg::kPrefix);
+  int* prefix = reinterpret_cast<int*>(sm + Cfg::kPrefix);
+  int2* entry = reinterpret_cast<int2*>(sm + Cfg::kEntry);
   int* slot_item = reinterpret_cast<int*>(sm + Cfg::kItem);
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, gi = lane >> 2, tg = lane & 3;
   const int G = a.G, n = a.n;
@@ -244,70 +245,72 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- pair offsets of the entries (an entry's pairs are counted once per kv head)
   {
-    int64_t* sums = reinterpret_cast<int64_t*>(sm + Cfg::kSlots);   // per-warp sums, before the slots are used
-    int64_t run = 0;
+    int* sums = reinterpret_cast<int*>(sm + Cfg::kSlots);   // per-warp sums, before the slots are used
+    int run = 0;
     for (int e0 = 0; e0 < n; e0 += Cfg::kThreads) {
       const int e = e0 + t;
-      uint32_t bad = 0;
-      int64_t x = e < n ? int64_t(kv4_entry_pairs(c, a, e, &bad)) : 0;
-      if (bad && blockIdx.x == 0) kv4_flag(c, bad);
-      const int64_t mine = x;
+      int mine = 0;
+      if (e < n) {
+        uint32_t bad;
+        const int2 sl = kv4_entry(c, a, e, &bad);
+        if (bad && blockIdx.x == 0) kv4_flag(c, bad);
+        entry[e] = sl;
+        mine = kv4_pairs(sl.y) * c.n_kv;
+      }
+      int x = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
       if (lane == 31) sums[warp] = x;
       __syncthreads();
-      int64_t before = 0, all = 0;
-      for (int w = 0; w < NW; w++) {
-        const int64_t y = sums[w];
+      int before = 0, all = 0;
+      for (int w = 0; w < NW && e0 + 32 * w < n; w++) {
+        const int y = sums[w];
         if (w < warp) before += y;
         all += y;
       }
-      if (e < n) prefix[e] = (run + before + x - mine) * c.n_kv;
+      if (e < n) prefix[e] = run + before + x - mine;
       run += all;
-      __syncthreads();
+      if (e0 + Cfg::kThreads < n) __syncthreads();
     }
-    if (t == 0) prefix[n] = run * c.n_kv;
+    if (t == 0) prefix[n] = run;
     if (lane < S) kv4_bar_init(kv4_smem(sm + Cfg::kBars + (warp * S + lane) * 8));
     if (lane < 2) slot_item[2 * warp + lane] = -1;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
   }
-  // the entries without a position: zeros, or NaN where they cannot be read
-  for (int e = blockIdx.x; e < n; e += gridDim.x) {
-    if (prefix[e + 1] != prefix[e]) continue;
-    uint32_t bad = 0;
-    kv4_entry_pairs(c, a, e, &bad);
-    for (int x = t; x < c.n_kv * G * HD; x += Cfg::kThreads) a.out[int64_t(e) * a.out_stride + x] = bad ? NAN : 0.f;
-  }
-  const int64_t total = prefix[n], warps = int64_t(gridDim.x) * NW;
-  int64_t share = (total + warps - 1) / warps;
+  const int total = prefix[n], warps = int(gridDim.x) * NW;
+  int share = (total + warps - 1) / warps;
   if (share < kKv4MinPairs) share = kKv4MinPairs;
-  const int64_t c0 = int64_t(blockIdx.x) * NW * share;   // the CTA's first pair
-  int64_t c1 = c0 + NW * share;
-  if (c1 > total) c1 = total;
+  const int c0 = int(blockIdx.x) * NW * share;           // the CTA's first pair (total + 152 NW pairs fit an int)
+  const int c1 = c0 + NW * share < total ? c0 + NW * share : total;
   float* part0 = a.part + int64_t(blockIdx.x) * 2 * Cfg::kPart;
   int* header = reinterpret_cast<int*>(part0 + 2 * Cfg::kPart - 4);   // of slot 1
   if (t == 0) header[0] = -1;
   asm volatile("griddepcontrol.launch_dependents;");
+  // the entries without a position: zeros, or NaN where they cannot be read
+  for (int e = blockIdx.x; e < n; e += gridDim.x)
+    if (entry[e].y == 0)
+      for (int x = t; x < c.n_kv * G * HD; x += Cfg::kThreads)
+        a.out[int64_t(e) * a.out_stride + x] = entry[e].x < 0 ? NAN : 0.f;
   if (c0 >= total) return;   // the whole CTA
 
-  const int64_t w0 = c0 + warp * share;
-  const int count = w0 >= c1 ? 0 : int(w0 + share > c1 ? c1 - w0 : share);
+  const int w0 = c0 + warp * share;
+  const int count = w0 >= c1 ? 0 : (w0 + share > c1 ? c1 - w0 : share);
   const uint32_t ring = kv4_smem(sm + Cfg::kRing) + uint32_t(warp) * (S * Cfg::kPair);
   const uint32_t bars = kv4_smem(sm + Cfg::kBars) + uint32_t(warp) * S * 8;
   const int cpp = c.page_len / kKv4Chunk;
   const uint8_t* layer_pool = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes();
 
   // the item of pair y: entry e, kv head g, pair pi of np
-  auto locate = [&](int64_t y, int& e, int& g, int& pi, int& np) {
+  auto locate = [&](int y, int& e, int& g, int& pi, int& np) {
     e = kv4_find(prefix, n, y);
-    np = int((prefix[e + 1] - prefix[e]) / c.n_kv);
-    const int64_t r = y - prefix[e];
-    g = int(r / np);
-    pi = int(r - int64_t(g) * np);
+    np = kv4_pairs(entry[e].y);
+    const int r = y - prefix[e];
+    g = int(unsigned(r) / unsigned(np));
+    pi = r - g * np;
   };
   // indexes of the two chunks of pair x of this warp within the layer's pool (in
   // chunks); -1: no page, -2: behind the sequence's end
@@ -315,17 +318,27 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
     if (x >= count) return make_int2(-2, -2);
     int e, g, pi, np;
     locate(w0 + x, e, g, pi, np);
-    const int s = a.seq ? a.seq[e] : a.seq0 + e, len = c.len[s];
-    const int32_t* row = c.table + int64_t(s) * c.max_pages;
+    const int len = entry[e].y;
+    const int32_t* row = c.table + int64_t(entry[e].x) * c.max_pages;
     auto chunk = [&](int ci) -> int {
-      if (ci * kKv4Chunk >= len) return -2;
-      const int page = row[ci / cpp];
+      if (ci * kKv4Chunk >= len) return -2;   // (len is at most 2^31 - 256)
+      const int page = row[unsigned(ci) / unsigned(cpp)];
       if (page < 0 || page >= c.n_pages) { kv4_flag(c, NT_KV4_BAD_PAGE); return -1; }
-      return int((int64_t(page) * c.n_kv + g) * cpp + ci % cpp);
+      return (page * c.n_kv + g) * cpp + int(unsigned(ci) % unsigned(cpp));
     };
     return make_int2(chunk(2 * pi), chunk(2 * pi + 1));
   };
 
+  // brings an item's q into L1, a line a lane
+  auto fetch_q = [&](int e, int g) {
+    for (int x = 32 * lane; x < G * HD; x += 32 * 32)
+      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD + x));
+  };
+  int e = 0, g = 0, pi0 = 0, np = 1;
+  if (count > 0) {
+    locate(w0, e, g, pi0, np);
+    fetch_q(e, g);         // in flight while the first pages are looked up and copied
+  }
   int2 addr = resolve(lane), addr_next = make_int2(-2, -2);   // of pairs 32 b + lane and the 32 behind
   int issued = 0, ist = 0;                    // pairs issued, stage of the next
   uint32_t missing = 0;                       // stages that lack a page
@@ -362,16 +375,13 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll 1
   while (k < count) {
     // ---- a segment: consecutive pairs of one item
-    int e, g, pi0, np;
-    locate(w0 + k, e, g, pi0, np);
     const int seg = np - pi0 < count - k ? np - pi0 : count - k;
-    const int s = a.seq ? a.seq[e] : a.seq0 + e;
-    int live = c.len[s] - pi0 * 2 * kKv4Chunk;   // positions from the pair on that exist
+    int live = entry[e].y - pi0 * 2 * kKv4Chunk;   // positions from the pair on that exist
     bool poison = false;
     {
-      // q of heads gi (and gi + 8), scaled so that the largest element is in [2^10, 2^11), split
+      // q of heads gi (and gi + 8), scaled so that a head's largest element is in [2^10, 2^11), split
       const float* qb = a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD;
-      float x[MT][NG][8];
+      float qx[MT][NG][8];
 #pragma unroll
       for (int m = 0; m < MT; m++) {
         const int h = gi + 8 * m;
@@ -380,13 +390,13 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
         for (int j = 0; j < NG; j++) {
           float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
           if (h < G) {
-            u = __ldcg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg));
-            v = __ldcg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg) + 1);
+            u = __ldg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg));
+            v = __ldg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg) + 1);
           }
-          x[m][j][0] = u.x; x[m][j][1] = u.y; x[m][j][2] = u.z; x[m][j][3] = u.w;
-          x[m][j][4] = v.x; x[m][j][5] = v.y; x[m][j][6] = v.z; x[m][j][7] = v.w;
+          qx[m][j][0] = u.x; qx[m][j][1] = u.y; qx[m][j][2] = u.z; qx[m][j][3] = u.w;
+          qx[m][j][4] = v.x; qx[m][j][5] = v.y; qx[m][j][6] = v.z; qx[m][j][7] = v.w;
 #pragma unroll
-          for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(x[m][j][i]));
+          for (int i = 0; i < 8; i++) top = fmaxf(top, fabsf(qx[m][j][i]));
         }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -397,7 +407,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll
         for (int j = 0; j < NG; j++)
 #pragma unroll
-          for (int i = 0; i < 8; i++) x[m][j][i] *= up;
+          for (int i = 0; i < 8; i++) qx[m][j][i] *= up;
       }
 #pragma unroll
       for (int j = 0; j < NG; j++)
@@ -405,10 +415,10 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
         for (int i = 0; i < 4; i++) {   // pair (code i, code i + 4): k-step 2 j + i / 2, half i % 2
           const int kk = 2 * j + (i >> 1), r = 2 * (i & 1);
           if (MT == 1) {
-            kv4_split(x[0][j][i], x[0][j][i + 4], qa[0][kk][r], qa[0][kk][r + 1]);
+            kv4_split(qx[0][j][i], qx[0][j][i + 4], qa[0][kk][r], qa[0][kk][r + 1]);
           } else {
-            kv4_split(x[0][j][i], x[0][j][i + 4], qa[0][kk][r], qa[MT - 1][kk][r]);
-            kv4_split(x[MT - 1][j][i], x[MT - 1][j][i + 4], qa[0][kk][r + 1], qa[MT - 1][kk][r + 1]);
+            kv4_split(qx[0][j][i], qx[0][j][i + 4], qa[0][kk][r], qa[MT - 1][kk][r]);
+            kv4_split(qx[MT - 1][j][i], qx[MT - 1][j][i + 4], qa[0][kk][r + 1], qa[MT - 1][kk][r + 1]);
           }
         }
 #pragma unroll
@@ -588,11 +598,15 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
       if (poison) l[m] = NAN;
     }
     const bool whole = pi0 == 0 && seg == np;
-    const int slot = 2 * warp + (pi0 > 0 ? 0 : 1);
+    const int slot = 2 * warp + (pi0 > 0 ? 0 : 1), e_was = e, g_was = g;
+    if (k < count) {
+      locate(w0 + k, e, g, pi0, np);
+      fetch_q(e, g);       // in flight while this item's results go out
+    }
     float* po = slot_ptr(slot);
-    if (!whole && lane == 0) slot_item[slot] = e * c.n_kv + g;
+    if (!whole && lane == 0) slot_item[slot] = e_was * c.n_kv + g_was;
     __syncwarp();   // (slot 1 is the ring: every lane has read its last pair)
-    float* to = whole ? a.out + int64_t(e) * a.out_stride + int64_t(g) * G * HD : po;
+    float* to = whole ? a.out + int64_t(e_was) * a.out_stride + int64_t(g_was) * G * HD : po;
 #pragma unroll
     for (int m = 0; m < MT; m++) {
       if (!whole && tg == 0) reinterpret_cast<float2*>(po + ROWS * HD)[gi + 8 * m] = make_float2(mref[m], l[m]);
@@ -610,53 +624,58 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
     }
   }
 
-  // ---- merge within the CTA: slots of the same item follow one another
-  float* weight = reinterpret_cast<float*>(sm + Cfg::kWeight);   // [slot][row]
+  // ---- merge within the CTA: a warp per head, a lane per slot; an item's slots in order
   __syncthreads();
-  for (int a0 = 0; a0 < 2 * NW;) {
-    const int item = slot_item[a0];
-    if (item < 0) { a0++; continue; }
-    int a1 = a0 + 1, last = a0;
-    for (; a1 < 2 * NW && (slot_item[a1] < 0 || slot_item[a1] == item); a1++)
-      if (slot_item[a1] == item) last = a1;
-    const int e = item / c.n_kv, g = item % c.n_kv;
-    const int64_t np = (prefix[e + 1] - prefix[e]) / c.n_kv, first = prefix[e] + g * np;
-    const bool whole = first >= c0 && first + np <= c1;
+  constexpr int V = HD / 32;
+  const int mine = lane < 2 * NW ? slot_item[lane] : -1;
+  for (uint32_t left = __ballot_sync(0xffffffffu, mine >= 0); left;) {
+    const int a0 = __ffs(left) - 1, item = __shfl_sync(0xffffffffu, mine, a0);
+    const uint32_t members = __ballot_sync(0xffffffffu, mine == item);
+    left &= ~members;
+    const int nm = __popc(members), nth = lane < nm ? int(__fns(members, 0, lane + 1)) : a0;   // lane i: the i-th slot
+    const int ie = item / c.n_kv, ig = item % c.n_kv, ip = kv4_pairs(entry[ie].y), first = prefix[ie] + ig * ip;
+    const bool whole = first >= c0 && first + ip <= c1;
     float* part = part0 + (first < c0 ? 0 : Cfg::kPart);
-    for (int h = warp; h < G; h += NW) {   // a warp per head, a lane per slot
-      const bool mine = lane >= a0 && lane <= last && slot_item[lane] == item;
+    float* to = whole ? a.out + int64_t(ie) * a.out_stride + int64_t(ig) * G * HD : part;
+    for (int h = warp; h < G; h += NW) {
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (mine) ml = reinterpret_cast<const float2*>(slot_ptr(lane) + ROWS * HD)[h];
+      if (lane < nm) ml = reinterpret_cast<const float2*>(slot_ptr(nth) + ROWS * HD)[h];
       float M = ml.x;
 #pragma unroll
       for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      const float f = mine ? kv4_ex2(ml.x - M) : 0.f;
-      float sum = ml.y * f;
+      float f = lane < nm ? kv4_ex2(ml.x - M) : 0.f, sum = ml.y * f;
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane < 2 * NW) weight[lane * ROWS + h] = whole ? f / sum : f;
+      if (whole) f /= sum;
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; v++) o[v] = 0.f;
+#pragma unroll 1
+      for (int i = 0; i < nm; i += 4) {
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+          const int w = __shfl_sync(0xffffffffu, nth, i + u);
+          const float fw = __shfl_sync(0xffffffffu, f, i + u);
+          const float* r = slot_ptr(w) + h * HD + V * lane;
+          if (i + u >= nm) continue;
+          if (V == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(r);
+            o[0] = fmaf(x.x, fw, o[0]); o[1] = fmaf(x.y, fw, o[1]);
+            o[2 % V] = fmaf(x.z, fw, o[2 % V]); o[3 % V] = fmaf(x.w, fw, o[3 % V]);
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(r);
+            o[0] = fmaf(x.x, fw, o[0]); o[1] = fmaf(x.y, fw, o[1]);
+          }
+        }
+      }
+      if (V == 4) *reinterpret_cast<float4*>(to + h * HD + V * lane) = make_float4(o[0], o[1], o[2 % V], o[3 % V]);
+      else *reinterpret_cast<float2*>(to + h * HD + V * lane) = make_float2(o[0], o[1]);
       if (!whole && lane == 0) reinterpret_cast<float2*>(part + ROWS * HD)[h] = make_float2(M, sum);
     }
-    __syncthreads();
-    float* to = whole ? a.out + int64_t(e) * a.out_stride + int64_t(g) * G * HD : part;
-    for (int x = t; x < G * HD / 4; x += Cfg::kThreads) {
-      const int h = x / (HD / 4);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-      for (int w = a0; w <= last; w++) {
-        if (slot_item[w] != item) continue;
-        const float f = weight[w * ROWS + h];
-        const float4 v = reinterpret_cast<const float4*>(slot_ptr(w))[x];
-        o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
-      }
-      reinterpret_cast<float4*>(to)[x] = o;
-    }
     if (!whole && first >= c0 && t == 0) {   // begun here: k_kv4_attn_merge collects it from here
-      header[1] = int((first + np - 1) / (NW * share)) - int(blockIdx.x) + 1;
+      header[1] = (first + ip - 1) / (NW * share) - int(blockIdx.x) + 1;
       header[0] = item;
     }
-    a0 = a1;
-    __syncthreads();
   }
 }
 
@@ -785,10 +804,10 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
   a.part = static_cast<float*>(dev_workspace);
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  const int64_t entry_pairs = int64_t(k.n_kv) * ((int64_t(k.max_pages) * k.page_len + 31) / (2 * kKv4Chunk));
-  // a launch's pairs are counted in 64 bits, a warp's share of them in 32
-  const int64_t most = int64_t(1) << 40;
-  if (entry_pairs > most) return bad("n_kv_heads * max_pages * page_len above 2^45");
+  const int64_t entry_pairs = int64_t(k.n_kv) * ((int64_t(k.max_pages) * k.page_len + 31) / 32);
+  // a launch's pairs are counted in 32 bits
+  const int64_t most = int64_t(1) << 30;
+  if (entry_pairs > most) return bad("n_kv_heads * max_pages * page_len above 2^35");
   const int32_t batch = entry_pairs * kKv4Batch <= most ? kKv4Batch : int32_t(most / entry_pairs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int32_t i = 0; i < n; i += batch) {
