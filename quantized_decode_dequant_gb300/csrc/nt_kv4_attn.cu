@@ -69,6 +69,7 @@ struct Kv4AttnCfg {
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kPart * 4 <= S * kPair && kPart % 4 == 0, "a warp's ring holds a partial result");
   static_assert(2 * NW <= 32, "a lane per slot");
+  static_assert((S & (S - 1)) == 0, "stages are found by masks");
 };
 
 size_t kv4_attn_ws_bytes(int n_heads, int n_kv, int hd) {
@@ -339,30 +340,29 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
     locate(w0, e, g, pi0, np);
     fetch_q(e, g);         // in flight while the first pages are looked up and copied
   }
-  int2 addr = resolve(lane), addr_next = make_int2(-2, -2);   // of pairs 32 b + lane and the 32 behind
-  int issued = 0, ist = 0;                    // pairs issued, stage of the next
-  uint32_t missing = 0;                       // stages that lack a page
-  bool dead = false;                          // a wait ran out: nothing more is copied or read
+  // Pair x stands in stage x % S and completes that stage's barrier phase x / S.
+  int2 addr = resolve(lane);                  // of pairs 32 b + lane
+  int issued = 0;
+  uint32_t missing = 0;                       // bit per stage: it lacks a page
+  constexpr uint32_t kDead = 1u << 31;        // a wait ran out: nothing more is copied or read
   auto issue = [&]() {
-    if (issued < count && !dead) {
-      const int x0 = __shfl_sync(0xffffffffu, addr.x, issued & 31), x1 = __shfl_sync(0xffffffffu, addr.y, issued & 31);
-      const uint32_t dst = ring + ist * Cfg::kPair, bar = bars + ist * 8;
-      const bool lacks = x0 < 0 || x1 == -1;
-      missing = lacks ? missing | (1u << ist) : missing & ~(1u << ist);
-      if (lane == 0) {
-        if (lacks) {
-          kv4_bar_arrive(bar);
-        } else {
-          kv4_bar_expect(bar, x1 < 0 ? CB : 2 * CB);
-          kv4_copy(dst, layer_pool + int64_t(x0) * CB, x1 == x0 + 1 ? 2 * CB : CB, bar);
-          if (x1 >= 0 && x1 != x0 + 1) kv4_copy(dst + CB, layer_pool + int64_t(x1) * CB, CB, bar);
-        }
+    if (issued >= count || (missing & kDead)) return;
+    if ((issued & 31) == 0 && issued) addr = resolve(issued + lane);
+    const int x0 = __shfl_sync(0xffffffffu, addr.x, issued & 31), x1 = __shfl_sync(0xffffffffu, addr.y, issued & 31);
+    const int at = issued & (S - 1);
+    const bool lacks = x0 < 0 || x1 == -1;
+    missing = lacks ? missing | (1u << at) : missing & ~(1u << at);
+    if (lane == 0) {
+      const uint32_t dst = ring + at * Cfg::kPair, bar = bars + at * 8;
+      if (lacks) {
+        kv4_bar_arrive(bar);
+      } else {
+        kv4_bar_expect(bar, x1 < 0 ? CB : 2 * CB);
+        kv4_copy(dst, layer_pool + int64_t(x0) * CB, x1 == x0 + 1 ? 2 * CB : CB, bar);
+        if (x1 >= 0 && x1 != x0 + 1) kv4_copy(dst + CB, layer_pool + int64_t(x1) * CB, CB, bar);
       }
-      issued++;
-      ist = ist + 1 == S ? 0 : ist + 1;
-      if ((issued & 31) == 16) addr_next = resolve((issued & ~31) + 32 + lane);
-      if ((issued & 31) == 0) addr = addr_next;
     }
+    issued++;
   };
 #pragma unroll 1
   for (int i = 0; i < S; i++) issue();
@@ -370,8 +370,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
   float O[NT / 2][MT][4];   // dimensions 32 j + 4 gi + 2 z (+ 1: the last two) of tile 2 j + z, heads 8 m + 2 tg, + 1
   uint32_t qa[MT][HD / 16][4];
   float mref[MT], l[MT], cs[MT];
-  int k = 0, st = 0;                          // pairs read, stage of the next
-  uint32_t parity = 0;
+  int k = 0;                                  // pairs read
 #pragma unroll 1
   while (k < count) {
     // ---- a segment: consecutive pairs of one item
@@ -431,23 +430,20 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 
 #pragma unroll 1
     for (const int k1 = k + seg; k < k1; k++, live -= 2 * kKv4Chunk) {
-      if (!__all_sync(0xffffffffu, dead || kv4_bar_wait(bars + st * 8, parity)) && !dead) {
-        dead = true;
+      const int st = k & (S - 1);
+      if (!(missing & kDead) &&
+          !__all_sync(0xffffffffu, kv4_bar_wait(bars + st * 8, uint32_t(k / S) & 1u))) {
+        missing |= kDead;
         if (lane == 0) kv4_flag(c, NT_KV4_TIMEOUT);
-        for (int y = k; y < issued; y++) {   // copies in flight land before anything else happens to the ring
-          const int at = st + y - k;
-          kv4_bar_wait(bars + (at < S ? at : at - S) * 8, at < S ? parity : parity ^ 1u);
-        }
+        for (int y = k; y < issued; y++)   // copies in flight land before anything else happens to the ring
+          kv4_bar_wait(bars + (y & (S - 1)) * 8, uint32_t(y / S) & 1u);
       }
-      const uint32_t base = ring + st * Cfg::kPair;
-      const bool lacks = dead || (missing >> st & 1u);
-      st++;
-      if (st == S) { st = 0; parity ^= 1u; }
-      if (lacks) {
+      if (missing & (kDead | (1u << st))) {
         poison = true;
         issue();
         continue;
       }
+      const uint32_t base = ring + st * Cfg::kPair;
 
       // ---- scores of 32 positions
       float sc[4][4];
@@ -467,18 +463,20 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
           }
         }
 #pragma unroll
-        for (int j = 0; j < NG; j++)
+        for (int j = 0; j < NG; j++) {
+          uint32_t b[2][4];
 #pragma unroll
           for (int i = 0; i < 2; i++) {
-            const uint32_t d = __byte_perm(ks[i][j >> 1], 0u, (j & 1) ? 0x3232u : 0x1010u), d72 = kv4_h2mul(d, kMinus72);
-            uint32_t b[4];
-            kv4_decode(kw[i][j], d, d72, b);
-#pragma unroll
-            for (int m = 0; m < MT; m++) {
-              kv4_mma(sc[2 * u + i], qa[m][2 * j], b[0], b[1]);
-              kv4_mma(sc[2 * u + i], qa[m][2 * j + 1], b[2], b[3]);
-            }
+            const uint32_t d = __byte_perm(ks[i][j >> 1], 0u, (j & 1) ? 0x3232u : 0x1010u);
+            kv4_decode(kw[i][j], d, kv4_h2mul(d, kMinus72), b[i]);
           }
+#pragma unroll
+          for (int m = 0; m < MT; m++)   // products into the same accumulators never follow one another
+#pragma unroll
+            for (int y = 0; y < 2; y++)
+#pragma unroll
+              for (int i = 0; i < 2; i++) kv4_mma(sc[2 * u + i], qa[m][2 * j + y], b[i][2 * y], b[i][2 * y + 1]);
+        }
       }
       // the scores of this lane's heads at positions 8 i + 2 tg and 8 i + 2 tg + 1, i < 4
       float x[MT][8];
@@ -578,14 +576,19 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll
           for (int r = 0; r < 2; r++) kv4_decode(vw[r][j], vs[r][j], kv4_h2mul(vs[r][j], kMinus72), b[r]);
 #pragma unroll
-          for (int z = 0; z < 2; z++) {
-            const uint32_t v[4] = {b[0][2 * z], b[0][2 * z + 1], b[1][2 * z], b[1][2 * z + 1]};
+          for (int m = 0; m < MT; m++)
 #pragma unroll
-            for (int m = 0; m < MT; m++) {
+            for (int z = 0; z < 2; z++) {
+              const uint32_t v[4] = {b[0][2 * z], b[0][2 * z + 1], b[1][2 * z], b[1][2 * z + 1]};
               kv4_mma(O[2 * j + z][m], v, hi[u][m][0], hi[u][m][1]);
+            }
+#pragma unroll
+          for (int m = 0; m < MT; m++)
+#pragma unroll
+            for (int z = 0; z < 2; z++) {
+              const uint32_t v[4] = {b[0][2 * z], b[0][2 * z + 1], b[1][2 * z], b[1][2 * z + 1]};
               kv4_mma(O[2 * j + z][m], v, lo[u][m][0], lo[u][m][1]);
             }
-          }
         }
       }
     }
