@@ -13,13 +13,17 @@
 // The words are laid out so that what a lane decodes is its own fragment of the
 // B operand of mma.sync m16n8k16: nothing passes through shared memory twice.
 //
-// Contractions.  Scores S[h][t] = q_h . K_t and outputs O[h][d] = sum_t P[h][t]
+// Contractions (G > 4; below 5 heads see N4).  Scores S[h][t] = q_h . K_t and outputs O[h][d] = sum_t P[h][t]
 // V_t[d].  q (scaled by a power of two) and P are split into two f16 terms, hi =
 // f16(x) and lo = f16(x - hi), about 22 bits.  With G <= 8 hi takes rows 0..7 of
 // the 16-row A operand of the scores and lo rows 8..15 (G = 16: a product each); for
 // the outputs V^T is the A operand, 16 dimensions a tile, and P, as the scores'
 // accumulators hold it, the B operand of 8 heads, hi and lo a product each into
 // the same accumulators: 32 registers of them for 8 heads of 128 dimensions.
+//
+// With G <= 4 the positions are the rows of the scores' A operand and the heads the
+// columns of B, hi of 4 heads and lo of 4 heads side by side, and the weights are
+// transposed in registers (movmatrix) to be B of the outputs: half the products.
 //
 // What bounds it: a byte of cache is 1.8 values, and a value costs about 2.3
 // instructions of a lane, so at 6.8 TB/s the SMs' issue slots are about 3/4 busy:
@@ -33,6 +37,12 @@ namespace nt {
 constexpr int kKv4Batch = 1024;        // sequences of one launch: their pair offsets are kept in shared memory
 constexpr int kKv4AttnMaxCtas = 152;   // one CTA per SM; the workspace holds two partial results of each
 constexpr int kKv4MinPairs = 1;        // fewest pairs of chunks of a warp: below, fewer CTAs work
+// An item's start and end cost a warp about as much as a pair (q to split, sums to
+// reduce, results to store): the share-out counts it as so many pairs more, in
+// front of the item's own.  (Measured, with 0, 1, 2 and 3: 56 sequences of up to 9001
+// positions 80.0, 81.0, 79.2, 78.6 us; 64 of up to 200: 18.2, 15.5, 13.8, 13.6; 8 of up
+// to 1500: 10.7, 10.6, 12.4, 12.7.)
+constexpr int kKv4ItemPairs = 2;
 
 struct Kv4AttnArgs {
   int32_t layer, n, G;
@@ -51,12 +61,13 @@ struct Kv4AttnArgs {
 // number of CTAs that worked on it).
 __host__ __device__ constexpr int kv4_part_floats(int hd, int rows) { return rows * hd + 2 * rows + 4; }
 
-template <int HD, int MT>
+// HB: query heads of a kv head that the instantiation is made for, up to 4, 8 or 16.
+template <int HD, int HB>
 struct Kv4AttnCfg {
-  static constexpr int NW = MT == 1 ? 16 : (HD == 128 ? 8 : 12);                       // warps: registers decide
-  static constexpr int S = HD == 128 && MT == 1 ? 2 : 4;                               // ring stages of a warp
+  static constexpr int NW = HB == 16 ? (HD == 128 ? 8 : 12) : (HD == 128 && HB == 8 ? 12 : 16);   // warps: registers decide
+  static constexpr int S = HD == 128 && HB < 16 ? 2 : 4;                               // ring stages of a warp
   static constexpr int kThreads = 32 * NW;
-  static constexpr int kRows = 8 * MT;                                                 // heads of a partial result
+  static constexpr int kRows = HB;                                                     // heads of a partial result
   static constexpr int kPart = kv4_part_floats(HD, kRows);
   static constexpr int kPair = 2 * kv4_chunk_bytes(HD);                                // a stage: two chunks
   static constexpr int kRing = 0;
@@ -65,7 +76,8 @@ struct Kv4AttnCfg {
   static constexpr int kEntry = kPrefix + (kKv4Batch + 4) * 4;                         // {sequence, length} of each
   static constexpr int kBars = kEntry + kKv4Batch * 8;
   static constexpr int kItem = kBars + NW * S * 8;                                     // item of each slot (-1: none)
-  static constexpr int kSmem = kItem + 2 * NW * 4;
+  static constexpr int kOrder = kItem + 2 * NW * 4;                                    // [NW][32] slots in order (merge)
+  static constexpr int kSmem = kOrder + NW * 32 * 4;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kPart * 4 <= S * kPair && kPart % 4 == 0, "a warp's ring holds a partial result");
   static_assert(2 * NW <= 32, "a lane per slot");
@@ -73,7 +85,7 @@ struct Kv4AttnCfg {
 };
 
 size_t kv4_attn_ws_bytes(int n_heads, int n_kv, int hd) {
-  return size_t(kKv4AttnMaxCtas) * 2 * size_t(kv4_part_floats(hd, n_heads / n_kv > 8 ? 16 : 8)) * 4;
+  return size_t(kKv4AttnMaxCtas) * 2 * size_t(kv4_part_floats(hd, n_heads / n_kv > 8 ? 16 : (n_heads / n_kv > 4 ? 8 : 4))) * 4;
 }
 
 // ------------------------------------------------------------ small pieces --
@@ -120,11 +132,6 @@ __device__ __forceinline__ uint32_t kv4_h2mul(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-__device__ __forceinline__ uint32_t kv4_h2add(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
 // (w & mask) | magic
 template <uint32_t mask>
 __device__ __forceinline__ uint32_t kv4_pick(uint32_t w, uint32_t magic) {
@@ -133,17 +140,15 @@ __device__ __forceinline__ uint32_t kv4_pick(uint32_t w, uint32_t magic) {
   return d;
 }
 // The four half2 of a word: value pairs (code k, code k + 4), k = 0..3, times the
-// scale pair d; d72 = -72 d.  Codes 1 and 3 stand (3 after a shift) in bits 4..7:
-// 64 + q, and one multiply-add.  Codes 0 and 2 stand in bits 0..3: 1024 + q, less
-// 1032, times d, three exact steps as well; two more shifts would spare one of
-// them but the logic pipe, at half the rate, is the busier one.
+// scale pair d; d72 = -72 d.  (Two of the shifts can be saved by taking codes 0 and
+// 2 as 1024 + q, less 1032, times d: measured 4% slower at 131077 positions, the
+// half2 and matrix instructions being what is short, not the shifts.)
 __device__ __forceinline__ void kv4_decode(uint32_t w, uint32_t d, uint32_t d72, uint32_t (&b)[4]) {
-  constexpr uint32_t k64 = 0x54005400u, k1024 = 0x64006400u, kMinus1032 = 0xe408e408u;
-  const uint32_t u = w >> 8;
-  b[0] = kv4_h2mul(kv4_h2add(kv4_pick<0x000f000fu>(w, k1024), kMinus1032), d);
+  constexpr uint32_t k64 = 0x54005400u;
+  b[0] = kv4_h2fma(kv4_pick<0x00f000f0u>(w << 4, k64), d, d72);
   b[1] = kv4_h2fma(kv4_pick<0x00f000f0u>(w, k64), d, d72);
-  b[2] = kv4_h2mul(kv4_h2add(kv4_pick<0x000f000fu>(u, k1024), kMinus1032), d);
-  b[3] = kv4_h2fma(kv4_pick<0x00f000f0u>(u, k64), d, d72);
+  b[2] = kv4_h2fma(kv4_pick<0x00f000f0u>(w >> 4, k64), d, d72);
+  b[3] = kv4_h2fma(kv4_pick<0x00f000f0u>(w >> 8, k64), d, d72);
 }
 constexpr uint32_t kMinus72 = 0xd480d480u;   // f16 -72 twice
 
@@ -161,6 +166,13 @@ __device__ __forceinline__ void kv4_mma(float (&d)[4], const uint32_t (&a)[4], u
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 transpose of f16 held as matrix fragments (a row of two per lane)
+__device__ __forceinline__ uint32_t kv4_transpose(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 __device__ __forceinline__ void kv4_bar_init(uint32_t bar) {
@@ -218,7 +230,8 @@ __device__ __forceinline__ int kv4_find(const int* prefix, int n, int x) {
 // ------------------------------------------------------------ the kernel --
 
 // The chunk pairs of all (entry, kv head) items in a row, item after item, are
-// shared out evenly: warp w of CTA b takes pairs [(b NW + w) C, (b NW + w + 1) C).
+// shared out evenly: warp w of CTA b takes units [(b NW + w) C, (b NW + w + 1) C),
+// a unit being a pair or an item's cost.
 // An item that lies within a warp's share is finished by it; one that lies within
 // a CTA's is merged in shared memory; the rest leaves partial results (at most two
 // a CTA: slot 0 of an item begun before it, slot 1 of one that goes on behind it)
@@ -228,11 +241,15 @@ __device__ __forceinline__ int kv4_find(const int* prefix, int n, int x) {
 // A warp leaves at most two partial results to the CTA: of the item it did not
 // begin (slot 2 warp, in memory of its own) and of the one it did not end (slot
 // 2 warp + 1, its last: it stands in the warp's ring, which is empty by then).
-template <int HD, int MT>
-__global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv4 c, Kv4AttnArgs a) {
-  using Cfg = Kv4AttnCfg<HD, MT>;
+template <int HD, int HB>
+__global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv4 c, Kv4AttnArgs a) {
+  using Cfg = Kv4AttnCfg<HD, HB>;
   using L = Kv4Chunk<HD>;
   constexpr int NW = Cfg::NW, S = Cfg::S, NG = HD / 32, NT = HD / 8, CB = L::kBytes, ROWS = Cfg::kRows;
+  constexpr bool N4 = HB == 4;             // hi and lo of up to 4 heads side by side as the 8 columns of a B operand
+  constexpr int MT = HB == 16 ? 2 : 1;     // accumulators of 8 head columns each
+  constexpr int NH = HB == 8 ? 1 : 2;      // heads whose scores a lane holds
+  constexpr int NX = N4 ? 4 : 8;           // scores of a head and pair that a lane holds
   extern __shared__ __align__(128) uint8_t sm[];
   int* prefix = reinterpret_cast<int*>(sm + Cfg::kPrefix);
   int2* entry = reinterpret_cast<int2*>(sm + Cfg::kEntry);
@@ -256,7 +273,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
         const int2 sl = kv4_entry(c, a, e, &bad);
         if (bad && blockIdx.x == 0) kv4_flag(c, bad);
         entry[e] = sl;
-        mine = kv4_pairs(sl.y) * c.n_kv;
+        mine = sl.y ? (kv4_pairs(sl.y) + kKv4ItemPairs) * c.n_kv : 0;
       }
       int x = mine;
 #pragma unroll
@@ -305,20 +322,21 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
   const int cpp = c.page_len / kKv4Chunk;
   const uint8_t* layer_pool = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes();
 
-  // the item of pair y: entry e, kv head g, pair pi of np
+  // the item of unit y of the share-out: entry e, kv head g, pair pi of np (below 0: the item's cost, nothing to read)
   auto locate = [&](int y, int& e, int& g, int& pi, int& np) {
     e = kv4_find(prefix, n, y);
     np = kv4_pairs(entry[e].y);
-    const int r = y - prefix[e];
-    g = int(unsigned(r) / unsigned(np));
-    pi = r - g * np;
+    const int r = y - prefix[e], units = np + kKv4ItemPairs;
+    g = int(unsigned(r) / unsigned(units));
+    pi = r - g * units - kKv4ItemPairs;
   };
   // indexes of the two chunks of pair x of this warp within the layer's pool (in
-  // chunks); -1: no page, -2: behind the sequence's end
+  // chunks); -1: no page, -2: behind the sequence's end, -3: no pair
   auto resolve = [&](int x) -> int2 {
     if (x >= count) return make_int2(-2, -2);
     int e, g, pi, np;
     locate(w0 + x, e, g, pi, np);
+    if (pi < 0) return make_int2(-3, -3);
     const int len = entry[e].y;
     const int32_t* row = c.table + int64_t(entry[e].x) * c.max_pages;
     auto chunk = [&](int ci) -> int {
@@ -367,23 +385,28 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll 1
   for (int i = 0; i < S; i++) issue();
 
-  float O[NT / 2][MT][4];   // dimensions 32 j + 4 gi + 2 z (+ 1: the last two) of tile 2 j + z, heads 8 m + 2 tg, + 1
-  uint32_t qa[MT][HD / 16][4];
-  float mref[MT], l[MT], cs[MT];
+  // O: dimensions 32 j + 4 gi + 2 z (+ 1: the last two) of tile 2 j + z; columns 2 tg, 2 tg + 1: heads 8 m + column, or
+  // (N4) hi of heads 0..3, then lo
+  float O[NT / 2][MT][4];
+  uint32_t qa[N4 ? 1 : MT][HD / 16][N4 ? 2 : 4];
+  // a lane's heads: gi (HB 8), gi and gi + 8 (HB 16), 2 (tg % 2) and the next one (N4)
+  float mref[NH], l[NH], cs[NH];
   int k = 0;                                  // pairs read
 #pragma unroll 1
   while (k < count) {
+    for (; pi0 < 0 && k < count; pi0++, k++) issue();
+    if (k == count) break;
     // ---- a segment: consecutive pairs of one item
     const int seg = np - pi0 < count - k ? np - pi0 : count - k;
     int live = entry[e].y - pi0 * 2 * kKv4Chunk;   // positions from the pair on that exist
     bool poison = false;
     {
-      // q of heads gi (and gi + 8), scaled so that a head's largest element is in [2^10, 2^11), split
+      // q of heads gi (and gi + 8; N4: gi % 4), scaled so that a head's largest element is in [2^10, 2^11), split
       const float* qb = a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD;
-      float qx[MT][NG][8];
+      float qx[MT][NG][8], back[MT];
 #pragma unroll
       for (int m = 0; m < MT; m++) {
-        const int h = gi + 8 * m;
+        const int h = N4 ? gi & 3 : gi + 8 * m;
         float top = 0.f;
 #pragma unroll
         for (int j = 0; j < NG; j++) {
@@ -402,7 +425,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
         int ex = int(__float_as_uint(top) >> 23);
         ex = ex < 11 ? 11 : ex;                                  // (zeros and values below 2^-116)
         const float up = __uint_as_float(uint32_t(264 - ex) << 23);   // 2^(137 - ex)
-        cs[m] = a.scale_log2 * __uint_as_float(uint32_t(ex - 10) << 23);
+        back[m] = a.scale_log2 * __uint_as_float(uint32_t(ex - 10) << 23);
 #pragma unroll
         for (int j = 0; j < NG; j++)
 #pragma unroll
@@ -412,16 +435,24 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
       for (int j = 0; j < NG; j++)
 #pragma unroll
         for (int i = 0; i < 4; i++) {   // pair (code i, code i + 4): k-step 2 j + i / 2, half i % 2
-          const int kk = 2 * j + (i >> 1), r = 2 * (i & 1);
-          if (MT == 1) {
-            kv4_split(qx[0][j][i], qx[0][j][i + 4], qa[0][kk][r], qa[0][kk][r + 1]);
+          const int kk = 2 * j + (i >> 1), r = i & 1;
+          if constexpr (N4) {
+            uint32_t hi, lo;
+            kv4_split(qx[0][j][i], qx[0][j][i + 4], hi, lo);
+            qa[0][kk][r] = gi < 4 ? hi : lo;
+          } else if constexpr (MT == 1) {
+            kv4_split(qx[0][j][i], qx[0][j][i + 4], qa[0][kk][2 * r], qa[0][kk][2 * r + 1]);
           } else {
-            kv4_split(qx[0][j][i], qx[0][j][i + 4], qa[0][kk][r], qa[MT - 1][kk][r]);
-            kv4_split(qx[MT - 1][j][i], qx[MT - 1][j][i + 4], qa[0][kk][r + 1], qa[MT - 1][kk][r + 1]);
+            kv4_split(qx[0][j][i], qx[0][j][i + 4], qa[0][kk][2 * r], qa[MT - 1][kk][2 * r]);
+            kv4_split(qx[MT - 1][j][i], qx[MT - 1][j][i + 4], qa[0][kk][2 * r + 1], qa[MT - 1][kk][2 * r + 1]);
           }
         }
 #pragma unroll
-      for (int m = 0; m < MT; m++) { mref[m] = -3e38f; l[m] = 0.f; }
+      for (int m = 0; m < NH; m++) {
+        cs[m] = N4 ? __shfl_sync(0xffffffffu, back[0], 4 * (2 * (tg & 1) + m)) : back[N4 ? 0 : m];
+        mref[m] = -3e38f;
+        l[m] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < NT / 2; i++)
 #pragma unroll
@@ -470,57 +501,78 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
             const uint32_t d = __byte_perm(ks[i][j >> 1], 0u, (j & 1) ? 0x3232u : 0x1010u);
             kv4_decode(kw[i][j], d, kv4_h2mul(d, kMinus72), b[i]);
           }
+          // (products into the same accumulators never follow one another)
+          if constexpr (N4) {   // 16 positions are the rows, the heads the columns; even and odd k-steps apart
 #pragma unroll
-          for (int m = 0; m < MT; m++)   // products into the same accumulators never follow one another
-#pragma unroll
-            for (int y = 0; y < 2; y++)
-#pragma unroll
-              for (int i = 0; i < 2; i++) kv4_mma(sc[2 * u + i], qa[m][2 * j + y], b[i][2 * y], b[i][2 * y + 1]);
-        }
-      }
-      // the scores of this lane's heads at positions 8 i + 2 tg and 8 i + 2 tg + 1, i < 4
-      float x[MT][8];
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-#pragma unroll
-        for (int y = 0; y < 2; y++) {
-          if (MT == 1) {
-            x[0][2 * i + y] = sc[i][y] + sc[i][y + 2];
+            for (int y = 0; y < 2; y++) {
+              const uint32_t w[4] = {b[0][2 * y], b[1][2 * y], b[0][2 * y + 1], b[1][2 * y + 1]};
+              kv4_mma(sc[2 * u + y], w, qa[0][2 * j + y][0], qa[0][2 * j + y][1]);
+            }
           } else {
-            x[0][2 * i + y] = sc[i][y];
-            x[MT - 1][2 * i + y] = sc[i][y + 2];
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+#pragma unroll
+              for (int y = 0; y < 2; y++)
+#pragma unroll
+                for (int i = 0; i < 2; i++) kv4_mma(sc[2 * u + i], qa[m][2 * j + y], b[i][2 * y], b[i][2 * y + 1]);
           }
         }
+      }
+      // the scores of this lane's heads; of the i-th this is the position
+      auto at = [&](int i) { return N4 ? 16 * (i >> 1) + 8 * (i & 1) + gi : 8 * (i >> 1) + 2 * tg + (i & 1); };
+      float x[NH][NX];
+      if constexpr (N4) {
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+          for (int y = 0; y < 4; y++) {
+            const float v = sc[2 * u][y] + sc[2 * u + 1][y];      // hi of columns tg < 2, lo of the others
+            x[y & (NH - 1)][2 * u + (y >> 1)] = v + __shfl_xor_sync(0xffffffffu, v, 2);
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+#pragma unroll
+          for (int y = 0; y < 2; y++) {
+            if (MT == 1) {
+              x[0][(2 * i + y) % NX] = sc[i][y] + sc[i][y + 2];
+            } else {
+              x[0][(2 * i + y) % NX] = sc[i][y];
+              x[NH - 1][(2 * i + y) % NX] = sc[i][y + 2];
+            }
+          }
+      }
       if (live < 2 * kKv4Chunk) {
 #pragma unroll
-        for (int m = 0; m < MT; m++)
+        for (int m = 0; m < NH; m++)
 #pragma unroll
-          for (int i = 0; i < 8; i++)
-            if (8 * (i >> 1) + 2 * tg + (i & 1) >= live) x[m][i] = -INFINITY;
+          for (int i = 0; i < NX; i++)
+            if (at(i) >= live) x[m][i] = -INFINITY;
       }
       // ---- weights p = 2^(s - mref).  Only where a lane's sum passes 2^15 (at first it is infinite) is the maximum looked
       // for; where that passes mref by 14, it less 6 becomes mref.  So weights stay below 2^15, within f16, and the largest
       // so far is at least 2^6: the lo terms of all that matter are ordinary f16 numbers.
-      float p[MT][8], sum[MT];
+      float p[NH][NX], sum[NH];
       auto weights = [&]() {
 #pragma unroll
-        for (int m = 0; m < MT; m++) {
+        for (int m = 0; m < NH; m++) {
 #pragma unroll
-          for (int i = 0; i < 8; i++) p[m][i] = kv4_ex2(fmaf(x[m][i], cs[m], -mref[m]));
-          sum[m] = ((p[m][0] + p[m][1]) + (p[m][2] + p[m][3])) + ((p[m][4] + p[m][5]) + (p[m][6] + p[m][7]));
+          for (int i = 0; i < NX; i++) p[m][i] = kv4_ex2(fmaf(x[m][i], cs[m], -mref[m]));
+          sum[m] = (p[m][0] + p[m][1]) + (p[m][2] + p[m][3]);
+          if constexpr (!N4) sum[m] += (p[m][4 % NX] + p[m][5 % NX]) + (p[m][6 % NX] + p[m][7 % NX]);
         }
       };
       weights();
-      if (__any_sync(0xffffffffu, sum[0] > 32768.f || sum[MT - 1] > 32768.f)) {
-        float f[MT];
+      if (__any_sync(0xffffffffu, sum[0] > 32768.f || sum[NH - 1] > 32768.f)) {
+        float f[NH];
 #pragma unroll
-        for (int m = 0; m < MT; m++) {
+        for (int m = 0; m < NH; m++) {
           float top = x[m][0];
 #pragma unroll
-          for (int i = 1; i < 8; i++) top = fmaxf(top, x[m][i]);
+          for (int i = 1; i < NX; i++) top = fmaxf(top, x[m][i]);
           top *= cs[m];
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+#pragma unroll
+          for (int o = N4 ? 4 : 1; o <= (N4 ? 16 : 2); o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           const float to = top > mref[m] + 14.f ? top - 6.f : mref[m];
           f[m] = kv4_ex2(mref[m] - to);
           mref[m] = to;
@@ -528,7 +580,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
         }
 #pragma unroll
         for (int m = 0; m < MT; m++) {
-          const float f0 = __shfl_sync(0xffffffffu, f[m], 8 * tg), f1 = __shfl_sync(0xffffffffu, f[m], 8 * tg + 4);
+          const float f0 = N4 ? f[0] : __shfl_sync(0xffffffffu, f[m], 8 * tg);
+          const float f1 = N4 ? f[NH - 1] : __shfl_sync(0xffffffffu, f[m], 8 * tg + 4);
 #pragma unroll
           for (int i = 0; i < NT / 2; i++) {
             O[i][m][0] *= f0; O[i][m][1] *= f1;
@@ -537,16 +590,24 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
         }
         weights();
       }
-      // P of the chunk u as B operand: positions 2 tg, 2 tg + 1 and 8 + 2 tg, 8 + 2 tg + 1 of head gi (+ 8 m)
-      uint32_t hi[2][MT][2], lo[2][MT][2];
 #pragma unroll
-      for (int m = 0; m < MT; m++) {
-        l[m] += sum[m];
+      for (int m = 0; m < NH; m++) l[m] += sum[m];
+      // P of chunk u as B operand: rows 2 tg, 2 tg + 1 (and + 8) are positions, column gi a head (+ 8 m)
+      uint32_t hi[2][MT][2], lo[2][MT][2];   // (N4: hi holds both)
 #pragma unroll
-        for (int u = 0; u < 2; u++)
+      for (int u = 0; u < 2; u++)
 #pragma unroll
-          for (int i = 0; i < 2; i++) kv4_split(p[m][4 * u + 2 * i], p[m][4 * u + 2 * i + 1], hi[u][m][i], lo[u][m][i]);
-      }
+        for (int i = 0; i < 2; i++) {
+          if constexpr (N4) {   // rows are positions, columns heads here: transposed
+            uint32_t h2, l2;
+            kv4_split(p[0][2 * u + i], p[NH - 1][2 * u + i], h2, l2);
+            hi[u][0][i] = kv4_transpose(tg < 2 ? h2 : l2);
+          } else {
+#pragma unroll
+            for (int m = 0; m < MT; m++)
+              kv4_split(p[m][(4 * u + 2 * i) % NX], p[m][(4 * u + 2 * i + 1) % NX], hi[u][m][i], lo[u][m][i]);
+          }
+        }
 
       // ---- weighted values
 #pragma unroll
@@ -564,8 +625,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
         if (live < 2 * kKv4Chunk) {   // positions behind the end: scale 0, whatever the page holds there
 #pragma unroll
           for (int r = 0; r < 2; r++) {
-            const int at = 16 * u + 8 * r + 2 * tg;
-            const uint32_t keep = (at < live ? 0xffffu : 0u) | (at + 1 < live ? 0xffff0000u : 0u);
+            const int v0 = 16 * u + 8 * r + 2 * tg;
+            const uint32_t keep = (v0 < live ? 0xffffu : 0u) | (v0 + 1 < live ? 0xffff0000u : 0u);
 #pragma unroll
             for (int j = 0; j < NG; j++) vs[r][j] &= keep;
           }
@@ -582,22 +643,24 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
               const uint32_t v[4] = {b[0][2 * z], b[0][2 * z + 1], b[1][2 * z], b[1][2 * z + 1]};
               kv4_mma(O[2 * j + z][m], v, hi[u][m][0], hi[u][m][1]);
             }
+          if constexpr (!N4) {
 #pragma unroll
-          for (int m = 0; m < MT; m++)
+            for (int m = 0; m < MT; m++)
 #pragma unroll
-            for (int z = 0; z < 2; z++) {
-              const uint32_t v[4] = {b[0][2 * z], b[0][2 * z + 1], b[1][2 * z], b[1][2 * z + 1]};
-              kv4_mma(O[2 * j + z][m], v, lo[u][m][0], lo[u][m][1]);
-            }
+              for (int z = 0; z < 2; z++) {
+                const uint32_t v[4] = {b[0][2 * z], b[0][2 * z + 1], b[1][2 * z], b[1][2 * z + 1]};
+                kv4_mma(O[2 * j + z][m], v, lo[u][m][0], lo[u][m][1]);
+              }
+          }
         }
       }
     }
 
     // ---- the end of the segment
 #pragma unroll
-    for (int m = 0; m < MT; m++) {
-      l[m] += __shfl_xor_sync(0xffffffffu, l[m], 1);
-      l[m] += __shfl_xor_sync(0xffffffffu, l[m], 2);
+    for (int m = 0; m < NH; m++) {
+#pragma unroll
+      for (int o = N4 ? 4 : 1; o <= (N4 ? 16 : 2); o <<= 1) l[m] += __shfl_xor_sync(0xffffffffu, l[m], o);
       if (poison) l[m] = NAN;
     }
     const bool whole = pi0 == 0 && seg == np;
@@ -610,18 +673,39 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
     if (!whole && lane == 0) slot_item[slot] = e_was * c.n_kv + g_was;
     __syncwarp();   // (slot 1 is the ring: every lane has read its last pair)
     float* to = whole ? a.out + int64_t(e_was) * a.out_stride + int64_t(g_was) * G * HD : po;
+    if constexpr (N4) {   // lanes tg < 2 store head 2 (tg % 2), the others the next one, dimensions 32 j + 4 gi + 0..3
+      const int y = tg >> 1, h = 2 * (tg & 1) + y;
+      const float f = whole ? 1.f / (y ? l[NH - 1] : l[0]) : 1.f;
+      if (!whole && gi == 0) reinterpret_cast<float2*>(po + ROWS * HD)[h] = make_float2(y ? mref[NH - 1] : mref[0], y ? l[NH - 1] : l[0]);
 #pragma unroll
-    for (int m = 0; m < MT; m++) {
-      if (!whole && tg == 0) reinterpret_cast<float2*>(po + ROWS * HD)[gi + 8 * m] = make_float2(mref[m], l[m]);
+      for (int j = 0; j < NG; j++) {
+        float o[2][4];
 #pragma unroll
-      for (int y = 0; y < 2; y++) {   // head 8 m + 2 tg + y: dimensions 32 j + 4 gi + 0..3
-        const int h = 8 * m + 2 * tg + y;
-        const float lh = __shfl_sync(0xffffffffu, l[m], 8 * tg + 4 * y), f = whole ? 1.f / lh : 1.f;
-        if (h < G) {
+        for (int z = 0; z < 2; z++)
 #pragma unroll
-          for (int j = 0; j < NG; j++)
-            *reinterpret_cast<float4*>(to + h * HD + 32 * j + 4 * gi) =
-                make_float4(O[2 * j][m][y] * f, O[2 * j][m][y + 2] * f, O[2 * j + 1][m][y] * f, O[2 * j + 1][m][y + 2] * f);
+          for (int i = 0; i < 4; i++) {   // hi + lo
+            const float v = O[2 * j + z][0][i];
+            o[z][i] = v + __shfl_xor_sync(0xffffffffu, v, 2);
+          }
+        if (h < G)
+          *reinterpret_cast<float4*>(to + h * HD + 32 * j + 4 * gi) =
+              make_float4((y ? o[0][1] : o[0][0]) * f, (y ? o[0][3] : o[0][2]) * f, (y ? o[1][1] : o[1][0]) * f,
+                          (y ? o[1][3] : o[1][2]) * f);
+      }
+    } else {
+#pragma unroll
+      for (int m = 0; m < MT; m++) {
+        if (!whole && tg == 0) reinterpret_cast<float2*>(po + ROWS * HD)[gi + 8 * m] = make_float2(mref[m], l[m]);
+#pragma unroll
+        for (int y = 0; y < 2; y++) {   // head 8 m + 2 tg + y: dimensions 32 j + 4 gi + 0..3
+          const int h = 8 * m + 2 * tg + y;
+          const float lh = __shfl_sync(0xffffffffu, l[m], 8 * tg + 4 * y), f = whole ? 1.f / lh : 1.f;
+          if (h < G) {
+#pragma unroll
+            for (int j = 0; j < NG; j++)
+              *reinterpret_cast<float4*>(to + h * HD + 32 * j + 4 * gi) =
+                  make_float4(O[2 * j][m][y] * f, O[2 * j][m][y + 2] * f, O[2 * j + 1][m][y] * f, O[2 * j + 1][m][y + 2] * f);
+          }
         }
       }
     }
@@ -631,12 +715,18 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, MT>::kThreads, 1) k_kv4_attn(Kv
   __syncthreads();
   constexpr int V = HD / 32;
   const int mine = lane < 2 * NW ? slot_item[lane] : -1;
+  int* order = reinterpret_cast<int*>(sm + Cfg::kOrder) + warp * 32;
   for (uint32_t left = __ballot_sync(0xffffffffu, mine >= 0); left;) {
     const int a0 = __ffs(left) - 1, item = __shfl_sync(0xffffffffu, mine, a0);
     const uint32_t members = __ballot_sync(0xffffffffu, mine == item);
     left &= ~members;
-    const int nm = __popc(members), nth = lane < nm ? int(__fns(members, 0, lane + 1)) : a0;   // lane i: the i-th slot
-    const int ie = item / c.n_kv, ig = item % c.n_kv, ip = kv4_pairs(entry[ie].y), first = prefix[ie] + ig * ip;
+    const int nm = __popc(members);
+    __syncwarp();
+    if (mine == item) order[__popc(members & ((1u << lane) - 1u))] = lane;
+    __syncwarp();
+    const int nth = order[lane < nm ? lane : 0];   // lane i: the item's i-th slot
+    const int ie = item / c.n_kv, ig = item % c.n_kv, ip = kv4_pairs(entry[ie].y);
+    const int first = prefix[ie] + ig * (ip + kKv4ItemPairs) + kKv4ItemPairs;
     const bool whole = first >= c0 && first + ip <= c1;
     float* part = part0 + (first < c0 ? 0 : Cfg::kPart);
     float* to = whole ? a.out + int64_t(ie) * a.out_stride + int64_t(ig) * G * HD : part;
@@ -690,58 +780,71 @@ template <int HD>
 __global__ void __launch_bounds__(32 * kKv4MergeWarps) k_kv4_attn_merge(Kv4 c, Kv4AttnArgs a, int part_floats, int rows) {
   constexpr int V = HD / 32;
   __shared__ float s_o[kKv4MergeWarps][HD];
-  __shared__ float s_l[kKv4MergeWarps];
+  __shared__ float2 s_ml[kKv4MergeWarps];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, h = blockIdx.y;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* first = a.part + (int64_t(blockIdx.x) * 2 + 1) * part_floats;   // slot 1, then slot 0 of the next CTAs
-  const int* header = reinterpret_cast<const int*>(first + part_floats - 4);
-  const int item = __ldcg(header), members = __ldcg(header + 1);
-  if (item < 0) return;
-  auto record = [&](int b) { return b ? first + (int64_t(b) * 2 - 1) * part_floats : first; };
-  float M = -INFINITY;
-  for (int b = lane; b < members; b += 32) M = fmaxf(M, __ldcg(record(b) + rows * HD + 2 * h));
-#pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float sum = 0.f, o[V];
+  const int2 header = __ldcg(reinterpret_cast<const int2*>(first + part_floats - 4));
+  const int most = int(gridDim.x + 1 - blockIdx.x);   // CTAs from this one on
+  // a warp takes members warp, warp + 8, ...; the first three are read beside the header, before it is known who they are
+  float M = -INFINITY, sum = 0.f, o[V];
 #pragma unroll
   for (int v = 0; v < V; v++) o[v] = 0.f;
-#pragma unroll 4
-  for (int b = warp; b < members; b += kKv4MergeWarps) {
-    const float* r = record(b);
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(r + rows * HD) + h);
-    float x[V];
-    if (V == 4) {
-      const float4 u = __ldcg(reinterpret_cast<const float4*>(r + h * HD) + lane);
-      x[0] = u.x; x[1] = u.y; x[2 % V] = u.z; x[3 % V] = u.w;
-    } else {
-      const float2 u = __ldcg(reinterpret_cast<const float2*>(r + h * HD) + lane);
-      x[0] = u.x; x[1] = u.y;
-    }
-    const float f = kv4_ex2(ml.x - M);
-    sum = fmaf(ml.y, f, sum);
+  int members = most;
+  for (int b0 = warp; b0 < members; b0 += 3 * kKv4MergeWarps) {
+    float2 ml[3];
+    float x[3][V];
 #pragma unroll
-    for (int v = 0; v < V; v++) o[v] = fmaf(x[v], f, o[v]);
+    for (int u = 0; u < 3; u++) {
+      const int b = b0 + u * kKv4MergeWarps;
+      if (b < members) {
+        const float* r = b ? first + (int64_t(b) * 2 - 1) * part_floats : first;
+        ml[u] = __ldcg(reinterpret_cast<const float2*>(r + rows * HD) + h);
+        if (V == 4) {
+          const float4 y = __ldcg(reinterpret_cast<const float4*>(r + h * HD) + lane);
+          x[u][0] = y.x; x[u][1] = y.y; x[u][2 % V] = y.z; x[u][3 % V] = y.w;
+        } else {
+          const float2 y = __ldcg(reinterpret_cast<const float2*>(r + h * HD) + lane);
+          x[u][0] = y.x; x[u][1] = y.y;
+        }
+      }
+    }
+    if (header.x < 0) return;   // (the whole CTA: no barrier has been passed)
+    members = header.y;
+#pragma unroll
+    for (int u = 0; u < 3; u++) {
+      if (b0 + u * kKv4MergeWarps >= members) continue;
+      const float to = fmaxf(M, ml[u].x), was = kv4_ex2(M - to), f = kv4_ex2(ml[u].x - to);
+      M = to;
+      sum = fmaf(sum, was, ml[u].y * f);
+#pragma unroll
+      for (int v = 0; v < V; v++) o[v] = fmaf(o[v], was, x[u][v] * f);
+    }
   }
+  if (header.x < 0) return;
 #pragma unroll
   for (int v = 0; v < V; v++) s_o[warp][lane * V + v] = o[v];
-  if (lane == 0) s_l[warp] = sum;
+  if (lane == 0) s_ml[warp] = make_float2(M, sum);
   __syncthreads();
   if (t < HD) {
-    float total = 0.f, x = 0.f;
+    float top = -INFINITY, total = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kKv4MergeWarps; w++) top = fmaxf(top, s_ml[w].x);
 #pragma unroll
     for (int w = 0; w < kKv4MergeWarps; w++) {
-      total += s_l[w];
-      x += s_o[w][t];
+      const float f = kv4_ex2(s_ml[w].x - top);
+      total = fmaf(s_ml[w].y, f, total);
+      y = fmaf(s_o[w][t], f, y);
     }
-    const int e = item / c.n_kv, g = item % c.n_kv;
-    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + t] = x / total;
+    const int e = header.x / c.n_kv, g = header.x % c.n_kv;
+    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + t] = y / total;
   }
 }
 
-template <int HD, int MT>
+template <int HD, int HB>
 static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_pairs, cudaStream_t s) {
-  using Cfg = Kv4AttnCfg<HD, MT>;
-  static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, MT>, Cfg::kSmem);
+  using Cfg = Kv4AttnCfg<HD, HB>;
+  static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, HB>, Cfg::kSmem);
   if (setup.err != cudaSuccess) return setup.err;
   const int64_t useful = (most_pairs + Cfg::NW * kKv4MinPairs - 1) / (Cfg::NW * kKv4MinPairs);
   int64_t ctas = setup.sms < kKv4AttnMaxCtas ? setup.sms : kKv4AttnMaxCtas;
@@ -756,7 +859,7 @@ static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_pai
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, MT>, k, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB>, k, a);
   if (e != cudaSuccess || ctas < 2) return e;
   cfg.gridDim = dim3(unsigned(ctas - 1), unsigned(a.G));   // the last CTA's items end with it
   cfg.blockDim = dim3(32 * kKv4MergeWarps);
@@ -807,7 +910,7 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
   a.part = static_cast<float*>(dev_workspace);
   a.q_stride = q_stride;
   a.out_stride = out_stride;
-  const int64_t entry_pairs = int64_t(k.n_kv) * ((int64_t(k.max_pages) * k.page_len + 31) / 32);
+  const int64_t entry_pairs = int64_t(k.n_kv) * ((int64_t(k.max_pages) * k.page_len + 31) / 32 + kKv4ItemPairs);
   // a launch's pairs are counted in 32 bits
   const int64_t most = int64_t(1) << 30;
   if (entry_pairs > most) return bad("n_kv_heads * max_pages * page_len above 2^35");
@@ -820,8 +923,13 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
     a.q = dev_q + int64_t(i) * q_stride;
     a.out = dev_out + int64_t(i) * out_stride;
     cudaError_t e;
-    if (k.hd == 64) e = G <= 8 ? kv4_launch_attn<64, 1>(k, a, a.n * entry_pairs, s) : kv4_launch_attn<64, 2>(k, a, a.n * entry_pairs, s);
-    else e = G <= 8 ? kv4_launch_attn<128, 1>(k, a, a.n * entry_pairs, s) : kv4_launch_attn<128, 2>(k, a, a.n * entry_pairs, s);
+    const int64_t units = a.n * entry_pairs;
+    if (k.hd == 64)
+      e = G <= 4 ? kv4_launch_attn<64, 4>(k, a, units, s)
+                 : (G == 8 ? kv4_launch_attn<64, 8>(k, a, units, s) : kv4_launch_attn<64, 16>(k, a, units, s));
+    else
+      e = G <= 4 ? kv4_launch_attn<128, 4>(k, a, units, s)
+                 : (G == 8 ? kv4_launch_attn<128, 8>(k, a, units, s) : kv4_launch_attn<128, 16>(k, a, units, s));
     if (e != cudaSuccess) return cuda_fail(e, "nt_attention_kv4");
   }
   return NT_OK;
