@@ -487,8 +487,10 @@ nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t*
  * starts at element r * row_stride + g * head_stride of dev_k and of dev_v (f32 or f16 by
  * `type`: NT_F32, NT_F16; both strides multiples of 16 bytes), head_dim elements
  * each: a projection's [row][kv head][dim] as well as an f16 cache's [kv
- * head][position][dim].  A row is passed over where its sequence or position is
- * out of range, or its page is not held by this sequence alone (refs other than 1).
+ * head][position][dim].  An entry is passed over where its sequence is out of
+ * range, it has more rows than the sequence positions or rows outside [0, n_rows);
+ * rows are where their page is out of range or not held by this sequence alone
+ * (refs other than 1).
  * A sequence listed twice is flagged; which of its rows are stored is not defined. */
 nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
                         const int32_t* dev_begin, int32_t n_rows, nt_qtype type, const void* dev_k, const void* dev_v,
@@ -496,7 +498,7 @@ nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const i
 
 /* The inverse: the last positions of the listed sequences, as nt_kv4_append would
  * write them, dequantized into dev_k and dev_v (f32 exactly; f16 rounded to nearest,
- * which is exact).  A sequence may be listed several times.  Rows passed over, and
+ * which is exact).  A sequence may be listed several times, and its pages shared.  Rows passed over, and
  * rows outside [dev_begin[0], dev_begin[n]), are left as they were. */
 nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
                       const int32_t* dev_begin, int32_t n_rows, nt_qtype type, void* dev_k, void* dev_v,

@@ -36,129 +36,388 @@ bool kv4_meets_cache(const Kv4& k, const void* p, int64_t bytes) {
 }
 
 // ------------------------------------------------------------ append, read --
+//
+// A warp handles K or V of one chunk of one sequence and kv head: the rows that
+// fall on its 16 positions.  Both kernels move bytes: a position's K and V are 2 hd
+// source elements and 9/8 hd bytes of cache.
+//
+// append: a lane takes whole blocks of 32 values (the second 16 bytes of a sector
+// come from L1), so that maxima and scales need no exchange, a scale is worked out once, and
+// three instructions a value are left; the codes cross to the chunk's order in
+// shared memory.  (With the chunk's own order in registers, 8 values of a block a lane,
+// the scales, worked out 4 and 8 times over, took most of the time: 64.7 us for
+// 2 x 20011 f16 rows of 8 heads of 128.)
+// read: a lane's words give values that lie side by side in a row across the lanes.
 
 struct Kv4Rows {
-  int32_t layer, n, n_rows;
+  int32_t layer, n, n_rows, units;
   const int32_t* seq;
   const int32_t* begin;
   int64_t row_stride, head_stride;
 };
 
-// The place of row r: its page (-1: the row is passed over) and position within it.
-__device__ __forceinline__ int kv4_place(const Kv4& c, const Kv4Rows& a, int r, bool append, int* at) {
-  int i = r, behind = 1;   // entry, and rows from this one to the entry's end
+// What a warp works on: positions [first, last) of the chunk at position p0 of
+// sequence s are rows of the call, position first's row is `row`.
+struct Kv4Span {
+  int s, p0, first, last, row;
+};
+
+// Unit u of the call: a chunk that entry i's rows may touch.  Entry i's units start
+// at begin[i] / 16 + 2 i: r rows touch at most r / 16 + 2 chunks, so they do not
+// meet entry i + 1's.  Without `begin` a unit is an entry.  false: nothing to do.
+// All lanes call it and get the same.
+__device__ __forceinline__ bool kv4_span(const Kv4& c, const Kv4Rows& a, int u, Kv4Span* sp) {
+  const int lane = threadIdx.x & 31;
+  int i = u, b0 = u, b1 = u + 1, start = u;
   if (a.begin) {
-    if (r < a.begin[0] || r >= a.begin[a.n]) return -1;
-    int lo = 0, hi = a.n;  // begin[lo] <= r < begin[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.begin[mid] <= r) lo = mid; else hi = mid;
+    int lo = 0, hi = a.n;   // entry lo .. hi - 1 has unit u (if any has)
+    int step = 1;
+    while (step * 32 < hi) step *= 32;
+    for (; step; step /= 32) {   // 32 candidates at a time
+      const int e = lo + lane * step;
+      const bool before = e < hi && a.begin[e] / kKv4Chunk + 2 * e <= u;
+      const uint32_t m = __ballot_sync(0xffffffffu, before);
+      if (!m) return false;
+      lo += (31 - __clz(m)) * step;
+      hi = lo + step < hi ? lo + step : hi;
     }
     i = lo;
-    behind = a.begin[i + 1] - r;
-  } else if (r >= a.n) {
-    return -1;
+    b0 = a.begin[i];
+    b1 = a.begin[i + 1];
+    start = b0 / kKv4Chunk + 2 * i;
+    if (b1 <= b0) return false;
+    if (b0 < 0 || b1 > a.n_rows) {
+      if (lane == 0 && u == start) kv4_flag(c, NT_KV4_BAD_LEN);
+      return false;
+    }
+  } else if (u >= a.n) {
+    return false;
   }
+  const int rows = b1 - b0;
   const int s = a.seq ? a.seq[i] : i;
-  if (s < 0 || s >= c.max_seqs) { kv4_flag(c, NT_KV4_BAD_SEQ); return -1; }
-  const int n = c.len[s], pos = n - behind;
-  if (n > c.capacity() || pos < 0 || behind < 1) { kv4_flag(c, NT_KV4_BAD_LEN); return -1; }
-  const int page = c.table[int64_t(s) * c.max_pages + pos / c.page_len];
-  if (page < 0 || page >= c.n_pages || (append && c.refs[page] != 1)) { kv4_flag(c, NT_KV4_BAD_PAGE); return -1; }
-  *at = pos % c.page_len;
-  return page;
+  uint32_t bad = 0;
+  int n = 0;
+  if (s < 0 || s >= c.max_seqs) bad = NT_KV4_BAD_SEQ;
+  else if ((n = c.len[s]) > c.capacity() || n < rows) bad = NT_KV4_BAD_LEN;   // (a row range above the length: no row)
+  if (bad) {
+    if (lane == 0 && u == start) kv4_flag(c, bad);
+    return false;
+  }
+  const int p0 = (n - rows) / kKv4Chunk * kKv4Chunk + (u - start) * kKv4Chunk;   // the chunk's first position
+  if (p0 >= n) return false;
+  const int first = p0 > n - rows ? p0 : n - rows;
+  sp->s = s;
+  sp->p0 = p0;
+  sp->row = b0 + first - (n - rows);
+  sp->first = first - p0;
+  sp->last = n - p0 < kKv4Chunk ? n - p0 : kKv4Chunk;
+  return true;
 }
 
-template <class T> __device__ __forceinline__ void kv4_load8(const T* p, float (&x)[8]);
-template <> __device__ __forceinline__ void kv4_load8<float>(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-template <> __device__ __forceinline__ void kv4_load8<__half>(const __half* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-    x[2 * i] = f.x; x[2 * i + 1] = f.y;
+// The span's chunk of kv head g; NULL where there is no such page, or (append) it
+// is not the sequence's own.
+__device__ __forceinline__ uint8_t* kv4_span_chunk(const Kv4& c, const Kv4Rows& a, const Kv4Span& sp, int g, bool append) {
+  const int page = c.table[int64_t(sp.s) * c.max_pages + sp.p0 / c.page_len];
+  if (page < 0 || page >= c.n_pages || (append && c.refs[page] != 1)) {
+    if ((threadIdx.x & 31) == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
+    return nullptr;
   }
+  return c.chunk(a.layer, page, g, sp.p0 % c.page_len);
 }
-template <class T> __device__ __forceinline__ void kv4_store8(T* p, const float (&x)[8]);
-template <> __device__ __forceinline__ void kv4_store8<float>(float* p, const float (&x)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+
+__device__ __forceinline__ float kv4_max_nan(float a, float b) {   // NaN if either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
-template <> __device__ __forceinline__ void kv4_store8<__half>(__half* p, const float (&x)[8]) {
-  uint32_t w[4];
+
+// maxima of f16 pairs, NaN where one is
+__device__ __forceinline__ uint32_t kv4_max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t kv4_abs_max2(uint32_t a, uint32_t b) { return kv4_max2(a & 0x7fff7fffu, b & 0x7fff7fffu); }
+__device__ __forceinline__ float kv4_top2(uint32_t m) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&m));
+  return kv4_max_nan(f.x, f.y);
+}
+
+__device__ __forceinline__ void kv4_unpack(uint32_t w, float* x) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  x[0] = f.x; x[1] = f.y;
+}
+
+// A block of 32 source elements in registers, 16 bytes a piece.
+template <class T> struct Kv4Block;
+template <> struct Kv4Block<float> {
+  float4 r[8];
+  __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-  for (int i = 0; i < 4; i++) {
+    for (int i = 0; i < 8; i++) r[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+  }
+  __device__ __forceinline__ float top() const {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      m = kv4_max_nan(m, kv4_max_nan(kv4_max_nan(fabsf(r[i].x), fabsf(r[i].y)), kv4_max_nan(fabsf(r[i].z), fabsf(r[i].w))));
+    return m;
+  }
+  __device__ __forceinline__ void get(int i, float (&x)[8]) const {   // elements 8 i..
+    x[0] = r[2 * i].x; x[1] = r[2 * i].y; x[2] = r[2 * i].z; x[3] = r[2 * i].w;
+    x[4] = r[2 * i + 1].x; x[5] = r[2 * i + 1].y; x[6] = r[2 * i + 1].z; x[7] = r[2 * i + 1].w;
+  }
+};
+template <> struct Kv4Block<__half> {
+  uint4 r[4];
+  __device__ __forceinline__ void load(const __half* p) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) r[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ __forceinline__ float top() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; i++) m = kv4_max2(m, kv4_max2(kv4_abs_max2(r[i].x, r[i].y), kv4_abs_max2(r[i].z, r[i].w)));
+    return kv4_top2(m);
+  }
+  __device__ __forceinline__ void get(int i, float (&x)[8]) const {
+    kv4_unpack(r[i].x, x); kv4_unpack(r[i].y, x + 2); kv4_unpack(r[i].z, x + 4); kv4_unpack(r[i].w, x + 6);
+  }
+};
+template <int N> __device__ __forceinline__ void kv4_store(float* p, const float (&x)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 4; i++)
+    reinterpret_cast<float4*>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+}
+template <int N> __device__ __forceinline__ void kv4_store(__half* p, const float (&x)[N]) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; i++) {
     const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (N == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[N / 2 - 2], w[N / 2 - 1]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
 
-// Codes of this lane's 8 values of a 32-value block (4 neighbouring lanes hold
-// it), the first in the lowest bits, and the block's scale bits.  All 32 lanes call it.
-__device__ __forceinline__ uint32_t kv4_quantize(const float (&x)[8], uint32_t* scale) {
-  float top = 0.f;
-  bool fin = true;
+// A block's scale from its largest magnitude (NaN where one of its values is).
+struct Kv4Scale {
+  uint32_t bits;    // f16; 0x7e00: the block cannot be held
+  float up, down;   // 1 / d a little enlarged and diminished (0 where all codes are 8)
+};
+__device__ __forceinline__ Kv4Scale kv4_scale(float top) {
+  // top / 7 correctly rounded (Markstein: the rounded reciprocal's product, corrected by its exact residual)
+  const float r7 = 1.0f / 7.0f, q = top * r7, d7 = fmaf(fmaf(-7.0f, q, top), r7, q);
+  Kv4Scale s;
+  s.bits = (uint32_t(__half_as_ushort(__float2half_rn(d7))) + 8u) & 0xfff0u;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(__half2float(__ushort_as_half(uint16_t(s.bits)))));
+  const bool bad = s.bits > 0x6300u;   // above 896, infinite or NaN
+  if (bad || s.bits == 0u) inv = 0.f;
+  if (bad) s.bits = 0x7e00u;
+  s.up = inv * (1.f + 0x1p-20f);
+  s.down = inv * (1.f - 0x1p-20f);
+  return s;
+}
+
+// Codes of 8 values, the first in the lowest bits: round(x / d) + 8, the quotient
+// rounded to fp32, halves away from zero.  1 / d is known within 2^-23, so x up
+// lies farther from 0 than the rounded quotient and x down nearer.
+//  fp32 x: where both round to the same number, so does the quotient; `differ` gets
+//    bits where they do not (a quotient within 2^-20 of a half), and the codes are
+//    formed by kv4_codes_exactly.
+//  f16 x (eleven bits; d has seven): x / d is a half or farther than 2^-12 of itself from
+//    it, so x up rounds as the quotient does, halves away from zero.  (Halves are
+//    common here: one value in a few hundred.)
+// Scales below f16's normal range, whose codes may need clamping, `differ` too.
+// 1.5 2^23 + 8 + q in fp32 has q + 8 in its lowest bits; the sum of the codes 16^e is
+// formed modulo 2^32 with the upper bits and rid of them at the end.
+template <bool F16>
+__device__ __forceinline__ uint32_t kv4_codes(const float (&x)[8], const Kv4Scale& s, uint32_t& differ) {
+  constexpr float kMagic = 12582920.f;
+  uint32_t w = 0u;
+#pragma unroll
+  for (int e = 7; e >= 0; e--) {
+    const uint32_t m = __float_as_uint(fmaf(x[e], s.up, kMagic));
+    if (!F16) differ |= m ^ __float_as_uint(fmaf(x[e], s.down, kMagic));
+    w = w * 16u + m;
+  }
+  return w - 0x4b400000u * 0x11111111u;
+}
+__device__ __noinline__ uint32_t kv4_codes_exactly(float x0, float x1, float x2, float x3, float x4, float x5, float x6,
+                                                   float x7, uint32_t bits) {
+  const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7}, d = __half2float(__ushort_as_half(uint16_t(bits)));
+  uint32_t w = 0u;
 #pragma unroll
   for (int e = 0; e < 8; e++) {
-    top = fmaxf(top, fabsf(x[e]));
-    fin = fin && fabsf(x[e]) < INFINITY;   // false for NaN too
+    const int q = int(roundf(__fdiv_rn(x[e], d))) + 8;
+    w |= uint32_t(q < 0 ? 0 : (q > 15 ? 15 : q)) << (4 * e);
   }
-  if (!fin) top = INFINITY;
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-  uint32_t h = (uint32_t(__half_as_ushort(__float2half_rn(__fdiv_rn(top, 7.0f)))) + 8u) & 0xfff0u;
-  const float d = __half2float(__ushort_as_half(uint16_t(h)));
-  uint32_t w = 0x88888888u;
-  if (h > 0x6300u) {   // above 896, infinite or NaN
-    h = 0x7e00u;
-  } else if (h != 0u) {
-    w = 0u;
-#pragma unroll
-    for (int e = 0; e < 8; e++) {
-      const int q = int(roundf(__fdiv_rn(x[e], d))) + 8;
-      w |= uint32_t(q < 0 ? 0 : (q > 15 ? 15 : q)) << (4 * e);
-    }
-  }
-  *scale = h;
   return w;
 }
 
-// One lane per 8 dimensions of a row of K or V.  A row of HD/8 lanes holds whole
-// blocks of 4 lanes; the grid-stride loop keeps warps together for the shuffles.
+constexpr int kKv4RowWarps = 4;   // warps of a CTA: each K or V of a (unit, kv head)
+
+// NG words to (from) consecutive addresses
+template <int NG>
+__device__ __forceinline__ void kv4_get(const void* p, uint32_t (&w)[NG]) {
+  if (NG == 4) {
+    const uint4 x = *static_cast<const uint4*>(p);
+    w[0] = x.x; w[1] = x.y; w[2 % NG] = x.z; w[3 % NG] = x.w;
+  } else {
+    const uint2 x = *static_cast<const uint2*>(p);
+    w[0] = x.x; w[1] = x.y;
+  }
+}
+
 template <int HD, class T>
-__global__ void __launch_bounds__(256) k_kv4_append(Kv4 c, Kv4Rows a, const T* k, const T* v) {
+__global__ void __launch_bounds__(32 * kKv4RowWarps) k_kv4_append(Kv4 c, Kv4Rows a, const T* k, const T* v) {
   using L = Kv4Chunk<HD>;
-  constexpr int LPR = HD / 8;
-  const int64_t total = int64_t(a.n_rows) * c.n_kv * 2 * LPR;
+  constexpr int NG = L::NG, NB = NG / 2;             // blocks of a lane
+  __shared__ __align__(16) uint8_t s_codes[kKv4RowWarps][8 * HD];
   const int lane = threadIdx.x & 31;
-  for (int64_t w0 = int64_t(blockIdx.x) * 256 + (threadIdx.x & ~31); w0 < total; w0 += int64_t(gridDim.x) * 256) {
-    const int64_t u = w0 + lane;
-    const bool live = u < total;
-    const int part = int(u % LPR), g = int(u / (LPR * 2) % c.n_kv);
-    const bool is_v = (u / LPR) & 1;
-    const int r = int(u / (int64_t(LPR) * 2 * c.n_kv));
-    int at = 0;
-    const int page = live ? kv4_place(c, a, r, true, &at) : -1;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (page >= 0) kv4_load8((is_v ? v : k) + int64_t(r) * a.row_stride + int64_t(g) * a.head_stride + part * 8, x);
-    uint32_t scale;
-    const uint32_t w = kv4_quantize(x, &scale);
-    if (page < 0) continue;
-    uint8_t* ch = c.chunk(a.layer, page, g, at);
-    const int p = at % kKv4Chunk, j = part >> 2, tg = part & 3;
-    if (is_v) {
-      *reinterpret_cast<uint16_t*>(ch + L::v_half(p, 2 * tg, j)) = uint16_t(w);
-      *reinterpret_cast<uint16_t*>(ch + L::v_half(p, 2 * tg + 1, j)) = uint16_t(w >> 16);
-      if (tg == 0) *reinterpret_cast<uint16_t*>(ch + L::v_scale(p, j)) = uint16_t(scale);
-    } else {
-      *reinterpret_cast<uint32_t*>(ch + L::k_word(p, tg, j)) = w;
-      if (tg == 0) *reinterpret_cast<uint16_t*>(ch + L::k_scale(p, j)) = uint16_t(scale);
+  const int64_t id = int64_t(blockIdx.x) * kKv4RowWarps + (threadIdx.x >> 5);
+  const int g = int(id / 2 % c.n_kv);
+  const int64_t u = id / 2 / c.n_kv;
+  const bool is_v = id & 1;
+  if (u >= a.units) return;
+  Kv4Span sp;
+  if (!kv4_span(c, a, int(u), &sp)) return;
+  const T* src = (is_v ? v : k) + int64_t(sp.row - sp.first) * a.row_stride + int64_t(g) * a.head_stride;   // of position 0
+  // block 32 i + lane: position / NG, dimensions 32 (block % NG) + 0..31
+  Kv4Block<T> raw[NB];
+  bool live[NB];
+#pragma unroll
+  for (int i = 0; i < NB; i++) {
+    const int b = 32 * i + lane, p = b / NG;
+    live[i] = p >= sp.first && p < sp.last;
+    if (live[i]) raw[i].load(src + int64_t(p) * a.row_stride + 32 * (b % NG));
+  }
+  uint8_t* chunk = kv4_span_chunk(c, a, sp, g, true);
+  if (!chunk) return;
+  uint8_t* codes = s_codes[threadIdx.x >> 5];
+#pragma unroll
+  for (int i = 0; i < NB; i++) {
+    if (!live[i]) continue;
+    const int b = 32 * i + lane, p = b / NG, j = b % NG;
+    const Kv4Scale sc = kv4_scale(raw[i].top());
+    *reinterpret_cast<uint16_t*>(chunk + (is_v ? L::v_scale(p, j) : L::k_scale(p, j))) = uint16_t(sc.bits);
+#pragma unroll
+    for (int y = 0; y < 4; y++) {
+      float x[8];
+      raw[i].get(y, x);
+      uint32_t differ = 0u, w = kv4_codes<sizeof(T) == 2>(x, sc, differ);
+      if (sc.bits - 1u < 0x3ffu) differ = 1u;
+      if (sc.bits == 0x7e00u) w = 0x88888888u;
+      else if (differ) w = kv4_codes_exactly(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], sc.bits);
+      if (is_v) {
+        *reinterpret_cast<uint16_t*>(codes + L::v_half(p, 2 * y, j) - L::kV) = uint16_t(w);
+        *reinterpret_cast<uint16_t*>(codes + L::v_half(p, 2 * y + 1, j) - L::kV) = uint16_t(w >> 16);
+      } else {
+        *reinterpret_cast<uint32_t*>(codes + L::k_word(p, y, j)) = w;
+      }
     }
+  }
+  __syncwarp();
+  // out, 4 NG bytes a lane: of K one position's, of V two positions'
+#pragma unroll
+  for (int i = 0; i < 2; i++) {
+    const int x = 32 * i + lane;
+    const uint8_t* from = codes + x * (4 * NG);
+    uint8_t* to = chunk + (is_v ? L::kV : 0) + x * (4 * NG);
+    const int p = is_v ? 8 * (x >> 5) + 2 * (x & 3) : x >> 2;
+    const bool live0 = p >= sp.first && p < sp.last, live1 = is_v ? p + 1 >= sp.first && p + 1 < sp.last : live0;
+    if (live0 && live1) {
+      if (NG == 4) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(from);
+      else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(from);
+    } else if (live0 || live1) {   // half of each word: the other position is not of this call
+#pragma unroll
+      for (int j = 0; j < NG; j++) {
+        const int o = 4 * j + (live0 ? 0 : 2);
+        *reinterpret_cast<uint16_t*>(to + o) = *reinterpret_cast<const uint16_t*>(from + o);
+      }
+    }
+  }
+}
+
+// N values of the codes in w's lowest bits, exactly.
+template <int N>
+__device__ __forceinline__ void kv4_values(uint32_t w, float d, float (&x)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; e++) x[e] = __fmul_rn(d, float(int((w >> (4 * e)) & 15u) - 8));
+}
+
+template <int HD, class T>
+__global__ void __launch_bounds__(32 * kKv4RowWarps) k_kv4_read(Kv4 c, Kv4Rows a, T* k, T* v) {
+  using L = Kv4Chunk<HD>;
+  constexpr int NG = L::NG;
+  const int lane = threadIdx.x & 31, gi = lane >> 2, tg = lane & 3;
+  const int64_t id = int64_t(blockIdx.x) * kKv4RowWarps + (threadIdx.x >> 5);
+  const int g = int(id / 2 % c.n_kv);
+  const int64_t u = id / 2 / c.n_kv;
+  if (u >= a.units) return;
+  Kv4Span sp;
+  if (!kv4_span(c, a, int(u), &sp)) return;
+  const uint8_t* chunk = kv4_span_chunk(c, a, sp, g, false);
+  if (!chunk) return;
+  const int64_t row0 = int64_t(sp.row - sp.first) * a.row_stride + int64_t(g) * a.head_stride;
+  uint32_t w[2][NG], s[2][NG];
+  if (!(id & 1)) {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      kv4_get<NG>(chunk + L::k_word(8 * i + gi, tg, 0), w[i]);
+      if (NG == 4) {
+        const uint2 y = *reinterpret_cast<const uint2*>(chunk + L::k_scale(8 * i + gi, 0));
+        s[i][0] = y.x; s[i][1] = y.y;
+      } else {
+        s[i][0] = *reinterpret_cast<const uint32_t*>(chunk + L::k_scale(8 * i + gi, 0));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const int p = 8 * i + gi;
+      if (8 * i >= sp.last || 8 * i + 8 <= sp.first) continue;
+      const bool live = p >= sp.first && p < sp.last;
+      T* r = k + row0 + int64_t(p) * a.row_stride;
+#pragma unroll
+      for (int j = 0; j < NG; j++) {
+        const float d = __half2float(__ushort_as_half(uint16_t(s[i][j >> 1] >> (16 * (j & 1)))));
+        if constexpr (sizeof(T) == 2) {
+          float x[8];
+          kv4_values<8>(w[i][j], d, x);
+          if (live) kv4_store<8>(r + 32 * j + 8 * tg, x);
+        } else {   // runs of 4 that lie side by side across the lanes: tg and 4 + tg
+          const uint32_t y = __shfl_sync(0xffffffffu, w[i][j], (lane & ~3) | (tg >> 1));
+          const uint32_t z = __shfl_sync(0xffffffffu, w[i][j], (lane & ~3) | 2 | (tg >> 1));
+          float x[4];
+          kv4_values<4>(y >> (16 * (tg & 1)), d, x);
+          if (live) kv4_store<4>(r + 32 * j + 4 * tg, x);
+          kv4_values<4>(z >> (16 * (tg & 1)), d, x);
+          if (live) kv4_store<4>(r + 32 * j + 16 + 4 * tg, x);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      kv4_get<NG>(chunk + L::v_half(8 * i + 2 * tg, gi, 0), w[i]);
+      kv4_get<NG>(chunk + L::v_scale(8 * i + 2 * tg, 0), s[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; i++)
+#pragma unroll
+      for (int y = 0; y < 2; y++) {
+        const int p = 8 * i + 2 * tg + y;
+        if (p < sp.first || p >= sp.last) continue;
+        T* r = v + row0 + int64_t(p) * a.row_stride;
+#pragma unroll
+        for (int j = 0; j < NG; j++) {
+          const float d = __half2float(__ushort_as_half(uint16_t(s[i][j] >> (16 * y))));
+          float x[4];
+          kv4_values<4>(w[i][j] >> (16 * y), d, x);
+          kv4_store<4>(r + 32 * j + 4 * gi, x);
+        }
+      }
   }
 }
 
@@ -171,34 +430,6 @@ __global__ void __launch_bounds__(1024) k_kv4_listed_twice(Kv4 c, int n, const i
     const int s = seq[i];
     if (s < 0 || s >= c.max_seqs) continue;
     if (atomicOr(&set[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u) kv4_flag(c, NT_KV4_BAD_SEQ);
-  }
-}
-
-template <int HD, class T>
-__global__ void __launch_bounds__(256) k_kv4_read(Kv4 c, Kv4Rows a, T* k, T* v) {
-  using L = Kv4Chunk<HD>;
-  constexpr int LPR = HD / 8;
-  const int64_t total = int64_t(a.n_rows) * c.n_kv * 2 * LPR;
-  for (int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x; u < total; u += int64_t(gridDim.x) * 256) {
-    const int part = int(u % LPR), g = int(u / (LPR * 2) % c.n_kv);
-    const bool is_v = (u / LPR) & 1;
-    const int r = int(u / (int64_t(LPR) * 2 * c.n_kv));
-    int at = 0;
-    const int page = kv4_place(c, a, r, false, &at);
-    if (page < 0) continue;
-    const uint8_t* ch = c.chunk(a.layer, page, g, at);
-    const int p = at % kKv4Chunk, j = part >> 2, tg = part & 3;
-    uint32_t w;
-    if (is_v)
-      w = uint32_t(*reinterpret_cast<const uint16_t*>(ch + L::v_half(p, 2 * tg, j))) |
-          uint32_t(*reinterpret_cast<const uint16_t*>(ch + L::v_half(p, 2 * tg + 1, j))) << 16;
-    else
-      w = *reinterpret_cast<const uint32_t*>(ch + L::k_word(p, tg, j));
-    const float d = __half2float(*reinterpret_cast<const __half*>(ch + (is_v ? L::v_scale(p, j) : L::k_scale(p, j))));
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; e++) x[e] = __fmul_rn(d, float(int((w >> (4 * e)) & 15u) - 8));
-    kv4_store8((is_v ? v : k) + int64_t(r) * a.row_stride + int64_t(g) * a.head_stride + part * 8, x);
   }
 }
 
@@ -540,12 +771,19 @@ static nt_status kv4_plan_apply(const char* who, const Kv4& k, Kv4PlanArgs a, vo
   return NT_OK;
 }
 
+// Units of a call (see kv4_span; 0: n or n_rows is out of range).
+static int32_t kv4_units(int32_t n, int32_t n_rows, const int32_t* begin) {
+  const int64_t u = begin ? int64_t(n_rows) / kKv4Chunk + 2 * int64_t(n) + 1 : n;
+  return n < 0 || n_rows < 0 || u > 0x7fffffff ? 0 : int32_t(begin ? u : (u < n_rows ? u : n_rows));
+}
+
 static nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a, nt_qtype type, const void* pk, const void* pv) {
   auto bad = [&](const char* what) { return fail(NT_E_INVAL, std::string(who) + ": " + what); };
   if (type != NT_F32 && type != NT_F16) return bad("type must be NT_F32 or NT_F16");
   if (a.layer < 0 || a.layer >= k.n_layers) return bad("layer out of range");
   if (a.n < 0 || (!a.seq && a.n > k.max_seqs)) return bad("n out of range");
   if (a.n_rows < 0) return bad("n_rows must not be negative");
+  if (int64_t(a.units) * k.n_kv > (int64_t(1) << 32) || (a.n && a.n_rows && !a.units)) return bad("too many rows");
   const int64_t es = type == NT_F32 ? 4 : 2, most = int64_t(1) << 40;
   if (a.row_stride < 0 || a.head_stride < 0 || a.row_stride > most || a.head_stride > most || a.row_stride * es % 16 ||
       a.head_stride * es % 16)
@@ -694,7 +932,7 @@ nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const i
   const char* who = "nt_kv4_append";
   Kv4 k;
   nt_status st = kv4_check(c, who, true, &k);
-  const Kv4Rows a{layer, n, n_rows, dev_seq, dev_begin, row_stride, head_stride};
+  const Kv4Rows a{layer, n, n_rows, kv4_units(n, n_rows, dev_begin), dev_seq, dev_begin, row_stride, head_stride};
   if (!st) st = kv4_rows_check(who, k, a, type, dev_k, dev_v);
   if (!st && n > k.max_seqs) st = fail(NT_E_INVAL, "nt_kv4_append: n above max_seqs");
   if (!st) st = kv4_array_check(k, who, dev_seq, n, true, nullptr, 0);
@@ -705,16 +943,15 @@ nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const i
   if (kv4_meets_cache(k, dev_k, bytes) || kv4_meets_cache(k, dev_v, bytes))
     return fail(NT_E_INVAL, "nt_kv4_append: k or v overlaps the cache");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t lanes = int64_t(n_rows) * k.n_kv * 2 * (k.hd / 8);
-  const unsigned grid = kv4_grid((lanes + 255) / 256, kKv4Blocks);
+  const unsigned grid = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv4RowWarps - 1) / kKv4RowWarps);
   if (type == NT_F32) {
     const float *pk = static_cast<const float*>(dev_k), *pv = static_cast<const float*>(dev_v);
-    if (k.hd == 64) k_kv4_append<64, float><<<grid, 256, 0, s>>>(k, a, pk, pv);
-    else k_kv4_append<128, float><<<grid, 256, 0, s>>>(k, a, pk, pv);
+    if (k.hd == 64) k_kv4_append<64, float><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
+    else k_kv4_append<128, float><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
   } else {
     const __half *pk = static_cast<const __half*>(dev_k), *pv = static_cast<const __half*>(dev_v);
-    if (k.hd == 64) k_kv4_append<64, __half><<<grid, 256, 0, s>>>(k, a, pk, pv);
-    else k_kv4_append<128, __half><<<grid, 256, 0, s>>>(k, a, pk, pv);
+    if (k.hd == 64) k_kv4_append<64, __half><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
+    else k_kv4_append<128, __half><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
   }
   NT_CUDA(cudaGetLastError());
   if (dev_seq && n > 1) {
@@ -730,7 +967,7 @@ nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int
   const char* who = "nt_kv4_read";
   Kv4 k;
   nt_status st = kv4_check(c, who, true, &k);
-  const Kv4Rows a{layer, n, n_rows, dev_seq, dev_begin, row_stride, head_stride};
+  const Kv4Rows a{layer, n, n_rows, kv4_units(n, n_rows, dev_begin), dev_seq, dev_begin, row_stride, head_stride};
   if (!st) st = kv4_rows_check(who, k, a, type, dev_k, dev_v);
   if (!st) st = kv4_array_check(k, who, dev_seq, n, true, nullptr, 0);
   if (!st) st = kv4_array_check(k, who, dev_begin, int64_t(n) + 1, true, nullptr, 0);
@@ -745,16 +982,15 @@ nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int
       kv4_overlap(dev_begin, int64_t(n) * 4 + 4, dev_k, bytes) || kv4_overlap(dev_begin, int64_t(n) * 4 + 4, dev_v, bytes))
     return fail(NT_E_INVAL, "nt_kv4_read: an output overlaps another buffer");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t lanes = int64_t(n_rows) * k.n_kv * 2 * (k.hd / 8);
-  const unsigned grid = kv4_grid((lanes + 255) / 256, kKv4Blocks);
+  const unsigned grid = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv4RowWarps - 1) / kKv4RowWarps);
   if (type == NT_F32) {
     float *pk = static_cast<float*>(dev_k), *pv = static_cast<float*>(dev_v);
-    if (k.hd == 64) k_kv4_read<64, float><<<grid, 256, 0, s>>>(k, a, pk, pv);
-    else k_kv4_read<128, float><<<grid, 256, 0, s>>>(k, a, pk, pv);
+    if (k.hd == 64) k_kv4_read<64, float><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
+    else k_kv4_read<128, float><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
   } else {
     __half *pk = static_cast<__half*>(dev_k), *pv = static_cast<__half*>(dev_v);
-    if (k.hd == 64) k_kv4_read<64, __half><<<grid, 256, 0, s>>>(k, a, pk, pv);
-    else k_kv4_read<128, __half><<<grid, 256, 0, s>>>(k, a, pk, pv);
+    if (k.hd == 64) k_kv4_read<64, __half><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
+    else k_kv4_read<128, __half><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
   }
   NT_CUDA(cudaGetLastError());
   return NT_OK;
