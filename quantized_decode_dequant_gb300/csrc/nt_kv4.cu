@@ -49,6 +49,27 @@ bool kv4_meets_cache(const Kv4& k, const void* p, int64_t bytes) {
 // 2 x 20011 f16 rows of 8 heads of 128.)
 // read: a lane's words give values that lie side by side in a row across the lanes.
 
+// Every kernel here is launched so that it may start while the one before it in the
+// stream ends, and lets the next one start: it touches memory only after that one has
+// ended and its writes are visible.
+__device__ __forceinline__ void kv4_dependent() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+template <class K, class... A>
+static cudaError_t kv4_launch(K kern, unsigned grid, unsigned block, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 struct Kv4Rows {
   int32_t layer, n, n_rows, units;
   const int32_t* seq;
@@ -281,6 +302,7 @@ __global__ void __launch_bounds__(32 * kKv4RowWarps) k_kv4_append(Kv4 c, Kv4Rows
   const int64_t u = id / 2 / c.n_kv;
   const bool is_v = id & 1;
   if (u >= a.units) return;
+  kv4_dependent();
   Kv4Span sp;
   if (!kv4_span(c, a, int(u), &sp)) return;
   const T* src = (is_v ? v : k) + int64_t(sp.row - sp.first) * a.row_stride + int64_t(g) * a.head_stride;   // of position 0
@@ -356,6 +378,7 @@ __global__ void __launch_bounds__(32 * kKv4RowWarps) k_kv4_read(Kv4 c, Kv4Rows a
   const int g = int(id / 2 % c.n_kv);
   const int64_t u = id / 2 / c.n_kv;
   if (u >= a.units) return;
+  kv4_dependent();
   Kv4Span sp;
   if (!kv4_span(c, a, int(u), &sp)) return;
   const uint8_t* chunk = kv4_span_chunk(c, a, sp, g, false);
@@ -423,6 +446,7 @@ __global__ void __launch_bounds__(32 * kKv4RowWarps) k_kv4_read(Kv4 c, Kv4Rows a
 
 // Flags sequences listed twice.
 __global__ void __launch_bounds__(1024) k_kv4_listed_twice(Kv4 c, int n, const int32_t* seq) {
+  kv4_dependent();
   __shared__ uint32_t set[kKv4MaxSeqs / 32];
   for (int i = threadIdx.x; i < kKv4MaxSeqs / 32; i += blockDim.x) set[i] = 0u;
   __syncthreads();
@@ -435,6 +459,9 @@ __global__ void __launch_bounds__(1024) k_kv4_listed_twice(Kv4 c, int n, const i
 
 // ------------------------------------------------------------ page operators --
 
+constexpr int64_t kKv4Blocks = 152 * 8;   // CTAs of 256 threads that the GPU holds at once
+
+
 // Exclusive prefix sum of one value per thread of a 1024-thread CTA; *total: the sum.
 __device__ __forceinline__ int64_t kv4_scan(int64_t x, int64_t* total) {
   __shared__ int64_t part[32];
@@ -445,16 +472,18 @@ __device__ __forceinline__ int64_t kv4_scan(int64_t x, int64_t* total) {
     const int64_t y = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += y;
   }
-  __syncthreads();   // the previous call's sums have been read
+  __syncthreads();   // (the sums of the call before have been read)
   if (lane == 31) part[warp] = s;
   __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int w = 0; w < 32; w++) {
-    if (w < warp) before += part[w];
-    all += part[w];
+  int64_t w = part[lane];
+  const int64_t mine = w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  *total = all;
-  return before + s - x;
+  *total = __shfl_sync(0xffffffffu, w, 31);
+  return __shfl_sync(0xffffffffu, w - mine, warp) + s - x;
 }
 
 __device__ __forceinline__ int kv4_pages(int len, int page_len) { return int((int64_t(len) + page_len - 1) / page_len); }
@@ -481,6 +510,8 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
   const int t = threadIdx.x;
   for (int i = t; i < kKv4MaxSeqs / 32; i += 1024) set[i] = 0u;
   if (t == 0) s_bad = 0u;
+  kv4_dependent();
+  const int refs0 = t < c.n_pages ? c.refs[t] : 1;   // of the first pages, while the entries are checked
   __syncthreads();
   const int32_t* listed = FORK ? a.b : a.a;
   for (int i = t; i < a.n; i += 1024) {
@@ -538,7 +569,7 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
   int64_t found = 0;
   for (int64_t p0 = 0; p0 < c.n_pages && found < run; p0 += 1024) {
     const int64_t p = p0 + t;
-    const bool is_free = p < c.n_pages && c.refs[p] == 0;
+    const bool is_free = p < c.n_pages && (p0 ? c.refs[p] : refs0) == 0;
     int64_t all;
     const int64_t before = kv4_scan(is_free ? 1 : 0, &all);
     if (is_free && found + before < run) a.free[found + before] = int32_t(p);
@@ -577,24 +608,43 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
     for (int i = t; i < a.n; i += 1024) c.len[a.a ? a.a[i] : i] += a.b[i];
 }
 
-// Copies pages in every layer: item = (pair, layer), 16 bytes a thread.
-__device__ __forceinline__ void kv4_copy_page(const Kv4& c, int src, int dst, int layer) {
-  const int64_t pb = c.page_bytes(), n16 = pb / 16;
+// Part `part` of `parts` of page src of a layer to page dst, by the whole CTA: 64
+// bytes a thread in flight.
+__device__ __forceinline__ void kv4_copy_part(const Kv4& c, int src, int dst, int layer, int part, int parts) {
+  const int64_t pb = c.page_bytes();
+  const int n16 = int(pb / 16), per = (n16 + parts - 1) / parts, hi = per * (part + 1) < n16 ? per * (part + 1) : n16;
   const uint4* from = reinterpret_cast<const uint4*>(c.pool + (int64_t(layer) * c.n_pages + src) * pb);
   uint4* to = reinterpret_cast<uint4*>(c.pool + (int64_t(layer) * c.n_pages + dst) * pb);
-  for (int64_t i = threadIdx.x; i < n16; i += blockDim.x) to[i] = from[i];
+  const int step = blockDim.x;
+  int i = per * part + threadIdx.x;
+  for (; i + 3 * step < hi; i += 4 * step) {
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; u++) v[u] = __ldcs(from + i + u * step);
+#pragma unroll
+    for (int u = 0; u < 4; u++) __stcs(to + i + u * step, v[u]);
+  }
+  for (; i < hi; i += step) __stcs(to + i, __ldcs(from + i));
+}
+
+// Parts that a page is cut into when n pages of every layer are copied: enough items
+// for the grid, 4 KB at least.
+static int kv4_parts(const Kv4& k, int64_t n) {
+  const int64_t items = n * k.n_layers, most = (k.page_bytes() + 4095) / 4096, want = (2 * kKv4Blocks + items - 1) / items;
+  return int(want < 1 ? 1 : (want > most ? most : want));
 }
 
 // The pairs of a plan; FORK: also the destinations' tables, counts and lengths.
 template <bool FORK>
-__global__ void __launch_bounds__(256) k_kv4_apply(Kv4 c, Kv4PlanArgs a) {
+__global__ void __launch_bounds__(256) k_kv4_apply(Kv4 c, Kv4PlanArgs a, int parts) {
+  kv4_dependent();
   if (!a.go[0]) return;
-  const int64_t items = int64_t(a.n) * c.n_layers;
+  const int64_t items = int64_t(a.n) * c.n_layers * parts;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = int(it % a.n), layer = int(it / a.n);
+    const int i = int(it % a.n), layer = int(it / a.n / parts), part = int(it / a.n % parts);
     const int2 pair = a.pair[i];
-    if (pair.x >= 0) kv4_copy_page(c, pair.x, pair.y, layer);
-    if (FORK && layer == 0) {
+    if (pair.x >= 0) kv4_copy_part(c, pair.x, pair.y, layer, part, parts);
+    if (FORK && layer == 0 && part == 0) {
       const int s = a.a[i], d = a.b[i], keep = a.keep ? a.keep[i] : c.len[s], full = keep / c.page_len;
       const int32_t* from = c.table + int64_t(s) * c.max_pages;
       int32_t* to = c.table + int64_t(d) * c.max_pages;
@@ -614,6 +664,7 @@ __global__ void __launch_bounds__(256) k_kv4_apply(Kv4 c, Kv4PlanArgs a) {
 
 __global__ void __launch_bounds__(256) k_kv4_free(Kv4 c, int n, const int32_t* seq, const int32_t* keep) {
   __shared__ int s_again;
+  kv4_dependent();
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
     const int s = seq ? seq[i] : i;
     __syncthreads();
@@ -647,23 +698,27 @@ __global__ void __launch_bounds__(256) k_kv4_free(Kv4 c, int n, const int32_t* s
   }
 }
 
-__global__ void __launch_bounds__(256) k_kv4_copy_pages(Kv4 c, int n, const int32_t* src, const int32_t* dst) {
-  __shared__ int s_bad;
-  const int64_t items = int64_t(n) * c.n_layers;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = int(it / c.n_layers), layer = int(it % c.n_layers);
+__global__ void __launch_bounds__(256) k_kv4_copy_pages(Kv4 c, int n, const int32_t* src, const int32_t* dst, int parts) {
+  kv4_dependent();
+  const int64_t per = int64_t(c.n_layers) * parts, items = n * per;
+  int checked = -1;   // the pair that `bad` is known of
+  bool bad = false;
+  // a CTA's items lie side by side: it looks through the list once per pair
+  const int64_t each = (items + gridDim.x - 1) / gridDim.x, last = (blockIdx.x + 1) * each < items ? (blockIdx.x + 1) * each : items;
+  for (int64_t it = blockIdx.x * each; it < last; it++) {
+    const int i = int(it / per), layer = int(it % per / parts), part = int(it % parts);
     const int s = src[i], d = dst[i];
-    __syncthreads();
-    if (threadIdx.x == 0) s_bad = s < 0 || s >= c.n_pages || d < 0 || d >= c.n_pages;
-    __syncthreads();
-    for (int e = threadIdx.x; e < n; e += blockDim.x)
-      if (e != i && (dst[e] == s || (e < i && dst[e] == d))) s_bad = 1;
-    __syncthreads();
-    if (s_bad) {
-      if (threadIdx.x == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
-      continue;
+    if (i != checked) {
+      bool mine = s < 0 || s >= c.n_pages || d < 0 || d >= c.n_pages;
+      for (int e = threadIdx.x; e < n; e += blockDim.x) {
+        const int x = dst[e];
+        mine = mine || (e != i && (x == s || (e < i && x == d)));
+      }
+      bad = __syncthreads_or(mine);
+      checked = i;
+      if (bad && threadIdx.x == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
     }
-    if (s != d) kv4_copy_page(c, s, d, layer);
+    if (!bad && s != d) kv4_copy_part(c, s, d, layer, part, parts);
   }
 }
 
@@ -672,6 +727,7 @@ __global__ void __launch_bounds__(256) k_kv4_copy_pages(Kv4 c, int n, const int3
 // in `pair`, the k-th page in use from L on to the k-th free page below.
 __global__ void __launch_bounds__(1024) k_kv4_compact_plan(Kv4 c, int32_t* go, int2* pair, int32_t* to, int32_t* live) {
   const int t = threadIdx.x;
+  kv4_dependent();
   int64_t used = 0;
   for (int64_t p0 = 0; p0 < c.n_pages; p0 += 1024) {
     int64_t all;
@@ -700,7 +756,8 @@ __global__ void __launch_bounds__(1024) k_kv4_compact_plan(Kv4 c, int32_t* go, i
 }
 
 __global__ void __launch_bounds__(256) k_kv4_compact_apply(Kv4 c, const int32_t* go, const int2* pair, const int32_t* to,
-                                                           int32_t* table_out, int32_t* refs_out) {
+                                                           int32_t* table_out, int32_t* refs_out, int parts) {
+  kv4_dependent();
   const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
   for (int64_t p = first; p < c.n_pages; p += step) {
     const int d = to[p], r = c.refs[p];
@@ -717,15 +774,14 @@ __global__ void __launch_bounds__(256) k_kv4_compact_apply(Kv4 c, const int32_t*
     }
     table_out[e] = p == -2 ? -1 : p;
   }
-  const int64_t items = int64_t(go[1]) * c.n_layers;
+  const int64_t items = int64_t(go[1]) * c.n_layers * parts;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int2 m = pair[it / c.n_layers];
-    kv4_copy_page(c, m.x, m.y, int(it % c.n_layers));
+    const int2 m = pair[it / parts / c.n_layers];
+    kv4_copy_part(c, m.x, m.y, int(it / parts % c.n_layers), int(it % parts), parts);
   }
 }
 
 static unsigned kv4_grid(int64_t blocks, int64_t most) { return unsigned(blocks < 1 ? 1 : (blocks > most ? most : blocks)); }
-constexpr int64_t kKv4Blocks = 152 * 8;
 
 static nt_status kv4_ws_check(const Kv4& k, const char* who, int64_t n, void* ws, size_t bytes, Kv4Ws* w) {
   *w = kv4_ws(k, n);
@@ -764,10 +820,9 @@ static nt_status kv4_plan_apply(const char* who, const Kv4& k, Kv4PlanArgs a, vo
   a.pair = reinterpret_cast<int2*>(base + w.pair);
   a.free = reinterpret_cast<int32_t*>(base + w.free);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  k_kv4_plan<FORK><<<1, 1024, 0, s>>>(k, a);
-  NT_CUDA(cudaGetLastError());
-  k_kv4_apply<FORK><<<kv4_grid(int64_t(a.n) * k.n_layers, kKv4Blocks), 256, 0, s>>>(k, a);
-  NT_CUDA(cudaGetLastError());
+  NT_CUDA(kv4_launch(k_kv4_plan<FORK>, 1u, 1024u, s, k, a));
+  const int parts = kv4_parts(k, a.n);
+  NT_CUDA(kv4_launch(k_kv4_apply<FORK>, kv4_grid(int64_t(a.n) * k.n_layers * parts, kKv4Blocks), 256u, s, k, a, parts));
   return NT_OK;
 }
 
@@ -877,8 +932,7 @@ nt_status nt_kv4_free(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, 
   if (!st) st = kv4_array_check(k, "nt_kv4_free", dev_seq, n, true, nullptr, 0);
   if (!st) st = kv4_array_check(k, "nt_kv4_free", dev_keep, n, true, nullptr, 0);
   if (st || n == 0) return st;
-  k_kv4_free<<<kv4_grid(n, kKv4Blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(k, n, dev_seq, dev_keep);
-  NT_CUDA(cudaGetLastError());
+  NT_CUDA(kv4_launch(k_kv4_free, kv4_grid(n, kKv4Blocks), 256u, static_cast<cudaStream_t>(stream), k, n, dev_seq, dev_keep));
   return NT_OK;
 }
 
@@ -890,9 +944,9 @@ nt_status nt_kv4_copy_pages(const nt_kv4_cache* c, int32_t n, const int32_t* dev
   if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_src, n, false, nullptr, 0);
   if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_dst, n, false, nullptr, 0);
   if (st || n == 0) return st;
-  k_kv4_copy_pages<<<kv4_grid(int64_t(n) * k.n_layers, kKv4Blocks), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-      k, n, dev_src, dev_dst);
-  NT_CUDA(cudaGetLastError());
+  const int parts = kv4_parts(k, n);
+  NT_CUDA(kv4_launch(k_kv4_copy_pages, kv4_grid(int64_t(n) * k.n_layers * parts, kKv4Blocks), 256u,
+                     static_cast<cudaStream_t>(stream), k, n, dev_src, dev_dst, parts));
   return NT_OK;
 }
 
@@ -919,10 +973,11 @@ nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t*
   int2* pair = reinterpret_cast<int2*>(base + w.pair);
   int32_t* to = reinterpret_cast<int32_t*>(base + w.free);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  k_kv4_compact_plan<<<1, 1024, 0, s>>>(k, go, pair, to, dev_live);
-  NT_CUDA(cudaGetLastError());
-  k_kv4_compact_apply<<<unsigned(kKv4Blocks), 256, 0, s>>>(k, go, pair, to, dev_table_out, dev_refs_out);
-  NT_CUDA(cudaGetLastError());
+  NT_CUDA(kv4_launch(k_kv4_compact_plan, 1u, 1024u, s, k, go, pair, to, dev_live));
+  // (how many pages move is known on the device only; at most half of them do)
+  NT_CUDA(kv4_launch(k_kv4_compact_apply, unsigned(kKv4Blocks), 256u, s, k, static_cast<const int32_t*>(go),
+                     static_cast<const int2*>(pair), static_cast<const int32_t*>(to), dev_table_out, dev_refs_out,
+                     kv4_parts(k, 8)));
   return NT_OK;
 }
 
@@ -946,17 +1001,13 @@ nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const i
   const unsigned grid = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv4RowWarps - 1) / kKv4RowWarps);
   if (type == NT_F32) {
     const float *pk = static_cast<const float*>(dev_k), *pv = static_cast<const float*>(dev_v);
-    if (k.hd == 64) k_kv4_append<64, float><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
-    else k_kv4_append<128, float><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
+    NT_CUDA(k.hd == 64 ? kv4_launch(k_kv4_append<64, float>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv) : kv4_launch(k_kv4_append<128, float>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv));
   } else {
     const __half *pk = static_cast<const __half*>(dev_k), *pv = static_cast<const __half*>(dev_v);
-    if (k.hd == 64) k_kv4_append<64, __half><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
-    else k_kv4_append<128, __half><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
+    NT_CUDA(k.hd == 64 ? kv4_launch(k_kv4_append<64, __half>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv) : kv4_launch(k_kv4_append<128, __half>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv));
   }
-  NT_CUDA(cudaGetLastError());
   if (dev_seq && n > 1) {
-    k_kv4_listed_twice<<<1, 1024, 0, s>>>(k, n, dev_seq);
-    NT_CUDA(cudaGetLastError());
+    NT_CUDA(kv4_launch(k_kv4_listed_twice, 1u, 1024u, s, k, n, dev_seq));
   }
   return NT_OK;
 }
@@ -985,14 +1036,11 @@ nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int
   const unsigned grid = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv4RowWarps - 1) / kKv4RowWarps);
   if (type == NT_F32) {
     float *pk = static_cast<float*>(dev_k), *pv = static_cast<float*>(dev_v);
-    if (k.hd == 64) k_kv4_read<64, float><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
-    else k_kv4_read<128, float><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
+    NT_CUDA(k.hd == 64 ? kv4_launch(k_kv4_read<64, float>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv) : kv4_launch(k_kv4_read<128, float>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv));
   } else {
     __half *pk = static_cast<__half*>(dev_k), *pv = static_cast<__half*>(dev_v);
-    if (k.hd == 64) k_kv4_read<64, __half><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
-    else k_kv4_read<128, __half><<<grid, 32 * kKv4RowWarps, 0, s>>>(k, a, pk, pv);
+    NT_CUDA(k.hd == 64 ? kv4_launch(k_kv4_read<64, __half>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv) : kv4_launch(k_kv4_read<128, __half>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv));
   }
-  NT_CUDA(cudaGetLastError());
   return NT_OK;
 }
 
