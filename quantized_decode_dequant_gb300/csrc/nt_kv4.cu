@@ -57,17 +57,22 @@ __device__ __forceinline__ void kv4_dependent() {
   asm volatile("griddepcontrol.launch_dependents;");
 }
 template <class K, class... A>
-static cudaError_t kv4_launch(K kern, unsigned grid, unsigned block, cudaStream_t s, A... args) {
+static cudaError_t kv4_launch_smem(K kern, unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <class K, class... A>
+static cudaError_t kv4_launch(K kern, unsigned grid, unsigned block, cudaStream_t s, A... args) {
+  return kv4_launch_smem(kern, grid, block, 0, s, args...);
 }
 
 struct Kv4Rows {
@@ -459,9 +464,6 @@ __global__ void __launch_bounds__(1024) k_kv4_listed_twice(Kv4 c, int n, const i
 
 // ------------------------------------------------------------ page operators --
 
-constexpr int64_t kKv4Blocks = 152 * 8;   // CTAs of 256 threads that the GPU holds at once
-
-
 // Exclusive prefix sum of one value per thread of a 1024-thread CTA; *total: the sum.
 __device__ __forceinline__ int64_t kv4_scan(int64_t x, int64_t* total) {
   __shared__ int64_t part[32];
@@ -493,23 +495,25 @@ struct Kv4PlanArgs {
   const int32_t* a;   // extend: sequences (nullable); fork: sources
   const int32_t* b;   // extend: counts; fork: destinations
   const int32_t* keep;
-  int32_t* go;
+  int32_t* go;        // [0]: the call goes ahead, [1]: pages to copy
   int64_t* off;
+  int32_t* from;      // page that entry i's first new page is a copy of (-1: none)
   int2* pair;
   int32_t* free;
 };
 
 // The plan of an extend (FORK = false) or a fork, by one CTA: checks every entry,
 // counts the pages it takes, finds that many free pages, the lowest first, and
-// (extend) writes the table, counts and lengths.  Nothing is changed unless every
+// writes their table entries and counts, and (extend) the lengths.  Nothing is changed unless every
 // entry is valid and the free pages suffice.  The pages to copy go to `pair`.
 template <bool FORK>
 __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
   __shared__ uint32_t set[kKv4MaxSeqs / 32];                  // sequences listed (fork: destinations)
   __shared__ uint32_t s_bad;
+  __shared__ int s_pairs;
   const int t = threadIdx.x;
   for (int i = t; i < kKv4MaxSeqs / 32; i += 1024) set[i] = 0u;
-  if (t == 0) s_bad = 0u;
+  if (t == 0) { s_bad = 0u; s_pairs = 0; }
   kv4_dependent();
   const int refs0 = t < c.n_pages ? c.refs[t] : 1;   // of the first pages, while the entries are checked
   __syncthreads();
@@ -524,7 +528,7 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
   for (int i0 = 0; i0 < a.n; i0 += 1024) {
     const int i = i0 + t;
     int64_t need = 0;
-    int2 pair = make_int2(-1, -1);
+    int from = -1;
     uint32_t bad = 0;
     if (i < a.n) {
       const int s = a.a ? a.a[i] : i;   // the sequence read from
@@ -539,8 +543,8 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
           if (d >= 0 && d < c.max_seqs && c.len[d] != 0) bad |= NT_KV4_BAD_SEQ;
           if (keep < 0 || keep > n) bad |= NT_KV4_BAD_LEN;
           if (!bad && keep % c.page_len) {
-            pair.x = c.table[int64_t(s) * c.max_pages + keep / c.page_len];
-            if (pair.x < 0 || pair.x >= c.n_pages) bad |= NT_KV4_BAD_PAGE;
+            from = c.table[int64_t(s) * c.max_pages + keep / c.page_len];
+            if (from < 0 || from >= c.n_pages) bad |= NT_KV4_BAD_PAGE;
             need = 1;
           }
         } else {
@@ -551,13 +555,13 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
             if (n % c.page_len) {
               const int p = c.table[int64_t(s) * c.max_pages + n / c.page_len];
               if (p < 0 || p >= c.n_pages || c.refs[p] < 1) bad |= NT_KV4_BAD_PAGE;
-              else if (c.refs[p] > 1) { pair.x = p; need++; }
+              else if (c.refs[p] > 1) { from = p; need++; }
             }
           }
         }
       }
       if (bad) atomicOr(&s_bad, bad);
-      a.pair[i] = pair;
+      a.from[i] = from;
     }
     int64_t all;
     const int64_t before = kv4_scan(need, &all);
@@ -581,7 +585,7 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
   const uint32_t bad = s_bad;
   if (t == 0) {
     a.go[0] = bad == 0u;
-    a.go[1] = bad == 0u ? a.n : 0;
+    if (bad) a.go[1] = 0;
     if (bad) kv4_flag(c, bad);
   }
   if (bad) return;
@@ -593,9 +597,12 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
     }
     const int page = a.free[f], kth = int(f - a.off[lo]);
     c.refs[page] = 1;
-    const bool copied = a.pair[lo].x >= 0;
-    if (copied && kth == 0) a.pair[lo].y = page;
-    if (!FORK) {
+    const bool copied = a.from[lo] >= 0;
+    if (copied && kth == 0) a.pair[atomicAdd(&s_pairs, 1)] = make_int2(a.from[lo], page);   // (in any order)
+    if (FORK) {
+      const int keep = a.keep ? a.keep[lo] : c.len[a.a[lo]];
+      c.table[int64_t(a.b[lo]) * c.max_pages + keep / c.page_len] = page;
+    } else {
       const int s = a.a ? a.a[lo] : lo, n = c.len[s];
       const int slot = copied ? n / c.page_len + kth : kv4_pages(n, c.page_len) + kth;
       int32_t* e = &c.table[int64_t(s) * c.max_pages + slot];
@@ -604,60 +611,113 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
     }
   }
   __syncthreads();
+  if (t == 0) a.go[1] = s_pairs;
   if (!FORK)
     for (int i = t; i < a.n; i += 1024) c.len[a.a ? a.a[i] : i] += a.b[i];
 }
 
-// Part `part` of `parts` of page src of a layer to page dst, by the whole CTA: 64
-// bytes a thread in flight.
-__device__ __forceinline__ void kv4_copy_part(const Kv4& c, int src, int dst, int layer, int part, int parts) {
-  const int64_t pb = c.page_bytes();
-  const int n16 = int(pb / 16), per = (n16 + parts - 1) / parts, hi = per * (part + 1) < n16 ? per * (part + 1) : n16;
-  const uint4* from = reinterpret_cast<const uint4*>(c.pool + (int64_t(layer) * c.n_pages + src) * pb);
-  uint4* to = reinterpret_cast<uint4*>(c.pool + (int64_t(layer) * c.n_pages + dst) * pb);
-  const int step = blockDim.x;
-  int i = per * part + threadIdx.x;
-  for (; i + 3 * step < hi; i += 4 * step) {
-    uint4 v[4];
-#pragma unroll
-    for (int u = 0; u < 4; u++) v[u] = __ldcs(from + i + u * step);
-#pragma unroll
-    for (int u = 0; u < 4; u++) __stcs(to + i + u * step, v[u]);
+// ---- copies.  One thread of a CTA moves pieces of pages through a ring in shared
+// memory by bulk copies, kKv4Ahead of them on the way in while others are on the way out;
+// the CTA's other warps do what else there is.  (Copies by all threads, 64 bytes
+// each in flight, 8 CTAs of 256 per SM: 53.6 us for 24 pages of 73.7 KB in 80 layers.)
+constexpr int kKv4Piece = 16384, kKv4Ring = 12, kKv4Ahead = 8;
+constexpr int kKv4CopyThreads = 256;
+struct Kv4CopyShared {
+  static constexpr int kBars = kKv4Piece * kKv4Ring, kTo = kBars + 8 * kKv4Ring, kBytes = kTo + 8 * kKv4Ring,
+                       kSize = kBytes + 4 * kKv4Ring + 16;
+};
+extern __shared__ __align__(128) uint8_t kv4_sm[];
+
+// Pieces q0, q0 + dq, .. below q1 by the calling thread.  piece(q, &from, &to, &bytes):
+// false where there is nothing to copy.  No piece's destination is another's source.
+template <class P>
+__device__ __forceinline__ void kv4_stream(const Kv4& c, int64_t q0, int64_t q1, int64_t dq, P piece) {
+  using Sh = Kv4CopyShared;
+  const uint32_t ring = kv4_smem(kv4_sm), bars = ring + Sh::kBars;
+  uint8_t** to = reinterpret_cast<uint8_t**>(kv4_sm + Sh::kTo);
+  uint32_t* bytes = reinterpret_cast<uint32_t*>(kv4_sm + Sh::kBytes);
+  for (int i = 0; i < kKv4Ring; i++) kv4_bar_init(bars + 8 * i);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  int64_t in = 0, out = 0;   // pieces whose copy in, out was begun
+  for (int64_t q = q0;;) {
+    for (; q < q1 && in - out < kKv4Ahead; q += dq) {
+      const uint8_t* f;
+      uint8_t* t;
+      uint32_t n;
+      if (!piece(q, &f, &t, &n)) continue;
+      const int st = int(in % kKv4Ring);
+      // the copy out of what stood there before has been read: all but the last kKv4Ring - kKv4Ahead have
+      asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kKv4Ring - kKv4Ahead) : "memory");
+      to[st] = t;
+      bytes[st] = n;
+      kv4_bar_expect(bars + 8 * st, n);
+      kv4_copy(ring + st * kKv4Piece, f, n, bars + 8 * st);
+      in++;
+    }
+    if (out == in) break;
+    const int st = int(out % kKv4Ring);
+    if (!kv4_bar_wait(bars + 8 * st, uint32_t(out / kKv4Ring) & 1u)) {
+      kv4_flag(c, NT_KV4_TIMEOUT);
+      for (int64_t x = out + 1; x < in; x++) kv4_bar_wait(bars + 8 * int(x % kKv4Ring), uint32_t(x / kKv4Ring) & 1u);
+      break;
+    }
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(to[st]),
+                 "r"(ring + st * kKv4Piece), "r"(bytes[st])
+                 : "memory");
+    out++;
   }
-  for (; i < hi; i += step) __stcs(to + i, __ldcs(from + i));
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// Parts that a page is cut into when n pages of every layer are copied: enough items
-// for the grid, 4 KB at least.
-static int kv4_parts(const Kv4& k, int64_t n) {
-  const int64_t items = n * k.n_layers, most = (k.page_bytes() + 4095) / 4096, want = (2 * kKv4Blocks + items - 1) / items;
-  return int(want < 1 ? 1 : (want > most ? most : want));
+// Bytes of a piece and pieces of a page when n pages of every layer are copied by
+// 152 CTAs: 16 KB, or less where that makes too few pieces (1 KB at least).
+struct Kv4Pieces {
+  int32_t bytes, count;
+};
+static Kv4Pieces kv4_pieces(const Kv4& k, int64_t n) {
+  const int64_t pb = k.page_bytes(), all = pb * k.n_layers * n;
+  int64_t b = kKv4Piece;
+  while (b > 1024 && all / b < 4 * 152) b /= 2;
+  Kv4Pieces p;
+  p.count = int32_t((pb + b - 1) / b);
+  p.bytes = int32_t(((pb + p.count - 1) / p.count + 15) / 16 * 16);
+  return p;
+}
+// Piece `part` of page src of a layer, to page dst.
+__device__ __forceinline__ bool kv4_piece(const Kv4& c, Kv4Pieces ps, int src, int dst, int layer, int part, const uint8_t** from,
+                                          uint8_t** to, uint32_t* bytes) {
+  const int64_t pb = c.page_bytes(), at = int64_t(part) * ps.bytes;
+  *from = c.pool + (int64_t(layer) * c.n_pages + src) * pb + at;
+  *to = c.pool + (int64_t(layer) * c.n_pages + dst) * pb + at;
+  *bytes = uint32_t(pb - at < ps.bytes ? pb - at : ps.bytes);
+  return at < pb;
 }
 
 // The pairs of a plan; FORK: also the destinations' tables, counts and lengths.
 template <bool FORK>
-__global__ void __launch_bounds__(256) k_kv4_apply(Kv4 c, Kv4PlanArgs a, int parts) {
+__global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_apply(Kv4 c, Kv4PlanArgs a, Kv4Pieces ps) {
   kv4_dependent();
   if (!a.go[0]) return;
-  const int64_t items = int64_t(a.n) * c.n_layers * parts;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = int(it % a.n), layer = int(it / a.n / parts), part = int(it / a.n % parts);
-    const int2 pair = a.pair[i];
-    if (pair.x >= 0) kv4_copy_part(c, pair.x, pair.y, layer, part, parts);
-    if (FORK && layer == 0 && part == 0) {
+  if (threadIdx.x == 0) {
+    const int64_t per = int64_t(c.n_layers) * ps.count;
+    kv4_stream(c, blockIdx.x, a.go[1] * per, gridDim.x, [&](int64_t q, const uint8_t** f, uint8_t** t, uint32_t* b) {
+      const int2 m = a.pair[q / per];
+      const int r = int(q % per);
+      return kv4_piece(c, ps, m.x, m.y, r / ps.count, r % ps.count, f, t, b);
+    });
+  }
+  if (FORK && threadIdx.x >= 32) {
+    for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
       const int s = a.a[i], d = a.b[i], keep = a.keep ? a.keep[i] : c.len[s], full = keep / c.page_len;
       const int32_t* from = c.table + int64_t(s) * c.max_pages;
       int32_t* to = c.table + int64_t(d) * c.max_pages;
-      for (int j = threadIdx.x; j < full; j += blockDim.x) {
+      for (int j = threadIdx.x - 32; j < full; j += kKv4CopyThreads - 32) {
         const int p = from[j];
         to[j] = p;
         if (p >= 0 && p < c.n_pages) atomicAdd(&c.refs[p], 1);
         else kv4_flag(c, NT_KV4_BAD_PAGE);
       }
-      if (threadIdx.x == 0) {
-        if (pair.x >= 0) to[full] = pair.y;
-        c.len[d] = keep;
-      }
+      if (threadIdx.x == 32) c.len[d] = keep;
     }
   }
 }
@@ -698,28 +758,37 @@ __global__ void __launch_bounds__(256) k_kv4_free(Kv4 c, int n, const int32_t* s
   }
 }
 
-__global__ void __launch_bounds__(256) k_kv4_copy_pages(Kv4 c, int n, const int32_t* src, const int32_t* dst, int parts) {
+// CTA b copies pieces [b each, (b + 1) each), which belong to few pairs: those are checked first.
+constexpr int kKv4CopyPairs = 8192;   // most pairs of a CTA
+__global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_copy_pages(Kv4 c, int n, const int32_t* src, const int32_t* dst,
+                                                                    Kv4Pieces ps) {
+  __shared__ uint32_t s_bad[kKv4CopyPairs / 32];
   kv4_dependent();
-  const int64_t per = int64_t(c.n_layers) * parts, items = n * per;
-  int checked = -1;   // the pair that `bad` is known of
-  bool bad = false;
-  // a CTA's items lie side by side: it looks through the list once per pair
-  const int64_t each = (items + gridDim.x - 1) / gridDim.x, last = (blockIdx.x + 1) * each < items ? (blockIdx.x + 1) * each : items;
-  for (int64_t it = blockIdx.x * each; it < last; it++) {
-    const int i = int(it / per), layer = int(it % per / parts), part = int(it % parts);
+  const int64_t per = int64_t(c.n_layers) * ps.count, all = n * per, each = (all + gridDim.x - 1) / gridDim.x;
+  const int64_t q0 = blockIdx.x * each, q1 = q0 + each < all ? q0 + each : all;
+  if (q0 >= q1) return;
+  const int i0 = int(q0 / per), i1 = int((q1 - 1) / per);
+  for (int i = threadIdx.x; i <= (i1 - i0) / 32; i += kKv4CopyThreads) s_bad[i] = 0u;
+  __syncthreads();
+  for (int i = i0; i <= i1; i++) {
     const int s = src[i], d = dst[i];
-    if (i != checked) {
-      bool mine = s < 0 || s >= c.n_pages || d < 0 || d >= c.n_pages;
-      for (int e = threadIdx.x; e < n; e += blockDim.x) {
-        const int x = dst[e];
-        mine = mine || (e != i && (x == s || (e < i && x == d)));
-      }
-      bad = __syncthreads_or(mine);
-      checked = i;
-      if (bad && threadIdx.x == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
+    bool bad = s < 0 || s >= c.n_pages || d < 0 || d >= c.n_pages;
+    for (int e = threadIdx.x; e < n; e += kKv4CopyThreads) {
+      const int x = dst[e];
+      bad = bad || (e != i && (x == s || (e < i && x == d)));
     }
-    if (!bad && s != d) kv4_copy_part(c, s, d, layer, part, parts);
+    if (bad) {
+      atomicOr(&s_bad[(i - i0) >> 5], 1u << ((i - i0) & 31));
+      kv4_flag(c, NT_KV4_BAD_PAGE);
+    }
   }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    kv4_stream(c, q0, q1, 1, [&](int64_t q, const uint8_t** f, uint8_t** t, uint32_t* b) {
+      const int i = int(q / per), r = int(q % per), s = src[i], d = dst[i];
+      return !(s_bad[(i - i0) >> 5] >> ((i - i0) & 31) & 1u) && s != d &&
+             kv4_piece(c, ps, s, d, r / ps.count, r % ps.count, f, t, b);
+    });
 }
 
 // The plan of a compaction by one CTA: L, the pages in use; `to[p]`, where page p
@@ -755,10 +824,22 @@ __global__ void __launch_bounds__(1024) k_kv4_compact_plan(Kv4 c, int32_t* go, i
   }
 }
 
-__global__ void __launch_bounds__(256) k_kv4_compact_apply(Kv4 c, const int32_t* go, const int2* pair, const int32_t* to,
-                                                           int32_t* table_out, int32_t* refs_out, int parts) {
+__global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_compact_apply(Kv4 c, const int32_t* go, const int2* pair, const int32_t* to,
+                                                           int32_t* table_out, int32_t* refs_out, Kv4Pieces ps) {
   kv4_dependent();
-  const int64_t first = int64_t(blockIdx.x) * 256 + threadIdx.x, step = int64_t(gridDim.x) * 256;
+  if (threadIdx.x < 32) {   // the first warp's first thread copies, the other warps write tables and counts
+    if (threadIdx.x == 0) {
+      const int64_t per = int64_t(c.n_layers) * ps.count;
+      kv4_stream(c, blockIdx.x, go[1] * per, gridDim.x, [&](int64_t q, const uint8_t** f, uint8_t** t, uint32_t* b) {
+        const int2 m = pair[q / per];
+        const int r = int(q % per);
+        return kv4_piece(c, ps, m.x, m.y, r / ps.count, r % ps.count, f, t, b);
+      });
+    }
+    return;
+  }
+  constexpr int kOthers = kKv4CopyThreads - 32;
+  const int64_t first = int64_t(blockIdx.x) * kOthers + threadIdx.x - 32, step = int64_t(gridDim.x) * kOthers;
   for (int64_t p = first; p < c.n_pages; p += step) {
     const int d = to[p], r = c.refs[p];
     if (d == -2) continue;                     // the page that moves here writes it
@@ -774,11 +855,14 @@ __global__ void __launch_bounds__(256) k_kv4_compact_apply(Kv4 c, const int32_t*
     }
     table_out[e] = p == -2 ? -1 : p;
   }
-  const int64_t items = int64_t(go[1]) * c.n_layers * parts;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int2 m = pair[it / parts / c.n_layers];
-    kv4_copy_part(c, m.x, m.y, int(it / parts % c.n_layers), int(it % parts), parts);
-  }
+}
+
+// A copying kernel: one CTA per SM, fewer where there are fewer pieces.
+template <class K, class... A>
+static cudaError_t kv4_launch_copy(const KernelSetup& setup, K kern, int64_t pieces, cudaStream_t s, A... args) {
+  if (setup.err != cudaSuccess) return setup.err;
+  const unsigned grid = unsigned(pieces < 1 ? 1 : (pieces < setup.sms ? pieces : setup.sms));
+  return kv4_launch_smem(kern, grid, kKv4CopyThreads, Kv4CopyShared::kSize, s, args...);
 }
 
 static unsigned kv4_grid(int64_t blocks, int64_t most) { return unsigned(blocks < 1 ? 1 : (blocks > most ? most : blocks)); }
@@ -817,12 +901,14 @@ static nt_status kv4_plan_apply(const char* who, const Kv4& k, Kv4PlanArgs a, vo
   uint8_t* base = static_cast<uint8_t*>(ws);
   a.go = reinterpret_cast<int32_t*>(base);
   a.off = reinterpret_cast<int64_t*>(base + w.off);
+  a.from = reinterpret_cast<int32_t*>(base + w.from);
   a.pair = reinterpret_cast<int2*>(base + w.pair);
   a.free = reinterpret_cast<int32_t*>(base + w.free);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   NT_CUDA(kv4_launch(k_kv4_plan<FORK>, 1u, 1024u, s, k, a));
-  const int parts = kv4_parts(k, a.n);
-  NT_CUDA(kv4_launch(k_kv4_apply<FORK>, kv4_grid(int64_t(a.n) * k.n_layers * parts, kKv4Blocks), 256u, s, k, a, parts));
+  static const KernelSetup setup = kernel_setup(k_kv4_apply<FORK>, Kv4CopyShared::kSize);
+  const Kv4Pieces ps = kv4_pieces(k, a.n);
+  NT_CUDA(kv4_launch_copy(setup, k_kv4_apply<FORK>, int64_t(a.n) * k.n_layers * ps.count, s, k, a, ps));
   return NT_OK;
 }
 
@@ -932,7 +1018,7 @@ nt_status nt_kv4_free(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, 
   if (!st) st = kv4_array_check(k, "nt_kv4_free", dev_seq, n, true, nullptr, 0);
   if (!st) st = kv4_array_check(k, "nt_kv4_free", dev_keep, n, true, nullptr, 0);
   if (st || n == 0) return st;
-  NT_CUDA(kv4_launch(k_kv4_free, kv4_grid(n, kKv4Blocks), 256u, static_cast<cudaStream_t>(stream), k, n, dev_seq, dev_keep));
+  NT_CUDA(kv4_launch(k_kv4_free, kv4_grid(n, 152 * 8), 256u, static_cast<cudaStream_t>(stream), k, n, dev_seq, dev_keep));
   return NT_OK;
 }
 
@@ -944,9 +1030,11 @@ nt_status nt_kv4_copy_pages(const nt_kv4_cache* c, int32_t n, const int32_t* dev
   if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_src, n, false, nullptr, 0);
   if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_dst, n, false, nullptr, 0);
   if (st || n == 0) return st;
-  const int parts = kv4_parts(k, n);
-  NT_CUDA(kv4_launch(k_kv4_copy_pages, kv4_grid(int64_t(n) * k.n_layers * parts, kKv4Blocks), 256u,
-                     static_cast<cudaStream_t>(stream), k, n, dev_src, dev_dst, parts));
+  static const KernelSetup setup = kernel_setup(k_kv4_copy_pages, Kv4CopyShared::kSize);
+  const Kv4Pieces ps = kv4_pieces(k, n);
+  const int64_t pieces = int64_t(n) * k.n_layers * ps.count;
+  if (n / setup.sms >= kKv4CopyPairs - 2) return fail(NT_E_INVAL, "nt_kv4_copy_pages: more pairs than one call takes");
+  NT_CUDA(kv4_launch_copy(setup, k_kv4_copy_pages, pieces, static_cast<cudaStream_t>(stream), k, n, dev_src, dev_dst, ps));
   return NT_OK;
 }
 
@@ -975,9 +1063,11 @@ nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t*
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   NT_CUDA(kv4_launch(k_kv4_compact_plan, 1u, 1024u, s, k, go, pair, to, dev_live));
   // (how many pages move is known on the device only; at most half of them do)
-  NT_CUDA(kv4_launch(k_kv4_compact_apply, unsigned(kKv4Blocks), 256u, s, k, static_cast<const int32_t*>(go),
-                     static_cast<const int2*>(pair), static_cast<const int32_t*>(to), dev_table_out, dev_refs_out,
-                     kv4_parts(k, 8)));
+  static const KernelSetup setup = kernel_setup(k_kv4_compact_apply, Kv4CopyShared::kSize);
+  const Kv4Pieces ps = kv4_pieces(k, k.n_pages > 16 ? k.n_pages / 8 : 1);
+  NT_CUDA(kv4_launch_copy(setup, k_kv4_compact_apply, int64_t(k.n_pages) * k.n_layers * ps.count, s, k,
+                          static_cast<const int32_t*>(go), static_cast<const int2*>(pair), static_cast<const int32_t*>(to),
+                          dev_table_out, dev_refs_out, ps));
   return NT_OK;
 }
 

@@ -64,16 +64,18 @@ bool kv4_meets_cache(const Kv4& k, const void* p, int64_t bytes);
 // Workspace of the page operators, 16-byte aligned parts.
 //   plan: int32 [4]: {the call goes ahead, pairs to copy, -, -}
 //   off:  int64 [n + 1] first free page of each entry's share
-//   pair: int2 [max(n, n_pages / 2)] pages to copy (source, destination; -1: none)
+//   from: int32 [n] page that an entry's first new page is a copy of (-1: none)
+//   pair: int2 [max(n, n_pages / 2)] pages to copy (source, destination)
 //   free: int32 [n_pages] free pages in order (extend, fork); where a page goes (compact)
 struct Kv4Ws {
-  size_t off = 16, pair = 0, free = 0, bytes = 0;
+  size_t off = 16, from = 0, pair = 0, free = 0, bytes = 0;
 };
 inline Kv4Ws kv4_ws(const Kv4& k, int64_t n) {
   auto up = [](size_t b) { return (b + 15) & ~size_t(15); };
   Kv4Ws w;
   const size_t pairs = size_t(n > k.n_pages / 2 ? n : k.n_pages / 2);
-  w.pair = up(w.off + size_t(n + 1) * 8);
+  w.from = up(w.off + size_t(n + 1) * 8);
+  w.pair = up(w.from + size_t(n) * 4);
   w.free = up(w.pair + pairs * 8);
   w.bytes = up(w.free + size_t(k.n_pages) * 4);
   return w;
@@ -85,5 +87,38 @@ size_t kv4_attn_ws_bytes(int n_heads, int n_kv, int hd);
 // ------------------------------------------------------------ device helpers --
 
 __device__ __forceinline__ void kv4_flag(const Kv4& k, uint32_t bits) { atomicOr(k.error, bits); }
+
+// ---- bulk copies into shared memory, counted on mbarriers of one arrival
+__device__ __forceinline__ uint32_t kv4_smem(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void kv4_bar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void kv4_bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Chunks from global to shared memory, their bytes counted on bar.
+__device__ __forceinline__ void kv4_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void kv4_bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// Waits for the phase of `parity` to complete, at most kKv4WaitTries tries (each
+// of which the hardware may hold for a while); false: gave up.
+constexpr int kKv4WaitTries = 1 << 20;
+__device__ __forceinline__ bool kv4_bar_wait(uint32_t bar, uint32_t parity) {
+  for (int i = 0; i < kKv4WaitTries; i++) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (done) return true;
+  }
+  return false;
+}
 
 }  // namespace nt
