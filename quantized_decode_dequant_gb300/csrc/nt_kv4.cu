@@ -616,49 +616,86 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
     for (int i = t; i < a.n; i += 1024) c.len[a.a ? a.a[i] : i] += a.b[i];
 }
 
-// ---- copies.  One thread of a CTA moves pieces of pages through a ring in shared
-// memory by bulk copies, kKv4Ahead of them on the way in while others are on the way out;
-// the CTA's other warps do what else there is.  (Copies by all threads, 64 bytes
-// each in flight, 8 CTAs of 256 per SM: 53.6 us for 24 pages of 73.7 KB in 80 layers.)
-constexpr int kKv4Piece = 16384, kKv4Ring = 12, kKv4Ahead = 8;
+// ---- copies.  Whole pages move in pieces through shared memory by bulk copies:
+// one thread of each of a CTA's first warps has a ring of its own, kKv4Ahead pieces on
+// the way in while others are on the way out; the remaining warps do what else there
+// is.  (Copies by all threads, 64 bytes each in flight, 8 CTAs of 256 per SM: 53.6
+// us for 24 pages of 73.7 KB in 80 layers.)
+constexpr int kKv4Streams = 4, kKv4Piece = 12288, kKv4Ring = 4, kKv4Ahead = 3;
 constexpr int kKv4CopyThreads = 256;
-struct Kv4CopyShared {
+struct Kv4CopyShared {   // of a stream
   static constexpr int kBars = kKv4Piece * kKv4Ring, kTo = kBars + 8 * kKv4Ring, kBytes = kTo + 8 * kKv4Ring,
-                       kSize = kBytes + 4 * kKv4Ring + 16;
+                       kStream = (kBytes + 4 * kKv4Ring + 127) / 128 * 128, kSize = kStream * kKv4Streams;
+  static_assert(kSize <= 220 * 1024, "shared memory of a CTA");
 };
 extern __shared__ __align__(128) uint8_t kv4_sm[];
 
-// Pieces q0, q0 + dq, .. below q1 by the calling thread.  piece(q, &from, &to, &bytes):
-// false where there is nothing to copy.  No piece's destination is another's source.
+// Pieces of n pages of every layer: `count` of `bytes` each (the last of a page the rest).
+struct Kv4Pieces {
+  int32_t bytes, count;
+};
+// 12 KB, or less where that makes fewer pieces than streams (1 KB at least).
+static Kv4Pieces kv4_pieces(const Kv4& k, int64_t n) {
+  const int64_t pb = k.page_bytes(), all = pb * k.n_layers * n;
+  int64_t b = kKv4Piece;
+  while (b > 1024 && all / b < kKv4Streams * 152) b /= 2;
+  Kv4Pieces p;
+  p.count = int32_t((pb + b - 1) / b);
+  p.bytes = int32_t(((pb + p.count - 1) / p.count + 15) / 16 * 16);
+  p.count = int32_t((pb + p.bytes - 1) / p.bytes);
+  return p;
+}
+
+// The stream's share of the pieces of `pairs` pages (source, destination) in every
+// layer, one after the other; by the calling thread.  pair(i): the i-th pair (x < 0:
+// it is not copied).  No pair's destination is another's source.
 template <class P>
-__device__ __forceinline__ void kv4_stream(const Kv4& c, int64_t q0, int64_t q1, int64_t dq, P piece) {
+__device__ __forceinline__ void kv4_stream(const Kv4& c, Kv4Pieces ps, int64_t pairs, int stream, P pair) {
   using Sh = Kv4CopyShared;
-  const uint32_t ring = kv4_smem(kv4_sm), bars = ring + Sh::kBars;
-  uint8_t** to = reinterpret_cast<uint8_t**>(kv4_sm + Sh::kTo);
-  uint32_t* bytes = reinterpret_cast<uint32_t*>(kv4_sm + Sh::kBytes);
+  const int64_t per = int64_t(c.n_layers) * ps.count, all = pairs * per, streams = int64_t(gridDim.x) * kKv4Streams;
+  const int64_t each = (all + streams - 1) / streams, q0 = (int64_t(blockIdx.x) * kKv4Streams + stream) * each;
+  int64_t todo = q0 + each < all ? each : all - q0;   // pieces not yet begun
+  if (todo <= 0) return;
+  uint8_t* sm = kv4_sm + stream * Sh::kStream;
+  const uint32_t ring = kv4_smem(sm), bars = ring + Sh::kBars;
+  uint8_t** to = reinterpret_cast<uint8_t**>(sm + Sh::kTo);
+  uint32_t* bytes = reinterpret_cast<uint32_t*>(sm + Sh::kBytes);
   for (int i = 0; i < kKv4Ring; i++) kv4_bar_init(bars + 8 * i);
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  int64_t in = 0, out = 0;   // pieces whose copy in, out was begun
-  for (int64_t q = q0;;) {
-    for (; q < q1 && in - out < kKv4Ahead; q += dq) {
-      const uint8_t* f;
-      uint8_t* t;
-      uint32_t n;
-      if (!piece(q, &f, &t, &n)) continue;
-      const int st = int(in % kKv4Ring);
-      // the copy out of what stood there before has been read: all but the last kKv4Ring - kKv4Ahead have
-      asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kKv4Ring - kKv4Ahead) : "memory");
-      to[st] = t;
-      bytes[st] = n;
-      kv4_bar_expect(bars + 8 * st, n);
-      kv4_copy(ring + st * kKv4Piece, f, n, bars + 8 * st);
-      in++;
+  const int64_t pb = c.page_bytes();
+  int64_t i = q0 / per;
+  int layer = int(q0 % per / ps.count), part = int(q0 % ps.count);
+  int2 m = pair(i);
+  uint32_t in = 0, out = 0;   // pieces whose copy in, out was begun
+  for (;;) {
+    while (todo > 0 && in - out < kKv4Ahead) {
+      if (m.x >= 0) {
+        const int st = in % kKv4Ring;
+        // the copy out of what stood there before has been read: all but the last kKv4Ring - kKv4Ahead have
+        asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kKv4Ring - kKv4Ahead) : "memory");
+        const int64_t at = int64_t(part) * ps.bytes, plane = int64_t(layer) * c.n_pages;
+        const uint32_t n = uint32_t(pb - at < ps.bytes ? pb - at : ps.bytes);
+        to[st] = c.pool + (plane + m.y) * pb + at;
+        bytes[st] = n;
+        kv4_bar_expect(bars + 8 * st, n);
+        kv4_copy(ring + st * kKv4Piece, c.pool + (plane + m.x) * pb + at, n, bars + 8 * st);
+        in++;
+      }
+      todo--;
+      if (++part == ps.count) {
+        part = 0;
+        if (++layer == c.n_layers) {
+          layer = 0;
+          i++;
+          if (todo > 0) m = pair(i);
+        }
+      }
     }
     if (out == in) break;
-    const int st = int(out % kKv4Ring);
-    if (!kv4_bar_wait(bars + 8 * st, uint32_t(out / kKv4Ring) & 1u)) {
+    const int st = out % kKv4Ring;
+    if (!kv4_bar_wait(bars + 8 * st, out / kKv4Ring & 1u)) {
       kv4_flag(c, NT_KV4_TIMEOUT);
-      for (int64_t x = out + 1; x < in; x++) kv4_bar_wait(bars + 8 * int(x % kKv4Ring), uint32_t(x / kKv4Ring) & 1u);
+      for (uint32_t x = out + 1; x < in; x++) kv4_bar_wait(bars + 8 * (x % kKv4Ring), x / kKv4Ring & 1u);
       break;
     }
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n\tcp.async.bulk.commit_group;" ::"l"(to[st]),
@@ -669,55 +706,29 @@ __device__ __forceinline__ void kv4_stream(const Kv4& c, int64_t q0, int64_t q1,
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// Bytes of a piece and pieces of a page when n pages of every layer are copied by
-// 152 CTAs: 16 KB, or less where that makes too few pieces (1 KB at least).
-struct Kv4Pieces {
-  int32_t bytes, count;
-};
-static Kv4Pieces kv4_pieces(const Kv4& k, int64_t n) {
-  const int64_t pb = k.page_bytes(), all = pb * k.n_layers * n;
-  int64_t b = kKv4Piece;
-  while (b > 1024 && all / b < 4 * 152) b /= 2;
-  Kv4Pieces p;
-  p.count = int32_t((pb + b - 1) / b);
-  p.bytes = int32_t(((pb + p.count - 1) / p.count + 15) / 16 * 16);
-  return p;
-}
-// Piece `part` of page src of a layer, to page dst.
-__device__ __forceinline__ bool kv4_piece(const Kv4& c, Kv4Pieces ps, int src, int dst, int layer, int part, const uint8_t** from,
-                                          uint8_t** to, uint32_t* bytes) {
-  const int64_t pb = c.page_bytes(), at = int64_t(part) * ps.bytes;
-  *from = c.pool + (int64_t(layer) * c.n_pages + src) * pb + at;
-  *to = c.pool + (int64_t(layer) * c.n_pages + dst) * pb + at;
-  *bytes = uint32_t(pb - at < ps.bytes ? pb - at : ps.bytes);
-  return at < pb;
-}
-
 // The pairs of a plan; FORK: also the destinations' tables, counts and lengths.
 template <bool FORK>
 __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_apply(Kv4 c, Kv4PlanArgs a, Kv4Pieces ps) {
   kv4_dependent();
   if (!a.go[0]) return;
-  if (threadIdx.x == 0) {
-    const int64_t per = int64_t(c.n_layers) * ps.count;
-    kv4_stream(c, blockIdx.x, a.go[1] * per, gridDim.x, [&](int64_t q, const uint8_t** f, uint8_t** t, uint32_t* b) {
-      const int2 m = a.pair[q / per];
-      const int r = int(q % per);
-      return kv4_piece(c, ps, m.x, m.y, r / ps.count, r % ps.count, f, t, b);
-    });
+  const int warp = threadIdx.x >> 5;
+  if (warp < kKv4Streams) {
+    if ((threadIdx.x & 31) == 0) kv4_stream(c, ps, a.go[1], warp, [&](int64_t i) { return a.pair[i]; });
+    return;
   }
-  if (FORK && threadIdx.x >= 32) {
+  if (FORK) {
+    constexpr int kFirst = 32 * kKv4Streams;
     for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
       const int s = a.a[i], d = a.b[i], keep = a.keep ? a.keep[i] : c.len[s], full = keep / c.page_len;
       const int32_t* from = c.table + int64_t(s) * c.max_pages;
       int32_t* to = c.table + int64_t(d) * c.max_pages;
-      for (int j = threadIdx.x - 32; j < full; j += kKv4CopyThreads - 32) {
+      for (int j = threadIdx.x - kFirst; j < full; j += kKv4CopyThreads - kFirst) {
         const int p = from[j];
         to[j] = p;
         if (p >= 0 && p < c.n_pages) atomicAdd(&c.refs[p], 1);
         else kv4_flag(c, NT_KV4_BAD_PAGE);
       }
-      if (threadIdx.x == 32) c.len[d] = keep;
+      if (threadIdx.x == kFirst) c.len[d] = keep;
     }
   }
 }
@@ -758,14 +769,14 @@ __global__ void __launch_bounds__(256) k_kv4_free(Kv4 c, int n, const int32_t* s
   }
 }
 
-// CTA b copies pieces [b each, (b + 1) each), which belong to few pairs: those are checked first.
+// A CTA's pieces belong to few pairs: those are checked first.
 constexpr int kKv4CopyPairs = 8192;   // most pairs of a CTA
 __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_copy_pages(Kv4 c, int n, const int32_t* src, const int32_t* dst,
                                                                     Kv4Pieces ps) {
   __shared__ uint32_t s_bad[kKv4CopyPairs / 32];
   kv4_dependent();
-  const int64_t per = int64_t(c.n_layers) * ps.count, all = n * per, each = (all + gridDim.x - 1) / gridDim.x;
-  const int64_t q0 = blockIdx.x * each, q1 = q0 + each < all ? q0 + each : all;
+  const int64_t per = int64_t(c.n_layers) * ps.count, all = n * per, streams = int64_t(gridDim.x) * kKv4Streams;
+  const int64_t each = (all + streams - 1) / streams * kKv4Streams, q0 = blockIdx.x * each, q1 = q0 + each < all ? q0 + each : all;
   if (q0 >= q1) return;
   const int i0 = int(q0 / per), i1 = int((q1 - 1) / per);
   for (int i = threadIdx.x; i <= (i1 - i0) / 32; i += kKv4CopyThreads) s_bad[i] = 0u;
@@ -783,11 +794,11 @@ __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_copy_pages(Kv4 c, int n
     }
   }
   __syncthreads();
-  if (threadIdx.x == 0)
-    kv4_stream(c, q0, q1, 1, [&](int64_t q, const uint8_t** f, uint8_t** t, uint32_t* b) {
-      const int i = int(q / per), r = int(q % per), s = src[i], d = dst[i];
-      return !(s_bad[(i - i0) >> 5] >> ((i - i0) & 31) & 1u) && s != d &&
-             kv4_piece(c, ps, s, d, r / ps.count, r % ps.count, f, t, b);
+  const int warp = threadIdx.x >> 5;
+  if (warp < kKv4Streams && (threadIdx.x & 31) == 0)
+    kv4_stream(c, ps, n, warp, [&](int64_t q) {
+      const int i = int(q), s = src[i], d = dst[i];
+      return (s_bad[(i - i0) >> 5] >> ((i - i0) & 31) & 1u) || s == d ? make_int2(-1, -1) : make_int2(s, d);
     });
 }
 
@@ -827,19 +838,13 @@ __global__ void __launch_bounds__(1024) k_kv4_compact_plan(Kv4 c, int32_t* go, i
 __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_compact_apply(Kv4 c, const int32_t* go, const int2* pair, const int32_t* to,
                                                            int32_t* table_out, int32_t* refs_out, Kv4Pieces ps) {
   kv4_dependent();
-  if (threadIdx.x < 32) {   // the first warp's first thread copies, the other warps write tables and counts
-    if (threadIdx.x == 0) {
-      const int64_t per = int64_t(c.n_layers) * ps.count;
-      kv4_stream(c, blockIdx.x, go[1] * per, gridDim.x, [&](int64_t q, const uint8_t** f, uint8_t** t, uint32_t* b) {
-        const int2 m = pair[q / per];
-        const int r = int(q % per);
-        return kv4_piece(c, ps, m.x, m.y, r / ps.count, r % ps.count, f, t, b);
-      });
-    }
+  const int warp = threadIdx.x >> 5;
+  if (warp < kKv4Streams) {
+    if ((threadIdx.x & 31) == 0) kv4_stream(c, ps, go[1], warp, [&](int64_t i) { return pair[i]; });
     return;
   }
-  constexpr int kOthers = kKv4CopyThreads - 32;
-  const int64_t first = int64_t(blockIdx.x) * kOthers + threadIdx.x - 32, step = int64_t(gridDim.x) * kOthers;
+  constexpr int kOthers = kKv4CopyThreads - 32 * kKv4Streams;   // the other warps write tables and counts
+  const int64_t first = int64_t(blockIdx.x) * kOthers + threadIdx.x - 32 * kKv4Streams, step = int64_t(gridDim.x) * kOthers;
   for (int64_t p = first; p < c.n_pages; p += step) {
     const int d = to[p], r = c.refs[p];
     if (d == -2) continue;                     // the page that moves here writes it
@@ -861,7 +866,8 @@ __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_compact_apply(Kv4 c, co
 template <class K, class... A>
 static cudaError_t kv4_launch_copy(const KernelSetup& setup, K kern, int64_t pieces, cudaStream_t s, A... args) {
   if (setup.err != cudaSuccess) return setup.err;
-  const unsigned grid = unsigned(pieces < 1 ? 1 : (pieces < setup.sms ? pieces : setup.sms));
+  const int64_t ctas = (pieces + kKv4Streams - 1) / kKv4Streams;
+  const unsigned grid = unsigned(ctas < 1 ? 1 : (ctas < setup.sms ? ctas : setup.sms));
   return kv4_launch_smem(kern, grid, kKv4CopyThreads, Kv4CopyShared::kSize, s, args...);
 }
 
