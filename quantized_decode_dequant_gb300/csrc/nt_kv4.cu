@@ -180,7 +180,7 @@ template <> struct Kv4Block<float> {
   float4 r[8];
   __device__ __forceinline__ void load(const float* p) {
 #pragma unroll
-    for (int i = 0; i < 8; i++) r[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+    for (int i = 0; i < 8; i++) r[i] = reinterpret_cast<const float4*>(p)[i];
   }
   __device__ __forceinline__ float top() const {
     float m = 0.f;
@@ -198,7 +198,7 @@ template <> struct Kv4Block<__half> {
   uint4 r[4];
   __device__ __forceinline__ void load(const __half* p) {
 #pragma unroll
-    for (int i = 0; i < 4; i++) r[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < 4; i++) r[i] = reinterpret_cast<const uint4*>(p)[i];
   }
   __device__ __forceinline__ float top() const {
     uint32_t m = 0u;

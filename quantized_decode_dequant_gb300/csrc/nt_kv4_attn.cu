@@ -228,9 +228,42 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     return reinterpret_cast<float*>(w & 1 ? sm + Cfg::kRing + (w >> 1) * (S * Cfg::kPair) : sm + Cfg::kSlots + (w >> 1) * (Cfg::kPart * 4));
   };
 
+  if (lane < S) kv4_bar_init(kv4_smem(sm + Cfg::kBars + (warp * S + lane) * 8));
+  if (lane < 2) slot_item[2 * warp + lane] = -1;
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // ---- pair offsets of the entries (an entry's pairs are counted once per kv head)
-  {
+  // ---- unit offsets of the entries
+  constexpr int kFew = 128;
+  if (n <= kFew) {   // every warp for itself, all to the same places: no barrier
+    int2 sl[kFew / 32];
+#pragma unroll
+    for (int i = 0; i < kFew / 32; i++) {
+      const int e = 32 * i + lane;
+      uint32_t bad = 0;
+      sl[i] = make_int2(-1, 0);
+      if (e < n) sl[i] = kv4_entry(c, a, e, &bad);
+      if (bad && blockIdx.x == 0 && warp == 0) kv4_flag(c, bad);
+    }
+    int run = 0;
+#pragma unroll
+    for (int i = 0; i < kFew / 32; i++) {
+      if (32 * i >= n) break;
+      const int e = 32 * i + lane, mine = sl[i].y ? (kv4_pairs(sl[i].y) + kKv4ItemPairs) * c.n_kv : 0;
+      int x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (e < n) {
+        entry[e] = sl[i];
+        prefix[e] = run + x - mine;
+      }
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) prefix[n] = run;
+    __syncwarp();
+  } else {
     int* sums = reinterpret_cast<int*>(sm + Cfg::kSlots);   // per-warp sums, before the slots are used
     int run = 0;
     for (int e0 = 0; e0 < n; e0 += Cfg::kThreads) {
@@ -259,12 +292,9 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
       }
       if (e < n) prefix[e] = run + before + x - mine;
       run += all;
-      if (e0 + Cfg::kThreads < n) __syncthreads();
+      __syncthreads();
     }
     if (t == 0) prefix[n] = run;
-    if (lane < S) kv4_bar_init(kv4_smem(sm + Cfg::kBars + (warp * S + lane) * 8));
-    if (lane < 2) slot_item[2 * warp + lane] = -1;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
   }
   const int total = prefix[n], warps = int(gridDim.x) * NW;
@@ -380,8 +410,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
         for (int j = 0; j < NG; j++) {
           float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
           if (h < G) {
-            u = __ldg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg));
-            v = __ldg(reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg) + 1);
+            u = *reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg);
+            v = *reinterpret_cast<const float4*>(qb + h * HD + 32 * j + 8 * tg + 4);
           }
           qx[m][j][0] = u.x; qx[m][j][1] = u.y; qx[m][j][2] = u.z; qx[m][j][3] = u.w;
           qx[m][j][4] = v.x; qx[m][j][5] = v.y; qx[m][j][6] = v.z; qx[m][j][7] = v.w;
@@ -684,7 +714,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   constexpr int V = HD / 32;
   const int mine = lane < 2 * NW ? slot_item[lane] : -1;
   int* order = reinterpret_cast<int*>(sm + Cfg::kOrder) + warp * 32;
-  for (uint32_t left = __ballot_sync(0xffffffffu, mine >= 0); left;) {
+  int turn = warp;   // (item, head) pairs go round the warps
+  for (uint32_t left = __ballot_sync(0xffffffffu, mine >= 0); left; turn = (turn + NW * G - G) % NW) {
     const int a0 = __ffs(left) - 1, item = __shfl_sync(0xffffffffu, mine, a0);
     const uint32_t members = __ballot_sync(0xffffffffu, mine == item);
     left &= ~members;
@@ -698,7 +729,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     const bool whole = first >= c0 && first + ip <= c1;
     float* part = part0 + (first < c0 ? 0 : Cfg::kPart);
     float* to = whole ? a.out + int64_t(ie) * a.out_stride + int64_t(ig) * G * HD : part;
-    for (int h = warp; h < G; h += NW) {
+    for (int h = turn; h < G; h += NW) {
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < nm) ml = reinterpret_cast<const float2*>(slot_ptr(nth) + ROWS * HD)[h];
       float M = ml.x;

@@ -197,6 +197,37 @@ def test_blocks_that_cannot_be_held_read_as_nan_and_others_are_exact(nt):
     assert np.isnan(want[[0, 1, 2, 3, 4, 6, 7], 0, :32]).all() and np.isfinite(want[:8, 0, 32:]).all()
 
 
+@pytest.mark.parametrize("half", [False, True])
+def test_quotients_next_to_halves(nt, half):
+    """Values at, just below and just above every half of the scale, for scales over the whole range: the codes are those
+    of the fp32 quotient, halves away from zero."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(33)
+    ref = R.RefCache(1, 1, 128, 16, 32, 1, 32)
+    ref.hold([512])
+    dev = Dev(nt, ref)
+    kind = np.float16 if half else np.float32
+    x = np.zeros((2, 512, 1, 128), np.float32)
+    bits = rng.integers(1, 0x631, (2, 512, 4)).astype(np.uint16) << 4        # scales that the format holds
+    d = bits.view(np.float16).astype(np.float64)
+    for side in (0, 1):
+        for r in range(512):
+            for j in range(4):
+                h = (rng.integers(0, 7, 32) + 0.5) * rng.choice([-1, 1], 32)
+                v = (h * d[side, r, j]).astype(kind)
+                way = rng.integers(-2, 3, 32)                                    # steps of the type towards 0 or away
+                for _ in range(2):
+                    v = np.where(way > 0, np.nextafter(v, kind(np.inf) * np.sign(v)), np.where(way < 0, np.nextafter(v, kind(0)), v))
+                    way = way - np.sign(way)
+                v[int(rng.integers(0, 32))] = 7 * d[side, r, j]
+                x[side, r, 0, 32 * j:32 * j + 32] = v
+    x = x.astype(kind)
+    k, v = _layout(torch, x, "rows")
+    dev.rows(k, v, [0, 512])
+    _store(ref, x.astype(np.float32), [0, 512], [0])
+    dev.check()
+
+
 def test_rows_that_do_not_fit_are_flagged_and_passed_over(nt):
     torch = torch_cuda()
     rng = np.random.default_rng(10)
@@ -393,6 +424,27 @@ def test_attention_lists_strides_workspaces_and_streams(nt):
     torch.cuda.synchronize()
     for o in outs:
         np.testing.assert_array_equal(o.cpu().numpy().view(np.uint32), first.view(np.uint32))
+
+
+@pytest.mark.parametrize("n", [129, 300, 1024, 1500])
+def test_attention_of_many_listed_sequences(nt, n):
+    """Lists beyond what a warp counts for itself, and beyond one launch; a sequence's result does not depend on its place
+    but for the order in which partial sums meet."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(43)
+    ref = R.RefCache(1, 1, 64, 16, 60, 9, 9)
+    ref.randomize(rng)
+    lens = [1, 0, 17, 140, 32, 33, 100, 5, 64]
+    ref.hold(lens, rng)
+    dev = Dev(nt, ref, 2)
+    seqs = rng.integers(0, 9, n)
+    q = rng.standard_normal((9, 2, 64)).astype(np.float32)
+    got = dev.attention(torch.from_numpy(q[seqs]).cuda(), seqs).cpu().numpy().reshape(n, 2, 64)
+    want = _want(ref, range(9), q.astype(np.float64), 2)
+    for s in range(9):
+        b = _bound(ref, s, q[s].astype(np.float64), 2)
+        assert (np.abs(got[seqs == s] - want[s]).max(axis=(0, 2)) <= b).all(), s
+    assert int(dev.error.cpu()[0]) == 0
 
 
 def test_attention_of_what_it_cannot_read_is_nan(nt):
