@@ -65,19 +65,20 @@ __host__ __device__ constexpr int kv4_part_floats(int hd, int rows) { return row
 template <int HD, int HB>
 struct Kv4AttnCfg {
   static constexpr int NW = HB == 16 ? (HD == 128 ? 8 : 12) : (HD == 128 && HB == 8 ? 12 : 16);   // warps: registers decide
-  static constexpr int S = HD == 128 && HB < 16 ? 2 : 4;                               // ring stages of a warp
+  static constexpr int S = HD == 128 ? 2 : 4;                                          // ring stages of a warp
   static constexpr int kThreads = 32 * NW;
   static constexpr int kRows = HB;                                                     // heads of a partial result
   static constexpr int kPart = kv4_part_floats(HD, kRows);
   static constexpr int kPair = 2 * kv4_chunk_bytes(HD);                                // a stage: two chunks
   static constexpr int kRing = 0;
   static constexpr int kSlots = kRing + NW * S * kPair;                                // a slot of each warp (see below)
-  static constexpr int kPrefix = kSlots + NW * kPart * 4;
+  static constexpr int kAcc = kSlots + NW * kPart * 4;                                 // sums of outputs, a warp's lane by lane
+  static constexpr int kPrefix = kAcc + NW * kRows * HD * 4;
   static constexpr int kEntry = kPrefix + (kKv4Batch + 4) * 4;                         // {sequence, length} of each
   static constexpr int kBars = kEntry + kKv4Batch * 8;
   static constexpr int kItem = kBars + NW * S * 8;                                     // item of each slot (-1: none)
-  static constexpr int kOrder = kItem + 2 * NW * 4;                                    // [NW][32] slots in order (merge)
-  static constexpr int kSmem = kOrder + NW * 32 * 4;
+  static constexpr int kLane = kItem + 2 * NW * 4;                                     // [NW][2][32] words of the lanes
+  static constexpr int kSmem = kLane + NW * 64 * 4;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kPart * 4 <= S * kPair && kPart % 4 == 0, "a warp's ring holds a partial result");
   static_assert(2 * NW <= 32, "a lane per slot");
@@ -361,6 +362,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   int issued = 0;
   uint32_t missing = 0;                       // bit per stage: it lacks a page
   constexpr uint32_t kDead = 1u << 31;        // a wait ran out: nothing more is copied or read
+  constexpr uint32_t kHeld = 1u << 30;        // sums of the item's outputs are held in shared memory
   auto issue = [&]() {
     if (issued >= count || (missing & kDead)) return;
     if ((issued & 31) == 0 && issued) addr = resolve(issued + lane);
@@ -389,6 +391,14 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   uint32_t qa[N4 ? 1 : MT][HD / 16][N4 ? 2 : 4];
   // a lane's heads: gi (HB 8), gi and gi + 8 (HB 16), 2 (tg % 2) and the next one (N4)
   float mref[NH], l[NH], cs[NH];
+  // The matrix products' sums lose a little towards 0 at each addition (131077 positions of 8 kv heads, 72 additions
+  // a warp: 1.6e-6 of the result, where fp32 sums rounded to nearest are 0.7e-6 off), so every kFlush pairs they go,
+  // rounded to nearest, to sums in shared memory, which stand in relation to the mref of then.  A pair is 4 additions
+  // (N4: 2).  At 6 pairs the result is 0.8e-6 off and 0.6 us of 44 are spent on it, at 4 0.7e-6 and 1.1 us.
+  // N4 holds hi + lo, the first half of the tiles with the lanes of hi, the others with those of lo.
+  constexpr int kFlush = N4 ? 32 : 6, TILES = N4 ? NT / 4 : NT / 2;
+  float4* acc = reinterpret_cast<float4*>(sm + Cfg::kAcc) + warp * (TILES * MT * 32) + lane;
+  float* macc = reinterpret_cast<float*>(sm + Cfg::kLane) + warp * 64 + lane;   // [NH][32]
   int k = 0;                                  // pairs read
 #pragma unroll 1
   while (k < count) {
@@ -457,8 +467,12 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
         for (int m = 0; m < MT; m++) O[i][m][0] = O[i][m][1] = O[i][m][2] = O[i][m][3] = 0.f;
     }
 
+    missing &= ~kHeld;
+    const int kseg = k + seg;
 #pragma unroll 1
-    for (const int k1 = k + seg; k < k1; k++, live -= 2 * kKv4Chunk) {
+    for (;;) {
+#pragma unroll 1
+    for (const int k1 = kseg - k < kFlush ? kseg : k + kFlush; k < k1; k++, live -= 2 * kKv4Chunk) {
       const int st = k & (S - 1);
       if (!(missing & kDead) &&
           !__all_sync(0xffffffffu, kv4_bar_wait(bars + st * 8, uint32_t(k / S) & 1u))) {
@@ -481,6 +495,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll
       for (int u = 0; u < 2; u++) {
         uint32_t kw[2][NG], ks[2][NG / 2];
+        float low[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};   // HB 16: the lo products' sums
 #pragma unroll
         for (int i = 0; i < 2; i++) {
           kv4_words<NG>(base + u * CB + (i * 32 + lane) * (4 * NG), kw[i]);
@@ -512,8 +527,15 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
 #pragma unroll
               for (int y = 0; y < 2; y++)
 #pragma unroll
-                for (int i = 0; i < 2; i++) kv4_mma(sc[2 * u + i], qa[m][2 * j + y], b[i][2 * y], b[i][2 * y + 1]);
+                for (int i = 0; i < 2; i++)
+                  kv4_mma(m ? low[i] : sc[2 * u + i], qa[m][2 * j + y], b[i][2 * y], b[i][2 * y + 1]);
           }
+        }
+        if constexpr (HB == 16) {
+#pragma unroll
+          for (int i = 0; i < 2; i++)
+#pragma unroll
+            for (int y = 0; y < 4; y++) sc[2 * u + i][y] += low[i][y];
         }
       }
       // the scores of this lane's heads; of the i-th this is the position
@@ -654,6 +676,47 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
       }
     }
 
+      // O, and what is held if anything is, to the sums; or, at the segment's end, into O
+      const bool last = k == kseg, held = missing & kHeld;
+      if (last && !held) break;
+#pragma unroll
+      for (int m = 0; m < MT; m++) {
+        float f0 = 0.f, f1 = 0.f;   // of the sums: 2^(their mref - mref)
+        if (held) {
+          const float f = kv4_ex2(macc[32 * m] - mref[m]);
+          f0 = N4 ? f : __shfl_sync(0xffffffffu, f, 8 * tg);
+          f1 = N4 ? kv4_ex2(macc[32 * (NH - 1)] - mref[NH - 1]) : __shfl_sync(0xffffffffu, f, 8 * tg + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < TILES; i++) {   // (N4: tile i of the lanes of hi, TILES + i of those of lo)
+          float4* y = acc + (i * MT + m) * 32;
+          const bool second = N4 && tg >= 2;
+          float o[4];
+#pragma unroll
+          for (int x = 0; x < 4; x++) {
+            o[x] = second ? O[(i + TILES) % (NT / 2)][m][x] : O[i][m][x];
+            if (N4 && !last) o[x] += __shfl_xor_sync(0xffffffffu, second ? O[i][m][x] : O[(i + TILES) % (NT / 2)][m][x], 2);
+          }
+          if (held) {
+            const float4 v = *y;
+            o[0] = fmaf(v.x, f0, o[0]); o[1] = fmaf(v.y, f1, o[1]);
+            o[2] = fmaf(v.z, f0, o[2]); o[3] = fmaf(v.w, f1, o[3]);
+          }
+          if (!last) *y = make_float4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+          for (int x = 0; x < 4; x++) {
+            if (!second) O[i][m][x] = last ? o[x] : 0.f;
+            if (N4 && (second || !last)) O[(i + TILES) % (NT / 2)][m][x] = last ? o[x] : 0.f;
+            if (N4 && second && !last) O[i][m][x] = 0.f;
+          }
+        }
+      }
+      if (last) break;
+#pragma unroll
+      for (int m = 0; m < NH; m++) macc[32 * m] = mref[m];
+      missing |= kHeld;
+    }
+
     // ---- the end of the segment
 #pragma unroll
     for (int m = 0; m < NH; m++) {
@@ -713,7 +776,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   __syncthreads();
   constexpr int V = HD / 32;
   const int mine = lane < 2 * NW ? slot_item[lane] : -1;
-  int* order = reinterpret_cast<int*>(sm + Cfg::kOrder) + warp * 32;
+  int* order = reinterpret_cast<int*>(sm + Cfg::kLane) + warp * 64;
   int turn = warp;   // (item, head) pairs go round the warps
   for (uint32_t left = __ballot_sync(0xffffffffu, mine >= 0); left; turn = (turn + NW * G - G) % NW) {
     const int a0 = __ffs(left) - 1, item = __shfl_sync(0xffffffffu, mine, a0);

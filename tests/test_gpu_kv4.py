@@ -447,6 +447,34 @@ def test_attention_of_many_listed_sequences(nt, n):
     assert int(dev.error.cpu()[0]) == 0
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+def test_attention_with_much_work_for_every_warp(nt, hd, G):
+    """Over 32 steps a warp, so that sums are put aside within an item and items follow one another; rising scores, so
+    that the maximum moves on again and again."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([47, hd, G])
+    lens = [3001, 2800, 17, 3100]
+    ref = R.RefCache(1, 1, hd, 64, 160, 4, 50)
+    ref.randomize(rng)
+    ref.hold(lens, rng)
+    for s in (1, 3):   # the second and fourth sequence's keys grow with their place
+        for j, page in enumerate(ref.table[s][ref.table[s] >= 0]):
+            ref.pool.reshape(1, 160, 4, -1)[0, page, :, 16 * hd:17 * hd] = np.full(
+                hd // 2, 0.02 * (j + 1), np.float16).view(np.uint16).__and__(0xFFF0).view(np.uint8)
+    dev = Dev(nt, ref, G)
+    seqs = np.arange(1000) % 4
+    q = (rng.standard_normal((4, G, hd)) * 2).astype(np.float32)
+    got = dev.attention(torch.from_numpy(q[seqs]).cuda(), seqs).cpu().numpy().reshape(1000, G, hd)
+    want = _want(ref, range(4), q.astype(np.float64), G)
+    for s in range(4):
+        b = _bound(ref, s, q[s].astype(np.float64), G)
+        err = np.abs(got[seqs == s] - want[s]).max(axis=(0, 2))
+        assert (err <= b).all(), (s, float((err / b).max()))
+        rel = np.linalg.norm(got[seqs == s] - want[s]) / np.linalg.norm(np.broadcast_to(want[s], got[seqs == s].shape))
+        print(f"hd {hd} G {G} n {lens[s]}: rel L2 {rel:.2e}")
+
+
 def test_attention_of_what_it_cannot_read_is_nan(nt):
     torch = torch_cuda()
     rng = np.random.default_rng(51)
