@@ -30,6 +30,8 @@
 // near the memory bound, with the arithmetic close behind.  (tcgen05 would need
 // the decoded f16 values, four times the bytes, written to shared memory first;
 // mma.sync takes them from registers, and at 16 rows its rate is not the limit.)
+#include <cooperative_groups.h>
+
 #include "nt_kv4.cuh"
 
 namespace nt {
@@ -210,7 +212,12 @@ __device__ __forceinline__ int kv4_find(const int* prefix, int n, int x) {
 // A warp leaves at most two partial results to the CTA: of the item it did not
 // begin (slot 2 warp, in memory of its own) and of the one it did not end (slot
 // 2 warp + 1, its last: it stands in the warp's ring, which is empty by then).
-template <int HD, int HB>
+//
+// CL: the form for few items whose capacity is small (see kv4_launch_attn).  A
+// thread-block cluster has an item to itself, its warps share the pairs out, and
+// the CTAs' partial results meet through distributed shared memory: no second launch,
+// and no counting of the other entries.
+template <int HD, int HB, bool CL>
 __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv4 c, Kv4AttnArgs a) {
   using Cfg = Kv4AttnCfg<HD, HB>;
   using L = Kv4Chunk<HD>;
@@ -233,9 +240,15 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   if (lane < 2) slot_item[2 * warp + lane] = -1;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // ---- unit offsets of the entries
+  // ---- unit offsets of the entries (CL: the item's entry alone)
   constexpr int kFew = 128;
-  if (n <= kFew) {   // every warp for itself, all to the same places: no barrier
+  if constexpr (CL) {
+    uint32_t bad;
+    const int2 sl = kv4_entry(c, a, int(blockIdx.y) / c.n_kv, &bad);
+    if (bad && t == 0) kv4_flag(c, bad);
+    if (t == 0) { entry[0] = sl; prefix[0] = 0; prefix[1] = kv4_pairs(sl.y); }
+    __syncthreads();
+  } else if (n <= kFew) {   // every warp for itself, all to the same places: no barrier
     int2 sl[kFew / 32];
 #pragma unroll
     for (int i = 0; i < kFew / 32; i++) {
@@ -298,21 +311,31 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     if (t == 0) prefix[n] = run;
     __syncthreads();
   }
-  const int total = prefix[n], warps = int(gridDim.x) * NW;
+  const int e_own = CL ? int(blockIdx.y) / c.n_kv : 0, g_own = CL ? int(blockIdx.y) % c.n_kv : 0;
+  auto ent = [&](int e) { return entry[CL ? 0 : e]; };   // sequence and length of entry e
+  const int total = prefix[CL ? 1 : n], warps = int(gridDim.x) * NW;
   int share = (total + warps - 1) / warps;
   if (share < kKv4MinPairs) share = kKv4MinPairs;
   const int c0 = int(blockIdx.x) * NW * share;           // the CTA's first pair (total + 152 NW pairs fit an int)
   const int c1 = c0 + NW * share < total ? c0 + NW * share : total;
-  float* part0 = a.part + int64_t(blockIdx.x) * 2 * Cfg::kPart;
+  float* part0 = CL ? reinterpret_cast<float*>(sm + Cfg::kAcc) : a.part + int64_t(blockIdx.x) * 2 * Cfg::kPart;
   int* header = reinterpret_cast<int*>(part0 + 2 * Cfg::kPart - 4);   // of slot 1
-  if (t == 0) header[0] = -1;
+  if (!CL && t == 0) header[0] = -1;
   asm volatile("griddepcontrol.launch_dependents;");
-  // the entries without a position: zeros, or NaN where they cannot be read
-  for (int e = blockIdx.x; e < n; e += gridDim.x)
-    if (entry[e].y == 0)
-      for (int x = t; x < c.n_kv * G * HD; x += Cfg::kThreads)
-        a.out[int64_t(e) * a.out_stride + x] = entry[e].x < 0 ? NAN : 0.f;
-  if (c0 >= total) return;   // the whole CTA
+  if constexpr (CL) {
+    if (total == 0) {   // no position: zeros, or NaN where the entry cannot be read
+      if (blockIdx.x == 0)
+        for (int x = t; x < G * HD; x += Cfg::kThreads)
+          a.out[int64_t(e_own) * a.out_stride + int64_t(g_own) * G * HD + x] = ent(0).x < 0 ? NAN : 0.f;
+      return;           // the whole cluster
+    }
+  } else {
+    for (int e = blockIdx.x; e < n; e += gridDim.x)
+      if (entry[e].y == 0)
+        for (int x = t; x < c.n_kv * G * HD; x += Cfg::kThreads)
+          a.out[int64_t(e) * a.out_stride + x] = entry[e].x < 0 ? NAN : 0.f;
+    if (c0 >= total) return;   // the whole CTA
+  }
 
   const int w0 = c0 + warp * share;
   const int count = w0 >= c1 ? 0 : (w0 + share > c1 ? c1 - w0 : share);
@@ -323,6 +346,10 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
 
   // the item of unit y of the share-out: entry e, kv head g, pair pi of np (below 0: the item's cost, nothing to read)
   auto locate = [&](int y, int& e, int& g, int& pi, int& np) {
+    if constexpr (CL) {
+      e = e_own; g = g_own; pi = y; np = total;
+      return;
+    }
     e = kv4_find(prefix, n, y);
     np = kv4_pairs(entry[e].y);
     const int r = y - prefix[e], units = np + kKv4ItemPairs;
@@ -336,8 +363,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     int e, g, pi, np;
     locate(w0 + x, e, g, pi, np);
     if (pi < 0) return make_int2(-3, -3);
-    const int len = entry[e].y;
-    const int32_t* row = c.table + int64_t(entry[e].x) * c.max_pages;
+    const int len = ent(e).y;
+    const int32_t* row = c.table + int64_t(ent(e).x) * c.max_pages;
     auto chunk = [&](int ci) -> int {
       if (ci * kKv4Chunk >= len) return -2;   // (len is at most 2^31 - 256)
       const int page = row[unsigned(ci) / unsigned(cpp)];
@@ -406,7 +433,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     if (k == count) break;
     // ---- a segment: consecutive pairs of one item
     const int seg = np - pi0 < count - k ? np - pi0 : count - k;
-    int live = entry[e].y - pi0 * 2 * kKv4Chunk;   // positions from the pair on that exist
+    int live = ent(e).y - pi0 * 2 * kKv4Chunk;   // positions from the pair on that exist
     bool poison = false;
     {
       // q of heads gi (and gi + 8; N4: gi % 4), scaled so that a head's largest element is in [2^10, 2^11), split
@@ -773,6 +800,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   }
 
   // ---- merge within the CTA: a warp per head, a lane per slot; an item's slots in order
+  if (CL && total <= share) return;   // one warp has done it all (the whole cluster knows)
   __syncthreads();
   constexpr int V = HD / 32;
   const int mine = lane < 2 * NW ? slot_item[lane] : -1;
@@ -787,10 +815,10 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     if (mine == item) order[__popc(members & ((1u << lane) - 1u))] = lane;
     __syncwarp();
     const int nth = order[lane < nm ? lane : 0];   // lane i: the item's i-th slot
-    const int ie = item / c.n_kv, ig = item % c.n_kv, ip = kv4_pairs(entry[ie].y);
-    const int first = prefix[ie] + ig * (ip + kKv4ItemPairs) + kKv4ItemPairs;
+    const int ie = item / c.n_kv, ig = item % c.n_kv, ip = kv4_pairs(ent(ie).y);
+    const int first = CL ? 0 : prefix[ie] + ig * (ip + kKv4ItemPairs) + kKv4ItemPairs;
     const bool whole = first >= c0 && first + ip <= c1;
-    float* part = part0 + (first < c0 ? 0 : Cfg::kPart);
+    float* part = CL || first < c0 ? part0 : part0 + Cfg::kPart;
     float* to = whole ? a.out + int64_t(ie) * a.out_stride + int64_t(ig) * G * HD : part;
     for (int h = turn; h < G; h += NW) {
       float2 ml = make_float2(-INFINITY, 0.f);
@@ -827,10 +855,50 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
       else *reinterpret_cast<float2*>(to + h * HD + V * lane) = make_float2(o[0], o[1]);
       if (!whole && lane == 0) reinterpret_cast<float2*>(part + ROWS * HD)[h] = make_float2(M, sum);
     }
-    if (!whole && first >= c0 && t == 0) {   // begun here: k_kv4_attn_merge collects it from here
+    if (!CL && !whole && first >= c0 && t == 0) {   // begun here: k_kv4_attn_merge collects it from here
       header[1] = (first + ip - 1) / (NW * share) - int(blockIdx.x) + 1;
       header[0] = item;
     }
+  }
+
+  // ---- CL: merge across the cluster, a warp per head
+  if constexpr (CL) {
+    if (total <= NW * share) return;   // the first CTA has had it all, and written it (the whole cluster knows)
+    namespace cg = cooperative_groups;
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    const int ranks = (total + NW * share - 1) / (NW * share);   // CTAs that had pairs
+    for (int h = int(blockIdx.x) * NW + warp; h < G; h += int(gridDim.x) * NW) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < ranks) ml = reinterpret_cast<const float2*>(cl.map_shared_rank(part0, unsigned(lane)) + ROWS * HD)[h];
+      float M = ml.x;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      float f = lane < ranks ? kv4_ex2(ml.x - M) : 0.f, sum = ml.y * f;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      f /= sum;
+      float o[V];
+#pragma unroll
+      for (int v = 0; v < V; v++) o[v] = 0.f;
+#pragma unroll 4
+      for (int b = 0; b < ranks; b++) {
+        const float fb = __shfl_sync(0xffffffffu, f, b);
+        const float* r = cl.map_shared_rank(part0, unsigned(b)) + h * HD + V * lane;
+        if (V == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(r);
+          o[0] = fmaf(x.x, fb, o[0]); o[1] = fmaf(x.y, fb, o[1]);
+          o[2 % V] = fmaf(x.z, fb, o[2 % V]); o[3 % V] = fmaf(x.w, fb, o[3 % V]);
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(r);
+          o[0] = fmaf(x.x, fb, o[0]); o[1] = fmaf(x.y, fb, o[1]);
+        }
+      }
+      float* to = a.out + int64_t(e_own) * a.out_stride + (int64_t(g_own) * G + h) * HD + V * lane;
+      if (V == 4) *reinterpret_cast<float4*>(to) = make_float4(o[0], o[1], o[2 % V], o[3 % V]);
+      else *reinterpret_cast<float2*>(to) = make_float2(o[0], o[1]);
+    }
+    cl.sync();   // the partial results stay until every CTA has read them
   }
 }
 
@@ -903,29 +971,83 @@ __global__ void __launch_bounds__(32 * kKv4MergeWarps) k_kv4_attn_merge(Kv4 c, K
   }
 }
 
+// CTAs of a cluster, and how many such clusters of the attention kernel the GPU
+// holds at once (0: none).
+constexpr int kKv4Clusters[6] = {1, 2, 4, 8, 12, 16};
+struct Kv4Fit {
+  KernelSetup setup;
+  int clusters[6] = {0, 0, 0, 0, 0, 0};
+};
+static void kv4_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], dim3 grid, int threads, size_t smem,
+                       cudaStream_t s, int cluster) {
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg = cudaLaunchConfig_t{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+}
 template <int HD, int HB>
-static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_pairs, cudaStream_t s) {
+static Kv4Fit kv4_fit() {
   using Cfg = Kv4AttnCfg<HD, HB>;
-  static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, HB>, Cfg::kSmem);
+  Kv4Fit f;
+  f.setup = kernel_setup(k_kv4_attn<HD, HB, true>, Cfg::kSmem);
+  if (f.setup.err == cudaSuccess)
+    f.setup.err = cudaFuncSetAttribute(k_kv4_attn<HD, HB, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int i = 0; i < 6 && f.setup.err == cudaSuccess; i++) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    kv4_config(cfg, attr, dim3(unsigned(kKv4Clusters[i])), Cfg::kThreads, Cfg::kSmem, nullptr, kKv4Clusters[i]);
+    cfg.numAttrs = 1;
+    attr[0] = attr[1];
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_kv4_attn<HD, HB, true>, &cfg) == cudaSuccess) f.clusters[i] = n;
+    else cudaGetLastError();   // (no such cluster: it is not taken)
+  }
+  return f;
+}
+
+// Most pairs of a warp in the form with a cluster per item.  (us, that form with up to 2
+// pairs, with up to 3, and the other: 1 sequence of 4161 positions, 64/8 heads: 10.0,
+// 10.0, 10.4; of 600: 8.4, 8.4, 9.9; 16 of 300, 32/8: 6.9, 6.9, 11.0; 1 of 9000, 16/1: 11.7, 15.0, 11.7.)
+constexpr int kKv4ClusterShare = 2;
+
+template <int HD, int HB>
+static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_units, cudaStream_t s) {
+  using Cfg = Kv4AttnCfg<HD, HB>;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  // A cluster per item where all of them fit the GPU at once and their capacity leaves no warp more than kKv4ClusterShare
+  // pairs: the smallest such that a warp has one pair at most, or the largest.
+  static const Kv4Fit fit = kv4_fit<HD, HB>();
+  if (fit.setup.err != cudaSuccess) return fit.setup.err;
+  const int64_t items = int64_t(a.n) * k.n_kv, pairs = (int64_t(k.max_pages) * k.page_len + 31) / 32;
+  int cluster = 0;
+  for (int i = 0; i < 6; i++) {
+    if (fit.clusters[i] < items || pairs > int64_t(kKv4Clusters[i]) * Cfg::NW * kKv4ClusterShare) continue;
+    cluster = kKv4Clusters[i];
+    if (pairs <= int64_t(cluster) * Cfg::NW) break;
+  }
+  if (cluster) {
+    kv4_config(cfg, attr, dim3(unsigned(cluster), unsigned(items)), Cfg::kThreads, Cfg::kSmem, s, cluster);
+    return cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB, true>, k, a);
+  }
+  static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, HB, false>, Cfg::kSmem);
   if (setup.err != cudaSuccess) return setup.err;
-  const int64_t useful = (most_pairs + Cfg::NW * kKv4MinPairs - 1) / (Cfg::NW * kKv4MinPairs);
+  const int64_t useful = (most_units + Cfg::NW * kKv4MinPairs - 1) / (Cfg::NW * kKv4MinPairs);
   int64_t ctas = setup.sms < kKv4AttnMaxCtas ? setup.sms : kKv4AttnMaxCtas;
   if (ctas > useful) ctas = useful;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(Cfg::kThreads);
-  cfg.dynamicSmemBytes = Cfg::kSmem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB>, k, a);
+  kv4_config(cfg, attr, dim3(unsigned(ctas)), Cfg::kThreads, Cfg::kSmem, s, 0);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB, false>, k, a);
   if (e != cudaSuccess || ctas < 2) return e;
-  cfg.gridDim = dim3(unsigned(ctas - 1), unsigned(a.G));   // the last CTA's items end with it
-  cfg.blockDim = dim3(32 * kKv4MergeWarps);
-  cfg.dynamicSmemBytes = 0;
+  // (the last CTA's items end with it)
+  kv4_config(cfg, attr, dim3(unsigned(ctas - 1), unsigned(a.G)), 32 * kKv4MergeWarps, 0, s, 0);
   return cudaLaunchKernelEx(&cfg, k_kv4_attn_merge<HD>, k, a, int(Cfg::kPart), int(Cfg::kRows));
 }
 
