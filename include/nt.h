@@ -462,7 +462,7 @@ nt_status nt_kv4_fork(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, 
  * entry (keep outside [0, len], a sequence listed before) is passed over. */
 nt_status nt_kv4_free(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_keep, void* stream);
 
-/* Page dev_dst[i] becomes a copy of page dev_src[i] in every layer (n <= n_pages);
+/* Page dev_dst[i] becomes a copy of page dev_src[i] in every layer (n <= n_pages and 2^20);
  * tables and counts stay.  A pair is passed over (NT_KV4_BAD_PAGE) where a page is out of
  * range, its destination is one of an earlier pair, or its source is the
  * destination of another. */
@@ -487,7 +487,7 @@ nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t*
  * starts at element r * row_stride + g * head_stride of dev_k and of dev_v (f32 or f16 by
  * `type`: NT_F32, NT_F16; both strides multiples of 16 bytes), head_dim elements
  * each: a projection's [row][kv head][dim] as well as an f16 cache's [kv
- * head][position][dim].  An entry is passed over where its sequence is out of
+ * head][position][dim].  n_rows / 16 + 2 n is at most 2^26.  An entry is passed over where its sequence is out of
  * range, it has more rows than the sequence positions or rows outside [0, n_rows);
  * rows are where their page is out of range or not held by this sequence alone
  * (refs other than 1).
@@ -513,6 +513,8 @@ nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int
  * The statistics and sums are fp32; K and V enter exactly, q and the softmax
  * weights with about 22 bits.  A sequence out of range, a length that the table
  * cannot hold and a page index out of range give NaN in that sequence's outputs.
+ * n at most 65536, n_kv_heads * max_pages * page_len at most 2^34 and a layer of the pool
+ * at most 2^31 - 1 chunks.
  * NT_E_UNSUPPORTED: n_heads / n_kv_heads other than 1, 2, 4, 8 or 16. */
 nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
                            const float* dev_q, int64_t q_stride, float* dev_out, int64_t out_stride,

@@ -284,7 +284,7 @@ __device__ __noinline__ uint32_t kv4_codes_exactly(float x0, float x1, float x2,
 
 constexpr int kKv4RowWarps = 4;   // warps of a CTA: each K or V of a (unit, kv head)
 
-// NG words to (from) consecutive addresses
+// NG words from consecutive addresses
 template <int NG>
 __device__ __forceinline__ void kv4_get(const void* p, uint32_t (&w)[NG]) {
   if (NG == 4) {
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(256) k_kv4_free(Kv4 c, int n, const int32_t* s
 }
 
 // A CTA's pieces belong to few pairs: those are checked first.
-constexpr int kKv4CopyPairs = 8192;   // most pairs of a CTA
+constexpr int kKv4CopyPairs = 8192;   // most pairs of a CTA: 2^20 pairs over at least 130
 __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_copy_pages(Kv4 c, int n, const int32_t* src, const int32_t* dst,
                                                                     Kv4Pieces ps) {
   __shared__ uint32_t s_bad[kKv4CopyPairs / 32];
@@ -918,10 +918,11 @@ static nt_status kv4_plan_apply(const char* who, const Kv4& k, Kv4PlanArgs a, vo
   return NT_OK;
 }
 
-// Units of a call (see kv4_span; 0: n or n_rows is out of range).
+// Units of a call (see kv4_span), at most 2^26, so that positions counted from units
+// fit 31 bits (0: n or n_rows is out of range).
 static int32_t kv4_units(int32_t n, int32_t n_rows, const int32_t* begin) {
-  const int64_t u = begin ? int64_t(n_rows) / kKv4Chunk + 2 * int64_t(n) + 1 : n;
-  return n < 0 || n_rows < 0 || u > 0x7fffffff ? 0 : int32_t(begin ? u : (u < n_rows ? u : n_rows));
+  const int64_t u = begin ? int64_t(n_rows) / kKv4Chunk + 2 * int64_t(n) + 1 : (n < n_rows ? n : n_rows);
+  return n < 0 || n_rows < 0 || u > (1 << 26) ? 0 : int32_t(u);
 }
 
 static nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a, nt_qtype type, const void* pk, const void* pv) {
@@ -930,7 +931,7 @@ static nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a,
   if (a.layer < 0 || a.layer >= k.n_layers) return bad("layer out of range");
   if (a.n < 0 || (!a.seq && a.n > k.max_seqs)) return bad("n out of range");
   if (a.n_rows < 0) return bad("n_rows must not be negative");
-  if (int64_t(a.units) * k.n_kv > (int64_t(1) << 32) || (a.n && a.n_rows && !a.units)) return bad("too many rows");
+  if (int64_t(a.units) * k.n_kv > (int64_t(1) << 32) || (a.n && a.n_rows && !a.units)) return bad("n_rows / 16 + 2 n above 2^26");
   const int64_t es = type == NT_F32 ? 4 : 2, most = int64_t(1) << 40;
   if (a.row_stride < 0 || a.head_stride < 0 || a.row_stride > most || a.head_stride > most || a.row_stride * es % 16 ||
       a.head_stride * es % 16)
@@ -1032,14 +1033,15 @@ nt_status nt_kv4_copy_pages(const nt_kv4_cache* c, int32_t n, const int32_t* dev
                             void* stream) {
   Kv4 k;
   nt_status st = kv4_check(c, "nt_kv4_copy_pages", true, &k);
-  if (!st) st = kv4_list_check(k, "nt_kv4_copy_pages", n, k.n_pages);
+  if (!st) st = kv4_list_check(k, "nt_kv4_copy_pages", n, k.n_pages < (1 << 20) ? k.n_pages : 1 << 20);
   if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_src, n, false, nullptr, 0);
   if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_dst, n, false, nullptr, 0);
   if (st || n == 0) return st;
   static const KernelSetup setup = kernel_setup(k_kv4_copy_pages, Kv4CopyShared::kSize);
+  if (setup.err == cudaSuccess && (int64_t(n) + setup.sms - 1) / setup.sms + 2 > kKv4CopyPairs)
+    return fail(NT_E_UNSUPPORTED, "nt_kv4_copy_pages: too many pairs for this GPU");
   const Kv4Pieces ps = kv4_pieces(k, n);
   const int64_t pieces = int64_t(n) * k.n_layers * ps.count;
-  if (n / setup.sms >= kKv4CopyPairs - 2) return fail(NT_E_INVAL, "nt_kv4_copy_pages: more pairs than one call takes");
   NT_CUDA(kv4_launch_copy(setup, k_kv4_copy_pages, pieces, static_cast<cudaStream_t>(stream), k, n, dev_src, dev_dst, ps));
   return NT_OK;
 }

@@ -10,9 +10,7 @@ namespace nt {
 constexpr int kKv4Chunk = 16;          // positions of a chunk
 constexpr int kKv4MaxSeqs = 65536;     // bits of the shared-memory sets of listed sequences (8 KB each)
 
-// Bytes of the parts of one chunk of HD dimensions.
-__host__ __device__ constexpr int kv4_code_bytes(int hd) { return 8 * hd; }         // K or V codes
-__host__ __device__ constexpr int kv4_scale_bytes(int hd) { return hd; }            // K or V scales: 16 hd/32 f16
+// Bytes of one chunk of hd dimensions: 8 hd of codes and hd of scales (16 hd / 32 f16) for K and for V.
 __host__ __device__ constexpr int kv4_chunk_bytes(int hd) { return 18 * hd; }
 
 // The cache as kernels see it.

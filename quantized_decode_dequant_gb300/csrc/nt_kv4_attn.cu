@@ -1097,7 +1097,7 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
   const int64_t entry_pairs = int64_t(k.n_kv) * ((int64_t(k.max_pages) * k.page_len + 31) / 32 + kKv4ItemPairs);
   // a launch's pairs are counted in 32 bits
   const int64_t most = int64_t(1) << 30;
-  if (entry_pairs > most) return bad("n_kv_heads * max_pages * page_len above 2^35");
+  if (entry_pairs > most) return bad("n_kv_heads * max_pages * page_len is too large");
   const int32_t batch = entry_pairs * kKv4Batch <= most ? kKv4Batch : int32_t(most / entry_pairs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (int32_t i = 0; i < n; i += batch) {

@@ -147,6 +147,7 @@ ROWS, LISTS = ["append", "read"], ["extend", "fork", "free", "copy_pages"]
     (["append", "read", "attention"], dict(layer=-1)), (["append", "read", "attention"], dict(layer=2)),
     (ROWS, dict(rows=-1)), (ROWS, dict(type="q8_0")), (ROWS, dict(k=0)), (ROWS, dict(v=O + 8)), (ROWS, dict(rs=130)),
     (ROWS, dict(hs=-64)), (ROWS, dict(rs=132, type="f16")), (ROWS, dict(k=GOOD["pool"])), (ROWS, dict(rs=1 << 50)),
+    (ROWS, dict(rows=(1 << 31) - 1, rs=0)), (ROWS, dict(rows=(1 << 30) + 16, rs=0)),
     (["read"], dict(v=Q)), (["read"], dict(rs=64)), (["read"], dict(hs=32)), (["read"], dict(hs=0)), (["read"], dict(rs=0)),
     (["read"], dict(v=Q + 256, rs=128)), (["read"], dict(seq=Q + 64)), (["read"], dict(count=O)),
     (["attention"], dict(heads=3)), (["attention"], dict(heads=0)), (["attention"], dict(qs=508)),
