@@ -88,8 +88,8 @@ __device__ __forceinline__ void kv4_flag(const Kv4& k, uint32_t bits) { atomicOr
 
 // ---- bulk copies into shared memory, counted on mbarriers of one arrival
 __device__ __forceinline__ uint32_t kv4_smem(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ void kv4_bar_init(uint32_t bar) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+__device__ __forceinline__ void kv4_bar_init(uint32_t bar, uint32_t arrivals = 1) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(arrivals) : "memory");
 }
 __device__ __forceinline__ void kv4_bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");

@@ -25,19 +25,19 @@
 // columns of B, hi of 4 heads and lo of 4 heads side by side, and the weights are
 // transposed in registers (movmatrix) to be B of the outputs: half the products.
 //
-// What bounds it: a byte of cache is 1.8 values, and a value costs about 2.3
-// instructions of a lane, so at 6.8 TB/s the SMs' issue slots are about 3/4 busy:
-// near the memory bound, with the arithmetic close behind.  (tcgen05 would need
-// the decoded f16 values, four times the bytes, written to shared memory first;
-// mma.sync takes them from registers, and at 16 rows its rate is not the limit.)
+// What bounds it.  A byte of cache is 1.8 values; 8 values cost a lane 7 shifts and logic ops, 5 half2 ops and a sixteenth
+// of a matrix product or more, and on this GPU mma.sync m16n8k16 (8 cycles of a sub-core) and the half2 ops (2) do
+// not overlap.  With 4 heads that is just behind the memory: 56 sequences of up to 9001 positions of 8 kv heads
+// (293 MB) take 65.1 us, 4.5 TB/s in all and 5.9 while data flows.  With 8 heads the products are twice as many
+// and decide (43.6 us for 131077 positions where memory wants 22.3), so long work of 8 and 16 heads of
+// 128 dimensions goes to the tcgen05 kernel of nt_kv4_attn_tc.cu (38.9 us).  Short work keeps to this kernel's cluster
+// form: its warps go about alone, and there a first result counts, not a rate.
 #include <cooperative_groups.h>
 
-#include "nt_kv4.cuh"
+#include "nt_kv4_attn.cuh"
 
 namespace nt {
 
-constexpr int kKv4Batch = 1024;        // sequences of one launch: their pair offsets are kept in shared memory
-constexpr int kKv4AttnMaxCtas = 152;   // one CTA per SM; the workspace holds two partial results of each
 constexpr int kKv4MinPairs = 1;        // fewest pairs of chunks of a warp: below, fewer CTAs work
 // An item's start and end cost a warp about as much as a pair (q to split, sums to
 // reduce, results to store): the share-out counts it as so many pairs more, in
@@ -45,23 +45,6 @@ constexpr int kKv4MinPairs = 1;        // fewest pairs of chunks of a warp: belo
 // positions 80.0, 81.0, 79.2, 78.6 us; 64 of up to 200: 18.2, 15.5, 13.8, 13.6; 8 of up
 // to 1500: 10.7, 10.6, 12.4, 12.7.)
 constexpr int kKv4ItemPairs = 2;
-
-struct Kv4AttnArgs {
-  int32_t layer, n, G;
-  int32_t seq0;                        // sequence of entry 0 where none are listed
-  const int32_t* seq;
-  const float* q;
-  int64_t q_stride;
-  float* out;
-  int64_t out_stride;
-  float scale_log2;                    // log2(e) / sqrt(hd)
-  float* part;                         // [CTA][2] partial results
-};
-
-// Partial result of one item: o [rows][HD], then (reference m, sum l) per row, then
-// a header of 4 words (used by the CTAs' slot 1: the item, -1 none, and the
-// number of CTAs that worked on it).
-__host__ __device__ constexpr int kv4_part_floats(int hd, int rows) { return rows * hd + 2 * rows + 4; }
 
 // HB: query heads of a kv head that the instantiation is made for, up to 4, 8 or 16.
 template <int HD, int HB>
@@ -91,77 +74,6 @@ size_t kv4_attn_ws_bytes(int n_heads, int n_kv, int hd) {
   return size_t(kKv4AttnMaxCtas) * 2 * size_t(kv4_part_floats(hd, n_heads / n_kv > 8 ? 16 : (n_heads / n_kv > 4 ? 8 : 4))) * 4;
 }
 
-// ------------------------------------------------------------ small pieces --
-
-__device__ __forceinline__ float kv4_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint4 kv4_lds16(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 kv4_lds8(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint32_t kv4_lds4(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-// NG consecutive words
-template <int NG>
-__device__ __forceinline__ void kv4_words(uint32_t a, uint32_t (&w)[NG]) {
-  if (NG == 4) {
-    const uint4 v = kv4_lds16(a);
-    w[0] = v.x; w[1] = v.y; w[2 % NG] = v.z; w[3 % NG] = v.w;
-  } else {
-    const uint2 v = kv4_lds8(a);
-    w[0] = v.x; w[1] = v.y;
-  }
-}
-__device__ __forceinline__ uint32_t kv4_h2fma(uint32_t a, uint32_t b, uint32_t c) {
-  uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-  return d;
-}
-__device__ __forceinline__ uint32_t kv4_h2mul(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// (w & mask) | magic
-template <uint32_t mask>
-__device__ __forceinline__ uint32_t kv4_pick(uint32_t w, uint32_t magic) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "n"(mask), "r"(magic));
-  return d;
-}
-// The four half2 of a word: value pairs (code k, code k + 4), k = 0..3, times the
-// scale pair d; d72 = -72 d.  (Two of the shifts can be saved by taking codes 0 and
-// 2 as 1024 + q, less 1032, times d: measured 4% slower at 131077 positions, the
-// half2 and matrix instructions being what is short, not the shifts.)
-__device__ __forceinline__ void kv4_decode(uint32_t w, uint32_t d, uint32_t d72, uint32_t (&b)[4]) {
-  constexpr uint32_t k64 = 0x54005400u;
-  b[0] = kv4_h2fma(kv4_pick<0x00f000f0u>(w << 4, k64), d, d72);
-  b[1] = kv4_h2fma(kv4_pick<0x00f000f0u>(w, k64), d, d72);
-  b[2] = kv4_h2fma(kv4_pick<0x00f000f0u>(w >> 4, k64), d, d72);
-  b[3] = kv4_h2fma(kv4_pick<0x00f000f0u>(w >> 8, k64), d, d72);
-}
-constexpr uint32_t kMinus72 = 0xd480d480u;   // f16 -72 twice
-
-// hi and lo f16 terms of two fp32 values
-__device__ __forceinline__ void kv4_split(float x0, float x1, uint32_t& hi, uint32_t& lo) {
-  const __half2 h = __floats2half2_rn(x0, x1);
-  const float2 f = __half22float2(h);
-  const __half2 l = __floats2half2_rn(x0 - f.x, x1 - f.y);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
-}
 __device__ __forceinline__ void kv4_mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -177,26 +89,7 @@ __device__ __forceinline__ uint32_t kv4_transpose(uint32_t a) {
   return d;
 }
 
-// Sequence and length of listed entry e (length 0 and *bad where it cannot be read).
-__device__ __forceinline__ int2 kv4_entry(const Kv4& c, const Kv4AttnArgs& a, int e, uint32_t* bad) {
-  const int s = a.seq ? a.seq[e] : a.seq0 + e;
-  *bad = NT_KV4_BAD_SEQ;
-  if (s < 0 || s >= c.max_seqs) return make_int2(-1, 0);
-  const int n = c.len[s];
-  *bad = n < 0 || n > c.capacity() ? NT_KV4_BAD_LEN : 0;
-  return make_int2(*bad ? -1 : s, *bad ? 0 : n);
-}
 __device__ __forceinline__ int kv4_pairs(int len) { return (len + 2 * kKv4Chunk - 1) / (2 * kKv4Chunk); }
-
-// Entry of prefix (ascending, prefix[0] = 0) that holds chunk x: prefix[i] <= x < prefix[i + 1].
-__device__ __forceinline__ int kv4_find(const int* prefix, int n, int x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid] <= x) lo = mid; else hi = mid;
-  }
-  return lo;
-}
 
 // ------------------------------------------------------------ the kernel --
 
@@ -241,75 +134,14 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // ---- unit offsets of the entries (CL: the item's entry alone)
-  constexpr int kFew = 128;
   if constexpr (CL) {
     uint32_t bad;
     const int2 sl = kv4_entry(c, a, int(blockIdx.y) / c.n_kv, &bad);
     if (bad && t == 0) kv4_flag(c, bad);
     if (t == 0) { entry[0] = sl; prefix[0] = 0; prefix[1] = kv4_pairs(sl.y); }
     __syncthreads();
-  } else if (n <= kFew) {   // every warp for itself, all to the same places: no barrier
-    int2 sl[kFew / 32];
-#pragma unroll
-    for (int i = 0; i < kFew / 32; i++) {
-      const int e = 32 * i + lane;
-      uint32_t bad = 0;
-      sl[i] = make_int2(-1, 0);
-      if (e < n) sl[i] = kv4_entry(c, a, e, &bad);
-      if (bad && blockIdx.x == 0 && warp == 0) kv4_flag(c, bad);
-    }
-    int run = 0;
-#pragma unroll
-    for (int i = 0; i < kFew / 32; i++) {
-      if (32 * i >= n) break;
-      const int e = 32 * i + lane, mine = sl[i].y ? (kv4_pairs(sl[i].y) + kKv4ItemPairs) * c.n_kv : 0;
-      int x = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (e < n) {
-        entry[e] = sl[i];
-        prefix[e] = run + x - mine;
-      }
-      run += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) prefix[n] = run;
-    __syncwarp();
   } else {
-    int* sums = reinterpret_cast<int*>(sm + Cfg::kSlots);   // per-warp sums, before the slots are used
-    int run = 0;
-    for (int e0 = 0; e0 < n; e0 += Cfg::kThreads) {
-      const int e = e0 + t;
-      int mine = 0;
-      if (e < n) {
-        uint32_t bad;
-        const int2 sl = kv4_entry(c, a, e, &bad);
-        if (bad && blockIdx.x == 0) kv4_flag(c, bad);
-        entry[e] = sl;
-        mine = sl.y ? (kv4_pairs(sl.y) + kKv4ItemPairs) * c.n_kv : 0;
-      }
-      int x = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) sums[warp] = x;
-      __syncthreads();
-      int before = 0, all = 0;
-      for (int w = 0; w < NW && e0 + 32 * w < n; w++) {
-        const int y = sums[w];
-        if (w < warp) before += y;
-        all += y;
-      }
-      if (e < n) prefix[e] = run + before + x - mine;
-      run += all;
-      __syncthreads();
-    }
-    if (t == 0) prefix[n] = run;
-    __syncthreads();
+    kv4_count<NW>(c, a, 2 * kKv4Chunk, kKv4ItemPairs, prefix, entry, reinterpret_cast<int*>(sm + Cfg::kSlots));
   }
   const int e_own = CL ? int(blockIdx.y) / c.n_kv : 0, g_own = CL ? int(blockIdx.y) % c.n_kv : 0;
   auto ent = [&](int e) { return entry[CL ? 0 : e]; };   // sequence and length of entry e
@@ -330,10 +162,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
       return;           // the whole cluster
     }
   } else {
-    for (int e = blockIdx.x; e < n; e += gridDim.x)
-      if (entry[e].y == 0)
-        for (int x = t; x < c.n_kv * G * HD; x += Cfg::kThreads)
-          a.out[int64_t(e) * a.out_stride + x] = entry[e].x < 0 ? NAN : 0.f;
+    kv4_empty_entries(c, a, entry, HD);
     if (c0 >= total) return;   // the whole CTA
   }
 
@@ -597,8 +426,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
             if (at(i) >= live) x[m][i] = -INFINITY;
       }
       // ---- weights p = 2^(s - mref).  Only where a lane's sum passes 2^15 (at first it is infinite) is the maximum looked
-      // for; where that passes mref by 14, it less 6 becomes mref.  So weights stay below 2^15, within f16, and the largest
-      // so far is at least 2^6: the lo terms of all that matter are ordinary f16 numbers.
+      // for; where that passes mref by 12, as one of 8 weights does then, it less 6 becomes mref.  So weights stay within
+      // f16, and the largest so far is at least 2^6: the lo terms of all that matter are ordinary f16 numbers.
       float p[NH][NX], sum[NH];
       auto weights = [&]() {
 #pragma unroll
@@ -620,7 +449,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
           top *= cs[m];
 #pragma unroll
           for (int o = N4 ? 4 : 1; o <= (N4 ? 16 : 2); o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float to = top > mref[m] + 14.f ? top - 6.f : mref[m];
+          const float to = top > mref[m] + 12.f ? top - 6.f : mref[m];
           f[m] = kv4_ex2(mref[m] - to);
           mref[m] = to;
           l[m] *= f[m];
@@ -803,63 +632,14 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   if (CL && total <= share) return;   // one warp has done it all (the whole cluster knows)
   __syncthreads();
   constexpr int V = HD / 32;
-  const int mine = lane < 2 * NW ? slot_item[lane] : -1;
-  int* order = reinterpret_cast<int*>(sm + Cfg::kLane) + warp * 64;
-  int turn = warp;   // (item, head) pairs go round the warps
-  for (uint32_t left = __ballot_sync(0xffffffffu, mine >= 0); left; turn = (turn + NW * G - G) % NW) {
-    const int a0 = __ffs(left) - 1, item = __shfl_sync(0xffffffffu, mine, a0);
-    const uint32_t members = __ballot_sync(0xffffffffu, mine == item);
-    left &= ~members;
-    const int nm = __popc(members);
-    __syncwarp();
-    if (mine == item) order[__popc(members & ((1u << lane) - 1u))] = lane;
-    __syncwarp();
-    const int nth = order[lane < nm ? lane : 0];   // lane i: the item's i-th slot
-    const int ie = item / c.n_kv, ig = item % c.n_kv, ip = kv4_pairs(ent(ie).y);
-    const int first = CL ? 0 : prefix[ie] + ig * (ip + kKv4ItemPairs) + kKv4ItemPairs;
-    const bool whole = first >= c0 && first + ip <= c1;
-    float* part = CL || first < c0 ? part0 : part0 + Cfg::kPart;
-    float* to = whole ? a.out + int64_t(ie) * a.out_stride + int64_t(ig) * G * HD : part;
-    for (int h = turn; h < G; h += NW) {
-      float2 ml = make_float2(-INFINITY, 0.f);
-      if (lane < nm) ml = reinterpret_cast<const float2*>(slot_ptr(nth) + ROWS * HD)[h];
-      float M = ml.x;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      float f = lane < nm ? kv4_ex2(ml.x - M) : 0.f, sum = ml.y * f;
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (whole) f /= sum;
-      float o[V];
-#pragma unroll
-      for (int v = 0; v < V; v++) o[v] = 0.f;
-#pragma unroll 1
-      for (int i = 0; i < nm; i += 4) {
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const int w = __shfl_sync(0xffffffffu, nth, i + u);
-          const float fw = __shfl_sync(0xffffffffu, f, i + u);
-          const float* r = slot_ptr(w) + h * HD + V * lane;
-          if (i + u >= nm) continue;
-          if (V == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(r);
-            o[0] = fmaf(x.x, fw, o[0]); o[1] = fmaf(x.y, fw, o[1]);
-            o[2 % V] = fmaf(x.z, fw, o[2 % V]); o[3 % V] = fmaf(x.w, fw, o[3 % V]);
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(r);
-            o[0] = fmaf(x.x, fw, o[0]); o[1] = fmaf(x.y, fw, o[1]);
-          }
-        }
-      }
-      if (V == 4) *reinterpret_cast<float4*>(to + h * HD + V * lane) = make_float4(o[0], o[1], o[2 % V], o[3 % V]);
-      else *reinterpret_cast<float2*>(to + h * HD + V * lane) = make_float2(o[0], o[1]);
-      if (!whole && lane == 0) reinterpret_cast<float2*>(part + ROWS * HD)[h] = make_float2(M, sum);
-    }
-    if (!CL && !whole && first >= c0 && t == 0) {   // begun here: k_kv4_attn_merge collects it from here
-      header[1] = (first + ip - 1) / (NW * share) - int(blockIdx.x) + 1;
-      header[0] = item;
-    }
-  }
+  kv4_merge<HD, ROWS, NW, 2 * NW>(
+      c, a, slot_item, slot_ptr, reinterpret_cast<int*>(sm + Cfg::kLane) + warp * 64,
+      [&](int item, int& first, int& units) {
+        const int ie = item / c.n_kv;
+        units = kv4_pairs(ent(ie).y);
+        first = CL ? 0 : prefix[ie] + item % c.n_kv * (units + kKv4ItemPairs) + kKv4ItemPairs;
+      },
+      c0, c1, NW * share, part0, CL ? nullptr : header);
 
   // ---- CL: merge across the cluster, a warp per head
   if constexpr (CL) {
@@ -1038,13 +818,19 @@ static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_uni
     kv4_config(cfg, attr, dim3(unsigned(cluster), unsigned(items)), Cfg::kThreads, Cfg::kSmem, s, cluster);
     return cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB, true>, k, a);
   }
-  static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, HB, false>, Cfg::kSmem);
-  if (setup.err != cudaSuccess) return setup.err;
-  const int64_t useful = (most_units + Cfg::NW * kKv4MinPairs - 1) / (Cfg::NW * kKv4MinPairs);
-  int64_t ctas = setup.sms < kKv4AttnMaxCtas ? setup.sms : kKv4AttnMaxCtas;
-  if (ctas > useful) ctas = useful;
-  kv4_config(cfg, attr, dim3(unsigned(ctas)), Cfg::kThreads, Cfg::kSmem, s, 0);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB, false>, k, a);
+  int ctas = 0;
+  cudaError_t e;
+  if constexpr (HD == 128 && HB >= 8) {
+    e = kv4_launch_attn_tc(k, a, s, &ctas);
+  } else {
+    static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, HB, false>, Cfg::kSmem);
+    if (setup.err != cudaSuccess) return setup.err;
+    const int64_t useful = (most_units + Cfg::NW * kKv4MinPairs - 1) / (Cfg::NW * kKv4MinPairs);
+    ctas = setup.sms < kKv4AttnMaxCtas ? setup.sms : kKv4AttnMaxCtas;
+    if (ctas > useful) ctas = int(useful);
+    kv4_config(cfg, attr, dim3(unsigned(ctas)), Cfg::kThreads, Cfg::kSmem, s, 0);
+    e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB, false>, k, a);
+  }
   if (e != cudaSuccess || ctas < 2) return e;
   // (the last CTA's items end with it)
   kv4_config(cfg, attr, dim3(unsigned(ctas - 1), unsigned(a.G)), 32 * kKv4MergeWarps, 0, s, 0);

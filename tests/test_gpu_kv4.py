@@ -527,6 +527,73 @@ def test_attention_of_nan_blocks_and_extreme_inputs(nt):
         assert (err <= b).all(), (lo, hi, qs, float((err / b).max()))
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("page_len", [16, 80, 256])
+def test_attention_where_the_capacity_is_large(nt, hd, G, page_len):
+    """Tables of 16384 positions and more a sequence, so that the work is shared out over the whole GPU: lengths around
+    chunks, tiles and pages; a sequence twice; dead positions of every kind; a head of NaN beside others; bad pages."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([83, hd, G, page_len])
+    lens = [1, 15, 16, 17, 0, 127, 128, 129, 255, 256, 257, 700, 1500]
+    need = sum(-(-n // page_len) for n in lens)
+    ref = R.RefCache(1, 2, hd, page_len, need + 3, len(lens), -(-16384 // page_len))
+    ref.randomize(rng)
+    ref.hold(lens, rng)
+    heads = 2 * G
+    seqs = list(range(len(lens))) + [11, 3]
+    q = rng.standard_normal((len(lens), heads, hd)).astype(np.float32)
+    want = _want(ref, range(len(lens)), q.astype(np.float64), heads)
+    qd = torch.from_numpy(q[seqs]).cuda()
+    dev = Dev(nt, ref, heads)
+    first = dev.attention(qd, seqs).cpu().numpy().reshape(len(seqs), heads, hd)
+    for i, s in enumerate(seqs):
+        err, b = np.abs(first[i] - want[s]).max(axis=1), _bound(ref, s, q[s].astype(np.float64), heads)
+        assert (err <= b).all(), (lens[s], float((err / b).max()))
+    assert int(dev.error.cpu()[0]) == 0
+    np.testing.assert_array_equal(first[[13, 14]].view(np.uint32), dev.attention(qd, seqs).cpu().numpy().reshape(
+        len(seqs), heads, hd)[[13, 14]].view(np.uint32))   # the same again, to the bit
+
+    # dead positions: every scale NaN or infinite, every code 15
+    k = np.arange(hd)
+    for fill in (0xFFFF, 0x7C00):
+        other = R.RefCache(1, 2, hd, page_len, need + 3, len(lens), -(-16384 // page_len))
+        other.pool.view(np.uint16)[:] = fill
+        other.table, other.len, other.refs = ref.table, ref.len, ref.refs
+        for s, n in enumerate(lens):
+            for t in range(n):
+                page, at = int(ref.table[s, t // page_len]), t % page_len
+                for g in range(2):
+                    for code, scale in ((ref._k_code, ref._k_scale), (ref._v_code, ref._v_scale)):
+                        b0 = scale(g, at, np.arange(ref.ng))
+                        for b in [code(g, at, k)[0], b0, b0 + 1]:
+                            other.pool[0, page, b] = ref.pool[0, page, b]
+        got = Dev(nt, other, heads).attention(qd, seqs).cpu().numpy().reshape(len(seqs), heads, hd)
+        np.testing.assert_array_equal(got.view(np.uint32), first.view(np.uint32))
+
+    # a head's NaN or infinity is its own affair
+    for bad in (np.nan, np.inf):
+        odd = q[seqs].copy()
+        odd[:, 1, 7] = bad
+        got = dev.attention(torch.from_numpy(odd).cuda(), seqs).cpu().numpy().reshape(len(seqs), heads, hd)
+        rest = [h for h in range(heads) if h != 1]
+        for i, s in enumerate(seqs):
+            if lens[s]:
+                assert np.isnan(got[i, 1]).all()
+                b = _bound(ref, s, q[s].astype(np.float64), heads)
+                assert (np.abs(got[i] - want[s]).max(axis=1)[rest] <= b[rest]).all(), lens[s]
+
+    # a page that is none, in the middle and at the end of a sequence; one behind the end is not looked at
+    ref.table[11, 0], ref.table[12, (1500 - 1) // page_len] = -1, need + 3
+    ref.table[5, -1] = need + 99
+    dev = Dev(nt, ref, heads)
+    got = dev.attention(qd, seqs).cpu().numpy().reshape(len(seqs), heads, hd)
+    assert np.isnan(got[[11, 12, 13]]).all() and np.isfinite(np.delete(got, [11, 12, 13], 0)).all()
+    fine = [i for i in range(len(seqs)) if i not in (11, 12, 13)]
+    np.testing.assert_array_equal(got[fine].view(np.uint32), first[fine].view(np.uint32))
+    assert int(dev.error.cpu()[0]) == R.BAD_PAGE
+
+
 def test_offsets_beyond_32_bits(nt):
     """A pool of over 4 GB whose used pages lie at its end, in the last layer."""
     torch = torch_cuda()
