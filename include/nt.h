@@ -372,7 +372,7 @@ nt_status nt_attention(int32_t n_heads, int32_t n_kv_heads, int32_t head_dim, in
  *
  * Values.  Every 32 consecutive dimensions of a position and kv head are a Q4_0
  * block, value d (q - 8), whose scale has six mantissa bits:
- *   A = max |x|, h = the bits of f16(A / 7) (both roundings to nearest),
+ *   A = max |x|, h = the bits of f16(A r), r = 1 / 7 in fp32 (all roundings to nearest),
  *   d = the f16 of bits (h + 8) & 0xfff0,
  *   q = min(max(round(x / d) + 8, 0), 15), halves away from zero; 8 where d = 0.
  * A block that holds a NaN or an infinity, or whose d is above 896, is stored as

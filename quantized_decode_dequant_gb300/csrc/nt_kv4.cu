@@ -232,8 +232,7 @@ struct Kv4Scale {
   float up, down;   // 1 / d a little enlarged and diminished (0 where all codes are 8)
 };
 __device__ __forceinline__ Kv4Scale kv4_scale(float top) {
-  // top / 7 correctly rounded (Markstein: the rounded reciprocal's product, corrected by its exact residual)
-  const float r7 = 1.0f / 7.0f, q = top * r7, d7 = fmaf(fmaf(-7.0f, q, top), r7, q);
+  const float d7 = top * (1.0f / 7.0f);
   Kv4Scale s;
   s.bits = (uint32_t(__half_as_ushort(__float2half_rn(d7))) + 8u) & 0xfff0u;
   float inv;

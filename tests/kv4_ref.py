@@ -9,12 +9,12 @@ BAD_SEQ, BAD_LEN, BAD_PAGE, NO_PAGE = 1, 2, 4, 8
 
 
 def scale_of(block):
-    """f16 scale of 32 fp32 values: max|x| / 7 in fp32, to f16, to six mantissa bits; NaN where it cannot be held."""
+    """f16 scale of 32 fp32 values: max|x| by 1 / 7 in fp32, to f16, to six mantissa bits; NaN where it cannot be held."""
     block = np.asarray(block, np.float32)
     if not np.isfinite(block).all():
         return np.float16(np.nan)
     with np.errstate(over="ignore"):
-        h = np.float16(np.float32(np.abs(block).max()) / np.float32(7))
+        h = np.float16(np.float32(np.abs(block).max()) * np.float32(1 / 7))
     bits = (int(h.view(np.uint16)) + 8) & 0xFFF0
     d = np.array([bits], np.uint16).view(np.float16)[0]
     return d if np.isfinite(d) and d <= 896 else np.float16(np.nan)
