@@ -203,16 +203,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     return make_int2(chunk(2 * pi), chunk(2 * pi + 1));
   };
 
-  // brings an item's q into L1, a line a lane
-  auto fetch_q = [&](int e, int g) {
-    for (int x = 32 * lane; x < G * HD; x += 32 * 32)
-      asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD + x));
-  };
   int e = 0, g = 0, pi0 = 0, np = 1;
-  if (count > 0) {
-    locate(w0, e, g, pi0, np);
-    fetch_q(e, g);         // in flight while the first pages are looked up and copied
-  }
+  if (count > 0) locate(w0, e, g, pi0, np);
   // Pair x stands in stage x % S and completes that stage's barrier phase x / S.
   int2 addr = resolve(lane);                  // of pairs 32 b + lane
   int issued = 0;
@@ -582,10 +574,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     }
     const bool whole = pi0 == 0 && seg == np;
     const int slot = 2 * warp + (pi0 > 0 ? 0 : 1), e_was = e, g_was = g;
-    if (k < count) {
-      locate(w0 + k, e, g, pi0, np);
-      fetch_q(e, g);       // in flight while this item's results go out
-    }
+    if (k < count) locate(w0 + k, e, g, pi0, np);
     float* po = slot_ptr(slot);
     if (!whole && lane == 0) slot_item[slot] = e_was * c.n_kv + g_was;
     __syncwarp();   // (slot 1 is the ring: every lane has read its last pair)
@@ -794,9 +783,15 @@ static Kv4Fit kv4_fit() {
 }
 
 // Most pairs of a warp in the form with a cluster per item.  (us, that form with up to 2
-// pairs, with up to 3, and the other: 1 sequence of 4161 positions, 64/8 heads: 10.0,
-// 10.0, 10.4; of 600: 8.4, 8.4, 9.9; 16 of 300, 32/8: 6.9, 6.9, 11.0; 1 of 9000, 16/1: 11.7, 15.0, 11.7.)
+// pairs, with up to 3, and the other: 1 sequence of 4161 positions, 64/8 heads: 9.6,
+// 9.6, 10.4; of 600: 8.1, 8.1, 9.9; 16 of 300, 32/8: 6.8, 6.8, 11.0; 1 of 9000, 16/1: 11.4, 14.7, 11.4.)
 constexpr int kKv4ClusterShare = 2;
+
+// Tiles of 128 positions an SM, by capacity, from which the tcgen05 kernel is taken (8 and 16 heads of 128 dimensions; below,
+// its tiles are too coarse a share).  (us, this file's kernel and that one: 1 sequence of 9000, 16/1 heads, 0.5 tiles
+// an SM: 11.4, 13.1; of 70000: 3.6: 17.3, 18.2; 30 of 300, 64/8: 4.7: 13.0, 14.0; 1 of 12000: 4.9: 13.1, 13.8; 100 of 90:
+// 5.3: 17.2, 16.5; 1 of 16000: 6.6: 15.0, 14.0.)
+constexpr int kKv4TcTiles = 6;
 
 template <int HD, int HB>
 static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_units, cudaStream_t s) {
@@ -819,10 +814,13 @@ static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_uni
     return cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB, true>, k, a);
   }
   int ctas = 0;
-  cudaError_t e;
+  cudaError_t e = cudaSuccess;
+  bool tc = false;
   if constexpr (HD == 128 && HB >= 8) {
-    e = kv4_launch_attn_tc(k, a, s, &ctas);
-  } else {
+    tc = items * ((pairs + 3) / 4) >= int64_t(kKv4TcTiles) * fit.setup.sms;
+    if (tc) e = kv4_launch_attn_tc(k, a, s, &ctas);
+  }
+  if (!tc) {
     static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, HB, false>, Cfg::kSmem);
     if (setup.err != cudaSuccess) return setup.err;
     const int64_t useful = (most_units + Cfg::NW * kKv4MinPairs - 1) / (Cfg::NW * kKv4MinPairs);

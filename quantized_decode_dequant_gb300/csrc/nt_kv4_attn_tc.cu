@@ -218,12 +218,7 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
   const int alone = 1 + group, all = 1 + Cfg::kGroups + group;   // barriers: of the warps that decode, of the whole group
   int k = 0, e = 0, g = 0, ti0 = 0, nt = 1;
   bool dead = false;   // a wait ran out: nothing more is copied or multiplied (the same in all of the group)
-  if (count > 0) {
-    locate(w0, e, g, ti0, nt);
-    if (!helps)   // brings q into L1, in flight while the tensor memory's address is waited for
-      for (int x = 32 * (t & 127); x < G * HD; x += 32 * 128)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD + x));
-  }
+  if (count > 0) locate(w0, e, g, ti0, nt);
 
   if (helps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kHelpRegs));
