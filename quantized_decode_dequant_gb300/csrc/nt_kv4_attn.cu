@@ -681,6 +681,7 @@ __global__ void __launch_bounds__(32 * kKv4MergeWarps) k_kv4_attn_merge(Kv4 c, K
   __shared__ float s_o[kKv4MergeWarps][HD];
   __shared__ float2 s_ml[kKv4MergeWarps];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, h = blockIdx.y;
+  asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const float* first = a.part + (int64_t(blockIdx.x) * 2 + 1) * part_floats;   // slot 1, then slot 0 of the next CTAs
   const int2 header = __ldcg(reinterpret_cast<const int2*>(first + part_floats - 4));
