@@ -594,6 +594,49 @@ def test_attention_where_the_capacity_is_large(nt, hd, G, page_len):
     assert int(dev.error.cpu()[0]) == R.BAD_PAGE
 
 
+@pytest.mark.parametrize("hd,G", [(128, 4), (128, 8), (128, 16), (64, 8)])
+def test_attention_replayed_and_on_two_streams_at_once(nt, hd, G):
+    """The shared-out forms in a captured graph whose lengths change between replays, and two callers at once with a
+    workspace each: to the bit what calls one after the other give."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([97, hd, G])
+    ref = R.RefCache(1, 4, hd, 64, 120, 4, 512)
+    ref.randomize(rng)
+    ref.hold([2000, 1500, 900, 1800], rng)
+    dev = Dev(nt, ref, 4 * G)
+    q = torch.from_numpy(rng.standard_normal((4, 4 * G, hd)).astype(np.float32)).cuda()
+    out = torch.empty(4, 4 * G * hd, device="cuda")
+    lens = [[2000, 1500, 900, 1800], [1, 0, 900, 129], [1999, 128, 16, 17], [0, 0, 0, 0]]
+    eager = []
+    for n in lens:
+        dev.len.copy_(torch.tensor(n, dtype=torch.int32))
+        eager.append(dev.attention(q).clone())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        dev.attention(q, out=out, stream=torch.cuda.current_stream())
+    for n, want in list(zip(lens, eager)) * 2:
+        dev.len.copy_(torch.tensor(n, dtype=torch.int32))
+        out.fill_(float("inf"))
+        graph.replay()
+        assert torch.equal(out.view(torch.int32), want.view(torch.int32)), n
+    dev.len.copy_(torch.tensor(lens[0], dtype=torch.int32))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.full((dev.wb,), 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [torch.full((20, 4, 4 * G * hd), float("inf"), device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(20):
+        for st, ws, o in zip(streams, spaces, outs):
+            with torch.cuda.stream(st):
+                dev.attention(q, out=o[i], ws=ws, stream=st)
+    torch.cuda.synchronize()
+    for o in outs:
+        for i in range(20):
+            assert torch.equal(o[i].view(torch.int32), eager[0].view(torch.int32))
+    assert int(dev.error.cpu()[0]) == 0
+
+
 def test_offsets_beyond_32_bits(nt):
     """A pool of over 4 GB whose used pages lie at its end, in the last layer."""
     torch = torch_cuda()
