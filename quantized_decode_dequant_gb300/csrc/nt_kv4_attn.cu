@@ -30,7 +30,7 @@
 // not overlap.  With 4 heads that is just behind the memory: 56 sequences of up to 9001 positions of 8 kv heads
 // (293 MB) take 65.1 us, 4.5 TB/s in all and 5.9 while data flows.  With 8 heads the products are twice as many
 // and decide (43.6 us for 131077 positions where memory wants 22.3), so long work of 8 and 16 heads of
-// 128 dimensions goes to the tcgen05 kernel of nt_kv4_attn_tc.cu (38.9 us).  Short work keeps to this kernel's cluster
+// 128 dimensions goes to the tcgen05 kernel of nt_kv4_attn_tc.cu (38.5 us).  Short work keeps to this kernel's cluster
 // form: its warps go about alone, and there a first result counts, not a rate.
 #include <cooperative_groups.h>
 
@@ -100,7 +100,7 @@ __device__ __forceinline__ int kv4_pairs(int len) { return (len + 2 * kKv4Chunk 
 // a CTA's is merged in shared memory; the rest leaves partial results (at most two
 // a CTA: slot 0 of an item begun before it, slot 1 of one that goes on behind it)
 // to k_kv4_attn_merge.  Partial results are merged in the order of the positions,
-// so the result does not depend on timing.
+// so the result does not depend on timing.  (WHOLE: CTA b's share is the items that begin in it; nothing is cut.)
 //
 // A warp leaves at most two partial results to the CTA: of the item it did not
 // begin (slot 2 warp, in memory of its own) and of the one it did not end (slot
@@ -110,7 +110,7 @@ __device__ __forceinline__ int kv4_pairs(int len) { return (len + 2 * kKv4Chunk 
 // thread-block cluster has an item to itself, its warps share the pairs out, and
 // the CTAs' partial results meet through distributed shared memory: no second launch,
 // and no counting of the other entries.
-template <int HD, int HB, bool CL>
+template <int HD, int HB, bool CL, bool WHOLE = false>
 __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv4 c, Kv4AttnArgs a) {
   using Cfg = Kv4AttnCfg<HD, HB>;
   using L = Kv4Chunk<HD>;
@@ -148,8 +148,21 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
   const int total = prefix[CL ? 1 : n], warps = int(gridDim.x) * NW;
   int share = (total + warps - 1) / warps;
   if (share < kKv4MinPairs) share = kKv4MinPairs;
-  const int c0 = int(blockIdx.x) * NW * share;           // the CTA's first pair (total + 152 NW pairs fit an int)
-  const int c1 = c0 + NW * share < total ? c0 + NW * share : total;
+  int c0 = int(blockIdx.x) * NW * share;                 // the CTA's first unit (total + 152 NW units fit an int)
+  int c1 = c0 + NW * share < total ? c0 + NW * share : total;
+  if constexpr (WHOLE) {   // the items that begin there, and a share of them for each warp; lane 1 looks for the end
+    int y = lane == 1 ? c1 : c0;
+    if (y < total) {
+      const int e = kv4_find(prefix, n, y), units = kv4_pairs(entry[e].y) + kKv4ItemPairs;
+      y = prefix[e] + int(unsigned(y - prefix[e] + units - 1) / unsigned(units)) * units;
+    } else {
+      y = total;
+    }
+    c0 = __shfl_sync(0xffffffffu, y, 0);
+    c1 = __shfl_sync(0xffffffffu, y, 1);
+    share = (c1 - c0 + NW - 1) / NW;
+    if (share < kKv4MinPairs) share = kKv4MinPairs;
+  }
   float* part0 = CL ? reinterpret_cast<float*>(sm + Cfg::kAcc) : a.part + int64_t(blockIdx.x) * 2 * Cfg::kPart;
   int* header = reinterpret_cast<int*>(part0 + 2 * Cfg::kPart - 4);   // of slot 1
   if (!CL && t == 0) header[0] = -1;
@@ -163,7 +176,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     }
   } else {
     kv4_empty_entries(c, a, entry, HD);
-    if (c0 >= total) return;   // the whole CTA
+    if (c0 >= c1) return;   // the whole CTA
   }
 
   const int w0 = c0 + warp * share;
@@ -794,8 +807,14 @@ constexpr int kKv4ClusterShare = 2;
 // 5.3: 17.2, 16.5; 1 of 16000: 6.6: 15.0, 14.0.)
 constexpr int kKv4TcTiles = 6;
 
+// Pairs of an item's capacity per warp of a CTA up to which CTAs take whole items: no second launch, a CTA's share uneven
+// by an item.  (us, whole and cut: 30 sequences of 300, 64/8 heads: 11.1, 13.0; 25 of 150: 9.4, 11.7; 100 of 90: 14.7,
+// 17.0; 64 of up to 200, 32/8: 14.0, 14.3; of 200, 64/8: 13.8, 13.5; at 2 pairs 20 of 700, 64/8: 14.8, 15.6, and 64 of 700,
+// 32/8: 22.6, 24.1; at 5 30 of up to 2500, 32/8: 28.7, 22.9.)
+constexpr int kKv4WholeShare = 2;
+
 template <int HD, int HB>
-static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_units, cudaStream_t s) {
+static cudaError_t kv4_launch_attn(const Kv4& k, const Kv4AttnArgs& a, int64_t most_units, cudaStream_t s) {
   using Cfg = Kv4AttnCfg<HD, HB>;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
@@ -816,21 +835,26 @@ static cudaError_t kv4_launch_attn(const Kv4& k, Kv4AttnArgs a, int64_t most_uni
   }
   int ctas = 0;
   cudaError_t e = cudaSuccess;
+  // Whole items for the CTAs where each is small: nothing is left to a second launch.
+  const bool whole = pairs <= int64_t(Cfg::NW) * kKv4WholeShare;
   bool tc = false;
   if constexpr (HD == 128 && HB >= 8) {
-    tc = items * ((pairs + 3) / 4) >= int64_t(kKv4TcTiles) * fit.setup.sms;
+    tc = !whole && items * ((pairs + 3) / 4) >= int64_t(kKv4TcTiles) * fit.setup.sms;
     if (tc) e = kv4_launch_attn_tc(k, a, s, &ctas);
   }
   if (!tc) {
-    static const KernelSetup setup = kernel_setup(k_kv4_attn<HD, HB, false>, Cfg::kSmem);
+    const auto kernel = whole ? k_kv4_attn<HD, HB, false, true> : k_kv4_attn<HD, HB, false>;
+    static const KernelSetup setups[2] = {kernel_setup(k_kv4_attn<HD, HB, false>, Cfg::kSmem),
+                                          kernel_setup(k_kv4_attn<HD, HB, false, true>, Cfg::kSmem)};
+    const KernelSetup& setup = setups[whole];
     if (setup.err != cudaSuccess) return setup.err;
     const int64_t useful = (most_units + Cfg::NW * kKv4MinPairs - 1) / (Cfg::NW * kKv4MinPairs);
     ctas = setup.sms < kKv4AttnMaxCtas ? setup.sms : kKv4AttnMaxCtas;
     if (ctas > useful) ctas = int(useful);
     kv4_config(cfg, attr, dim3(unsigned(ctas)), Cfg::kThreads, Cfg::kSmem, s, 0);
-    e = cudaLaunchKernelEx(&cfg, k_kv4_attn<HD, HB, false>, k, a);
+    e = cudaLaunchKernelEx(&cfg, kernel, k, a);
   }
-  if (e != cudaSuccess || ctas < 2) return e;
+  if (e != cudaSuccess || ctas < 2 || whole) return e;
   // (the last CTA's items end with it)
   kv4_config(cfg, attr, dim3(unsigned(ctas - 1), unsigned(a.G)), 32 * kKv4MergeWarps, 0, s, 0);
   return cudaLaunchKernelEx(&cfg, k_kv4_attn_merge<HD>, k, a, int(Cfg::kPart), int(Cfg::kRows));

@@ -81,8 +81,8 @@ __device__ __forceinline__ uint32_t kv4_pick(uint32_t w, uint32_t magic) {
 }
 // The four half2 of a word: value pairs (code k, code k + 4), k = 0..3, times the
 // scale pair d; d72 = -72 d.  (Two of the shifts can be saved by taking codes 0 and
-// 2 as 1024 + q, less 1032, times d: measured 4% slower at 131077 positions, the
-// half2 and matrix instructions being what is short, not the shifts.)
+// 2 as 1024 + q, less 1032, times d: measured 4% slower at 131077 positions with
+// mma.sync and 2% with tcgen05: as many instructions, more of them half2.)
 __device__ __forceinline__ void kv4_decode(uint32_t w, uint32_t d, uint32_t d72, uint32_t (&b)[4]) {
   constexpr uint32_t k64 = 0x54005400u;
   b[0] = kv4_h2fma(kv4_pick<0x00f000f0u>(w << 4, k64), d, d72);

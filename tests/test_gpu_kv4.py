@@ -637,6 +637,33 @@ def test_attention_replayed_and_on_two_streams_at_once(nt, hd, G):
     assert int(dev.error.cpu()[0]) == 0
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("G", [1, 4, 8, 16])
+def test_attention_of_many_short_sequences(nt, hd, G):
+    """More (sequence, kv head) items than the GPU holds at once, each of few positions: 80, 300 and 1500 entries of nine
+    sequences, empty ones among them, in any order."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([103, hd, G])
+    lens = [0, 1, 16, 17, 33, 64, 100, 191, 192]
+    ref = R.RefCache(1, 3, hd, 16, 60, 9, 12)
+    ref.randomize(rng)
+    ref.hold(lens, rng)
+    heads = 3 * G
+    q = rng.standard_normal((9, heads, hd)).astype(np.float32)
+    want = _want(ref, range(9), q.astype(np.float64), heads)
+    bounds = [_bound(ref, s, q[s].astype(np.float64), heads) for s in range(9)]
+    dev = Dev(nt, ref, heads)
+    for n in (80, 300, 1500):
+        seqs = rng.integers(0, 9, n)
+        seqs[-3:] = [0, 8, 0]
+        got = dev.attention(torch.from_numpy(q[seqs]).cuda(), seqs).cpu().numpy().reshape(n, heads, hd)
+        for s in range(9):
+            mine = got[seqs == s]
+            assert (np.abs(mine - want[s]).max(axis=(0, 2)) <= bounds[s]).all(), (n, lens[s])
+            assert lens[s] or (mine == 0).all()
+    assert int(dev.error.cpu()[0]) == 0
+
+
 def test_offsets_beyond_32_bits(nt):
     """A pool of over 4 GB whose used pages lie at its end, in the last layer."""
     torch = torch_cuda()
