@@ -41,9 +41,9 @@ namespace nt {
 constexpr int kKv4MinPairs = 1;        // fewest pairs of chunks of a warp: below, fewer CTAs work
 // An item's start and end cost a warp about as much as a pair (q to split, sums to
 // reduce, results to store): the share-out counts it as so many pairs more, in
-// front of the item's own.  (Measured, with 0, 1, 2 and 3: 56 sequences of up to 9001
-// positions 80.0, 81.0, 79.2, 78.6 us; 64 of up to 200: 18.2, 15.5, 13.8, 13.6; 8 of up
-// to 1500: 10.7, 10.6, 12.4, 12.7.)
+// front of the item's own.  (Measured, with 1, 2 and 3: 56 sequences of up to 9001
+// positions 66.4, 65.4, 65.0 us; 50 of 3000 with heads of 64 32.3, 32.1, 32.1; 64 of 200 12.6, 12.4, 14.6; 64 of
+// up to 200 10.9, 14.0, 12.9; 64 of 700 22.7, 22.6, 24.2.)
 constexpr int kKv4ItemPairs = 2;
 
 // HB: query heads of a kv head that the instantiation is made for, up to 4, 8 or 16.
@@ -803,8 +803,7 @@ constexpr int kKv4ClusterShare = 2;
 
 // Tiles of 128 positions an SM, by capacity, from which the tcgen05 kernel is taken (8 and 16 heads of 128 dimensions; below,
 // its tiles are too coarse a share).  (us, this file's kernel and that one: 1 sequence of 9000, 16/1 heads, 0.5 tiles
-// an SM: 11.4, 13.1; of 70000: 3.6: 17.3, 18.2; 30 of 300, 64/8: 4.7: 13.0, 14.0; 1 of 12000: 4.9: 13.1, 13.8; 100 of 90:
-// 5.3: 17.2, 16.5; 1 of 16000: 6.6: 15.0, 14.0.)
+// an SM: 11.4, 13.1; of 70000: 3.6: 17.3, 18.2; 1 of 12000, 64/8: 4.9: 13.1, 13.8; 1 of 16000: 6.6: 15.0, 14.0.)
 constexpr int kKv4TcTiles = 6;
 
 // Pairs of an item's capacity per warp of a CTA up to which CTAs take whole items: no second launch, a CTA's share uneven
