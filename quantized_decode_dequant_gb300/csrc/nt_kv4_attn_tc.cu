@@ -39,11 +39,11 @@ template <int HB>
 struct Kv4TcCfg {
   static constexpr int HD = 128, N = 16, kRowBlocks = HB / 4, CB = kv4_chunk_bytes(HD);
   static constexpr int kGroups = HB == 8 ? 4 : 3, kWarps = 4 * kGroups;   // warps that decode
-  static constexpr int kThreads = 128 * (kGroups + 1);                    // and one of each group that copies and starts products
+  static constexpr int kThreads = 128 * (kGroups + 1);                    // and one of each that copies and starts products
   static constexpr int S = 2;                                       // ring stages of a group
   static constexpr int kRegs = HB == 8 ? 112 : 152, kHelpRegs = HB == 8 ? 32 : 56;   // the launch's, shared out again
   static constexpr int kLaunchRegs = 65536 / kThreads / 8 * 8;
-  static_assert(kGroups * kRegs + kHelpRegs <= (kGroups + 1) * kLaunchRegs, "an increase beyond what was launched waits for ever");
+  static_assert(kGroups * kRegs + kHelpRegs <= (kGroups + 1) * kLaunchRegs, "an increase past the launch's waits for ever");
   static_assert(kHelpRegs < kLaunchRegs && kLaunchRegs < kRegs, "the helpers give, the others take");
   static constexpr int kTileBytes = 8 * CB;
   static constexpr int kPart = kv4_part_floats(HD, HB);
@@ -69,7 +69,8 @@ struct Kv4TcCfg {
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
   static_assert(kPart * 4 <= S * kTileBytes, "a group's ring holds a partial result");
   // tensor memory of a group, in columns.  HB 8: the scores stand where V^T will, the outputs where K was
-  static constexpr int kColK = 0, kColV = 64, kColS = HB == 8 ? 64 : 128, kColO = HB == 8 ? 0 : 144, kCols = HB == 8 ? 128 : 160;
+  static constexpr int kColK = 0, kColV = 64, kColS = HB == 8 ? 64 : 128, kColO = HB == 8 ? 0 : 144;
+  static constexpr int kCols = HB == 8 ? 128 : 160;
   static_assert(kGroups * kCols <= 512, "tensor memory of an SM");
 };
 
@@ -167,15 +168,14 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
   if (helps && warp < Cfg::kWarps + Cfg::kGroups && lane < S + 3) kv4_bar_init(bars + 8 * lane, lane == S + 2 ? 4 : 1);
   if (t < 2 * Cfg::kGroups) slot_item[t] = -1;
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __syncthreads();   // barriers
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Tensor memory is taken only now, though 0.3 us earlier would be for nothing: a kernel that this one waits for could want
+  // it on this SM.  The other fifth warps hear of it before they copy, those that decode with their first tile.
   if (warp == Cfg::kWarps)
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(kv4_smem(sm + Cfg::kTmem))
                  : "memory");
-  kv4_tc_before();
-  __syncthreads();   // barriers, the tensor memory's address
-  kv4_tc_after();
-  const uint32_t tmem_all = __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sm + Cfg::kTmem), 0);
-  const uint32_t tmem = tmem_all + group * Cfg::kCols;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const volatile uint32_t* tensor_memory = reinterpret_cast<const volatile uint32_t*>(sm + Cfg::kTmem);
   kv4_count<Cfg::kThreads / 32>(c, a, kTcTile, kTcItemTiles, prefix, entry, reinterpret_cast<int*>(sm + Cfg::kOrder));
   const int total = prefix[n], groups = int(gridDim.x) * Cfg::kGroups;
   int share = (total + groups - 1) / groups;
@@ -222,6 +222,10 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
 
   if (helps) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(Cfg::kHelpRegs));
+    kv4_tc_before();
+    asm volatile("barrier.cta.sync.aligned 14, 128;" ::: "memory");
+    kv4_tc_after();
+    const uint32_t tmem = *tensor_memory + group * Cfg::kCols;
     if (warp < Cfg::kWarps + Cfg::kGroups) {
       // Copies: the group's tile x (an item's cost is none) into stage x % S, whose barrier phase x / S completes.  A lane
       // knows chunk lane % 8 of unit 4 b + lane / 8: addr those of the units up to the next multiple of 4, next four more.
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
     asm volatile("barrier.cta.sync.aligned 15, %0;" ::"n"(Cfg::kThreads) : "memory");
     if (warp == Cfg::kWarps) {
       asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem_all));
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(*tensor_memory));
     }
     return;
   }
@@ -322,6 +326,7 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
   float O[HB], l[HB], mref[HB], cs[HB];
   uint32_t ps = 0, po = 0;      // parities of the products' barriers
   int tile_no = 0;              // tiles behind
+  uint32_t tmem = 0;            // known with the first tile
   bool pending = false;         // an O^T has been started and not been taken in
 
   // adds the last tile's outputs to the sums; false: they never came
@@ -385,10 +390,14 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
     for (const int k1 = k + seg; k < k1; k++, tile_no++, live -= kTcTile) {
       const int st = tile_no % S;
       if (dead) continue;
-      bool fail = !kv4_bar_wait(bars + 8 * st, uint32_t(tile_no / S) & 1u);
+      bool fail = !__all_sync(0xffffffffu, kv4_bar_wait(bars + 8 * st, uint32_t(tile_no / S) & 1u));
       uint8_t* tile = gs + Cfg::kRing + st * Cfg::kTileBytes;
       const uint32_t base = kv4_smem(tile);
-      const bool lacks = miss[st];
+      const bool lacks = fail || miss[st];
+      if (tile_no == 0) {
+        kv4_tc_after();
+        tmem = *tensor_memory + group * Cfg::kCols;
+      }
       // ---- K of chunks 2 wq and 2 wq + 1: rows are positions
       if (!lacks) {
 #pragma unroll
