@@ -30,7 +30,7 @@
 // not overlap.  With 4 heads that is just behind the memory: 56 sequences of up to 9001 positions of 8 kv heads
 // (293 MB) take 65.1 us, 4.5 TB/s in all and 5.9 while data flows.  With 8 heads the products are twice as many
 // and decide (43.6 us for 131077 positions where memory wants 22.3), so long work of 8 and 16 heads of
-// 128 dimensions goes to the tcgen05 kernel of nt_kv4_attn_tc.cu (38.5 us).  Short work keeps to this kernel's cluster
+// 128 dimensions goes to the tcgen05 kernel of nt_kv4_attn_tc.cu (38.7 us).  Short work keeps to this kernel's cluster
 // form: its warps go about alone, and there a first result counts, not a rate.
 #include <cooperative_groups.h>
 

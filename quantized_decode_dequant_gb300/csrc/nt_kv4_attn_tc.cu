@@ -22,8 +22,8 @@
 // What bounds it: issue slots.  A tile costs each of the four warps 800 instructions (26.3 M in all for 8192 tiles), over half
 // of them decoding, and the SM's 4 groups take 0.52 us a tile together; issue is 68% busy, the start included.  That
 // start is 10 us: lengths, pages and first tiles one after the other, and a second launch merges partial results.
-// 131077 positions of 8 kv heads (151 MB): 38.5 us, with mma.sync 43.6; 4 x 40000 of 4 kv heads with 16 heads each 37.7
-// and 46.8; 4 x 20000 of 8 30.0 and 31.8; 64 of up to 1000 26.8 and 26.2; 64 of up to 200 14.1 and 14.9.
+// 131077 positions of 8 kv heads (151 MB): 38.7 us, with mma.sync 43.6; 4 x 40000 of 4 kv heads with 16 heads each 37.4
+// and 46.8; 4 x 20000 of 8 29.8 and 31.8; 16 of up to 4000 22.8 and 23.1; 64 of up to 1000 26.5 and 26.2.
 // (On the way, for the first: three groups, a warp of theirs starting products by its thread 0: 62.0; by an elected
 // thread: 54.8; a fifth warp for it: 44.5; that warp awaiting K by an mbarrier, q in one pass: 42.4; four groups: 40.6.)
 #include "nt_kv4_attn.cuh"
