@@ -90,7 +90,8 @@ struct Kv4Span {
 
 // Unit u of the call: a chunk that entry i's rows may touch.  Entry i's units start
 // at begin[i] / 16 + 2 i: r rows touch at most r / 16 + 2 chunks, so they do not
-// meet entry i + 1's.  Without `begin` a unit is an entry.  false: nothing to do.
+// meet entry i + 1's; the units between belong to nobody.  Without `begin` a unit is an
+// entry.  false: nothing to do.
 // All lanes call it and get the same.
 __device__ __forceinline__ bool kv4_span(const Kv4& c, const Kv4Rows& a, int u, Kv4Span* sp) {
   const int lane = threadIdx.x & 31;
@@ -129,6 +130,7 @@ __device__ __forceinline__ bool kv4_span(const Kv4& c, const Kv4Rows& a, int u, 
     if (lane == 0 && u == start) kv4_flag(c, bad);
     return false;
   }
+  if (u - start > rows / kKv4Chunk + 1) return false;   // behind the entry's last chunk (n, up to 2^31 - 256, and more would not fit an int)
   const int p0 = (n - rows) / kKv4Chunk * kKv4Chunk + (u - start) * kKv4Chunk;   // the chunk's first position
   if (p0 >= n) return false;
   const int first = p0 > n - rows ? p0 : n - rows;
@@ -917,7 +919,7 @@ static nt_status kv4_plan_apply(const char* who, const Kv4& k, Kv4PlanArgs a, vo
   return NT_OK;
 }
 
-// Units of a call (see kv4_span), at most 2^26, so that positions counted from units
+// Units of a call (see kv4_span), at most 2^26, so that begin / 16 + 2 i and the grid
 // fit 31 bits (0: n or n_rows is out of range).
 static int32_t kv4_units(int32_t n, int32_t n_rows, const int32_t* begin) {
   const int64_t u = begin ? int64_t(n_rows) / kKv4Chunk + 2 * int64_t(n) + 1 : (n < n_rows ? n : n_rows);

@@ -947,3 +947,34 @@ def test_a_captured_step_replays(nt):
         for i, s in enumerate((2, 0)):
             assert (np.abs(got[i] - want[i]).max(axis=1) <= _bound(ref, s, qn[i].astype(np.float64), 4)).all()
     dev.check()
+
+
+# ------------------------------------------------------------ rows at the limits --
+
+@pytest.mark.parametrize("rows", [1, 16, 17, 40])
+@pytest.mark.parametrize("padded", [0, 4096, 1 << 24])
+def test_rows_of_the_longest_sequence_in_a_padded_batch(nt, rows, padded):
+    """Length 2^31 - 256, and more rows in the call than anybody has: the chunks behind the entry's last one, positions
+    beyond 2^31, are nobody's.  (Rows of stride 0: all are the same, so the padding needs no memory.)"""
+    torch = torch_cuda()
+    ref = R.RefCache(1, 1, 64, 256, 3, 3, (1 << 23) - 1, fill=0x5A)
+    ref.len[2] = 256 * ref.M
+    assert ref.len[2] == (1 << 31) - 256
+    ref.table[2, -1], ref.refs[1] = 1, 1
+    dev = Dev(nt, ref)
+    x = np.repeat(_rows(np.random.default_rng(rows), 1, 1, 64), rows, 1)
+    k, v = _layout(torch, x[:, :1], "rows")
+    first = 3 if padded else 0
+    begin = [first, first + rows]
+    nt.nt_kv4_append(dev.c, 0, 1, dev.ints([2]), dev.ints(begin), begin[1] + padded, "f32", k.data_ptr(), v.data_ptr(), 0, 64,
+                     dev.stream())
+    _store(ref, np.pad(x, [(0, 0), (first, 0), (0, 0), (0, 0)]), begin, [2])
+    dev.check()
+    if padded <= 4096:
+        out = torch.full((2, begin[1] + padded, 1, 64), 5.5, device="cuda")
+        dev.rows(out[0], out[1], begin, [2], read=True)
+        want = np.full(out.shape, 5.5)
+        for side in (0, 1):
+            want[side, first:begin[1]] = R.values(*R.quantize(x[side]))
+        np.testing.assert_array_equal(out.cpu().numpy().astype(np.float64), want)
+        dev.check()
