@@ -511,7 +511,8 @@ nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int
  * and zeros where len = 0.  dev_q and dev_out: fp32, sequence i at element i * q_stride
  * and i * out_stride (multiples of 4, at least n_heads * head_dim), [n_heads][head_dim] each.
  * The statistics and sums are fp32; K and V enter exactly, q and the softmax
- * weights with about 22 bits.  A sequence out of range, a length that the table
+ * weights with about 22 bits (a weight of less than 2^-9 of the head's largest to 2^-31 of that, as
+ * an f16 pair ends there).  Scores may be of any size below 2^126.  A sequence out of range, a length that the table
  * cannot hold and a page index out of range give NaN in that sequence's outputs.
  * n at most 65536, n_kv_heads * max_pages * page_len at most 2^34 and a layer of the pool
  * at most 2^31 - 1 chunks.

@@ -14,7 +14,7 @@
 // B operand of mma.sync m16n8k16: nothing passes through shared memory twice.
 //
 // Contractions (G > 4; below 5 heads see N4).  Scores S[h][t] = q_h . K_t and outputs O[h][d] = sum_t P[h][t]
-// V_t[d].  q (scaled by a power of two) and P are split into two f16 terms, hi =
+// V_t[d].  q (scaled) and P are split into two f16 terms, hi =
 // f16(x) and lo = f16(x - hi), about 22 bits.  With G <= 8 hi takes rows 0..7 of
 // the 16-row A operand of the scores and lo rows 8..15 (G = 16: a product each); for
 // the outputs V^T is the A operand, 16 dimensions a tile, and P, as the scores'
@@ -270,7 +270,10 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     int live = ent(e).y - pi0 * 2 * kKv4Chunk;   // positions from the pair on that exist
     bool poison = false;
     {
-      // q of heads gi (and gi + 8; N4: gi % 4), scaled so that a head's largest element is in [2^10, 2^11), split
+      // q of heads gi (and gi + 8; N4: gi % 4), split.  It is scaled by 8 log2(e) / sqrt(hd) (below 2) and a power of two that
+      // brings a head's largest element into [2^10, 2^12), so that a score times cs, a power of two, is an exponent of 2 and
+      // that product exact: the same number in the maximum and in the multiply-add of the weights, however large.  (With
+      // the scale in cs, a maximum rounded by itself was off by up to half its last place, from scores of 2^28 on more than a weight's range.)
       const float* qb = a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD;
       float qx[MT][NG][8], back[MT];
 #pragma unroll
@@ -292,9 +295,9 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int ex = int(__float_as_uint(top) >> 23);
-        ex = ex < 11 ? 11 : ex;                                  // (zeros and values below 2^-116)
-        const float up = __uint_as_float(uint32_t(264 - ex) << 23);   // 2^(137 - ex)
-        back[m] = a.scale_log2 * __uint_as_float(uint32_t(ex - 10) << 23);
+        ex = ex < 14 ? 14 : ex;                                  // (zeros and values below 2^-113)
+        const float up = __uint_as_float(uint32_t(264 - ex) << 23) * a.q_scale;   // 2^(137 - ex) q_scale
+        back[m] = __uint_as_float(uint32_t(ex - 13) << 23);      // 2^(ex - 140)
 #pragma unroll
         for (int j = 0; j < NG; j++)
 #pragma unroll
@@ -432,7 +435,8 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
       }
       // ---- weights p = 2^(s - mref).  Only where a lane's sum passes 2^15 (at first it is infinite) is the maximum looked
       // for; where that passes mref by 12, as one of 8 weights does then, it less 6 becomes mref.  So weights stay within
-      // f16, and the largest so far is at least 2^6: the lo terms of all that matter are ordinary f16 numbers.
+      // f16, and the largest so far is at least 2^6: the lo terms of all that matter are ordinary f16 numbers.  (Exponents of
+      // 2^25 and more are 4 or more apart, mref among them: the largest weight is 2^0 to 2^8 there, which serves as well.)
       float p[NH][NX], sum[NH];
       auto weights = [&]() {
 #pragma unroll
@@ -454,7 +458,7 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
           top *= cs[m];
 #pragma unroll
           for (int o = N4 ? 4 : 1; o <= (N4 ? 16 : 2); o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const float to = top > mref[m] + 12.f ? top - 6.f : mref[m];
+          const float to = top - mref[m] > 12.f ? top - 6.f : mref[m];   // (mref + 12 could round past top)
           f[m] = kv4_ex2(mref[m] - to);
           mref[m] = to;
           l[m] *= f[m];
@@ -898,7 +902,7 @@ extern "C" nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int3
   Kv4AttnArgs a{};
   a.layer = layer;
   a.G = G;
-  a.scale_log2 = 1.4426950408889634f / sqrtf(float(k.hd));
+  a.q_scale = 11.541560327111707f / sqrtf(float(k.hd));
   a.part = static_cast<float*>(dev_workspace);
   a.q_stride = q_stride;
   a.out_stride = out_stride;

@@ -17,7 +17,7 @@ struct Kv4AttnArgs {
   int64_t q_stride;
   float* out;
   int64_t out_stride;
-  float scale_log2;                    // log2(e) / sqrt(hd)
+  float q_scale;                       // 8 log2(e) / sqrt(hd): what q is multiplied by on top of a power of two
   float* part;                         // [CTA][2] partial results
 };
 

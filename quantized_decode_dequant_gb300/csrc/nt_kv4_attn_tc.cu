@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
     int live = entry[e].y - ti0 * kTcTile;
     bool poison = false;
     {
-      // q, a head by one warp: scaled so that its largest element is in [2^10, 2^11), split
+      // q, a head by one warp: scaled (as in nt_kv4_attn.cu) so that its largest element is in [2^10, 2^12), split
       const float* qb = a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD;
       float* red = reinterpret_cast<float*>(gs + Cfg::kRed);
 #pragma unroll
@@ -362,9 +362,9 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         int ex = int(__float_as_uint(top) >> 23);
-        ex = ex < 11 ? 11 : ex;                                       // (zeros and values below 2^-116)
-        const float up = __uint_as_float(uint32_t(264 - ex) << 23);   // 2^(137 - ex)
-        if (lane == 0) red[h] = a.scale_log2 * __uint_as_float(uint32_t(ex - 10) << 23);
+        ex = ex < 14 ? 14 : ex;                                       // (zeros and values below 2^-113)
+        const float up = __uint_as_float(uint32_t(264 - ex) << 23) * a.q_scale;   // 2^(137 - ex) q_scale
+        if (lane == 0) red[h] = __uint_as_float(uint32_t(ex - 13) << 23);         // 2^(ex - 140)
         // dimension 32 j + 8 tg + 4 b + p is row 32 j + 8 p + 2 tg + b of the product: K's pairs
         const float x[4] = {u.x * up, u.y * up, u.z * up, u.w * up};
         const int row = 2 * ((lane >> 1) & 3) + (lane & 1);
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(Kv4TcCfg<HB>::kThreads, 1) k_kv4_attn_tc(Kv4 c
 #pragma unroll
         for (int h = 0; h < HB; h++) {
           const float top = fmaxf(fmaxf(red[h], red[HB + h]), fmaxf(red[2 * HB + h], red[3 * HB + h])) * cs[h];
-          const float to = top > mref[h] + 11.f ? top - 6.f : mref[h], f = kv4_ex2(mref[h] - to);
+          const float to = top - mref[h] > 11.f ? top - 6.f : mref[h], f = kv4_ex2(mref[h] - to);
           mref[h] = to;
           l[h] *= f;
           O[h] *= f;

@@ -978,3 +978,45 @@ def test_rows_of_the_longest_sequence_in_a_padded_batch(nt, rows, padded):
             want[side, first:begin[1]] = R.values(*R.quantize(x[side]))
         np.testing.assert_array_equal(out.cpu().numpy().astype(np.float64), want)
         dev.check()
+
+
+# ------------------------------------------------------------ scores of any size --
+
+@pytest.mark.parametrize("hd,G", [(64, 1), (64, 8), (64, 16), (128, 2), (128, 4), (128, 8), (128, 16)])
+@pytest.mark.parametrize("capacity", [704, 16384])
+def test_attention_where_scores_are_huge(nt, hd, G, capacity):
+    """Scores from 2^24 to 2^104, whose fp32 neighbours are up to 2^80 apart: the largest takes all the weight.
+
+    A score is off by at most (as in _bound) ((hd / 16 + 3) 2u + 2^-22) sum |q K| / sqrt(hd); with two scores further apart
+    than twice that and 60 the other weights come to less than 2^-60 of the largest, and the output is the largest's value, whose
+    weight enters as hi + lo (2^-22) into products and sums (an addition a step, 2u each, of numbers that are zero but for
+    one), and is divided out (2u): 2^-21 of the value.  The inputs are such that this holds for every head."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([113, hd, G])
+    lens = [1, 2, 33, 129, 700]
+    powers = [24, 26, 27, 28, 29, 30, 31, 34, 60, 102]
+    n_kv, heads = 2, 2 * G
+    ref = R.RefCache(1, n_kv, hd, 32, 40, len(lens), capacity // 32)
+    ref.randomize(rng)
+    ref.hold(lens, rng)
+    dev = Dev(nt, ref, heads)
+    kv = {(s, g): ref.kv(0, s, g) for s in range(len(lens)) for g in range(n_kv)}
+    checked = 0
+    for power in powers:
+        q = (rng.standard_normal((len(lens), heads, hd)) * 2.0 ** power).astype(np.float32)
+        got = dev.attention(torch.from_numpy(q).cuda()).cpu().numpy().reshape(q.shape)
+        for s, n in enumerate(lens):
+            for j in range(heads):
+                k, v = kv[s, j // G]
+                q64 = q[s, j].astype(np.float64)
+                score, dot = k @ q64 / np.sqrt(hd), np.abs(k) @ np.abs(q64) / np.sqrt(hd)
+                order = np.argsort(score)
+                apart = score[order[-1]] - score[order[-2]] if n > 1 else np.inf
+                if apart <= 2 * ((hd // 16 + 3) * 2 * U + 2.0 ** -22) * dot.max() + 60:
+                    continue                       # (two keys that near: which one wins is not defined)
+                want = v[order[-1]]
+                err = np.abs(got[s, j] - want)
+                assert (err <= 2.0 ** -21 * np.abs(want)).all(), (power, n, j, got[s, j][:4], want[:4])
+                checked += 1
+    assert checked >= 0.99 * len(powers) * len(lens) * heads
+    assert int(dev.error.cpu()[0]) == 0
