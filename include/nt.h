@@ -452,8 +452,8 @@ nt_status nt_kv4_extend(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq
  * dev_src[i] (dev_keep NULL: all of them): the full pages are shared, a partly
  * filled last one is copied into the lowest free page.  A source may be listed
  * several times, a destination once; a destination may be no source.  If any entry
- * is invalid or the free pages do not suffice, the call changes nothing but
- * *error. */
+ * is invalid, a page of a source's kept positions is out of range or held by nobody (refs
+ * below 1), or the free pages do not suffice, the call changes nothing but *error. */
 nt_status nt_kv4_fork(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
                       const int32_t* dev_keep, void* dev_workspace, size_t workspace_bytes, void* stream);
 

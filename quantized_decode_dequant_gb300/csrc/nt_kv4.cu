@@ -503,12 +503,12 @@ struct Kv4PlanArgs {
   int32_t* free;
 };
 
-// The plan of an extend (FORK = false) or a fork, by one CTA: checks every entry,
-// counts the pages it takes, finds that many free pages, the lowest first, and
+// The plan of an extend (FORK = false) or a fork, by one CTA: checks every entry and
+// every page that it will share or copy, counts the pages it takes, finds that many free pages, the lowest first, and
 // writes their table entries and counts, and (extend) the lengths.  Nothing is changed unless every
 // entry is valid and the free pages suffice.  The pages to copy go to `pair`.
 template <bool FORK>
-__global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
+__global__ void __launch_bounds__(1024, 1) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
   __shared__ uint32_t set[kKv4MaxSeqs / 32];                  // sequences listed (fork: destinations)
   __shared__ uint32_t s_bad;
   __shared__ int s_pairs;
@@ -516,7 +516,12 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
   for (int i = t; i < kKv4MaxSeqs / 32; i += 1024) set[i] = 0u;
   if (t == 0) { s_bad = 0u; s_pairs = 0; }
   kv4_dependent();
-  const int refs0 = t < c.n_pages ? c.refs[t] : 1;   // of the first pages, while the entries are checked
+  // (fork) 2^lg threads look at a source's full pages: all 1024 shared out to the entries, at least 8 each, the last threads first
+  const int ceil_lg = 32 - __clz(a.n - 1), lg = ceil_lg < 7 ? 10 - ceil_lg : 3;
+  const int i_pages = (1023 - t) >> lg, j_pages = (1023 - t) & ((1 << lg) - 1);
+  // on the way while the entries are checked: counts of the first pages, and (fork) the sources that this thread begins with
+  const int refs0 = t < c.n_pages ? c.refs[t] : 1;
+  const int src0 = FORK && t < a.n ? a.a[t] : 0, src1 = FORK && i_pages < a.n ? a.a[i_pages] : 0;
   __syncthreads();
   const int32_t* listed = FORK ? a.b : a.a;
   for (int i = t; i < a.n; i += 1024) {
@@ -525,6 +530,22 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
       atomicOr(&s_bad, NT_KV4_BAD_SEQ);
   }
   __syncthreads();
+  if (FORK) {   // the full pages to be shared
+    for (int i = i_pages; i < a.n; i += 1024 >> lg) {
+      const int s = i == i_pages ? src1 : a.a[i];
+      if (s < 0 || s >= c.max_seqs) continue;
+      const int n = c.len[s], keep = a.keep ? a.keep[i] : n, full = keep / c.page_len;
+      if (n > c.capacity() || keep > n) continue;
+      const int32_t* row = c.table + int64_t(s) * c.max_pages;
+      bool bad = false;
+#pragma unroll 4
+      for (int j = j_pages; j < full; j += 1 << lg) {
+        const int p = row[j];
+        bad |= p < 0 || p >= c.n_pages || c.refs[p] < 1;
+      }
+      if (bad) atomicOr(&s_bad, NT_KV4_BAD_PAGE);
+    }
+  }
   int64_t run = 0;   // pages taken by the entries before
   for (int i0 = 0; i0 < a.n; i0 += 1024) {
     const int i = i0 + t;
@@ -532,7 +553,7 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
     int from = -1;
     uint32_t bad = 0;
     if (i < a.n) {
-      const int s = a.a ? a.a[i] : i;   // the sequence read from
+      const int s = FORK && i == t ? src0 : a.a ? a.a[i] : i;   // the sequence read from
       if (s < 0 || s >= c.max_seqs) {
         bad = NT_KV4_BAD_SEQ;
       } else {
@@ -545,7 +566,7 @@ __global__ void __launch_bounds__(1024) k_kv4_plan(Kv4 c, Kv4PlanArgs a) {
           if (keep < 0 || keep > n) bad |= NT_KV4_BAD_LEN;
           if (!bad && keep % c.page_len) {
             from = c.table[int64_t(s) * c.max_pages + keep / c.page_len];
-            if (from < 0 || from >= c.n_pages) bad |= NT_KV4_BAD_PAGE;
+            if (from < 0 || from >= c.n_pages || c.refs[from] < 1) bad |= NT_KV4_BAD_PAGE;
             need = 1;
           }
         } else {
@@ -724,10 +745,9 @@ __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_apply(Kv4 c, Kv4PlanArg
       const int32_t* from = c.table + int64_t(s) * c.max_pages;
       int32_t* to = c.table + int64_t(d) * c.max_pages;
       for (int j = threadIdx.x - kFirst; j < full; j += kKv4CopyThreads - kFirst) {
-        const int p = from[j];
+        const int p = from[j];   // (the plan has checked it)
         to[j] = p;
-        if (p >= 0 && p < c.n_pages) atomicAdd(&c.refs[p], 1);
-        else kv4_flag(c, NT_KV4_BAD_PAGE);
+        atomicAdd(&c.refs[p], 1);
       }
       if (threadIdx.x == kFirst) c.len[d] = keep;
     }

@@ -1020,3 +1020,38 @@ def test_attention_where_scores_are_huge(nt, hd, G, capacity):
                 checked += 1
     assert checked >= 0.99 * len(powers) * len(lens) * heads
     assert int(dev.error.cpu()[0]) == 0
+
+
+# ------------------------------------------------------------ forks of damaged tables --
+
+@pytest.mark.parametrize("what", ["low", "high", "unheld"])
+@pytest.mark.parametrize("where", ["first", "last full", "tail", "far"])
+def test_fork_of_a_damaged_source_changes_nothing(nt, what, where):
+    """A page of a source that is out of range or that nobody holds, among full pages or the partly filled one: nothing
+    changes but the error word, whichever entry of the call it is."""
+    rng = np.random.default_rng(17)
+    pages = 70 if where == "far" else 5
+    for entry in (0, 1, 37, 39):
+        ref = R.RefCache(2, 1, 64, 16, 200, 60, 80)
+        ref.randomize(rng)
+        ref.hold([16 * pages - 7, 33, 40], rng)
+        slot = {"first": 0, "last full": pages - 2, "tail": pages - 1, "far": 67}[where]
+        if what == "unheld":
+            low = ref.free_pages(1)[0]             # the page that the call would take first
+            old = ref.table[0, slot]
+            ref.refs[old], ref.table[0, slot] = 0, low if low < old else old
+        else:
+            ref.table[0, slot] = -3 if what == "low" else ref.P
+        src = [1, 2] * 20
+        src[entry] = 0
+        dst = list(range(10, 50))
+        dev = Dev(nt, ref)
+        dev.fork(src, dst)
+        ref.error = R.BAD_PAGE
+        dev.check(R.BAD_PAGE)
+        # what lies behind the positions that are kept is not looked at
+        keep = [16 * slot if s == 0 else int(ref.len[s]) for s in src]
+        for x in (ref, dev):
+            x.fork(src, dst, keep)
+        dev.check(R.BAD_PAGE)
+        assert (ref.len[10:50] == keep).all()
