@@ -487,10 +487,11 @@ nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t*
  * starts at element r * row_stride + g * head_stride of dev_k and of dev_v (f32 or f16 by
  * `type`: NT_F32, NT_F16; both strides multiples of 16 bytes), head_dim elements
  * each: a projection's [row][kv head][dim] as well as an f16 cache's [kv
- * head][position][dim].  n_rows / 16 + 2 n is at most 2^26.  An entry is passed over where its sequence is out of
- * range, it has more rows than the sequence positions or rows outside [0, n_rows);
- * rows are where their page is out of range or not held by this sequence alone
- * (refs other than 1).
+ * head][position][dim].  n_rows / 16 + 2 n is at most 2^26, and n_kv_heads times that (and 1)
+ * 2^32 - 2^17.  An entry is passed over where its sequence is out of range, it has more rows than the sequence positions or rows outside [0, n_rows) (dev_begin
+ * NULL: entry i's row is row i), or its range runs backwards (rows of other entries
+ * may be passed over then too); rows are where their page is out of range or not held by this
+ * sequence alone (refs other than 1).  With n_rows = 0 the lists are not looked at.
  * A sequence listed twice is flagged; which of its rows are stored is not defined. */
 nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
                         const int32_t* dev_begin, int32_t n_rows, nt_qtype type, const void* dev_k, const void* dev_v,

@@ -76,7 +76,7 @@ static cudaError_t kv4_launch(K kern, unsigned grid, unsigned block, cudaStream_
 }
 
 struct Kv4Rows {
-  int32_t layer, n, n_rows, units;
+  int32_t layer, n, n_rows, units, checks;
   const int32_t* seq;
   const int32_t* begin;
   int64_t row_stride, head_stride;
@@ -87,6 +87,25 @@ struct Kv4Rows {
 struct Kv4Span {
   int s, p0, first, last, row;
 };
+
+// Flags entries whose rows do not all lie within the call's: their units may be none of the call's.  CTAs of their own
+// do it, the grid's first a.checks, so that no warp with rows waits for it.  (16 tokens and 2 x 20011
+// f16 rows stored and read back, 5.04 and 71.0 us without: so 5.16 and 71.2; by the warps with rows, at their start or
+// end, 5.16 to 5.72 and 71.5 to 75.0.)  Without `begin` there is one such CTA where there
+// are more entries than rows.
+constexpr int kKv4CheckEntries = 1024;   // of a CTA
+__device__ __forceinline__ bool kv4_check_rows(const Kv4& c, const Kv4Rows& a) {
+  if (int(blockIdx.x) >= a.checks) return false;
+  bool bad = !a.begin;
+  const int e1 = (int(blockIdx.x) + 1) * kKv4CheckEntries;   // (2^25 entries at most)
+  if (a.begin)
+    for (int i = e1 - kKv4CheckEntries + int(threadIdx.x); i < e1 && i < a.n; i += blockDim.x) {
+      const int b0 = a.begin[i], b1 = a.begin[i + 1];
+      bad |= b0 != b1 && (b0 < 0 || b1 < b0 || b1 > a.n_rows);
+    }
+  if (bad) kv4_flag(c, NT_KV4_BAD_LEN);
+  return true;
+}
 
 // Unit u of the call: a chunk that entry i's rows may touch.  Entry i's units start
 // at begin[i] / 16 + 2 i: r rows touch at most r / 16 + 2 chunks, so they do not
@@ -112,11 +131,7 @@ __device__ __forceinline__ bool kv4_span(const Kv4& c, const Kv4Rows& a, int u, 
     b0 = a.begin[i];
     b1 = a.begin[i + 1];
     start = b0 / kKv4Chunk + 2 * i;
-    if (b1 <= b0) return false;
-    if (b0 < 0 || b1 > a.n_rows) {
-      if (lane == 0 && u == start) kv4_flag(c, NT_KV4_BAD_LEN);
-      return false;
-    }
+    if (b1 <= b0 || b0 < 0 || b1 > a.n_rows) return false;
   } else if (u >= a.n) {
     return false;
   }
@@ -303,12 +318,13 @@ __global__ void __launch_bounds__(32 * kKv4RowWarps) k_kv4_append(Kv4 c, Kv4Rows
   constexpr int NG = L::NG, NB = NG / 2;             // blocks of a lane
   __shared__ __align__(16) uint8_t s_codes[kKv4RowWarps][8 * HD];
   const int lane = threadIdx.x & 31;
-  const int64_t id = int64_t(blockIdx.x) * kKv4RowWarps + (threadIdx.x >> 5);
+  const int64_t id = (int64_t(blockIdx.x) - a.checks) * kKv4RowWarps + (threadIdx.x >> 5);   // (below 0: see kv4_check_rows)
   const int g = int(id / 2 % c.n_kv);
   const int64_t u = id / 2 / c.n_kv;
   const bool is_v = id & 1;
   if (u >= a.units) return;
   kv4_dependent();
+  if (kv4_check_rows(c, a)) return;
   Kv4Span sp;
   if (!kv4_span(c, a, int(u), &sp)) return;
   const T* src = (is_v ? v : k) + int64_t(sp.row - sp.first) * a.row_stride + int64_t(g) * a.head_stride;   // of position 0
@@ -380,11 +396,12 @@ __global__ void __launch_bounds__(32 * kKv4RowWarps) k_kv4_read(Kv4 c, Kv4Rows a
   using L = Kv4Chunk<HD>;
   constexpr int NG = L::NG;
   const int lane = threadIdx.x & 31, gi = lane >> 2, tg = lane & 3;
-  const int64_t id = int64_t(blockIdx.x) * kKv4RowWarps + (threadIdx.x >> 5);
+  const int64_t id = (int64_t(blockIdx.x) - a.checks) * kKv4RowWarps + (threadIdx.x >> 5);   // (below 0: see kv4_check_rows)
   const int g = int(id / 2 % c.n_kv);
   const int64_t u = id / 2 / c.n_kv;
   if (u >= a.units) return;
   kv4_dependent();
+  if (kv4_check_rows(c, a)) return;
   Kv4Span sp;
   if (!kv4_span(c, a, int(u), &sp)) return;
   const uint8_t* chunk = kv4_span_chunk(c, a, sp, g, false);
@@ -946,13 +963,20 @@ static int32_t kv4_units(int32_t n, int32_t n_rows, const int32_t* begin) {
   return n < 0 || n_rows < 0 || u > (1 << 26) ? 0 : int32_t(u);
 }
 
+// CTAs that look over the entries.
+static int32_t kv4_checks(int32_t n, int32_t n_rows, const int32_t* begin) {
+  return begin ? int32_t((int64_t(n) + kKv4CheckEntries - 1) / kKv4CheckEntries) : n > n_rows;
+}
+
 static nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a, nt_qtype type, const void* pk, const void* pv) {
   auto bad = [&](const char* what) { return fail(NT_E_INVAL, std::string(who) + ": " + what); };
   if (type != NT_F32 && type != NT_F16) return bad("type must be NT_F32 or NT_F16");
   if (a.layer < 0 || a.layer >= k.n_layers) return bad("layer out of range");
   if (a.n < 0 || (!a.seq && a.n > k.max_seqs)) return bad("n out of range");
   if (a.n_rows < 0) return bad("n_rows must not be negative");
-  if (int64_t(a.units) * k.n_kv > (int64_t(1) << 32) || (a.n && a.n_rows && !a.units)) return bad("n_rows / 16 + 2 n above 2^26");
+  if (a.n && a.n_rows && !a.units) return bad("n_rows / 16 + 2 n above 2^26");
+  if (int64_t(a.units) * k.n_kv > (int64_t(1) << 32) - (1 << 17))   // (so that a.units n_kv / 2 + a.checks CTAs are a grid)
+    return bad("n_kv_heads (n_rows / 16 + 2 n) above 2^32 - 2^17");
   const int64_t es = type == NT_F32 ? 4 : 2, most = int64_t(1) << 40;
   if (a.row_stride < 0 || a.head_stride < 0 || a.row_stride > most || a.head_stride > most || a.row_stride * es % 16 ||
       a.head_stride * es % 16)
@@ -1106,7 +1130,7 @@ nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const i
   const char* who = "nt_kv4_append";
   Kv4 k;
   nt_status st = kv4_check(c, who, true, &k);
-  const Kv4Rows a{layer, n, n_rows, kv4_units(n, n_rows, dev_begin), dev_seq, dev_begin, row_stride, head_stride};
+  const Kv4Rows a{layer, n, n_rows, kv4_units(n, n_rows, dev_begin), kv4_checks(n, n_rows, dev_begin), dev_seq, dev_begin, row_stride, head_stride};
   if (!st) st = kv4_rows_check(who, k, a, type, dev_k, dev_v);
   if (!st && n > k.max_seqs) st = fail(NT_E_INVAL, "nt_kv4_append: n above max_seqs");
   if (!st) st = kv4_array_check(k, who, dev_seq, n, true, nullptr, 0);
@@ -1117,7 +1141,7 @@ nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const i
   if (kv4_meets_cache(k, dev_k, bytes) || kv4_meets_cache(k, dev_v, bytes))
     return fail(NT_E_INVAL, "nt_kv4_append: k or v overlaps the cache");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv4RowWarps - 1) / kKv4RowWarps);
+  const unsigned grid = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv4RowWarps - 1) / kKv4RowWarps + a.checks);
   if (type == NT_F32) {
     const float *pk = static_cast<const float*>(dev_k), *pv = static_cast<const float*>(dev_v);
     NT_CUDA(k.hd == 64 ? kv4_launch(k_kv4_append<64, float>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv) : kv4_launch(k_kv4_append<128, float>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv));
@@ -1137,7 +1161,7 @@ nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int
   const char* who = "nt_kv4_read";
   Kv4 k;
   nt_status st = kv4_check(c, who, true, &k);
-  const Kv4Rows a{layer, n, n_rows, kv4_units(n, n_rows, dev_begin), dev_seq, dev_begin, row_stride, head_stride};
+  const Kv4Rows a{layer, n, n_rows, kv4_units(n, n_rows, dev_begin), kv4_checks(n, n_rows, dev_begin), dev_seq, dev_begin, row_stride, head_stride};
   if (!st) st = kv4_rows_check(who, k, a, type, dev_k, dev_v);
   if (!st) st = kv4_array_check(k, who, dev_seq, n, true, nullptr, 0);
   if (!st) st = kv4_array_check(k, who, dev_begin, int64_t(n) + 1, true, nullptr, 0);
@@ -1152,7 +1176,7 @@ nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int
       kv4_overlap(dev_begin, int64_t(n) * 4 + 4, dev_k, bytes) || kv4_overlap(dev_begin, int64_t(n) * 4 + 4, dev_v, bytes))
     return fail(NT_E_INVAL, "nt_kv4_read: an output overlaps another buffer");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv4RowWarps - 1) / kKv4RowWarps);
+  const unsigned grid = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv4RowWarps - 1) / kKv4RowWarps + a.checks);
   if (type == NT_F32) {
     float *pk = static_cast<float*>(dev_k), *pv = static_cast<float*>(dev_v);
     NT_CUDA(k.hd == 64 ? kv4_launch(k_kv4_read<64, float>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv) : kv4_launch(k_kv4_read<128, float>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv));

@@ -1055,3 +1055,73 @@ def test_fork_of_a_damaged_source_changes_nothing(nt, what, where):
             x.fork(src, dst, keep)
         dev.check(R.BAD_PAGE)
         assert (ref.len[10:50] == keep).all()
+
+
+# ------------------------------------------------------------ row ranges that do not fit --
+
+BIG = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("begin,good", [
+    ([3, 1, 5], [1]), ([6, 0], []), ([-100, -90], []), ([-100, 2], []), ([-1, 0, 3], [1]), ([100, 110], []),
+    ([2, 7], []), ([0, 2, 7], [0]), ([1 << 30, BIG], []), ([-BIG - 1, BIG], []), ([0, 1, BIG, BIG], [0]),
+    ([BIG, -BIG], []), ([0, 2, 2, 2, 4, 9], [0, 3])])
+def test_row_ranges_outside_the_rows_are_flagged(nt, begin, good):
+    """Ranges that run backwards, begin before the rows or end behind them, wholly or partly: a bit in the error word, and
+    neither their rows nor the cache are touched; entries beside them that fit are stored and read."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(12)
+    ref = R.RefCache(1, 1, 64, 16, 16, 5, 4, fill=3)
+    ref.hold([40, 33, 20, 50, 64], rng)
+    dev = Dev(nt, ref)
+    x = _rows(rng, 6, 1, 64)
+    k, v = _layout(torch, x, "rows")
+    dev.rows(k, v, begin)
+    for i in good:
+        _store(ref, x, [begin[i], begin[i + 1]], [i])
+    ref.error = R.BAD_LEN
+    dev.check(R.BAD_LEN)
+    dev.error.zero_()
+    out = torch.full((2, 6, 1, 64), 5.5, device="cuda")
+    dev.rows(out[0], out[1], begin, read=True)
+    want = np.full(out.shape, 5.5)
+    for i in good:
+        for side in (0, 1):
+            want[side, begin[i]:begin[i + 1]] = R.values(*R.quantize(x[side, begin[i]:begin[i + 1]]))
+    np.testing.assert_array_equal(out.cpu().numpy().astype(np.float64), want)
+    dev.check(R.BAD_LEN)
+
+
+def test_empty_row_ranges_are_no_fault(nt):
+    """Entries without rows, wherever they stand, have none outside."""
+    torch = torch_cuda()
+    ref = R.RefCache(1, 1, 64, 16, 8, 3, 2, fill=3)
+    ref.hold([20, 3, 0])
+    dev = Dev(nt, ref)
+    x = _rows(np.random.default_rng(1), 3, 1, 64)
+    k, v = _layout(torch, x, "rows")
+    for begin in ([0, 0, 0], [3, 3, 3, 3], [9, 9], [-4, -4], [0, 2, 2, 2]):
+        dev.rows(k, v, begin)
+        _store(ref, x, [0, begin[1] if begin[0] == 0 else 0], [0])
+        dev.check()
+
+
+def test_more_entries_than_rows_without_ranges_are_flagged(nt):
+    torch = torch_cuda()
+    rng = np.random.default_rng(13)
+    ref = R.RefCache(1, 1, 64, 16, 400, 300, 2, fill=3)
+    ref.hold([1 + s % 5 for s in range(300)], rng)
+    x = _rows(rng, 2, 1, 64)
+    for n in (3, 300):
+        dev = Dev(nt, ref)
+        k, v = _layout(torch, x, "rows")
+        nt.nt_kv4_append(dev.c, 0, n, None, None, 2, "f32", k.data_ptr(), v.data_ptr(), 64, 64, dev.stream())
+        _store(ref, x, [0, 1, 2], [0, 1])
+        ref.error = R.BAD_LEN
+        dev.check(R.BAD_LEN)
+        dev.error.zero_()
+        out = torch.full((2, 2, 1, 64), 5.5, device="cuda")
+        nt.nt_kv4_read(dev.c, 0, n, None, None, 2, "f32", out[0].data_ptr(), out[1].data_ptr(), 64, 64, dev.stream())
+        want = np.stack([R.values(*R.quantize(y)) for y in x])
+        np.testing.assert_array_equal(out.cpu().numpy().astype(np.float64), want)
+        dev.check(R.BAD_LEN)
