@@ -475,7 +475,8 @@ nt_status nt_kv4_copy_pages(const nt_kv4_cache* c, int32_t n, const int32_t* dev
  * [n_pages] receive the table and counts that go with it; each is either the
  * cache's own array or one that does not overlap it (the cache then still
  * describes the state before: moved pages keep their old bytes until they are
- * taken).  dev_live: L.  Table entries out of range are copied as they are. */
+ * taken).  dev_live: L.  Table entries other than -1 that are out of range
+ * are copied as they are, those that name a free page become -1; both set NT_KV4_BAD_PAGE. */
 nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t* dev_refs_out, int32_t* dev_live,
                          void* dev_workspace, size_t workspace_bytes, void* stream);
 

@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_copy_pages(Kv4 c, int n
 }
 
 // The plan of a compaction by one CTA: L, the pages in use; `to[p]`, where page p
-// goes (itself, or -2 for a free page below L, which receives another); the moves
+// goes (or -2 for a free page below L, which receives another, -3 for one from L on); the moves
 // in `pair`, the k-th page in use from L on to the k-th free page below.
 __global__ void __launch_bounds__(1024) k_kv4_compact_plan(Kv4 c, int32_t* go, int2* pair, int32_t* to, int32_t* live) {
   const int t = threadIdx.x;
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(1024) k_kv4_compact_plan(Kv4 c, int32_t* go, i
     const int64_t h = holes + kv4_scan(hole ? 1 : 0, &nh), m = movers + kv4_scan(mover ? 1 : 0, &nm);
     if (hole) pair[h].y = int32_t(p);
     if (mover) pair[m].x = int32_t(p);
-    if (in) to[p] = hole ? -2 : int32_t(p);
+    if (in) to[p] = hole ? -2 : (use ? int32_t(p) : -3);
     holes += nh;
     movers += nm;
   }
@@ -886,17 +886,19 @@ __global__ void __launch_bounds__(kKv4CopyThreads) k_kv4_compact_apply(Kv4 c, co
   for (int64_t p = first; p < c.n_pages; p += step) {
     const int d = to[p], r = c.refs[p];
     if (d == -2) continue;                     // the page that moves here writes it
-    if (d != int(p)) refs_out[d] = r;
-    refs_out[p] = d == int(p) ? r : 0;
+    if (d >= 0 && d != int(p)) refs_out[d] = r;
+    refs_out[p] = d < 0 || d == int(p) ? r : 0;
   }
   for (int64_t e = first; e < int64_t(c.max_seqs) * c.max_pages; e += step) {
     int p = c.table[e];
-    if (p >= c.n_pages) kv4_flag(c, NT_KV4_BAD_PAGE);
-    else if (p >= 0) {
+    bool bad = p < -1 || p >= c.n_pages;
+    if (p >= 0 && !bad) {
       p = to[p];
-      if (p < 0) kv4_flag(c, NT_KV4_BAD_PAGE);   // an entry that names a free page: it holds nothing
+      bad = p < 0;               // it names a free page: it holds nothing
+      if (bad) p = -1;
     }
-    table_out[e] = p == -2 ? -1 : p;
+    if (bad) kv4_flag(c, NT_KV4_BAD_PAGE);
+    table_out[e] = p;
   }
 }
 

@@ -1125,3 +1125,40 @@ def test_more_entries_than_rows_without_ranges_are_flagged(nt):
         want = np.stack([R.values(*R.quantize(y)) for y in x])
         np.testing.assert_array_equal(out.cpu().numpy().astype(np.float64), want)
         dev.check(R.BAD_LEN)
+
+
+def test_compact_copies_entries_that_name_no_page(nt):
+    """Table entries out of range, below as well as above, come out as they are and are flagged; -1 is nothing of note."""
+    ref = _cache(10)
+    ref.hold([96, 20, 50], np.random.default_rng(4))
+    dev = Dev(nt, ref)
+    for x in (ref, dev):
+        x.free([1])                                    # holes
+    odd = {(4, 0): -2, (4, 1): -3, (5, 2): -(1 << 31), (6, 5): ref.P, (7, 5): (1 << 31) - 1}
+    kept = ref.table.copy()
+    table, refs, live = ref.compact()
+    ref.table, ref.refs = table, refs
+    for at, p in odd.items():
+        assert kept[at] == -1
+        ref.table[at] = p
+        dev.table[at] = p
+    assert dev.compact() == live
+    ref.error = R.BAD_PAGE
+    dev.check(R.BAD_PAGE)
+
+
+def test_compact_drops_entries_that_name_free_pages(nt):
+    """Below the number of pages in use as well as behind it: an entry of a page that nobody holds becomes -1."""
+    ref = _cache(11)
+    ref.hold([96, 20, 50], np.random.default_rng(5))
+    ref.free([1])
+    used = int((ref.refs > 0).sum())
+    free = ref.free_pages(ref.P)
+    assert free[0] < used <= free[-1]
+    dev = Dev(nt, ref)
+    dev.table[5, 0], dev.table[5, 1] = free[0], free[-1]
+    table, refs, live = ref.compact()
+    ref.table, ref.refs = table, refs
+    assert dev.compact() == live == used
+    ref.error = R.BAD_PAGE
+    dev.check(R.BAD_PAGE)
