@@ -1001,7 +1001,8 @@ static bool kv4_rows_meet(const Kv4& k, const Kv4Rows& a, int64_t es, int64_t d,
   const int64_t rs = a.row_stride * es, hs = a.head_stride * es, w = k.hd * es;
   for (int64_t h = -(k.n_kv - 1); h <= k.n_kv - 1; h++) {
     const int64_t x = d + h * hs;                 // then + r rs, r in (-n_rows, n_rows)
-    int64_t r0 = rs ? -x / rs : 0;                // near the row difference that brings it to 0
+    int64_t r0 = rs ? -x / rs : 0;                // near the row difference that brings it to 0, or the nearest there is
+    r0 = r0 < 1 - int64_t(a.n_rows) ? 1 - int64_t(a.n_rows) : (r0 > int64_t(a.n_rows) - 1 ? int64_t(a.n_rows) - 1 : r0);
     for (int64_t r = r0 - 1; r <= r0 + 1; r++) {
       if (r <= -int64_t(a.n_rows) || r >= a.n_rows || (same && r == 0 && h == 0)) continue;
       const int64_t y = x + r * rs;

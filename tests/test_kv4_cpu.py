@@ -194,3 +194,30 @@ def test_rows_that_interleave_are_not_taken_for_overlapping(built):
         nt.nt_kv4_read(cache(), 0, 2, A, Q + 4, 3, "f32", Q, Q + 512, 256, 64)   # dev_begin inside the output
     assert "another buffer" in str(ei.value)
     assert lib.nt_last_error()
+
+
+def _meet(begin_k, begin_v, rows, kv, hd, es, rs, hs):
+    """Whether two (row, kv head) vectors of K and V, or of one of them, share bytes: every pair of them."""
+    at = np.add.outer(np.arange(rows) * rs, np.arange(kv) * hs).reshape(-1) * es
+    at = np.sort(np.concatenate([begin_k + at, begin_v + at]))
+    return bool((np.diff(at) < hd * es).any())
+
+
+def test_read_refuses_exactly_the_outputs_that_overlap(built):
+    """Strides of every kind, small ones and few rows among them (a row stride plays no part with a single row)."""
+    rng = np.random.default_rng(3)
+    seen = [0, 0]
+    for _ in range(4000):
+        half, rows, kv = bool(rng.integers(2)), int(rng.choice([1, 1, 2, 3, 5])), int(rng.choice([1, 2, 3]))
+        es = 2 if half else 4
+        unit = 16 // es
+        rs, hs = (int(rng.choice([0, unit, 3 * unit, 5 * unit, 40, 64, 72, 64 * kv, 128 * kv, 64 * kv + unit, 64 * rows])) for _ in "rh")
+        apart = int(rng.choice([16, 80, 64 * es, 64 * es * kv, 64 * es * kv * rows, 128 * es, 1 << 16, 64 * es - 16])) * int(rng.choice([-1, 1]))
+        want = _meet(Q, Q + apart, rows, kv, 64, es, rs, hs)
+        seen[want] += 1
+        c = cache(n_kv_heads=kv)
+        # a list inside the outputs is refused after their own overlap: either message, no launch
+        with pytest.raises(nt.NtError) as ei:
+            nt.nt_kv4_read(c, 0, 1, A, Q, rows, "f16" if half else "f32", Q, Q + apart, rs, hs)
+        assert ("rows of the outputs" in str(ei.value)) == want, (half, rows, kv, rs, hs, apart)
+    assert min(seen) > 500
