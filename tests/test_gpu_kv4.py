@@ -1162,3 +1162,128 @@ def test_compact_drops_entries_that_name_free_pages(nt):
     assert dev.compact() == live == used
     ref.error = R.BAD_PAGE
     dev.check(R.BAD_PAGE)
+
+
+# ------------------------------------------------------------ long sequences, as a whole --
+
+def _rel_limit(k, q, hd):
+    """What |got - want| / |want| over a head's outputs may be for values of mean zero that the weights' errors know nothing
+    of.  With out = sum w V, relative errors e of the weights move it by sum w e (V - out), in the mean square by the root
+    mean square of e times |out|.  e is the scores' error (see _bound) and 2^-22 each of the exponential and the split.  A sum
+    is held over at most 64 additions in the matrix products (truncated, 2^-23 of the sum so far, which is half the final one
+    in the mean) and then goes through at most 67 that round to nearest, each its own way: sqrt(67) u."""
+    dot = np.abs(k) @ np.abs(q) / np.sqrt(hd)
+    ds = ((hd // 16 + 3) * 2 * U + 2.0 ** -22) * dot + 6 * U * np.abs(k @ q / np.sqrt(hd))
+    return np.sqrt((ds * ds).mean()) + 2 * 2.0 ** -22 + 64 / 2 * 2.0 ** -23 + np.sqrt(67) * U
+
+
+def _balanced(ref, rng):
+    """Random codes 1..15, the values' mean zero."""
+    ref.randomize(rng)
+    codes = ref.pool.reshape(ref.L, ref.P, ref.n_kv, ref.pl // 16, -1)[..., :16 * ref.hd]
+    codes[:] = rng.integers(1, 16, codes.shape, np.uint8) | rng.integers(1, 16, codes.shape, np.uint8) << 4
+
+
+# (n_kv, G, hd, page_len, capacity, lengths)
+LONG = [
+    (1, 8, 128, 64, 131136, [131077]),        # one item across every CTA
+    (1, 16, 128, 64, 131136, [131077]),
+    (1, 4, 128, 64, 131136, [131077]),
+    (1, 8, 64, 16, 131136, [131077]),
+    (4, 8, 128, 48, 131136, [131077]),
+    (4, 4, 128, 256, 131328, [131077]),
+    (2, 1, 64, 128, 131200, [131077, 70000, 129]),
+    (2, 16, 64, 64, 131136, [131077, 40001]),
+    (3, 8, 128, 64, 33024, [33001, 2047, 20000, 1]),
+    (8, 8, 128, 64, 4224, [4161]),            # a cluster per item
+    (8, 4, 128, 32, 9024, [9001, 5000, 4097]),
+]
+
+
+@pytest.mark.parametrize("n_kv,G,hd,page_len,capacity,lens", LONG)
+def test_attention_of_long_sequences_misses_nothing(nt, n_kv, G, hd, page_len, capacity, lens):
+    """Weights of the same size, so that every position counts: a position left out anywhere, or the lower terms of queries or
+    weights, would show at many times what is allowed."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([127, n_kv, G, hd])
+    pages = sum(-(-n // page_len) for n in lens)
+    ref = R.RefCache(1, n_kv, hd, page_len, pages + 2, len(lens), capacity // page_len)
+    _balanced(ref, rng)
+    ref.hold(lens, rng)
+    heads = n_kv * G
+    dev = Dev(nt, ref, heads)
+    q = (rng.standard_normal((len(lens), heads, hd)) * 0.3).astype(np.float32)
+    got = dev.attention(torch.from_numpy(q).cuda()).cpu().numpy().reshape(q.shape)
+    assert int(dev.error.cpu()[0]) == 0
+    worst = 0.0
+    for s, n in enumerate(lens):
+        for g in range(n_kv):
+            k, v = ref.kv(0, s, g)
+            for j in range(g * G, (g + 1) * G):
+                qj = q[s, j].astype(np.float64)
+                want, limit = R.attend(qj, k, v), _rel_limit(k, qj, hd)
+                size = np.linalg.norm(want)
+                rel = np.linalg.norm(got[s, j] - want) / size
+                assert rel <= limit, (n, j, rel, limit)
+                worst = max(worst, rel)
+                if j % G == 0 and n > 2000:
+                    for lost in (0, n // 3, n - 1):
+                        less = R.attend(qj, np.delete(k, lost, 0), np.delete(v, lost, 0)) if n < 20000 else (
+                            want - (v[lost] - want) * np.exp(k[lost] @ qj / np.sqrt(hd)) / np.exp(k @ qj / np.sqrt(hd)).sum())
+                        assert np.linalg.norm(less - want) > 20 * limit * size, (n, lost)
+                    coarse = qj.astype(np.float16).astype(np.float64)
+                    assert np.linalg.norm(R.attend(coarse, k, v) - want) > 2 * limit * size
+                    p = np.exp(k @ qj / np.sqrt(hd) - 1)
+                    assert np.linalg.norm(p.astype(np.float16).astype(np.float64) @ v / p.sum() - want) > 2 * limit * size
+    print(f"kv {n_kv} G {G} hd {hd} page {page_len} lengths {lens}: rel L2 {worst:.2e}, allowed {limit:.2e}")
+
+
+@pytest.mark.parametrize("n_kv,G,hd,page_len,capacity,lens", [x for x in LONG if x[0] < 8])
+def test_attention_of_long_sequences_with_a_few_positions_that_count(nt, n_kv, G, hd, page_len, capacity, lens):
+    """Every 61st position of the last two thirds, and the last one, has the same key, whose score is 30 and more above all
+    others': the output is the mean of those positions' values.  References move in the middle of the work, and the first
+    third's partial results vanish in the merges.  The others' weights are below 2^-40 of the largest, all 131077 together
+    below 2^-22 of a position that counts.  Equal keys go through the same products, so of the scores' error only the roundings
+    on the way to the exponent are left (6u of the score), then 2^-22 of the exponential, the split and the others, and the sums'
+    as in _rel_limit."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([131, n_kv, G, hd])
+    pages = sum(-(-n // page_len) for n in lens)
+    ref = R.RefCache(1, n_kv, hd, page_len, pages + 2, len(lens), capacity // page_len)
+    _balanced(ref, rng)
+    ref.hold(lens, rng)
+    heads = n_kv * G
+    u = rng.choice([-1.0, 1.0], (n_kv, hd))
+    e, j = np.arange(hd), np.arange(ref.ng)
+    quarter = np.array([0.25], np.float16).view(np.uint8)
+    places = []
+    for s, n in enumerate(lens):
+        t = np.unique(np.append(np.arange(n - 1 - n // 3 * 2, n, 61), n - 1))
+        t = t[t >= 0]
+        places.append(t)
+        page, at = ref.table[s, t // page_len][:, None], (t % page_len)[:, None]
+        for g in range(n_kv):
+            for half in (0, 1):                           # the low and the high codes of a byte: +-7 times 0.25
+                b, sh = ref._k_code(g, at, e[half::2])
+                code = (8 + 7 * u[g, half::2]).astype(np.uint8)
+                old = ref.pool[0][page, b]
+                ref.pool[0][page, b] = (old & (0xF0 if half == 0 else 0x0F)) | (code << (4 * half))
+            b = ref._k_scale(g, at, j)
+            ref.pool[0][page, b], ref.pool[0][page, b + 1] = quarter
+    q = (u.repeat(G, 0) * rng.uniform(3.6, 4.0, (len(lens), heads, 1)) * np.sqrt(128 / hd)).astype(np.float32)
+    dev = Dev(nt, ref, heads)
+    got = dev.attention(torch.from_numpy(q).cuda()).cpu().numpy().reshape(q.shape)
+    assert int(dev.error.cpu()[0]) == 0
+    for s, n in enumerate(lens):
+        for g in range(n_kv):
+            k, v = ref.kv(0, s, g)
+            for h in range(g * G, (g + 1) * G):
+                qh = q[s, h].astype(np.float64)
+                score, t = k @ qh / np.sqrt(hd), places[s]
+                rest = np.delete(score, t)
+                assert np.ptp(score[t]) < 1e-9 and (not len(rest) or score[t[0]] - rest.max() > 30)
+                want, limit = v[t].mean(0), 6 * U * score[t[0]] + 4 * 2.0 ** -22 + 64 / 2 * 2.0 ** -23 + np.sqrt(67) * U
+                assert np.linalg.norm(got[s, h] - want) <= limit * np.linalg.norm(want), (n, h)
+                if len(t) > 1:
+                    less = v[np.delete(t, len(t) // 2)].mean(0)
+                    assert np.linalg.norm(less - want) > 100 * limit * np.linalg.norm(want)
