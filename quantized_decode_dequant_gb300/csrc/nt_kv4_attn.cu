@@ -842,7 +842,7 @@ static cudaError_t kv4_launch_attn(const Kv4& k, const Kv4AttnArgs& a, int64_t m
   const bool whole = pairs <= int64_t(Cfg::NW) * kKv4WholeShare;
   bool tc = false;
   if constexpr (HD == 128 && HB >= 8) {
-    tc = !whole && items * ((pairs + 3) / 4) >= int64_t(kKv4TcTiles) * fit.setup.sms;
+    tc = !whole && items * ((pairs + 3) / 4) >= int64_t(kKv4TcTiles) * fit.setup.sms && kv4_attn_tc_runs(a.G);
     if (tc) e = kv4_launch_attn_tc(k, a, s, &ctas);
   }
   if (!tc) {

@@ -21,7 +21,9 @@ struct Kv4AttnArgs {
   float* part;                         // [CTA][2] partial results
 };
 
-// The attention kernel on tcgen05 (nt_kv4_attn_tc.cu): 128 dimensions, G 8 or 16; *ctas: its CTAs.
+// The attention kernel on tcgen05 (nt_kv4_attn_tc.cu): 128 dimensions, G 8 or 16; *ctas: its CTAs.  Whether it can run is asked
+// first: not where it was compiled for other registers than it shares out (as for a debugger).
+bool kv4_attn_tc_runs(int G);
 cudaError_t kv4_launch_attn_tc(const Kv4& k, const Kv4AttnArgs& a, cudaStream_t s, int* ctas);
 
 // Partial result of one item: o [rows][HD], then (reference m, sum l) per row, then

@@ -572,12 +572,6 @@ static cudaError_t kv4_launch_tc(const Kv4& k, const Kv4AttnArgs& a, int64_t mos
   using Cfg = Kv4TcCfg<HB>;
   static const KernelSetup setup = kernel_setup(k_kv4_attn_tc<HB>, Cfg::kSmem);
   if (setup.err != cudaSuccess) return setup.err;
-  static const cudaError_t shared = [] {   // the registers that the block shares out again are those it is launched with
-    cudaFuncAttributes f;
-    const cudaError_t e = cudaFuncGetAttributes(&f, k_kv4_attn_tc<HB>);
-    return e != cudaSuccess ? e : f.numRegs == Cfg::kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
-  }();
-  if (shared != cudaSuccess) return shared;
   const int64_t useful = (most_units + Cfg::kGroups - 1) / Cfg::kGroups;
   int64_t n = setup.sms < kKv4AttnMaxCtas ? setup.sms : kKv4AttnMaxCtas;
   if (n > useful) n = useful;
@@ -593,6 +587,19 @@ static cudaError_t kv4_launch_tc(const Kv4& k, const Kv4AttnArgs& a, int64_t mos
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k_kv4_attn_tc<HB>, k, a);
+}
+
+// The registers that a block shares out again have to be those it is launched with: an increase past them waits for ever.
+template <int HB>
+static bool kv4_tc_runs() {
+  cudaFuncAttributes f;
+  if (cudaFuncGetAttributes(&f, k_kv4_attn_tc<HB>) == cudaSuccess) return f.numRegs == Kv4TcCfg<HB>::kLaunchRegs;
+  cudaGetLastError();
+  return false;
+}
+bool kv4_attn_tc_runs(int G) {
+  static const bool runs[2] = {kv4_tc_runs<8>(), kv4_tc_runs<16>()};
+  return runs[G == 16];
 }
 
 cudaError_t kv4_launch_attn_tc(const Kv4& k, const Kv4AttnArgs& a, cudaStream_t s, int* ctas) {
