@@ -19,8 +19,9 @@
 // the outputs where K was, 128 of the 512 columns a group; with 16 heads the registers allow three, which need not share.
 // The fifth warps give registers up to the others (setmaxnreg).
 //
-// What bounds it: issue slots.  A tile costs each of the four warps 800 instructions (26.3 M in all for 8192 tiles), over half
-// of them decoding, and the SM's 4 groups take 0.52 us a tile together; issue is 68% busy, the start included.  That
+// What bounds it: issue slots and waits.  A tile costs each of the four warps 800 instructions (26.3 M in all for 8192 tiles),
+// over half of them decoding, and the SM's 4 groups take 0.52 us a tile together, of which the instructions are 0.39; issue is
+// 68% busy, the start included.  (Registers spill: 60 bytes stored and 40 loaded with 8 heads, 24 and 12 with 16.)  The
 // start is 10 us: lengths, pages and first tiles one after the other, and a second launch merges partial results.
 // 131077 positions of 8 kv heads (151 MB): 38.7 us, with mma.sync 43.6; 4 x 40000 of 4 kv heads with 16 heads each 37.4
 // and 46.8; 4 x 20000 of 8 29.8 and 31.8; 16 of up to 4000 22.8 and 23.1; 64 of up to 1000 26.5 and 26.2.
