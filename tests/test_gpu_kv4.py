@@ -1287,3 +1287,210 @@ def test_attention_of_long_sequences_with_a_few_positions_that_count(nt, n_kv, G
                 if len(t) > 1:
                     less = v[np.delete(t, len(t) // 2)].mean(0)
                     assert np.linalg.norm(less - want) > 100 * limit * np.linalg.norm(want)
+
+
+# ------------------------------------------------------------ lists and lengths at the limits --
+
+@pytest.mark.parametrize("bad", [None, 1, 1500, 2499])
+def test_row_ranges_of_many_entries(nt, bad):
+    """More entries than one CTA looks over; one of them, early or late, runs backwards."""
+    torch = torch_cuda()
+    rng = np.random.default_rng(19)
+    ref = R.RefCache(1, 1, 64, 16, 8000, 2500, 3, fill=3)
+    ref.hold(rng.integers(16, 48, 2500), rng)
+    seqs = rng.permutation(2500)
+    counts = rng.integers(0, 5, 2500)
+    begin = [2] + [int(b) for b in 2 + np.cumsum(counts)]
+    rows = begin[-1] + 3
+    x = _rows(rng, rows, 1, 64)
+    k, v = _layout(torch, x, "rows")
+    dev = Dev(nt, ref)
+    want = np.full((2, rows, 1, 64), 5.5)
+    for i, s in enumerate(seqs):
+        _store(ref, x[:, begin[i]:begin[i + 1]], [0, int(counts[i])], [s])
+        for side in (0, 1):
+            want[side, begin[i]:begin[i + 1]] = R.values(*R.quantize(x[side, begin[i]:begin[i + 1]]))
+    near = []
+    if bad is not None:                       # entry `bad` ends a row before it begins; the next one has some of its rows
+        near = [seqs[i] for i in (bad, bad + 1) if i < 2500]
+        want[:, begin[bad] - 1:begin[min(bad + 2, 2500)]] = np.nan
+        begin[bad + 1] = begin[bad] - 1
+    dev.rows(k, v, begin, seqs)
+    out = torch.full((2, rows, 1, 64), 5.5, device="cuda")
+    dev.rows(out[0], out[1], begin, seqs, read=True)
+    torch.cuda.synchronize()
+    assert int(dev.error.cpu()[0]) == (0 if bad is None else R.BAD_LEN)
+    pool, got = dev.pool.cpu().numpy(), out.cpu().numpy().astype(np.float64)
+    sure = np.ones(ref.P, bool)
+    sure[ref.table[near].reshape(-1)] = False
+    np.testing.assert_array_equal(pool[:, sure], ref.pool[:, sure])
+    np.testing.assert_array_equal(got[~np.isnan(want)], want[~np.isnan(want)])
+
+
+def test_fork_of_many_with_one_damaged_source(nt):
+    rng = np.random.default_rng(23)
+    ref = R.RefCache(1, 1, 64, 16, 9000, 4000, 9)
+    ref.randomize(rng)
+    ref.hold(rng.integers(1, 140, 900), rng)
+    src, dst = [int(s) for s in rng.integers(0, 899, 2600)], list(range(1000, 3600))
+    for i in (0, 1023, 1024, 2599):
+        dev = Dev(nt, ref)
+        odd = list(src)
+        odd[i] = 899
+        last = (int(ref.len[899]) - 1) // 16
+        dev.table[899, last] = -2
+        dev.fork(odd, dst)
+        torch_cuda().cuda.synchronize()
+        assert int(dev.error.cpu()[0]) == R.BAD_PAGE
+        assert not dev.len[1000:].any() and (dev.table[1000:] == -1).all()
+        np.testing.assert_array_equal(dev.refs.cpu().numpy(), ref.refs)
+    dev = Dev(nt, ref)
+    for x in (ref, dev):
+        x.fork(src, dst)
+    dev.check()
+
+
+@pytest.mark.parametrize("hd,G", [(64, 8), (128, 4), (128, 16)])
+def test_huge_scores_of_many_short_sequences(nt, hd, G):
+    """The form of whole items for the CTAs; limits as where scores are huge."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([137, hd, G])
+    lens = [1, 15, 100, 300]
+    ref = R.RefCache(1, 2, hd, 16, 40, 4, 19)
+    ref.randomize(rng)
+    ref.hold(lens, rng)
+    dev = Dev(nt, ref, 2 * G)
+    seqs = np.arange(200) % 4
+    checked = 0
+    for power in (20, 27, 30, 80):
+        q = (rng.standard_normal((4, 2 * G, hd)) * 2.0 ** power).astype(np.float32)
+        got = dev.attention(torch.from_numpy(q[seqs]).cuda(), seqs).cpu().numpy().reshape(200, 2 * G, hd)
+        for s in range(4):
+            for j in range(2 * G):
+                k, v = ref.kv(0, s, j // G)
+                q64 = q[s, j].astype(np.float64)
+                score, dot = k @ q64 / np.sqrt(hd), np.abs(k) @ np.abs(q64) / np.sqrt(hd)
+                order = np.argsort(score)
+                if lens[s] > 1 and score[order[-1]] - score[order[-2]] <= 2 * (
+                        (hd // 16 + 3) * 2 * U + 2.0 ** -22) * dot.max() + 60:
+                    continue
+                want = v[order[-1]]
+                assert (np.abs(got[seqs == s, j] - want) <= 2.0 ** -21 * np.abs(want)).all(), (power, s, j)
+                checked += 1
+    assert checked >= 0.98 * 4 * 4 * 2 * G
+
+
+@pytest.mark.parametrize("hd,G", [(64, 1), (128, 8)])
+def test_attention_of_the_longest_sequence(nt, hd, G):
+    """2^31 - 256 positions, the pages of all columns of the table the same one: what attention over that page gives.  Then
+    a page of its own in the last column, whose last key outweighs all others.  Seventeen entries, so that the call is cut
+    into two launches.
+
+    A thread adds up the weights of all its steps (a pair of chunks, or a tile of 128) one after the other in fp32, of
+    which there are at most 2^31 / 32 / (152 * 12) = 36793; the outputs take fewer."""
+    torch = torch_cuda()
+    rng = np.random.default_rng([139, hd, G])
+    ref = R.RefCache(1, 1, hd, 256, 2, 1, 1)
+    ref.randomize(rng)
+    ref.table[0, 0], ref.len[0] = 0, 256
+    columns = (1 << 23) - 1
+    long = R.RefCache(1, 1, hd, 256, 2, 1, 1)
+    long.shape.update(max_pages=columns)
+    long.pool[:], long.len[0], long.refs[0] = ref.pool, 256 * columns, 1
+    dev = Dev(nt, long, G)
+    dev.table = torch.zeros((1, columns), dtype=torch.int32, device="cuda")
+    dev.c.table = dev.table.data_ptr()
+    q = rng.standard_normal((1, G, hd)).astype(np.float32)
+    got = dev.attention(torch.from_numpy(q).cuda(), [0]).cpu().numpy().reshape(G, hd)
+    q64 = q[0].astype(np.float64)
+    want = _want(ref, [0], q64[None], G)[0]
+    vm = np.abs(ref.kv(0, 0, 0)[1]).max()
+    bound = _bound(ref, 0, q64, G) + 2 * vm * 36793 * U + 2 * vm * 36793 * 2.0 ** -31
+    assert (np.abs(got - want).max(axis=1) <= bound).all()
+    # the last key: the sign of the first head's query, for all heads; half of them
+    ref.table[0, 0] = 1
+    sign = np.where(rng.integers(0, 2, hd) > 0, 1.0, -1.0)
+    ref.put(0, 1, 0, 255, (sign * 700).astype(np.float32), rng.standard_normal(hd).astype(np.float32))
+    dev.pool.copy_(torch.from_numpy(ref.pool))
+    dev.table[0, -1] = 1
+    q = (np.broadcast_to(sign, (17, G, hd)) * rng.uniform(1, 2, (17, G, 1))).astype(np.float32)
+    got = dev.attention(torch.from_numpy(q).cuda(), [0] * 17).cpu().numpy().reshape(17, G, hd)
+    v = ref.kv(0, 0, 0)[1][255]
+    assert (np.abs(got - v) <= 2.0 ** -21 * np.abs(v)).all()
+    assert int(dev.error.cpu()[0]) == 0
+
+
+FIRST_CALLS = """
+import sys
+sys.path[:0] = ["tests", "."]
+import numpy as np, torch
+import kv4_ref as R
+from test_gpu_kv4 import Dev, _rows, _layout
+from quantized_decode_dequant_gb300 import nt
+torch.zeros(1, device="cuda")
+rng = np.random.default_rng(5)
+
+def make():
+    ref = R.RefCache(2, 2, 128, 32, 80, 8, 1024)
+    ref.randomize(np.random.default_rng(6))
+    ref.hold([300, 65, 0, 40], np.random.default_rng(7))
+    return ref
+
+x = _rows(rng, 2, 2, 128)
+q = torch.from_numpy(rng.standard_normal((2, 16, 128)).astype(np.float32)).cuda()
+k, v = _layout(torch, x, "rows")
+
+def calls(dev, out, back):
+    dev.fork(dev.l_src, dev.l_dst)
+    dev.extend(dev.l_dst, dev.l_one)
+    for layer in (0, 1):
+        dev.rows(k, v, None, dev.l_dst, layer)
+        dev.rows(back[layer][0], back[layer][1], None, dev.l_dst, layer, read=True)
+        dev.attention(q, dev.l_dst, layer, out=out[layer])
+    dev.free(dev.l_drop)
+    dev.copy_pages(dev.l_from, dev.l_to)
+
+class Fixed(Dev):
+    def ints(self, x):          # lists made before the capture
+        return None if x is None else x.data_ptr()
+
+    def compact_only(self, live):
+        self.nt.nt_kv4_compact(self.c, self.table.data_ptr(), self.refs.data_ptr(), live.data_ptr(), self.ws.data_ptr(),
+                               self.wb, self.stream())
+
+def fresh():
+    dev = Fixed(nt, make(), 16)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    dev.l_src, dev.l_dst, dev.l_one, dev.l_drop = i32(0, 1), i32(4, 5), i32(1, 1), i32(1)
+    dev.l_from, dev.l_to, dev.live = i32(3, 4), i32(78, 79), i32(0)
+    return dev, torch.zeros(2, 2, 2048, device="cuda"), torch.zeros(2, 2, 2, 2, 128, device="cuda")
+
+dev, out, back = fresh()
+side = torch.cuda.Stream()
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=side):        # every operator for the first time in this process
+    calls(dev, out, back)
+    dev.compact_only(dev.live)
+graph.replay()
+torch.cuda.synchronize()
+dev2, out2, back2 = fresh()
+calls(dev2, out2, back2)
+dev2.compact_only(dev2.live)
+torch.cuda.synchronize()
+for a, b in ((out, out2), (back, back2), (dev.pool, dev2.pool), (dev.table, dev2.table), (dev.len, dev2.len),
+             (dev.refs, dev2.refs), (dev.error, dev2.error), (dev.live, dev2.live)):
+    assert torch.equal(a, b)
+assert int(dev.error) == 0 and torch.isfinite(out).all() and out.any()
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(nt):
+    """What a kernel is set up with at its first launch does not disturb a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
