@@ -221,3 +221,12 @@ def test_read_refuses_exactly_the_outputs_that_overlap(built):
             nt.nt_kv4_read(c, 0, 1, A, Q, rows, "f16" if half else "f32", Q, Q + apart, rs, hs)
         assert ("rows of the outputs" in str(ei.value)) == want, (half, rows, kv, rs, hs, apart)
     assert min(seen) > 500
+
+
+def test_rows_calls_whose_grid_would_pass_2_to_the_31(built):
+    """65535 kv heads: 65535 units of 16 rows and two an entry are one too many."""
+    rows = (65535 - 5) * 16
+    for op in ROWS:
+        with pytest.raises(nt.NtError) as ei:
+            calls(cache(n_kv_heads=65535), rows=rows, rs=64, hs=64 * rows, type="f32")[op]()
+        assert ei.value.status == nt.NT_E_INVAL and "2^32 - 2^17" in str(ei.value)
