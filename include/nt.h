@@ -452,8 +452,9 @@ nt_status nt_kv4_extend(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq
  * dev_src[i] (dev_keep NULL: all of them): the full pages are shared, a partly
  * filled last one is copied into the lowest free page.  A source may be listed
  * several times, a destination once; a destination may be no source.  If any entry
- * is invalid, a page of a source's kept positions is out of range or held by nobody (refs
- * below 1), or the free pages do not suffice, the call changes nothing but *error. */
+ * is invalid, a page of a source's kept positions is out of range or held by nobody
+ * (refs below 1), or the free pages do not suffice, the call changes nothing but
+ * *error. */
 nt_status nt_kv4_fork(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
                       const int32_t* dev_keep, void* dev_workspace, size_t workspace_bytes, void* stream);
 
@@ -475,8 +476,8 @@ nt_status nt_kv4_copy_pages(const nt_kv4_cache* c, int32_t n, const int32_t* dev
  * [n_pages] receive the table and counts that go with it; each is either the
  * cache's own array or one that does not overlap it (the cache then still
  * describes the state before: moved pages keep their old bytes until they are
- * taken).  dev_live: L.  Table entries other than -1 that are out of range
- * are copied as they are, those that name a free page become -1; both set NT_KV4_BAD_PAGE. */
+ * taken).  dev_live: L.  Table entries other than -1 that are out of range are copied
+ * as they are, those that name a free page become -1; both set NT_KV4_BAD_PAGE. */
 nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t* dev_refs_out, int32_t* dev_live,
                          void* dev_workspace, size_t workspace_bytes, void* stream);
 
@@ -488,11 +489,13 @@ nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t*
  * starts at element r * row_stride + g * head_stride of dev_k and of dev_v (f32 or f16 by
  * `type`: NT_F32, NT_F16; both strides multiples of 16 bytes), head_dim elements
  * each: a projection's [row][kv head][dim] as well as an f16 cache's [kv
- * head][position][dim].  n_rows / 16 + 2 n is at most 2^26, and n_kv_heads times that (and 1)
- * 2^32 - 2^17.  An entry is passed over where its sequence is out of range, it has more rows than the sequence positions or rows outside [0, n_rows) (dev_begin
- * NULL: entry i's row is row i), or its range runs backwards (rows of other entries
- * may be passed over then too); rows are where their page is out of range or not held by this
- * sequence alone (refs other than 1).  With n_rows = 0 the lists are not looked at.
+ * head][position][dim].  n_rows / 16 + 2 n is at most 2^26, and n_kv_heads times
+ * one more than that 2^32 - 2^17.  An entry is passed over where its sequence is out
+ * of range, it has more rows than the sequence positions or rows outside [0, n_rows)
+ * (dev_begin NULL: entry i's row is row i), or its range runs backwards (rows of other
+ * entries may be passed over then too); rows are where their page is out of range or
+ * not held by this sequence alone (refs other than 1).  With n_rows = 0 the lists are
+ * not looked at.
  * A sequence listed twice is flagged; which of its rows are stored is not defined. */
 nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
                         const int32_t* dev_begin, int32_t n_rows, nt_qtype type, const void* dev_k, const void* dev_v,
@@ -513,8 +516,9 @@ nt_status nt_kv4_read(const nt_kv4_cache* c, int32_t layer, int32_t n, const int
  * and zeros where len = 0.  dev_q and dev_out: fp32, sequence i at element i * q_stride
  * and i * out_stride (multiples of 4, at least n_heads * head_dim), [n_heads][head_dim] each.
  * The statistics and sums are fp32; K and V enter exactly, q and the softmax
- * weights with about 22 bits (a weight of less than 2^-9 of the head's largest to 2^-31 of that, as
- * an f16 pair ends there).  Scores may be of any size below 2^126.  A sequence out of range, a length that the table
+ * weights with about 22 bits (a weight of less than 2^-9 of the head's largest to
+ * 2^-31 of that: an f16 pair ends there).  Scores may be of any size below 2^126.
+ * A sequence out of range, a length that the table
  * cannot hold and a page index out of range give NaN in that sequence's outputs.
  * n at most 65536, n_kv_heads * max_pages * page_len at most 2^34 and a layer of the pool
  * at most 2^31 - 1 chunks.

@@ -145,7 +145,7 @@ __device__ __forceinline__ bool kv4_span(const Kv4& c, const Kv4Rows& a, int u, 
     if (lane == 0 && u == start) kv4_flag(c, bad);
     return false;
   }
-  if (u - start > rows / kKv4Chunk + 1) return false;   // behind the entry's last chunk (n, up to 2^31 - 256, and more would not fit an int)
+  if (u - start > rows / kKv4Chunk + 1) return false;   // behind the entry's last chunk (n may be 2^31 - 256: more would not fit an int)
   const int p0 = (n - rows) / kKv4Chunk * kKv4Chunk + (u - start) * kKv4Chunk;   // the chunk's first position
   if (p0 >= n) return false;
   const int first = p0 > n - rows ? p0 : n - rows;

@@ -272,8 +272,9 @@ __global__ void __launch_bounds__(Kv4AttnCfg<HD, HB>::kThreads, 1) k_kv4_attn(Kv
     {
       // q of heads gi (and gi + 8; N4: gi % 4), split.  It is scaled by 8 log2(e) / sqrt(hd) (below 2) and a power of two that
       // brings a head's largest element into [2^10, 2^12), so that a score times cs, a power of two, is an exponent of 2 and
-      // that product exact: the same number in the maximum and in the multiply-add of the weights, however large.  (With
-      // the scale in cs, a maximum rounded by itself was off by up to half its last place, from scores of 2^28 on more than a weight's range.)
+      // that product exact: the same number in the maximum and in the multiply-add of the weights, however large.  (With the
+      // scale in cs, a maximum rounded by itself was off by up to half its last place: digits lost from scores of 2^26
+      // on, the weight's whole range from 2^28.)
       const float* qb = a.q + int64_t(e) * a.q_stride + int64_t(g) * G * HD;
       float qx[MT][NG][8], back[MT];
 #pragma unroll
