@@ -4,28 +4,33 @@
 
 namespace nt {
 
-nt_status kv4_check(const nt_kv4_cache* c, const char* who, bool pointers, Kv4* k) {
+nt_status kv4_check_pages(const Kv4& c, const char* who, bool pointers) {
   auto bad = [&](const char* what) { return fail(NT_E_INVAL, std::string(who) + ": " + what); };
-  if (!c) return bad("NULL cache");
-  if (c->n_layers < 1 || c->n_layers > 65535) return bad("n_layers outside [1, 65535]");
-  if (c->n_kv_heads < 1 || c->n_kv_heads > 65535) return bad("n_kv_heads outside [1, 65535]");
-  if (c->page_len < 16 || c->page_len > 256 || c->page_len % 16) return bad("page_len must be a multiple of 16, 16..256");
-  if (c->n_pages < 1) return bad("n_pages must be positive");
-  if (c->max_seqs < 1 || c->max_seqs > kKv4MaxSeqs) return bad("max_seqs outside [1, 65536]");
-  if (c->max_pages < 1 || int64_t(c->max_pages) * c->page_len > 0x7fffffffLL - 255)
+  if (c.n_layers < 1 || c.n_layers > 65535) return bad("n_layers outside [1, 65535]");
+  if (c.n_kv < 1 || c.n_kv > 65535) return bad("n_kv_heads outside [1, 65535]");
+  if (c.n_pages < 1) return bad("n_pages must be positive");
+  if (c.max_seqs < 1 || c.max_seqs > kKv4MaxSeqs) return bad("max_seqs outside [1, 65536]");
+  if (c.max_pages < 1 || int64_t(c.max_pages) * c.page_len > 0x7fffffffLL - 255)
     return bad("max_pages must be positive and max_pages * page_len at most 2^31 - 256");
-  if (c->head_dim != 64 && c->head_dim != 128)
-    return fail(NT_E_UNSUPPORTED, std::string(who) + ": head_dim must be 64 or 128");
-  *k = Kv4{c->n_layers, c->n_kv_heads, c->head_dim, c->page_len, c->n_pages, c->max_seqs, c->max_pages,
-           static_cast<uint8_t*>(c->pool), c->table, c->len, c->refs, c->error};
+  if (c.hd != 64 && c.hd != 128) return fail(NT_E_UNSUPPORTED, std::string(who) + ": head_dim must be 64 or 128");
   // every byte offset into the pool fits 62 bits
-  if (double(k->page_bytes()) * c->n_pages * c->n_layers > 4e18) return bad("the pool is too large");
+  if (double(c.page_bytes()) * c.n_pages * c.n_layers > 4e18) return bad("the pool is too large");
   if (pointers) {
-    if (!kv4_aligned(c->pool, 16)) return bad("pool is NULL or not 16-byte aligned");
-    if (!kv4_aligned(c->table, 4) || !kv4_aligned(c->len, 4) || !kv4_aligned(c->refs, 4) || !kv4_aligned(c->error, 4))
+    if (!kv4_aligned(c.pool, 16)) return bad("pool is NULL or not 16-byte aligned");
+    if (!kv4_aligned(c.table, 4) || !kv4_aligned(c.len, 4) || !kv4_aligned(c.refs, 4) || !kv4_aligned(c.error, 4))
       return bad("table, len, refs or error is NULL or not 4-byte aligned");
   }
   return NT_OK;
+}
+
+nt_status kv4_check(const nt_kv4_cache* c, const char* who, bool pointers, Kv4* k) {
+  if (!c) return fail(NT_E_INVAL, std::string(who) + ": NULL cache");
+  if (c->page_len < 16 || c->page_len > 256 || c->page_len % 16)
+    return fail(NT_E_INVAL, std::string(who) + ": page_len must be a multiple of 16, 16..256");
+  *k = Kv4{c->n_layers, c->n_kv_heads, c->head_dim, c->page_len, c->n_pages, c->max_seqs, c->max_pages,
+           static_cast<uint8_t*>(c->pool), c->table, c->len, c->refs, c->error,
+           int64_t(c->n_kv_heads) * (c->page_len / kKv4Chunk) * kv4_chunk_bytes(c->head_dim)};
+  return kv4_check_pages(*k, who, pointers);
 }
 
 bool kv4_meets_cache(const Kv4& k, const void* p, int64_t bytes) {
@@ -48,114 +53,6 @@ bool kv4_meets_cache(const Kv4& k, const void* p, int64_t bytes) {
 // the scales, worked out 4 and 8 times over, took most of the time: 64.7 us for
 // 2 x 20011 f16 rows of 8 heads of 128.)
 // read: a lane's words give values that lie side by side in a row across the lanes.
-
-// Every kernel here is launched so that it may start while the one before it in the
-// stream ends, and lets the next one start: it touches memory only after that one has
-// ended and its writes are visible.
-__device__ __forceinline__ void kv4_dependent() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-}
-template <class K, class... A>
-static cudaError_t kv4_launch_smem(K kern, unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-template <class K, class... A>
-static cudaError_t kv4_launch(K kern, unsigned grid, unsigned block, cudaStream_t s, A... args) {
-  return kv4_launch_smem(kern, grid, block, 0, s, args...);
-}
-
-struct Kv4Rows {
-  int32_t layer, n, n_rows, units, checks;
-  const int32_t* seq;
-  const int32_t* begin;
-  int64_t row_stride, head_stride;
-};
-
-// What a warp works on: positions [first, last) of the chunk at position p0 of
-// sequence s are rows of the call, position first's row is `row`.
-struct Kv4Span {
-  int s, p0, first, last, row;
-};
-
-// Flags entries whose rows do not all lie within the call's: their units may be none of the call's.  CTAs of their own
-// do it, the grid's first a.checks, so that no warp with rows waits for it.  (16 tokens and 2 x 20011
-// f16 rows stored and read back, 5.04 and 71.0 us without: so 5.16 and 71.2; by the warps with rows, at their start or
-// end, 5.16 to 5.72 and 71.5 to 75.0.)  Without `begin` there is one such CTA where there
-// are more entries than rows.
-constexpr int kKv4CheckEntries = 1024;   // of a CTA
-__device__ __forceinline__ bool kv4_check_rows(const Kv4& c, const Kv4Rows& a) {
-  if (int(blockIdx.x) >= a.checks) return false;
-  bool bad = !a.begin;
-  const int e1 = (int(blockIdx.x) + 1) * kKv4CheckEntries;   // (2^25 entries at most)
-  if (a.begin)
-    for (int i = e1 - kKv4CheckEntries + int(threadIdx.x); i < e1 && i < a.n; i += blockDim.x) {
-      const int b0 = a.begin[i], b1 = a.begin[i + 1];
-      bad |= b0 != b1 && (b0 < 0 || b1 < b0 || b1 > a.n_rows);
-    }
-  if (bad) kv4_flag(c, NT_KV4_BAD_LEN);
-  return true;
-}
-
-// Unit u of the call: a chunk that entry i's rows may touch.  Entry i's units start
-// at begin[i] / 16 + 2 i: r rows touch at most r / 16 + 2 chunks, so they do not
-// meet entry i + 1's; the units between belong to nobody.  Without `begin` a unit is an
-// entry.  false: nothing to do.
-// All lanes call it and get the same.
-__device__ __forceinline__ bool kv4_span(const Kv4& c, const Kv4Rows& a, int u, Kv4Span* sp) {
-  const int lane = threadIdx.x & 31;
-  int i = u, b0 = u, b1 = u + 1, start = u;
-  if (a.begin) {
-    int lo = 0, hi = a.n;   // entry lo .. hi - 1 has unit u (if any has)
-    int step = 1;
-    while (step * 32 < hi) step *= 32;
-    for (; step; step /= 32) {   // 32 candidates at a time
-      const int e = lo + lane * step;
-      const bool before = e < hi && a.begin[e] / kKv4Chunk + 2 * e <= u;
-      const uint32_t m = __ballot_sync(0xffffffffu, before);
-      if (!m) return false;
-      lo += (31 - __clz(m)) * step;
-      hi = lo + step < hi ? lo + step : hi;
-    }
-    i = lo;
-    b0 = a.begin[i];
-    b1 = a.begin[i + 1];
-    start = b0 / kKv4Chunk + 2 * i;
-    if (b1 <= b0 || b0 < 0 || b1 > a.n_rows) return false;
-  } else if (u >= a.n) {
-    return false;
-  }
-  const int rows = b1 - b0;
-  const int s = a.seq ? a.seq[i] : i;
-  uint32_t bad = 0;
-  int n = 0;
-  if (s < 0 || s >= c.max_seqs) bad = NT_KV4_BAD_SEQ;
-  else if ((n = c.len[s]) > c.capacity() || n < rows) bad = NT_KV4_BAD_LEN;   // (a row range above the length: no row)
-  if (bad) {
-    if (lane == 0 && u == start) kv4_flag(c, bad);
-    return false;
-  }
-  if (u - start > rows / kKv4Chunk + 1) return false;   // behind the entry's last chunk (n may be 2^31 - 256: more would not fit an int)
-  const int p0 = (n - rows) / kKv4Chunk * kKv4Chunk + (u - start) * kKv4Chunk;   // the chunk's first position
-  if (p0 >= n) return false;
-  const int first = p0 > n - rows ? p0 : n - rows;
-  sp->s = s;
-  sp->p0 = p0;
-  sp->row = b0 + first - (n - rows);
-  sp->first = first - p0;
-  sp->last = n - p0 < kKv4Chunk ? n - p0 : kKv4Chunk;
-  return true;
-}
 
 // The span's chunk of kv head g; NULL where there is no such page, or (append) it
 // is not the sequence's own.
@@ -478,6 +375,10 @@ __global__ void __launch_bounds__(1024) k_kv4_listed_twice(Kv4 c, int n, const i
     if (s < 0 || s >= c.max_seqs) continue;
     if (atomicOr(&set[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u) kv4_flag(c, NT_KV4_BAD_SEQ);
   }
+}
+
+cudaError_t kv4_launch_listed_twice(const Kv4& k, int32_t n, const int32_t* seq, cudaStream_t s) {
+  return kv4_launch(k_kv4_listed_twice, 1u, 1024u, s, k, n, seq);
 }
 
 // ------------------------------------------------------------ page operators --
@@ -926,8 +827,7 @@ static nt_status kv4_list_check(const Kv4& k, const char* who, int64_t n, int64_
   return NT_OK;
 }
 
-// A list of n int32 on the device: aligned, and apart from the cache and the workspace.
-static nt_status kv4_array_check(const Kv4& k, const char* who, const void* p, int64_t n, bool nullable, const void* ws,
+nt_status kv4_array_check(const Kv4& k, const char* who, const void* p, int64_t n, bool nullable, const void* ws,
                                  size_t ws_bytes) {
   if (!p && nullable) return NT_OK;
   if (!kv4_aligned(p, 4)) return fail(NT_E_INVAL, std::string(who) + ": a list is NULL or not 4-byte aligned");
@@ -958,19 +858,7 @@ static nt_status kv4_plan_apply(const char* who, const Kv4& k, Kv4PlanArgs a, vo
   return NT_OK;
 }
 
-// Units of a call (see kv4_span), at most 2^26, so that begin / 16 + 2 i and the grid
-// fit 31 bits (0: n or n_rows is out of range).
-static int32_t kv4_units(int32_t n, int32_t n_rows, const int32_t* begin) {
-  const int64_t u = begin ? int64_t(n_rows) / kKv4Chunk + 2 * int64_t(n) + 1 : (n < n_rows ? n : n_rows);
-  return n < 0 || n_rows < 0 || u > (1 << 26) ? 0 : int32_t(u);
-}
-
-// CTAs that look over the entries.
-static int32_t kv4_checks(int32_t n, int32_t n_rows, const int32_t* begin) {
-  return begin ? int32_t((int64_t(n) + kKv4CheckEntries - 1) / kKv4CheckEntries) : n > n_rows;
-}
-
-static nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a, nt_qtype type, const void* pk, const void* pv) {
+nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a, nt_qtype type, const void* pk, const void* pv) {
   auto bad = [&](const char* what) { return fail(NT_E_INVAL, std::string(who) + ": " + what); };
   if (type != NT_F32 && type != NT_F16) return bad("type must be NT_F32 or NT_F16");
   if (a.layer < 0 || a.layer >= k.n_layers) return bad("layer out of range");
@@ -987,17 +875,13 @@ static nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a,
   return NT_OK;
 }
 
-// Bytes from the first to the last element of the rows (-1: beyond 2^60).
-static int64_t kv4_rows_bytes(const Kv4& k, const Kv4Rows& a, nt_qtype type) {
+int64_t kv4_rows_bytes(const Kv4& k, const Kv4Rows& a, nt_qtype type) {
   const double most = double(a.n_rows) * double(a.row_stride) + double(k.n_kv) * double(a.head_stride);
   if (most > 1e17) return -1;
   return ((int64_t(a.n_rows) - 1) * a.row_stride + int64_t(k.n_kv - 1) * a.head_stride + k.hd) * (type == NT_F32 ? 4 : 2);
 }
 
-// Whether a (row, kv head) vector of one tensor shares bytes with one of another
-// of the same strides that starts d bytes further (same: the tensor itself, each
-// vector apart from itself).
-static bool kv4_rows_meet(const Kv4& k, const Kv4Rows& a, int64_t es, int64_t d, bool same) {
+bool kv4_rows_meet(const Kv4& k, const Kv4Rows& a, int64_t es, int64_t d, bool same) {
   const int64_t rs = a.row_stride * es, hs = a.head_stride * es, w = k.hd * es;
   for (int64_t h = -(k.n_kv - 1); h <= k.n_kv - 1; h++) {
     const int64_t x = d + h * hs;                 // then + r rs, r in (-n_rows, n_rows)
@@ -1010,6 +894,82 @@ static bool kv4_rows_meet(const Kv4& k, const Kv4Rows& a, int64_t es, int64_t d,
     }
   }
   return false;
+}
+
+nt_status kv4_extend(const char* who, const Kv4& k, int32_t n, const int32_t* seq, const int32_t* count, void* ws,
+                     size_t ws_bytes, void* stream) {
+  const nt_status st = kv4_list_check(k, who, n, k.max_seqs);
+  if (st) return st;
+  Kv4PlanArgs a{};
+  a.n = n;
+  a.a = seq;
+  a.b = count;
+  return kv4_plan_apply<false>(who, k, a, ws, ws_bytes, stream);
+}
+
+nt_status kv4_fork(const char* who, const Kv4& k, int32_t n, const int32_t* src, const int32_t* dst, const int32_t* keep,
+                   void* ws, size_t ws_bytes, void* stream) {
+  const nt_status st = kv4_list_check(k, who, n, k.max_seqs);
+  if (st) return st;
+  Kv4PlanArgs a{};
+  a.n = n;
+  a.a = src;
+  a.b = dst;
+  a.keep = keep;
+  return kv4_plan_apply<true>(who, k, a, ws, ws_bytes, stream);
+}
+
+nt_status kv4_free(const char* who, const Kv4& k, int32_t n, const int32_t* seq, const int32_t* keep, void* stream) {
+  nt_status st = kv4_list_check(k, who, n, k.max_seqs);
+  if (!st) st = kv4_array_check(k, who, seq, n, true, nullptr, 0);
+  if (!st) st = kv4_array_check(k, who, keep, n, true, nullptr, 0);
+  if (st || n == 0) return st;
+  NT_CUDA(kv4_launch(k_kv4_free, kv4_grid(n, 152 * 8), 256u, static_cast<cudaStream_t>(stream), k, n, seq, keep));
+  return NT_OK;
+}
+
+nt_status kv4_copy_pages(const char* who, const Kv4& k, int32_t n, const int32_t* src, const int32_t* dst, void* stream) {
+  nt_status st = kv4_list_check(k, who, n, k.n_pages < (1 << 20) ? k.n_pages : 1 << 20);
+  if (!st) st = kv4_array_check(k, who, src, n, false, nullptr, 0);
+  if (!st) st = kv4_array_check(k, who, dst, n, false, nullptr, 0);
+  if (st || n == 0) return st;
+  static const KernelSetup setup = kernel_setup(k_kv4_copy_pages, Kv4CopyShared::kSize);
+  if (setup.err == cudaSuccess && (int64_t(n) + setup.sms - 1) / setup.sms + 2 > kKv4CopyPairs)
+    return fail(NT_E_UNSUPPORTED, std::string(who) + ": too many pairs for this GPU");
+  const Kv4Pieces ps = kv4_pieces(k, n);
+  const int64_t pieces = int64_t(n) * k.n_layers * ps.count;
+  NT_CUDA(kv4_launch_copy(setup, k_kv4_copy_pages, pieces, static_cast<cudaStream_t>(stream), k, n, src, dst, ps));
+  return NT_OK;
+}
+
+nt_status kv4_compact(const char* who, const Kv4& k, int32_t* dev_table_out, int32_t* dev_refs_out, int32_t* dev_live,
+                      void* dev_workspace, size_t workspace_bytes, void* stream) {
+  Kv4Ws w;
+  const nt_status st = kv4_ws_check(k, who, 0, dev_workspace, workspace_bytes, &w);
+  if (st) return st;
+  const int64_t tb = int64_t(k.max_seqs) * k.max_pages * 4, rb = int64_t(k.n_pages) * 4;
+  if (!kv4_aligned(dev_table_out, 4) || !kv4_aligned(dev_refs_out, 4) || !kv4_aligned(dev_live, 4))
+    return fail(NT_E_INVAL, std::string(who) + ": an output is NULL or not 4-byte aligned");
+  if ((dev_table_out != k.table && kv4_meets_cache(k, dev_table_out, tb)) ||
+      (dev_refs_out != k.refs && kv4_meets_cache(k, dev_refs_out, rb)) || kv4_meets_cache(k, dev_live, 4) ||
+      kv4_overlap(dev_table_out, tb, dev_refs_out, rb) || kv4_overlap(dev_table_out, tb, dev_live, 4) ||
+      kv4_overlap(dev_refs_out, rb, dev_live, 4) || kv4_overlap(dev_workspace, int64_t(w.bytes), dev_table_out, tb) ||
+      kv4_overlap(dev_workspace, int64_t(w.bytes), dev_refs_out, rb) ||
+      kv4_overlap(dev_workspace, int64_t(w.bytes), dev_live, 4))
+    return fail(NT_E_INVAL, std::string(who) + ": an output overlaps another buffer");
+  uint8_t* base = static_cast<uint8_t*>(dev_workspace);
+  int32_t* go = reinterpret_cast<int32_t*>(base);
+  int2* pair = reinterpret_cast<int2*>(base + w.pair);
+  int32_t* to = reinterpret_cast<int32_t*>(base + w.free);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  NT_CUDA(kv4_launch(k_kv4_compact_plan, 1u, 1024u, s, k, go, pair, to, dev_live));
+  // (how many pages move is known on the device only; at most half of them do)
+  static const KernelSetup setup = kernel_setup(k_kv4_compact_apply, Kv4CopyShared::kSize);
+  const Kv4Pieces ps = kv4_pieces(k, k.n_pages > 16 ? k.n_pages / 8 : 1);
+  NT_CUDA(kv4_launch_copy(setup, k_kv4_compact_apply, int64_t(k.n_pages) * k.n_layers * ps.count, s, k,
+                          static_cast<const int32_t*>(go), static_cast<const int2*>(pair), static_cast<const int32_t*>(to),
+                          dev_table_out, dev_refs_out, ps));
+  return NT_OK;
 }
 
 }  // namespace nt
@@ -1042,89 +1002,35 @@ nt_status nt_kv4_workspace_bytes(const nt_kv4_cache* c, int32_t n_heads, int32_t
 nt_status nt_kv4_extend(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_count,
                         void* dev_workspace, size_t workspace_bytes, void* stream) {
   Kv4 k;
-  nt_status st = kv4_check(c, "nt_kv4_extend", true, &k);
-  if (!st) st = kv4_list_check(k, "nt_kv4_extend", n, k.max_seqs);
-  if (st) return st;
-  Kv4PlanArgs a{};
-  a.n = n;
-  a.a = dev_seq;
-  a.b = dev_count;
-  return kv4_plan_apply<false>("nt_kv4_extend", k, a, dev_workspace, workspace_bytes, stream);
+  const nt_status st = kv4_check(c, "nt_kv4_extend", true, &k);
+  return st ? st : kv4_extend("nt_kv4_extend", k, n, dev_seq, dev_count, dev_workspace, workspace_bytes, stream);
 }
 
 nt_status nt_kv4_fork(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
                       const int32_t* dev_keep, void* dev_workspace, size_t workspace_bytes, void* stream) {
   Kv4 k;
-  nt_status st = kv4_check(c, "nt_kv4_fork", true, &k);
-  if (!st) st = kv4_list_check(k, "nt_kv4_fork", n, k.max_seqs);
-  if (st) return st;
-  Kv4PlanArgs a{};
-  a.n = n;
-  a.a = dev_src;
-  a.b = dev_dst;
-  a.keep = dev_keep;
-  return kv4_plan_apply<true>("nt_kv4_fork", k, a, dev_workspace, workspace_bytes, stream);
+  const nt_status st = kv4_check(c, "nt_kv4_fork", true, &k);
+  return st ? st : kv4_fork("nt_kv4_fork", k, n, dev_src, dev_dst, dev_keep, dev_workspace, workspace_bytes, stream);
 }
 
 nt_status nt_kv4_free(const nt_kv4_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_keep, void* stream) {
   Kv4 k;
-  nt_status st = kv4_check(c, "nt_kv4_free", true, &k);
-  if (!st) st = kv4_list_check(k, "nt_kv4_free", n, k.max_seqs);
-  if (!st) st = kv4_array_check(k, "nt_kv4_free", dev_seq, n, true, nullptr, 0);
-  if (!st) st = kv4_array_check(k, "nt_kv4_free", dev_keep, n, true, nullptr, 0);
-  if (st || n == 0) return st;
-  NT_CUDA(kv4_launch(k_kv4_free, kv4_grid(n, 152 * 8), 256u, static_cast<cudaStream_t>(stream), k, n, dev_seq, dev_keep));
-  return NT_OK;
+  const nt_status st = kv4_check(c, "nt_kv4_free", true, &k);
+  return st ? st : kv4_free("nt_kv4_free", k, n, dev_seq, dev_keep, stream);
 }
 
 nt_status nt_kv4_copy_pages(const nt_kv4_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
                             void* stream) {
   Kv4 k;
-  nt_status st = kv4_check(c, "nt_kv4_copy_pages", true, &k);
-  if (!st) st = kv4_list_check(k, "nt_kv4_copy_pages", n, k.n_pages < (1 << 20) ? k.n_pages : 1 << 20);
-  if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_src, n, false, nullptr, 0);
-  if (!st) st = kv4_array_check(k, "nt_kv4_copy_pages", dev_dst, n, false, nullptr, 0);
-  if (st || n == 0) return st;
-  static const KernelSetup setup = kernel_setup(k_kv4_copy_pages, Kv4CopyShared::kSize);
-  if (setup.err == cudaSuccess && (int64_t(n) + setup.sms - 1) / setup.sms + 2 > kKv4CopyPairs)
-    return fail(NT_E_UNSUPPORTED, "nt_kv4_copy_pages: too many pairs for this GPU");
-  const Kv4Pieces ps = kv4_pieces(k, n);
-  const int64_t pieces = int64_t(n) * k.n_layers * ps.count;
-  NT_CUDA(kv4_launch_copy(setup, k_kv4_copy_pages, pieces, static_cast<cudaStream_t>(stream), k, n, dev_src, dev_dst, ps));
-  return NT_OK;
+  const nt_status st = kv4_check(c, "nt_kv4_copy_pages", true, &k);
+  return st ? st : kv4_copy_pages("nt_kv4_copy_pages", k, n, dev_src, dev_dst, stream);
 }
 
 nt_status nt_kv4_compact(const nt_kv4_cache* c, int32_t* dev_table_out, int32_t* dev_refs_out, int32_t* dev_live,
                          void* dev_workspace, size_t workspace_bytes, void* stream) {
-  const char* who = "nt_kv4_compact";
   Kv4 k;
-  Kv4Ws w;
-  nt_status st = kv4_check(c, who, true, &k);
-  if (!st) st = kv4_ws_check(k, who, 0, dev_workspace, workspace_bytes, &w);
-  if (st) return st;
-  const int64_t tb = int64_t(k.max_seqs) * k.max_pages * 4, rb = int64_t(k.n_pages) * 4;
-  if (!kv4_aligned(dev_table_out, 4) || !kv4_aligned(dev_refs_out, 4) || !kv4_aligned(dev_live, 4))
-    return fail(NT_E_INVAL, "nt_kv4_compact: an output is NULL or not 4-byte aligned");
-  if ((dev_table_out != k.table && kv4_meets_cache(k, dev_table_out, tb)) ||
-      (dev_refs_out != k.refs && kv4_meets_cache(k, dev_refs_out, rb)) || kv4_meets_cache(k, dev_live, 4) ||
-      kv4_overlap(dev_table_out, tb, dev_refs_out, rb) || kv4_overlap(dev_table_out, tb, dev_live, 4) ||
-      kv4_overlap(dev_refs_out, rb, dev_live, 4) || kv4_overlap(dev_workspace, int64_t(w.bytes), dev_table_out, tb) ||
-      kv4_overlap(dev_workspace, int64_t(w.bytes), dev_refs_out, rb) ||
-      kv4_overlap(dev_workspace, int64_t(w.bytes), dev_live, 4))
-    return fail(NT_E_INVAL, "nt_kv4_compact: an output overlaps another buffer");
-  uint8_t* base = static_cast<uint8_t*>(dev_workspace);
-  int32_t* go = reinterpret_cast<int32_t*>(base);
-  int2* pair = reinterpret_cast<int2*>(base + w.pair);
-  int32_t* to = reinterpret_cast<int32_t*>(base + w.free);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  NT_CUDA(kv4_launch(k_kv4_compact_plan, 1u, 1024u, s, k, go, pair, to, dev_live));
-  // (how many pages move is known on the device only; at most half of them do)
-  static const KernelSetup setup = kernel_setup(k_kv4_compact_apply, Kv4CopyShared::kSize);
-  const Kv4Pieces ps = kv4_pieces(k, k.n_pages > 16 ? k.n_pages / 8 : 1);
-  NT_CUDA(kv4_launch_copy(setup, k_kv4_compact_apply, int64_t(k.n_pages) * k.n_layers * ps.count, s, k,
-                          static_cast<const int32_t*>(go), static_cast<const int2*>(pair), static_cast<const int32_t*>(to),
-                          dev_table_out, dev_refs_out, ps));
-  return NT_OK;
+  const nt_status st = kv4_check(c, "nt_kv4_compact", true, &k);
+  return st ? st : kv4_compact("nt_kv4_compact", k, dev_table_out, dev_refs_out, dev_live, dev_workspace, workspace_bytes, stream);
 }
 
 nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
@@ -1153,7 +1059,7 @@ nt_status nt_kv4_append(const nt_kv4_cache* c, int32_t layer, int32_t n, const i
     NT_CUDA(k.hd == 64 ? kv4_launch(k_kv4_append<64, __half>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv) : kv4_launch(k_kv4_append<128, __half>, grid, 32u * kKv4RowWarps, s, k, a, pk, pv));
   }
   if (dev_seq && n > 1) {
-    NT_CUDA(kv4_launch(k_kv4_listed_twice, 1u, 1024u, s, k, n, dev_seq));
+    NT_CUDA(kv4_launch_listed_twice(k, n, dev_seq, s));
   }
   return NT_OK;
 }

@@ -1,6 +1,7 @@
 // nt_kv4.cuh -- layout, argument checks and workspace of the paged 4-bit K/V
 // cache (include/nt.h, nt_kv4_cache), shared by its operators (nt_kv4.cu) and
-// the attention over it (nt_kv4_attn.cu).
+// the attention over it (nt_kv4_attn.cu); and what the 8-bit cache (nt_kv8.cuh),
+// whose pages differ in size and contents only, has in common with it.
 #pragma once
 
 #include "nt_internal.cuh"
@@ -21,8 +22,9 @@ struct Kv4 {
   int32_t* len;
   int32_t* refs;
   uint32_t* error;
+  int64_t pb;          // bytes of a page of one layer
 
-  __host__ __device__ int64_t page_bytes() const { return int64_t(n_kv) * (page_len / kKv4Chunk) * kv4_chunk_bytes(hd); }
+  __host__ __device__ int64_t page_bytes() const { return pb; }
   // chunk holding position `at` (within its page) of kv head g
   __device__ uint8_t* chunk(int layer, int page, int g, int at) const {
     return pool + (int64_t(layer) * n_pages + page) * page_bytes() +
@@ -56,6 +58,8 @@ inline bool kv4_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 // Checks the sizes of a description (pointers too with `pointers`) and fills k.
 nt_status kv4_check(const nt_kv4_cache* c, const char* who, bool pointers, Kv4* k);
+// The same for pages of page_bytes, whose page_len is right.
+nt_status kv4_check_pages(const Kv4& c, const char* who, bool pointers);
 // Whether [p, p + bytes) meets one of the cache's buffers.
 bool kv4_meets_cache(const Kv4& k, const void* p, int64_t bytes);
 
@@ -85,6 +89,150 @@ size_t kv4_attn_ws_bytes(int n_heads, int n_kv, int hd);
 // ------------------------------------------------------------ device helpers --
 
 __device__ __forceinline__ void kv4_flag(const Kv4& k, uint32_t bits) { atomicOr(k.error, bits); }
+
+// Every kernel of the row and page operators is launched so that it may start while the one before it in the
+// stream ends, and lets the next one start: it touches memory only after that one has
+// ended and its writes are visible.
+__device__ __forceinline__ void kv4_dependent() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+template <class K, class... A>
+inline cudaError_t kv4_launch_smem(K kern, unsigned grid, unsigned block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <class K, class... A>
+inline cudaError_t kv4_launch(K kern, unsigned grid, unsigned block, cudaStream_t s, A... args) {
+  return kv4_launch_smem(kern, grid, block, 0, s, args...);
+}
+
+// Rows of a call (include/nt.h, nt_kv4_append).
+struct Kv4Rows {
+  int32_t layer, n, n_rows, units, checks;
+  const int32_t* seq;
+  const int32_t* begin;
+  int64_t row_stride, head_stride;
+};
+
+// What a warp (8-bit cache: a CTA) works on: positions [first, last) of the chunk (page) at position p0 of
+// sequence s are rows of the call, position first's row is `row`.
+struct Kv4Span {
+  int s, p0, first, last, row;
+};
+
+// Flags entries whose rows do not all lie within the call's: their units may be none of the call's.  CTAs of their own
+// do it, the grid's first a.checks, so that no warp with rows waits for it.  (16 tokens and 2 x 20011
+// f16 rows stored and read back, 5.04 and 71.0 us without: so 5.16 and 71.2; by the warps with rows, at their start or
+// end, 5.16 to 5.72 and 71.5 to 75.0.)  Without `begin` there is one such CTA where there
+// are more entries than rows.
+constexpr int kKv4CheckEntries = 1024;   // of a CTA
+__device__ __forceinline__ bool kv4_check_rows(const Kv4& c, const Kv4Rows& a) {
+  if (int(blockIdx.x) >= a.checks) return false;
+  bool bad = !a.begin;
+  const int e1 = (int(blockIdx.x) + 1) * kKv4CheckEntries;   // (2^25 entries at most)
+  if (a.begin)
+    for (int i = e1 - kKv4CheckEntries + int(threadIdx.x); i < e1 && i < a.n; i += blockDim.x) {
+      const int b0 = a.begin[i], b1 = a.begin[i + 1];
+      bad |= b0 != b1 && (b0 < 0 || b1 < b0 || b1 > a.n_rows);
+    }
+  if (bad) kv4_flag(c, NT_KV4_BAD_LEN);
+  return true;
+}
+
+// Unit u of the call: a chunk of `len` positions (16; 8-bit cache: a page) that entry i's rows may touch.  Entry i's units start
+// at begin[i] / len + 2 i: r rows touch at most r / len + 2 chunks, so they do not
+// meet entry i + 1's; the units between belong to nobody.  Without `begin` a unit is an
+// entry.  false: nothing to do.
+// All lanes call it and get the same.
+__device__ __forceinline__ bool kv4_span(const Kv4& c, const Kv4Rows& a, int u, Kv4Span* sp, const int len = kKv4Chunk) {
+  const int lane = threadIdx.x & 31;
+  int i = u, b0 = u, b1 = u + 1, start = u;
+  if (a.begin) {
+    int lo = 0, hi = a.n;   // entry lo .. hi - 1 has unit u (if any has)
+    int step = 1;
+    while (step * 32 < hi) step *= 32;
+    for (; step; step /= 32) {   // 32 candidates at a time
+      const int e = lo + lane * step;
+      const bool before = e < hi && a.begin[e] / len + 2 * e <= u;
+      const uint32_t m = __ballot_sync(0xffffffffu, before);
+      if (!m) return false;
+      lo += (31 - __clz(m)) * step;
+      hi = lo + step < hi ? lo + step : hi;
+    }
+    i = lo;
+    b0 = a.begin[i];
+    b1 = a.begin[i + 1];
+    start = b0 / len + 2 * i;
+    if (b1 <= b0 || b0 < 0 || b1 > a.n_rows) return false;
+  } else if (u >= a.n) {
+    return false;
+  }
+  const int rows = b1 - b0;
+  const int s = a.seq ? a.seq[i] : i;
+  uint32_t bad = 0;
+  int n = 0;
+  if (s < 0 || s >= c.max_seqs) bad = NT_KV4_BAD_SEQ;
+  else if ((n = c.len[s]) > c.capacity() || n < rows) bad = NT_KV4_BAD_LEN;   // (a row range above the length: no row)
+  if (bad) {
+    if (lane == 0 && u == start) kv4_flag(c, bad);
+    return false;
+  }
+  if (u - start > rows / len + 1) return false;   // behind the entry's last chunk (n may be 2^31 - 256: more would not fit an int)
+  const int p0 = (n - rows) / len * len + (u - start) * len;   // the chunk's first position
+  if (p0 >= n) return false;
+  const int first = p0 > n - rows ? p0 : n - rows;
+  sp->s = s;
+  sp->p0 = p0;
+  sp->row = b0 + first - (n - rows);
+  sp->first = first - p0;
+  sp->last = n - p0 < len ? n - p0 : len;
+  return true;
+}
+
+// Units of a call (see kv4_span), at most 2^26, so that begin / len + 2 i and the grid
+// fit 31 bits (0: n or n_rows is out of range).
+inline int32_t kv4_units(int32_t n, int32_t n_rows, const int32_t* begin, int len = kKv4Chunk) {
+  const int64_t u = begin ? int64_t(n_rows) / len + 2 * int64_t(n) + 1 : (n < n_rows ? n : n_rows);
+  return n < 0 || n_rows < 0 || u > (1 << 26) ? 0 : int32_t(u);
+}
+
+// CTAs that look over the entries.
+inline int32_t kv4_checks(int32_t n, int32_t n_rows, const int32_t* begin) {
+  return begin ? int32_t((int64_t(n) + kKv4CheckEntries - 1) / kKv4CheckEntries) : n > n_rows;
+}
+
+// Host checks of a row call's arguments; bytes from the first to the last element of
+// the rows (-1: beyond 2^60); whether a (row, kv head) vector of one tensor shares
+// bytes with one of another of the same strides that starts d bytes further (same:
+// the tensor itself, each vector apart from itself).
+nt_status kv4_rows_check(const char* who, const Kv4& k, const Kv4Rows& a, nt_qtype type, const void* pk, const void* pv);
+int64_t kv4_rows_bytes(const Kv4& k, const Kv4Rows& a, nt_qtype type);
+bool kv4_rows_meet(const Kv4& k, const Kv4Rows& a, int64_t es, int64_t d, bool same);
+// A list of n int32 on the device: aligned, and apart from the cache and the workspace.
+nt_status kv4_array_check(const Kv4& k, const char* who, const void* p, int64_t n, bool nullable, const void* ws,
+                          size_t ws_bytes);
+// Flags sequences listed twice.
+cudaError_t kv4_launch_listed_twice(const Kv4& k, int32_t n, const int32_t* seq, cudaStream_t s);
+
+// The page operators (include/nt.h) on a checked cache.
+nt_status kv4_extend(const char* who, const Kv4& k, int32_t n, const int32_t* seq, const int32_t* count, void* ws,
+                     size_t ws_bytes, void* stream);
+nt_status kv4_fork(const char* who, const Kv4& k, int32_t n, const int32_t* src, const int32_t* dst, const int32_t* keep,
+                   void* ws, size_t ws_bytes, void* stream);
+nt_status kv4_free(const char* who, const Kv4& k, int32_t n, const int32_t* seq, const int32_t* keep, void* stream);
+nt_status kv4_copy_pages(const char* who, const Kv4& k, int32_t n, const int32_t* src, const int32_t* dst, void* stream);
+nt_status kv4_compact(const char* who, const Kv4& k, int32_t* table_out, int32_t* refs_out, int32_t* live, void* ws,
+                      size_t ws_bytes, void* stream);
 
 // ---- bulk copies into shared memory, counted on mbarriers of one arrival
 __device__ __forceinline__ uint32_t kv4_smem(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
