@@ -527,6 +527,139 @@ nt_status nt_attention_kv4(const nt_kv4_cache* c, int32_t layer, int32_t n_heads
                            const float* dev_q, int64_t q_stride, float* dev_out, int64_t out_stride,
                            void* dev_workspace, size_t workspace_bytes, void* stream);
 
+/* --------------------------------------------------- paged 8-bit K/V cache -- */
+
+/* The paged cache at 8 bits per value: between the 4-bit one, whose pages, tables
+ * and page operators it shares, and the f16 one; with the position rotation on the
+ * way in, and attention to all positions or to the pages that a cheap score selects.
+ * The pages have no counterpart.
+ *
+ * Values.  A page (page_len positions of one layer) has, for each kv head, one
+ * exponent for its keys and one for its values; a value is an e4m3 code (1 sign, 4
+ * exponent and 3 mantissa bits, bias 7, no infinity) times 2^exponent.  With A the
+ * largest magnitude among the finite values up to 448 2^100,
+ *   e(A) = the smallest integer from -100 on with A <= 448 2^e(A),
+ *   code = x 2^-e rounded to nearest, ties to even.
+ * NaN, infinities and magnitudes above 448 2^100 are stored as the code NaN, and
+ * attention to such a position gives NaN.  The exponent of a page is e(A) of the rows
+ * that began it; rows added later raise it to theirs where that is larger, and the
+ * codes held are then rounded again for the larger one (an exact step but for codes
+ * that lose bits at the lower end).  It falls when the page is begun anew: rows that
+ * start at its first position.
+ * Bounds.  Each page and kv head also has lo[d] and hi[d], whole numbers in units of
+ * 2^(key exponent + 2): floor of the least and ceiling of the largest key code value
+ * / 4 among the rows since the page was begun (-127 and 127 where one was NaN); when
+ * the exponent rises, they are halved as often, rounded outwards.
+ *
+ * Pages.  page p of layer l starts at pool + (l * n_pages + p) * page bytes:
+ *   for each kv head  K codes [page_len / 8][head_dim / 16][8][16]: (t / 8, d / 16, t % 8, d % 16)
+ *                     V codes [page_len / 16][head_dim][16]:        (t / 16, d, t % 16)
+ *   for each kv head  int8 K exponent, int8 V exponent, 14 bytes unused, int8 lo [head_dim], hi [head_dim]
+ * The layouts are those in which the tensor cores read 8-bit operands from shared
+ * memory, so a page's codes are copied there and multiplied as they are.
+ *
+ * Ownership, tables, lengths, counts, error bits, overlap of calls, host checks: as
+ * for nt_kv4_cache, with NT_KV4_* bits.  NT_E_UNSUPPORTED: head_dim other than 64 or
+ * 128, page_len other than 16, 32, 64 or 128. */
+typedef struct {
+  int32_t n_layers;     /* 1..65535                                                      */
+  int32_t n_kv_heads;   /* 1..65535                                                      */
+  int32_t head_dim;     /* 64 or 128                                                     */
+  int32_t page_len;     /* positions per page: 16, 32, 64 or 128                         */
+  int32_t n_pages;      /* pages of each layer, at least 1                               */
+  int32_t max_seqs;     /* rows of the table, 1..65536                                   */
+  int32_t max_pages;    /* columns of the table; max_pages * page_len at most 2^31 - 256 */
+  void* pool;           /* dev: nt_kv8_pool_bytes() bytes                                */
+  int32_t* table;       /* dev [max_seqs][max_pages]                                     */
+  int32_t* len;         /* dev [max_seqs]: positions held                                */
+  int32_t* refs;        /* dev [n_pages]                                                 */
+  uint32_t* error;      /* dev [1]: NT_KV4_* bits                                        */
+} nt_kv8_cache;
+
+/* Bytes of one page of one layer, and of the whole pool (either nullable). */
+nt_status nt_kv8_pool_bytes(const nt_kv8_cache* c, size_t* page_bytes, size_t* pool_bytes);
+
+/* Bytes of a workspace that serves every call below on this cache with at most n
+ * listed sequences, and nt_kv8_select and nt_attention_kv8 with n_heads query heads.
+ * Its contents on entry do not matter. */
+nt_status nt_kv8_workspace_bytes(const nt_kv8_cache* c, int32_t n_heads, int32_t n, size_t* bytes);
+
+/* The page operators, as nt_kv4_extend, nt_kv4_fork, nt_kv4_free, nt_kv4_copy_pages
+ * and nt_kv4_compact.  A copied page keeps its exponents and bounds, also where fewer
+ * positions of it are kept: the bounds still hold. */
+nt_status nt_kv8_extend(const nt_kv8_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_count,
+                        void* dev_workspace, size_t workspace_bytes, void* stream);
+nt_status nt_kv8_fork(const nt_kv8_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
+                      const int32_t* dev_keep, void* dev_workspace, size_t workspace_bytes, void* stream);
+nt_status nt_kv8_free(const nt_kv8_cache* c, int32_t n, const int32_t* dev_seq, const int32_t* dev_keep, void* stream);
+nt_status nt_kv8_copy_pages(const nt_kv8_cache* c, int32_t n, const int32_t* dev_src, const int32_t* dev_dst,
+                            void* stream);
+nt_status nt_kv8_compact(const nt_kv8_cache* c, int32_t* dev_table_out, int32_t* dev_refs_out, int32_t* dev_live,
+                         void* dev_workspace, size_t workspace_bytes, void* stream);
+
+/* Rows of keys and values into the last positions of the listed sequences, as
+ * nt_kv4_append takes them (lists, row ranges, strides, types, limits with page_len in the
+ * place of 16, what is passed over and flagged).
+ * freq (host, head_dim / 2 doubles, read before the call returns; NULL: the keys
+ * are rotated already): pair (2i, 2i + 1) of a key at position p is rotated by the
+ * angle p freq[i], in radians (RoPE with base theta: freq[i] = theta^(-2i / head_dim)),
+ *   (a, b) -> (a cos - b sin, a sin + b cos), rounded to fp32 once: products and sums carry about 45 bits,
+ * the angle is exact to 2^-33 of a turn at any position.
+ * dev_q (nullable; needs freq): queries of the same rows and type, row r at element
+ * r * q_stride, [n_heads][head_dim]; dev_q_out (fp32, row r at element r *
+ * q_out_stride) receives them rotated by their rows' positions.  Both strides are
+ * multiples of 16 bytes and at least n_heads * head_dim.  In place (dev_q_out ==
+ * dev_q) with NT_F32 and equal strides, else apart from every other buffer.  Rows of
+ * entries that are passed over are left as they were in dev_q_out.
+ * NT_E_INVAL: a frequency that is not finite or above 2^20 in magnitude. */
+nt_status nt_kv8_append(const nt_kv8_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
+                        const int32_t* dev_begin, int32_t n_rows, nt_qtype type, const void* dev_k, const void* dev_v,
+                        int64_t row_stride, int64_t head_stride, const double* freq, int32_t n_heads, const void* dev_q,
+                        int64_t q_stride, float* dev_q_out, int64_t q_out_stride, void* stream);
+
+/* The last positions of the listed sequences out of the cache, as nt_kv4_read (f32:
+ * exactly; f16: rounded to nearest). */
+nt_status nt_kv8_read(const nt_kv8_cache* c, int32_t layer, int32_t n, const int32_t* dev_seq,
+                      const int32_t* dev_begin, int32_t n_rows, nt_qtype type, void* dev_k, void* dev_v,
+                      int64_t row_stride, int64_t head_stride, void* stream);
+
+/* Which pages each listed sequence's query should attend to, by an upper bound of its
+ * scores on each page.  For entry i and kv head g, with q_h the query heads of g,
+ * f the smallest integer such that the largest finite |q_hd| is at most 63 2^f (0
+ * where all are zero),
+ *   w_hd = q_hd 2^-f rounded to nearest, ties to even (infinities +-63, NaN 0),
+ *   score(j) = 2^e_j sum_h sum_d max(w_hd lo_jd, w_hd hi_jd),   e_j page j's key exponent,
+ * a sum of whole numbers below 2^24, so the choice does not depend on any order of
+ * additions.  Of the m pages that hold the first ctx positions (dev_ctx[i]; NULL: all
+ * of len), the first n_first and the last n_last are chosen and, up to n_select in
+ * all, those of the highest scores, the lower page where scores are equal; all of them
+ * where m <= n_select.  dev_pages [n][n_kv_heads][n_select] receives their places in
+ * the sequence's table row, ascending, -1 behind.
+ * An entry whose sequence or length is out of range gets -1 and sets its error bit; a page index
+ * out of range counts as a page without bounds (score 0) and sets NT_KV4_BAD_PAGE.
+ * NT_E_INVAL: n_select outside [1, 65536], n_first or n_last negative or n_first + n_last above n_select.
+ * NT_E_UNSUPPORTED: more than 16 query heads per kv head. */
+nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
+                        const int32_t* dev_ctx, const float* dev_q, int64_t q_stride, int32_t n_select, int32_t n_first,
+                        int32_t n_last, int32_t* dev_pages, void* dev_workspace, size_t workspace_bytes, void* stream);
+
+/* nt_attention over the 8-bit cache, as nt_attention_kv4 (lists, strides, empty and
+ * unreadable sequences, limits).  dev_ctx (nullable): entry i attends to the first dev_ctx[i]
+ * positions of its sequence, 0 <= dev_ctx[i] <= len, so that drafted tokens, listed
+ * with their sequence once each, see the positions up to their own.
+ * n_select = 0: all positions.  n_select > 0: those in the pages dev_pages
+ * [n][n_kv_heads][n_select] names (nt_kv8_select): places in the table row, ascending,
+ * each once, the first negative one ends the list.  A place at or beyond the pages that hold
+ * ctx positions, or not above the one before it, gives NaN in that entry's and kv head's outputs and sets
+ * NT_KV4_BAD_PAGE.
+ * Statistics and sums are fp32; codes enter exactly, q with about 24 bits and the
+ * softmax weights to 2^-28 of a head's largest.  Any 1 to 16 query heads per kv head
+ * (NT_E_UNSUPPORTED beyond). */
+nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
+                           const int32_t* dev_ctx, int32_t n_select, const int32_t* dev_pages, const float* dev_q,
+                           int64_t q_stride, float* dev_out, int64_t out_stride, void* dev_workspace,
+                           size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------ allocation-free variant -- */
 
 /* y = W x as nt_gemv_q, then the index of the largest y (ties to the lowest

@@ -68,11 +68,15 @@ class nt_kv4_cache(C.Structure):
                 ("error", C.c_void_p)]
 
 
+class nt_kv8_cache(C.Structure):
+    _fields_ = nt_kv4_cache._fields_
+
+
 NT_KV4_BAD_SEQ, NT_KV4_BAD_LEN, NT_KV4_BAD_PAGE, NT_KV4_NO_PAGE, NT_KV4_TIMEOUT = 1, 2, 4, 8, 16
 
 _lib = None
 _vp, _i32, _i64, _u64, _f32p = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64, C.POINTER(C.c_float)
-_kv4p = C.POINTER(nt_kv4_cache)
+_kv4p, _kv8p = C.POINTER(nt_kv4_cache), C.POINTER(nt_kv8_cache)
 _SIGS = {
     "nt_last_error": (C.c_char_p, []),
     "nt_model_create": (C.c_int, [C.POINTER(nt_config), C.POINTER(C.c_void_p)]),
@@ -116,6 +120,20 @@ _SIGS = {
     "nt_kv4_append": (C.c_int, [_kv4p, _i32, _i32, _vp, _vp, _i32, C.c_int, _vp, _vp, _i64, _i64, _vp]),
     "nt_kv4_read": (C.c_int, [_kv4p, _i32, _i32, _vp, _vp, _i32, C.c_int, _vp, _vp, _i64, _i64, _vp]),
     "nt_attention_kv4": (C.c_int, [_kv4p, _i32, _i32, _i32, _vp, _vp, _i64, _vp, _i64, _vp, C.c_size_t, _vp]),
+    "nt_kv8_pool_bytes": (C.c_int, [_kv8p, C.POINTER(C.c_size_t), C.POINTER(C.c_size_t)]),
+    "nt_kv8_workspace_bytes": (C.c_int, [_kv8p, _i32, _i32, C.POINTER(C.c_size_t)]),
+    "nt_kv8_extend": (C.c_int, [_kv8p, _i32, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "nt_kv8_fork": (C.c_int, [_kv8p, _i32, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "nt_kv8_free": (C.c_int, [_kv8p, _i32, _vp, _vp, _vp]),
+    "nt_kv8_copy_pages": (C.c_int, [_kv8p, _i32, _vp, _vp, _vp]),
+    "nt_kv8_compact": (C.c_int, [_kv8p, _vp, _vp, _vp, _vp, C.c_size_t, _vp]),
+    "nt_kv8_append": (C.c_int, [_kv8p, _i32, _i32, _vp, _vp, _i32, C.c_int, _vp, _vp, _i64, _i64,
+                                C.POINTER(C.c_double), _i32, _vp, _i64, _vp, _i64, _vp]),
+    "nt_kv8_read": (C.c_int, [_kv8p, _i32, _i32, _vp, _vp, _i32, C.c_int, _vp, _vp, _i64, _i64, _vp]),
+    "nt_kv8_select": (C.c_int, [_kv8p, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _vp, _vp, C.c_size_t,
+                                _vp]),
+    "nt_attention_kv8": (C.c_int, [_kv8p, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _i64, _vp, _i64, _vp, C.c_size_t,
+                                   _vp]),
 }
 
 
@@ -444,6 +462,96 @@ def nt_attention_kv4(c: nt_kv4_cache, layer: int, n_heads: int, n: int, dev_seq,
     """GQA attention of fp32 q over the listed sequences of a paged 4-bit cache."""
     _check(lib().nt_attention_kv4(c, layer, n_heads, n, dev_seq, dev_q, q_stride, dev_out, out_stride, dev_workspace,
                                   workspace_bytes, _stream(stream)), "nt_attention_kv4")
+
+
+# ------------------------------------------------------ paged 8-bit K/V cache --
+
+def make_kv8_cache(*, n_layers, n_kv_heads, head_dim, page_len, n_pages, max_seqs, max_pages, pool=0, table=0, len=0,
+                   refs=0, error=0) -> nt_kv8_cache:
+    """Description of a paged 8-bit K/V cache; pool, table, len, refs and error are device addresses."""
+    return nt_kv8_cache(n_layers, n_kv_heads, head_dim, page_len, n_pages, max_seqs, max_pages, pool, table, len, refs,
+                        error)
+
+
+def nt_kv8_pool_bytes(c: nt_kv8_cache) -> tuple[int, int]:
+    """(bytes of one page of one layer, bytes of the pool)."""
+    page, pool = C.c_size_t(), C.c_size_t()
+    _check(lib().nt_kv8_pool_bytes(c, page, pool), "nt_kv8_pool_bytes")
+    return int(page.value), int(pool.value)
+
+
+def nt_kv8_workspace_bytes(c: nt_kv8_cache, n_heads: int, n: int) -> int:
+    b = C.c_size_t()
+    _check(lib().nt_kv8_workspace_bytes(c, n_heads, n, b), "nt_kv8_workspace_bytes")
+    return int(b.value)
+
+
+def nt_kv8_extend(c: nt_kv8_cache, n: int, dev_seq, dev_count: int, dev_workspace: int, workspace_bytes: int,
+                  stream=None) -> None:
+    """Room for dev_count[i] more positions of each listed sequence."""
+    _check(lib().nt_kv8_extend(c, n, dev_seq, dev_count, dev_workspace, workspace_bytes, _stream(stream)),
+           "nt_kv8_extend")
+
+
+def nt_kv8_fork(c: nt_kv8_cache, n: int, dev_src: int, dev_dst: int, dev_keep, dev_workspace: int,
+                workspace_bytes: int, stream=None) -> None:
+    """The empty sequences dev_dst[i] become (the first dev_keep[i] positions of) dev_src[i]."""
+    _check(lib().nt_kv8_fork(c, n, dev_src, dev_dst, dev_keep, dev_workspace, workspace_bytes, _stream(stream)),
+           "nt_kv8_fork")
+
+
+def nt_kv8_free(c: nt_kv8_cache, n: int, dev_seq, dev_keep=None, stream=None) -> None:
+    """The listed sequences keep their first dev_keep[i] positions (None: nothing)."""
+    _check(lib().nt_kv8_free(c, n, dev_seq, dev_keep, _stream(stream)), "nt_kv8_free")
+
+
+def nt_kv8_copy_pages(c: nt_kv8_cache, n: int, dev_src: int, dev_dst: int, stream=None) -> None:
+    _check(lib().nt_kv8_copy_pages(c, n, dev_src, dev_dst, _stream(stream)), "nt_kv8_copy_pages")
+
+
+def nt_kv8_compact(c: nt_kv8_cache, dev_table_out: int, dev_refs_out: int, dev_live: int, dev_workspace: int,
+                   workspace_bytes: int, stream=None) -> None:
+    """The pages in use move below their number; table and counts that go with it into dev_table_out, dev_refs_out."""
+    _check(lib().nt_kv8_compact(c, dev_table_out, dev_refs_out, dev_live, dev_workspace, workspace_bytes,
+                                _stream(stream)), "nt_kv8_compact")
+
+
+def nt_kv8_append(c: nt_kv8_cache, layer: int, n: int, dev_seq, dev_begin, n_rows: int, qtype: str, dev_k: int,
+                  dev_v: int, row_stride: int, head_stride: int, freq=None, n_heads: int = 0, dev_q=None,
+                  q_stride: int = 0, dev_q_out=None, q_out_stride: int = 0, stream=None) -> None:
+    """Rows of K ("f32" or "f16", rotated by position * freq[i] per pair of dimensions) and V into the last positions of
+    the listed sequences; queries of the same rows, rotated, into dev_q_out (fp32)."""
+    if freq is not None:
+        if len(freq) != c.head_dim // 2:
+            raise ValueError(f"nt_kv8_append: {c.head_dim // 2} frequencies expected, {len(freq)} given")
+        freq = (C.c_double * len(freq))(*freq)
+    _check(lib().nt_kv8_append(c, layer, n, dev_seq, dev_begin, n_rows, QTYPES[qtype], dev_k, dev_v, row_stride,
+                               head_stride, freq, n_heads, dev_q, q_stride, dev_q_out, q_out_stride, _stream(stream)),
+           "nt_kv8_append")
+
+
+def nt_kv8_read(c: nt_kv8_cache, layer: int, n: int, dev_seq, dev_begin, n_rows: int, qtype: str, dev_k: int,
+                dev_v: int, row_stride: int, head_stride: int, stream=None) -> None:
+    """Dequantizes the last positions of the listed sequences into rows of K and V ("f32" or "f16")."""
+    _check(lib().nt_kv8_read(c, layer, n, dev_seq, dev_begin, n_rows, QTYPES[qtype], dev_k, dev_v, row_stride,
+                             head_stride, _stream(stream)), "nt_kv8_read")
+
+
+def nt_kv8_select(c: nt_kv8_cache, layer: int, n_heads: int, n: int, dev_seq, dev_ctx, dev_q: int, q_stride: int,
+                  n_select: int, n_first: int, n_last: int, dev_pages: int, dev_workspace: int, workspace_bytes: int,
+                  stream=None) -> None:
+    """The pages whose bounds promise the highest scores, [n][n_kv_heads][n_select] places in the table rows."""
+    _check(lib().nt_kv8_select(c, layer, n_heads, n, dev_seq, dev_ctx, dev_q, q_stride, n_select, n_first, n_last,
+                               dev_pages, dev_workspace, workspace_bytes, _stream(stream)), "nt_kv8_select")
+
+
+def nt_attention_kv8(c: nt_kv8_cache, layer: int, n_heads: int, n: int, dev_seq, dev_ctx, n_select: int, dev_pages,
+                     dev_q: int, q_stride: int, dev_out: int, out_stride: int, dev_workspace: int, workspace_bytes: int,
+                     stream=None) -> None:
+    """GQA attention of fp32 q over the listed sequences of a paged 8-bit cache: over all positions (n_select 0) or those of
+    the pages listed."""
+    _check(lib().nt_attention_kv8(c, layer, n_heads, n, dev_seq, dev_ctx, n_select, dev_pages, dev_q, q_stride, dev_out,
+                                  out_stride, dev_workspace, workspace_bytes, _stream(stream)), "nt_attention_kv8")
 
 
 def nt_gemv_argmax_noalloc(t: int, dev_x: int, dev_y: int, dev_index: int, dev_margin: int, stream=None) -> None:
