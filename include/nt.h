@@ -649,9 +649,9 @@ nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, i
  * with their sequence once each, see the positions up to their own.
  * n_select = 0: all positions.  n_select > 0: those in the pages dev_pages
  * [n][n_kv_heads][n_select] names (nt_kv8_select): places in the table row, ascending,
- * each once, the first negative one ends the list.  A place at or beyond the pages that hold
- * ctx positions, or not above the one before it, gives NaN in that entry's and kv head's outputs and sets
- * NT_KV4_BAD_PAGE.
+ * each once, negative ones only behind them.  A place at or beyond the pages that hold
+ * ctx positions, not above the one before it, or behind a negative one, gives NaN in that entry's and kv
+ * head's outputs and sets NT_KV4_BAD_PAGE.  No place at all gives zeros.
  * Statistics and sums are fp32; codes enter exactly, q with about 24 bits and the
  * softmax weights to 2^-28 of a head's largest.  Any 1 to 16 query heads per kv head
  * (NT_E_UNSUPPORTED beyond). */

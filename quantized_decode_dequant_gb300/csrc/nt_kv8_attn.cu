@@ -1,11 +1,36 @@
 // nt_kv8_attn.cu -- attention over the paged 8-bit cache (include/nt.h,
 // nt_attention_kv8).
+//
+// The mathematics.  For one (entry, kv head), an item, with G query heads, tiles of 128
+// positions go through two products on tcgen05, kind::f8f6f4, whose A operand is the
+// cache itself, copied from its page to shared memory and never decoded:
+//   S^T [128 positions][6 G] = K [128][hd] . q^T        q as six e4m3 terms, each 1/16 of the one before
+//   O^T [hd][8 G]            = V^T [hd][128] . P^T      the weights as eight digits
+// e4m3 has four significant bits, so six terms, each the rounding of what the ones before left,
+// hold q to 2^-24 and more.  A weight w in [0, 16) is the whole number round(w 2^28), cut into
+// eight digits of four bits: the e4m3 codes 0 to 15 are the numbers 0 to 15 times 2^-9, so a
+// digit is its own code and an and and a shift make four of them.  Every product is exact; the tensor cores add
+// with 2^-25 of the largest product dropped, and truncate sums, so a tile's outputs
+// are taken out of tensor memory and added in registers.
+//   A key's exponent multiplies its scores, a value's its weight: powers of two.  The weights are
+// 2^(score - m), m the head's largest score of the first tile, moved only where a later one passes it by
+// 2^3.9.  log2(e) / sqrt(hd) is multiplied into q, so that what brings a score to the exponent is a power of two
+// and the maximum and the weights see the same number however large it is.
+//
+// The tiles of all items in a row go evenly to the CTAs, two per SM; an item that is cut leaves
+// partial results for a second launch.  In a CTA one warp copies, one starts products, four have a
+// position (then a dimension) per thread.
 #include "nt_kv8.cuh"
 
 namespace nt {
 
+constexpr int kKv8Batch = 512;          // entries of a launch: their first tiles are kept in shared memory
+constexpr int kKv8MaxCtas = 304;        // two per SM; the workspace holds two partial results of each
+constexpr int kKv8Tile = 128;
+
 struct Kv8AttnArgs {
   int32_t layer, n, G, k;
+  int32_t seq0;                         // sequence of entry 0 where none are listed
   const int32_t* seq;
   const int32_t* ctx;
   const int32_t* pages;
@@ -13,107 +38,698 @@ struct Kv8AttnArgs {
   int64_t q_stride;
   float* out;
   int64_t out_stride;
-  float scale;          // log2(e) / sqrt(hd)
+  float scale;                          // log2(e) / sqrt(hd)
+  float* part;                          // [CTA][2] partial results
 };
 
-size_t kv8_attn_ws_bytes(int n_heads, int n_kv, int hd) { return 16; }
+// Partial result of one item: o [HB][HD], then (reference m, sum l) per head, then a header of 4 words (used by a
+// CTA's second: the item, -1 none, and the number of CTAs that worked on it).
+constexpr int kv8_part_floats(int hd, int hb) { return hb * hd + 2 * hb + 4; }
+constexpr int kv8_heads_block(int g) { return g <= 2 ? 2 : g <= 4 ? 4 : g <= 8 ? 8 : 16; }
 
-// A CTA per (entry, kv head), a warp per query head: 32 positions at a time, a lane's
-// score that of its position, then a lane's sums those of its dimensions.
-template <int HD>
-__global__ void __launch_bounds__(256) k_kv8_attn(Kv4 c, Kv8AttnArgs a) {
-  constexpr int V = HD / 32;
-  __shared__ float s_q[kKv8MaxGroup * HD];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int i = int(blockIdx.x / c.n_kv), g = int(blockIdx.x % c.n_kv);
-  kv4_dependent();
-  const int s = a.seq ? a.seq[i] : i;
-  float* out = a.out + int64_t(i) * a.out_stride + int64_t(g) * a.G * HD;
-  uint32_t bad = 0;
-  int n = 0;
-  if (s < 0 || s >= c.max_seqs) {
-    bad = NT_KV4_BAD_SEQ;
-  } else {
-    const int len = c.len[s];
-    n = a.ctx ? a.ctx[i] : len;
-    if (len < 0 || len > c.capacity() || n < 0 || n > len) bad = NT_KV4_BAD_LEN;
-  }
-  if (bad || n == 0) {
-    if (bad && t == 0) kv4_flag(c, bad);
-    for (int x = t; x < a.G * HD; x += 256) out[x] = bad ? NAN : 0.f;
-    return;
-  }
-  for (int x = t; x < a.G * HD; x += 256) s_q[x] = a.q[int64_t(i) * a.q_stride + int64_t(g) * a.G * HD + x];
-  __syncthreads();
-  const int m = int((int64_t(n) + c.page_len - 1) / c.page_len), count = a.k ? a.k : m;
-  const int32_t* list = a.k ? a.pages + (int64_t(i) * c.n_kv + g) * a.k : nullptr;
-  const Kv8Page L(c);
-  for (int h = warp; h < a.G; h += 8) {
-    float M = -INFINITY, sum = 0.f, o[V];
-    bool nan = false;
-    int seen = 0, before = -1;
+size_t kv8_attn_ws_bytes(int n_heads, int n_kv, int hd) {
+  const int g = n_heads / n_kv;
+  return size_t(kKv8MaxCtas) * 2 * kv8_part_floats(hd, kv8_heads_block(g < kKv8MaxGroup ? g : kKv8MaxGroup)) * 4;
+}
+
+template <int HD, int HB>
+struct Kv8AttnCfg {
+  static constexpr int kThreads = 192;                              // four warps of the softmax, one that copies, one that starts products
+  static constexpr int kTerms = 6, kDigits = 8;
+  static constexpr int NS = (kTerms * HB + 15) / 16 * 16, NP = kDigits * HB;
+  static constexpr int S = HD == 128 ? 2 : 4;                       // ring stages
+  static constexpr int kK = kKv8Tile * HD, kStage = 2 * kK + 8 * 16;   // K, V, the pages' exponents
+  static constexpr int kPart = kv8_part_floats(HD, HB);
+  // P^T: blocks of 8 rows (a head's digits) by 16 positions; 16 positions further 64 bytes beyond a multiple of 128, so that
+  // a warp's two runs of 16 bytes fall on different banks
+  static constexpr int kPStep = NP * 16 + 64;
+  // shared memory (V's rows 64 to 127 with 64 dimensions, which nobody looks at, reach 1 KB behind it)
+  static constexpr int kQ = S * kStage;
+  static constexpr int kP = kQ + NS * HD;
+  static constexpr int kRed = kP + 8 * kPStep;                      // [4][HB] of the warps, twice: maxima, sums
+  static constexpr int kPrefix = kRed + 8 * HB * 4;
+  static constexpr int kEntry = kPrefix + (kKv8Batch + 4) * 4;
+  static constexpr int kSums = kEntry + kKv8Batch * 8;
+  static constexpr int kInfo = kSums + 32;                          // [S]: positions of the tile (0: none, -1: it lacks a page)
+  static constexpr int kBars = (kInfo + 4 * S + 7) / 8 * 8;         // full [S], empty [S], scores, taken, weights, outputs
+  static constexpr int kTmem = kBars + 8 * (2 * S + 4);
+  static constexpr int kSegs = kTmem + 4;                           // items whose q is there
+  static constexpr int kSmem = kTmem + 16;
+  static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
+  static constexpr int kColS = 0, kColO = NS, kCols = NS + NP <= 32 ? 32 : NS + NP <= 64 ? 64 : NS + NP <= 128 ? 128 : 256;
+  static_assert(NS + NP <= 256, "tensor memory of two CTAs");
+};
+
+// ------------------------------------------------------------ small pieces --
+
+__device__ __forceinline__ float kv8_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// An operand without swizzle: blocks of 8 rows by 16 bytes; 16 bytes of k further `kstep` bytes, 8 rows further `rstep`.
+__device__ __forceinline__ uint64_t kv8_desc(uint32_t a, uint32_t kstep, uint32_t rstep) {
+  return uint64_t((a & 0x3ffffu) >> 4) | uint64_t(kstep >> 4) << 16 | uint64_t(rstep >> 4) << 32 | uint64_t(1) << 46;
+}
+__device__ __forceinline__ void kv8_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
+      : "memory");
+}
+__device__ __forceinline__ void kv8_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// this lane's row, 16 columns; awaited by kv8_tc_wait
+__device__ __forceinline__ void kv8_tc_ld16(uint32_t a, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a));
+}
+// The loads before have arrived: n registers of theirs are named so that no use moves above.
+template <int N>
+__device__ __forceinline__ void kv8_tc_wait(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int v = 0; v < V; v++) o[v] = 0.f;
-    for (int x = 0; x < count; x++) {
-      const int j = list ? list[x] : x;
-      if (j < 0) break;
-      const int page = j < m && j > before ? c.table[int64_t(s) * c.max_pages + j] : -1;
-      before = j;
-      if (page < 0 || page >= c.n_pages) {
-        if (lane == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
-        nan = true;
+  for (int i = 0; i < N; i++) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void kv8_tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void kv8_tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// One thread of a converged warp, known as such to the compiler.
+__device__ __forceinline__ bool kv8_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// (by a whole warp, the same for all of it)
+__device__ __forceinline__ bool kv8_bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return __all_sync(0xffffffffu, done);
+}
+// Barrier of the four softmax warps; whether any of their threads says so.
+__device__ __forceinline__ bool kv8_any(bool p) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(uint32_t(p))
+      : "memory");
+  return r;
+}
+
+// Sequence and positions of listed entry e (0 positions and *bad where it cannot be read).
+__device__ __forceinline__ int2 kv8_attn_entry(const Kv4& c, const Kv8AttnArgs& a, int e, uint32_t* bad) {
+  const int s = a.seq ? a.seq[e] : a.seq0 + e;
+  *bad = NT_KV4_BAD_SEQ;
+  if (s < 0 || s >= c.max_seqs) return make_int2(-1, 0);
+  const int len = c.len[s], n = a.ctx ? a.ctx[e] : len;
+  *bad = len < 0 || len > c.capacity() || n < 0 || n > len ? NT_KV4_BAD_LEN : 0;
+  return make_int2(*bad ? -1 : s, *bad ? 0 : n);
+}
+
+// Where a CTA is in the row of all tiles: tile ti of nt of kv head g of entry e.
+struct Kv8At {
+  int e, g, ti, nt;
+};
+
+// ------------------------------------------------------------ the kernel --
+
+template <int HD, int HB>
+__global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv4 c, Kv8AttnArgs a) {
+  using Cfg = Kv8AttnCfg<HD, HB>;
+  constexpr int S = Cfg::S, NT = Cfg::kThreads;
+  extern __shared__ __align__(128) uint8_t kv8_sm[];
+  uint8_t* sm = kv8_sm;
+  const uint32_t smu = kv4_smem(sm);
+  int* prefix = reinterpret_cast<int*>(sm + Cfg::kPrefix);
+  int2* entry = reinterpret_cast<int2*>(sm + Cfg::kEntry);
+  volatile int* info = reinterpret_cast<volatile int*>(sm + Cfg::kInfo);
+  volatile int* segs_ready = reinterpret_cast<volatile int*>(sm + Cfg::kSegs);
+  const volatile uint32_t* tensor_memory = reinterpret_cast<const volatile uint32_t*>(sm + Cfg::kTmem);
+  const uint32_t full = smu + Cfg::kBars, empty = full + 8 * S, bar_s = empty + 8 * S, bar_taken = bar_s + 8,
+                 bar_p = bar_taken + 8, bar_o = bar_p + 8;
+  const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31, n = a.n, P = c.page_len;
+
+  if (t == 0) {
+    for (int i = 0; i < S; i++) {
+      kv4_bar_init(full + 8 * i);
+      kv4_bar_init(empty + 8 * i, 5);
+    }
+    kv4_bar_init(bar_s);
+    kv4_bar_init(bar_taken, 4);
+    kv4_bar_init(bar_p, 4);
+    kv4_bar_init(bar_o);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *segs_ready = 0;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (tensor memory only now: a kernel that this one waits for could want it on this SM)
+  if (warp == 5)
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smu + Cfg::kTmem), "n"(Cfg::kCols)
+                 : "memory");
+  // ---- first tiles of all entries
+  auto tiles = [&](int len) {   // of an item whose entry sees len positions
+    int64_t x = (int64_t(len) + P - 1) / P;
+    if (a.k && x > a.k) x = a.k;
+    return a.k ? int((x * P + kKv8Tile - 1) / kKv8Tile) : int((int64_t(len) + kKv8Tile - 1) / kKv8Tile);
+  };
+  {
+    int* sums = reinterpret_cast<int*>(sm + Cfg::kSums);
+    int run = 0;
+    for (int e0 = 0; e0 < n; e0 += NT) {
+      const int e = e0 + t;
+      int mine = 0;
+      if (e < n) {
+        uint32_t bad;
+        const int2 sl = kv8_attn_entry(c, a, e, &bad);
+        if (bad && blockIdx.x == 0) kv4_flag(c, bad);
+        entry[e] = sl;
+        mine = tiles(sl.y) * c.n_kv;
+      }
+      int x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) sums[warp] = x;
+      __syncthreads();
+      int before = 0, all = 0;
+#pragma unroll
+      for (int w = 0; w < NT / 32; w++) {
+        const int y = sums[w];
+        if (w < warp) before += y;
+        all += y;
+      }
+      if (e < n) prefix[e] = run + before + x - mine;
+      run += all;
+      __syncthreads();
+    }
+    if (t == 0) prefix[n] = run;
+    kv8_tc_before();
+    __syncthreads();
+    kv8_tc_after();
+  }
+  const uint32_t tmem = *tensor_memory;
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int total = prefix[n];
+  int share = (total + int(gridDim.x) - 1) / int(gridDim.x);
+  if (share < 1) share = 1;
+  const int c0 = int(blockIdx.x) * share < total ? int(blockIdx.x) * share : total, c1 = c0 + share < total ? c0 + share : total;
+  float* part0 = a.part + int64_t(blockIdx.x) * 2 * Cfg::kPart;
+  int* header = reinterpret_cast<int*>(part0 + 2 * Cfg::kPart - 4);
+
+  auto locate = [&](int x, Kv8At& at) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (prefix[mid] <= x) lo = mid; else hi = mid;
+    }
+    at.e = lo;
+    at.nt = tiles(entry[lo].y);
+    const int r = x - prefix[lo];
+    at.g = r / at.nt;
+    at.ti = r - at.g * at.nt;
+  };
+  auto segment = [&](int x, const Kv8At& at) { return at.nt - at.ti < c1 - x ? at.nt - at.ti : c1 - x; };   // tiles up to the item's or the CTA's end
+
+  if (warp == 4) {
+    // ---- copies.  Lane y knows the page at place first + y of the item's list; the next 32 are looked up a batch ahead.
+    const Kv8Page L(c);
+    const uint8_t* layer_pool = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes();
+    const int per = kKv8Tile / P, codes = P * HD;
+    int no = 0;
+    bool dead = false;
+    for (int x = c0; x < c1 && !dead;) {
+      Kv8At at;
+      locate(x, at);
+      const int count = segment(x, at), len = entry[at.e].y;
+      const int m = int((int64_t(len) + P - 1) / P), listed = a.k && a.k < m ? a.k : m;
+      const int32_t* row = c.table + int64_t(entry[at.e].x) * c.max_pages;
+      const int32_t* list = a.k ? a.pages + (int64_t(at.e) * c.n_kv + at.g) * a.k : nullptr;
+      const int end = (at.ti + count) * per < listed ? (at.ti + count) * per : listed;
+      // the page at place i of the list; -1: none there, -2: the list has ended; *last: it is the sequence's last page
+      auto look = [&](int i, bool* last) -> int {
+        *last = false;
+        if (i >= end) return -2;
+        int j = i;
+        if (list) {
+          j = list[i];
+          const int before = i ? list[i - 1] : -1;
+          if (j < 0) return -2;
+          if (j >= m || j <= before || (i && before < 0)) { kv4_flag(c, NT_KV4_BAD_PAGE); return -1; }
+        }
+        *last = j == m - 1;
+        const int page = row[j];
+        if (page < 0 || page >= c.n_pages) { kv4_flag(c, NT_KV4_BAD_PAGE); return -1; }
+        return page;
+      };
+      bool last, next_last;
+      int first = at.ti * per, page = look(first + lane, &last), next = look(first + 32 + lane, &next_last);
+      for (int i = 0; i < count; i++, no++) {
+        const int at_list = (at.ti + i) * per;
+        if (at_list - first >= 32) {
+          first += 32;
+          page = next;
+          last = next_last;
+          next = look(first + 32 + lane, &next_last);
+        }
+        const int st = no % S, y = at_list - first + lane % 8;
+        const int mine = __shfl_sync(0xffffffffu, page, y & 31);
+        const bool is_last = __shfl_sync(0xffffffffu, int(last), y & 31);
+        const bool live = lane % 8 < per && mine >= 0;
+        const bool lacks = __any_sync(0xffffffffu, lane < per && mine == -1);
+        const int have = __popc(__ballot_sync(0xffffffffu, lane < 8 && live));
+        const bool ends = __any_sync(0xffffffffu, live && is_last);
+        if (no >= S && !__all_sync(0xffffffffu, kv4_bar_wait(empty + 8 * st, uint32_t(no / S - 1) & 1u))) { dead = true; break; }
+        const uint32_t bar = full + 8 * st;
+        __syncwarp();
+        if (lane == 0) {
+          info[st] = lacks ? -1 : have * P - (ends ? m * P - len : 0);
+          if (lacks || !have) kv4_bar_arrive(bar);
+          else kv4_bar_expect(bar, uint32_t(have) * uint32_t(2 * codes + 16));
+        }
+        __syncwarp();
+        if (!lacks && live && lane < 24) {
+          const uint8_t* from = layer_pool + mine * c.page_bytes();
+          const uint32_t to = smu + st * Cfg::kStage;
+          const int z = lane % 8;
+          if (lane < 8) kv4_copy(to + z * codes, from + L.k(at.g), codes, bar);
+          else if (lane < 16) kv4_copy(to + Cfg::kK + z * codes, from + L.v(at.g), codes, bar);
+          else kv4_copy(to + 2 * Cfg::kK + z * 16, from + L.exps(at.g), 16, bar);
+        }
+      }
+      x += count;
+    }
+    if (dead) {   // copies in flight land before the shared memory is given up
+      if (lane == 0) kv4_flag(c, NT_KV4_TIMEOUT);
+      for (int i = no < S ? 0 : no - S; i < no; i++) kv4_bar_wait(full + 8 * (i % S), uint32_t(i / S) & 1u);
+    }
+  } else if (warp == 5) {
+    // ---- products: scores of tile ns as soon as it and q are there and the scores before are taken, outputs of
+    // tile np as soon as its weights are there, whichever comes first
+    constexpr uint32_t kIdesc = 1u << 4 | uint32_t(kKv8Tile / 16) << 24;   // fp32 += e4m3 e4m3, 128 rows
+    constexpr uint32_t kIdescS = kIdesc | uint32_t(Cfg::NS / 8) << 17, kIdescO = kIdesc | uint32_t(Cfg::NP / 8) << 17;
+    const int all = c1 - c0;
+    int ns = 0, np = 0, scored = 0, weighed = 0, segs = 0, left = 0, idle = 0;   // left: tiles of the segment without scores
+    while (np < all) {
+      bool moved = false;
+      if (ns < all && ns - np < S) {
+        const int st = ns % S;
+        bool ok = true;
+        if (left == 0) {
+          ok = __all_sync(0xffffffffu, *segs_ready > segs);   // (a count: items without a live tile may pass several at a time)
+          if (ok) {
+            Kv8At at;
+            locate(c0 + ns, at);
+            left = segment(c0 + ns, at);
+            segs++;
+          }
+        }
+        if (ok && kv8_bar_test(full + 8 * st, uint32_t(ns / S) & 1u)) {
+          if (info[st] <= 0) {
+            ns++;
+            left--;
+            moved = true;
+          } else if (scored == 0 || kv8_bar_test(bar_taken, uint32_t(scored - 1) & 1u)) {
+            kv8_tc_after();
+            if (kv8_elect()) {
+              const uint32_t k0 = smu + st * Cfg::kStage, q0 = smu + Cfg::kQ;
+#pragma unroll
+              for (int kk = 0; kk < HD / 32; kk++)
+                kv8_mma(tmem + Cfg::kColS, kv8_desc(k0 + kk * 256, 128, 8 * HD), kv8_desc(q0 + kk * 256, 128, 8 * HD), kIdescS, kk > 0);
+              kv8_commit(bar_s);
+            }
+            __syncwarp();
+            scored++;
+            ns++;
+            left--;
+            moved = true;
+          }
+        }
+      }
+      if (np < ns) {
+        const int st = np % S;
+        if (info[st] <= 0) {
+          if (lane == 0) kv4_bar_arrive(empty + 8 * st);
+          __syncwarp();
+          np++;
+          moved = true;
+        } else if (kv8_bar_test(bar_p, uint32_t(weighed) & 1u)) {
+          kv8_tc_after();
+          if (kv8_elect()) {
+            const uint32_t v0 = smu + st * Cfg::kStage + Cfg::kK, p0 = smu + Cfg::kP;
+#pragma unroll
+            for (int kk = 0; kk < kKv8Tile / 32; kk++)
+              kv8_mma(tmem + Cfg::kColO, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
+                      kv8_desc(p0 + kk * 2 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
+            kv8_commit(bar_o);
+            kv8_commit(empty + 8 * st);
+          }
+          __syncwarp();
+          weighed++;
+          np++;
+          moved = true;
+        }
+      }
+      idle = moved ? 0 : idle + 1;
+      if (idle > (1 << 24)) {
+        if (lane == 0) kv4_flag(c, NT_KV4_TIMEOUT);
         break;
       }
-      const uint8_t* base = c.pool + (int64_t(a.layer) * c.n_pages + page) * c.page_bytes();
-      const int8_t* ex = reinterpret_cast<const int8_t*>(base + L.exps(g));
-      const float fk = kv8_exp2i(ex[0]), fv = kv8_exp2i(ex[1]);
-      const int live = n - j * c.page_len < c.page_len ? n - j * c.page_len : c.page_len;
-      for (int p0 = 0; p0 < live; p0 += 32) {
-        const int p = p0 + lane;
-        float y = -INFINITY;
-        if (p < live) {
-          y = 0.f;
-          for (int ch = 0; ch < HD / 16; ch++) {
-            const uint4 w = *reinterpret_cast<const uint4*>(base + L.k(g) + kv8_k_at(HD, p, ch));
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int d = 0; d < 8; d++) {
-              const float2 z = kv8_value2(u[d >> 1] >> (16 * (d & 1)));
-              y = fmaf(z.x, s_q[h * HD + 16 * ch + 2 * d], y);
-              y = fmaf(z.y, s_q[h * HD + 16 * ch + 2 * d + 1], y);
-            }
-          }
-          y = y * fk * a.scale;
-          nan |= y != y;
-        }
-        float top = y;
-#pragma unroll
-        for (int b = 16; b; b >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, b));
-        const float to = fmaxf(M, top), f = exp2f(M - to), w = p < live ? exp2f(y - to) : 0.f;
-        M = to;
-        sum = sum * f + w;
-#pragma unroll
-        for (int v = 0; v < V; v++) o[v] *= f;
-        for (int tc = p0 / 16; tc * 16 < live && tc < p0 / 16 + 2; tc++)
-#pragma unroll
-          for (int v = 0; v < V; v++) {
-            const uint4 z = *reinterpret_cast<const uint4*>(base + L.v(g) + kv8_v_at(HD, tc, 32 * v + lane));
-            const uint32_t u[4] = {z.x, z.y, z.z, z.w};
-            for (int b = 0; b < 16; b++) {
-              if (tc * 16 + b >= live) break;
-              const float2 r = kv8_value2(u[b >> 2] >> (16 * (b >> 1 & 1)));
-              o[v] = fmaf((b & 1 ? r.y : r.x) * fv, __shfl_sync(0xffffffffu, w, tc * 16 - p0 + b), o[v]);
-            }
-          }
-      }
-      seen += live;
     }
-    nan = __any_sync(0xffffffffu, nan);
+  } else {
+    // ---- softmax: thread t has position t of a tile, and dimension t of the outputs
+    const uint32_t mine = uint32_t(32 * warp) << 16;   // this warp's rows of tensor memory
+    float* red = reinterpret_cast<float*>(sm + Cfg::kRed);
+    uint8_t* my_p = sm + Cfg::kP + (t >> 4) * Cfg::kPStep + (t & 15);
+    float O[HB], l[HB], mref[HB], cs[HB];
+    uint32_t ps = 0, po = 0;
+    int no = 0, segs = 0;
+    bool dead = false, pending = false;
+    float out_scale = 0.f;                             // of the outputs under way
+
+    auto take = [&]() -> bool {                        // adds them to the sums; false: they never came
+      if (!pending) return true;
+      pending = false;
+      const bool ok = __all_sync(0xffffffffu, kv4_bar_wait(bar_o, po));
+      po ^= 1u;
+      kv8_tc_after();
+      if (HD == 128 || warp < 2) {
 #pragma unroll
-    for (int b = 16; b; b >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, b);
+        for (int b = 0; b < HB / 2; b++) {             // two heads' digits, the lowest first
+          uint32_t r[16];
+          kv8_tc_ld16(tmem + mine + Cfg::kColO + 16 * b, r);
+          kv8_tc_wait(r);
 #pragma unroll
-    for (int v = 0; v < V; v++) out[h * HD + 32 * v + lane] = nan ? NAN : seen ? o[v] / sum : 0.f;
+          for (int h = 0; h < 2; h++) {
+            float v = __uint_as_float(r[8 * h + 7]);
+#pragma unroll
+            for (int d = 6; d >= 0; d--) v = fmaf(v, 16.f, __uint_as_float(r[8 * h + d]));
+            O[2 * b + h] = fmaf(v, out_scale, O[2 * b + h]);
+          }
+        }
+      }
+      kv8_tc_before();
+      return ok;
+    };
+
+#pragma unroll 1
+    for (int x = c0; x < c1;) {
+      Kv8At at;
+      locate(x, at);
+      const int count = segment(x, at);
+      bool poison = dead;
+      // ---- q: scaled so that its largest element is in [2^7, 2^8), in six terms.  A warp takes every fourth head.
+      {
+        const float* qb = a.q + int64_t(at.e) * a.q_stride + int64_t(at.g) * a.G * HD;
+        constexpr int V = HD / 32;
+#pragma unroll 1
+        for (int h = warp; h < HB; h += 4) {
+          float y[V], top = 0.f;
+#pragma unroll
+          for (int i = 0; i < V; i++) {
+            y[i] = h < a.G ? qb[h * HD + V * lane + i] * a.scale : 0.f;
+            if (!(fabsf(y[i]) < INFINITY)) y[i] = NAN;
+            top = fmaxf(top, fabsf(y[i]));             // (a NaN is passed over)
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          int ex = int(__float_as_uint(top) >> 23);
+          ex = ex < 14 ? 14 : ex;                      // (zeros and values below 2^-113)
+          const float up = __uint_as_float(uint32_t(261 - ex) << 23);                  // 2^(134 - ex)
+          if (lane == 0) red[h] = __uint_as_float(uint32_t(ex - 7) << 23);             // 2^(ex - 134)
+          uint8_t* to = sm + Cfg::kQ + (V * lane >> 4) * 128 + (V * lane & 15);
+#pragma unroll
+          for (int i = 0; i < V; i++) y[i] *= up;
+#pragma unroll
+          for (int k = 0; k < Cfg::kTerms; k++) {
+            const int row = k * HB + h;
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+              const uint32_t w = kv8_code2(y[i], y[i + 1]);
+              *reinterpret_cast<uint16_t*>(to + (row >> 3) * 8 * HD + (row & 7) * 16 + i) = uint16_t(w);
+              const float2 f = kv8_value2(w);
+              y[i] = (y[i] - f.x) * 16.f;
+              y[i + 1] = (y[i + 1] - f.y) * 16.f;
+            }
+          }
+        }
+        if constexpr (Cfg::NS > Cfg::kTerms * HB)      // rows of no head
+          for (int i = t; i < (Cfg::NS - Cfg::kTerms * HB) * HD / 16; i += 128) {
+            const int row = Cfg::kTerms * HB + i / (HD / 16);
+            *reinterpret_cast<uint4*>(sm + Cfg::kQ + (row >> 3) * 8 * HD + i % (HD / 16) * 128 + (row & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        kv8_any(false);
+        if (t == 0) {
+          __threadfence_block();
+          *segs_ready = ++segs;
+        }
+#pragma unroll
+        for (int h = 0; h < HB; h++) {
+          cs[h] = red[h];
+          O[h] = l[h] = 0.f;
+          mref[h] = -3e38f;
+        }
+        kv8_any(false);                                // red is read
+      }
+#pragma unroll 1
+      for (int i = 0; i < count; i++, no++) {
+        if (dead) continue;
+        const int st = no % S;
+        bool fail = !__all_sync(0xffffffffu, kv4_bar_wait(full + 8 * st, uint32_t(no / S) & 1u));
+        const int live = info[st];
+        if (live <= 0 || fail) {
+          if (kv8_any(fail)) dead = kv8_any(fail);     // (as many barriers as a tile with scores has)
+          poison = poison || dead || live < 0;
+          __syncwarp();
+          if (lane == 0) kv4_bar_arrive(empty + 8 * st);
+          continue;
+        }
+        const int8_t* exps = reinterpret_cast<const int8_t*>(sm + st * Cfg::kStage + 2 * Cfg::kK);
+        int vmax = -128;
+        for (int y = 0; y * P < live; y++) vmax = max(vmax, int(exps[16 * y + 1]));
+        const bool here = t < live;
+        const int page = here ? t / P : 0, dv = 28 + exps[16 * page + 1] - vmax;
+        const float fk = kv8_exp2i(exps[16 * page]), fv = dv < -126 ? 0.f : kv8_exp2i(dv);
+        if (live < kKv8Tile) {   // values behind the end: zeros, whatever the page holds there
+          uint8_t* v = sm + st * Cfg::kStage + Cfg::kK;
+          if (t < HD)
+            for (int ch = live >> 4; ch < 8; ch++) {
+              uint4* at16 = reinterpret_cast<uint4*>(v + kv8_v_at(HD, ch, t));
+              uint4 w = make_uint4(0u, 0u, 0u, 0u);
+              const int keep = live - 16 * ch;         // bytes that stay
+              if (keep > 0) {
+                w = *at16;
+                auto cut = [&](uint32_t z, int b) { return keep >= b + 4 ? z : keep <= b ? 0u : z & ((1u << (8 * (keep - b))) - 1u); };
+                w = make_uint4(cut(w.x, 0), cut(w.y, 4), cut(w.z, 8), cut(w.w, 12));
+              }
+              *at16 = w;
+            }
+        }
+        // ---- scores
+        fail = !__all_sync(0xffffffffu, kv4_bar_wait(bar_s, ps)) || fail;
+        ps ^= 1u;
+        kv8_tc_after();
+        float s[HB];
+        {
+          constexpr int kCols = HB == 16 ? 48 : Cfg::NS;   // three terms at a time with 16 heads, all otherwise
+#pragma unroll
+          for (int b = Cfg::NS / kCols - 1; b >= 0; b--) {
+            uint32_t r[kCols];
+#pragma unroll
+            for (int y = 0; y < kCols / 16; y++) kv8_tc_ld16(tmem + mine + Cfg::kColS + b * kCols + 16 * y, r + 16 * y);
+            kv8_tc_wait(r);
+            constexpr int kT = HB == 16 ? 3 : Cfg::kTerms;
+#pragma unroll
+            for (int h = 0; h < HB; h++) {
+              float z = __uint_as_float(r[(kT - 1) * HB + h]);
+              if (HB == 16 && b == 0) z = fmaf(s[h], 1.f / 16.f, z);
+#pragma unroll
+              for (int k = kT - 2; k >= 0; k--) z = fmaf(z, 1.f / 16.f, __uint_as_float(r[k * HB + h]));
+              s[h] = z;
+            }
+          }
+        }
+        kv8_tc_before();
+        __syncwarp();
+        if (lane == 0) kv4_bar_arrive(bar_taken);
+#pragma unroll
+        for (int h = 0; h < HB; h++) s[h] = here ? s[h] * fk : -INFINITY;
+        fail = !take() || fail;
+        // ---- weights
+        float p[HB], most;
+        auto weights = [&]() {
+          most = 0.f;
+#pragma unroll
+          for (int h = 0; h < HB; h++) {
+            p[h] = kv8_ex2(fmaf(s[h], cs[h], -mref[h]));
+            most = fmaxf(most, p[h]);
+          }
+        };
+        weights();
+        if (kv8_any(!(most <= 15.f) || fail)) {
+          // A weight may have passed 2^3.9 (at first all are infinite): the maxima over the tile's positions.
+#pragma unroll
+          for (int h = 0; h < HB; h++) {
+            float top = s[h];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (lane == 0) red[warp * HB + h] = top;
+          }
+          dead = kv8_any(fail);
+#pragma unroll
+          for (int h = 0; h < HB; h++) {
+            const float top = fmaxf(fmaxf(red[h], red[HB + h]), fmaxf(red[2 * HB + h], red[3 * HB + h])) * cs[h];
+            const float to = top - mref[h] > 3.f ? top : mref[h], f = kv8_ex2(mref[h] - to);
+            mref[h] = to;
+            l[h] *= f;
+            O[h] *= f;
+          }
+          if (dead) {
+            poison = true;
+            continue;
+          }
+          weights();
+        }
+#pragma unroll
+        for (int h = 0; h < HB; h++) {
+          l[h] += p[h];
+          const uint32_t u = __float2uint_rn(p[h] * fv);
+          const uint32_t even = u & 0x0f0f0f0fu, odd = (u >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+          for (int d = 0; d < 4; d++) {
+            my_p[h * 128 + (2 * d) * 16] = uint8_t(even >> (8 * d));
+            my_p[h * 128 + (2 * d + 1) * 16] = uint8_t(odd >> (8 * d));
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        kv8_tc_before();
+        __syncwarp();
+        if (lane == 0) {
+          kv4_bar_arrive(bar_p);
+          kv4_bar_arrive(empty + 8 * st);
+        }
+        out_scale = kv8_exp2i(vmax - 19);              // digits are 2^-9 of themselves, weights 2^28
+        pending = true;
+      }
+      // ---- the segment's end
+      if (!take() || dead) poison = true;
+      float* sums = red + 4 * HB;
+#pragma unroll
+      for (int h = 0; h < HB; h++) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
+        if (lane == 0) sums[warp * HB + h] = l[h];
+      }
+      poison = kv8_any(poison);
+      const bool whole = at.ti == 0 && count == at.nt, begun = at.ti == 0;
+      float* to = whole ? a.out + int64_t(at.e) * a.out_stride + int64_t(at.g) * a.G * HD : part0 + (begun ? Cfg::kPart : 0);
+#pragma unroll
+      for (int h = 0; h < HB; h++) {
+        float sum = (sums[h] + sums[HB + h]) + (sums[2 * HB + h] + sums[3 * HB + h]);
+        if (poison) sum = NAN;
+        if (t < HD && h < a.G) to[h * HD + t] = whole ? (sum == 0.f ? 0.f : O[h] / sum) : O[h];
+        if (!whole && t == 0) reinterpret_cast<float2*>(to + HB * HD)[h] = make_float2(mref[h], sum);
+      }
+      if (begun && !whole && t == 0) {
+        const int units0 = x;                          // the item's first tile
+        header[1] = (units0 + at.nt - 1) / share - int(blockIdx.x) + 1;
+        header[0] = at.e * c.n_kv + at.g;
+      }
+      x += count;
+      if (x >= c1 && t == 0 && (whole || !begun)) header[0] = -1;   // nothing is left open here
+      kv8_any(false);                                  // the sums are read
+    }
+    if (c0 >= c1 && t == 0) header[0] = -1;
+    // entries without a position: zeros, or NaN where they cannot be read
+    for (int e = blockIdx.x; e < n; e += gridDim.x)
+      if (entry[e].y == 0)
+        for (int y = t; y < c.n_kv * a.G * HD; y += 128) a.out[int64_t(e) * a.out_stride + y] = entry[e].x < 0 ? NAN : 0.f;
   }
+  kv8_tc_before();
+  __syncthreads();
+  if (warp == 5) {
+    kv8_tc_after();
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Cfg::kCols));
+  }
+}
+
+// Items that were cut: block (CTA, head) merges what the CTA blockIdx.x began with what the next ones left, in their order.
+constexpr int kKv8MergeWarps = 4;
+template <int HD>
+__global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8AttnArgs a, int part_floats, int rows) {
+  constexpr int V = HD / 32, NW = kKv8MergeWarps;
+  __shared__ float s_o[NW][HD];
+  __shared__ float2 s_ml[NW];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, h = blockIdx.y;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const float* first = a.part + (int64_t(blockIdx.x) * 2 + 1) * part_floats;   // the second of this CTA, then the first of the next ones
+  const int2 header = __ldcg(reinterpret_cast<const int2*>(first + part_floats - 4));
+  if (header.x < 0) return;
+  float M = -INFINITY, sum = 0.f, o[V];
+#pragma unroll
+  for (int v = 0; v < V; v++) o[v] = 0.f;
+  for (int b = warp; b < header.y; b += NW) {
+    const float* r = b ? first + (int64_t(b) * 2 - 1) * part_floats : first;
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(r + rows * HD) + h);
+    const float to = fmaxf(M, ml.x), was = kv8_ex2(M - to), f = kv8_ex2(ml.x - to);
+    M = to;
+    sum = fmaf(sum, was, ml.y * f);
+#pragma unroll
+    for (int v = 0; v < V; v++) o[v] = fmaf(o[v], was, __ldcg(r + h * HD + 32 * v + lane) * f);
+  }
+#pragma unroll
+  for (int v = 0; v < V; v++) s_o[warp][32 * v + lane] = o[v];
+  if (lane == 0) s_ml[warp] = make_float2(M, sum);
+  __syncthreads();
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < NW; w++) top = fmaxf(top, s_ml[w].x);
+  for (int d = t; d < HD; d += 32 * NW) {
+    float total = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+      const float f = kv8_ex2(s_ml[w].x - top);
+      total = fmaf(s_ml[w].y, f, total);
+      y = fmaf(s_o[w][d], f, y);
+    }
+    const int e = header.x / c.n_kv, g = header.x % c.n_kv;
+    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + d] = total == 0.f ? 0.f : y / total;
+  }
+}
+
+template <int HD, int HB>
+static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t most_tiles, cudaStream_t s) {
+  using Cfg = Kv8AttnCfg<HD, HB>;
+  static const KernelSetup setup = kernel_setup(k_kv8_attn<HD, HB>, Cfg::kSmem);
+  if (setup.err != cudaSuccess) return setup.err;
+  int64_t ctas = 2 * setup.sms < kKv8MaxCtas ? 2 * setup.sms : kKv8MaxCtas;
+  if (ctas > most_tiles) ctas = most_tiles;
+  cudaError_t e = kv4_launch_smem(k_kv8_attn<HD, HB>, unsigned(ctas), unsigned(Cfg::kThreads), size_t(Cfg::kSmem), s, k, a);
+  if (e != cudaSuccess || ctas < 2) return e;
+  // (the last CTA's items end with it)
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(ctas - 1), unsigned(a.G));
+  cfg.blockDim = dim3(32 * kKv8MergeWarps);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_kv8_merge<HD>, k, a, int(Cfg::kPart), HB);
 }
 
 }  // namespace nt
@@ -131,7 +747,8 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
   if (st) return st;
   if (layer < 0 || layer >= k.n_layers) return bad("layer out of range");
   if (n_heads < 1 || n_heads % k.n_kv) return bad("n_heads must be a positive multiple of n_kv_heads");
-  if (n_heads / k.n_kv > kKv8MaxGroup) return fail(NT_E_UNSUPPORTED, std::string(who) + ": more than 16 query heads per kv head");
+  const int G = n_heads / k.n_kv;
+  if (G > kKv8MaxGroup) return fail(NT_E_UNSUPPORTED, std::string(who) + ": more than 16 query heads per kv head");
   if (n < 0 || n > 65536 || (!dev_seq && n > k.max_seqs)) return bad("n out of range");
   if (n_select < 0 || n_select > 65536) return bad("n_select outside [0, 65536]");
   const int64_t row = int64_t(n_heads) * k.hd;
@@ -145,9 +762,8 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
   if (!n_select && dev_pages) return bad("pages without n_select");
   const size_t wb = kv8_attn_ws_bytes(n_heads, k.n_kv, k.hd);
   if (workspace_bytes < wb) return bad("workspace too small");
-  const int64_t items = int64_t(n) * k.n_kv;
-  if (items > (1 << 24)) return bad("n * n_kv_heads above 2^24");
   if (n == 0) return NT_OK;
+  const int64_t items = int64_t(n) * k.n_kv;
   const int64_t qb = ((n - 1) * q_stride + row) * 4, ob = ((n - 1) * out_stride + row) * 4, lb = int64_t(n) * 4;
   auto meets = [&](const void* p, int64_t bytes) {   // a written buffer and everything else
     return kv4_meets_cache(k, p, bytes) || kv4_overlap(p, bytes, dev_q, qb) || (dev_seq && kv4_overlap(p, bytes, dev_seq, lb)) ||
@@ -155,9 +771,39 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
   };
   if (meets(dev_out, ob) || meets(dev_workspace, int64_t(wb)) || kv4_overlap(dev_out, ob, dev_workspace, int64_t(wb)))
     return bad("the output or the workspace overlaps another buffer");
-  const Kv8AttnArgs a{layer, n, n_heads / k.n_kv, n_select, dev_seq, dev_ctx, dev_pages, dev_q, q_stride, dev_out, out_stride,
-                      1.4426950408889634f / sqrtf(float(k.hd))};
+  // a launch's tiles are counted in 32 bits
+  const int64_t entry_pages = n_select && n_select < k.max_pages ? n_select : k.max_pages;
+  const int64_t entry_tiles = int64_t(k.n_kv) * ((entry_pages * k.page_len + kKv8Tile - 1) / kKv8Tile), most = int64_t(1) << 30;
+  if (entry_tiles > most) return bad("n_kv_heads * max_pages * page_len is too large");
+  const int32_t batch = entry_tiles * kKv8Batch <= most ? kKv8Batch : int32_t(most / entry_tiles);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  NT_CUDA(k.hd == 64 ? kv4_launch(k_kv8_attn<64>, unsigned(items), 256u, s, k, a) : kv4_launch(k_kv8_attn<128>, unsigned(items), 256u, s, k, a));
+  Kv8AttnArgs a{};
+  a.layer = layer;
+  a.G = G;
+  a.k = n_select;
+  a.q_stride = q_stride;
+  a.out_stride = out_stride;
+  a.scale = 1.4426950408889634f / sqrtf(float(k.hd));
+  a.part = static_cast<float*>(dev_workspace);
+  for (int32_t i = 0; i < n; i += batch) {
+    a.n = n - i < batch ? n - i : batch;
+    a.seq0 = i;
+    a.seq = dev_seq ? dev_seq + i : nullptr;
+    a.ctx = dev_ctx ? dev_ctx + i : nullptr;
+    a.pages = n_select ? dev_pages + int64_t(i) * k.n_kv * n_select : nullptr;
+    a.q = dev_q + int64_t(i) * q_stride;
+    a.out = dev_out + int64_t(i) * out_stride;
+    const int64_t tiles = a.n * entry_tiles;
+    cudaError_t e;
+    if (k.hd == 64)
+      e = G <= 2 ? kv8_launch_attn<64, 2>(k, a, tiles, s)
+                 : G <= 4 ? kv8_launch_attn<64, 4>(k, a, tiles, s)
+                          : G <= 8 ? kv8_launch_attn<64, 8>(k, a, tiles, s) : kv8_launch_attn<64, 16>(k, a, tiles, s);
+    else
+      e = G <= 2 ? kv8_launch_attn<128, 2>(k, a, tiles, s)
+                 : G <= 4 ? kv8_launch_attn<128, 4>(k, a, tiles, s)
+                          : G <= 8 ? kv8_launch_attn<128, 8>(k, a, tiles, s) : kv8_launch_attn<128, 16>(k, a, tiles, s);
+    if (e != cudaSuccess) return cuda_fail(e, who);
+  }
   return NT_OK;
 }
