@@ -191,10 +191,13 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     *segs_ready = 0;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  // (tensor memory only now: a kernel that this one waits for could want it on this SM)
-  if (warp == 5)
+  // (tensor memory only now: a kernel that this one waits for could want it on this SM; and the right to take it goes on at
+  // once: the other CTA of the SM waits for it)
+  if (warp == 5) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smu + Cfg::kTmem), "n"(Cfg::kCols)
                  : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
   // ---- first tiles of all entries
   auto tiles = [&](int len) {   // of an item whose entry sees len positions
     int64_t x = (int64_t(len) + P - 1) / P;
@@ -660,7 +663,6 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   __syncthreads();
   if (warp == 5) {
     kv8_tc_after();
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Cfg::kCols));
   }
 }
