@@ -26,8 +26,11 @@ nt_status kv8_check(const nt_kv8_cache* c, const char* who, bool pointers, Kv4* 
 // for it; in plain fp32 a key next to the border of two codes would get the wrong one
 // about once in 10^6 values.)
 
+struct __align__(16) Kv8Point {
+  float c, cl, s, sl;   // cos, sin: the sums of two terms
+};
 struct Kv8Circle {
-  float c[256], cl[256], s[256], sl[256];
+  Kv8Point p[256];
 };
 constexpr double kv8_series(double x, bool sine) {   // |x| <= pi / 4
   double term = sine ? x : 1.0, sum = term;
@@ -45,24 +48,21 @@ constexpr Kv8Circle kv8_circle() {
     const double x = off * kPi / 128, cc = kv8_series(x, false), ss = kv8_series(x, true);
     const double c = quarter % 4 == 0 ? cc : quarter % 4 == 1 ? -ss : quarter % 4 == 2 ? -cc : ss;
     const double s = quarter % 4 == 0 ? ss : quarter % 4 == 1 ? cc : quarter % 4 == 2 ? -ss : -cc;
-    t.c[i] = float(c);
-    t.cl[i] = float(c - double(t.c[i]));
-    t.s[i] = float(s);
-    t.sl[i] = float(s - double(t.s[i]));
+    t.p[i].c = float(c);
+    t.p[i].cl = float(c - double(t.p[i].c));
+    t.p[i].s = float(s);
+    t.p[i].sl = float(s - double(t.p[i].s));
   }
   return t;
 }
 __device__ constexpr Kv8Circle kKv8Circle = kv8_circle();
 
-struct Kv8Turn {
-  float c, cl, s, sl;   // cos, sin: the sums of two terms
-};
 // a + b in two terms (a in hi already: hi = a + b rounded)
 __device__ __forceinline__ float kv8_rest(float a, float b, float hi) {
   const float bb = __fsub_rn(hi, a);
   return __fadd_rn(__fsub_rn(a, __fsub_rn(hi, bb)), __fsub_rn(b, bb));
 }
-__device__ __forceinline__ Kv8Turn kv8_turn(uint64_t phase, int pos) {
+__device__ __forceinline__ Kv8Point kv8_turn(uint64_t phase, int pos) {
   const uint64_t turn = phase * uint64_t(uint32_t(pos));
   const uint32_t i = uint32_t((turn + (1ull << 55)) >> 56) & 255u;
   const int64_t rest = int64_t(turn - (uint64_t(i) << 56));                  // in [-2^55, 2^55)
@@ -75,12 +75,13 @@ __device__ __forceinline__ Kv8Turn kv8_turn(uint64_t phase, int pos) {
   // sin r and cos r - 1
   const float s = r, sl = __fsub_rn(rl, __fmul_rn(__fmul_rn(q, r), __fmaf_rn(q, -1.f / 120.f, 1.f / 6.f)));
   const float m = -0.5f * q, ml = __fmaf_rn(__fmul_rn(q, q), __fmaf_rn(q, -1.f / 720.f, 1.f / 24.f), -0.5f * ql);
-  const float C = kKv8Circle.c[i], Cl = kKv8Circle.cl[i], S = kKv8Circle.s[i], Sl = kKv8Circle.sl[i];
+  const float4 at = *reinterpret_cast<const float4*>(&kKv8Circle.p[i]);
+  const float C = at.x, Cl = at.y, S = at.z, Sl = at.w;
   auto times = [](float x, float xl, float y, float yl, float& p) {          // (x + xl) (y + yl) = p + the rest
     p = __fmul_rn(x, y);
     return __fadd_rn(__fmaf_rn(x, y, -p), __fmaf_rn(x, yl, __fmul_rn(xl, y)));
   };
-  Kv8Turn t;
+  Kv8Point t;
   float p1, p2;
   const float e1 = times(C, Cl, m, ml, p1), e2 = times(S, Sl, s, sl, p2);
   const float d = __fsub_rn(p1, p2);
@@ -99,25 +100,43 @@ __device__ __forceinline__ float kv8_dot2(float a, float c, float cl, float b, f
   const float r = __fadd_rn(d, __fadd_rn(kv8_rest(p, q, d), __fadd_rn(e, f)));
   return fabsf(r) <= 3.4028234e38f && (r != 0.f || d != 0.f) ? r : d;   // (an infinity leaves no rest, a zero keeps its sign)
 }
-__device__ __forceinline__ void kv8_rotate(const Kv8Turn& t, float& a, float& b) {
+__device__ __forceinline__ void kv8_rotate(const Kv8Point& t, float& a, float& b) {
   const float x = kv8_dot2(a, t.c, t.cl, b, -t.s, -t.sl);
   b = kv8_dot2(a, t.s, t.sl, b, t.c, t.cl);
   a = x;
 }
 
+// cos and sin to fp32's last bit (within 2^-24.9 of 1)
+__device__ __forceinline__ float2 kv8_turn_fast(uint64_t phase, int pos) {
+  const uint64_t turn = phase * uint64_t(uint32_t(pos));
+  const uint32_t i = uint32_t((turn + (1ull << 55)) >> 56) & 255u;
+  constexpr float k = float(6.283185307179586477 * 0x1p-32);
+  const float r = float(int32_t(uint32_t(turn >> 32) - (i << 24))) * k, q = r * r;
+  const float s = fmaf(r * q, -1.f / 6.f, r), m = q * fmaf(q, 1.f / 24.f, -0.5f);
+  const float4 at = *reinterpret_cast<const float4*>(&kKv8Circle.p[i]);
+  return make_float2(at.x + fmaf(at.x, m, fmaf(-at.z, s, at.y)), at.z + fmaf(at.z, m, fmaf(at.x, s, at.w)));
+}
+
 // ------------------------------------------------------------ append, read --
 //
-// A CTA handles K or V of one page of one sequence and kv head, the rows that fall on
-// its positions: the page's exponent needs all of them before the first code.
+// append: a CTA takes the K or the V of one page of one sequence, the rows that fall on its positions, for
+// several kv heads one after the other, the next one's rows on the way; the page's exponent needs all rows of a head before the
+// first code.  A thread has 32 values: of K 4 dimensions of 8 positions (cos and sin of the page's positions stand in
+// shared memory for all heads, and four threads exchange their codes for runs of 16), of V 2 dimensions of 16 positions (a run each).
+//   A key is rotated in fp32, which is off by less than d = 2^-21 (|x| + |y|) of its pair; where x + d and x - d have
+// different codes (about one value in 10^4), or the largest magnitude of a warp lies that near to where the exponent changes, the warp
+// takes those rows again to 2^-45.
+// read: a warp handles K or V of 16 positions of one sequence and kv head.
 
 struct Kv8Rot {
   uint64_t phase[64];   // turns per position, as 64-bit fractions
   int32_t on, heads;
+  int32_t splits, per;  // CTAs that share a page's kv heads, and heads (times those side by side) that each takes
   int64_t q_stride, out_stride;
   float* out;
 };
 
-constexpr int kKv8RowThreads = 256;
+constexpr int kKv8AppendCtas = 4 * 152;   // (see nt_kv8_append)
 constexpr int kKv8QHeads = 4;   // heads that a warp rotates
 
 template <class T> struct Kv8Quad;   // four elements of a source
@@ -160,13 +179,13 @@ __device__ __forceinline__ void kv8_rotate_q(const Kv4& c, const Kv4Rows& a, con
                                              int64_t id) {
   constexpr int kLanes = HD / 4;           // of a head
   const int lane = threadIdx.x & 31, groups = (r.heads + kKv8QHeads - 1) / kKv8QHeads;
-  const int64_t unit = id * (kKv8RowThreads / 32) + (threadIdx.x >> 5);
+  const int64_t unit = id * (blockDim.x / 32) + (threadIdx.x >> 5);
   if (unit >= int64_t(a.n_rows) * groups) return;
   const int row = int(unit / groups), h0 = int(unit % groups) * kKv8QHeads;
   const int pos = kv8_row_pos(c, a, row);
   if (pos < 0) return;
   const int i = lane % kLanes;
-  const Kv8Turn t0 = kv8_turn(phase[2 * i], pos), t1 = kv8_turn(phase[2 * i + 1], pos);
+  const Kv8Point t0 = kv8_turn(phase[2 * i], pos), t1 = kv8_turn(phase[2 * i + 1], pos);
 #pragma unroll
   for (int y = 0; y < kKv8QHeads; y += 32 / kLanes) {
     const int h = h0 + y + lane / kLanes;
@@ -178,183 +197,444 @@ __device__ __forceinline__ void kv8_rotate_q(const Kv4& c, const Kv4Rows& a, con
   }
 }
 
-template <int HD, class T>
-__global__ void __launch_bounds__(kKv8RowThreads) k_kv8_append(Kv4 c, Kv4Rows a, Kv8Rot r, const T* k, const T* v, const T* q) {
-  constexpr int NT = kKv8RowThreads, kQuads = HD / 4, kStride = HD + 4;
-  extern __shared__ __align__(16) float kv8_rows[];   // [page_len][kStride]
-  __shared__ uint64_t s_phase[HD / 2];
-  __shared__ float s_top[NT / 32];
+// What the threads of an append know of their page.
+struct Kv8Mine {
+  uint8_t* base;         // the page
+  int64_t row_stride;    // of the source
+  int p0, pos0;          // first position within the page, and of the sequence
+  int d0;                // first dimension
+  int first, last;       // the page's new positions
+  uint32_t live;         // bit i: position p0 + i is one of them
+  bool fresh;
+  __device__ __forceinline__ bool has(int i) const { return live >> i & 1u; }
+};
+template <int HD, int NT>
+struct Kv8AppendShared {
+  static constexpr int kGroups = NT / (HD / 4);     // of 8 positions, over all heads side by side
+  uint64_t phase[HD / 2];
+  int exp[2][NT / 32];
+  uint32_t lo[2][kGroups * HD / 2], hi[2][kGroups * HD / 2];   // f16 pairs
+};
+extern __shared__ __align__(16) float kv8_turns[];   // [position of the page][pair / 2]: cos of both pairs, sin of both
+
+// Keys of the positions in `which` (of 8; 4 dimensions each) to 2^-45, into out [8][4].
+template <class T>
+__device__ __noinline__ void kv8_exact_keys(const T* from, int64_t row_stride, uint32_t which, bool turned, const uint64_t* phase, int pos0,
+                                            float* out) {
+#pragma unroll 1
+  for (int i = 0; i < 8; i++) {
+    if (!(which >> i & 1u)) continue;
+    float4 y = Kv8Quad<T>::get(from + i * row_stride);
+    if (turned) {
+      kv8_rotate(kv8_turn(phase[0], pos0 + i), y.x, y.y);
+      kv8_rotate(kv8_turn(phase[1], pos0 + i), y.z, y.w);
+    }
+    out[4 * i] = kv8_held(y.x) ? y.x : NAN;
+    out[4 * i + 1] = kv8_held(y.y) ? y.y : NAN;
+    out[4 * i + 2] = kv8_held(y.z) ? y.z : NAN;
+    out[4 * i + 3] = kv8_held(y.w) ? y.w : NAN;
+  }
+}
+
+template <class T> struct Kv8Raw;   // what a thread has of a head as it comes: 8 times 4 (K) or 16 times 2 (V) elements
+template <> struct Kv8Raw<float> {
+  static constexpr int kWords = 32;
+  static __device__ __forceinline__ void get4(const float* p, uint32_t* w) {
+    const uint4 y = *reinterpret_cast<const uint4*>(p);
+    w[0] = y.x; w[1] = y.y; w[2] = y.z; w[3] = y.w;
+  }
+  static __device__ __forceinline__ void get2(const float* p, uint32_t* w) {
+    const uint2 y = *reinterpret_cast<const uint2*>(p);
+    w[0] = y.x; w[1] = y.y;
+  }
+  static __device__ __forceinline__ float2 pair(const uint32_t* w, int i) { return make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])); }
+};
+template <> struct Kv8Raw<__half> {
+  static constexpr int kWords = 16;
+  static __device__ __forceinline__ void get4(const __half* p, uint32_t* w) {
+    const uint2 y = *reinterpret_cast<const uint2*>(p);
+    w[0] = y.x; w[1] = y.y;
+  }
+  static __device__ __forceinline__ void get2(const __half* p, uint32_t* w) { w[0] = *reinterpret_cast<const uint32_t*>(p); }
+  static __device__ __forceinline__ float2 pair(const uint32_t* w, int i) { return __half22float2(*reinterpret_cast<const __half2*>(w + i)); }
+};
+
+__device__ __forceinline__ uint32_t kv8_min2(uint32_t a, uint32_t b) {   // of f16 pairs, NaN where one is
+  uint32_t d;
+  asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t kv8_max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+template <class T, bool V>
+__device__ __forceinline__ void kv8_load(const Kv8Mine& me, const T* from, bool on, uint32_t (&w)[Kv8Raw<T>::kWords]) {
+  constexpr int N = V ? 16 : 8, E = Kv8Raw<T>::kWords / N;
+#pragma unroll
+  for (int i = 0; i < N; i++) {
+    if (on && me.has(i)) {
+      if (V) Kv8Raw<T>::get2(from, w + E * i); else Kv8Raw<T>::get4(from, w + E * i);
+    } else {
+#pragma unroll
+      for (int j = 0; j < E; j++) w[E * i + j] = 0u;
+    }
+    from += me.row_stride;
+  }
+}
+
+// Exponent that a warp's values need; an infinity or what lies beyond the largest that can be held is the caller's affair first.
+__device__ __forceinline__ float kv8_largest(const float (&x)[32]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));   // (a NaN is passed over)
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+
+// Codes of a head's V: a thread's 2 dimensions of 16 positions, a run each.
+template <int HD>
+__device__ __forceinline__ void kv8_put_v(const Kv8Mine& me, const float (&x)[32], uint8_t* to, float up, bool again, float f) {
+  uint32_t w[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; j++)
+#pragma unroll
+    for (int i = 0; i < 4; i++) w[j][i] = kv8_code4(x[8 * i + j] * up, x[8 * i + 2 + j] * up, x[8 * i + 4 + j] * up, x[8 * i + 6 + j] * up);
+  uint4* at = reinterpret_cast<uint4*>(to + kv8_v_at(HD, me.p0 >> 4, me.d0));
+  if (me.live == 0xffffu) {
+#pragma unroll
+    for (int j = 0; j < 2; j++) at[j] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+    return;
+  }
+  // positions of this run: new [first, last), older below
+  const int first = max(me.first - me.p0, 0), last = min(me.last - me.p0, 16);
+  if (!(last > first || (again && first > 0))) return;
+#pragma unroll
+  for (int j = 0; j < 2; j++) {
+    const uint4 was = at[j];
+    const uint32_t old[4] = {was.x, was.y, was.z, was.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      auto below = [&](int n) { n -= 4 * i; return n >= 4 ? 0xffffffffu : n <= 0 ? 0u : (1u << (8 * n)) - 1u; };   // bytes of positions below n
+      const uint32_t older = below(first < 16 ? first : 16), mine = below(last) & ~older;
+      const uint32_t kept = again ? kv8_again(old[i], f) : old[i];
+      w[j][i] = (w[j][i] & mine) | (kept & older) | (old[i] & ~(mine | older));
+    }
+    at[j] = make_uint4(w[j][0], w[j][1], w[j][2], w[j][3]);
+  }
+}
+
+// Codes of a head's K: a thread's 4 dimensions of 8 positions (w), which four threads exchange for 16 dimensions of 2 positions each.
+template <int HD>
+__device__ __forceinline__ void kv8_put_k(const Kv8Mine& me, uint32_t (&w)[8], uint8_t* to, bool on, bool again, float f) {
+  const int n = threadIdx.x & 3;
+  // w[2 m + b] is position 2 m + b: exchange the m of threads whose n differs in bit 1, then in bit 0
+#pragma unroll
+  for (int b = 0; b < 2; b++) {
+#pragma unroll
+    for (int m = 0; m < 2; m++) {
+      const uint32_t give = n & 2 ? w[2 * m + b] : w[2 * (m + 2) + b], got = __shfl_xor_sync(0xffffffffu, give, 2);
+      if (n & 2) w[2 * m + b] = got; else w[2 * (m + 2) + b] = got;
+    }
+#pragma unroll
+    for (int m = 0; m < 4; m += 2) {
+      const uint32_t give = n & 1 ? w[2 * m + b] : w[2 * (m + 1) + b], got = __shfl_xor_sync(0xffffffffu, give, 1);
+      if (n & 1) w[2 * m + b] = got; else w[2 * (m + 1) + b] = got;
+    }
+  }
+  if (!on) return;
+#pragma unroll
+  for (int b = 0; b < 2; b++) {
+    const int p = me.p0 + 2 * n + b;
+    uint4* at = reinterpret_cast<uint4*>(to + kv8_k_at(HD, p, me.d0 >> 4));
+    if (me.has(2 * n + b)) *at = make_uint4(w[b], w[2 + b], w[4 + b], w[6 + b]);
+    else if (again && p < me.first) *at = kv8_again(*at, f);
+  }
+}
+
+// K (or V) of a page for the kv heads g, g + abreast, ... below g1 and of the split's `steps`.
+template <int HD, class T, int NT, bool V>
+__device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, const Kv8Mine& me, Kv8AppendShared<HD, NT>& sh, const T* src,
+                                                int64_t head_stride, bool turned, int g, int abreast, int steps) {
+  const int t = threadIdx.x, lane = t & 31, P = c.page_len, tph = P * HD / 32, hp = t / tph, th = t % tph, wph = tph / 32;
+  uint32_t raw[Kv8Raw<T>::kWords];
+  kv8_load<T, V>(me, src + int64_t(g) * head_stride, g < c.n_kv, raw);
+#pragma unroll 1
+  for (int step = 0; step < steps; step++, g += abreast) {
+    const int buf = step & 1;
+    const bool on = g < c.n_kv;
+    int8_t* exps = reinterpret_cast<int8_t*>(me.base + L.exps(on ? g : 0)) + V;
+    const int was = me.fresh ? kKv8MinExp : *exps;
+    float x[32];
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      const float2 y = Kv8Raw<T>::pair(raw, i);
+      x[2 * i] = y.x; x[2 * i + 1] = y.y;
+    }
+    const T* from = src + int64_t(g) * head_stride;
+    if (step + 1 < steps) kv8_load<T, V>(me, from + int64_t(abreast) * head_stride, g + abreast < c.n_kv, raw);   // the next head's, on the way
+    if (!V && turned) {
+      const float4* turn = reinterpret_cast<const float4*>(kv8_turns) + me.p0 * (HD / 4) + me.d0 / 4;
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const float4 z = turn[i * (HD / 4)];
+        const float u0 = x[4 * i], u1 = x[4 * i + 1], u2 = x[4 * i + 2], u3 = x[4 * i + 3];
+        x[4 * i] = fmaf(u0, z.x, -u1 * z.z);
+        x[4 * i + 2] = fmaf(u2, z.y, -u3 * z.w);
+        const float2 y = kv8_unpack(kv8_fma2(kv8_pack(u0, u2), kv8_pack(z.z, z.w), kv8_mul2(kv8_pack(u1, u3), kv8_pack(z.x, z.y))));
+        x[4 * i + 1] = y.x;
+        x[4 * i + 3] = y.y;
+      }
+    }
+    bool exact = V || !turned;
+    float top = kv8_largest(x);
+    constexpr uint32_t kNear = 64;                                     // of 2^-23: farther than the error of x
+    const uint32_t from_border = (__float_as_uint(top) & 0x7fffffu) - (0x600000u - kNear);
+    if (__float_as_uint(top) > __float_as_uint(kKv8Most) - kNear || (!exact && from_border <= 2 * kNear)) {
+      if (V) {
+#pragma unroll
+        for (int i = 0; i < 32; i++) x[i] = kv8_held(x[i]) ? x[i] : NAN;
+      } else {
+        float y[32];
+#pragma unroll
+        for (int i = 0; i < 32; i++) y[i] = 0.f;
+        kv8_exact_keys(from, me.row_stride, on ? me.live : 0u, turned, sh.phase + me.d0 / 2, me.pos0, y);
+#pragma unroll
+        for (int i = 0; i < 32; i++) x[i] = y[i];
+      }
+      exact = true;
+      top = kv8_largest(x);
+    }
+    if (lane == 0) sh.exp[buf][t >> 5] = kv8_exponent(top);
+    __syncthreads();
+    const int e = max(was, __reduce_max_sync(0xffffffffu, lane < wph ? sh.exp[buf][hp * wph + lane] : kKv8MinExp));
+    const float up = kv8_exp2i(-e);
+    const int less = e - was;                                          // exponents that older codes are rounded for
+    const bool again = !me.fresh && less > 0;
+    const float f = kv8_exp2i(less > 126 ? -126 : -less);              // (from 2^-20 on every code is rounded to zero)
+    if (V) {
+      if (on) kv8_put_v<HD>(me, x, me.base + L.v(g), up, again, f);
+    } else {
+      uint32_t w[8], z[8], differ = 0u;                                // codes of a position's 4 dimensions, of x - d and x + d
+      const uint64_t up2 = kv8_pack(up, up), off = kv8_pack(up * 0x1p-21f, up * 0x1p-21f), minus = kv8_pack(up * -0x1p-21f, up * -0x1p-21f);
+      if (exact) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) w[i] = z[i] = kv8_code4(x[4 * i] * up, x[4 * i + 1] * up, x[4 * i + 2] * up, x[4 * i + 3] * up);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          const uint64_t x02 = kv8_pack(x[4 * i], x[4 * i + 2]), x13 = kv8_pack(x[4 * i + 1], x[4 * i + 3]);
+          const uint64_t size = kv8_pack(fabsf(x[4 * i]) + fabsf(x[4 * i + 1]), fabsf(x[4 * i + 2]) + fabsf(x[4 * i + 3]));
+          const uint64_t d = kv8_mul2(size, off), md = kv8_mul2(size, minus);
+          const float2 l02 = kv8_unpack(kv8_fma2(x02, up2, md)), l13 = kv8_unpack(kv8_fma2(x13, up2, md));
+          const float2 h02 = kv8_unpack(kv8_fma2(x02, up2, d)), h13 = kv8_unpack(kv8_fma2(x13, up2, d));
+          w[i] = kv8_code4(l02.x, l13.x, l02.y, l13.y);
+          z[i] = kv8_code4(h02.x, h13.x, h02.y, h13.y);
+          differ |= w[i] ^ z[i];
+        }
+        if (differ) {
+          differ = 0u;
+#pragma unroll
+          for (int i = 0; i < 8; i++) differ |= uint32_t(w[i] != z[i]) << i;
+        }
+      }
+      differ = __reduce_or_sync(0xffffffffu, differ);
+      if (differ) {
+        float y[32];
+        kv8_exact_keys(from, me.row_stride, on ? me.live & differ : 0u, turned, sh.phase + me.d0 / 2, me.pos0, y);
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          if (on && (me.live & differ) >> i & 1u) w[i] = kv8_code4(y[4 * i] * up, y[4 * i + 1] * up, y[4 * i + 2] * up, y[4 * i + 3] * up);
+      }
+      // ---- bounds of this thread's positions
+      uint32_t lo[2] = {0x7c007c00u, 0x7c007c00u}, hi[2] = {0xfc00fc00u, 0xfc00fc00u};
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        uint32_t y[2];
+        kv8_half4(w[i], y[0], y[1]);
+        if (me.has(i)) {
+#pragma unroll
+          for (int j = 0; j < 2; j++) {
+            lo[j] = kv8_min2(lo[j], y[j]);
+            hi[j] = kv8_max2(hi[j], y[j]);
+          }
+        }
+      }
+      const int group = t / (HD / 4);
+      *reinterpret_cast<uint2*>(&sh.lo[buf][group * (HD / 2) + me.d0 / 2]) = make_uint2(lo[0], lo[1]);
+      *reinterpret_cast<uint2*>(&sh.hi[buf][group * (HD / 2) + me.d0 / 2]) = make_uint2(hi[0], hi[1]);
+      kv8_put_k<HD>(me, w, me.base + L.k(on ? g : 0), on, again, f);
+      __syncthreads();
+      // ---- the page's
+      const int groups = P / 8;
+      if (on)
+        for (int i = th; i < HD / 2; i += tph) {   // two dimensions
+          uint32_t least = 0x7c007c00u, most = 0xfc00fc00u;
+#pragma unroll 4
+          for (int y = 0; y < groups; y++) {
+            least = kv8_min2(least, sh.lo[buf][(hp * groups + y) * (HD / 2) + i]);
+            most = kv8_max2(most, sh.hi[buf][(hp * groups + y) * (HD / 2) + i]);
+          }
+          int8_t* b = reinterpret_cast<int8_t*>(me.base + L.bounds(g)) + 2 * i;
+#pragma unroll
+          for (int j = 0; j < 2; j++) {
+            const float l = __half2float(__ushort_as_half(uint16_t(least >> (16 * j)))), h = __half2float(__ushort_as_half(uint16_t(most >> (16 * j))));
+            int lo1 = l != l ? -127 : int(floorf(l * 0.25f)), hi1 = l != l ? 127 : int(ceilf(h * 0.25f));
+            if (!me.fresh) {
+              int lo0 = b[j], hi0 = b[HD + j];
+              if (lo0 != -127) lo0 = int(floorf(lo0 * f));
+              if (hi0 != 127) hi0 = int(ceilf(hi0 * f));
+              lo1 = min(lo1, lo0);
+              hi1 = max(hi1, hi0);
+            }
+            b[j] = int8_t(lo1);
+            b[HD + j] = int8_t(hi1);
+          }
+        }
+    }
+    if (on && th == 0) *exps = int8_t(e);
+  }
+}
+
+template <int HD, class T, int NT>
+__global__ void __launch_bounds__(NT, NT == 512 ? 1 : sizeof(T) == 2 ? 3 : 2) k_kv8_append(Kv4 c, Kv4Rows a, Kv8Rot r, const T* k, const T* v,
+                                                                                         const T* q) {
+  __shared__ Kv8AppendShared<HD, NT> sh;
   const int t = threadIdx.x;
-  for (int i = t; i < HD / 2; i += NT) s_phase[i] = r.phase[i];
-  __syncthreads();
+  if (r.on)
+    for (int i = t; i < HD / 2; i += NT) sh.phase[i] = r.phase[i];
   kv4_dependent();
   if (kv4_check_rows(c, a)) return;
-  const int64_t id = int64_t(blockIdx.x) - a.checks, pages = int64_t(a.units) * c.n_kv * 2;
+  const int64_t id = int64_t(blockIdx.x) - a.checks, pages = int64_t(a.units) * r.splits * 2;
   if (id >= pages) {
-    kv8_rotate_q<HD, T>(c, a, r, s_phase, q, id - pages);
+    __syncthreads();
+    kv8_rotate_q<HD, T>(c, a, r, sh.phase, q, id - pages);
     return;
   }
   const bool is_v = id & 1;
-  const int g = int(id / 2 % c.n_kv);
+  const int P = c.page_len, split = int(id / 2 % r.splits);
   Kv4Span sp;
-  if (!kv4_span(c, a, int(id / 2 / c.n_kv), &sp, c.page_len)) return;
-  const int page = c.table[int64_t(sp.s) * c.max_pages + sp.p0 / c.page_len];
+  if (!kv4_span(c, a, int(id / 2 / r.splits), &sp, P)) return;
+  const int page = c.table[int64_t(sp.s) * c.max_pages + sp.p0 / P];
   if (page < 0 || page >= c.n_pages || c.refs[page] != 1) {
     if (t == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
     return;
   }
   const Kv8Page L(c);
-  uint8_t* base = c.pool + (int64_t(a.layer) * c.n_pages + page) * c.page_bytes();
-  // ---- the rows, rotated, into shared memory; their largest magnitude
-  const T* src = (is_v ? v : k) + int64_t(sp.row - sp.first) * a.row_stride + int64_t(g) * a.head_stride;   // of position 0
-  float top = 0.f;
-  const int quad = t % kQuads;
-  for (int p = sp.first + t / kQuads; p < sp.last; p += NT / kQuads) {
-    float4 x = Kv8Quad<T>::get(src + int64_t(p) * a.row_stride + 4 * quad);
-    if (!is_v && r.on) {
-      kv8_rotate(kv8_turn(s_phase[2 * quad], sp.p0 + p), x.x, x.y);
-      kv8_rotate(kv8_turn(s_phase[2 * quad + 1], sp.p0 + p), x.z, x.w);
-    }
-    *reinterpret_cast<float4*>(kv8_rows + p * kStride + 4 * quad) = x;
-    auto size = [](float y) { return kv8_held(y) ? fabsf(y) : 0.f; };
-    top = fmaxf(top, fmaxf(fmaxf(size(x.x), size(x.y)), fmaxf(size(x.z), size(x.w))));
+  const int tph = P * HD / 32, th = t % tph, abreast = NT / tph;      // threads of a head, heads side by side
+  Kv8Mine me;
+  me.base = c.pool + (int64_t(a.layer) * c.n_pages + page) * c.page_bytes();
+  me.row_stride = a.row_stride;
+  me.d0 = is_v ? 2 * (th % (HD / 2)) : 4 * (th % (HD / 4));
+  me.p0 = is_v ? 16 * (th / (HD / 2)) : 8 * (th / (HD / 4));
+  me.pos0 = sp.p0 + me.p0;
+  me.first = sp.first;
+  me.last = sp.last;
+  me.fresh = sp.first == 0;
+  me.live = 0u;
+  for (int i = 0; i < (is_v ? 16 : 8); i++)
+    if (me.p0 + i >= sp.first && me.p0 + i < sp.last) me.live |= 1u << i;
+  const int g = split * r.per * abreast + t / tph;
+  const int left = (c.n_kv - split * r.per * abreast + abreast - 1) / abreast, steps = left < r.per ? left : r.per;
+  const T* src = (is_v ? v : k) + int64_t(sp.row - sp.first + me.p0) * a.row_stride + me.d0;
+  if (is_v) {
+    kv8_append_page<HD, T, NT, true>(c, L, me, sh, src, a.head_stride, false, g, abreast, steps);
+    return;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((t & 31) == 0) s_top[t >> 5] = top;
-  int8_t* exps = reinterpret_cast<int8_t*>(base + L.exps(g)) + is_v;
-  const bool fresh = sp.first == 0;
-  const int was = fresh ? kKv8MinExp : *exps;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < NT / 32; i++) top = fmaxf(top, s_top[i]);
-  int e = kv8_exponent(top);
-  if (e < was) e = was;
-  const float up = kv8_exp2i(-e);
-  const int less = e - was;                                            // exponents that older codes are rounded for
-  const bool again = !fresh && less > 0;
-  const float f = kv8_exp2i(less > 126 ? -126 : -less);                // (from 2^-20 on every code is rounded to zero)
-  if (!is_v) {
-    uint8_t* to = base + L.k(g);
-    for (int i = t; i < sp.last * (HD / 16); i += NT) {
-      const int p = i % sp.last, ch = i / sp.last;
-      uint4* at = reinterpret_cast<uint4*>(to + kv8_k_at(HD, p, ch));
-      if (p < sp.first) {
-        if (again) *at = kv8_again(*at, f);
-        continue;
-      }
-      uint32_t w[4];
-#pragma unroll
-      for (int y = 0; y < 4; y++) {
-        const float4 x = *reinterpret_cast<const float4*>(kv8_rows + p * kStride + 16 * ch + 4 * y);
-        w[y] = kv8_code4(kv8_scaled(x.x, up), kv8_scaled(x.y, up), kv8_scaled(x.z, up), kv8_scaled(x.w, up));
-      }
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
+  __syncthreads();   // the phases
+  if (r.on) {
+    for (int i = t + sp.first * (HD / 2); i < sp.last * (HD / 2); i += NT) {
+      const float2 z = kv8_turn_fast(sh.phase[i % (HD / 2)], sp.p0 + i / (HD / 2));
+      kv8_turns[(i >> 1) * 4 + (i & 1)] = z.x;
+      kv8_turns[(i >> 1) * 4 + (i & 1) + 2] = z.y;
     }
-    // bounds: the least and the largest value round to the least and the largest code
-    if (t < HD) {
-      float least = INFINITY, most = -INFINITY;
-      bool nan = false;
-      for (int p = sp.first; p < sp.last; p++) {
-        const float x = kv8_rows[p * kStride + t];
-        nan |= !kv8_held(x);
-        least = fminf(least, x);
-        most = fmaxf(most, x);
-      }
-      const float2 y = kv8_value2(kv8_code2(least * up, most * up));
-      int lo = nan ? -127 : int(floorf(y.x * 0.25f)), hi = nan ? 127 : int(ceilf(y.y * 0.25f));
-      int8_t* b = reinterpret_cast<int8_t*>(base + L.bounds(g)) + t;
-      if (!fresh) {
-        int lo0 = b[0], hi0 = b[HD];
-        if (lo0 != -127) lo0 = int(floorf(lo0 * f));
-        if (hi0 != 127) hi0 = int(ceilf(hi0 * f));
-        lo = lo0 < lo ? lo0 : lo;
-        hi = hi0 > hi ? hi0 : hi;
-      }
-      b[0] = int8_t(lo);
-      b[HD] = int8_t(hi);
-    }
-  } else {
-    uint8_t* to = base + L.v(g);
-    const int tc0 = again ? 0 : sp.first / 16, tcs = (sp.last + 15) / 16 - tc0;
-    for (int i = t; i < tcs * HD; i += NT) {
-      const int tc = tc0 + i / HD, d = i % HD, p0 = 16 * tc;
-      uint4* at = reinterpret_cast<uint4*>(to + kv8_v_at(HD, tc, d));
-      uint4 old = make_uint4(0u, 0u, 0u, 0u);
-      if (p0 < sp.first || p0 + 16 > sp.last) old = *at;
-      uint32_t w[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-      for (int y = 0; y < 4; y++) {
-        const uint32_t kept = again ? kv8_again(w[y], f) : w[y];
-        uint32_t mine = 0u, mask = 0u, held = 0u;                      // the word's new bytes, and those of older positions
-        float x[4];
-#pragma unroll
-        for (int b = 0; b < 4; b++) {
-          const int p = p0 + 4 * y + b;
-          const bool live = p >= sp.first && p < sp.last;
-          x[b] = live ? kv8_scaled(kv8_rows[p * kStride + d], up) : 0.f;
-          if (live) mask |= 0xffu << (8 * b);
-          if (p < sp.first) held |= 0xffu << (8 * b);
-        }
-        mine = kv8_code4(x[0], x[1], x[2], x[3]);
-        w[y] = (mine & mask) | (kept & held) | (w[y] & ~(mask | held));
-      }
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    __syncthreads();
   }
-  if (t == 0) *exps = int8_t(e);
+  kv8_append_page<HD, T, NT, false>(c, L, me, sh, src, a.head_stride, r.on, g, abreast, steps);
 }
 
-__device__ __forceinline__ void kv8_put(float* p, float x) { *p = x; }
-__device__ __forceinline__ void kv8_put(__half* p, float x) { *p = __float2half_rn(x); }
+// Four values into consecutive elements.
+__device__ __forceinline__ void kv8_put4(float* p, float2 a, float2 b) { *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y); }
+__device__ __forceinline__ void kv8_put4(__half* p, float2 a, float2 b) {
+  const __half2 lo = __floats2half2_rn(a.x, a.y), hi = __floats2half2_rn(b.x, b.y);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+// Four words of four bytes each, transposed.
+__device__ __forceinline__ void kv8_transpose(uint32_t (&w)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[0], w[1], 0x7362);
+  const uint32_t c = __byte_perm(w[2], w[3], 0x5140), d = __byte_perm(w[2], w[3], 0x7362);
+  w[0] = __byte_perm(a, c, 0x5410);
+  w[1] = __byte_perm(a, c, 0x7632);
+  w[2] = __byte_perm(b, d, 0x5410);
+  w[3] = __byte_perm(b, d, 0x7632);
+}
+
+constexpr int kKv8ReadWarps = 4;   // warps of a CTA: each K or V of a (unit, kv head)
 
 template <int HD, class T>
-__global__ void __launch_bounds__(kKv8RowThreads) k_kv8_read(Kv4 c, Kv4Rows a, T* k, T* v) {
-  constexpr int NT = kKv8RowThreads;
-  const int t = threadIdx.x;
+__global__ void __launch_bounds__(32 * kKv8ReadWarps) k_kv8_read(Kv4 c, Kv4Rows a, T* k, T* v) {
+  const int lane = threadIdx.x & 31;
+  const int64_t id = (int64_t(blockIdx.x) - a.checks) * kKv8ReadWarps + (threadIdx.x >> 5);   // (below 0: see kv4_check_rows)
+  const int g = int(id / 2 % c.n_kv);
+  const int64_t u = id / 2 / c.n_kv;
+  if (u >= a.units) return;
   kv4_dependent();
   if (kv4_check_rows(c, a)) return;
-  const int64_t id = int64_t(blockIdx.x) - a.checks;
-  const bool is_v = id & 1;
-  const int g = int(id / 2 % c.n_kv);
   Kv4Span sp;
-  if (!kv4_span(c, a, int(id / 2 / c.n_kv), &sp, c.page_len)) return;
+  if (!kv4_span(c, a, int(u), &sp)) return;
   const int page = c.table[int64_t(sp.s) * c.max_pages + sp.p0 / c.page_len];
   if (page < 0 || page >= c.n_pages) {
-    if (t == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
+    if (lane == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
     return;
   }
   const Kv8Page L(c);
   const uint8_t* base = c.pool + (int64_t(a.layer) * c.n_pages + page) * c.page_bytes();
-  const float f = kv8_exp2i(reinterpret_cast<const int8_t*>(base + L.exps(g))[is_v]);
-  T* to = (is_v ? v : k) + int64_t(sp.row - sp.first) * a.row_stride + int64_t(g) * a.head_stride;   // of position 0
-  if (!is_v) {
-    const uint8_t* from = base + L.k(g);
-    for (int i = t; i < (sp.last - sp.first) * (HD / 16); i += NT) {
-      const int p = sp.first + i / (HD / 16), ch = i % (HD / 16);
-      const uint4 w = *reinterpret_cast<const uint4*>(from + kv8_k_at(HD, p, ch));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const int at0 = sp.p0 % c.page_len;                                  // the chunk's place in its page
+  const int8_t* exps = reinterpret_cast<const int8_t*>(base + L.exps(g));
+  const int64_t row0 = int64_t(sp.row - sp.first) * a.row_stride + int64_t(g) * a.head_stride;
+  constexpr int kLanes = HD / 4, kRows = 32 / kLanes;                  // lanes of a row, rows side by side
+  const int d = 4 * (lane % kLanes), sub = lane / kLanes;
+  auto put = [&](T* to, uint32_t w, float f) {
+    float2 x = kv8_value2(w & 0xffffu), y = kv8_value2(w >> 16);
+    x.x *= f; x.y *= f; y.x *= f; y.y *= f;
+    kv8_put4(to, x, y);
+  };
+  if (!(id & 1)) {
+    // four dimensions a lane, a word
+    const uint8_t* from = base + L.k(g) + kv8_k_at(HD, at0, d >> 4) + (d & 15);
+    uint32_t w[16 / kRows];
 #pragma unroll
-      for (int y = 0; y < 8; y++) {
-        const float2 x = kv8_value2(u[y >> 1] >> (16 * (y & 1)));
-        T* at = to + int64_t(p) * a.row_stride + 16 * ch + 2 * y;
-        kv8_put(at, x.x * f);
-        kv8_put(at + 1, x.y * f);
-      }
+    for (int i = 0; i < 16 / kRows; i++) w[i] = *reinterpret_cast<const uint32_t*>(from + kv8_k_at(HD, i * kRows + sub, 0));
+    const float f = kv8_exp2i(exps[0]);
+#pragma unroll
+    for (int i = 0; i < 16 / kRows; i++) {
+      const int p = i * kRows + sub;
+      if (p >= sp.first && p < sp.last) put(k + row0 + int64_t(p) * a.row_stride + d, w[i], f);
     }
   } else {
-    const uint8_t* from = base + L.v(g);
-    const int tc0 = sp.first / 16, tcs = (sp.last + 15) / 16 - tc0;
-    for (int i = t; i < tcs * HD; i += NT) {
-      const int tc = tc0 + i / HD, d = i % HD;
-      const uint4 w = *reinterpret_cast<const uint4*>(from + kv8_v_at(HD, tc, d));
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    // four dimensions of 16 positions (64 dimensions: of 8), their bytes turned round
+    constexpr int kPos = 16 / kRows;
+    const uint8_t* from = base + L.v(g) + kv8_v_at(HD, at0 >> 4, d) + kPos * sub;
+    uint32_t w[kPos / 4][4];
 #pragma unroll
-      for (int y = 0; y < 16; y++) {
-        const int p = 16 * tc + y;
-        if (p < sp.first || p >= sp.last) continue;
-        const float2 x = kv8_value2(u[y >> 2] >> (16 * (y >> 1 & 1)));
-        kv8_put(to + int64_t(p) * a.row_stride + d, (y & 1 ? x.y : x.x) * f);
+    for (int j = 0; j < 4; j++) {
+      if (kPos == 16) {
+        const uint4 y = *reinterpret_cast<const uint4*>(from + 16 * j);
+        w[0][j] = y.x; w[1][j] = y.y; w[2 % (kPos / 4)][j] = y.z; w[3 % (kPos / 4)][j] = y.w;
+      } else {
+        const uint2 y = *reinterpret_cast<const uint2*>(from + 16 * j);
+        w[0][j] = y.x; w[1][j] = y.y;
+      }
+    }
+    const float f = kv8_exp2i(exps[1]);
+#pragma unroll
+    for (int i = 0; i < kPos / 4; i++) {
+      kv8_transpose(w[i]);
+#pragma unroll
+      for (int b = 0; b < 4; b++) {
+        const int p = kPos * sub + 4 * i + b;
+        if (p >= sp.first && p < sp.last) put(v + row0 + int64_t(p) * a.row_stride + d, w[i][b], f);
       }
     }
   }
@@ -371,13 +651,23 @@ static uint64_t kv8_phase(double f) {
   return (uint64_t(a) << 32) + uint64_t(int64_t(std::nearbyint(b)) + int64_t(rest));
 }
 
-template <int HD, class T>
+// CTA of an append: the threads of one page and kv head, 256 at least (then several heads side by side).
+static int kv8_append_threads(const Kv4& k) { return k.page_len * k.hd / 32 > 256 ? 512 : 256; }
+
+template <int HD, class T, int NT>
 static cudaError_t kv8_launch_append(const Kv4& k, const Kv4Rows& a, const Kv8Rot& r, unsigned grid, cudaStream_t s, const void* pk,
                                      const void* pv, const void* pq) {
-  static const KernelSetup setup = kernel_setup(k_kv8_append<HD, T>, 128 * (HD + 4) * 4);
+  static const KernelSetup setup = kernel_setup(k_kv8_append<HD, T, NT>, 128 * HD * 4);
   if (setup.err != cudaSuccess) return setup.err;
-  return kv4_launch_smem(k_kv8_append<HD, T>, grid, unsigned(kKv8RowThreads), size_t(k.page_len) * (HD + 4) * 4, s, k, a, r,
+  return kv4_launch_smem(k_kv8_append<HD, T, NT>, grid, unsigned(NT), r.on ? size_t(k.page_len) * HD * 4 : 0, s, k, a, r,
                          static_cast<const T*>(pk), static_cast<const T*>(pv), static_cast<const T*>(pq));
+}
+template <class T>
+static cudaError_t kv8_launch_append(const Kv4& k, const Kv4Rows& a, const Kv8Rot& r, unsigned grid, cudaStream_t s, const void* pk,
+                                     const void* pv, const void* pq) {
+  if (k.hd == 64) return kv8_launch_append<64, T, 256>(k, a, r, grid, s, pk, pv, pq);
+  return kv8_append_threads(k) == 512 ? kv8_launch_append<128, T, 512>(k, a, r, grid, s, pk, pv, pq)
+                                      : kv8_launch_append<128, T, 256>(k, a, r, grid, s, pk, pv, pq);
 }
 
 }  // namespace nt
@@ -495,19 +785,18 @@ nt_status nt_kv8_append(const nt_kv8_cache* c, int32_t layer, int32_t n, const i
         kv4_overlap(dev_seq, dev_seq ? int64_t(n) * 4 : 0, dev_q_out, ob) ||
         kv4_overlap(dev_begin, dev_begin ? int64_t(n) * 4 + 4 : 0, dev_q_out, ob))
       return bad("q_out overlaps another buffer");
-    const int64_t warps = int64_t(n_rows) * ((n_heads + kKv8QHeads - 1) / kKv8QHeads);
-    q_ctas = (warps + kKv8RowThreads / 32 - 1) / (kKv8RowThreads / 32);
+    const int64_t warps = int64_t(n_rows) * ((n_heads + kKv8QHeads - 1) / kKv8QHeads), of_cta = kv8_append_threads(k) / 32;
+    q_ctas = (warps + of_cta - 1) / of_cta;
   }
-  const int64_t grid = int64_t(a.units) * k.n_kv * 2 + a.checks + q_ctas;
+  // Heads of a page one after the other in a CTA where there are CTAs enough; else each in a CTA of its own.
+  const int abreast = kv8_append_threads(k) * 32 / (k.page_len * k.hd), steps = (k.n_kv + abreast - 1) / abreast;
+  r.per = int64_t(a.units) * 2 >= kKv8AppendCtas ? steps : 1;
+  r.splits = (steps + r.per - 1) / r.per;
+  const int64_t grid = int64_t(a.units) * r.splits * 2 + a.checks + q_ctas;
   if (grid > 0x7fffffffLL) return bad("too many rows for one call");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if (type == NT_F32)
-    e = k.hd == 64 ? kv8_launch_append<64, float>(k, a, r, unsigned(grid), s, dev_k, dev_v, dev_q)
-                   : kv8_launch_append<128, float>(k, a, r, unsigned(grid), s, dev_k, dev_v, dev_q);
-  else
-    e = k.hd == 64 ? kv8_launch_append<64, __half>(k, a, r, unsigned(grid), s, dev_k, dev_v, dev_q)
-                   : kv8_launch_append<128, __half>(k, a, r, unsigned(grid), s, dev_k, dev_v, dev_q);
+  const cudaError_t e = type == NT_F32 ? kv8_launch_append<float>(k, a, r, unsigned(grid), s, dev_k, dev_v, dev_q)
+                                       : kv8_launch_append<__half>(k, a, r, unsigned(grid), s, dev_k, dev_v, dev_q);
   if (e != cudaSuccess) return cuda_fail(e, who);
   if (dev_seq && n > 1) NT_CUDA(kv4_launch_listed_twice(k, n, dev_seq, s));
   return NT_OK;
@@ -521,8 +810,8 @@ nt_status nt_kv8_read(const nt_kv8_cache* c, int32_t layer, int32_t n, const int
   Kv4 k;
   nt_status st = kv8_check(c, who, true, &k);
   if (st) return st;
-  const Kv4Rows a{layer, n, n_rows, kv4_units(n, n_rows, dev_begin, k.page_len), kv4_checks(n, n_rows, dev_begin), dev_seq,
-                  dev_begin, row_stride, head_stride};
+  const Kv4Rows a{layer, n, n_rows, kv4_units(n, n_rows, dev_begin), kv4_checks(n, n_rows, dev_begin), dev_seq, dev_begin, row_stride,
+                  head_stride};
   st = kv4_rows_check(who, k, a, type, dev_k, dev_v);
   if (!st) st = kv4_array_check(k, who, dev_seq, n, true, nullptr, 0);
   if (!st) st = kv4_array_check(k, who, dev_begin, int64_t(n) + 1, true, nullptr, 0);
@@ -536,10 +825,8 @@ nt_status nt_kv8_read(const nt_kv8_cache* c, int32_t layer, int32_t n, const int
       kv4_overlap(dev_seq, int64_t(n) * 4, dev_k, bytes) || kv4_overlap(dev_seq, int64_t(n) * 4, dev_v, bytes) ||
       kv4_overlap(dev_begin, int64_t(n) * 4 + 4, dev_k, bytes) || kv4_overlap(dev_begin, int64_t(n) * 4 + 4, dev_v, bytes))
     return bad("an output overlaps another buffer");
-  const int64_t grid = int64_t(a.units) * k.n_kv * 2 + a.checks;
-  if (grid > 0x7fffffffLL) return bad("too many rows for one call");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned nt = kKv8RowThreads, gr = unsigned(grid);
+  const unsigned nt = 32u * kKv8ReadWarps, gr = unsigned((int64_t(a.units) * k.n_kv * 2 + kKv8ReadWarps - 1) / kKv8ReadWarps + a.checks);
   if (type == NT_F32) {
     float *pk = static_cast<float*>(dev_k), *pv = static_cast<float*>(dev_v);
     NT_CUDA(k.hd == 64 ? kv4_launch(k_kv8_read<64, float>, gr, nt, s, k, a, pk, pv) : kv4_launch(k_kv8_read<128, float>, gr, nt, s, k, a, pk, pv));
