@@ -356,16 +356,20 @@ __device__ __forceinline__ void kv8_put_k(const Kv8Mine& me, uint32_t (&w)[8], u
 // K (or V) of a page for the kv heads g, g + abreast, ... below g1 and of the split's `steps`.
 template <int HD, class T, int NT, bool V>
 __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, const Kv8Mine& me, Kv8AppendShared<HD, NT>& sh, const T* src,
-                                                int64_t head_stride, bool turned, int g, int abreast, int steps) {
+                                                int64_t head_stride, bool turned, int g, int abreast, int steps,
+                                                uint32_t (&raw)[Kv8Raw<T>::kWords]) {
   const int t = threadIdx.x, lane = t & 31, P = c.page_len, tph = P * HD / 32, hp = t / tph, th = t % tph, wph = tph / 32;
-  uint32_t raw[Kv8Raw<T>::kWords];
-  kv8_load<T, V>(me, src + int64_t(g) * head_stride, g < c.n_kv, raw);
+  const bool busy = __any_sync(0xffffffffu, me.live != 0u);            // the warp has new positions
 #pragma unroll 1
   for (int step = 0; step < steps; step++, g += abreast) {
     const int buf = step & 1;
     const bool on = g < c.n_kv;
     int8_t* exps = reinterpret_cast<int8_t*>(me.base + L.exps(on ? g : 0)) + V;
     const int was = me.fresh ? kKv8MinExp : *exps;
+    const bool two = !V && on && th < HD / 2;                          // two dimensions of the page's bounds
+    int8_t* bounds = reinterpret_cast<int8_t*>(me.base + L.bounds(on ? g : 0)) + 2 * th;
+    const char2 lo_was = two && !me.fresh ? *reinterpret_cast<const char2*>(bounds) : make_char2(127, 127);
+    const char2 hi_was = two && !me.fresh ? *reinterpret_cast<const char2*>(bounds + HD) : make_char2(-127, -127);
     float x[32];
 #pragma unroll
     for (int i = 0; i < 16; i++) {
@@ -374,7 +378,7 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
     }
     const T* from = src + int64_t(g) * head_stride;
     if (step + 1 < steps) kv8_load<T, V>(me, from + int64_t(abreast) * head_stride, g + abreast < c.n_kv, raw);   // the next head's, on the way
-    if (!V && turned) {
+    if (!V && turned && busy) {
       const float4* turn = reinterpret_cast<const float4*>(kv8_turns) + me.p0 * (HD / 4) + me.d0 / 4;
 #pragma unroll
       for (int i = 0; i < 8; i++) {
@@ -416,7 +420,10 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
     if (V) {
       if (on) kv8_put_v<HD>(me, x, me.base + L.v(g), up, again, f);
     } else {
-      uint32_t w[8], z[8], differ = 0u;                                // codes of a position's 4 dimensions, of x - d and x + d
+      uint32_t lo[2] = {0x7c007c00u, 0x7c007c00u}, hi[2] = {0xfc00fc00u, 0xfc00fc00u};   // bounds of this thread's positions
+      uint32_t w[8] = {};
+      if (busy) {
+      uint32_t z[8], differ = 0u;                                      // codes of a position's 4 dimensions, of x - d and x + d
       const uint64_t up2 = kv8_pack(up, up), off = kv8_pack(up * 0x1p-21f, up * 0x1p-21f), minus = kv8_pack(up * -0x1p-21f, up * -0x1p-21f);
       if (exact) {
 #pragma unroll
@@ -447,8 +454,6 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
         for (int i = 0; i < 8; i++)
           if (on && (me.live & differ) >> i & 1u) w[i] = kv8_code4(y[4 * i] * up, y[4 * i + 1] * up, y[4 * i + 2] * up, y[4 * i + 3] * up);
       }
-      // ---- bounds of this thread's positions
-      uint32_t lo[2] = {0x7c007c00u, 0x7c007c00u}, hi[2] = {0xfc00fc00u, 0xfc00fc00u};
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         uint32_t y[2];
@@ -461,44 +466,46 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
           }
         }
       }
+      }
       const int group = t / (HD / 4);
       *reinterpret_cast<uint2*>(&sh.lo[buf][group * (HD / 2) + me.d0 / 2]) = make_uint2(lo[0], lo[1]);
       *reinterpret_cast<uint2*>(&sh.hi[buf][group * (HD / 2) + me.d0 / 2]) = make_uint2(hi[0], hi[1]);
-      kv8_put_k<HD>(me, w, me.base + L.k(on ? g : 0), on, again, f);
+      if (busy || again) kv8_put_k<HD>(me, w, me.base + L.k(on ? g : 0), on, again, f);
       __syncthreads();
       // ---- the page's
       const int groups = P / 8;
-      if (on)
-        for (int i = th; i < HD / 2; i += tph) {   // two dimensions
-          uint32_t least = 0x7c007c00u, most = 0xfc00fc00u;
+      if (two) {
+        uint32_t least = 0x7c007c00u, most = 0xfc00fc00u;
 #pragma unroll 4
-          for (int y = 0; y < groups; y++) {
-            least = kv8_min2(least, sh.lo[buf][(hp * groups + y) * (HD / 2) + i]);
-            most = kv8_max2(most, sh.hi[buf][(hp * groups + y) * (HD / 2) + i]);
-          }
-          int8_t* b = reinterpret_cast<int8_t*>(me.base + L.bounds(g)) + 2 * i;
-#pragma unroll
-          for (int j = 0; j < 2; j++) {
-            const float l = __half2float(__ushort_as_half(uint16_t(least >> (16 * j)))), h = __half2float(__ushort_as_half(uint16_t(most >> (16 * j))));
-            int lo1 = l != l ? -127 : int(floorf(l * 0.25f)), hi1 = l != l ? 127 : int(ceilf(h * 0.25f));
-            if (!me.fresh) {
-              int lo0 = b[j], hi0 = b[HD + j];
-              if (lo0 != -127) lo0 = int(floorf(lo0 * f));
-              if (hi0 != 127) hi0 = int(ceilf(hi0 * f));
-              lo1 = min(lo1, lo0);
-              hi1 = max(hi1, hi0);
-            }
-            b[j] = int8_t(lo1);
-            b[HD + j] = int8_t(hi1);
-          }
+        for (int y = 0; y < groups; y++) {
+          least = kv8_min2(least, sh.lo[buf][(hp * groups + y) * (HD / 2) + th]);
+          most = kv8_max2(most, sh.hi[buf][(hp * groups + y) * (HD / 2) + th]);
         }
+        auto bound = [&](int j, int lo0, int hi0, int8_t& l1, int8_t& h1) {
+          const float l = __half2float(__ushort_as_half(uint16_t(least >> (16 * j)))), h = __half2float(__ushort_as_half(uint16_t(most >> (16 * j))));
+          int lo1 = l != l ? -127 : int(floorf(l * 0.25f)), hi1 = l != l ? 127 : int(ceilf(h * 0.25f));
+          if (!me.fresh) {
+            if (lo0 != -127) lo0 = int(floorf(lo0 * f));
+            if (hi0 != 127) hi0 = int(ceilf(hi0 * f));
+            lo1 = min(lo1, lo0);
+            hi1 = max(hi1, hi0);
+          }
+          l1 = int8_t(lo1);
+          h1 = int8_t(hi1);
+        };
+        int8_t l0, l1, h0, h1;
+        bound(0, lo_was.x, hi_was.x, l0, h0);
+        bound(1, lo_was.y, hi_was.y, l1, h1);
+        *reinterpret_cast<char2*>(bounds) = make_char2(l0, l1);
+        *reinterpret_cast<char2*>(bounds + HD) = make_char2(h0, h1);
+      }
     }
     if (on && th == 0) *exps = int8_t(e);
   }
 }
 
 template <int HD, class T, int NT>
-__global__ void __launch_bounds__(NT, NT == 512 ? 1 : sizeof(T) == 2 ? 3 : 2) k_kv8_append(Kv4 c, Kv4Rows a, Kv8Rot r, const T* k, const T* v,
+__global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) k_kv8_append(Kv4 c, Kv4Rows a, Kv8Rot r, const T* k, const T* v,
                                                                                          const T* q) {
   __shared__ Kv8AppendShared<HD, NT> sh;
   const int t = threadIdx.x;
@@ -516,15 +523,9 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : sizeof(T) == 2 ? 3 : 2) k_
   const int P = c.page_len, split = int(id / 2 % r.splits);
   Kv4Span sp;
   if (!kv4_span(c, a, int(id / 2 / r.splits), &sp, P)) return;
-  const int page = c.table[int64_t(sp.s) * c.max_pages + sp.p0 / P];
-  if (page < 0 || page >= c.n_pages || c.refs[page] != 1) {
-    if (t == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
-    return;
-  }
   const Kv8Page L(c);
   const int tph = P * HD / 32, th = t % tph, abreast = NT / tph;      // threads of a head, heads side by side
   Kv8Mine me;
-  me.base = c.pool + (int64_t(a.layer) * c.n_pages + page) * c.page_bytes();
   me.row_stride = a.row_stride;
   me.d0 = is_v ? 2 * (th % (HD / 2)) : 4 * (th % (HD / 4));
   me.p0 = is_v ? 16 * (th / (HD / 2)) : 8 * (th / (HD / 4));
@@ -538,12 +539,12 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : sizeof(T) == 2 ? 3 : 2) k_
   const int g = split * r.per * abreast + t / tph;
   const int left = (c.n_kv - split * r.per * abreast + abreast - 1) / abreast, steps = left < r.per ? left : r.per;
   const T* src = (is_v ? v : k) + int64_t(sp.row - sp.first + me.p0) * a.row_stride + me.d0;
-  if (is_v) {
-    kv8_append_page<HD, T, NT, true>(c, L, me, sh, src, a.head_stride, false, g, abreast, steps);
-    return;
-  }
-  __syncthreads();   // the phases
-  if (r.on) {
+  uint32_t raw[Kv8Raw<T>::kWords];                                    // (on the way while the page is looked up)
+  if (is_v) kv8_load<T, true>(me, src + int64_t(g) * a.head_stride, g < c.n_kv, raw);
+  else kv8_load<T, false>(me, src + int64_t(g) * a.head_stride, g < c.n_kv, raw);
+  const int page = c.table[int64_t(sp.s) * c.max_pages + sp.p0 / P];
+  if (!is_v && r.on) {
+    __syncthreads();   // the phases
     for (int i = t + sp.first * (HD / 2); i < sp.last * (HD / 2); i += NT) {
       const float2 z = kv8_turn_fast(sh.phase[i % (HD / 2)], sp.p0 + i / (HD / 2));
       kv8_turns[(i >> 1) * 4 + (i & 1)] = z.x;
@@ -551,7 +552,13 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : sizeof(T) == 2 ? 3 : 2) k_
     }
     __syncthreads();
   }
-  kv8_append_page<HD, T, NT, false>(c, L, me, sh, src, a.head_stride, r.on, g, abreast, steps);
+  if (page < 0 || page >= c.n_pages || c.refs[page] != 1) {
+    if (t == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
+    return;
+  }
+  me.base = c.pool + (int64_t(a.layer) * c.n_pages + page) * c.page_bytes();
+  if (is_v) kv8_append_page<HD, T, NT, true>(c, L, me, sh, src, a.head_stride, false, g, abreast, steps, raw);
+  else kv8_append_page<HD, T, NT, false>(c, L, me, sh, src, a.head_stride, r.on, g, abreast, steps, raw);
 }
 
 // Four values into consecutive elements.
