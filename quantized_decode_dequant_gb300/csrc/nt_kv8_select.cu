@@ -16,11 +16,12 @@ struct Kv8SelectArgs {
   const int32_t* ctx;
   const float* q;
   int64_t q_stride;
-  uint32_t* keys;       // [n][n_kv][max_pages]
+  uint32_t* keys;       // [n][n_kv][kv8_key_stride]
   int32_t* out;         // [n][n_kv][k]
 };
 
-size_t kv8_select_ws_bytes(const Kv4& k, int64_t n) { return (size_t(n) * k.n_kv * k.max_pages * 4 + 15) / 16 * 16; }
+__host__ __device__ __forceinline__ int64_t kv8_key_stride(const Kv4& k) { return (int64_t(k.max_pages) + 3) / 4 * 4; }
+size_t kv8_select_ws_bytes(const Kv4& k, int64_t n) { return size_t(n) * k.n_kv * kv8_key_stride(k) * 4; }
 
 // Sequence of entry i and the positions that it sees (-1: cannot be read, the bit in *bad).
 __device__ __forceinline__ int2 kv8_entry(const Kv4& c, const int32_t* seq, const int32_t* ctx, int i, uint32_t* bad) {
@@ -33,13 +34,15 @@ __device__ __forceinline__ int2 kv8_entry(const Kv4& c, const int32_t* seq, cons
 }
 
 constexpr int kKv8ScoreThreads = 256;
+constexpr int kKv8ScorePages = 16;   // of a warp at a time
 
-// Keys of the pages of (entry, kv head) blockIdx.x / a.splits: whole numbers in the order of the scores.
+// Keys of the pages of (entry, kv head) blockIdx.x / a.splits: whole numbers in the order of the scores.  A warp takes 16
+// pages at a time, eight lanes each; their places in the pool are looked up a round ahead.
 template <int HD>
 __global__ void __launch_bounds__(kKv8ScoreThreads) k_kv8_scores(Kv4 c, Kv8SelectArgs a) {
-  constexpr int NT = kKv8ScoreThreads, kLanes = HD / 4;   // lanes of a page, 8 bytes each
-  __shared__ int16_t s_w[2 * HD];                         // for lo: sums of the negative w; for hi: of the positive ones
-  __shared__ float s_top[NT / 32];
+  constexpr int NT = kKv8ScoreThreads, NW = NT / 32, kRun = 16, kRuns = 2 * HD / (8 * kRun);   // runs of 16 bounds of a lane: hd 128: one of lo, one of hi
+  __shared__ __align__(16) int16_t s_w[2 * HD];           // for lo: sums of the negative w; for hi: of the positive ones
+  __shared__ float s_top[NW];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t item = blockIdx.x / a.splits;
   const int split = int(blockIdx.x % a.splits), i = int(item / c.n_kv), g = int(item % c.n_kv);
@@ -52,6 +55,11 @@ __global__ void __launch_bounds__(kKv8ScoreThreads) k_kv8_scores(Kv4 c, Kv8Selec
   }
   const int m = (int64_t(e.y) + c.page_len - 1) / c.page_len;
   if (m <= a.k) return;
+  const int32_t* row = c.table + int64_t(e.x) * c.max_pages;
+  auto look = [&](int j0) { return lane < kKv8ScorePages && j0 + lane < m ? row[j0 + lane] : 0; };
+  const int step = a.splits * NW * kKv8ScorePages;
+  int j0 = (split * NW + warp) * kKv8ScorePages, page = j0 < m ? look(j0) : 0;
+  // ---- the weights of the group's queries
   const float* q = a.q + int64_t(i) * a.q_stride + int64_t(g) * a.G * HD;
   float top = 0.f;
   for (int x = t; x < a.G * HD; x += NT) {
@@ -63,7 +71,7 @@ __global__ void __launch_bounds__(kKv8ScoreThreads) k_kv8_scores(Kv4 c, Kv8Selec
   if (lane == 0) s_top[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < NT / 32; w++) top = fmaxf(top, s_top[w]);
+  for (int w = 0; w < NW; w++) top = fmaxf(top, s_top[w]);
   // 63 is 1.96875 2^5: f = exponent - 5, one more above 1.96875
   int f = 0;
   if (top > 0.f) {
@@ -84,50 +92,72 @@ __global__ void __launch_bounds__(kKv8ScoreThreads) k_kv8_scores(Kv4 c, Kv8Selec
     s_w[HD + t] = int16_t(pos);
   }
   __syncthreads();
-  const int sub = lane % kLanes;
-  int w[4];
+  const int sub = lane & 7, of = lane >> 3;               // this lane's part of page `of` of four
+  int w[kRuns][kRun / 2];
 #pragma unroll
-  for (int y = 0; y < 4; y++) w[y] = reinterpret_cast<const int*>(s_w)[4 * sub + y];
+  for (int r = 0; r < kRuns; r++)
+#pragma unroll
+    for (int y = 0; y < kRun / 2; y++) w[r][y] = reinterpret_cast<const int*>(s_w)[(r * 8 + sub) * (kRun / 2) + y];
   const Kv8Page L(c);
-  const uint8_t* pool = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes();
-  const int32_t* row = c.table + int64_t(e.x) * c.max_pages;
-  uint32_t* keys = a.keys + item * c.max_pages;
-  constexpr int kPer = 32 / kLanes;                       // pages of a warp at a time
-  const int step = a.splits * (NT / 32) * kPer;
-  for (int j0 = (split * (NT / 32) + warp) * kPer; j0 < m; j0 += step) {
-    const int j = j0 + lane / kLanes;
-    int page = j < m ? row[j] : -1, sum = 0, ex = 0;
-    if (page < 0 || page >= c.n_pages) {
-      if (j < m && sub == 0) kv4_flag(c, NT_KV4_BAD_PAGE);
-      page = -1;
-    }
-    if (page >= 0) {
-      const uint8_t* at = pool + page * c.page_bytes() + L.exps(g);
-      const uint2 b = *reinterpret_cast<const uint2*>(at + 16 + 8 * sub);
-      ex = *reinterpret_cast<const int8_t*>(at);
-      sum = __dp2a_lo(w[0], int(b.x), 0);
-      sum = __dp2a_hi(w[1], int(b.x), sum);
-      sum = __dp2a_lo(w[2], int(b.y), sum);
-      sum = __dp2a_hi(w[3], int(b.y), sum);
-    }
+  const uint8_t* heads = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes() + L.exps(g);
+  uint32_t* keys = a.keys + item * kv8_key_stride(c);
+  for (; j0 < m; j0 += step) {
+    const int next = j0 + step < m ? look(j0 + step) : 0;
+    const bool there = lane < kKv8ScorePages && j0 + lane < m, good = page >= 0 && page < c.n_pages;
+    if (there && !good) kv4_flag(c, NT_KV4_BAD_PAGE);
+    if (!good) page = -1;
+    uint4 b[kKv8ScorePages / 4][kRuns];
 #pragma unroll
-    for (int o = kLanes / 2; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (j < m && sub == 0) {
-      const uint32_t s = __float_as_uint(float(sum) * kv8_exp2i(ex));
-      const uint32_t key = s >> 31 ? ~s : s | 0x80000000u;
+    for (int y = 0; y < kKv8ScorePages / 4; y++) {
+      const int p = __shfl_sync(0xffffffffu, page, 4 * y + of);
+#pragma unroll
+      for (int r = 0; r < kRuns; r++) {
+        b[y][r] = make_uint4(0u, 0u, 0u, 0u);
+        if (p >= 0 && j0 + 4 * y + of < m) b[y][r] = *reinterpret_cast<const uint4*>(heads + p * c.page_bytes() + 16 + (r * 8 + sub) * kRun);
+      }
+    }
+    int ex = 0;
+    if (there && page >= 0) ex = *reinterpret_cast<const int8_t*>(heads + page * c.page_bytes());
+    int mine = 0;                                         // the sum of this lane's page
+#pragma unroll
+    for (int y = 0; y < kKv8ScorePages / 4; y++) {
+      int sum = 0;
+#pragma unroll
+      for (int r = 0; r < kRuns; r++) {
+        const uint32_t u[4] = {b[y][r].x, b[y][r].y, b[y][r].z, b[y][r].w};
+#pragma unroll
+        for (int z = 0; z < 4; z++) {
+          sum = __dp2a_lo(w[r][2 * z], int(u[z]), sum);
+          sum = __dp2a_hi(w[r][2 * z + 1], int(u[z]), sum);
+        }
+      }
+#pragma unroll
+      for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum = __shfl_sync(0xffffffffu, sum, 8 * (lane & 3));
+      if (lane >> 2 == y) mine = sum;
+    }
+    if (there) {
+      const int j = j0 + lane;
+      const uint32_t z = __float_as_uint(float(mine) * kv8_exp2i(ex)), key = z >> 31 ? ~z : z | 0x80000000u;
       keys[j] = j < a.first || j >= m - a.last ? 0xffffffffu : key;   // (no score has the key 0xffffffff)
     }
+    page = next;
   }
 }
 
-constexpr int kKv8PickThreads = 512;
+constexpr int kKv8PickThreads = 256;
+constexpr int kKv8PickBins = 1024;
 
-// The places of the a.k largest keys of (entry, kv head) blockIdx.x, the lower place
-// first among equals, ascending: the a.k-th largest key digit by digit from counts, then one pass
-// that writes what is above it and the first of those equal to it.
+// The places of the a.k largest keys of (entry, kv head) blockIdx.x, the lower place first among equals, ascending.  A thread has 16
+// keys, in its registers where there are no more than 4096.  The a.k-th largest is found by counting keys in 1024 bins of
+// equal width between the least and the largest, then in the bin where it lies, and so on; as soon as all keys of
+// that bin are wanted they and those above are the choice.  (Bins of the keys' upper bits, which few scores differ in, had all
+// threads count in the same few: 8.7 us for 2049 keys; candidates bit by bit with a count of all keys each: 12.5.)
 __global__ void __launch_bounds__(kKv8PickThreads) k_kv8_pick(Kv4 c, Kv8SelectArgs a) {
-  constexpr int NT = kKv8PickThreads;
-  __shared__ int s_count[256], s_part[2][NT / 32], s_digit, s_left;
+  constexpr int NT = kKv8PickThreads, NW = NT / 32, R = 16, kChunk = R * NT, kBins = kKv8PickBins, kOwn = kBins / NT;
+  __shared__ int s_bins[kBins];
+  __shared__ uint32_t s_part[3][NW];
+  __shared__ int s_bin, s_left, s_in;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t item = blockIdx.x;
   kv4_dependent();
@@ -139,68 +169,130 @@ __global__ void __launch_bounds__(kKv8PickThreads) k_kv8_pick(Kv4 c, Kv8SelectAr
     for (int j = t; j < a.k; j += NT) out[j] = j < m ? j : -1;
     return;
   }
-  const uint32_t* keys = a.keys + item * c.max_pages;
-  uint32_t prefix = 0u;
-  int left = a.k;                                        // of those whose upper digits are prefix's
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int x = t; x < 256; x += NT) s_count[x] = 0;
-    __syncthreads();
-    for (int j = t; j < m; j += NT) {
-      const uint32_t key = keys[j];
-      if (shift == 24 || (key ^ prefix) >> (shift + 8) == 0u) atomicAdd(&s_count[key >> shift & 255u], 1);
-    }
-    __syncthreads();
-    if (warp == 0) {                                     // lane x has digits 255 - 8 x and the 7 below
-      int mine = 0;
+  const uint32_t* keys = a.keys + item * kv8_key_stride(c);
+  constexpr uint32_t kAlways = 0xffffffffu;
+  uint32_t key[R];
+  auto get = [&](int j0) {                               // keys j0 + 16 t ..
 #pragma unroll
-      for (int y = 0; y < 8; y++) mine += s_count[255 - 8 * lane - y];
-      int upto = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int z = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += z;
-      }
-      int before = upto - mine;
-      if (before < left && upto >= left)
-        for (int y = 0; y < 8; y++) {
-          const int d = 255 - 8 * lane - y, n = s_count[d];
-          if (before < left && before + n >= left) {
-            s_digit = d;
-            s_left = left - before;
-          }
-          before += n;
-        }
+    for (int y = 0; y < R; y += 4) {
+      const int j = j0 + R * t + y;
+      const uint4 x = j < m ? *reinterpret_cast<const uint4*>(keys + j) : make_uint4(0u, 0u, 0u, 0u);
+      key[y] = x.x; key[y + 1] = x.y; key[y + 2] = x.z; key[y + 3] = x.w;
     }
-    __syncthreads();
-    prefix |= uint32_t(s_digit) << shift;
-    left = s_left;
-    __syncthreads();
+  };
+  auto each = [&](auto f) {                              // f(key) for all of this thread's
+    for (int j0 = 0; j0 < m; j0 += kChunk) {
+      if (m > kChunk) get(j0);
+#pragma unroll
+      for (int y = 0; y < R; y++)
+        if (j0 + R * t + y < m) f(key[y]);
+    }
+  };
+  get(0);
+  uint32_t least = kAlways, most = 0u, always = 0u;      // of the keys that are not always taken, and how many are
+  each([&](uint32_t x) {
+    if (x == kAlways) { always++; return; }
+    least = min(least, x);
+    most = max(most, x);
+  });
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  always = __reduce_add_sync(0xffffffffu, always);
+  if (lane == 0) { s_part[0][warp] = least; s_part[1][warp] = most; s_part[2][warp] = always; }
+  __syncthreads();
+  always = 0u;
+#pragma unroll
+  for (int w = 0; w < NW; w++) {
+    least = min(least, s_part[0][w]);
+    most = max(most, s_part[1][w]);
+    always += s_part[2][w];
   }
-  int above = 0, equal = 0;                              // of the places before this round's
-  for (int j0 = 0; j0 < m; j0 += NT) {
-    const int j = j0 + t;
-    const uint32_t key = j < m ? keys[j] : 0u;
-    const bool over = j < m && key > prefix, same = j < m && key == prefix;
-    const uint32_t mo = __ballot_sync(0xffffffffu, over), ms = __ballot_sync(0xffffffffu, same);
-    if (lane == 0) {
-      s_part[0][warp] = __popc(mo);
-      s_part[1][warp] = __popc(ms);
-    }
+  // keys from `base` on, 2^width of them, are looked at; those above are taken, `left` of these are
+  uint32_t base = least;
+  int width = 32 - __clz(most - least), left = a.k - int(always);
+  bool found = left == 0;                                // (m > a.k: there are others)
+  if (found) base = kAlways;
+  while (!found && width > 0) {
+    const int shift = width > 10 ? width - 10 : 0;
     __syncthreads();
-    int po = above, ps = equal, ao = 0, as = 0;
 #pragma unroll
-    for (int w = 0; w < NT / 32; w++) {
-      if (w < warp) { po += s_part[0][w]; ps += s_part[1][w]; }
-      ao += s_part[0][w];
-      as += s_part[1][w];
-    }
-    po += __popc(mo & ((1u << lane) - 1u));
-    ps += __popc(ms & ((1u << lane) - 1u));
-    if (over) out[po + (ps < left ? ps : left)] = j;
-    if (same && ps < left) out[po + ps] = j;
-    above += ao;
-    equal += as;
+    for (int y = 0; y < kOwn; y++) s_bins[kOwn * t + y] = 0;
     __syncthreads();
+    each([&](uint32_t x) {
+      const uint32_t bin = (x - base) >> shift;          // (keys below base wrap round to large numbers)
+      if (x >= base && bin < uint32_t(kBins) && x != kAlways) atomicAdd(&s_bins[kBins - 1 - bin], 1);   // the largest keys first
+    });
+    __syncthreads();
+    int n[kOwn], mine = 0;
+#pragma unroll
+    for (int y = 0; y < kOwn; y++) mine += n[y] = s_bins[kOwn * t + y];
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += z;
+    }
+    if (lane == 31) s_part[0][warp] = uint32_t(upto);
+    __syncthreads();
+    int before = upto - mine;
+#pragma unroll
+    for (int w = 0; w < NW; w++)
+      if (w < warp) before += int(s_part[0][w]);
+#pragma unroll
+    for (int y = 0; y < kOwn; y++) {
+      if (before < left && before + n[y] >= left) {
+        s_bin = kBins - 1 - (kOwn * t + y);
+        s_left = left - before;
+        s_in = n[y];
+      }
+      before += n[y];
+    }
+    __syncthreads();
+    base += uint32_t(s_bin) << shift;
+    width = shift;
+    left = s_left;
+    found = s_in == left;
+  }
+  const int ties = found ? m : left;                     // of those equal to base, how many are taken
+  int taken = 0, equal = 0;                              // of the places before this round's
+  for (int j0 = 0; j0 < m; j0 += kChunk) {
+    if (m > kChunk) get(j0);
+    int over = 0, same = 0;
+#pragma unroll
+    for (int y = 0; y < R; y++) {
+      const bool in = j0 + R * t + y < m;
+      over += in && key[y] > base;
+      same += in && key[y] == base;
+    }
+    int both = over | same << 16;                        // (4096 at most)
+    const int own = both;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, both, o);
+      if (lane >= o) both += z;
+    }
+    __syncthreads();
+    if (lane == 31) s_part[1][warp] = uint32_t(both);
+    __syncthreads();
+    int all = 0;
+    both -= own;
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+      if (w < warp) both += int(s_part[1][w]);
+      all += int(s_part[1][w]);
+    }
+    int po = taken + (both & 0xffff), ps = equal + (both >> 16);   // those above base, and equal to it, before this thread's
+#pragma unroll
+    for (int y = 0; y < R; y++) {
+      const int j = j0 + R * t + y;
+      if (j < m && key[y] > base) { out[po + min(ps, ties)] = j; po++; }
+      if (j < m && key[y] == base) {
+        if (ps < ties) out[po + ps] = j;
+        ps++;
+      }
+    }
+    taken += all & 0xffff;
+    equal += all >> 16;
   }
 }
 
@@ -244,7 +336,7 @@ extern "C" nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t
                         static_cast<uint32_t*>(dev_workspace), dev_pages};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (k.max_pages > n_select) {
-    const int64_t rounds = (k.max_pages + 8 * 4 - 1) / (8 * 4);       // four pages a warp
+    const int64_t per = kKv8ScoreThreads / 32 * kKv8ScorePages, rounds = (k.max_pages + per - 1) / per;
     const int64_t splits = 152 * 4 / items;
     a.splits = int32_t(splits < 1 ? 1 : (splits > rounds ? rounds : splits));
     const unsigned grid = unsigned(items * a.splits);
