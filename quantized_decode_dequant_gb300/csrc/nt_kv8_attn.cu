@@ -57,22 +57,25 @@ struct Kv8AttnCfg {
   static constexpr int kThreads = 192;                              // four warps of the softmax, one that copies, one that starts products
   static constexpr int kTerms = 6, kDigits = 8;
   static constexpr int NS = (kTerms * HB + 15) / 16 * 16, NP = kDigits * HB;
-  static constexpr int S = HD == 128 ? 2 : 4;                       // ring stages
-  static constexpr int kK = kKv8Tile * HD, kStage = 2 * kK + 8 * 16;   // K, V, the pages' exponents
+  // ring: a tile's K, then its V, a slot each, so that K's is free again with the scores; the pages' exponents and the number
+  // of positions in a ring of their own, by tile
+  static constexpr int H = HD == 128 ? (HB <= 4 ? 6 : HB == 8 ? 5 : 4) : (HB <= 8 ? 10 : 8), E = H / 2 + 1;
+  static constexpr int kSlot = kKv8Tile * HD;
   static constexpr int kPart = kv8_part_floats(HD, HB);
   // P^T: blocks of 8 rows (a head's digits) by 16 positions; 16 positions further 64 bytes beyond a multiple of 128, so that
   // a warp's two runs of 16 bytes fall on different banks
   static constexpr int kPStep = NP * 16 + 64;
   // shared memory (V's rows 64 to 127 with 64 dimensions, which nobody looks at, reach 1 KB behind it)
-  static constexpr int kQ = S * kStage;
+  static constexpr int kExps = H * kSlot;
+  static constexpr int kQ = kExps + E * 8 * 16;
   static constexpr int kP = kQ + NS * HD;
   static constexpr int kRed = kP + 8 * kPStep;                      // [4][HB] of the warps, twice: maxima, sums
   static constexpr int kPrefix = kRed + 8 * HB * 4;
   static constexpr int kEntry = kPrefix + (kKv8Batch + 4) * 4;
   static constexpr int kSums = kEntry + kKv8Batch * 8;
-  static constexpr int kInfo = kSums + 32;                          // [S]: positions of the tile (0: none, -1: it lacks a page)
-  static constexpr int kBars = (kInfo + 4 * S + 7) / 8 * 8;         // full [S], empty [S], scores, taken, weights, outputs
-  static constexpr int kTmem = kBars + 8 * (2 * S + 4);
+  static constexpr int kInfo = kSums + 32;                          // [E]: positions of the tile (0: none, -1: it lacks a page)
+  static constexpr int kBars = (kInfo + 4 * E + 7) / 8 * 8;         // full [H], empty [H], scores, taken, weights, outputs
+  static constexpr int kTmem = kBars + 8 * (2 * H + 4);
   static constexpr int kSegs = kTmem + 4;                           // items whose q is there
   static constexpr int kSmem = kTmem + 16;
   static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
@@ -165,7 +168,7 @@ struct Kv8At {
 template <int HD, int HB>
 __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv4 c, Kv8AttnArgs a) {
   using Cfg = Kv8AttnCfg<HD, HB>;
-  constexpr int S = Cfg::S, NT = Cfg::kThreads;
+  constexpr int H = Cfg::H, E = Cfg::E, NT = Cfg::kThreads;
   extern __shared__ __align__(128) uint8_t kv8_sm[];
   uint8_t* sm = kv8_sm;
   const uint32_t smu = kv4_smem(sm);
@@ -174,14 +177,14 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   volatile int* info = reinterpret_cast<volatile int*>(sm + Cfg::kInfo);
   volatile int* segs_ready = reinterpret_cast<volatile int*>(sm + Cfg::kSegs);
   const volatile uint32_t* tensor_memory = reinterpret_cast<const volatile uint32_t*>(sm + Cfg::kTmem);
-  const uint32_t full = smu + Cfg::kBars, empty = full + 8 * S, bar_s = empty + 8 * S, bar_taken = bar_s + 8,
+  const uint32_t full = smu + Cfg::kBars, empty = full + 8 * H, bar_s = empty + 8 * H, bar_taken = bar_s + 8,
                  bar_p = bar_taken + 8, bar_o = bar_p + 8;
   const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31, n = a.n, P = c.page_len;
 
   if (t == 0) {
-    for (int i = 0; i < S; i++) {
+    for (int i = 0; i < H; i++) {
       kv4_bar_init(full + 8 * i);
-      kv4_bar_init(empty + 8 * i, 5);
+      kv4_bar_init(empty + 8 * i);
     }
     kv4_bar_init(bar_s);
     kv4_bar_init(bar_taken, 4);
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     const Kv8Page L(c);
     const uint8_t* layer_pool = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes();
     const int per = kKv8Tile / P, codes = P * HD;
-    int no = 0;
+    int no = 0, begun = 0;                             // tiles; slots filled
     bool dead = false;
     for (int x = c0; x < c1 && !dead;) {
       Kv8At at;
@@ -305,36 +308,40 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           last = next_last;
           next = look(first + 32 + lane, &next_last);
         }
-        const int st = no % S, y = at_list - first + lane % 8;
+        const int y = at_list - first + lane % 8;
         const int mine = __shfl_sync(0xffffffffu, page, y & 31);
         const bool is_last = __shfl_sync(0xffffffffu, int(last), y & 31);
         const bool live = lane % 8 < per && mine >= 0;
         const bool lacks = __any_sync(0xffffffffu, lane < per && mine == -1);
         const int have = __popc(__ballot_sync(0xffffffffu, lane < 8 && live));
         const bool ends = __any_sync(0xffffffffu, live && is_last);
-        if (no >= S && !__all_sync(0xffffffffu, kv4_bar_wait(empty + 8 * st, uint32_t(no / S - 1) & 1u))) { dead = true; break; }
-        const uint32_t bar = full + 8 * st;
-        __syncwarp();
-        if (lane == 0) {
-          info[st] = lacks ? -1 : have * P - (ends ? m * P - len : 0);
-          if (lacks || !have) kv4_bar_arrive(bar);
-          else kv4_bar_expect(bar, uint32_t(have) * uint32_t(2 * codes + 16));
+        const bool nothing = lacks || !have;
+        const uint8_t* from = layer_pool + (live ? mine : 0) * c.page_bytes();
+#pragma unroll
+        for (int v = 0; v < 2; v++) {                  // K, V
+          const int fill = 2 * no + v, slot = fill % H;
+          if (fill >= H && !__all_sync(0xffffffffu, kv4_bar_wait(empty + 8 * slot, uint32_t(fill / H - 1) & 1u))) { dead = true; break; }
+          const uint32_t bar = full + 8 * slot;
+          if (lane == 0) {
+            if (v == 0) info[no % E] = lacks ? -1 : have * P - (ends ? m * P - len : 0);
+            if (nothing) kv4_bar_arrive(bar);
+            else kv4_bar_expect(bar, uint32_t(have) * uint32_t(codes + (v ? 0 : 16)));
+          }
+          __syncwarp();
+          if (!nothing && live && lane < (v ? 8 : 16)) {
+            const int z = lane % 8;
+            if (lane < 8) kv4_copy(smu + slot * Cfg::kSlot + z * codes, from + (v ? L.v(at.g) : L.k(at.g)), codes, bar);
+            else kv4_copy(smu + Cfg::kExps + (no % E * 8 + z) * 16, from + L.exps(at.g), 16, bar);
+          }
+          begun = fill + 1;
         }
-        __syncwarp();
-        if (!lacks && live && lane < 24) {
-          const uint8_t* from = layer_pool + mine * c.page_bytes();
-          const uint32_t to = smu + st * Cfg::kStage;
-          const int z = lane % 8;
-          if (lane < 8) kv4_copy(to + z * codes, from + L.k(at.g), codes, bar);
-          else if (lane < 16) kv4_copy(to + Cfg::kK + z * codes, from + L.v(at.g), codes, bar);
-          else kv4_copy(to + 2 * Cfg::kK + z * 16, from + L.exps(at.g), 16, bar);
-        }
+        if (dead) break;
       }
       x += count;
     }
     if (dead) {   // copies in flight land before the shared memory is given up
       if (lane == 0) kv4_flag(c, NT_KV4_TIMEOUT);
-      for (int i = no < S ? 0 : no - S; i < no; i++) kv4_bar_wait(full + 8 * (i % S), uint32_t(i / S) & 1u);
+      for (int i = begun < H ? 0 : begun - H; i < begun; i++) kv4_bar_wait(full + 8 * (i % H), uint32_t(i / H) & 1u);
     }
   } else if (warp == 5) {
     // ---- products: scores of tile ns as soon as it and q are there and the scores before are taken, outputs of
@@ -342,11 +349,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     constexpr uint32_t kIdesc = 1u << 4 | uint32_t(kKv8Tile / 16) << 24;   // fp32 += e4m3 e4m3, 128 rows
     constexpr uint32_t kIdescS = kIdesc | uint32_t(Cfg::NS / 8) << 17, kIdescO = kIdesc | uint32_t(Cfg::NP / 8) << 17;
     const int all = c1 - c0;
-    int ns = 0, np = 0, scored = 0, weighed = 0, segs = 0, left = 0, idle = 0;   // left: tiles of the segment without scores
+    int ns = 0, np = 0, weighed = 0, segs = 0, left = 0, idle = 0;   // left: tiles of the segment without scores
     while (np < all) {
       bool moved = false;
-      if (ns < all && ns - np < S) {
-        const int st = ns % S;
+      if (ns < all && ns - np < E - 1) {
+        const int slot = 2 * ns % H;
         bool ok = true;
         if (left == 0) {
           ok = __all_sync(0xffffffffu, *segs_ready > segs);   // (a count: items without a live tile may pass several at a time)
@@ -357,50 +364,53 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             segs++;
           }
         }
-        if (ok && kv8_bar_test(full + 8 * st, uint32_t(ns / S) & 1u)) {
-          if (info[st] <= 0) {
-            ns++;
-            left--;
-            moved = true;
-          } else if (scored == 0 || kv8_bar_test(bar_taken, uint32_t(scored - 1) & 1u)) {
+        if (ok && kv8_bar_test(full + 8 * slot, uint32_t(2 * ns / H) & 1u) && (ns == 0 || kv8_bar_test(bar_taken, uint32_t(ns - 1) & 1u))) {
+          if (info[ns % E] > 0) {
             kv8_tc_after();
             if (kv8_elect()) {
-              const uint32_t k0 = smu + st * Cfg::kStage, q0 = smu + Cfg::kQ;
+              const uint32_t k0 = smu + slot * Cfg::kSlot, q0 = smu + Cfg::kQ;
 #pragma unroll
               for (int kk = 0; kk < HD / 32; kk++)
                 kv8_mma(tmem + Cfg::kColS, kv8_desc(k0 + kk * 256, 128, 8 * HD), kv8_desc(q0 + kk * 256, 128, 8 * HD), kIdescS, kk > 0);
               kv8_commit(bar_s);
+              kv8_commit(empty + 8 * slot);
             }
-            __syncwarp();
-            scored++;
-            ns++;
-            left--;
-            moved = true;
+          } else if (lane == 0) {                      // nothing to multiply: the tile goes the same way
+            kv4_bar_arrive(bar_s);
+            kv4_bar_arrive(empty + 8 * slot);
           }
+          __syncwarp();
+          ns++;
+          left--;
+          moved = true;
         }
       }
       if (np < ns) {
-        const int st = np % S;
-        if (info[st] <= 0) {
-          if (lane == 0) kv4_bar_arrive(empty + 8 * st);
-          __syncwarp();
-          np++;
-          moved = true;
-        } else if (kv8_bar_test(bar_p, uint32_t(weighed) & 1u)) {
-          kv8_tc_after();
-          if (kv8_elect()) {
-            const uint32_t v0 = smu + st * Cfg::kStage + Cfg::kK, p0 = smu + Cfg::kP;
+        const int fill = 2 * np + 1, slot = fill % H;
+        if (kv8_bar_test(full + 8 * slot, uint32_t(fill / H) & 1u)) {
+          if (info[np % E] <= 0) {                     // free once the softmax warps have seen that there is nothing
+            if (ns > np + 1 || kv8_bar_test(bar_taken, uint32_t(np) & 1u)) {
+              if (lane == 0) kv4_bar_arrive(empty + 8 * slot);
+              __syncwarp();
+              np++;
+              moved = true;
+            }
+          } else if (kv8_bar_test(bar_p, uint32_t(weighed) & 1u)) {
+            kv8_tc_after();
+            if (kv8_elect()) {
+              const uint32_t v0 = smu + slot * Cfg::kSlot, p0 = smu + Cfg::kP;
 #pragma unroll
-            for (int kk = 0; kk < kKv8Tile / 32; kk++)
-              kv8_mma(tmem + Cfg::kColO, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
-                      kv8_desc(p0 + kk * 2 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
-            kv8_commit(bar_o);
-            kv8_commit(empty + 8 * st);
+              for (int kk = 0; kk < kKv8Tile / 32; kk++)
+                kv8_mma(tmem + Cfg::kColO, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
+                        kv8_desc(p0 + kk * 2 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
+              kv8_commit(bar_o);
+              kv8_commit(empty + 8 * slot);
+            }
+            __syncwarp();
+            weighed++;
+            np++;
+            moved = true;
           }
-          __syncwarp();
-          weighed++;
-          np++;
-          moved = true;
         }
       }
       idle = moved ? 0 : idle + 1;
@@ -508,24 +518,28 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
 #pragma unroll 1
       for (int i = 0; i < count; i++, no++) {
         if (dead) continue;
-        const int st = no % S;
-        bool fail = !__all_sync(0xffffffffu, kv4_bar_wait(full + 8 * st, uint32_t(no / S) & 1u));
-        const int live = info[st];
+        // (not K's own barrier: its slot may have been filled again by now)
+        bool fail = !__all_sync(0xffffffffu, kv4_bar_wait(bar_s, ps));
+        ps ^= 1u;
+        const int live = info[no % E];
         if (live <= 0 || fail) {
           if (kv8_any(fail)) dead = kv8_any(fail);     // (as many barriers as a tile with scores has)
           poison = poison || dead || live < 0;
           __syncwarp();
-          if (lane == 0) kv4_bar_arrive(empty + 8 * st);
+          if (lane == 0) kv4_bar_arrive(bar_taken);
           continue;
         }
-        const int8_t* exps = reinterpret_cast<const int8_t*>(sm + st * Cfg::kStage + 2 * Cfg::kK);
+        kv8_tc_after();
+        const int8_t* exps = reinterpret_cast<const int8_t*>(sm + Cfg::kExps + no % E * 8 * 16);
         int vmax = -128;
         for (int y = 0; y * P < live; y++) vmax = max(vmax, int(exps[16 * y + 1]));
         const bool here = t < live;
         const int page = here ? t / P : 0, dv = 28 + exps[16 * page + 1] - vmax;
         const float fk = kv8_exp2i(exps[16 * page]), fv = dv < -126 ? 0.f : kv8_exp2i(dv);
         if (live < kKv8Tile) {   // values behind the end: zeros, whatever the page holds there
-          uint8_t* v = sm + st * Cfg::kStage + Cfg::kK;
+          const int vfill = 2 * no + 1;
+          fail = !__all_sync(0xffffffffu, kv4_bar_wait(full + 8 * (vfill % H), uint32_t(vfill / H) & 1u)) || fail;
+          uint8_t* v = sm + vfill % H * Cfg::kSlot;
           if (t < HD)
             for (int ch = live >> 4; ch < 8; ch++) {
               uint4* at16 = reinterpret_cast<uint4*>(v + kv8_v_at(HD, ch, t));
@@ -540,9 +554,6 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             }
         }
         // ---- scores
-        fail = !__all_sync(0xffffffffu, kv4_bar_wait(bar_s, ps)) || fail;
-        ps ^= 1u;
-        kv8_tc_after();
         float s[HB];
         {
           constexpr int kCols = HB == 16 ? 48 : Cfg::NS;   // three terms at a time with 16 heads, all otherwise
@@ -618,10 +629,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         kv8_tc_before();
         __syncwarp();
-        if (lane == 0) {
-          kv4_bar_arrive(bar_p);
-          kv4_bar_arrive(empty + 8 * st);
-        }
+        if (lane == 0) kv4_bar_arrive(bar_p);
         out_scale = kv8_exp2i(vmax - 19);              // digits are 2^-9 of themselves, weights 2^28
         pending = true;
       }
