@@ -17,8 +17,9 @@
 // 2^3.9.  log2(e) / sqrt(hd) is multiplied into q, so that what brings a score to the exponent is a power of two
 // and the maximum and the weights see the same number however large it is.
 //
-// The tiles of all items in a row go evenly to the CTAs, two per SM; an item that is cut leaves
-// partial results for a second launch.  In a CTA one warp copies, one starts products, four have a
+// Two forms, chosen on the host (kv8_launch_attn).  Where there are few items of a small capacity, a thread-block cluster per
+// item, whose CTAs share out its tiles and merge their partial results through distributed shared memory.  Else the tiles of all
+// items in a row go evenly to the CTAs, two per SM; an item that is cut leaves partial results for a second launch.  In a CTA one warp copies, one starts products, four have a
 // position (then a dimension) per thread.
 #include "nt_kv8.cuh"
 
@@ -27,6 +28,7 @@ namespace nt {
 constexpr int kKv8Batch = 512;          // entries of a launch: their first tiles are kept in shared memory
 constexpr int kKv8MaxCtas = 304;        // two per SM; the workspace holds two partial results of each
 constexpr int kKv8Tile = 128;
+constexpr int kKv8MaxCluster = 16;
 
 struct Kv8AttnArgs {
   int32_t layer, n, G, k;
@@ -39,17 +41,17 @@ struct Kv8AttnArgs {
   float* out;
   int64_t out_stride;
   float scale;                          // log2(e) / sqrt(hd)
-  float* part;                          // [CTA][2] partial results
+  float* part;                          // [CTA][2] partial results: of an item begun before this CTA, of one that goes on behind it
+  int2* open;                           // [CTA]: the latter's item (-1: none) and the number of CTAs that work on it
 };
 
-// Partial result of one item: o [HB][HD], then (reference m, sum l) per head, then a header of 4 words (used by a
-// CTA's second: the item, -1 none, and the number of CTAs that worked on it).
-constexpr int kv8_part_floats(int hd, int hb) { return hb * hd + 2 * hb + 4; }
+// Partial result of one item: o [HB][HD], then (reference m, sum l) per head.
+constexpr int kv8_part_floats(int hd, int hb) { return hb * hd + 2 * hb; }
 constexpr int kv8_heads_block(int g) { return g <= 2 ? 2 : g <= 4 ? 4 : g <= 8 ? 8 : 16; }
 
 size_t kv8_attn_ws_bytes(int n_heads, int n_kv, int hd) {
   const int g = n_heads / n_kv;
-  return size_t(kKv8MaxCtas) * 2 * kv8_part_floats(hd, kv8_heads_block(g < kKv8MaxGroup ? g : kKv8MaxGroup)) * 4;
+  return size_t(kKv8MaxCtas) * (2 * kv8_part_floats(hd, kv8_heads_block(g < kKv8MaxGroup ? g : kKv8MaxGroup)) * 4 + 8);
 }
 
 template <int HD, int HB>
@@ -62,6 +64,7 @@ struct Kv8AttnCfg {
   static constexpr int H = HD == 128 ? (HB <= 4 ? 6 : HB == 8 ? 5 : 4) : (HB <= 8 ? 10 : 8), E = H / 2 + 1;
   static constexpr int kSlot = kKv8Tile * HD;
   static constexpr int kPart = kv8_part_floats(HD, HB);
+  static_assert(kPart * 4 <= H * kSlot, "a partial result fits the ring");
   // P^T: blocks of 8 rows (a head's digits) by 16 positions; 16 positions further 64 bytes beyond a multiple of 128, so that
   // a warp's two runs of 16 bytes fall on different banks
   static constexpr int kPStep = NP * 16 + 64;
@@ -165,7 +168,8 @@ struct Kv8At {
 
 // ------------------------------------------------------------ the kernel --
 
-template <int HD, int HB>
+// CL: block (rank, item) of a cluster per item.
+template <int HD, int HB, bool CL>
 __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv4 c, Kv8AttnArgs a) {
   using Cfg = Kv8AttnCfg<HD, HB>;
   constexpr int H = Cfg::H, E = Cfg::E, NT = Cfg::kThreads;
@@ -207,7 +211,15 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     if (a.k && x > a.k) x = a.k;
     return a.k ? int((x * P + kKv8Tile - 1) / kKv8Tile) : int((int64_t(len) + kKv8Tile - 1) / kKv8Tile);
   };
-  {
+  int2 only = make_int2(-1, 0);                        // CL: the item's entry
+  if (CL) {
+    uint32_t bad;
+    only = kv8_attn_entry(c, a, int(blockIdx.y) / c.n_kv, &bad);
+    if (bad && blockIdx.x == 0 && t == 0) kv4_flag(c, bad);
+    kv8_tc_before();
+    __syncthreads();
+    kv8_tc_after();
+  } else {
     int* sums = reinterpret_cast<int*>(sm + Cfg::kSums);
     int run = 0;
     for (int e0 = 0; e0 < n; e0 += NT) {
@@ -246,14 +258,18 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   }
   const uint32_t tmem = *tensor_memory;
   asm volatile("griddepcontrol.launch_dependents;");
-  const int total = prefix[n];
+  auto seen = [&](int e) { return CL ? only : entry[e]; };
+  const int total = CL ? tiles(only.y) : prefix[n];
   int share = (total + int(gridDim.x) - 1) / int(gridDim.x);
   if (share < 1) share = 1;
   const int c0 = int(blockIdx.x) * share < total ? int(blockIdx.x) * share : total, c1 = c0 + share < total ? c0 + share : total;
   float* part0 = a.part + int64_t(blockIdx.x) * 2 * Cfg::kPart;
-  int* header = reinterpret_cast<int*>(part0 + 2 * Cfg::kPart - 4);
 
   auto locate = [&](int x, Kv8At& at) {
+    if (CL) {
+      at = Kv8At{int(blockIdx.y) / c.n_kv, int(blockIdx.y) % c.n_kv, x, total};
+      return;
+    }
     int lo = 0, hi = n;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -277,9 +293,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     for (int x = c0; x < c1 && !dead;) {
       Kv8At at;
       locate(x, at);
-      const int count = segment(x, at), len = entry[at.e].y;
+      const int count = segment(x, at), len = seen(at.e).y;
       const int m = int((int64_t(len) + P - 1) / P), listed = a.k && a.k < m ? a.k : m;
-      const int32_t* row = c.table + int64_t(entry[at.e].x) * c.max_pages;
+      const int32_t* row = c.table + int64_t(seen(at.e).x) * c.max_pages;
       const int32_t* list = a.k ? a.pages + (int64_t(at.e) * c.n_kv + at.g) * a.k : nullptr;
       const int end = (at.ti + count) * per < listed ? (at.ti + count) * per : listed;
       // the page at place i of the list; -1: none there, -2: the list has ended; *last: it is the sequence's last page
@@ -643,8 +659,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         if (lane == 0) sums[warp * HB + h] = l[h];
       }
       poison = kv8_any(poison);
-      const bool whole = at.ti == 0 && count == at.nt, begun = at.ti == 0;
-      float* to = whole ? a.out + int64_t(at.e) * a.out_stride + int64_t(at.g) * a.G * HD : part0 + (begun ? Cfg::kPart : 0);
+      const bool whole = !CL && at.ti == 0 && count == at.nt, begun = at.ti == 0;
+      float* to = CL ? reinterpret_cast<float*>(sm) : whole ? a.out + int64_t(at.e) * a.out_stride + int64_t(at.g) * a.G * HD : part0 + (begun ? Cfg::kPart : 0);
 #pragma unroll
       for (int h = 0; h < HB; h++) {
         float sum = (sums[h] + sums[HB + h]) + (sums[2 * HB + h] + sums[3 * HB + h]);
@@ -652,94 +668,232 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         if (t < HD && h < a.G) to[h * HD + t] = whole ? (sum == 0.f ? 0.f : O[h] / sum) : O[h];
         if (!whole && t == 0) reinterpret_cast<float2*>(to + HB * HD)[h] = make_float2(mref[h], sum);
       }
-      if (begun && !whole && t == 0) {
-        const int units0 = x;                          // the item's first tile
-        header[1] = (units0 + at.nt - 1) / share - int(blockIdx.x) + 1;
-        header[0] = at.e * c.n_kv + at.g;
-      }
       x += count;
-      if (x >= c1 && t == 0 && (whole || !begun)) header[0] = -1;   // nothing is left open here
+      // the CTA's last item is open where it was begun here and goes on behind
+      if (!CL && x >= c1 && t == 0)
+        a.open[blockIdx.x] = begun && !whole ? make_int2(at.e * c.n_kv + at.g, (x - count + at.nt - 1) / share - int(blockIdx.x) + 1) : make_int2(-1, 0);
       kv8_any(false);                                  // the sums are read
     }
-    if (c0 >= c1 && t == 0) header[0] = -1;
-    // entries without a position: zeros, or NaN where they cannot be read
-    for (int e = blockIdx.x; e < n; e += gridDim.x)
-      if (entry[e].y == 0)
-        for (int y = t; y < c.n_kv * a.G * HD; y += 128) a.out[int64_t(e) * a.out_stride + y] = entry[e].x < 0 ? NAN : 0.f;
+    if (!CL) {
+      if (c0 >= c1 && t == 0) a.open[blockIdx.x] = make_int2(-1, 0);
+      // entries without a position: zeros, or NaN where they cannot be read
+      for (int e = blockIdx.x; e < n; e += gridDim.x)
+        if (entry[e].y == 0)
+          for (int y = t; y < c.n_kv * a.G * HD; y += 128) a.out[int64_t(e) * a.out_stride + y] = entry[e].x < 0 ? NAN : 0.f;
+    } else if (c0 >= c1) {                             // no tile of this CTA's
+      float* to = reinterpret_cast<float*>(sm);
+      for (int y = t; y < HB * HD; y += 128) to[y] = 0.f;
+      if (t < HB) reinterpret_cast<float2*>(to + HB * HD)[t] = make_float2(-3e38f, 0.f);
+    }
   }
   kv8_tc_before();
-  __syncthreads();
+  if (CL) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  else __syncthreads();
   if (warp == 5) {
     kv8_tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Cfg::kCols));
   }
+  if (CL) {
+    // ---- the item's partial results, each CTA a share of the outputs, in the ranks' order
+    const int ranks = int(gridDim.x), outs = a.G * HD;
+    float* out = a.out + int64_t(int(blockIdx.y) / c.n_kv) * a.out_stride + int64_t(int(blockIdx.y) % c.n_kv) * outs;
+    auto there = [&](int r, uint32_t at) {             // shared memory of rank r
+      uint32_t y;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(smu + at), "r"(r));
+      return y;
+    };
+    auto load = [](uint32_t at) {
+      float y;
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(y) : "r"(at));
+      return y;
+    };
+    for (int i = int(blockIdx.x) * NT + t; i < outs; i += ranks * NT) {
+      const int h = i / HD;
+      float m[kKv8MaxCluster], l[kKv8MaxCluster], o[kKv8MaxCluster], top = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < kKv8MaxCluster; r++) {
+        if (r >= ranks) break;
+        m[r] = load(there(r, (HB * HD + 2 * h) * 4));
+        l[r] = load(there(r, (HB * HD + 2 * h + 1) * 4));
+        o[r] = load(there(r, i * 4));
+      }
+#pragma unroll
+      for (int r = 0; r < kKv8MaxCluster; r++)
+        if (r < ranks) top = fmaxf(top, m[r]);
+      float sum = 0.f, y = 0.f;
+#pragma unroll
+      for (int r = 0; r < kKv8MaxCluster; r++)
+        if (r < ranks) {
+          const float f = kv8_ex2(m[r] - top);
+          sum = fmaf(l[r], f, sum);
+          y = fmaf(o[r], f, y);
+        }
+      out[i] = only.x < 0 ? NAN : sum == 0.f ? 0.f : y / sum;
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");   // all have read this CTA's
+  }
 }
 
-// Items that were cut: block (CTA, head) merges what the CTA blockIdx.x began with what the next ones left, in their order.
-constexpr int kKv8MergeWarps = 4;
+// Items that were cut: block (y, head) merges what CTA c began, the y-th of those that left an item open, with what the next ones left, in
+// their order.
+constexpr int kKv8MergeWarps = 8;
 template <int HD>
-__global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8AttnArgs a, int part_floats, int rows) {
-  constexpr int V = HD / 32, NW = kKv8MergeWarps;
+__global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8AttnArgs a, int ctas, int part_floats, int rows) {
+  constexpr int V = HD / 32, NW = kKv8MergeWarps, NT = 32 * NW, kFew = 5;   // partial results of a warp on the way together
   __shared__ float s_o[NW][HD];
   __shared__ float2 s_ml[NW];
+  __shared__ int s_count[NW];
+  __shared__ int s_cta, s_item, s_members;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, h = blockIdx.y;
+  if (t == 0) s_cta = -1;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const float* first = a.part + (int64_t(blockIdx.x) * 2 + 1) * part_floats;   // the second of this CTA, then the first of the next ones
-  const int2 header = __ldcg(reinterpret_cast<const int2*>(first + part_floats - 4));
-  if (header.x < 0) return;
+  if (int(gridDim.x) >= ctas - 1) {   // as many blocks as CTAs: no need to count
+    const int2 x = __ldcg(a.open + blockIdx.x);
+    if (x.x < 0) return;
+    if (t == 0) { s_cta = int(blockIdx.x); s_item = x.x; s_members = x.y; }
+    __syncthreads();
+  }
+  int before = 0;
+  for (int i0 = int(gridDim.x) >= ctas - 1 ? ctas : 0; i0 < ctas; i0 += NT) {
+    const int2 x = i0 + t < ctas ? __ldcg(a.open + i0 + t) : make_int2(-1, 0);
+    const uint32_t m = __ballot_sync(0xffffffffu, x.x >= 0);
+    if (lane == 0) s_count[warp] = __popc(m);
+    __syncthreads();
+    int mine = before;
+#pragma unroll
+    for (int w = 0; w < NW; w++) {
+      if (w < warp) mine += s_count[w];
+      before += s_count[w];
+    }
+    if (x.x >= 0 && mine + __popc(m & ((1u << lane) - 1u)) == int(blockIdx.x)) {
+      s_cta = i0 + t;
+      s_item = x.x;
+      s_members = x.y;
+    }
+    __syncthreads();
+  }
+  if (s_cta < 0) return;
+  const int members = s_members;
+  const float* first = a.part + (int64_t(s_cta) * 2 + 1) * part_floats;   // the second of this CTA, then the first of the next ones
   float M = -INFINITY, sum = 0.f, o[V];
 #pragma unroll
   for (int v = 0; v < V; v++) o[v] = 0.f;
-  for (int b = warp; b < header.y; b += NW) {
-    const float* r = b ? first + (int64_t(b) * 2 - 1) * part_floats : first;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(r + rows * HD) + h);
-    const float to = fmaxf(M, ml.x), was = kv8_ex2(M - to), f = kv8_ex2(ml.x - to);
-    M = to;
-    sum = fmaf(sum, was, ml.y * f);
+  for (int b0 = warp; b0 < members; b0 += kFew * NW) {
+    float2 ml[kFew];
+    float x[kFew][V];
 #pragma unroll
-    for (int v = 0; v < V; v++) o[v] = fmaf(o[v], was, __ldcg(r + h * HD + 32 * v + lane) * f);
+    for (int u = 0; u < kFew; u++) {
+      const int b = b0 + u * NW;
+      if (b >= members) break;
+      const float* r = b ? first + (int64_t(b) * 2 - 1) * part_floats : first;
+      ml[u] = __ldcg(reinterpret_cast<const float2*>(r + rows * HD) + h);
+#pragma unroll
+      for (int v = 0; v < V; v++) x[u][v] = __ldcg(r + h * HD + 32 * v + lane);
+    }
+#pragma unroll
+    for (int u = 0; u < kFew; u++) {
+      if (b0 + u * NW >= members) break;
+      const float to = fmaxf(M, ml[u].x), was = kv8_ex2(M - to), f = kv8_ex2(ml[u].x - to);
+      M = to;
+      sum = fmaf(sum, was, ml[u].y * f);
+#pragma unroll
+      for (int v = 0; v < V; v++) o[v] = fmaf(o[v], was, x[u][v] * f);
+    }
   }
 #pragma unroll
   for (int v = 0; v < V; v++) s_o[warp][32 * v + lane] = o[v];
   if (lane == 0) s_ml[warp] = make_float2(M, sum);
   __syncthreads();
-  float top = -INFINITY;
+  if (t < HD) {
+    float top = -INFINITY, total = 0.f, y = 0.f;
 #pragma unroll
-  for (int w = 0; w < NW; w++) top = fmaxf(top, s_ml[w].x);
-  for (int d = t; d < HD; d += 32 * NW) {
-    float total = 0.f, y = 0.f;
+    for (int w = 0; w < NW; w++) top = fmaxf(top, s_ml[w].x);
 #pragma unroll
     for (int w = 0; w < NW; w++) {
       const float f = kv8_ex2(s_ml[w].x - top);
       total = fmaf(s_ml[w].y, f, total);
-      y = fmaf(s_o[w][d], f, y);
+      y = fmaf(s_o[w][t], f, y);
     }
-    const int e = header.x / c.n_kv, g = header.x % c.n_kv;
-    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + d] = total == 0.f ? 0.f : y / total;
+    const int e = s_item / c.n_kv, g = s_item % c.n_kv;
+    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + t] = total == 0.f ? 0.f : y / total;
   }
 }
 
+// CTAs of a cluster, and how many such clusters of the attention kernel the GPU holds at once (0: none).
+constexpr int kKv8Clusters[8] = {1, 2, 3, 4, 6, 8, 12, 16};
+struct Kv8Fit {
+  KernelSetup setup;
+  int clusters[8] = {};
+};
+static void kv8_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster) {
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg = cudaLaunchConfig_t{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+}
 template <int HD, int HB>
-static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t most_tiles, cudaStream_t s) {
+static Kv8Fit kv8_fit() {
   using Cfg = Kv8AttnCfg<HD, HB>;
-  static const KernelSetup setup = kernel_setup(k_kv8_attn<HD, HB>, Cfg::kSmem);
+  Kv8Fit f;
+  f.setup = kernel_setup(k_kv8_attn<HD, HB, true>, Cfg::kSmem);
+  if (f.setup.err == cudaSuccess) f.setup.err = cudaFuncSetAttribute(k_kv8_attn<HD, HB, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  for (int i = 0; i < 8 && f.setup.err == cudaSuccess; i++) {
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[2];
+    kv8_config(cfg, attr, dim3(unsigned(kKv8Clusters[i])), Cfg::kThreads, Cfg::kSmem, nullptr, kKv8Clusters[i]);
+    cfg.numAttrs = 1;
+    attr[0] = attr[1];
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_kv8_attn<HD, HB, true>, &cfg) == cudaSuccess) f.clusters[i] = n;
+    else cudaGetLastError();   // (no such cluster: it is not taken)
+  }
+  return f;
+}
+
+// Most tiles of a CTA in the form with a cluster per item, for up to 8 and for 16 query heads.  (us, that form and the other: 1
+// sequence of 600 positions, 64/8 heads: 6.5, 8.5; of 4161, 3 tiles a CTA: 8.9, 11.1; of 8000, 4: 11.8, 15.5; of 12000, 6: 14.0, 16.7; of 16000,
+// 8: 18.3, 18.3; 16 of 300, 32/8: 8.2, 13.6; 1 of 9000, 16/1, 5 tiles a CTA: 14.9, 12.3.)
+constexpr int kKv8ClusterShare[2] = {6, 3};
+
+template <int HD, int HB>
+static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t item_tiles, cudaStream_t s) {
+  using Cfg = Kv8AttnCfg<HD, HB>;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr[2];
+  const int64_t items = int64_t(a.n) * k.n_kv;
+  // A cluster per item where all of them fit the GPU at once and their capacity leaves no CTA more than kKv8ClusterShare tiles: the smallest
+  // cluster such that a CTA has one tile at most, or the largest.
+  static const Kv8Fit fit = kv8_fit<HD, HB>();
+  if (fit.setup.err != cudaSuccess) return fit.setup.err;
+  int cluster = 0;
+  for (int i = 0; i < 8; i++) {
+    if (fit.clusters[i] < items || item_tiles > int64_t(kKv8Clusters[i]) * kKv8ClusterShare[HB == 16]) continue;
+    cluster = kKv8Clusters[i];
+    if (item_tiles <= cluster) break;
+  }
+  if (cluster) {
+    kv8_config(cfg, attr, dim3(unsigned(cluster), unsigned(items)), Cfg::kThreads, Cfg::kSmem, s, cluster);
+    return cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, true>, k, a);
+  }
+  static const KernelSetup setup = kernel_setup(k_kv8_attn<HD, HB, false>, Cfg::kSmem);
   if (setup.err != cudaSuccess) return setup.err;
   int64_t ctas = 2 * setup.sms < kKv8MaxCtas ? 2 * setup.sms : kKv8MaxCtas;
-  if (ctas > most_tiles) ctas = most_tiles;
-  cudaError_t e = kv4_launch_smem(k_kv8_attn<HD, HB>, unsigned(ctas), unsigned(Cfg::kThreads), size_t(Cfg::kSmem), s, k, a);
+  if (ctas > items * item_tiles) ctas = items * item_tiles;
+  kv8_config(cfg, attr, dim3(unsigned(ctas)), Cfg::kThreads, Cfg::kSmem, s, 0);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, false>, k, a);
   if (e != cudaSuccess || ctas < 2) return e;
   // (the last CTA's items end with it)
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(unsigned(ctas - 1), unsigned(a.G));
-  cfg.blockDim = dim3(32 * kKv8MergeWarps);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv8_merge<HD>, k, a, int(Cfg::kPart), HB);
+  kv8_config(cfg, attr, dim3(unsigned(ctas - 1 < items ? ctas - 1 : items), unsigned(a.G)), 32 * kKv8MergeWarps, 0, s, 0);
+  return cudaLaunchKernelEx(&cfg, k_kv8_merge<HD>, k, a, int(ctas), int(Cfg::kPart), HB);
 }
 
 }  // namespace nt
@@ -794,7 +948,8 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.scale = 1.4426950408889634f / sqrtf(float(k.hd));
-  a.part = static_cast<float*>(dev_workspace);
+  a.open = static_cast<int2*>(dev_workspace);
+  a.part = static_cast<float*>(dev_workspace) + 2 * kKv8MaxCtas;
   for (int32_t i = 0; i < n; i += batch) {
     a.n = n - i < batch ? n - i : batch;
     a.seq0 = i;
@@ -803,7 +958,7 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
     a.pages = n_select ? dev_pages + int64_t(i) * k.n_kv * n_select : nullptr;
     a.q = dev_q + int64_t(i) * q_stride;
     a.out = dev_out + int64_t(i) * out_stride;
-    const int64_t tiles = a.n * entry_tiles;
+    const int64_t tiles = entry_tiles / k.n_kv;         // of an item, by capacity
     cudaError_t e;
     if (k.hd == 64)
       e = G <= 2 ? kv8_launch_attn<64, 2>(k, a, tiles, s)
