@@ -33,7 +33,7 @@ nt_status kv8_check(const nt_kv8_cache* c, const char* who, bool pointers, Kv4* 
 
 // Bytes of the workspace of the selection and of the attention.
 size_t kv8_select_ws_bytes(const Kv4& k, int64_t n);
-size_t kv8_attn_ws_bytes(int n_heads, int n_kv, int hd);
+size_t kv8_attn_ws_bytes(int hd);
 
 // ------------------------------------------------------------ device helpers --
 

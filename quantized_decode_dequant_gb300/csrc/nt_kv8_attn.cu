@@ -1,11 +1,12 @@
 // nt_kv8_attn.cu -- attention over the paged 8-bit cache (include/nt.h,
 // nt_attention_kv8).
 //
-// The mathematics.  For one (entry, kv head), an item, with G query heads, tiles of 128
+// The mathematics.  For one (entry, kv head), an item, with G query heads, or several
+// such entries of one sequence (drafted tokens, whose items are taken together), R rows of queries in all, tiles of 128
 // positions go through two products on tcgen05, kind::f8f6f4, whose A operand is the
 // cache itself, copied from its page to shared memory and never decoded:
-//   S^T [128 positions][6 G] = K [128][hd] . q^T        q as six e4m3 terms, each 1/16 of the one before
-//   O^T [hd][8 G]            = V^T [hd][128] . P^T      the weights as eight digits
+//   S^T [128 positions][6 R] = K [128][hd] . q^T        q as six e4m3 terms, each 1/16 of the one before
+//   O^T [hd][8 R]            = V^T [hd][128] . P^T      the weights as eight digits
 // e4m3 has four significant bits, so six terms, each the rounding of what the ones before left,
 // hold q to 2^-24 and more.  A weight w in [0, 16) is the whole number round(w 2^28), cut into
 // eight digits of four bits: the e4m3 codes 0 to 15 are the numbers 0 to 15 times 2^-9, so a
@@ -32,6 +33,7 @@ constexpr int kKv8MaxCluster = 16;
 
 struct Kv8AttnArgs {
   int32_t layer, n, G, k;
+  int32_t R;                            // entries that may share an item: e / R the same, one after the other, of one sequence
   int32_t seq0;                         // sequence of entry 0 where none are listed
   const int32_t* seq;
   const int32_t* ctx;
@@ -42,16 +44,14 @@ struct Kv8AttnArgs {
   int64_t out_stride;
   float scale;                          // log2(e) / sqrt(hd)
   float* part;                          // [CTA][2] partial results: of an item begun before this CTA, of one that goes on behind it
-  int2* open;                           // [CTA]: the latter's item (-1: none) and the number of CTAs that work on it
+  int2* open;                           // [CTA]: the latter's item (-1: none); the number of CTAs that work on it and (from bit 16) of its entries
 };
 
 // Partial result of one item: o [HB][HD], then (reference m, sum l) per head.
 constexpr int kv8_part_floats(int hd, int hb) { return hb * hd + 2 * hb; }
-constexpr int kv8_heads_block(int g) { return g <= 2 ? 2 : g <= 4 ? 4 : g <= 8 ? 8 : 16; }
 
-size_t kv8_attn_ws_bytes(int n_heads, int n_kv, int hd) {
-  const int g = n_heads / n_kv;
-  return size_t(kKv8MaxCtas) * (2 * kv8_part_floats(hd, kv8_heads_block(g < kKv8MaxGroup ? g : kKv8MaxGroup)) * 4 + 8);
+size_t kv8_attn_ws_bytes(int hd) {
+  return size_t(kKv8MaxCtas) * (2 * kv8_part_floats(hd, kKv8MaxGroup) * 4 + 8);
 }
 
 template <int HD, int HB>
@@ -65,19 +65,20 @@ struct Kv8AttnCfg {
   static constexpr int kSlot = kKv8Tile * HD;
   static constexpr int kPart = kv8_part_floats(HD, HB);
   static_assert(kPart * 4 <= H * kSlot, "a partial result fits the ring");
-  // P^T: blocks of 8 rows (a head's digits) by 16 positions; 16 positions further 64 bytes beyond a multiple of 128, so that
-  // a warp's two runs of 16 bytes fall on different banks
-  static constexpr int kPStep = NP * 16 + 64;
+  // P^T: blocks of 8 positions by 16 rows, the digits of two heads, which a thread stores as 16 bytes; 8 positions further kPStep
+  static constexpr int kPStep = NP * 8;
   // shared memory (V's rows 64 to 127 with 64 dimensions, which nobody looks at, reach 1 KB behind it)
   static constexpr int kExps = H * kSlot;
   static constexpr int kQ = kExps + E * 8 * 16;
   static constexpr int kP = kQ + NS * HD;
-  static constexpr int kRed = kP + 8 * kPStep;                      // [4][HB] of the warps, twice: maxima, sums
+  static constexpr int kRed = kP + 16 * kPStep;                     // [4][HB] of the warps, twice: maxima, sums
   static constexpr int kPrefix = kRed + 8 * HB * 4;
   static constexpr int kEntry = kPrefix + (kKv8Batch + 4) * 4;
   static constexpr int kSums = kEntry + kKv8Batch * 8;
-  static constexpr int kInfo = kSums + 32;                          // [E]: positions of the tile (0: none, -1: it lacks a page)
-  static constexpr int kBars = (kInfo + 4 * E + 7) / 8 * 8;         // full [H], empty [H], scores, taken, weights, outputs
+  static constexpr int kInfo = kSums + 32;                          // [E]: positions of the tile, and kLacks: behind them a page is not there
+  static constexpr int kLacks = 1 << 16;
+  static constexpr int kRows = kInfo + 4 * E;                       // [HB]: positions that a row of queries sees
+  static constexpr int kBars = (kRows + 4 * HB + 7) / 8 * 8;         // full [H], empty [H], scores, taken, weights, outputs
   static constexpr int kTmem = kBars + 8 * (2 * H + 4);
   static constexpr int kSegs = kTmem + 4;                           // items whose q is there
   static constexpr int kSmem = kTmem + 16;
@@ -168,8 +169,8 @@ struct Kv8At {
 
 // ------------------------------------------------------------ the kernel --
 
-// CL: block (rank, item) of a cluster per item.
-template <int HD, int HB, bool CL>
+// CL: block (rank, item) of a cluster per item.  GR: entries may share items.
+template <int HD, int HB, bool CL, bool GR>
 __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv4 c, Kv8AttnArgs a) {
   using Cfg = Kv8AttnCfg<HD, HB>;
   constexpr int H = Cfg::H, E = Cfg::E, NT = Cfg::kThreads;
@@ -211,14 +212,43 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     if (a.k && x > a.k) x = a.k;
     return a.k ? int((x * P + kKv8Tile - 1) / kKv8Tile) : int((int64_t(len) + kKv8Tile - 1) / kKv8Tile);
   };
-  int2 only = make_int2(-1, 0);                        // CL: the item's entry
+  // entries are kept from `base` on: CL: the item's only
+  const int base = CL ? int(blockIdx.y) / c.n_kv : 0, R = GR ? a.R : 1;
+  // whether entry e goes with the one before it
+  auto joins = [&](int e) { return e % R != 0 && entry[e - base].x >= 0 && entry[e - base].x == entry[e - 1 - base].x; };
+  // entries of the item that begins with e, and the most positions that one of them sees
+  auto item_of = [&](int e, int& len) {
+    int r = 1;
+    len = entry[e - base].y;
+    if (!GR) return 1;
+    while (r < R && e + r < n && joins(e + r)) {
+      len = max(len, entry[e + r - base].y);
+      r++;
+    }
+    return r;
+  };
+  int total = 0;
   if (CL) {
-    uint32_t bad;
-    only = kv8_attn_entry(c, a, int(blockIdx.y) / c.n_kv, &bad);
-    if (bad && blockIdx.x == 0 && t == 0) kv4_flag(c, bad);
+    // (the entry before: does this one go with it?)
+    bool with = false;
+    if (t < R && base + t < n) {
+      uint32_t bad;
+      entry[t] = kv8_attn_entry(c, a, base + t, &bad);
+      if (t == 0 && bad && blockIdx.x == 0) kv4_flag(c, bad);
+      if (GR && t == 0 && base % R) with = !bad && entry[0].x == kv8_attn_entry(c, a, base - 1, &bad).x;
+    }
     kv8_tc_before();
-    __syncthreads();
+    if (GR) with = __syncthreads_or(with);
+    else __syncthreads();
     kv8_tc_after();
+    if (GR && with) {                                  // (the whole cluster)
+      if (warp == 5)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tensor_memory), "n"(Cfg::kCols));
+      return;
+    }
+    int len;
+    item_of(base, len);
+    total = tiles(len);
   } else {
     int* sums = reinterpret_cast<int*>(sm + Cfg::kSums);
     int run = 0;
@@ -231,6 +261,17 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         if (bad && blockIdx.x == 0) kv4_flag(c, bad);
         entry[e] = sl;
         mine = tiles(sl.y) * c.n_kv;
+      }
+      if (GR) {
+        __syncthreads();
+        if (e < n) {   // (a round's entries may go with some of the round before, not with the next one's: NT is a multiple of R)
+          mine = 0;
+          if (!joins(e)) {
+            int len;
+            item_of(e, len);
+            mine = tiles(len) * c.n_kv;
+          }
+        }
       }
       int x = mine;
 #pragma unroll
@@ -258,8 +299,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   }
   const uint32_t tmem = *tensor_memory;
   asm volatile("griddepcontrol.launch_dependents;");
-  auto seen = [&](int e) { return CL ? only : entry[e]; };
-  const int total = CL ? tiles(only.y) : prefix[n];
+  if (!CL) total = prefix[n];
   int share = (total + int(gridDim.x) - 1) / int(gridDim.x);
   if (share < 1) share = 1;
   const int c0 = int(blockIdx.x) * share < total ? int(blockIdx.x) * share : total, c1 = c0 + share < total ? c0 + share : total;
@@ -267,7 +307,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
 
   auto locate = [&](int x, Kv8At& at) {
     if (CL) {
-      at = Kv8At{int(blockIdx.y) / c.n_kv, int(blockIdx.y) % c.n_kv, x, total};
+      at = Kv8At{base, int(blockIdx.y) % c.n_kv, x, total};
       return;
     }
     int lo = 0, hi = n;
@@ -276,7 +316,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       if (prefix[mid] <= x) lo = mid; else hi = mid;
     }
     at.e = lo;
-    at.nt = tiles(entry[lo].y);
+    int len;
+    item_of(lo, len);
+    at.nt = tiles(len);
     const int r = x - prefix[lo];
     at.g = r / at.nt;
     at.ti = r - at.g * at.nt;
@@ -293,9 +335,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     for (int x = c0; x < c1 && !dead;) {
       Kv8At at;
       locate(x, at);
-      const int count = segment(x, at), len = seen(at.e).y;
+      const int count = segment(x, at);
+      int len;
+      item_of(at.e, len);
       const int m = int((int64_t(len) + P - 1) / P), listed = a.k && a.k < m ? a.k : m;
-      const int32_t* row = c.table + int64_t(seen(at.e).x) * c.max_pages;
+      const int32_t* row = c.table + int64_t(entry[at.e - base].x) * c.max_pages;
       const int32_t* list = a.k ? a.pages + (int64_t(at.e) * c.n_kv + at.g) * a.k : nullptr;
       const int end = (at.ti + count) * per < listed ? (at.ti + count) * per : listed;
       // the page at place i of the list; -1: none there, -2: the list has ended; *last: it is the sequence's last page
@@ -327,11 +371,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         const int y = at_list - first + lane % 8;
         const int mine = __shfl_sync(0xffffffffu, page, y & 31);
         const bool is_last = __shfl_sync(0xffffffffu, int(last), y & 31);
-        const bool live = lane % 8 < per && mine >= 0;
-        const bool lacks = __any_sync(0xffffffffu, lane < per && mine == -1);
+        // what lies behind a page that is not there is not looked at either
+        const uint32_t lacking = __ballot_sync(0xffffffffu, lane < per && mine == -1);
+        const bool live = lane % 8 < per && mine >= 0 && (lacking == 0u || lane % 8 < __ffs(lacking) - 1);
         const int have = __popc(__ballot_sync(0xffffffffu, lane < 8 && live));
-        const bool ends = __any_sync(0xffffffffu, live && is_last);
-        const bool nothing = lacks || !have;
+        const bool ends = __any_sync(0xffffffffu, live && is_last), nothing = !have;
         const uint8_t* from = layer_pool + (live ? mine : 0) * c.page_bytes();
 #pragma unroll
         for (int v = 0; v < 2; v++) {                  // K, V
@@ -339,7 +383,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           if (fill >= H && !__all_sync(0xffffffffu, kv4_bar_wait(empty + 8 * slot, uint32_t(fill / H - 1) & 1u))) { dead = true; break; }
           const uint32_t bar = full + 8 * slot;
           if (lane == 0) {
-            if (v == 0) info[no % E] = lacks ? -1 : have * P - (ends ? m * P - len : 0);
+            if (v == 0) info[no % E] = (have * P - (ends ? m * P - len : 0)) | (lacking ? Cfg::kLacks : 0);
             if (nothing) kv4_bar_arrive(bar);
             else kv4_bar_expect(bar, uint32_t(have) * uint32_t(codes + (v ? 0 : 16)));
           }
@@ -363,7 +407,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     // ---- products: scores of tile ns as soon as it and q are there and the scores before are taken, outputs of
     // tile np as soon as its weights are there, whichever comes first
     constexpr uint32_t kIdesc = 1u << 4 | uint32_t(kKv8Tile / 16) << 24;   // fp32 += e4m3 e4m3, 128 rows
-    constexpr uint32_t kIdescS = kIdesc | uint32_t(Cfg::NS / 8) << 17, kIdescO = kIdesc | uint32_t(Cfg::NP / 8) << 17;
+    constexpr uint32_t kIdescS = kIdesc | uint32_t(Cfg::NS / 8) << 17, kIdescO = kIdesc | uint32_t(Cfg::NP / 8) << 17 | 1u << 16;   // P^T: rows side by side
     const int all = c1 - c0;
     int ns = 0, np = 0, weighed = 0, segs = 0, left = 0, idle = 0;   // left: tiles of the segment without scores
     while (np < all) {
@@ -381,7 +425,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           }
         }
         if (ok && kv8_bar_test(full + 8 * slot, uint32_t(2 * ns / H) & 1u) && (ns == 0 || kv8_bar_test(bar_taken, uint32_t(ns - 1) & 1u))) {
-          if (info[ns % E] > 0) {
+          if (info[ns % E] & (Cfg::kLacks - 1)) {
             kv8_tc_after();
             if (kv8_elect()) {
               const uint32_t k0 = smu + slot * Cfg::kSlot, q0 = smu + Cfg::kQ;
@@ -404,7 +448,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       if (np < ns) {
         const int fill = 2 * np + 1, slot = fill % H;
         if (kv8_bar_test(full + 8 * slot, uint32_t(fill / H) & 1u)) {
-          if (info[np % E] <= 0) {                     // free once the softmax warps have seen that there is nothing
+          if (!(info[np % E] & (Cfg::kLacks - 1))) {                     // free once the softmax warps have seen that there is nothing
             if (ns > np + 1 || kv8_bar_test(bar_taken, uint32_t(np) & 1u)) {
               if (lane == 0) kv4_bar_arrive(empty + 8 * slot);
               __syncwarp();
@@ -418,7 +462,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
 #pragma unroll
               for (int kk = 0; kk < kKv8Tile / 32; kk++)
                 kv8_mma(tmem + Cfg::kColO, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
-                        kv8_desc(p0 + kk * 2 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
+                        kv8_desc(p0 + kk * 4 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
               kv8_commit(bar_o);
               kv8_commit(empty + 8 * slot);
             }
@@ -439,13 +483,14 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     // ---- softmax: thread t has position t of a tile, and dimension t of the outputs
     const uint32_t mine = uint32_t(32 * warp) << 16;   // this warp's rows of tensor memory
     float* red = reinterpret_cast<float*>(sm + Cfg::kRed);
-    uint8_t* my_p = sm + Cfg::kP + (t >> 4) * Cfg::kPStep + (t & 15);
+    uint8_t* my_p = sm + Cfg::kP + (t >> 3) * Cfg::kPStep + (t & 7) * 16;
     float O[HB], l[HB], mref[HB], cs[HB];
     uint32_t ps = 0, po = 0;
     int no = 0, segs = 0;
     bool dead = false, pending = false;
     float out_scale = 0.f;                             // of the outputs under way
 
+    constexpr int kTake = HB < 4 ? HB : 4;             // heads taken together
     auto take = [&]() -> bool {                        // adds them to the sums; false: they never came
       if (!pending) return true;
       pending = false;
@@ -453,17 +498,18 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       po ^= 1u;
       kv8_tc_after();
       if (HD == 128 || warp < 2) {
+        const uint64_t k16 = kv8_pack(16.f, 16.f), k65536 = kv8_pack(65536.f, 65536.f);
 #pragma unroll
-        for (int b = 0; b < HB / 2; b++) {             // two heads' digits, the lowest first
-          uint32_t r[16];
-          kv8_tc_ld16(tmem + mine + Cfg::kColO + 16 * b, r);
+        for (int b = 0; b < HB / kTake; b++) {
+          uint32_t r[8 * kTake];
+#pragma unroll
+          for (int y = 0; y < kTake / 2; y++) kv8_tc_ld16(tmem + mine + Cfg::kColO + 8 * kTake * b + 16 * y, r + 16 * y);
           kv8_tc_wait(r);
 #pragma unroll
-          for (int h = 0; h < 2; h++) {
-            float v = __uint_as_float(r[8 * h + 7]);
-#pragma unroll
-            for (int d = 6; d >= 0; d--) v = fmaf(v, 16.f, __uint_as_float(r[8 * h + d]));
-            O[2 * b + h] = fmaf(v, out_scale, O[2 * b + h]);
+          for (int h = 0; h < kTake; h++) {            // a head's digits 0, 2, 4, 6, 1, 3, 5, 7
+            auto two = [&](int i) { return kv8_pack(__uint_as_float(r[8 * h + i]), __uint_as_float(r[8 * h + i + 1])); };
+            const float2 v = kv8_unpack(kv8_fma2(kv8_fma2(two(6), k16, two(2)), k65536, kv8_fma2(two(4), k16, two(0))));
+            O[kTake * b + h] = fmaf(fmaf(v.y, 256.f, v.x), out_scale, O[kTake * b + h]);
           }
         }
       }
@@ -476,17 +522,42 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       Kv8At at;
       locate(x, at);
       const int count = segment(x, at);
+      int len;
+      const int rows = item_of(at.e, len) * a.G;       // of queries
       bool poison = dead;
+      int lacking = 0x7fffffff;                        // rows that see more positions are not known
+      int* sees = reinterpret_cast<int*>(sm + Cfg::kRows);
+      int least = 0x7fffffff;                          // positions that every row sees
       // ---- q: scaled so that its largest element is in [2^7, 2^8), in six terms.  A warp takes every fourth head.
       {
-        const float* qb = a.q + int64_t(at.e) * a.q_stride + int64_t(at.g) * a.G * HD;
         constexpr int V = HD / 32;
-#pragma unroll 1
-        for (int h = warp; h < HB; h += 4) {
-          float y[V], top = 0.f;
+        if (GR && t < HB) sees[t] = t < rows ? entry[at.e + t / a.G - base].y : 0;
+        constexpr int kMine = (HB + 3) / 4;            // rows of a warp: all on the way together
+        float z[kMine][V];
+#pragma unroll
+        for (int j = 0; j < kMine; j++) {
+          const int h = warp + 4 * j, sub = GR ? h / a.G : 0;
+          const float* qb = a.q + int64_t(at.e + sub) * a.q_stride + int64_t(at.g * a.G + h - sub * a.G) * HD + V * lane;
+#pragma unroll
+          for (int i = 0; i < V; i++) z[j][i] = 0.f;
+          if (h < rows) {
+            if (V == 4) {
+              const float4 w = *reinterpret_cast<const float4*>(qb);
+              z[j][0] = w.x; z[j][1] = w.y; z[j][2 % V] = w.z; z[j][3 % V] = w.w;
+            } else {
+              const float2 w = *reinterpret_cast<const float2*>(qb);
+              z[j][0] = w.x; z[j][1] = w.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kMine; j++) {
+          const int h = warp + 4 * j;
+          if (h >= HB) break;
+          float (&y)[V] = z[j], top = 0.f;
 #pragma unroll
           for (int i = 0; i < V; i++) {
-            y[i] = h < a.G ? qb[h * HD + V * lane + i] * a.scale : 0.f;
+            y[i] *= a.scale;
             if (!(fabsf(y[i]) < INFINITY)) y[i] = NAN;
             top = fmaxf(top, fabsf(y[i]));             // (a NaN is passed over)
           }
@@ -529,6 +600,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           O[h] = l[h] = 0.f;
           mref[h] = -3e38f;
         }
+        if (GR)
+          for (int h = 0; h < rows; h++) least = min(least, sees[h]);
         kv8_any(false);                                // red is read
       }
 #pragma unroll 1
@@ -537,10 +610,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         // (not K's own barrier: its slot may have been filled again by now)
         bool fail = !__all_sync(0xffffffffu, kv4_bar_wait(bar_s, ps));
         ps ^= 1u;
-        const int live = info[no % E];
-        if (live <= 0 || fail) {
+        const int word = info[no % E], live = word & (Cfg::kLacks - 1), start = (at.ti + i) * kKv8Tile;
+        if (word & Cfg::kLacks) lacking = min(lacking, start + live);
+        if (live == 0 || fail) {
           if (kv8_any(fail)) dead = kv8_any(fail);     // (as many barriers as a tile with scores has)
-          poison = poison || dead || live < 0;
+          poison = poison || dead;
           __syncwarp();
           if (lane == 0) kv4_bar_arrive(bar_taken);
           continue;
@@ -580,13 +654,17 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             for (int y = 0; y < kCols / 16; y++) kv8_tc_ld16(tmem + mine + Cfg::kColS + b * kCols + 16 * y, r + 16 * y);
             kv8_tc_wait(r);
             constexpr int kT = HB == 16 ? 3 : Cfg::kTerms;
+            const uint64_t k16th = kv8_pack(1.f / 16.f, 1.f / 16.f);
 #pragma unroll
-            for (int h = 0; h < HB; h++) {
-              float z = __uint_as_float(r[(kT - 1) * HB + h]);
-              if (HB == 16 && b == 0) z = fmaf(s[h], 1.f / 16.f, z);
+            for (int h = 0; h < HB; h += 2) {
+              auto two = [&](int k) { return kv8_pack(__uint_as_float(r[k * HB + h]), __uint_as_float(r[k * HB + h + 1])); };
+              uint64_t z = two(kT - 1);
+              if (HB == 16 && b == 0) z = kv8_fma2(kv8_pack(s[h], s[h + 1]), k16th, z);
 #pragma unroll
-              for (int k = kT - 2; k >= 0; k--) z = fmaf(z, 1.f / 16.f, __uint_as_float(r[k * HB + h]));
-              s[h] = z;
+              for (int k = kT - 2; k >= 0; k--) z = kv8_fma2(z, k16th, two(k));
+              const float2 y = kv8_unpack(z);
+              s[h] = y.x;
+              s[h + 1] = y.y;
             }
           }
         }
@@ -595,6 +673,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         if (lane == 0) kv4_bar_arrive(bar_taken);
 #pragma unroll
         for (int h = 0; h < HB; h++) s[h] = here ? s[h] * fk : -INFINITY;
+        if (GR && start + kKv8Tile > least) {       // some rows end in this tile, or before it
+#pragma unroll
+          for (int h = 0; h < HB; h++)
+            if (start + t >= sees[h]) s[h] = -INFINITY;
+        }
         fail = !take() || fail;
         // ---- weights
         float p[HB], most;
@@ -632,15 +715,15 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           weights();
         }
 #pragma unroll
-        for (int h = 0; h < HB; h++) {
-          l[h] += p[h];
-          const uint32_t u = __float2uint_rn(p[h] * fv);
-          const uint32_t even = u & 0x0f0f0f0fu, odd = (u >> 4) & 0x0f0f0f0fu;
+        for (int h = 0; h < HB; h += 2) {
+          uint32_t u[2];
 #pragma unroll
-          for (int d = 0; d < 4; d++) {
-            my_p[h * 128 + (2 * d) * 16] = uint8_t(even >> (8 * d));
-            my_p[h * 128 + (2 * d + 1) * 16] = uint8_t(odd >> (8 * d));
+          for (int y = 0; y < 2; y++) {
+            l[h + y] += p[h + y];
+            u[y] = __float2uint_rn(p[h + y] * fv);
           }
+          *reinterpret_cast<uint4*>(my_p + h * 64) =
+              make_uint4(u[0] & 0x0f0f0f0fu, (u[0] >> 4) & 0x0f0f0f0fu, u[1] & 0x0f0f0f0fu, (u[1] >> 4) & 0x0f0f0f0fu);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         kv8_tc_before();
@@ -660,18 +743,22 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       }
       poison = kv8_any(poison);
       const bool whole = !CL && at.ti == 0 && count == at.nt, begun = at.ti == 0;
-      float* to = CL ? reinterpret_cast<float*>(sm) : whole ? a.out + int64_t(at.e) * a.out_stride + int64_t(at.g) * a.G * HD : part0 + (begun ? Cfg::kPart : 0);
+      float* part = CL ? reinterpret_cast<float*>(sm) : part0 + (begun ? Cfg::kPart : 0);
 #pragma unroll
       for (int h = 0; h < HB; h++) {
         float sum = (sums[h] + sums[HB + h]) + (sums[2 * HB + h] + sums[3 * HB + h]);
-        if (poison) sum = NAN;
-        if (t < HD && h < a.G) to[h * HD + t] = whole ? (sum == 0.f ? 0.f : O[h] / sum) : O[h];
-        if (!whole && t == 0) reinterpret_cast<float2*>(to + HB * HD)[h] = make_float2(mref[h], sum);
+        if (poison || (GR ? sees[h] > lacking : lacking != 0x7fffffff)) sum = NAN;
+        if (h < rows) {
+          const int sub = GR ? h / a.G : 0;
+          float* to = whole ? a.out + int64_t(at.e + sub) * a.out_stride + int64_t(at.g * a.G + h - sub * a.G) * HD : part + h * HD;
+          if (t < HD) to[t] = whole ? (sum == 0.f ? 0.f : O[h] / sum) : O[h];
+        }
+        if (!whole && t == 0) reinterpret_cast<float2*>(part + HB * HD)[h] = make_float2(mref[h], sum);
       }
       x += count;
       // the CTA's last item is open where it was begun here and goes on behind
       if (!CL && x >= c1 && t == 0)
-        a.open[blockIdx.x] = begun && !whole ? make_int2(at.e * c.n_kv + at.g, (x - count + at.nt - 1) / share - int(blockIdx.x) + 1) : make_int2(-1, 0);
+        a.open[blockIdx.x] = begun && !whole ? make_int2(at.e * c.n_kv + at.g, ((x - count + at.nt - 1) / share - int(blockIdx.x) + 1) | (GR ? rows / a.G : 1) << 16) : make_int2(-1, 0);
       kv8_any(false);                                  // the sums are read
     }
     if (!CL) {
@@ -695,8 +782,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   }
   if (CL) {
     // ---- the item's partial results, each CTA a share of the outputs, in the ranks' order
-    const int ranks = int(gridDim.x), outs = a.G * HD;
-    float* out = a.out + int64_t(int(blockIdx.y) / c.n_kv) * a.out_stride + int64_t(int(blockIdx.y) % c.n_kv) * outs;
+    int len;
+    const int ranks = int(gridDim.x), outs = item_of(base, len) * a.G * HD;
+    float* out = a.out + int64_t(base) * a.out_stride + int64_t(int(blockIdx.y) % c.n_kv) * a.G * HD;
     auto there = [&](int r, uint32_t at) {             // shared memory of rank r
       uint32_t y;
       asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(smu + at), "r"(r));
@@ -728,7 +816,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           sum = fmaf(l[r], f, sum);
           y = fmaf(o[r], f, y);
         }
-      out[i] = only.x < 0 ? NAN : sum == 0.f ? 0.f : y / sum;
+      const int sub = GR ? h / a.G : 0;
+      out[int64_t(sub) * a.out_stride + i - sub * a.G * HD] = entry[0].x < 0 ? NAN : sum == 0.f ? 0.f : y / sum;
     }
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");   // all have read this CTA's
   }
@@ -751,7 +840,7 @@ __global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8Att
   if (int(gridDim.x) >= ctas - 1) {   // as many blocks as CTAs: no need to count
     const int2 x = __ldcg(a.open + blockIdx.x);
     if (x.x < 0) return;
-    if (t == 0) { s_cta = int(blockIdx.x); s_item = x.x; s_members = x.y; }
+    if (t == 0) { s_cta = int(blockIdx.x); s_item = x.x; s_members = x.y; }   
     __syncthreads();
   }
   int before = 0;
@@ -774,7 +863,8 @@ __global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8Att
     __syncthreads();
   }
   if (s_cta < 0) return;
-  const int members = s_members;
+  const int members = s_members & 0xffff;
+  if (h >= (s_members >> 16) * a.G) return;            // (the item has fewer entries)
   const float* first = a.part + (int64_t(s_cta) * 2 + 1) * part_floats;   // the second of this CTA, then the first of the next ones
   float M = -INFINITY, sum = 0.f, o[V];
 #pragma unroll
@@ -815,8 +905,8 @@ __global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8Att
       total = fmaf(s_ml[w].y, f, total);
       y = fmaf(s_o[w][t], f, y);
     }
-    const int e = s_item / c.n_kv, g = s_item % c.n_kv;
-    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h) * HD + t] = total == 0.f ? 0.f : y / total;
+    const int sub = h / a.G, e = s_item / c.n_kv + sub, g = s_item % c.n_kv;
+    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h - sub * a.G) * HD + t] = total == 0.f ? 0.f : y / total;
   }
 }
 
@@ -840,12 +930,12 @@ static void kv8_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], 
   cfg.attrs = attr;
   cfg.numAttrs = cluster ? 2 : 1;
 }
-template <int HD, int HB>
+template <int HD, int HB, bool GR>
 static Kv8Fit kv8_fit() {
   using Cfg = Kv8AttnCfg<HD, HB>;
   Kv8Fit f;
-  f.setup = kernel_setup(k_kv8_attn<HD, HB, true>, Cfg::kSmem);
-  if (f.setup.err == cudaSuccess) f.setup.err = cudaFuncSetAttribute(k_kv8_attn<HD, HB, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  f.setup = kernel_setup(k_kv8_attn<HD, HB, true, GR>, Cfg::kSmem);
+  if (f.setup.err == cudaSuccess) f.setup.err = cudaFuncSetAttribute(k_kv8_attn<HD, HB, true, GR>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   for (int i = 0; i < 8 && f.setup.err == cudaSuccess; i++) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
@@ -853,7 +943,7 @@ static Kv8Fit kv8_fit() {
     cfg.numAttrs = 1;
     attr[0] = attr[1];
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k_kv8_attn<HD, HB, true>, &cfg) == cudaSuccess) f.clusters[i] = n;
+    if (cudaOccupancyMaxActiveClusters(&n, k_kv8_attn<HD, HB, true, GR>, &cfg) == cudaSuccess) f.clusters[i] = n;
     else cudaGetLastError();   // (no such cluster: it is not taken)
   }
   return f;
@@ -864,7 +954,7 @@ static Kv8Fit kv8_fit() {
 // 8: 18.3, 18.3; 16 of 300, 32/8: 8.2, 13.6; 1 of 9000, 16/1, 5 tiles a CTA: 14.9, 12.3.)
 constexpr int kKv8ClusterShare[2] = {6, 3};
 
-template <int HD, int HB>
+template <int HD, int HB, bool GR>
 static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t item_tiles, cudaStream_t s) {
   using Cfg = Kv8AttnCfg<HD, HB>;
   cudaLaunchConfig_t cfg;
@@ -872,7 +962,7 @@ static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t i
   const int64_t items = int64_t(a.n) * k.n_kv;
   // A cluster per item where all of them fit the GPU at once and their capacity leaves no CTA more than kKv8ClusterShare tiles: the smallest
   // cluster such that a CTA has one tile at most, or the largest.
-  static const Kv8Fit fit = kv8_fit<HD, HB>();
+  static const Kv8Fit fit = kv8_fit<HD, HB, GR>();
   if (fit.setup.err != cudaSuccess) return fit.setup.err;
   int cluster = 0;
   for (int i = 0; i < 8; i++) {
@@ -882,18 +972,27 @@ static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t i
   }
   if (cluster) {
     kv8_config(cfg, attr, dim3(unsigned(cluster), unsigned(items)), Cfg::kThreads, Cfg::kSmem, s, cluster);
-    return cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, true>, k, a);
+    return cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, true, GR>, k, a);
   }
-  static const KernelSetup setup = kernel_setup(k_kv8_attn<HD, HB, false>, Cfg::kSmem);
+  static const KernelSetup setup = kernel_setup(k_kv8_attn<HD, HB, false, GR>, Cfg::kSmem);
   if (setup.err != cudaSuccess) return setup.err;
   int64_t ctas = 2 * setup.sms < kKv8MaxCtas ? 2 * setup.sms : kKv8MaxCtas;
   if (ctas > items * item_tiles) ctas = items * item_tiles;
   kv8_config(cfg, attr, dim3(unsigned(ctas)), Cfg::kThreads, Cfg::kSmem, s, 0);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, false>, k, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, false, GR>, k, a);
   if (e != cudaSuccess || ctas < 2) return e;
   // (the last CTA's items end with it)
-  kv8_config(cfg, attr, dim3(unsigned(ctas - 1 < items ? ctas - 1 : items), unsigned(a.G)), 32 * kKv8MergeWarps, 0, s, 0);
+  kv8_config(cfg, attr, dim3(unsigned(ctas - 1 < items ? ctas - 1 : items), unsigned(a.R * a.G)), 32 * kKv8MergeWarps, 0, s, 0);
   return cudaLaunchKernelEx(&cfg, k_kv8_merge<HD>, k, a, int(ctas), int(Cfg::kPart), HB);
+}
+
+template <int HD>
+static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t item_tiles, cudaStream_t s) {
+  const int rows = a.R * a.G;
+  if (a.R > 1) return rows <= 8 ? kv8_launch_attn<HD, 8, true>(k, a, item_tiles, s) : kv8_launch_attn<HD, 16, true>(k, a, item_tiles, s);
+  if (rows <= 2) return kv8_launch_attn<HD, 2, false>(k, a, item_tiles, s);
+  if (rows <= 4) return kv8_launch_attn<HD, 4, false>(k, a, item_tiles, s);
+  return rows <= 8 ? kv8_launch_attn<HD, 8, false>(k, a, item_tiles, s) : kv8_launch_attn<HD, 16, false>(k, a, item_tiles, s);
 }
 
 }  // namespace nt
@@ -924,7 +1023,7 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
   if ((n_select && !kv4_aligned(dev_pages, 4)) || (dev_seq && !kv4_aligned(dev_seq, 4)) || (dev_ctx && !kv4_aligned(dev_ctx, 4)))
     return bad("a list is NULL or not 4-byte aligned");
   if (!n_select && dev_pages) return bad("pages without n_select");
-  const size_t wb = kv8_attn_ws_bytes(n_heads, k.n_kv, k.hd);
+  const size_t wb = kv8_attn_ws_bytes(k.hd);
   if (workspace_bytes < wb) return bad("workspace too small");
   if (n == 0) return NT_OK;
   const int64_t items = int64_t(n) * k.n_kv;
@@ -945,6 +1044,10 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
   a.layer = layer;
   a.G = G;
   a.k = n_select;
+  // Entries of one sequence share items where the call says that there may be some: it lists sequences, and how much of them is seen.
+  a.R = dev_seq && dev_ctx && !n_select ? kKv8MaxGroup / G : 1;
+  if (a.R > n) a.R = n;
+  while (192 % a.R) a.R--;                             // (a round of the kernel's threads holds whole items)
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.scale = 1.4426950408889634f / sqrtf(float(k.hd));
@@ -959,15 +1062,7 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
     a.q = dev_q + int64_t(i) * q_stride;
     a.out = dev_out + int64_t(i) * out_stride;
     const int64_t tiles = entry_tiles / k.n_kv;         // of an item, by capacity
-    cudaError_t e;
-    if (k.hd == 64)
-      e = G <= 2 ? kv8_launch_attn<64, 2>(k, a, tiles, s)
-                 : G <= 4 ? kv8_launch_attn<64, 4>(k, a, tiles, s)
-                          : G <= 8 ? kv8_launch_attn<64, 8>(k, a, tiles, s) : kv8_launch_attn<64, 16>(k, a, tiles, s);
-    else
-      e = G <= 2 ? kv8_launch_attn<128, 2>(k, a, tiles, s)
-                 : G <= 4 ? kv8_launch_attn<128, 4>(k, a, tiles, s)
-                          : G <= 8 ? kv8_launch_attn<128, 8>(k, a, tiles, s) : kv8_launch_attn<128, 16>(k, a, tiles, s);
+    const cudaError_t e = k.hd == 64 ? kv8_launch_attn<64>(k, a, tiles, s) : kv8_launch_attn<128>(k, a, tiles, s);
     if (e != cudaSuccess) return cuda_fail(e, who);
   }
   return NT_OK;

@@ -461,6 +461,51 @@ def test_drafts_see_the_positions_up_to_their_own(nt):
     assert (got[9] == 0).all()
 
 
+@pytest.mark.parametrize("hd,kv,heads,page_len,longest,n", [
+    (128, 2, 2, 16, 700, 60), (128, 2, 4, 64, 1500, 37), (64, 3, 9, 32, 900, 41), (128, 1, 4, 128, 6000, 23), (64, 2, 14, 16, 400, 30),
+    (128, 4, 32, 64, 2000, 25), (64, 1, 16, 64, 3000, 9), (64, 1, 1, 16, 200, 3), (128, 8, 32, 64, 4000, 20)])
+def test_entries_of_one_sequence_share_items(nt, hd, kv, heads, page_len, longest, n):
+    """Runs of any length of the same sequence, lengths in any order, nothing at all among them."""
+    rng = np.random.default_rng(29 + n)
+    lens = [longest, 1, longest // 2, 130]
+    P = sum(-(-x // page_len) for x in lens)
+    ref = R.RefCache(1, kv, hd, page_len, P, 4, -(-longest // page_len))
+    ref.randomize(rng)
+    ref.hold(lens, rng)
+    seqs, ctx = [], []
+    while len(seqs) < n:
+        s = int(rng.integers(4))
+        for _ in range(int(rng.choice([1, 2, 5, 9]))):
+            seqs.append(s)
+            ctx.append(int(rng.choice([lens[s], max(0, lens[s] - int(rng.integers(6))), int(rng.integers(lens[s] + 1)), 0],
+                                      p=[0.4, 0.3, 0.2, 0.1])))
+    got, _ = check_attention(Dev(nt, ref, heads, n), rng, seqs[:n], ctx[:n])
+    assert (got[np.array(ctx[:n]) == 0] == 0).all()
+
+
+def test_a_missing_page_concerns_the_entries_that_see_it(nt):
+    import torch
+    rng = np.random.default_rng(30)
+    for longest, bad_at in ((1000, 12), (1000, 0), (150, 8), (5000, 300)):
+        ref = R.RefCache(1, 1, 64, 16, 400, 2, 320)
+        ref.randomize(rng)
+        ref.hold([longest, 40], rng)
+        dev = Dev(nt, ref, 2, 8)
+        dev.table[0, bad_at] = 400
+        at = 16 * bad_at
+        seqs, ctx = [0, 0, 0, 0, 1, 0, 0, 9], [longest, at, at + 1, max(0, at - 20), 40, longest // 2, min(longest, at + 16), 5]
+        q = rng.standard_normal((8, 2, 64)).astype(np.float32)
+        got = dev.attention(torch.from_numpy(q).cuda(), seqs, ctx).cpu().numpy()
+        assert int(dev.error.cpu()[0]) == 1 | 4
+        for i, (s, c) in enumerate(zip(seqs, ctx)):
+            if s == 9 or (s == 0 and c > at):
+                assert np.isnan(got[i]).all(), (longest, i)
+                continue
+            k, v = ref.kv(0, s, 0, c)
+            parts = R.attend(q[i].astype(np.float64), k, v)
+            assert (np.abs(got[i] - parts[0]) <= bound(parts, len(k), np.abs(v).max() if c else 0)).all(), (longest, i)
+
+
 def test_strides_and_layers(nt):
     import torch
     rng = np.random.default_rng(14)
