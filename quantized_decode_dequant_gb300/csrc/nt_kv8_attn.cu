@@ -71,14 +71,14 @@ struct Kv8AttnCfg {
   static constexpr int kExps = H * kSlot;
   static constexpr int kQ = kExps + E * 8 * 16;
   static constexpr int kP = kQ + NS * HD;
-  static constexpr int kRed = kP + 16 * kPStep;                     // [4][HB] of the warps, twice: maxima, sums
-  static constexpr int kPrefix = kRed + 8 * HB * 4;
+  static constexpr int kRed = kP + 16 * kPStep;                      // [4][HB] of the warps, twice: maxima, sums; [2][HB] scales of q
+  static constexpr int kPrefix = kRed + 10 * HB * 4;
   static constexpr int kEntry = kPrefix + (kKv8Batch + 4) * 4;
   static constexpr int kSums = kEntry + kKv8Batch * 8;
   static constexpr int kInfo = kSums + 32;                          // [E]: positions of the tile, and kLacks: behind them a page is not there
   static constexpr int kLacks = 1 << 16;
-  static constexpr int kRows = kInfo + 4 * E;                       // [HB]: positions that a row of queries sees
-  static constexpr int kBars = (kRows + 4 * HB + 7) / 8 * 8;         // full [H], empty [H], scores, taken, weights, outputs
+  static constexpr int kRows = kInfo + 4 * E;                       // [2][HB]: positions that a row of queries sees
+  static constexpr int kBars = (kRows + 8 * HB + 7) / 8 * 8;         // full [H], empty [H], scores, taken, weights, outputs
   static constexpr int kTmem = kBars + 8 * (2 * H + 4);
   static constexpr int kSegs = kTmem + 4;                           // items whose q is there
   static constexpr int kSmem = kTmem + 16;
@@ -151,6 +151,28 @@ __device__ __forceinline__ bool kv8_any(bool p) {
       : "memory");
   return r;
 }
+
+// N values of every lane joined over the warp by f, value by value: halves of them are exchanged while there are several, so that it takes
+// N + log2(32 / N) - 1 exchanges; lane l is left with value kv8_joined<N>(l).
+template <int N, class F>
+__device__ __forceinline__ float kv8_join(float (&x)[N], F f) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int n = N, o = 16; n > 1; n /= 2, o /= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < n / 2; i++) {
+      const float got = __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + n / 2], o);
+      x[i] = f(up ? x[i + n / 2] : x[i], got);
+    }
+  }
+  float y = x[0];
+#pragma unroll
+  for (int o = 16 / N; o; o /= 2) y = f(y, __shfl_xor_sync(0xffffffffu, y, o));
+  return y;
+}
+template <int N>
+__device__ __forceinline__ int kv8_joined(int lane) { return lane / (32 / N); }
 
 // Sequence and positions of listed entry e (0 positions and *bad where it cannot be read).
 __device__ __forceinline__ int2 kv8_attn_entry(const Kv4& c, const Kv8AttnArgs& a, int e, uint32_t* bad) {
@@ -486,7 +508,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     uint8_t* my_p = sm + Cfg::kP + (t >> 3) * Cfg::kPStep + (t & 7) * 16;
     float O[HB], l[HB], mref[HB], cs[HB];
     uint32_t ps = 0, po = 0;
-    int no = 0, segs = 0;
+    int no = 0, segs = 0;                              // tiles; items whose q was prepared
     bool dead = false, pending = false;
     float out_scale = 0.f;                             // of the outputs under way
 
@@ -517,93 +539,103 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       return ok;
     };
 
+    // The q of the item at `at` into shared memory, scaled so that its largest element is in [2^7, 2^8), in six terms; a warp takes every fourth
+    // row.  It is done before the item before it is finished with, once that one's scores are all there.
+    int* sees0 = reinterpret_cast<int*>(sm + Cfg::kRows);
+    float* scales = red + 8 * HB;
+    auto prepare = [&](const Kv8At& at, int odd) {
+      int len;
+      const int rows = item_of(at.e, len) * a.G;
+      constexpr int V = HD / 32;
+      if (GR && t < HB) sees0[odd * HB + t] = t < rows ? entry[at.e + t / a.G - base].y : 0;
+      constexpr int kMine = (HB + 3) / 4;            // rows of a warp: all on the way together
+      float z[kMine][V];
+#pragma unroll
+      for (int j = 0; j < kMine; j++) {
+        const int h = warp + 4 * j, sub = GR ? h / a.G : 0;
+        const float* qb = a.q + int64_t(at.e + sub) * a.q_stride + int64_t(at.g * a.G + h - sub * a.G) * HD + V * lane;
+#pragma unroll
+        for (int i = 0; i < V; i++) z[j][i] = 0.f;
+        if (h < rows) {
+          if (V == 4) {
+            const float4 w = *reinterpret_cast<const float4*>(qb);
+            z[j][0] = w.x; z[j][1] = w.y; z[j][2 % V] = w.z; z[j][3 % V] = w.w;
+          } else {
+            const float2 w = *reinterpret_cast<const float2*>(qb);
+            z[j][0] = w.x; z[j][1] = w.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kMine; j++) {
+        const int h = warp + 4 * j;
+        if (h >= HB) break;
+        float (&y)[V] = z[j], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; i++) {
+          y[i] *= a.scale;
+          if (!(fabsf(y[i]) < INFINITY)) y[i] = NAN;
+          top = fmaxf(top, fabsf(y[i]));             // (a NaN is passed over)
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        int ex = int(__float_as_uint(top) >> 23);
+        ex = ex < 14 ? 14 : ex;                      // (zeros and values below 2^-113)
+        const float up = __uint_as_float(uint32_t(261 - ex) << 23);                  // 2^(134 - ex)
+        if (lane == 0) scales[odd * HB + h] = __uint_as_float(uint32_t(ex - 7) << 23);             // 2^(ex - 134)
+        uint8_t* to = sm + Cfg::kQ + (V * lane >> 4) * 128 + (V * lane & 15);
+#pragma unroll
+        for (int i = 0; i < V; i++) y[i] *= up;
+#pragma unroll
+        for (int k = 0; k < Cfg::kTerms; k++) {
+          const int row = k * HB + h;
+#pragma unroll
+          for (int i = 0; i < V; i += 2) {
+            const uint32_t w = kv8_code2(y[i], y[i + 1]);
+            *reinterpret_cast<uint16_t*>(to + (row >> 3) * 8 * HD + (row & 7) * 16 + i) = uint16_t(w);
+            const float2 f = kv8_value2(w);
+            y[i] = (y[i] - f.x) * 16.f;
+            y[i + 1] = (y[i + 1] - f.y) * 16.f;
+          }
+        }
+      }
+      if constexpr (Cfg::NS > Cfg::kTerms * HB)      // rows of no head
+        for (int i = t; i < (Cfg::NS - Cfg::kTerms * HB) * HD / 16; i += 128) {
+          const int row = Cfg::kTerms * HB + i / (HD / 16);
+          *reinterpret_cast<uint4*>(sm + Cfg::kQ + (row >> 3) * 8 * HD + i % (HD / 16) * 128 + (row & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      kv8_any(false);
+      if (t == 0) {
+        __threadfence_block();
+        *segs_ready = ++segs;
+      }
+    };
+    Kv8At at, next;
+    if (c0 < c1) {
+      locate(c0, next);
+      prepare(next, 0);
+    }
+    int odd = 0;
 #pragma unroll 1
-    for (int x = c0; x < c1;) {
-      Kv8At at;
-      locate(x, at);
+    for (int x = c0; x < c1; odd ^= 1) {
+      at = next;
       const int count = segment(x, at);
       int len;
       const int rows = item_of(at.e, len) * a.G;       // of queries
       bool poison = dead;
       int lacking = 0x7fffffff;                        // rows that see more positions are not known
-      int* sees = reinterpret_cast<int*>(sm + Cfg::kRows);
+      int nan_from = 0x7fffffff;                       // (GR) the same for this thread's dimension
+      const int* sees = sees0 + odd * HB;
       int least = 0x7fffffff;                          // positions that every row sees
-      // ---- q: scaled so that its largest element is in [2^7, 2^8), in six terms.  A warp takes every fourth head.
-      {
-        constexpr int V = HD / 32;
-        if (GR && t < HB) sees[t] = t < rows ? entry[at.e + t / a.G - base].y : 0;
-        constexpr int kMine = (HB + 3) / 4;            // rows of a warp: all on the way together
-        float z[kMine][V];
 #pragma unroll
-        for (int j = 0; j < kMine; j++) {
-          const int h = warp + 4 * j, sub = GR ? h / a.G : 0;
-          const float* qb = a.q + int64_t(at.e + sub) * a.q_stride + int64_t(at.g * a.G + h - sub * a.G) * HD + V * lane;
-#pragma unroll
-          for (int i = 0; i < V; i++) z[j][i] = 0.f;
-          if (h < rows) {
-            if (V == 4) {
-              const float4 w = *reinterpret_cast<const float4*>(qb);
-              z[j][0] = w.x; z[j][1] = w.y; z[j][2 % V] = w.z; z[j][3 % V] = w.w;
-            } else {
-              const float2 w = *reinterpret_cast<const float2*>(qb);
-              z[j][0] = w.x; z[j][1] = w.y;
-            }
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kMine; j++) {
-          const int h = warp + 4 * j;
-          if (h >= HB) break;
-          float (&y)[V] = z[j], top = 0.f;
-#pragma unroll
-          for (int i = 0; i < V; i++) {
-            y[i] *= a.scale;
-            if (!(fabsf(y[i]) < INFINITY)) y[i] = NAN;
-            top = fmaxf(top, fabsf(y[i]));             // (a NaN is passed over)
-          }
-#pragma unroll
-          for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          int ex = int(__float_as_uint(top) >> 23);
-          ex = ex < 14 ? 14 : ex;                      // (zeros and values below 2^-113)
-          const float up = __uint_as_float(uint32_t(261 - ex) << 23);                  // 2^(134 - ex)
-          if (lane == 0) red[h] = __uint_as_float(uint32_t(ex - 7) << 23);             // 2^(ex - 134)
-          uint8_t* to = sm + Cfg::kQ + (V * lane >> 4) * 128 + (V * lane & 15);
-#pragma unroll
-          for (int i = 0; i < V; i++) y[i] *= up;
-#pragma unroll
-          for (int k = 0; k < Cfg::kTerms; k++) {
-            const int row = k * HB + h;
-#pragma unroll
-            for (int i = 0; i < V; i += 2) {
-              const uint32_t w = kv8_code2(y[i], y[i + 1]);
-              *reinterpret_cast<uint16_t*>(to + (row >> 3) * 8 * HD + (row & 7) * 16 + i) = uint16_t(w);
-              const float2 f = kv8_value2(w);
-              y[i] = (y[i] - f.x) * 16.f;
-              y[i + 1] = (y[i + 1] - f.y) * 16.f;
-            }
-          }
-        }
-        if constexpr (Cfg::NS > Cfg::kTerms * HB)      // rows of no head
-          for (int i = t; i < (Cfg::NS - Cfg::kTerms * HB) * HD / 16; i += 128) {
-            const int row = Cfg::kTerms * HB + i / (HD / 16);
-            *reinterpret_cast<uint4*>(sm + Cfg::kQ + (row >> 3) * 8 * HD + i % (HD / 16) * 128 + (row & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        kv8_any(false);
-        if (t == 0) {
-          __threadfence_block();
-          *segs_ready = ++segs;
-        }
-#pragma unroll
-        for (int h = 0; h < HB; h++) {
-          cs[h] = red[h];
-          O[h] = l[h] = 0.f;
-          mref[h] = -3e38f;
-        }
-        if (GR)
-          for (int h = 0; h < rows; h++) least = min(least, sees[h]);
-        kv8_any(false);                                // red is read
+      for (int h = 0; h < HB; h++) {
+        cs[h] = scales[odd * HB + h];
+        O[h] = l[h] = 0.f;
+        mref[h] = -3e38f;
       }
+      if (GR)
+        for (int h = 0; h < rows; h++) least = min(least, sees[h]);
 #pragma unroll 1
       for (int i = 0; i < count; i++, no++) {
         if (dead) continue;
@@ -626,22 +658,32 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         const bool here = t < live;
         const int page = here ? t / P : 0, dv = 28 + exps[16 * page + 1] - vmax;
         const float fk = kv8_exp2i(exps[16 * page]), fv = dv < -126 ? 0.f : kv8_exp2i(dv);
-        if (live < kKv8Tile) {   // values behind the end: zeros, whatever the page holds there
+        const bool ends = GR && start + kKv8Tile > least;   // some rows end in this tile, or before it
+        if (live < kKv8Tile || ends) {
           const int vfill = 2 * no + 1;
           fail = !__all_sync(0xffffffffu, kv4_bar_wait(full + 8 * (vfill % H), uint32_t(vfill / H) & 1u)) || fail;
           uint8_t* v = sm + vfill % H * Cfg::kSlot;
-          if (t < HD)
-            for (int ch = live >> 4; ch < 8; ch++) {
+          if (t < HD) {
+            const int first = ends ? max(least - start, 0) : live;
+            for (int ch = first >> 4; ch < 8; ch++) {
               uint4* at16 = reinterpret_cast<uint4*>(v + kv8_v_at(HD, ch, t));
-              uint4 w = make_uint4(0u, 0u, 0u, 0u);
-              const int keep = live - 16 * ch;         // bytes that stay
-              if (keep > 0) {
-                w = *at16;
-                auto cut = [&](uint32_t z, int b) { return keep >= b + 4 ? z : keep <= b ? 0u : z & ((1u << (8 * (keep - b))) - 1u); };
-                w = make_uint4(cut(w.x, 0), cut(w.y, 4), cut(w.z, 8), cut(w.w, 12));
+              uint4 w4 = *at16;
+              uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+              for (int y = 0; y < 4; y++) {
+                const int p0 = 16 * ch + 4 * y, keep = live - p0;   // values behind the end: zeros, whatever the page holds there
+                if (GR && ends)                        // a value that is no number, which not every row sees: those that do are told
+#pragma unroll
+                  for (int b = 0; b < 4; b++)
+                    if (p0 + b >= first && b < keep && (w[y] >> (8 * b) & 0x7fu) == kKv8Nan) {
+                      nan_from = min(nan_from, start + p0 + b);
+                      w[y] &= ~(0xffu << (8 * b));
+                    }
+                w[y] = keep >= 4 ? w[y] : keep <= 0 ? 0u : w[y] & ((1u << (8 * keep)) - 1u);
               }
-              *at16 = w;
+              *at16 = make_uint4(w[0], w[1], w[2], w[3]);
             }
+          }
         }
         // ---- scores
         float s[HB];
@@ -673,7 +715,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         if (lane == 0) kv4_bar_arrive(bar_taken);
 #pragma unroll
         for (int h = 0; h < HB; h++) s[h] = here ? s[h] * fk : -INFINITY;
-        if (GR && start + kKv8Tile > least) {       // some rows end in this tile, or before it
+        if (ends) {
 #pragma unroll
           for (int h = 0; h < HB; h++)
             if (start + t >= sees[h]) s[h] = -INFINITY;
@@ -692,12 +734,12 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         weights();
         if (kv8_any(!(most <= 15.f) || fail)) {
           // A weight may have passed 2^3.9 (at first all are infinite): the maxima over the tile's positions.
+          {
+            float x[HB];
 #pragma unroll
-          for (int h = 0; h < HB; h++) {
-            float top = s[h];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (lane == 0) red[warp * HB + h] = top;
+            for (int h = 0; h < HB; h++) x[h] = s[h];
+            const float top = kv8_join(x, [](float u, float v) { return fmaxf(u, v); });
+            if (lane % (32 / HB) == 0) red[warp * HB + kv8_joined<HB>(lane)] = top;
           }
           dead = kv8_any(fail);
 #pragma unroll
@@ -732,26 +774,35 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         out_scale = kv8_exp2i(vmax - 19);              // digits are 2^-9 of themselves, weights 2^28
         pending = true;
       }
-      // ---- the segment's end
+      // ---- the segment's end, behind the next one's q
+      if (x + count < c1) {
+        locate(x + count, next);
+        prepare(next, odd ^ 1);
+      }
       if (!take() || dead) poison = true;
       float* sums = red + 4 * HB;
-#pragma unroll
-      for (int h = 0; h < HB; h++) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], o);
-        if (lane == 0) sums[warp * HB + h] = l[h];
+      {
+        const float sum = kv8_join(l, [](float u, float v) { return u + v; });
+        if (lane % (32 / HB) == 0) sums[warp * HB + kv8_joined<HB>(lane)] = sum;
       }
       poison = kv8_any(poison);
       const bool whole = !CL && at.ti == 0 && count == at.nt, begun = at.ti == 0;
       float* part = CL ? reinterpret_cast<float*>(sm) : part0 + (begun ? Cfg::kPart : 0);
+      float* to = whole ? a.out + int64_t(at.e) * a.out_stride + int64_t(at.g) * a.G * HD : part;
+      const int64_t next_entry = whole ? a.out_stride - int64_t(a.G - 1) * HD : HD;   // from an entry's last row to the next one's first
 #pragma unroll
-      for (int h = 0; h < HB; h++) {
+      for (int h = 0, n = 1; h < HB; h++, n++) {
         float sum = (sums[h] + sums[HB + h]) + (sums[2 * HB + h] + sums[3 * HB + h]);
         if (poison || (GR ? sees[h] > lacking : lacking != 0x7fffffff)) sum = NAN;
         if (h < rows) {
-          const int sub = GR ? h / a.G : 0;
-          float* to = whole ? a.out + int64_t(at.e + sub) * a.out_stride + int64_t(at.g * a.G + h - sub * a.G) * HD : part + h * HD;
+          if (GR && sees[h] > nan_from) O[h] = NAN;
           if (t < HD) to[t] = whole ? (sum == 0.f ? 0.f : O[h] / sum) : O[h];
+          if (GR && n == a.G) {
+            to += next_entry;
+            n = 0;
+          } else {
+            to += HD;
+          }
         }
         if (!whole && t == 0) reinterpret_cast<float2*>(part + HB * HD)[h] = make_float2(mref[h], sum);
       }
@@ -823,58 +874,59 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   }
 }
 
-// Items that were cut: block (y, head) merges what CTA c began, the y-th of those that left an item open, with what the next ones left, in
-// their order.
+// Items that were cut: block (x, y) merges rows y 8 / per .. of what CTA c began, the x-th of those that left an item open, with what the next
+// ones left, in their order; `per` warps a row.
 constexpr int kKv8MergeWarps = 8;
 template <int HD>
-__global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8AttnArgs a, int ctas, int part_floats, int rows) {
+__global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8AttnArgs a, int ctas, int part_floats, int rows, int per) {
   constexpr int V = HD / 32, NW = kKv8MergeWarps, NT = 32 * NW, kFew = 5;   // partial results of a warp on the way together
   __shared__ float s_o[NW][HD];
   __shared__ float2 s_ml[NW];
   __shared__ int s_count[NW];
   __shared__ int s_cta, s_item, s_members;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, h = blockIdx.y;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, h = int(blockIdx.y) * (NW / per) + warp / per, rank = warp % per;
   if (t == 0) s_cta = -1;
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (int(gridDim.x) >= ctas - 1) {   // as many blocks as CTAs: no need to count
     const int2 x = __ldcg(a.open + blockIdx.x);
     if (x.x < 0) return;
-    if (t == 0) { s_cta = int(blockIdx.x); s_item = x.x; s_members = x.y; }   
+    if (t == 0) { s_cta = int(blockIdx.x); s_item = x.x; s_members = x.y; }
     __syncthreads();
-  }
-  int before = 0;
-  for (int i0 = int(gridDim.x) >= ctas - 1 ? ctas : 0; i0 < ctas; i0 += NT) {
-    const int2 x = i0 + t < ctas ? __ldcg(a.open + i0 + t) : make_int2(-1, 0);
-    const uint32_t m = __ballot_sync(0xffffffffu, x.x >= 0);
-    if (lane == 0) s_count[warp] = __popc(m);
-    __syncthreads();
-    int mine = before;
+  } else {
+    int before = 0;
+    for (int i0 = 0; i0 < ctas; i0 += NT) {
+      const int2 x = i0 + t < ctas ? __ldcg(a.open + i0 + t) : make_int2(-1, 0);
+      const uint32_t m = __ballot_sync(0xffffffffu, x.x >= 0);
+      if (lane == 0) s_count[warp] = __popc(m);
+      __syncthreads();
+      int mine = before;
 #pragma unroll
-    for (int w = 0; w < NW; w++) {
-      if (w < warp) mine += s_count[w];
-      before += s_count[w];
+      for (int w = 0; w < NW; w++) {
+        if (w < warp) mine += s_count[w];
+        before += s_count[w];
+      }
+      if (x.x >= 0 && mine + __popc(m & ((1u << lane) - 1u)) == int(blockIdx.x)) {
+        s_cta = i0 + t;
+        s_item = x.x;
+        s_members = x.y;
+      }
+      __syncthreads();
+      if (before > int(blockIdx.x)) break;
     }
-    if (x.x >= 0 && mine + __popc(m & ((1u << lane) - 1u)) == int(blockIdx.x)) {
-      s_cta = i0 + t;
-      s_item = x.x;
-      s_members = x.y;
-    }
-    __syncthreads();
   }
   if (s_cta < 0) return;
-  const int members = s_members & 0xffff;
-  if (h >= (s_members >> 16) * a.G) return;            // (the item has fewer entries)
-  const float* first = a.part + (int64_t(s_cta) * 2 + 1) * part_floats;   // the second of this CTA, then the first of the next ones
+  const int members = s_members & 0xffff, all = (s_members >> 16) * a.G;   // rows of the item
+  const float* first = a.part + (int64_t(s_cta) * 2 + 1) * part_floats;    // the second of this CTA, then the first of the next ones
   float M = -INFINITY, sum = 0.f, o[V];
 #pragma unroll
   for (int v = 0; v < V; v++) o[v] = 0.f;
-  for (int b0 = warp; b0 < members; b0 += kFew * NW) {
+  for (int b0 = rank; b0 < members && h < all; b0 += kFew * per) {
     float2 ml[kFew];
     float x[kFew][V];
 #pragma unroll
     for (int u = 0; u < kFew; u++) {
-      const int b = b0 + u * NW;
+      const int b = b0 + u * per;
       if (b >= members) break;
       const float* r = b ? first + (int64_t(b) * 2 - 1) * part_floats : first;
       ml[u] = __ldcg(reinterpret_cast<const float2*>(r + rows * HD) + h);
@@ -883,7 +935,7 @@ __global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8Att
     }
 #pragma unroll
     for (int u = 0; u < kFew; u++) {
-      if (b0 + u * NW >= members) break;
+      if (b0 + u * per >= members) break;
       const float to = fmaxf(M, ml[u].x), was = kv8_ex2(M - to), f = kv8_ex2(ml[u].x - to);
       M = to;
       sum = fmaf(sum, was, ml[u].y * f);
@@ -895,18 +947,19 @@ __global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8Att
   for (int v = 0; v < V; v++) s_o[warp][32 * v + lane] = o[v];
   if (lane == 0) s_ml[warp] = make_float2(M, sum);
   __syncthreads();
-  if (t < HD) {
+  const int e0 = s_item / c.n_kv, g = s_item % c.n_kv;
+  for (int i = t; i < NW / per * HD; i += NT) {
+    const int j = i / HD, d = i % HD, row = int(blockIdx.y) * (NW / per) + j;
+    if (row >= all) break;
     float top = -INFINITY, total = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; w++) top = fmaxf(top, s_ml[w].x);
-#pragma unroll
-    for (int w = 0; w < NW; w++) {
+    for (int w = j * per; w < (j + 1) * per; w++) top = fmaxf(top, s_ml[w].x);
+    for (int w = j * per; w < (j + 1) * per; w++) {
       const float f = kv8_ex2(s_ml[w].x - top);
       total = fmaf(s_ml[w].y, f, total);
-      y = fmaf(s_o[w][t], f, y);
+      y = fmaf(s_o[w][d], f, y);
     }
-    const int sub = h / a.G, e = s_item / c.n_kv + sub, g = s_item % c.n_kv;
-    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + h - sub * a.G) * HD + t] = total == 0.f ? 0.f : y / total;
+    const int sub = row / a.G;
+    a.out[int64_t(e0 + sub) * a.out_stride + (int64_t(g) * a.G + row - sub * a.G) * HD + d] = total == 0.f ? 0.f : y / total;
   }
 }
 
@@ -982,8 +1035,12 @@ static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t i
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, false, GR>, k, a);
   if (e != cudaSuccess || ctas < 2) return e;
   // (the last CTA's items end with it)
-  kv8_config(cfg, attr, dim3(unsigned(ctas - 1 < items ? ctas - 1 : items), unsigned(a.R * a.G)), 32 * kKv8MergeWarps, 0, s, 0);
-  return cudaLaunchKernelEx(&cfg, k_kv8_merge<HD>, k, a, int(ctas), int(Cfg::kPart), HB);
+  // a warp per row where there are many rows, up to a block's eight where there are few
+  const int64_t cuts = ctas - 1 < items ? ctas - 1 : items, rows = a.R * a.G;
+  int per = kKv8MergeWarps;
+  while (per > 1 && cuts * ((rows * per + kKv8MergeWarps - 1) / kKv8MergeWarps) > 4 * setup.sms) per /= 2;
+  kv8_config(cfg, attr, dim3(unsigned(cuts), unsigned((rows * per + kKv8MergeWarps - 1) / kKv8MergeWarps)), 32 * kKv8MergeWarps, 0, s, 0);
+  return cudaLaunchKernelEx(&cfg, k_kv8_merge<HD>, k, a, int(ctas), int(Cfg::kPart), HB, per);
 }
 
 template <int HD>
@@ -1045,7 +1102,7 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
   a.G = G;
   a.k = n_select;
   // Entries of one sequence share items where the call says that there may be some: it lists sequences, and how much of them is seen.
-  a.R = dev_seq && dev_ctx && !n_select ? kKv8MaxGroup / G : 1;
+  a.R = dev_seq && dev_ctx && !n_select ? (G <= 4 ? 8 : 16) / G : 1;
   if (a.R > n) a.R = n;
   while (192 % a.R) a.R--;                             // (a round of the kernel's threads holds whole items)
   a.q_stride = q_stride;

@@ -506,6 +506,26 @@ def test_a_missing_page_concerns_the_entries_that_see_it(nt):
             assert (np.abs(got[i] - parts[0]) <= bound(parts, len(k), np.abs(v).max() if c else 0)).all(), (longest, i)
 
 
+def test_a_value_that_is_no_number_concerns_the_entries_that_see_it(nt):
+    import torch
+    rng = np.random.default_rng(31)
+    for hd, heads in ((128, 2), (64, 8)):
+        ref = R.RefCache(1, 1, hd, 32, 20, 1, 20)
+        ref.randomize(rng)
+        ref.hold([300], rng)
+        for pos, d in ((290, 5), (293, 60), (130, 7)):
+            ref.pool[0, ref.table[0, pos // 32]][ref.v_at(0, pos % 32, d)] = 0xFF
+        ref.pool[0, ref.table[0, 296 // 32]][ref.k_at(0, 296 % 32, 3)] = 0x7F
+        ctx = [297, 290, 291, 294, 130, 131, 296, 295, 300, 0, 128]
+        q = rng.standard_normal((len(ctx), heads, hd)).astype(np.float32)
+        got = Dev(nt, ref, heads, len(ctx)).attention(torch.from_numpy(q).cuda(), [0] * len(ctx), ctx).cpu().numpy()
+        for i, c in enumerate(ctx):
+            nan = {d for pos, d in ((290, 5), (293, 60), (130, 7)) if pos < c}
+            if c > 296:
+                nan = set(range(hd))
+            assert {int(d) for d in np.nonzero(np.isnan(got[i, 0]))[0]} == nan, (hd, c)
+
+
 def test_strides_and_layers(nt):
     import torch
     rng = np.random.default_rng(14)
