@@ -83,8 +83,10 @@ struct Kv8AttnCfg {
   static constexpr int kSegs = kTmem + 4;                           // items whose q is there
   static constexpr int kSmem = kTmem + 16;
   static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
-  static constexpr int kColS = 0, kColO = NS, kCols = NS + NP <= 32 ? 32 : NS + NP <= 64 ? 64 : NS + NP <= 128 ? 128 : 256;
-  static_assert(NS + NP <= 256, "tensor memory of two CTAs");
+  // tensor memory: scores; outputs, twice where there is room, so that a tile's are taken while the next one's are formed
+  static constexpr int kOuts = HB <= 8 ? 2 : 1, kUsed = NS + kOuts * NP;
+  static constexpr int kColS = 0, kColO = NS, kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
+  static_assert(kUsed <= 256, "tensor memory of two CTAs");
 };
 
 // ------------------------------------------------------------ small pieces --
@@ -206,7 +208,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   const volatile uint32_t* tensor_memory = reinterpret_cast<const volatile uint32_t*>(sm + Cfg::kTmem);
   const uint32_t full = smu + Cfg::kBars, empty = full + 8 * H, bar_s = empty + 8 * H, bar_taken = bar_s + 8,
                  bar_p = bar_taken + 8, bar_o = bar_p + 8;
-  const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31, n = a.n, P = c.page_len;
+  const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31, n = a.n, P = c.page_len, lg = 31 - __clz(P);
 
   if (t == 0) {
     for (int i = 0; i < H; i++) {
@@ -230,9 +232,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   }
   // ---- first tiles of all entries
   auto tiles = [&](int len) {   // of an item whose entry sees len positions
-    int64_t x = (int64_t(len) + P - 1) / P;
-    if (a.k && x > a.k) x = a.k;
-    return a.k ? int((x * P + kKv8Tile - 1) / kKv8Tile) : int((int64_t(len) + kKv8Tile - 1) / kKv8Tile);
+    uint32_t x = uint32_t(len);                        // (at most 2^31 - 256)
+    if (a.k) x = min((x + P - 1) >> lg, uint32_t(a.k)) << lg;
+    return int((x + kKv8Tile - 1) / kKv8Tile);
   };
   // entries are kept from `base` on: CL: the item's only
   const int base = CL ? int(blockIdx.y) / c.n_kv : 0, R = GR ? a.R : 1;
@@ -342,7 +344,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     item_of(lo, len);
     at.nt = tiles(len);
     const int r = x - prefix[lo];
-    at.g = r / at.nt;
+    at.g = int(uint32_t(r) / uint32_t(at.nt));
     at.ti = r - at.g * at.nt;
   };
   auto segment = [&](int x, const Kv8At& at) { return at.nt - at.ti < c1 - x ? at.nt - at.ti : c1 - x; };   // tiles up to the item's or the CTA's end
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     // ---- copies.  Lane y knows the page at place first + y of the item's list; the next 32 are looked up a batch ahead.
     const Kv8Page L(c);
     const uint8_t* layer_pool = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes();
-    const int per = kKv8Tile / P, codes = P * HD;
+    const int per = kKv8Tile >> lg, codes = P * HD;
     int no = 0, begun = 0;                             // tiles; slots filled
     bool dead = false;
     for (int x = c0; x < c1 && !dead;) {
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       const int count = segment(x, at);
       int len;
       item_of(at.e, len);
-      const int m = int((int64_t(len) + P - 1) / P), listed = a.k && a.k < m ? a.k : m;
+      const int m = int((uint32_t(len) + P - 1) >> lg), listed = a.k && a.k < m ? a.k : m;
       const int32_t* row = c.table + int64_t(entry[at.e - base].x) * c.max_pages;
       const int32_t* list = a.k ? a.pages + (int64_t(at.e) * c.n_kv + at.g) * a.k : nullptr;
       const int end = (at.ti + count) * per < listed ? (at.ti + count) * per : listed;
@@ -432,6 +434,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     constexpr uint32_t kIdescS = kIdesc | uint32_t(Cfg::NS / 8) << 17, kIdescO = kIdesc | uint32_t(Cfg::NP / 8) << 17 | 1u << 16;   // P^T: rows side by side
     const int all = c1 - c0;
     int ns = 0, np = 0, weighed = 0, segs = 0, left = 0, idle = 0;   // left: tiles of the segment without scores
+    bool has_k = false, has_v = false;                 // tile ns has its K, tile np its V
     while (np < all) {
       bool moved = false;
       if (ns < all && ns - np < E - 1) {
@@ -446,7 +449,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             segs++;
           }
         }
-        if (ok && kv8_bar_test(full + 8 * slot, uint32_t(2 * ns / H) & 1u) && (ns == 0 || kv8_bar_test(bar_taken, uint32_t(ns - 1) & 1u))) {
+        if (!has_k) has_k = kv8_bar_test(full + 8 * slot, uint32_t(2 * ns / H) & 1u);
+        if (ok && has_k && (ns == 0 || kv8_bar_test(bar_taken, uint32_t(ns - 1) & 1u))) {
           if (info[ns % E] & (Cfg::kLacks - 1)) {
             kv8_tc_after();
             if (kv8_elect()) {
@@ -462,6 +466,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             kv4_bar_arrive(empty + 8 * slot);
           }
           __syncwarp();
+          has_k = false;
           ns++;
           left--;
           moved = true;
@@ -469,11 +474,13 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       }
       if (np < ns) {
         const int fill = 2 * np + 1, slot = fill % H;
-        if (kv8_bar_test(full + 8 * slot, uint32_t(fill / H) & 1u)) {
+        if (!has_v) has_v = kv8_bar_test(full + 8 * slot, uint32_t(fill / H) & 1u);
+        if (has_v) {
           if (!(info[np % E] & (Cfg::kLacks - 1))) {                     // free once the softmax warps have seen that there is nothing
             if (ns > np + 1 || kv8_bar_test(bar_taken, uint32_t(np) & 1u)) {
               if (lane == 0) kv4_bar_arrive(empty + 8 * slot);
               __syncwarp();
+              has_v = false;
               np++;
               moved = true;
             }
@@ -483,12 +490,13 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
               const uint32_t v0 = smu + slot * Cfg::kSlot, p0 = smu + Cfg::kP;
 #pragma unroll
               for (int kk = 0; kk < kKv8Tile / 32; kk++)
-                kv8_mma(tmem + Cfg::kColO, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
+                kv8_mma(tmem + Cfg::kColO + weighed % Cfg::kOuts * Cfg::NP, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
                         kv8_desc(p0 + kk * 4 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
               kv8_commit(bar_o);
               kv8_commit(empty + 8 * slot);
             }
             __syncwarp();
+            has_v = false;
             weighed++;
             np++;
             moved = true;
@@ -509,23 +517,31 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     float O[HB], l[HB], mref[HB], cs[HB];
     uint32_t ps = 0, po = 0;
     int no = 0, segs = 0;                              // tiles; items whose q was prepared
-    bool dead = false, pending = false;
-    float out_scale = 0.f;                             // of the outputs under way
-
-    constexpr int kTake = HB < 4 ? HB : 4;             // heads taken together
-    auto take = [&]() -> bool {                        // adds them to the sums; false: they never came
-      if (!pending) return true;
-      pending = false;
+    bool dead = false;
+    // outputs of the last tile with scores: none under way, under way, there; their scale, and which of the columns
+    int pending = 0, taken = 0;
+    float out_scale = 0.f;
+    auto await = [&]() -> bool {                       // false: they never came
+      if (pending != 1) return true;
+      pending = 2;
       const bool ok = __all_sync(0xffffffffu, kv4_bar_wait(bar_o, po));
       po ^= 1u;
       kv8_tc_after();
+      return ok;
+    };
+    constexpr int kTake = HB < 4 ? HB : 4;             // heads taken together
+    auto take = [&]() {                                // adds them to the sums
+      if (pending != 2) return;
+      pending = 0;
+      const uint32_t from = tmem + mine + Cfg::kColO + taken % Cfg::kOuts * Cfg::NP;
+      taken++;
       if (HD == 128 || warp < 2) {
         const uint64_t k16 = kv8_pack(16.f, 16.f), k65536 = kv8_pack(65536.f, 65536.f);
 #pragma unroll
         for (int b = 0; b < HB / kTake; b++) {
           uint32_t r[8 * kTake];
 #pragma unroll
-          for (int y = 0; y < kTake / 2; y++) kv8_tc_ld16(tmem + mine + Cfg::kColO + 8 * kTake * b + 16 * y, r + 16 * y);
+          for (int y = 0; y < kTake / 2; y++) kv8_tc_ld16(from + 8 * kTake * b + 16 * y, r + 16 * y);
           kv8_tc_wait(r);
 #pragma unroll
           for (int h = 0; h < kTake; h++) {            // a head's digits 0, 2, 4, 6, 1, 3, 5, 7
@@ -536,7 +552,6 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         }
       }
       kv8_tc_before();
-      return ok;
     };
 
     // The q of the item at `at` into shared memory, scaled so that its largest element is in [2^7, 2^8), in six terms; a warp takes every fourth
@@ -652,12 +667,6 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           continue;
         }
         kv8_tc_after();
-        const int8_t* exps = reinterpret_cast<const int8_t*>(sm + Cfg::kExps + no % E * 8 * 16);
-        int vmax = -128;
-        for (int y = 0; y * P < live; y++) vmax = max(vmax, int(exps[16 * y + 1]));
-        const bool here = t < live;
-        const int page = here ? t / P : 0, dv = 28 + exps[16 * page + 1] - vmax;
-        const float fk = kv8_exp2i(exps[16 * page]), fv = dv < -126 ? 0.f : kv8_exp2i(dv);
         const bool ends = GR && start + kKv8Tile > least;   // some rows end in this tile, or before it
         if (live < kKv8Tile || ends) {
           const int vfill = 2 * no + 1;
@@ -685,23 +694,36 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             }
           }
         }
-        // ---- scores
-        float s[HB];
+        // ---- scores; while they come, the exponents of the tile's pages: this position's key's and value's, the largest value's
+        float s[HB], fk, fv;
+        int vmax;
         {
-          constexpr int kCols = HB == 16 ? 48 : Cfg::NS;   // three terms at a time with 16 heads, all otherwise
+          constexpr int kParts = HB == 16 ? 2 : 1, kCols = Cfg::NS / kParts, kT = Cfg::kTerms / kParts;   // with 16 heads three terms at a time
+          const int8_t* exps = reinterpret_cast<const int8_t*>(sm + Cfg::kExps + no % E * 8 * 16);
 #pragma unroll
-          for (int b = Cfg::NS / kCols - 1; b >= 0; b--) {
+          for (int b = kParts - 1; b >= 0; b--) {
             uint32_t r[kCols];
 #pragma unroll
             for (int y = 0; y < kCols / 16; y++) kv8_tc_ld16(tmem + mine + Cfg::kColS + b * kCols + 16 * y, r + 16 * y);
+            if (b == kParts - 1) {
+              const int of = t < live ? t >> lg : 0, ek = exps[16 * of], ev = exps[16 * of + 1];
+              vmax = __reduce_max_sync(0xffffffffu, (lane & 7) << lg < live ? int(exps[16 * (lane & 7) + 1]) : -128);
+              const int dv = 28 + ev - vmax;
+              fk = kv8_exp2i(ek);
+              fv = dv < -126 ? 0.f : kv8_exp2i(dv);
+            }
             kv8_tc_wait(r);
-            constexpr int kT = HB == 16 ? 3 : Cfg::kTerms;
+            if (b == 0) {
+              kv8_tc_before();
+              __syncwarp();
+              if (lane == 0) kv4_bar_arrive(bar_taken);
+            }
             const uint64_t k16th = kv8_pack(1.f / 16.f, 1.f / 16.f);
 #pragma unroll
             for (int h = 0; h < HB; h += 2) {
               auto two = [&](int k) { return kv8_pack(__uint_as_float(r[k * HB + h]), __uint_as_float(r[k * HB + h + 1])); };
               uint64_t z = two(kT - 1);
-              if (HB == 16 && b == 0) z = kv8_fma2(kv8_pack(s[h], s[h + 1]), k16th, z);
+              if (b < kParts - 1) z = kv8_fma2(kv8_pack(s[h], s[h + 1]), k16th, z);
 #pragma unroll
               for (int k = kT - 2; k >= 0; k--) z = kv8_fma2(z, k16th, two(k));
               const float2 y = kv8_unpack(z);
@@ -710,17 +732,13 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             }
           }
         }
-        kv8_tc_before();
-        __syncwarp();
-        if (lane == 0) kv4_bar_arrive(bar_taken);
 #pragma unroll
-        for (int h = 0; h < HB; h++) s[h] = here ? s[h] * fk : -INFINITY;
+        for (int h = 0; h < HB; h++) s[h] = t < live ? s[h] * fk : -INFINITY;
         if (ends) {
 #pragma unroll
           for (int h = 0; h < HB; h++)
             if (start + t >= sees[h]) s[h] = -INFINITY;
         }
-        fail = !take() || fail;
         // ---- weights
         float p[HB], most;
         auto weights = [&]() {
@@ -734,6 +752,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         weights();
         if (kv8_any(!(most <= 15.f) || fail)) {
           // A weight may have passed 2^3.9 (at first all are infinite): the maxima over the tile's positions.
+          fail = !await() || fail;
+          take();
           {
             float x[HB];
 #pragma unroll
@@ -756,6 +776,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           }
           weights();
         }
+        if (!await()) poison = true;                   // (the last tile's products have read the weights before)
+        if (Cfg::kOuts == 1) take();
 #pragma unroll
         for (int h = 0; h < HB; h += 2) {
           uint32_t u[2];
@@ -771,15 +793,17 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         kv8_tc_before();
         __syncwarp();
         if (lane == 0) kv4_bar_arrive(bar_p);
+        take();
         out_scale = kv8_exp2i(vmax - 19);              // digits are 2^-9 of themselves, weights 2^28
-        pending = true;
+        pending = 1;
       }
       // ---- the segment's end, behind the next one's q
       if (x + count < c1) {
         locate(x + count, next);
         prepare(next, odd ^ 1);
       }
-      if (!take() || dead) poison = true;
+      if (!await() || dead) poison = true;
+      take();
       float* sums = red + 4 * HB;
       {
         const float sum = kv8_join(l, [](float u, float v) { return u + v; });
@@ -788,29 +812,34 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       poison = kv8_any(poison);
       const bool whole = !CL && at.ti == 0 && count == at.nt, begun = at.ti == 0;
       float* part = CL ? reinterpret_cast<float*>(sm) : part0 + (begun ? Cfg::kPart : 0);
-      float* to = whole ? a.out + int64_t(at.e) * a.out_stride + int64_t(at.g) * a.G * HD : part;
+      if (t < HB) {                                    // what row t's outputs are multiplied by
+        float sum = (sums[t] + sums[HB + t]) + (sums[2 * HB + t] + sums[3 * HB + t]);
+        if (poison || (GR ? sees[t] > lacking : lacking != 0x7fffffff)) sum = NAN;
+        red[t] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+        if (!whole) part[HB * HD + 2 * t + 1] = sum;
+      }
+      if (!whole && t == 0) {
+#pragma unroll
+        for (int h = 0; h < HB; h++) part[HB * HD + 2 * h] = mref[h];
+      }
+      kv8_any(false);
+      float* to = (whole ? a.out + int64_t(at.e) * a.out_stride + int64_t(at.g) * a.G * HD : part) + t;
       const int64_t next_entry = whole ? a.out_stride - int64_t(a.G - 1) * HD : HD;   // from an entry's last row to the next one's first
 #pragma unroll
       for (int h = 0, n = 1; h < HB; h++, n++) {
-        float sum = (sums[h] + sums[HB + h]) + (sums[2 * HB + h] + sums[3 * HB + h]);
-        if (poison || (GR ? sees[h] > lacking : lacking != 0x7fffffff)) sum = NAN;
-        if (h < rows) {
-          if (GR && sees[h] > nan_from) O[h] = NAN;
-          if (t < HD) to[t] = whole ? (sum == 0.f ? 0.f : O[h] / sum) : O[h];
-          if (GR && n == a.G) {
-            to += next_entry;
-            n = 0;
-          } else {
-            to += HD;
-          }
+        if (GR && sees[h] > nan_from) O[h] = NAN;
+        if (h < rows && t < HD) *to = O[h] * red[h];
+        if (GR && n == a.G) {
+          to += next_entry;
+          n = 0;
+        } else {
+          to += HD;
         }
-        if (!whole && t == 0) reinterpret_cast<float2*>(part + HB * HD)[h] = make_float2(mref[h], sum);
       }
       x += count;
       // the CTA's last item is open where it was begun here and goes on behind
       if (!CL && x >= c1 && t == 0)
         a.open[blockIdx.x] = begun && !whole ? make_int2(at.e * c.n_kv + at.g, ((x - count + at.nt - 1) / share - int(blockIdx.x) + 1) | (GR ? rows / a.G : 1) << 16) : make_int2(-1, 0);
-      kv8_any(false);                                  // the sums are read
     }
     if (!CL) {
       if (c0 >= c1 && t == 0) a.open[blockIdx.x] = make_int2(-1, 0);
