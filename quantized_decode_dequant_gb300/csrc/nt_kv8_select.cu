@@ -11,7 +11,8 @@
 namespace nt {
 
 struct Kv8SelectArgs {
-  int32_t layer, n, G, k, first, last, splits;
+  int32_t layer, n, G, k, first, last;
+  int32_t seq0;         // sequence of entry 0 where none are listed
   const int32_t* seq;
   const int32_t* ctx;
   const float* q;
@@ -24,8 +25,8 @@ __host__ __device__ __forceinline__ int64_t kv8_key_stride(const Kv4& k) { retur
 size_t kv8_select_ws_bytes(const Kv4& k, int64_t n) { return size_t(n) * k.n_kv * kv8_key_stride(k) * 4; }
 
 // Sequence of entry i and the positions that it sees (-1: cannot be read, the bit in *bad).
-__device__ __forceinline__ int2 kv8_entry(const Kv4& c, const int32_t* seq, const int32_t* ctx, int i, uint32_t* bad) {
-  const int s = seq ? seq[i] : i;
+__device__ __forceinline__ int2 kv8_entry(const Kv4& c, const int32_t* seq, const int32_t* ctx, int seq0, int i, uint32_t* bad) {
+  const int s = seq ? seq[i] : seq0 + i;
   *bad = NT_KV4_BAD_SEQ;
   if (s < 0 || s >= c.max_seqs) return make_int2(-1, 0);
   const int len = c.len[s], n = ctx ? ctx[i] : len;
@@ -33,143 +34,21 @@ __device__ __forceinline__ int2 kv8_entry(const Kv4& c, const int32_t* seq, cons
   return make_int2(*bad ? -1 : s, *bad ? 0 : n);
 }
 
-constexpr int kKv8ScoreThreads = 256;
+constexpr int kKv8SelectThreads = 256;
 constexpr int kKv8ScorePages = 16;   // of a warp at a time
-
-// Keys of the pages of (entry, kv head) blockIdx.x / a.splits: whole numbers in the order of the scores.  A warp takes 16
-// pages at a time, eight lanes each; their places in the pool are looked up a round ahead.
-template <int HD>
-__global__ void __launch_bounds__(kKv8ScoreThreads) k_kv8_scores(Kv4 c, Kv8SelectArgs a) {
-  constexpr int NT = kKv8ScoreThreads, NW = NT / 32, kRun = 16, kRuns = 2 * HD / (8 * kRun);   // runs of 16 bounds of a lane: hd 128: one of lo, one of hi
-  __shared__ __align__(16) int16_t s_w[2 * HD];           // for lo: sums of the negative w; for hi: of the positive ones
-  __shared__ float s_top[NW];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int64_t item = blockIdx.x / a.splits;
-  const int split = int(blockIdx.x % a.splits), i = int(item / c.n_kv), g = int(item % c.n_kv);
-  kv4_dependent();
-  uint32_t bad;
-  const int2 e = kv8_entry(c, a.seq, a.ctx, i, &bad);
-  if (bad) {
-    if (t == 0 && split == 0) kv4_flag(c, bad);
-    return;
-  }
-  const int m = (int64_t(e.y) + c.page_len - 1) / c.page_len;
-  if (m <= a.k) return;
-  const int32_t* row = c.table + int64_t(e.x) * c.max_pages;
-  auto look = [&](int j0) { return lane < kKv8ScorePages && j0 + lane < m ? row[j0 + lane] : 0; };
-  const int step = a.splits * NW * kKv8ScorePages;
-  int j0 = (split * NW + warp) * kKv8ScorePages, page = j0 < m ? look(j0) : 0;
-  // ---- the weights of the group's queries
-  const float* q = a.q + int64_t(i) * a.q_stride + int64_t(g) * a.G * HD;
-  float top = 0.f;
-  for (int x = t; x < a.G * HD; x += NT) {
-    const float y = fabsf(q[x]);
-    if (y < INFINITY) top = fmaxf(top, y);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (lane == 0) s_top[warp] = top;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < NW; w++) top = fmaxf(top, s_top[w]);
-  // 63 is 1.96875 2^5: f = exponent - 5, one more above 1.96875
-  int f = 0;
-  if (top > 0.f) {
-    const float up = top < 0x1p-100f ? top * 0x1p60f : top;
-    const uint32_t b = __float_as_uint(up);
-    f = int(b >> 23) - 132 + ((b & 0x7fffffu) > 0x7c0000u) - (top < 0x1p-100f ? 60 : 0);
-  }
-  if (t < HD) {
-    int pos = 0, neg = 0;
-    for (int h = 0; h < a.G; h++) {
-      const float x = q[h * HD + t];
-      int w = 0;
-      if (fabsf(x) < INFINITY) w = __float2int_rn(scalbnf(x, -f));
-      else if (x == x) w = x > 0.f ? 63 : -63;
-      if (w > 0) pos += w; else neg += w;
-    }
-    s_w[t] = int16_t(neg);
-    s_w[HD + t] = int16_t(pos);
-  }
-  __syncthreads();
-  const int sub = lane & 7, of = lane >> 3;               // this lane's part of page `of` of four
-  int w[kRuns][kRun / 2];
-#pragma unroll
-  for (int r = 0; r < kRuns; r++)
-#pragma unroll
-    for (int y = 0; y < kRun / 2; y++) w[r][y] = reinterpret_cast<const int*>(s_w)[(r * 8 + sub) * (kRun / 2) + y];
-  const Kv8Page L(c);
-  const uint8_t* heads = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes() + L.exps(g);
-  uint32_t* keys = a.keys + item * kv8_key_stride(c);
-  for (; j0 < m; j0 += step) {
-    const int next = j0 + step < m ? look(j0 + step) : 0;
-    const bool there = lane < kKv8ScorePages && j0 + lane < m, good = page >= 0 && page < c.n_pages;
-    if (there && !good) kv4_flag(c, NT_KV4_BAD_PAGE);
-    if (!good) page = -1;
-    uint4 b[kKv8ScorePages / 4][kRuns];
-#pragma unroll
-    for (int y = 0; y < kKv8ScorePages / 4; y++) {
-      const int p = __shfl_sync(0xffffffffu, page, 4 * y + of);
-#pragma unroll
-      for (int r = 0; r < kRuns; r++) {
-        b[y][r] = make_uint4(0u, 0u, 0u, 0u);
-        if (p >= 0 && j0 + 4 * y + of < m) b[y][r] = *reinterpret_cast<const uint4*>(heads + p * c.page_bytes() + 16 + (r * 8 + sub) * kRun);
-      }
-    }
-    int ex = 0;
-    if (there && page >= 0) ex = *reinterpret_cast<const int8_t*>(heads + page * c.page_bytes());
-    int mine = 0;                                         // the sum of this lane's page
-#pragma unroll
-    for (int y = 0; y < kKv8ScorePages / 4; y++) {
-      int sum = 0;
-#pragma unroll
-      for (int r = 0; r < kRuns; r++) {
-        const uint32_t u[4] = {b[y][r].x, b[y][r].y, b[y][r].z, b[y][r].w};
-#pragma unroll
-        for (int z = 0; z < 4; z++) {
-          sum = __dp2a_lo(w[r][2 * z], int(u[z]), sum);
-          sum = __dp2a_hi(w[r][2 * z + 1], int(u[z]), sum);
-        }
-      }
-#pragma unroll
-      for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      sum = __shfl_sync(0xffffffffu, sum, 8 * (lane & 3));
-      if (lane >> 2 == y) mine = sum;
-    }
-    if (there) {
-      const int j = j0 + lane;
-      const uint32_t z = __float_as_uint(float(mine) * kv8_exp2i(ex)), key = z >> 31 ? ~z : z | 0x80000000u;
-      keys[j] = j < a.first || j >= m - a.last ? 0xffffffffu : key;   // (no score has the key 0xffffffff)
-    }
-    page = next;
-  }
-}
-
-constexpr int kKv8PickThreads = 256;
 constexpr int kKv8PickBins = 1024;
 
-// The places of the a.k largest keys of (entry, kv head) blockIdx.x, the lower place first among equals, ascending.  A thread has 16
+// The places of the a.k largest of an item's m keys, the lower place first among equals, ascending, by a whole CTA.  A thread has 16
 // keys, in its registers where there are no more than 4096.  The a.k-th largest is found by counting keys in 1024 bins of
 // equal width between the least and the largest, then in the bin where it lies, and so on; as soon as all keys of
 // that bin are wanted they and those above are the choice.  (Bins of the keys' upper bits, which few scores differ in, had all
 // threads count in the same few: 8.7 us for 2049 keys; candidates bit by bit with a count of all keys each: 12.5.)
-__global__ void __launch_bounds__(kKv8PickThreads) k_kv8_pick(Kv4 c, Kv8SelectArgs a) {
-  constexpr int NT = kKv8PickThreads, NW = NT / 32, R = 16, kChunk = R * NT, kBins = kKv8PickBins, kOwn = kBins / NT;
+__device__ __forceinline__ void kv8_pick(const uint32_t* keys, int m, int k, int32_t* out) {
+  constexpr int NT = kKv8SelectThreads, NW = NT / 32, R = 16, kChunk = R * NT, kBins = kKv8PickBins, kOwn = kBins / NT;
   __shared__ int s_bins[kBins];
   __shared__ uint32_t s_part[3][NW];
   __shared__ int s_bin, s_left, s_in;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int64_t item = blockIdx.x;
-  kv4_dependent();
-  uint32_t bad;
-  const int2 e = kv8_entry(c, a.seq, a.ctx, int(item / c.n_kv), &bad);
-  const int m = (int64_t(e.y) + c.page_len - 1) / c.page_len;
-  int32_t* out = a.out + item * a.k;
-  if (m <= a.k) {
-    for (int j = t; j < a.k; j += NT) out[j] = j < m ? j : -1;
-    return;
-  }
-  const uint32_t* keys = a.keys + item * kv8_key_stride(c);
   constexpr uint32_t kAlways = 0xffffffffu;
   uint32_t key[R];
   auto get = [&](int j0) {                               // keys j0 + 16 t ..
@@ -209,8 +88,8 @@ __global__ void __launch_bounds__(kKv8PickThreads) k_kv8_pick(Kv4 c, Kv8SelectAr
   }
   // keys from `base` on, 2^width of them, are looked at; those above are taken, `left` of these are
   uint32_t base = least;
-  int width = 32 - __clz(most - least), left = a.k - int(always);
-  bool found = left == 0;                                // (m > a.k: there are others)
+  int width = 32 - __clz(most - least), left = k - int(always);
+  bool found = left == 0;                                // (m > k: there are others)
   if (found) base = kAlways;
   while (!found && width > 0) {
     const int shift = width > 10 ? width - 10 : 0;
@@ -296,6 +175,121 @@ __global__ void __launch_bounds__(kKv8PickThreads) k_kv8_pick(Kv4 c, Kv8SelectAr
   }
 }
 
+// A cluster per (entry, kv head): its CTAs share out the pages' scores, the first one picks.  Keys are whole numbers in the order of the scores.  A
+// warp takes 16 pages at a time, eight lanes each; their places in the pool are looked up a round ahead.  (As two launches, with
+// the same code: 1 x 131k 8.5 us, 24 x 30k 16.3.)
+template <int HD>
+__global__ void __launch_bounds__(kKv8SelectThreads) k_kv8_select(Kv4 c, Kv8SelectArgs a) {
+  constexpr int NT = kKv8SelectThreads, NW = NT / 32, kRun = 16, kRuns = 2 * HD / (8 * kRun);   // runs of 16 bounds of a lane: hd 128: one of lo, one of hi
+  __shared__ __align__(16) int16_t s_w[2 * HD];           // for lo: sums of the negative w; for hi: of the positive ones
+  __shared__ float s_top[NW];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int64_t item = blockIdx.y;
+  const int split = int(blockIdx.x), splits = int(gridDim.x), i = int(item / c.n_kv), g = int(item % c.n_kv);
+  kv4_dependent();
+  // the queries are on the way while the entry is looked up
+  const float* q = a.q + int64_t(i) * a.q_stride + int64_t(g) * a.G * HD;
+  float top = 0.f;
+  for (int x = 4 * t; x < a.G * HD; x += 4 * NT) {
+    const float4 y = *reinterpret_cast<const float4*>(q + x);
+    auto size = [](float z) { return fabsf(z) < INFINITY ? fabsf(z) : 0.f; };
+    top = fmaxf(top, fmaxf(fmaxf(size(y.x), size(y.y)), fmaxf(size(y.z), size(y.w))));
+  }
+  uint32_t bad;
+  const int2 e = kv8_entry(c, a.seq, a.ctx, a.seq0, i, &bad);
+  if (bad && t == 0 && split == 0) kv4_flag(c, bad);
+  const int m = int((int64_t(e.y) + c.page_len - 1) / c.page_len);
+  int32_t* out = a.out + item * a.k;
+  if (m <= a.k) {                                         // (the whole cluster; m is 0 where the entry cannot be read)
+    for (int j = split * NT + t; j < a.k; j += splits * NT) out[j] = j < m ? j : -1;
+    return;
+  }
+  const int32_t* row = c.table + int64_t(e.x) * c.max_pages;
+  auto look = [&](int j0) { return lane < kKv8ScorePages && j0 + lane < m ? row[j0 + lane] : 0; };
+  const int step = splits * NW * kKv8ScorePages;
+  int j0 = (split * NW + warp) * kKv8ScorePages, page = j0 < m ? look(j0) : 0;
+  // ---- the weights of the group's queries
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) s_top[warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < NW; w++) top = fmaxf(top, s_top[w]);
+  // 63 is 1.96875 2^5: f = exponent - 5, one more above 1.96875
+  int f = 0;
+  if (top > 0.f) {
+    const float up = top < 0x1p-100f ? top * 0x1p60f : top;
+    const uint32_t b = __float_as_uint(up);
+    f = int(b >> 23) - 132 + ((b & 0x7fffffu) > 0x7c0000u) - (top < 0x1p-100f ? 60 : 0);
+  }
+  if (t < HD) {
+    int pos = 0, neg = 0;
+    for (int h = 0; h < a.G; h++) {
+      const float x = q[h * HD + t];
+      int w = 0;
+      if (fabsf(x) < INFINITY) w = __float2int_rn(scalbnf(x, -f));
+      else if (x == x) w = x > 0.f ? 63 : -63;
+      if (w > 0) pos += w; else neg += w;
+    }
+    s_w[t] = int16_t(neg);
+    s_w[HD + t] = int16_t(pos);
+  }
+  __syncthreads();
+  const int sub = lane & 7, of = lane >> 3;               // this lane's part of page `of` of four
+  int w[kRuns][kRun / 2];
+#pragma unroll
+  for (int r = 0; r < kRuns; r++)
+#pragma unroll
+    for (int y = 0; y < kRun / 2; y++) w[r][y] = reinterpret_cast<const int*>(s_w)[(r * 8 + sub) * (kRun / 2) + y];
+  const Kv8Page L(c);
+  const uint8_t* heads = c.pool + int64_t(a.layer) * c.n_pages * c.page_bytes() + L.exps(g);
+  uint32_t* keys = a.keys + item * kv8_key_stride(c);
+  for (; j0 < m; j0 += step) {
+    const int next = j0 + step < m ? look(j0 + step) : 0;
+    const bool there = lane < kKv8ScorePages && j0 + lane < m, good = page >= 0 && page < c.n_pages;
+    if (there && !good) kv4_flag(c, NT_KV4_BAD_PAGE);
+    if (!good) page = -1;
+    uint4 b[kKv8ScorePages / 4][kRuns];
+#pragma unroll
+    for (int y = 0; y < kKv8ScorePages / 4; y++) {
+      const int p = __shfl_sync(0xffffffffu, page, 4 * y + of);
+#pragma unroll
+      for (int r = 0; r < kRuns; r++) {
+        b[y][r] = make_uint4(0u, 0u, 0u, 0u);
+        if (p >= 0 && j0 + 4 * y + of < m) b[y][r] = *reinterpret_cast<const uint4*>(heads + p * c.page_bytes() + 16 + (r * 8 + sub) * kRun);
+      }
+    }
+    int ex = 0;
+    if (there && page >= 0) ex = *reinterpret_cast<const int8_t*>(heads + page * c.page_bytes());
+    int mine = 0;                                         // the sum of this lane's page
+#pragma unroll
+    for (int y = 0; y < kKv8ScorePages / 4; y++) {
+      int sum = 0;
+#pragma unroll
+      for (int r = 0; r < kRuns; r++) {
+        const uint32_t u[4] = {b[y][r].x, b[y][r].y, b[y][r].z, b[y][r].w};
+#pragma unroll
+        for (int z = 0; z < 4; z++) {
+          sum = __dp2a_lo(w[r][2 * z], int(u[z]), sum);
+          sum = __dp2a_hi(w[r][2 * z + 1], int(u[z]), sum);
+        }
+      }
+#pragma unroll
+      for (int o = 4; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      sum = __shfl_sync(0xffffffffu, sum, 8 * (lane & 3));
+      if (lane >> 2 == y) mine = sum;
+    }
+    if (there) {
+      const int j = j0 + lane;
+      const uint32_t z = __float_as_uint(float(mine) * kv8_exp2i(ex)), key = z >> 31 ? ~z : z | 0x80000000u;
+      keys[j] = j < a.first || j >= m - a.last ? 0xffffffffu : key;   // (no score has the key 0xffffffff)
+    }
+    page = next;
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (split == 0) kv8_pick(keys, m, a.k, out);
+}
+
 }  // namespace nt
 
 using namespace nt;
@@ -332,17 +326,40 @@ extern "C" nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t
   };
   if (meets(dev_pages, ob) || meets(dev_workspace, int64_t(wb)) || kv4_overlap(dev_pages, ob, dev_workspace, int64_t(wb)))
     return bad("the output or the workspace overlaps another buffer");
-  Kv8SelectArgs a{layer, n, n_heads / k.n_kv, n_select, n_first, n_last, 1, dev_seq, dev_ctx, dev_q, q_stride,
+  const Kv8SelectArgs a{layer, n, n_heads / k.n_kv, n_select, n_first, n_last, 0, dev_seq, dev_ctx, dev_q, q_stride,
                         static_cast<uint32_t*>(dev_workspace), dev_pages};
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (k.max_pages > n_select) {
-    const int64_t per = kKv8ScoreThreads / 32 * kKv8ScorePages, rounds = (k.max_pages + per - 1) / per;
-    const int64_t splits = 152 * 4 / items;
-    a.splits = int32_t(splits < 1 ? 1 : (splits > rounds ? rounds : splits));
-    const unsigned grid = unsigned(items * a.splits);
-    NT_CUDA(k.hd == 64 ? kv4_launch(k_kv8_scores<64>, grid, unsigned(kKv8ScoreThreads), s, k, a)
-                       : kv4_launch(k_kv8_scores<128>, grid, unsigned(kKv8ScoreThreads), s, k, a));
+  // a cluster of up to 16 CTAs per item, as far as the GPU holds four CTAs an SM and each has pages to look at
+  const int64_t per = kKv8SelectThreads / 32 * kKv8ScorePages, rounds = (k.max_pages + per - 1) / per;
+  int64_t splits = 152 * 4 / items;
+  splits = splits > 16 ? 16 : splits;
+  splits = k.max_pages <= n_select || splits < 1 ? 1 : (splits > rounds ? rounds : splits);
+  static const cudaError_t wide[2] = {cudaFuncSetAttribute(k_kv8_select<64>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1),
+                                      cudaFuncSetAttribute(k_kv8_select<128>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)};
+  if (wide[k.hd == 128] != cudaSuccess) return cuda_fail(wide[k.hd == 128], who);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(splits);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(unsigned(splits), 0u);
+  cfg.blockDim = dim3(unsigned(kKv8SelectThreads));
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  constexpr int64_t kMost = 65535;                        // items of a launch
+  for (int64_t at = 0; at < n; at += kMost / k.n_kv) {
+    Kv8SelectArgs part = a;
+    part.n = int32_t(n - at < kMost / k.n_kv ? n - at : kMost / k.n_kv);
+    part.seq0 = int32_t(at);
+    if (dev_seq) part.seq += at;
+    if (dev_ctx) part.ctx += at;
+    part.q += at * q_stride;
+    part.keys += at * k.n_kv * kv8_key_stride(k);
+    part.out += at * k.n_kv * n_select;
+    cfg.gridDim.y = unsigned(int64_t(part.n) * k.n_kv);
+    NT_CUDA(k.hd == 64 ? cudaLaunchKernelEx(&cfg, k_kv8_select<64>, k, part) : cudaLaunchKernelEx(&cfg, k_kv8_select<128>, k, part));
   }
-  NT_CUDA(kv4_launch(k_kv8_pick, unsigned(items), unsigned(kKv8PickThreads), s, k, a));
   return NT_OK;
 }
