@@ -123,7 +123,7 @@ __device__ __forceinline__ float2 kv8_turn_fast(uint64_t phase, int pos) {
 // several kv heads one after the other, the next one's rows on the way; the page's exponent needs all rows of a head before the
 // first code.  A thread has 32 values: of K 4 dimensions of 8 positions (cos and sin of the page's positions stand in
 // shared memory for all heads, and four threads exchange their codes for runs of 16), of V 2 dimensions of 16 positions (a run each).
-//   A key is rotated in fp32, which is off by less than d = 2^-21 (|x| + |y|) of its pair; where x + d and x - d have
+//   A key is rotated in fp32, which is off by less than d = 1.25 2^-22 (|x| + |y|) of its pair (kUnsure); where x + d and x - d have
 // different codes (about one value in 10^4), or the largest magnitude of a warp lies that near to where the exponent changes, the warp
 // takes those rows again to 2^-45.
 // read: a warp handles K or V of 16 positions of one sequence and kv head.
@@ -196,6 +196,11 @@ __device__ __forceinline__ void kv8_rotate_q(const Kv4& c, const Kv4Rows& a, con
     *reinterpret_cast<float4*>(r.out + int64_t(row) * r.out_stride + h * HD + 4 * i) = x;
   }
 }
+
+// Error of a rotated key in fp32, relative to S = |x| + |y| of its pair, in units of 2^-24: cos and sin are off by 2^-24.8, which (|a| +
+// |b|) <= sqrt(2) S multiplies (0.82); the first product rounds (|b| <= S: 1), the multiply-add (1), and the key that the format defines is rounded to
+// fp32 once itself (1); forming x 2^-e -+ d rounds (1).  4.82 2^-24 in all.
+constexpr float kUnsure = 0x1.4p-22f;
 
 // What the threads of an append know of their page.
 struct Kv8Mine {
@@ -393,7 +398,7 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
     }
     bool exact = V || !turned;
     float top = kv8_largest(x);
-    constexpr uint32_t kNear = 64;                                     // of 2^-23: farther than the error of x
+    constexpr uint32_t kNear = 64;                                     // of 2^-23: farther than the error of x (S is at most twice the largest)
     const uint32_t from_border = (__float_as_uint(top) & 0x7fffffu) - (0x600000u - kNear);
     if (__float_as_uint(top) > __float_as_uint(kKv8Most) - kNear || (!exact && from_border <= 2 * kNear)) {
       if (V) {
@@ -424,7 +429,7 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
       uint32_t w[8] = {};
       if (busy) {
       uint32_t z[8], differ = 0u;                                      // codes of a position's 4 dimensions, of x - d and x + d
-      const uint64_t up2 = kv8_pack(up, up), off = kv8_pack(up * 0x1p-21f, up * 0x1p-21f), minus = kv8_pack(up * -0x1p-21f, up * -0x1p-21f);
+      const uint64_t up2 = kv8_pack(up, up), off = kv8_pack(up * kUnsure, up * kUnsure), minus = kv8_pack(up * -kUnsure, up * -kUnsure);
       if (exact) {
 #pragma unroll
         for (int i = 0; i < 8; i++) w[i] = z[i] = kv8_code4(x[4 * i] * up, x[4 * i + 1] * up, x[4 * i + 2] * up, x[4 * i + 3] * up);

@@ -9,6 +9,7 @@ is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import os
 import re
@@ -524,7 +525,7 @@ def nt_kv8_append(c: nt_kv8_cache, layer: int, n: int, dev_seq, dev_begin, n_row
     if freq is not None:
         if len(freq) != c.head_dim // 2:
             raise ValueError(f"nt_kv8_append: {c.head_dim // 2} frequencies expected, {len(freq)} given")
-        freq = (C.c_double * len(freq))(*freq)
+        freq = (C.c_double * len(freq)).from_buffer(array.array("d", freq))
     _check(lib().nt_kv8_append(c, layer, n, dev_seq, dev_begin, n_rows, QTYPES[qtype], dev_k, dev_v, row_stride,
                                head_stride, freq, n_heads, dev_q, q_stride, dev_q_out, q_out_stride, _stream(stream)),
            "nt_kv8_append")
