@@ -646,8 +646,7 @@ nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, i
 /* nt_attention over the 8-bit cache, as nt_attention_kv4 (lists, strides, empty and
  * unreadable sequences, limits).  dev_ctx (nullable): entry i attends to the first dev_ctx[i]
  * positions of its sequence, 0 <= dev_ctx[i] <= len, so that drafted tokens, listed
- * with their sequence once each, see the positions up to their own.  Entries of one sequence
- * listed one after the other share reads of the cache where both dev_seq and dev_ctx are given.
+ * with their sequence once each, see the positions up to their own.
  * n_select = 0: all positions.  n_select > 0: those in the pages dev_pages
  * [n][n_kv_heads][n_select] names (nt_kv8_select): places in the table row, ascending,
  * each once, negative ones only behind them.  A place at or beyond the pages that hold

@@ -1,12 +1,11 @@
 // nt_kv8_attn.cu -- attention over the paged 8-bit cache (include/nt.h,
 // nt_attention_kv8).
 //
-// The mathematics.  For one (entry, kv head), an item, with G query heads, or several
-// such entries of one sequence (drafted tokens, whose items are taken together), R rows of queries in all, tiles of 128
+// The mathematics.  For one (entry, kv head), an item, with G query heads, tiles of 128
 // positions go through two products on tcgen05, kind::f8f6f4, whose A operand is the
 // cache itself, copied from its page to shared memory and never decoded:
-//   S^T [128 positions][6 R] = K [128][hd] . q^T        q as six e4m3 terms, each 1/16 of the one before
-//   O^T [hd][8 R]            = V^T [hd][128] . P^T      the weights as eight digits
+//   S^T [128 positions][6 G] = K [128][hd] . q^T        q as six e4m3 terms, each 1/16 of the one before
+//   O^T [hd][8 G]            = V^T [hd][128] . P^T      the weights as eight digits
 // e4m3 has four significant bits, so six terms, each the rounding of what the ones before left,
 // hold q to 2^-24 and more.  A weight w in [0, 16) is the whole number round(w 2^28), cut into
 // eight digits of four bits: the e4m3 codes 0 to 15 are the numbers 0 to 15 times 2^-9, so a
@@ -33,7 +32,6 @@ constexpr int kKv8MaxCluster = 16;
 
 struct Kv8AttnArgs {
   int32_t layer, n, G, k;
-  int32_t R;                            // entries that may share an item: e / R the same, one after the other, of one sequence
   int32_t seq0;                         // sequence of entry 0 where none are listed
   const int32_t* seq;
   const int32_t* ctx;
@@ -44,7 +42,7 @@ struct Kv8AttnArgs {
   int64_t out_stride;
   float scale;                          // log2(e) / sqrt(hd)
   float* part;                          // [CTA][2] partial results: of an item begun before this CTA, of one that goes on behind it
-  int2* open;                           // [CTA]: the latter's item (-1: none); the number of CTAs that work on it and (from bit 16) of its entries
+  int2* open;                           // [CTA]: the latter's item (-1: none) and the number of CTAs that work on it
 };
 
 // Partial result of one item: o [HB][HD], then (reference m, sum l) per head.
@@ -77,8 +75,7 @@ struct Kv8AttnCfg {
   static constexpr int kSums = kEntry + kKv8Batch * 8;
   static constexpr int kInfo = kSums + 32;                          // [E]: positions of the tile, and kLacks: behind them a page is not there
   static constexpr int kLacks = 1 << 16;
-  static constexpr int kRows = kInfo + 4 * E;                       // [2][HB]: positions that a row of queries sees
-  static constexpr int kBars = (kRows + 8 * HB + 7) / 8 * 8;         // full [H], empty [H], scores, taken, weights, outputs
+  static constexpr int kBars = (kInfo + 4 * E + 7) / 8 * 8;         // full [H], empty [H], scores, taken, weights, outputs
   static constexpr int kTmem = kBars + 8 * (2 * H + 4);
   static constexpr int kSegs = kTmem + 4;                           // items whose q is there
   static constexpr int kSmem = kTmem + 16;
@@ -193,8 +190,8 @@ struct Kv8At {
 
 // ------------------------------------------------------------ the kernel --
 
-// CL: block (rank, item) of a cluster per item.  GR: entries may share items.
-template <int HD, int HB, bool CL, bool GR>
+// CL: block (rank, item) of a cluster per item.
+template <int HD, int HB, bool CL>
 __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv4 c, Kv8AttnArgs a) {
   using Cfg = Kv8AttnCfg<HD, HB>;
   constexpr int H = Cfg::H, E = Cfg::E, NT = Cfg::kThreads;
@@ -236,43 +233,16 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     if (a.k) x = min((x + P - 1) >> lg, uint32_t(a.k)) << lg;
     return int((x + kKv8Tile - 1) / kKv8Tile);
   };
-  // entries are kept from `base` on: CL: the item's only
-  const int base = CL ? int(blockIdx.y) / c.n_kv : 0, R = GR ? a.R : 1;
-  // whether entry e goes with the one before it
-  auto joins = [&](int e) { return e % R != 0 && entry[e - base].x >= 0 && entry[e - base].x == entry[e - 1 - base].x; };
-  // entries of the item that begins with e, and the most positions that one of them sees
-  auto item_of = [&](int e, int& len) {
-    int r = 1;
-    len = entry[e - base].y;
-    if (!GR) return 1;
-    while (r < R && e + r < n && joins(e + r)) {
-      len = max(len, entry[e + r - base].y);
-      r++;
-    }
-    return r;
-  };
+  int2 only = make_int2(-1, 0);                        // CL: the item's entry
   int total = 0;
   if (CL) {
-    // (the entry before: does this one go with it?)
-    bool with = false;
-    if (t < R && base + t < n) {
-      uint32_t bad;
-      entry[t] = kv8_attn_entry(c, a, base + t, &bad);
-      if (t == 0 && bad && blockIdx.x == 0) kv4_flag(c, bad);
-      if (GR && t == 0 && base % R) with = !bad && entry[0].x == kv8_attn_entry(c, a, base - 1, &bad).x;
-    }
+    uint32_t bad;
+    only = kv8_attn_entry(c, a, int(blockIdx.y) / c.n_kv, &bad);
+    if (bad && blockIdx.x == 0 && t == 0) kv4_flag(c, bad);
+    total = tiles(only.y);
     kv8_tc_before();
-    if (GR) with = __syncthreads_or(with);
-    else __syncthreads();
+    __syncthreads();
     kv8_tc_after();
-    if (GR && with) {                                  // (the whole cluster)
-      if (warp == 5)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(*tensor_memory), "n"(Cfg::kCols));
-      return;
-    }
-    int len;
-    item_of(base, len);
-    total = tiles(len);
   } else {
     int* sums = reinterpret_cast<int*>(sm + Cfg::kSums);
     int run = 0;
@@ -285,17 +255,6 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         if (bad && blockIdx.x == 0) kv4_flag(c, bad);
         entry[e] = sl;
         mine = tiles(sl.y) * c.n_kv;
-      }
-      if (GR) {
-        __syncthreads();
-        if (e < n) {   // (a round's entries may go with some of the round before, not with the next one's: NT is a multiple of R)
-          mine = 0;
-          if (!joins(e)) {
-            int len;
-            item_of(e, len);
-            mine = tiles(len) * c.n_kv;
-          }
-        }
       }
       int x = mine;
 #pragma unroll
@@ -324,6 +283,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   const uint32_t tmem = *tensor_memory;
   asm volatile("griddepcontrol.launch_dependents;");
   if (!CL) total = prefix[n];
+  auto seen = [&](int e) { return CL ? only : entry[e]; };
   int share = (total + int(gridDim.x) - 1) / int(gridDim.x);
   if (share < 1) share = 1;
   const int c0 = int(blockIdx.x) * share < total ? int(blockIdx.x) * share : total, c1 = c0 + share < total ? c0 + share : total;
@@ -331,7 +291,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
 
   auto locate = [&](int x, Kv8At& at) {
     if (CL) {
-      at = Kv8At{base, int(blockIdx.y) % c.n_kv, x, total};
+      at = Kv8At{int(blockIdx.y) / c.n_kv, int(blockIdx.y) % c.n_kv, x, total};
       return;
     }
     int lo = 0, hi = n;
@@ -340,9 +300,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       if (prefix[mid] <= x) lo = mid; else hi = mid;
     }
     at.e = lo;
-    int len;
-    item_of(lo, len);
-    at.nt = tiles(len);
+    at.nt = tiles(entry[lo].y);
     const int r = x - prefix[lo];
     at.g = int(uint32_t(r) / uint32_t(at.nt));
     at.ti = r - at.g * at.nt;
@@ -359,11 +317,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     for (int x = c0; x < c1 && !dead;) {
       Kv8At at;
       locate(x, at);
-      const int count = segment(x, at);
-      int len;
-      item_of(at.e, len);
+      const int count = segment(x, at), len = seen(at.e).y;
       const int m = int((uint32_t(len) + P - 1) >> lg), listed = a.k && a.k < m ? a.k : m;
-      const int32_t* row = c.table + int64_t(entry[at.e - base].x) * c.max_pages;
+      const int32_t* row = c.table + int64_t(seen(at.e).x) * c.max_pages;
       const int32_t* list = a.k ? a.pages + (int64_t(at.e) * c.n_kv + at.g) * a.k : nullptr;
       const int end = (at.ti + count) * per < listed ? (at.ti + count) * per : listed;
       // the page at place i of the list; -1: none there, -2: the list has ended; *last: it is the sequence's last page
@@ -556,22 +512,18 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
 
     // The q of the item at `at` into shared memory, scaled so that its largest element is in [2^7, 2^8), in six terms; a warp takes every fourth
     // row.  It is done before the item before it is finished with, once that one's scores are all there.
-    int* sees0 = reinterpret_cast<int*>(sm + Cfg::kRows);
     float* scales = red + 8 * HB;
     auto prepare = [&](const Kv8At& at, int odd) {
-      int len;
-      const int rows = item_of(at.e, len) * a.G;
       constexpr int V = HD / 32;
-      if (GR && t < HB) sees0[odd * HB + t] = t < rows ? entry[at.e + t / a.G - base].y : 0;
       constexpr int kMine = (HB + 3) / 4;            // rows of a warp: all on the way together
       float z[kMine][V];
 #pragma unroll
       for (int j = 0; j < kMine; j++) {
-        const int h = warp + 4 * j, sub = GR ? h / a.G : 0;
-        const float* qb = a.q + int64_t(at.e + sub) * a.q_stride + int64_t(at.g * a.G + h - sub * a.G) * HD + V * lane;
+        const int h = warp + 4 * j;
+        const float* qb = a.q + int64_t(at.e) * a.q_stride + (int64_t(at.g) * a.G + h) * HD + V * lane;
 #pragma unroll
         for (int i = 0; i < V; i++) z[j][i] = 0.f;
-        if (h < rows) {
+        if (h < a.G) {
           if (V == 4) {
             const float4 w = *reinterpret_cast<const float4*>(qb);
             z[j][0] = w.x; z[j][1] = w.y; z[j][2 % V] = w.z; z[j][3 % V] = w.w;
@@ -636,29 +588,21 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     for (int x = c0; x < c1; odd ^= 1) {
       at = next;
       const int count = segment(x, at);
-      int len;
-      const int rows = item_of(at.e, len) * a.G;       // of queries
       bool poison = dead;
-      int lacking = 0x7fffffff;                        // rows that see more positions are not known
-      int nan_from = 0x7fffffff;                       // (GR) the same for this thread's dimension
-      const int* sees = sees0 + odd * HB;
-      int least = 0x7fffffff;                          // positions that every row sees
 #pragma unroll
       for (int h = 0; h < HB; h++) {
         cs[h] = scales[odd * HB + h];
         O[h] = l[h] = 0.f;
         mref[h] = -3e38f;
       }
-      if (GR)
-        for (int h = 0; h < rows; h++) least = min(least, sees[h]);
 #pragma unroll 1
       for (int i = 0; i < count; i++, no++) {
         if (dead) continue;
         // (not K's own barrier: its slot may have been filled again by now)
         bool fail = !__all_sync(0xffffffffu, kv4_bar_wait(bar_s, ps));
         ps ^= 1u;
-        const int word = info[no % E], live = word & (Cfg::kLacks - 1), start = (at.ti + i) * kKv8Tile;
-        if (word & Cfg::kLacks) lacking = min(lacking, start + live);
+        const int word = info[no % E], live = word & (Cfg::kLacks - 1);
+        if (word & Cfg::kLacks) poison = true;
         if (live == 0 || fail) {
           if (kv8_any(fail)) dead = kv8_any(fail);     // (as many barriers as a tile with scores has)
           poison = poison || dead;
@@ -667,32 +611,22 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           continue;
         }
         kv8_tc_after();
-        const bool ends = GR && start + kKv8Tile > least;   // some rows end in this tile, or before it
-        if (live < kKv8Tile || ends) {
+        if (live < kKv8Tile) {   // values behind the end: zeros, whatever the page holds there
           const int vfill = 2 * no + 1;
           fail = !__all_sync(0xffffffffu, kv4_bar_wait(full + 8 * (vfill % H), uint32_t(vfill / H) & 1u)) || fail;
           uint8_t* v = sm + vfill % H * Cfg::kSlot;
-          if (t < HD) {
-            const int first = ends ? max(least - start, 0) : live;
-            for (int ch = first >> 4; ch < 8; ch++) {
+          if (t < HD)
+            for (int ch = live >> 4; ch < 8; ch++) {
               uint4* at16 = reinterpret_cast<uint4*>(v + kv8_v_at(HD, ch, t));
-              uint4 w4 = *at16;
-              uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-              for (int y = 0; y < 4; y++) {
-                const int p0 = 16 * ch + 4 * y, keep = live - p0;   // values behind the end: zeros, whatever the page holds there
-                if (GR && ends)                        // a value that is no number, which not every row sees: those that do are told
-#pragma unroll
-                  for (int b = 0; b < 4; b++)
-                    if (p0 + b >= first && b < keep && (w[y] >> (8 * b) & 0x7fu) == kKv8Nan) {
-                      nan_from = min(nan_from, start + p0 + b);
-                      w[y] &= ~(0xffu << (8 * b));
-                    }
-                w[y] = keep >= 4 ? w[y] : keep <= 0 ? 0u : w[y] & ((1u << (8 * keep)) - 1u);
+              uint4 w = make_uint4(0u, 0u, 0u, 0u);
+              const int keep = live - 16 * ch;         // bytes that stay
+              if (keep > 0) {
+                w = *at16;
+                auto cut = [&](uint32_t z, int b) { return keep >= b + 4 ? z : keep <= b ? 0u : z & ((1u << (8 * (keep - b))) - 1u); };
+                w = make_uint4(cut(w.x, 0), cut(w.y, 4), cut(w.z, 8), cut(w.w, 12));
               }
-              *at16 = make_uint4(w[0], w[1], w[2], w[3]);
+              *at16 = w;
             }
-          }
         }
         // ---- scores; while they come, the exponents of the tile's pages: this position's key's and value's, the largest value's
         float s[HB], fk, fv;
@@ -734,11 +668,6 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         }
 #pragma unroll
         for (int h = 0; h < HB; h++) s[h] = t < live ? s[h] * fk : -INFINITY;
-        if (ends) {
-#pragma unroll
-          for (int h = 0; h < HB; h++)
-            if (start + t >= sees[h]) s[h] = -INFINITY;
-        }
         // ---- weights
         float p[HB], most;
         auto weights = [&]() {
@@ -814,7 +743,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       float* part = CL ? reinterpret_cast<float*>(sm) : part0 + (begun ? Cfg::kPart : 0);
       if (t < HB) {                                    // what row t's outputs are multiplied by
         float sum = (sums[t] + sums[HB + t]) + (sums[2 * HB + t] + sums[3 * HB + t]);
-        if (poison || (GR ? sees[t] > lacking : lacking != 0x7fffffff)) sum = NAN;
+        if (poison) sum = NAN;
         red[t] = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
         if (!whole) part[HB * HD + 2 * t + 1] = sum;
       }
@@ -824,22 +753,13 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       }
       kv8_any(false);
       float* to = (whole ? a.out + int64_t(at.e) * a.out_stride + int64_t(at.g) * a.G * HD : part) + t;
-      const int64_t next_entry = whole ? a.out_stride - int64_t(a.G - 1) * HD : HD;   // from an entry's last row to the next one's first
 #pragma unroll
-      for (int h = 0, n = 1; h < HB; h++, n++) {
-        if (GR && sees[h] > nan_from) O[h] = NAN;
-        if (h < rows && t < HD) *to = O[h] * red[h];
-        if (GR && n == a.G) {
-          to += next_entry;
-          n = 0;
-        } else {
-          to += HD;
-        }
-      }
+      for (int h = 0; h < HB; h++)
+        if (h < a.G && t < HD) to[h * HD] = O[h] * red[h];
       x += count;
       // the CTA's last item is open where it was begun here and goes on behind
       if (!CL && x >= c1 && t == 0)
-        a.open[blockIdx.x] = begun && !whole ? make_int2(at.e * c.n_kv + at.g, ((x - count + at.nt - 1) / share - int(blockIdx.x) + 1) | (GR ? rows / a.G : 1) << 16) : make_int2(-1, 0);
+        a.open[blockIdx.x] = begun && !whole ? make_int2(at.e * c.n_kv + at.g, (x - count + at.nt - 1) / share - int(blockIdx.x) + 1) : make_int2(-1, 0);
     }
     if (!CL) {
       if (c0 >= c1 && t == 0) a.open[blockIdx.x] = make_int2(-1, 0);
@@ -862,9 +782,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   }
   if (CL) {
     // ---- the item's partial results, each CTA a share of the outputs, in the ranks' order
-    int len;
-    const int ranks = int(gridDim.x), outs = item_of(base, len) * a.G * HD;
-    float* out = a.out + int64_t(base) * a.out_stride + int64_t(int(blockIdx.y) % c.n_kv) * a.G * HD;
+    const int ranks = int(gridDim.x), outs = a.G * HD;
+    float* out = a.out + int64_t(int(blockIdx.y) / c.n_kv) * a.out_stride + int64_t(int(blockIdx.y) % c.n_kv) * outs;
     auto there = [&](int r, uint32_t at) {             // shared memory of rank r
       uint32_t y;
       asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(smu + at), "r"(r));
@@ -896,8 +815,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           sum = fmaf(l[r], f, sum);
           y = fmaf(o[r], f, y);
         }
-      const int sub = GR ? h / a.G : 0;
-      out[int64_t(sub) * a.out_stride + i - sub * a.G * HD] = entry[0].x < 0 ? NAN : sum == 0.f ? 0.f : y / sum;
+      out[i] = only.x < 0 ? NAN : sum == 0.f ? 0.f : y / sum;
     }
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");   // all have read this CTA's
   }
@@ -945,7 +863,7 @@ __global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8Att
     }
   }
   if (s_cta < 0) return;
-  const int members = s_members & 0xffff, all = (s_members >> 16) * a.G;   // rows of the item
+  const int members = s_members, all = a.G;
   const float* first = a.part + (int64_t(s_cta) * 2 + 1) * part_floats;    // the second of this CTA, then the first of the next ones
   float M = -INFINITY, sum = 0.f, o[V];
 #pragma unroll
@@ -976,7 +894,7 @@ __global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8Att
   for (int v = 0; v < V; v++) s_o[warp][32 * v + lane] = o[v];
   if (lane == 0) s_ml[warp] = make_float2(M, sum);
   __syncthreads();
-  const int e0 = s_item / c.n_kv, g = s_item % c.n_kv;
+  const int e = s_item / c.n_kv, g = s_item % c.n_kv;
   for (int i = t; i < NW / per * HD; i += NT) {
     const int j = i / HD, d = i % HD, row = int(blockIdx.y) * (NW / per) + j;
     if (row >= all) break;
@@ -987,8 +905,7 @@ __global__ void __launch_bounds__(32 * kKv8MergeWarps) k_kv8_merge(Kv4 c, Kv8Att
       total = fmaf(s_ml[w].y, f, total);
       y = fmaf(s_o[w][d], f, y);
     }
-    const int sub = row / a.G;
-    a.out[int64_t(e0 + sub) * a.out_stride + (int64_t(g) * a.G + row - sub * a.G) * HD + d] = total == 0.f ? 0.f : y / total;
+    a.out[int64_t(e) * a.out_stride + (int64_t(g) * a.G + row) * HD + d] = total == 0.f ? 0.f : y / total;
   }
 }
 
@@ -1012,12 +929,12 @@ static void kv8_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute (&attr)[2], 
   cfg.attrs = attr;
   cfg.numAttrs = cluster ? 2 : 1;
 }
-template <int HD, int HB, bool GR>
+template <int HD, int HB>
 static Kv8Fit kv8_fit() {
   using Cfg = Kv8AttnCfg<HD, HB>;
   Kv8Fit f;
-  f.setup = kernel_setup(k_kv8_attn<HD, HB, true, GR>, Cfg::kSmem);
-  if (f.setup.err == cudaSuccess) f.setup.err = cudaFuncSetAttribute(k_kv8_attn<HD, HB, true, GR>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  f.setup = kernel_setup(k_kv8_attn<HD, HB, true>, Cfg::kSmem);
+  if (f.setup.err == cudaSuccess) f.setup.err = cudaFuncSetAttribute(k_kv8_attn<HD, HB, true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   for (int i = 0; i < 8 && f.setup.err == cudaSuccess; i++) {
     cudaLaunchConfig_t cfg;
     cudaLaunchAttribute attr[2];
@@ -1025,7 +942,7 @@ static Kv8Fit kv8_fit() {
     cfg.numAttrs = 1;
     attr[0] = attr[1];
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, k_kv8_attn<HD, HB, true, GR>, &cfg) == cudaSuccess) f.clusters[i] = n;
+    if (cudaOccupancyMaxActiveClusters(&n, k_kv8_attn<HD, HB, true>, &cfg) == cudaSuccess) f.clusters[i] = n;
     else cudaGetLastError();   // (no such cluster: it is not taken)
   }
   return f;
@@ -1036,7 +953,7 @@ static Kv8Fit kv8_fit() {
 // 8: 18.3, 18.3; 16 of 300, 32/8: 8.2, 13.6; 1 of 9000, 16/1, 5 tiles a CTA: 14.9, 12.3.)
 constexpr int kKv8ClusterShare[2] = {6, 3};
 
-template <int HD, int HB, bool GR>
+template <int HD, int HB>
 static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t item_tiles, cudaStream_t s) {
   using Cfg = Kv8AttnCfg<HD, HB>;
   cudaLaunchConfig_t cfg;
@@ -1044,7 +961,7 @@ static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t i
   const int64_t items = int64_t(a.n) * k.n_kv;
   // A cluster per item where all of them fit the GPU at once and their capacity leaves no CTA more than kKv8ClusterShare tiles: the smallest
   // cluster such that a CTA has one tile at most, or the largest.
-  static const Kv8Fit fit = kv8_fit<HD, HB, GR>();
+  static const Kv8Fit fit = kv8_fit<HD, HB>();
   if (fit.setup.err != cudaSuccess) return fit.setup.err;
   int cluster = 0;
   for (int i = 0; i < 8; i++) {
@@ -1054,18 +971,18 @@ static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t i
   }
   if (cluster) {
     kv8_config(cfg, attr, dim3(unsigned(cluster), unsigned(items)), Cfg::kThreads, Cfg::kSmem, s, cluster);
-    return cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, true, GR>, k, a);
+    return cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, true>, k, a);
   }
-  static const KernelSetup setup = kernel_setup(k_kv8_attn<HD, HB, false, GR>, Cfg::kSmem);
+  static const KernelSetup setup = kernel_setup(k_kv8_attn<HD, HB, false>, Cfg::kSmem);
   if (setup.err != cudaSuccess) return setup.err;
   int64_t ctas = 2 * setup.sms < kKv8MaxCtas ? 2 * setup.sms : kKv8MaxCtas;
   if (ctas > items * item_tiles) ctas = items * item_tiles;
   kv8_config(cfg, attr, dim3(unsigned(ctas)), Cfg::kThreads, Cfg::kSmem, s, 0);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, false, GR>, k, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, false>, k, a);
   if (e != cudaSuccess || ctas < 2) return e;
   // (the last CTA's items end with it)
   // a warp per row where there are many rows, up to a block's eight where there are few
-  const int64_t cuts = ctas - 1 < items ? ctas - 1 : items, rows = a.R * a.G;
+  const int64_t cuts = ctas - 1 < items ? ctas - 1 : items, rows = a.G;
   int per = kKv8MergeWarps;
   while (per > 1 && cuts * ((rows * per + kKv8MergeWarps - 1) / kKv8MergeWarps) > 4 * setup.sms) per /= 2;
   kv8_config(cfg, attr, dim3(unsigned(cuts), unsigned((rows * per + kKv8MergeWarps - 1) / kKv8MergeWarps)), 32 * kKv8MergeWarps, 0, s, 0);
@@ -1074,11 +991,9 @@ static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t i
 
 template <int HD>
 static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t item_tiles, cudaStream_t s) {
-  const int rows = a.R * a.G;
-  if (a.R > 1) return rows <= 8 ? kv8_launch_attn<HD, 8, true>(k, a, item_tiles, s) : kv8_launch_attn<HD, 16, true>(k, a, item_tiles, s);
-  if (rows <= 2) return kv8_launch_attn<HD, 2, false>(k, a, item_tiles, s);
-  if (rows <= 4) return kv8_launch_attn<HD, 4, false>(k, a, item_tiles, s);
-  return rows <= 8 ? kv8_launch_attn<HD, 8, false>(k, a, item_tiles, s) : kv8_launch_attn<HD, 16, false>(k, a, item_tiles, s);
+  if (a.G <= 2) return kv8_launch_attn<HD, 2>(k, a, item_tiles, s);
+  if (a.G <= 4) return kv8_launch_attn<HD, 4>(k, a, item_tiles, s);
+  return a.G <= 8 ? kv8_launch_attn<HD, 8>(k, a, item_tiles, s) : kv8_launch_attn<HD, 16>(k, a, item_tiles, s);
 }
 
 }  // namespace nt
@@ -1130,10 +1045,6 @@ extern "C" nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int3
   a.layer = layer;
   a.G = G;
   a.k = n_select;
-  // Entries of one sequence share items where the call says that there may be some: it lists sequences, and how much of them is seen.
-  a.R = dev_seq && dev_ctx && !n_select ? (G <= 4 ? 8 : 16) / G : 1;
-  if (a.R > n) a.R = n;
-  while (192 % a.R) a.R--;                             // (a round of the kernel's threads holds whole items)
   a.q_stride = q_stride;
   a.out_stride = out_stride;
   a.scale = 1.4426950408889634f / sqrtf(float(k.hd));

@@ -464,7 +464,7 @@ def test_drafts_see_the_positions_up_to_their_own(nt):
 @pytest.mark.parametrize("hd,kv,heads,page_len,longest,n", [
     (128, 2, 2, 16, 700, 60), (128, 2, 4, 64, 1500, 37), (64, 3, 9, 32, 900, 41), (128, 1, 4, 128, 6000, 23), (64, 2, 14, 16, 400, 30),
     (128, 4, 32, 64, 2000, 25), (64, 1, 16, 64, 3000, 9), (64, 1, 1, 16, 200, 3), (128, 8, 32, 64, 4000, 20)])
-def test_entries_of_one_sequence_share_items(nt, hd, kv, heads, page_len, longest, n):
+def test_entries_of_one_sequence_in_any_order(nt, hd, kv, heads, page_len, longest, n):
     """Runs of any length of the same sequence, lengths in any order, nothing at all among them."""
     rng = np.random.default_rng(29 + n)
     lens = [longest, 1, longest // 2, 130]
