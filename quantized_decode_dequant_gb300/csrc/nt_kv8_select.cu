@@ -93,13 +93,14 @@ __device__ __forceinline__ void kv8_pick(const uint32_t* keys, int m, int k, int
   if (found) base = kAlways;
   while (!found && width > 0) {
     const int shift = width > 10 ? width - 10 : 0;
+    const uint32_t bins = 1u << (width - shift);         // (fewer at last: keys further up are taken already)
     __syncthreads();
 #pragma unroll
     for (int y = 0; y < kOwn; y++) s_bins[kOwn * t + y] = 0;
     __syncthreads();
     each([&](uint32_t x) {
       const uint32_t bin = (x - base) >> shift;          // (keys below base wrap round to large numbers)
-      if (x >= base && bin < uint32_t(kBins) && x != kAlways) atomicAdd(&s_bins[kBins - 1 - bin], 1);   // the largest keys first
+      if (x >= base && bin < bins && x != kAlways) atomicAdd(&s_bins[kBins - 1 - bin], 1);   // the largest keys first
     });
     __syncthreads();
     int n[kOwn], mine = 0;

@@ -677,6 +677,27 @@ def test_select_many_pages_with_many_ties(nt):
             np.testing.assert_array_equal(got[s, 0], ref.select(0, s, 0, q[s], top, first, last))
 
 
+@pytest.mark.parametrize("pages", [300, 938, 2500, 4096, 5000, 9001])
+def test_select_among_many_scores(nt, pages):
+    """Scores that lie close together, so that the last bins hold few numbers each; more pages than a CTA holds in registers."""
+    import torch
+    rng = np.random.default_rng(32 + pages)
+    ref = R.RefCache(1, 1, 64, 16, pages, 1, pages)
+    ref.hold([16 * pages - 3], rng)
+    at = ref.exp_at(0, 0)
+    for p in range(pages):
+        ref.pool[0, p][at] = np.int8(rng.integers(-7, -5)).view(np.uint8)
+        ref.pool[0, p][at + 16:at + 144] = np.sort(rng.integers(-112, 113, (2, 64)), 0).reshape(-1).astype(np.int8).view(np.uint8)
+    dev = Dev(nt, ref, 4)
+    for k, spread in enumerate((1.0, 0.01, 30.0)):
+        q = (rng.standard_normal((1, 4, 64)) * spread).astype(np.float32)
+        if k == 1:
+            q[0, :, 1:] = 0                                  # one dimension decides: many equal scores, and neighbours
+        for top, first, last in ((1, 0, 0), (7, 1, 2), (64, 1, 4), (96, 0, 0), (255, 3, 3), (pages - 1, 0, 1)):
+            got = dev.select(torch.from_numpy(q).cuda(), top, first, last).cpu().numpy()
+            np.testing.assert_array_equal(got[0, 0], ref.select(0, 0, 0, q[0], top, first, last), err_msg=str((k, top)))
+
+
 def test_select_with_ctx_lists_and_odd_queries(nt):
     import torch
     rng = np.random.default_rng(22)
