@@ -365,16 +365,45 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
                                                 uint32_t (&raw)[Kv8Raw<T>::kWords]) {
   const int t = threadIdx.x, lane = t & 31, P = c.page_len, tph = P * HD / 32, hp = t / tph, th = t % tph, wph = tph / 32;
   const bool busy = __any_sync(0xffffffffu, me.live != 0u);            // the warp has new positions
+  // The page's bounds of a head, two dimensions a thread, are put together behind the next head's barrier: one barrier a head.
+  const bool two = !V && th < HD / 2;
+  int8_t* bounds = nullptr;                                            // of the head before (nullptr: none)
+  char2 lo_was = make_char2(0, 0), hi_was = lo_was;
+  float f_was = 1.f;
+  auto join_bounds = [&](int buf) {
+    if (V || !bounds) return;
+    const int groups = P / 8;
+    uint32_t least = 0x7c007c00u, most = 0xfc00fc00u;
+#pragma unroll 4
+    for (int y = 0; y < groups; y++) {
+      least = kv8_min2(least, sh.lo[buf][(hp * groups + y) * (HD / 2) + th]);
+      most = kv8_max2(most, sh.hi[buf][(hp * groups + y) * (HD / 2) + th]);
+    }
+    auto bound = [&](int j, int lo0, int hi0, int8_t& l1, int8_t& h1) {
+      const float l = __half2float(__ushort_as_half(uint16_t(least >> (16 * j)))), h = __half2float(__ushort_as_half(uint16_t(most >> (16 * j))));
+      int lo1 = l != l ? -127 : int(floorf(l * 0.25f)), hi1 = l != l ? 127 : int(ceilf(h * 0.25f));
+      if (!me.fresh) {
+        if (lo0 != -127) lo0 = int(floorf(lo0 * f_was));
+        if (hi0 != 127) hi0 = int(ceilf(hi0 * f_was));
+        lo1 = min(lo1, lo0);
+        hi1 = max(hi1, hi0);
+      }
+      l1 = int8_t(lo1);
+      h1 = int8_t(hi1);
+    };
+    int8_t l0, l1, h0, h1;
+    bound(0, lo_was.x, hi_was.x, l0, h0);
+    bound(1, lo_was.y, hi_was.y, l1, h1);
+    *reinterpret_cast<char2*>(bounds) = make_char2(l0, l1);
+    *reinterpret_cast<char2*>(bounds + HD) = make_char2(h0, h1);
+    bounds = nullptr;
+  };
 #pragma unroll 1
   for (int step = 0; step < steps; step++, g += abreast) {
     const int buf = step & 1;
     const bool on = g < c.n_kv;
     int8_t* exps = reinterpret_cast<int8_t*>(me.base + L.exps(on ? g : 0)) + V;
     const int was = me.fresh ? kKv8MinExp : *exps;
-    const bool two = !V && on && th < HD / 2;                          // two dimensions of the page's bounds
-    int8_t* bounds = reinterpret_cast<int8_t*>(me.base + L.bounds(on ? g : 0)) + 2 * th;
-    const char2 lo_was = two && !me.fresh ? *reinterpret_cast<const char2*>(bounds) : make_char2(127, 127);
-    const char2 hi_was = two && !me.fresh ? *reinterpret_cast<const char2*>(bounds + HD) : make_char2(-127, -127);
     float x[32];
 #pragma unroll
     for (int i = 0; i < 16; i++) {
@@ -417,6 +446,14 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
     }
     if (lane == 0) sh.exp[buf][t >> 5] = kv8_exponent(top);
     __syncthreads();
+    join_bounds(buf ^ 1);
+    if (two && on) {
+      bounds = reinterpret_cast<int8_t*>(me.base + L.bounds(g)) + 2 * th;
+      if (!me.fresh) {
+        lo_was = *reinterpret_cast<const char2*>(bounds);
+        hi_was = *reinterpret_cast<const char2*>(bounds + HD);
+      }
+    }
     const int e = max(was, __reduce_max_sync(0xffffffffu, lane < wph ? sh.exp[buf][hp * wph + lane] : kKv8MinExp));
     const float up = kv8_exp2i(-e);
     const int less = e - was;                                          // exponents that older codes are rounded for
@@ -476,36 +513,13 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
       *reinterpret_cast<uint2*>(&sh.lo[buf][group * (HD / 2) + me.d0 / 2]) = make_uint2(lo[0], lo[1]);
       *reinterpret_cast<uint2*>(&sh.hi[buf][group * (HD / 2) + me.d0 / 2]) = make_uint2(hi[0], hi[1]);
       if (busy || again) kv8_put_k<HD>(me, w, me.base + L.k(on ? g : 0), on, again, f);
-      __syncthreads();
-      // ---- the page's
-      const int groups = P / 8;
-      if (two) {
-        uint32_t least = 0x7c007c00u, most = 0xfc00fc00u;
-#pragma unroll 4
-        for (int y = 0; y < groups; y++) {
-          least = kv8_min2(least, sh.lo[buf][(hp * groups + y) * (HD / 2) + th]);
-          most = kv8_max2(most, sh.hi[buf][(hp * groups + y) * (HD / 2) + th]);
-        }
-        auto bound = [&](int j, int lo0, int hi0, int8_t& l1, int8_t& h1) {
-          const float l = __half2float(__ushort_as_half(uint16_t(least >> (16 * j)))), h = __half2float(__ushort_as_half(uint16_t(most >> (16 * j))));
-          int lo1 = l != l ? -127 : int(floorf(l * 0.25f)), hi1 = l != l ? 127 : int(ceilf(h * 0.25f));
-          if (!me.fresh) {
-            if (lo0 != -127) lo0 = int(floorf(lo0 * f));
-            if (hi0 != 127) hi0 = int(ceilf(hi0 * f));
-            lo1 = min(lo1, lo0);
-            hi1 = max(hi1, hi0);
-          }
-          l1 = int8_t(lo1);
-          h1 = int8_t(hi1);
-        };
-        int8_t l0, l1, h0, h1;
-        bound(0, lo_was.x, hi_was.x, l0, h0);
-        bound(1, lo_was.y, hi_was.y, l1, h1);
-        *reinterpret_cast<char2*>(bounds) = make_char2(l0, l1);
-        *reinterpret_cast<char2*>(bounds + HD) = make_char2(h0, h1);
-      }
+      f_was = f;
     }
     if (on && th == 0) *exps = int8_t(e);
+  }
+  if (!V) {
+    __syncthreads();
+    join_bounds((steps - 1) & 1);
   }
 }
 
