@@ -38,95 +38,90 @@ constexpr int kKv8SelectThreads = 256;
 constexpr int kKv8ScorePages = 16;   // of a warp at a time
 constexpr int kKv8PickBins = 1024;
 
-// The places of the a.k largest of an item's m keys, the lower place first among equals, ascending, by a whole CTA.  A thread has 16
-// keys, in its registers where there are no more than 4096.  The a.k-th largest is found by counting keys in 1024 bins of
+// The places of the k largest of an item's m keys, the lower place first among equals, ascending, by a whole CTA.  A thread has m / 256
+// keys side by side, in its registers where there are no more than 4096 in all.  The k-th largest is found by counting keys in 1024 bins of
 // equal width between the least and the largest, then in the bin where it lies, and so on; as soon as all keys of
 // that bin are wanted they and those above are the choice.  (Bins of the keys' upper bits, which few scores differ in, had all
-// threads count in the same few: 8.7 us for 2049 keys; candidates bit by bit with a count of all keys each: 12.5.)
+// threads count in the same few: 8.7 us for 2049 keys; candidates bit by bit with a count of all keys each: 12.5; 16 keys for each of the first
+// threads: 4.6, this 3.9.)
 __device__ __forceinline__ void kv8_pick(const uint32_t* keys, int m, int k, int32_t* out) {
-  constexpr int NT = kKv8SelectThreads, NW = NT / 32, R = 16, kChunk = R * NT, kBins = kKv8PickBins, kOwn = kBins / NT;
-  __shared__ int s_bins[kBins];
-  __shared__ uint32_t s_part[3][NW];
+  constexpr int NT = kKv8SelectThreads, NW = NT / 32, R = 16, kBins = kKv8PickBins, kOwn = kBins / NT;
+  __shared__ __align__(16) int s_bins[2][kBins];
+  __shared__ uint32_t s_part[4][NW];
   __shared__ int s_bin, s_left, s_in;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   constexpr uint32_t kAlways = 0xffffffffu;
+  const int chunk = R * NT, per = m < chunk ? (m + NT - 1) / NT : R;     // keys of a thread in a round of NT * per
   uint32_t key[R];
-  auto get = [&](int j0) {                               // keys j0 + 16 t ..
+  auto get = [&](int j0) {                               // keys j0 + per t ..; behind the end zeros
 #pragma unroll
-    for (int y = 0; y < R; y += 4) {
-      const int j = j0 + R * t + y;
-      const uint4 x = j < m ? *reinterpret_cast<const uint4*>(keys + j) : make_uint4(0u, 0u, 0u, 0u);
-      key[y] = x.x; key[y + 1] = x.y; key[y + 2] = x.z; key[y + 3] = x.w;
+    for (int y = 0; y < R; y++) {
+      const int j = j0 + per * t + y;
+      key[y] = y < per && j < m ? keys[j] : 0u;
     }
   };
-  auto each = [&](auto f) {                              // f(key) for all of this thread's
-    for (int j0 = 0; j0 < m; j0 += kChunk) {
-      if (m > kChunk) get(j0);
+  auto each = [&](auto f) {                              // f(key, whether it is one) for all of this thread's
+    for (int j0 = 0; j0 < m; j0 += NT * per) {
+      if (m > chunk) get(j0);
 #pragma unroll
       for (int y = 0; y < R; y++)
-        if (j0 + R * t + y < m) f(key[y]);
+        if (y < per) f(key[y], j0 + per * t + y < m);
     }
   };
   get(0);
+  *reinterpret_cast<int4*>(&s_bins[0][4 * t]) = make_int4(0, 0, 0, 0);
   uint32_t least = kAlways, most = 0u, always = 0u;      // of the keys that are not always taken, and how many are
-  each([&](uint32_t x) {
-    if (x == kAlways) { always++; return; }
-    least = min(least, x);
-    most = max(most, x);
+  each([&](uint32_t x, bool is) {
+    const bool taken = is && x == kAlways;
+    always += taken;
+    if (is && !taken) {
+      least = min(least, x);
+      most = max(most, x);
+    }
   });
   least = __reduce_min_sync(0xffffffffu, least);
   most = __reduce_max_sync(0xffffffffu, most);
   always = __reduce_add_sync(0xffffffffu, always);
   if (lane == 0) { s_part[0][warp] = least; s_part[1][warp] = most; s_part[2][warp] = always; }
   __syncthreads();
-  always = 0u;
-#pragma unroll
-  for (int w = 0; w < NW; w++) {
-    least = min(least, s_part[0][w]);
-    most = max(most, s_part[1][w]);
-    always += s_part[2][w];
-  }
+  least = __reduce_min_sync(0xffffffffu, s_part[0][lane % NW]);
+  most = __reduce_max_sync(0xffffffffu, s_part[1][lane % NW]);
+  always = __reduce_add_sync(0xffffffffu, lane < NW ? s_part[2][lane] : 0u);
   // keys from `base` on, 2^width of them, are looked at; those above are taken, `left` of these are
   uint32_t base = least;
   int width = 32 - __clz(most - least), left = k - int(always);
   bool found = left == 0;                                // (m > k: there are others)
   if (found) base = kAlways;
-  while (!found && width > 0) {
+  for (int buf = 0; !found && width > 0; buf ^= 1) {     // (s_bins[buf] is zero)
     const int shift = width > 10 ? width - 10 : 0;
     const uint32_t bins = 1u << (width - shift);         // (fewer at last: keys further up are taken already)
-    __syncthreads();
-#pragma unroll
-    for (int y = 0; y < kOwn; y++) s_bins[kOwn * t + y] = 0;
-    __syncthreads();
-    each([&](uint32_t x) {
+    each([&](uint32_t x, bool is) {
       const uint32_t bin = (x - base) >> shift;          // (keys below base wrap round to large numbers)
-      if (x >= base && bin < bins && x != kAlways) atomicAdd(&s_bins[kBins - 1 - bin], 1);   // the largest keys first
+      if (is && x >= base && bin < bins && x != kAlways) atomicAdd(&s_bins[buf][kBins - 1 - bin], 1);   // the largest keys first
     });
+    *reinterpret_cast<int4*>(&s_bins[buf ^ 1][4 * t]) = make_int4(0, 0, 0, 0);
     __syncthreads();
-    int n[kOwn], mine = 0;
-#pragma unroll
-    for (int y = 0; y < kOwn; y++) mine += n[y] = s_bins[kOwn * t + y];
+    const int4 own = *reinterpret_cast<const int4*>(&s_bins[buf][kOwn * t]);
+    const int n[kOwn] = {own.x, own.y, own.z, own.w}, mine = own.x + own.y + own.z + own.w;
     int upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int z = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += z;
     }
-    if (lane == 31) s_part[0][warp] = uint32_t(upto);
+    if (lane == 31) s_part[3][warp] = uint32_t(upto);
     __syncthreads();
-    int before = upto - mine;
+    int before = upto - mine + int(__reduce_add_sync(0xffffffffu, lane < warp ? s_part[3][lane % NW] : 0u));
+    if (before < left && before + mine >= left)
 #pragma unroll
-    for (int w = 0; w < NW; w++)
-      if (w < warp) before += int(s_part[0][w]);
-#pragma unroll
-    for (int y = 0; y < kOwn; y++) {
-      if (before < left && before + n[y] >= left) {
-        s_bin = kBins - 1 - (kOwn * t + y);
-        s_left = left - before;
-        s_in = n[y];
+      for (int y = 0; y < kOwn; y++) {
+        if (before < left && before + n[y] >= left) {
+          s_bin = kBins - 1 - (kOwn * t + y);
+          s_left = left - before;
+          s_in = n[y];
+        }
+        before += n[y];
       }
-      before += n[y];
-    }
     __syncthreads();
     base += uint32_t(s_bin) << shift;
     width = shift;
@@ -135,12 +130,12 @@ __device__ __forceinline__ void kv8_pick(const uint32_t* keys, int m, int k, int
   }
   const int ties = found ? m : left;                     // of those equal to base, how many are taken
   int taken = 0, equal = 0;                              // of the places before this round's
-  for (int j0 = 0; j0 < m; j0 += kChunk) {
-    if (m > kChunk) get(j0);
+  for (int j0 = 0; j0 < m; j0 += NT * per) {
+    if (m > chunk) get(j0);
     int over = 0, same = 0;
 #pragma unroll
     for (int y = 0; y < R; y++) {
-      const bool in = j0 + R * t + y < m;
+      const bool in = y < per && j0 + per * t + y < m;
       over += in && key[y] > base;
       same += in && key[y] == base;
     }
@@ -154,23 +149,21 @@ __device__ __forceinline__ void kv8_pick(const uint32_t* keys, int m, int k, int
     __syncthreads();
     if (lane == 31) s_part[1][warp] = uint32_t(both);
     __syncthreads();
-    int all = 0;
-    both -= own;
-#pragma unroll
-    for (int w = 0; w < NW; w++) {
-      if (w < warp) both += int(s_part[1][w]);
-      all += int(s_part[1][w]);
-    }
+    const uint32_t w = s_part[1][lane % NW];
+    both += int(__reduce_add_sync(0xffffffffu, lane < warp ? w : 0u)) - own;
+    const int all = int(__reduce_add_sync(0xffffffffu, lane < NW ? w : 0u));
     int po = taken + (both & 0xffff), ps = equal + (both >> 16);   // those above base, and equal to it, before this thread's
+    if (over + same)
 #pragma unroll
-    for (int y = 0; y < R; y++) {
-      const int j = j0 + R * t + y;
-      if (j < m && key[y] > base) { out[po + min(ps, ties)] = j; po++; }
-      if (j < m && key[y] == base) {
-        if (ps < ties) out[po + ps] = j;
-        ps++;
+      for (int y = 0; y < R; y++) {
+        const int j = j0 + per * t + y;
+        if (y >= per || j >= m) continue;
+        if (key[y] > base) { out[po + min(ps, ties)] = j; po++; }
+        if (key[y] == base) {
+          if (ps < ties) out[po + ps] = j;
+          ps++;
+        }
       }
-    }
     taken += all & 0xffff;
     equal += all >> 16;
   }
