@@ -669,12 +669,13 @@ __global__ void __launch_bounds__(32 * kKv8ReadWarps) k_kv8_read(Kv4 c, Kv4Rows 
 // f / (2 pi) modulo 1 as a 64-bit fraction, to its last bit or two (|f| up to 2^20).
 static uint64_t kv8_phase(double f) {
   constexpr double h = 0.15915494309189535, l = -9.839338337591243e-18;   // 1 / (2 pi) as a sum of two doubles
-  const double p = f * h, e = std::fma(f, h, -p) + f * l;                   // p + e: within 2^-80 or so
-  const double whole = std::floor(p), frac = p - whole;                    // exact
+  const double a = std::fabs(f), p = a * h, e = std::fma(a, h, -p) + a * l;   // p + e: within 2^-80 or so
+  const double frac = p - std::floor(p);                                    // exact (not so below zero: the sign comes last)
   // the fraction in two exact steps of 32 bits
-  const double a = std::floor(frac * 4294967296.0), b = (frac * 4294967296.0 - a) * 4294967296.0;
+  const double upper = std::floor(frac * 4294967296.0), lower = (frac * 4294967296.0 - upper) * 4294967296.0;
   const double rest = std::nearbyint(e * 18446744073709551616.0);          // |e| < 2^-33: below 2^31
-  return (uint64_t(a) << 32) + uint64_t(int64_t(std::nearbyint(b)) + int64_t(rest));
+  const uint64_t turn = (uint64_t(upper) << 32) + uint64_t(int64_t(std::nearbyint(lower)) + int64_t(rest));
+  return f < 0 ? 0 - turn : turn;
 }
 
 // CTA of an append: the threads of one page and kv head, 256 at least (then several heads side by side).
@@ -803,8 +804,8 @@ nt_status nt_kv8_append(const nt_kv8_cache* c, int32_t layer, int32_t n, const i
   if (kv4_meets_cache(k, dev_k, bytes) || kv4_meets_cache(k, dev_v, bytes)) return bad("k or v overlaps the cache");
   int64_t q_ctas = 0;
   if (dev_q) {
-    const int64_t row = int64_t(n_heads) * k.hd, qb = ((n_rows - 1) * q_stride + row) * es, ob = ((n_rows - 1) * q_out_stride + row) * 4;
     if (double(n_rows) * double(q_stride > q_out_stride ? q_stride : q_out_stride) > 1e17) return bad("the strides are too large");
+    const int64_t row = int64_t(n_heads) * k.hd, qb = ((n_rows - 1) * q_stride + row) * es, ob = ((n_rows - 1) * q_out_stride + row) * 4;
     const bool in_place = static_cast<const void*>(dev_q_out) == dev_q && type == NT_F32 && q_stride == q_out_stride;
     if ((!in_place && kv4_overlap(dev_q_out, ob, dev_q, qb)) || kv4_overlap(dev_q_out, ob, dev_k, bytes) ||
         kv4_overlap(dev_q_out, ob, dev_v, bytes) || kv4_meets_cache(k, dev_q_out, ob) || kv4_meets_cache(k, dev_q, qb) ||
