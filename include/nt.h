@@ -637,7 +637,8 @@ nt_status nt_kv8_read(const nt_kv8_cache* c, int32_t layer, int32_t n, const int
  * the sequence's table row, ascending, -1 behind.
  * An entry whose sequence or length is out of range gets -1 and sets its error bit; a page index
  * out of range counts as a page without bounds (score 0) and sets NT_KV4_BAD_PAGE.
- * NT_E_INVAL: n_select outside [1, 65536], n_first or n_last negative or n_first + n_last above n_select.
+ * NT_E_INVAL: n_select outside [1, 65536], n_first or n_last negative, n_first + n_last above n_select, or
+ * n * n_kv_heads above 2^24.
  * NT_E_UNSUPPORTED: more than 16 query heads per kv head. */
 nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
                         const int32_t* dev_ctx, const float* dev_q, int64_t q_stride, int32_t n_select, int32_t n_first,
@@ -649,9 +650,10 @@ nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, i
  * with their sequence once each, see the positions up to their own.
  * n_select = 0: all positions.  n_select > 0: those in the pages dev_pages
  * [n][n_kv_heads][n_select] names (nt_kv8_select): places in the table row, ascending,
- * each once, negative ones only behind them.  A place at or beyond the pages that hold
- * ctx positions, not above the one before it, or behind a negative one, gives NaN in that entry's and kv
- * head's outputs and sets NT_KV4_BAD_PAGE.  No place at all gives zeros.
+ * each once, negative ones only behind them.  Where m pages hold the ctx positions, the
+ * first min(m, n_select) places are looked at (no more can be right); one of them that is m or more,
+ * not above the one before it, or behind a negative one, gives NaN in that entry's and kv
+ * head's outputs and sets NT_KV4_BAD_PAGE.  No place at all, or no position, gives zeros.
  * Statistics and sums are fp32; codes enter exactly, q with about 24 bits and the
  * softmax weights to 2^-28 of a head's largest.  Any 1 to 16 query heads per kv head
  * (NT_E_UNSUPPORTED beyond). */

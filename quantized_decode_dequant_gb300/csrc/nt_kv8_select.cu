@@ -276,7 +276,8 @@ __global__ void __launch_bounds__(kKv8SelectThreads) k_kv8_select(Kv4 c, Kv8Sele
     if (there) {
       const int j = j0 + lane;
       const uint32_t z = __float_as_uint(float(mine) * kv8_exp2i(ex)), key = z >> 31 ? ~z : z | 0x80000000u;
-      keys[j] = j < a.first || j >= m - a.last ? 0xffffffffu : key;   // (no score has the key 0xffffffff)
+      // (0xffffffff is always chosen: n_first + n_last of them and no more, whatever the bytes of a page that was never written)
+      keys[j] = j < a.first || j >= m - a.last ? 0xffffffffu : min(key, 0xfffffffeu);
     }
     page = next;
   }
