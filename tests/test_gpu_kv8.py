@@ -253,12 +253,13 @@ def test_queries_are_rotated_beside_the_keys(nt, hd, heads, half):
         np.testing.assert_array_equal(tq.cpu().numpy(), got[:, :heads * hd].reshape(q.shape))
 
 
-def test_rotation_at_far_positions(nt):
+@pytest.mark.parametrize("sign", [1, -1])
+def test_rotation_at_far_positions(nt, sign):
     """Positions up to 2^31 - 257 without their pages: a table row whose last page is there is enough."""
     import torch
     rng = np.random.default_rng(7)
     n, M = (1 << 31) - 256, ((1 << 31) - 256) // 128
-    freq = [1.0, 0.7, 1e-3, 2.0 ** 19] + freqs(64)[4:]
+    freq = [sign * f for f in [1.0, 0.7, 1e-3, 2.0 ** 19] + freqs(64)[4:]]
     pool = torch.zeros(1, 1, nt.nt_kv8_pool_bytes(nt.make_kv8_cache(n_layers=1, n_kv_heads=1, head_dim=64, page_len=128, n_pages=1,
                                                                     max_seqs=1, max_pages=M))[0], dtype=torch.uint8, device="cuda")
     table = torch.full((M,), -1, dtype=torch.int32, device="cuda")
@@ -767,6 +768,123 @@ def test_page_lists_of_the_caller(nt, lists, bad):
     assert np.isnan(got[0, 2:]).all() and np.isfinite(got[0, :2]).all() and int(dev.error.cpu()[0]) == 4
 
 
+def test_lists_longer_than_the_table_and_places_that_are_not_looked_at(nt):
+    """n_select above the table's columns, in a selection and a caller's lists; what stands behind the first m places is nobody's."""
+    import torch
+    rng = np.random.default_rng(33)
+    ref = R.RefCache(1, 2, 64, 32, 30, 3, 12)
+    ref.randomize(rng)
+    ref.hold([12 * 32, 77, 0], rng)
+    dev = Dev(nt, ref, 6)
+    q = rng.standard_normal((3, 6, 64)).astype(np.float32)
+    got = dev.select(torch.from_numpy(q).cuda(), 70, 2, 3).cpu().numpy()
+    for s in range(3):
+        m = ref.pages(int(ref.len[s]))
+        assert (got[s, :, :m] == np.arange(m)).all() and (got[s, :, m:] == -1).all()
+    check_attention(dev, rng, pages=got, q=q)
+    behind = got.copy()
+    for s in range(3):
+        behind[s, :, ref.pages(int(ref.len[s])):] = rng.integers(-5, 1 << 30, 70 - ref.pages(int(ref.len[s])))
+    out = dev.attention(torch.from_numpy(q).cuda(), pages=torch.from_numpy(behind).cuda())
+    assert torch.equal(out, dev.attention(torch.from_numpy(q).cuda(), pages=torch.from_numpy(got).cuda()))
+    dev.check()
+
+
+def test_pages_of_any_bytes(nt):
+    """Pages that were never written hold anything: the selection stays a selection, and nothing beside the outputs is touched."""
+    import torch
+    rng = np.random.default_rng(34)
+    ref = R.RefCache(1, 2, 64, 16, 700, 2, 600)
+    ref.pool[:] = rng.integers(0, 256, ref.pool.shape)
+    for p in range(0, 700, 3):   # exponents of which no number is made
+        for g in range(2):
+            ref.pool[0, p, ref.exp_at(g, 0):ref.exp_at(g, 0) + 2] = rng.choice([127, 128, 129], 2)
+    ref.hold([16 * 600 - 1, 1500], rng)
+    dev = Dev(nt, ref, 4)
+    q = torch.from_numpy(rng.standard_normal((2, 4, 64)).astype(np.float32)).cuda()
+    for top, first, last in ((1, 0, 0), (1, 0, 1), (60, 0, 0), (90, 3, 4)):
+        out = torch.full((3, 2, 2, top), -7, dtype=torch.int32, device="cuda")
+        nt.nt_kv8_select(dev.c, 0, 4, 2, None, None, q.data_ptr(), 256, top, first, last, out[1].data_ptr(), dev.ws.data_ptr(), dev.wb,
+                         dev.stream())
+        assert (out[0] == -7).all() and (out[2] == -7).all()
+        for s in range(2):
+            m = ref.pages(int(ref.len[s]))
+            for row in out[1, s].cpu().numpy():
+                assert (np.diff(row) > 0).all() and row[0] >= 0 and row[-1] < m
+                assert set(range(first)) | set(range(m - last, m)) <= set(row.tolist())
+        dev.attention(q, pages=out[1].contiguous())
+    dev.attention(q)
+    dev.check()
+
+
+def test_more_entries_than_one_launch_takes(nt):
+    """Over 512 entries, listed and not, dense and over selected pages; over 65535 (entry, kv head) pairs in a selection."""
+    import torch
+    rng = np.random.default_rng(35)
+    S, hd = 700, 64
+    lens = rng.integers(0, 40, S)
+    lens[[3, 511, 512, 699]] = 190, 200, 0, 129
+    ref = R.RefCache(1, 1, hd, 16, sum(-(-int(x) // 16) for x in lens), S, 13)
+    ref.randomize(rng)
+    ref.hold(lens, rng)
+    dev = Dev(nt, ref, 2, 70000)
+    check_attention(dev, rng)
+    seqs = rng.integers(0, S, 1100)
+    ctx = [int(rng.integers(0, lens[s] + 1)) for s in seqs]
+    q = rng.standard_normal((1100, 2, hd)).astype(np.float32)
+    check_attention(dev, rng, seqs, ctx, q=q)
+    pages = dev.select(torch.from_numpy(q).cuda(), 3, 1, 1, seqs, ctx).cpu().numpy()
+    for i in range(1100):
+        np.testing.assert_array_equal(pages[i, 0], ref.select(0, seqs[i], 0, q[i], 3, 1, 1, ctx[i]))
+    check_attention(dev, rng, seqs, ctx, pages, q=q)
+    many = torch.arange(65536, device="cuda") % 1100
+    for n in (65535, 65536):
+        got = dev.select(torch.from_numpy(q).cuda()[many[:n]].contiguous(), 3, 1, 1, seqs[many[:n].cpu().numpy()], np.asarray(ctx)[many[:n].cpu().numpy()])
+        assert torch.equal(got, torch.from_numpy(pages).cuda()[many[:n]])
+    dev.check()
+
+
+def test_offsets_beyond_32_bits(nt):
+    """A pool of over 4 GB whose used pages lie at its end, in the last layer."""
+    import torch
+    rng = np.random.default_rng(36)
+    small = R.RefCache(1, 8, 128, 64, 6, 2, 3)
+    small.randomize(rng)
+    small.hold([150, 65], rng)
+    pages, layers = 10000, 4
+    pool = torch.zeros(layers, pages, small.page_bytes, dtype=torch.uint8, device="cuda")
+    assert pool.numel() > 1 << 32
+    pool[-1, pages - 6:] = torch.from_numpy(small.pool[0]).cuda()
+    big = R.RefCache(1, 8, 128, 64, 1, 2, 3)
+    big.shape.update(n_pages=pages, n_layers=layers)
+    big.table = np.where(small.table >= 0, small.table + pages - 6, -1).astype(np.int32)
+    big.len, big.refs = small.len, np.zeros(pages, np.int32)
+    big.refs[big.table[big.table >= 0]] = 1
+    dev, near = Dev(nt, big, 64), Dev(nt, small, 64)
+    dev.pool = pool
+    dev.c.pool = pool.data_ptr()
+    q = torch.from_numpy(rng.standard_normal((2, 64, 128)).astype(np.float32)).cuda()
+    assert torch.equal(dev.attention(q, layer=layers - 1), near.attention(q))
+    chosen = dev.select(q, 1, 0, 0, layer=layers - 1)
+    assert torch.equal(chosen, near.select(q, 1, 0, 0))
+    assert torch.equal(dev.attention(q, pages=chosen, layer=layers - 1), near.attention(q, pages=chosen))
+    x = rows(rng, 70, 8, 128)
+    k, v = layout(torch, x, "rows")
+    dev.append(k, v, [0, 5, 70], layer=layers - 1, freq=freqs(128))
+    store(small, x, [0, 5, 70], [0, 1], freq=freqs(128))
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(pool[-1, pages - 6:].cpu().numpy(), small.pool[0])
+    back, want = [torch.zeros_like(k) for _ in range(4)], Dev(nt, small, 64)
+    dev.read(*back[:2], [0, 5, 70], layer=layers - 1)
+    want.read(*back[2:], [0, 5, 70])
+    assert torch.equal(back[0], back[2]) and torch.equal(back[1], back[3]) and back[0].any()
+    src, dst = torch.tensor([pages - 6, pages - 1], dtype=torch.int32).cuda(), torch.tensor([0, pages - 7], dtype=torch.int32).cuda()
+    nt.nt_kv8_copy_pages(dev.c, 2, src.data_ptr(), dst.data_ptr(), dev.stream())
+    for s, d in zip(src.tolist(), dst.tolist()):
+        assert torch.equal(pool[:, s], pool[:, d])
+    assert not pool[0].any() and int(dev.error.cpu()[0]) == 0
+
+
 # ------------------------------------------------------- graphs and streams --
 
 def test_a_decode_loop_in_one_graph(nt):
@@ -874,3 +992,76 @@ def test_two_graphs_that_share_a_workspace(nt):
         graphs[i].replay()
         torch.cuda.synchronize()
         assert torch.equal(outs[i], (want, want_sparse)[i])
+
+
+FIRST_CALLS = """
+import numpy as np, torch
+import kv8_ref as R
+from test_gpu_kv8 import Dev, freqs, layout, rows
+from quantized_decode_dequant_gb300 import nt
+rng = np.random.default_rng(37)
+i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+
+class Fixed(Dev):
+    def ints(self, x):          # lists made before the capture
+        return None if x is None else x.data_ptr()
+
+def fresh(hd, page_len, heads):
+    r = np.random.default_rng(38)
+    ref = R.RefCache(2, 2, hd, page_len, 40, 4, 18)
+    ref.randomize(r)
+    ref.hold([17 * page_len + 3, 40, 0, 0], r)
+    dev = Fixed(nt, ref, heads)
+    dev.l = [i32(0, 1), i32(2, 3), i32(1, 1), i32(1), i32(3, 4), i32(38, 39), i32(0)]
+    dev.x = [torch.zeros(2, heads, hd, device="cuda") for _ in range(4)]
+    dev.back = [torch.zeros(2, 2, hd, device="cuda") for _ in range(2)]
+    dev.chosen = torch.zeros(2, 2, 3, dtype=torch.int32, device="cuda")
+    return dev
+
+def calls(dev, k, v, q):
+    src, dst, one, drop, a, b, live = dev.l
+    hd, heads = dev.ref.hd, dev.heads
+    nt.nt_kv8_fork(dev.c, 2, src.data_ptr(), dst.data_ptr(), None, dev.ws.data_ptr(), dev.wb, dev.stream())
+    nt.nt_kv8_extend(dev.c, 2, dst.data_ptr(), one.data_ptr(), dev.ws.data_ptr(), dev.wb, dev.stream())
+    nt.nt_kv8_append(dev.c, 1, 2, dst.data_ptr(), None, 2, "f16" if k.dtype == torch.float16 else "f32", k.data_ptr(), v.data_ptr(),
+                     2 * hd, hd, freqs(hd), heads, q.data_ptr(), heads * hd, dev.x[0].data_ptr(), heads * hd, dev.stream())
+    nt.nt_kv8_read(dev.c, 1, 2, dst.data_ptr(), None, 2, "f32", dev.back[0].data_ptr(), dev.back[1].data_ptr(), 2 * hd, hd, dev.stream())
+    dev.attention(dev.x[0], dst, layer=1, out=dev.x[1])
+    nt.nt_kv8_select(dev.c, 1, heads, 2, dst.data_ptr(), None, dev.x[0].data_ptr(), heads * hd, 3, 1, 1, dev.chosen.data_ptr(),
+                     dev.ws.data_ptr(), dev.wb, dev.stream())
+    dev.attention(dev.x[0], dst, pages=dev.chosen, layer=1, out=dev.x[2])
+    nt.nt_kv8_free(dev.c, 1, drop.data_ptr(), None, dev.stream())
+    nt.nt_kv8_copy_pages(dev.c, 2, a.data_ptr(), b.data_ptr(), dev.stream())
+    nt.nt_kv8_compact(dev.c, dev.table.data_ptr(), dev.refs.data_ptr(), live.data_ptr(), dev.ws.data_ptr(), dev.wb, dev.stream())
+
+shapes = [(64, 16, 2, False), (64, 128, 32, True), (128, 64, 8, False), (128, 128, 16, True), (128, 16, 6, False)]
+for hd, page_len, heads, half in shapes:
+    x = rows(rng, 2, 2, hd)
+    k, v = layout(torch, x, "rows", half)
+    q = torch.from_numpy(rng.standard_normal((2, heads, hd)).astype(np.float32)).cuda().to(k.dtype)
+    dev, dev2, side = fresh(hd, page_len, heads), fresh(hd, page_len, heads), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):        # every operator for the first time in this process
+        calls(dev, k, v, q)
+    graph.replay()
+    torch.cuda.synchronize()
+    calls(dev2, k, v, q)
+    torch.cuda.synchronize()
+    for a, b in zip((dev.pool, dev.table, dev.len, dev.refs, dev.error, dev.chosen, *dev.x, *dev.back),
+                    (dev2.pool, dev2.table, dev2.len, dev2.refs, dev2.error, dev2.chosen, *dev2.x, *dev2.back)):
+        assert torch.equal(a, b)
+    assert int(dev.error) == 0 and all(torch.isfinite(y).all() and y.any() for y in dev.x[:3])
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(nt):
+    """What a kernel is set up with at its first launch does not disturb a capture."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=os.path.dirname(here), env=env, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
