@@ -136,7 +136,11 @@ struct Kv8Rot {
   float* out;
 };
 
-constexpr int kKv8AppendCtas = 4 * 152;   // (see nt_kv8_append)
+// Heads of a page go one after the other in a CTA (cos and sin are formed once, the next rows are on the way), but not in fewer
+// CTAs than this (of 256 threads; by the units of the call, of which entries of few rows use half).  (us with 1, 2, 4 and 8 heads of
+// 128 a CTA: 500 rows 7.7, 9.5, 13.4, 20; 2000 rows 13.2, 10.7, 13.3, 21; 8000 rows 37, 28.5, 27.0, 27.9; 2 x 20011 rows
+// 173, 122, 98, 88; 64 sequences of 1 row 22, 16.6, 14.2, 19.8.)
+constexpr int kKv8AppendCtas = 3 * 152;
 constexpr int kKv8QHeads = 4;   // heads that a warp rotates
 
 template <class T> struct Kv8Quad;   // four elements of a source
@@ -815,9 +819,10 @@ nt_status nt_kv8_append(const nt_kv8_cache* c, int32_t layer, int32_t n, const i
     const int64_t warps = int64_t(n_rows) * ((n_heads + kKv8QHeads - 1) / kKv8QHeads), of_cta = kv8_append_threads(k) / 32;
     q_ctas = (warps + of_cta - 1) / of_cta;
   }
-  // Heads of a page one after the other in a CTA where there are CTAs enough; else each in a CTA of its own.
-  const int abreast = kv8_append_threads(k) * 32 / (k.page_len * k.hd), steps = (k.n_kv + abreast - 1) / abreast;
-  r.per = int64_t(a.units) * 2 >= kKv8AppendCtas ? steps : 1;
+  const int threads = kv8_append_threads(k), abreast = threads * 32 / (k.page_len * k.hd), steps = (k.n_kv + abreast - 1) / abreast;
+  const int64_t each = (int64_t(a.units) * 2 * steps * threads / 256 + kKv8AppendCtas - 1) / kKv8AppendCtas;
+  r.splits = each >= steps ? 1 : int32_t((steps + each - 1) / each);
+  r.per = (steps + r.splits - 1) / r.splits;
   r.splits = (steps + r.per - 1) / r.per;
   const int64_t grid = int64_t(a.units) * r.splits * 2 + a.checks + q_ctas;
   if (grid > 0x7fffffffLL) return bad("too many rows for one call");
