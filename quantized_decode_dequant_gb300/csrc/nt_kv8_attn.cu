@@ -17,10 +17,15 @@
 // 2^3.9.  log2(e) / sqrt(hd) is multiplied into q, so that what brings a score to the exponent is a power of two
 // and the maximum and the weights see the same number however large it is.
 //
-// Two forms, chosen on the host (kv8_launch_attn).  Where there are few items of a small capacity, a thread-block cluster per
-// item, whose CTAs share out its tiles and merge their partial results through distributed shared memory.  Else the tiles of all
-// items in a row go evenly to the CTAs, two per SM; an item that is cut leaves partial results for a second launch.  In a CTA one warp copies, one starts products, four have a
-// position (then a dimension) per thread.
+// Two forms, chosen on the host (kv8_launch_attn).  Where there are few items of a small capacity, a thread-block
+// cluster per item, whose CTAs share out its tiles and merge their partial results through distributed shared memory.
+// Else the tiles of all items in a row go evenly to the CTAs, two per SM; an item that is cut leaves partial results for a
+// second launch.  In a CTA one warp copies, one starts products, four have a position (then a dimension) per thread.
+//
+// What bounds it: memory while it streams.  1 sequence of 131077 positions, 64/8 heads of 128, 268 MB: 47.9 us, of which 43
+// at 6.1 TB/s, the start 2, the second launch 3; 56 ragged ones, 32/8, 520 MB: 90.9; 1 with 128/8 heads: 52.6 (instructions:
+// a tile takes a CTA 1600 cycles with 8 heads a kv head).  1 of 4161: 7.9 us, a chain of length, page, tile
+// and q (3900 cycles to the first scores), then the cluster's merge.
 #include "nt_kv8.cuh"
 
 namespace nt {
@@ -58,7 +63,8 @@ struct Kv8AttnCfg {
   static constexpr int kTerms = 6, kDigits = 8;
   static constexpr int NS = (kTerms * HB + 15) / 16 * 16, NP = kDigits * HB;
   // ring: a tile's K, then its V, a slot each, so that K's is free again with the scores; the pages' exponents and the number
-  // of positions in a ring of their own, by tile
+  // of positions in a ring of their own, by tile.  (As many as two CTAs an SM have room for; 131077 positions with whole tiles
+  // a slot: 57.8 us, half ones 54.6, all else equal.)
   static constexpr int H = HD == 128 ? (HB <= 4 ? 6 : HB == 8 ? 5 : 4) : (HB <= 8 ? 10 : 8), E = H / 2 + 1;
   static constexpr int kSlot = kKv8Tile * HD;
   static constexpr int kPart = kv8_part_floats(HD, HB);
@@ -80,9 +86,8 @@ struct Kv8AttnCfg {
   static constexpr int kSegs = kTmem + 4;                           // items whose q is there
   static constexpr int kSmem = kTmem + 16;
   static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
-  // tensor memory: scores; outputs, twice where there is room, so that a tile's are taken while the next one's are formed
-  static constexpr int kOuts = HB <= 8 ? 2 : 1, kUsed = NS + kOuts * NP;
-  static constexpr int kColS = 0, kColO = NS, kCols = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
+  // tensor memory: scores, outputs (twice, so that a tile's can be taken while the next one's are formed, gained nothing)
+  static constexpr int kColS = 0, kColO = NS, kUsed = NS + NP, kCols = kUsed <= 32 ? 32 : kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : 256;
   static_assert(kUsed <= 256, "tensor memory of two CTAs");
 };
 
@@ -446,7 +451,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
               const uint32_t v0 = smu + slot * Cfg::kSlot, p0 = smu + Cfg::kP;
 #pragma unroll
               for (int kk = 0; kk < kKv8Tile / 32; kk++)
-                kv8_mma(tmem + Cfg::kColO + weighed % Cfg::kOuts * Cfg::NP, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
+                kv8_mma(tmem + Cfg::kColO, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
                         kv8_desc(p0 + kk * 4 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
               kv8_commit(bar_o);
               kv8_commit(empty + 8 * slot);
@@ -474,8 +479,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     uint32_t ps = 0, po = 0;
     int no = 0, segs = 0;                              // tiles; items whose q was prepared
     bool dead = false;
-    // outputs of the last tile with scores: none under way, under way, there; their scale, and which of the columns
-    int pending = 0, taken = 0;
+    // outputs of the last tile with scores: none under way, under way, there; their scale
+    int pending = 0;
     float out_scale = 0.f;
     auto await = [&]() -> bool {                       // false: they never came
       if (pending != 1) return true;
@@ -489,8 +494,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     auto take = [&]() {                                // adds them to the sums
       if (pending != 2) return;
       pending = 0;
-      const uint32_t from = tmem + mine + Cfg::kColO + taken % Cfg::kOuts * Cfg::NP;
-      taken++;
+      const uint32_t from = tmem + mine + Cfg::kColO;
       if (HD == 128 || warp < 2) {
         const uint64_t k16 = kv8_pack(16.f, 16.f), k65536 = kv8_pack(65536.f, 65536.f);
 #pragma unroll
@@ -706,7 +710,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           weights();
         }
         if (!await()) poison = true;                   // (the last tile's products have read the weights before)
-        if (Cfg::kOuts == 1) take();
+        take();
 #pragma unroll
         for (int h = 0; h < HB; h += 2) {
           uint32_t u[2];
@@ -722,7 +726,6 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         kv8_tc_before();
         __syncwarp();
         if (lane == 0) kv4_bar_arrive(bar_p);
-        take();
         out_scale = kv8_exp2i(vmax - 19);              // digits are 2^-9 of themselves, weights 2^28
         pending = 1;
       }
@@ -948,10 +951,13 @@ static Kv8Fit kv8_fit() {
   return f;
 }
 
-// Most tiles of a CTA in the form with a cluster per item, for up to 8 and for 16 query heads.  (us, that form and the other: 1
-// sequence of 600 positions, 64/8 heads: 6.5, 8.5; of 4161, 3 tiles a CTA: 8.9, 11.1; of 8000, 4: 11.8, 15.5; of 12000, 6: 14.0, 16.7; of 16000,
-// 8: 18.3, 18.3; 16 of 300, 32/8: 8.2, 13.6; 1 of 9000, 16/1, 5 tiles a CTA: 14.9, 12.3.)
-constexpr int kKv8ClusterShare[2] = {6, 3};
+// Most tiles of a CTA in the form with a cluster per item: as many as there are items, 7 at most, and 3 (16 query heads per kv head:
+// 2) more, since the more items there are, the more tiles a CTA of the other form has, and the longer its second launch takes.  (us, that
+// form and the other, heads of 128.  8/1 heads, 1 sequence of 600 positions: 6.0, 7.2; 7000, 4 tiles a CTA: 8.1, 8.3; 9000, 5: 8.8,
+// 8.5.  16/2, 12000, 6: 9.6, 9.7.  64/8, 4161, 3: 7.9, 9.2; 8000, 6: 9.7, 11.9; 12000, 8: 11.3, 12.8; 16000, 11: 14.4, 13.9; 20000,
+// 14: 17.1, 16.6.  32/8, 2 of 9000, 9: 13.2, 14.4; 16 of 1000, 8: 11.1, 12.1.  16/1, 6000, 3: 9.3, 9.5; 8000, 4: 10.3, 9.7; 128/8,
+// 8000, 6: 12.6, 15.2.)
+constexpr int kKv8ClusterShare[2] = {3, 2};
 
 template <int HD, int HB>
 static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t item_tiles, cudaStream_t s) {
@@ -959,13 +965,14 @@ static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t i
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[2];
   const int64_t items = int64_t(a.n) * k.n_kv;
-  // A cluster per item where all of them fit the GPU at once and their capacity leaves no CTA more than kKv8ClusterShare tiles: the smallest
+  // A cluster per item where all of them fit the GPU at once and their capacity leaves no CTA too many tiles: the smallest
   // cluster such that a CTA has one tile at most, or the largest.
+  const int64_t most = kKv8ClusterShare[HB == 16] + (items < 7 ? items : 7);
   static const Kv8Fit fit = kv8_fit<HD, HB>();
   if (fit.setup.err != cudaSuccess) return fit.setup.err;
   int cluster = 0;
   for (int i = 0; i < 8; i++) {
-    if (fit.clusters[i] < items || item_tiles > int64_t(kKv8Clusters[i]) * kKv8ClusterShare[HB == 16]) continue;
+    if (fit.clusters[i] < items || item_tiles > kKv8Clusters[i] * most) continue;
     cluster = kKv8Clusters[i];
     if (item_tiles <= cluster) break;
   }
@@ -981,7 +988,8 @@ static cudaError_t kv8_launch_attn(const Kv4& k, const Kv8AttnArgs& a, int64_t i
   const cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_attn<HD, HB, false>, k, a);
   if (e != cudaSuccess || ctas < 2) return e;
   // (the last CTA's items end with it)
-  // a warp per row where there are many rows, up to a block's eight where there are few
+  // a warp per row where there are many rows, up to a block's eight where there are few (1 x 131077 positions, 64/8 heads, eight:
+  // 48.7 us, one: 56.7; 56 ragged, 32/8, by this rule: 92.2, eight: 92.9, one: 94.2)
   const int64_t cuts = ctas - 1 < items ? ctas - 1 : items, rows = a.G;
   int per = kKv8MergeWarps;
   while (per > 1 && cuts * ((rows * per + kKv8MergeWarps - 1) / kKv8MergeWarps) > 4 * setup.sms) per /= 2;
