@@ -123,9 +123,10 @@ __device__ __forceinline__ float2 kv8_turn_fast(uint64_t phase, int pos) {
 // several kv heads one after the other, the next one's rows on the way; the page's exponent needs all rows of a head before the
 // first code.  A thread has 32 values: of K 4 dimensions of 8 positions (cos and sin of the page's positions stand in
 // shared memory for all heads, and four threads exchange their codes for runs of 16), of V 2 dimensions of 16 positions (a run each).
-//   A key is rotated in fp32, which is off by less than d = 1.25 2^-22 (|x| + |y|) of its pair (kUnsure); where x + d and x - d have
-// different codes (about one value in 10^4), or the largest magnitude of a warp lies that near to where the exponent changes, the warp
-// takes those rows again to 2^-45.
+//   A key is rotated in fp32, which is off by less than d = 1.25 2^-22 (|x| + |y|) of its pair (kUnsure).  Where x + d and x - d have
+// different codes (about one value in 10^4), the warp puts the key on a list and forms it again to 2^-45 when all heads are through,
+// one key a lane, in place of 1000 cycles and more that the other warps would wait for at the next head's barrier; where
+// the largest magnitude of a warp lies that near to where the exponent changes, or the list is full, it does so at once.
 // read: a warp handles K or V of 16 positions of one sequence and kv head.
 
 struct Kv8Rot {
@@ -223,6 +224,7 @@ struct Kv8AppendShared {
   uint64_t phase[HD / 2];
   int exp[2][NT / 32];
   uint32_t lo[2][kGroups * HD / 2], hi[2][kGroups * HD / 2];   // f16 pairs
+  uint32_t later[NT / 32][32];                      // a warp's keys to be formed again: step, lane, position of eight
 };
 extern __shared__ __align__(16) float kv8_turns[];   // [position of the page][pair / 2]: cos of both pairs, sin of both
 
@@ -243,6 +245,18 @@ __device__ __noinline__ void kv8_exact_keys(const T* from, int64_t row_stride, u
     out[4 * i + 2] = kv8_held(y.z) ? y.z : NAN;
     out[4 * i + 3] = kv8_held(y.w) ? y.w : NAN;
   }
+}
+
+// The key quad at `from` to 2^-45, as codes.
+template <class T>
+__device__ __forceinline__ uint32_t kv8_exact_codes(const T* from, bool turned, const uint64_t* phase, int pos, float up) {
+  float4 y = Kv8Quad<T>::get(from);
+  if (turned) {
+    kv8_rotate(kv8_turn(phase[0], pos), y.x, y.y);
+    kv8_rotate(kv8_turn(phase[1], pos), y.z, y.w);
+  }
+  auto held = [&](float x) { return kv8_held(x) ? x * up : NAN; };
+  return kv8_code4(held(y.x), held(y.y), held(y.z), held(y.w));
 }
 
 template <class T> struct Kv8Raw;   // what a thread has of a head as it comes: 8 times 4 (K) or 16 times 2 (V) elements
@@ -371,6 +385,8 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
   const bool busy = __any_sync(0xffffffffu, me.live != 0u);            // the warp has new positions
   // The page's bounds of a head, two dimensions a thread, are put together behind the next head's barrier: one barrier a head.
   const bool two = !V && th < HD / 2;
+  const int g0 = g;
+  int later = 0;                                                       // keys on the warp's list
   int8_t* bounds = nullptr;                                            // of the head before (nullptr: none)
   char2 lo_was = make_char2(0, 0), hi_was = lo_was;
   float f_was = 1.f;
@@ -385,7 +401,8 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
     }
     auto bound = [&](int j, int lo0, int hi0, int8_t& l1, int8_t& h1) {
       const float l = __half2float(__ushort_as_half(uint16_t(least >> (16 * j)))), h = __half2float(__ushort_as_half(uint16_t(most >> (16 * j))));
-      int lo1 = l != l ? -127 : int(floorf(l * 0.25f)), hi1 = l != l ? 127 : int(ceilf(h * 0.25f));
+      // (infinities where every row's key is on a list)
+      int lo1 = l != l ? -127 : min(int(floorf(l * 0.25f)), 127), hi1 = l != l ? 127 : max(int(ceilf(h * 0.25f)), -127);
       if (!me.fresh) {
         if (lo0 != -127) lo0 = int(floorf(lo0 * f_was));
         if (hi0 != 127) hi0 = int(ceilf(hi0 * f_was));
@@ -467,7 +484,7 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
       if (on) kv8_put_v<HD>(me, x, me.base + L.v(g), up, again, f);
     } else {
       uint32_t lo[2] = {0x7c007c00u, 0x7c007c00u}, hi[2] = {0xfc00fc00u, 0xfc00fc00u};   // bounds of this thread's positions
-      uint32_t w[8] = {};
+      uint32_t w[8] = {}, mine = me.live;                              // mine: of whose keys the codes are right
       if (busy) {
       uint32_t z[8], differ = 0u;                                      // codes of a position's 4 dimensions, of x - d and x + d
       const uint64_t up2 = kv8_pack(up, up), off = kv8_pack(up * kUnsure, up * kUnsure), minus = kv8_pack(up * -kUnsure, up * -kUnsure);
@@ -492,19 +509,31 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
           for (int i = 0; i < 8; i++) differ |= uint32_t(w[i] != z[i]) << i;
         }
       }
-      differ = __reduce_or_sync(0xffffffffu, differ);
-      if (differ) {
-        float y[32];
-        kv8_exact_keys(from, me.row_stride, on ? me.live & differ : 0u, turned, sh.phase + me.d0 / 2, me.pos0, y);
+      differ &= on ? me.live : 0u;                                     // (a zero of no row may differ in its sign)
+      if (__any_sync(0xffffffffu, differ != 0u)) {
+        const int more = __reduce_add_sync(0xffffffffu, __popc(differ));
+        if (later + more <= 32) {
+          mine &= ~differ;
+#pragma unroll 1
+          for (int i = 0; i < 8; i++) {
+            const uint32_t m = __ballot_sync(0xffffffffu, differ >> i & 1u);
+            if (differ >> i & 1u) sh.later[t >> 5][later + __popc(m & ((1u << lane) - 1u))] = uint32_t(step << 8 | lane << 3 | i);
+            later += __popc(m);
+          }
+        } else {
+          const uint32_t again_in = __reduce_or_sync(0xffffffffu, differ);
+          float y[32];
+          kv8_exact_keys(from, me.row_stride, on ? me.live & again_in : 0u, turned, sh.phase + me.d0 / 2, me.pos0, y);
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-          if (on && (me.live & differ) >> i & 1u) w[i] = kv8_code4(y[4 * i] * up, y[4 * i + 1] * up, y[4 * i + 2] * up, y[4 * i + 3] * up);
+          for (int i = 0; i < 8; i++)
+            if (on && (me.live & again_in) >> i & 1u) w[i] = kv8_code4(y[4 * i] * up, y[4 * i + 1] * up, y[4 * i + 2] * up, y[4 * i + 3] * up);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 8; i++) {
         uint32_t y[2];
         kv8_half4(w[i], y[0], y[1]);
-        if (me.has(i)) {
+        if (mine >> i & 1u) {
 #pragma unroll
           for (int j = 0; j < 2; j++) {
             lo[j] = kv8_min2(lo[j], y[j]);
@@ -524,6 +553,34 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
   if (!V) {
     __syncthreads();
     join_bounds((steps - 1) & 1);
+    if (!__syncthreads_or(later)) return;
+    if (lane >= later) return;
+    // a key of this warp's: the codes in their places, and the bounds (which other warps' keys may reach too)
+    const uint32_t what = sh.later[t >> 5][lane];
+    const int of = (t & ~31) | int(what >> 3 & 31u), th1 = of % tph, g1 = g0 + (of / tph - hp) + int(what >> 8) * abreast;
+    const int d1 = 4 * (th1 % (HD / 4)), p1 = 8 * (th1 / (HD / 4)) + int(what & 7u);
+    const T* from = src + int64_t(p1 - me.p0) * me.row_stride + (d1 - me.d0) + int64_t(g1) * head_stride;
+    const int e = *reinterpret_cast<const int8_t*>(me.base + L.exps(g1));
+    const uint32_t w = kv8_exact_codes(from, turned, sh.phase + d1 / 2, me.pos0 - me.p0 + p1, kv8_exp2i(-e));
+    *reinterpret_cast<uint32_t*>(me.base + L.k(g1) + kv8_k_at(HD, p1, d1 >> 4) + (d1 & 15)) = w;
+    uint32_t y[2], least = 0u, most = 0u;
+    kv8_half4(w, y[0], y[1]);
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const float x = __half2float(__ushort_as_half(uint16_t(y[j / 2] >> (16 * (j & 1)))));
+      least |= uint32_t(uint8_t(x != x ? -127 : int(floorf(x * 0.25f)))) << (8 * j);
+      most |= uint32_t(uint8_t(x != x ? 127 : int(ceilf(x * 0.25f)))) << (8 * j);
+    }
+    auto join = [](uint32_t* at, uint32_t x, bool up) {
+      uint32_t is = *reinterpret_cast<volatile uint32_t*>(at), was;
+      do {
+        was = is;
+        is = atomicCAS(at, was, up ? __vmaxs4(was, x) : __vmins4(was, x));
+      } while (is != was);
+    };
+    uint32_t* at = reinterpret_cast<uint32_t*>(me.base + L.bounds(g1) + d1);
+    join(at, least, false);
+    join(at + HD / 4, most, true);
   }
 }
 
