@@ -126,7 +126,8 @@ __device__ __forceinline__ float2 kv8_turn_fast(uint64_t phase, int pos) {
 //   A key is rotated in fp32, which is off by less than d = 1.25 2^-22 (|x| + |y|) of its pair (kUnsure).  Where x + d and x - d have
 // different codes (about one value in 10^4), the warp puts the key on a list and forms it again to 2^-45 when all heads are through,
 // one key a lane, in place of 1000 cycles and more that the other warps would wait for at the next head's barrier; where
-// the largest magnitude of a warp lies that near to where the exponent changes, or the list is full, it does so at once.
+// the largest magnitude of a warp lies that near to where the exponent changes, the list is full or there is one head only, it
+// does so at once.
 // read: a warp handles K or V of 16 positions of one sequence and kv head.
 
 struct Kv8Rot {
@@ -512,7 +513,7 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
       differ &= on ? me.live : 0u;                                     // (a zero of no row may differ in its sign)
       if (__any_sync(0xffffffffu, differ != 0u)) {
         const int more = __reduce_add_sync(0xffffffffu, __popc(differ));
-        if (later + more <= 32) {
+        if (steps > 1 && later + more <= 32) {
           mine &= ~differ;
 #pragma unroll 1
           for (int i = 0; i < 8; i++) {
@@ -599,10 +600,12 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) k_kv8_append(Kv4 c, Kv4
     kv8_rotate_q<HD, T>(c, a, r, sh.phase, q, id - pages);
     return;
   }
-  const bool is_v = id & 1;
-  const int P = c.page_len, split = int(id / 2 % r.splits);
+  // K first: a CTA of it takes longer (16000 f16 rows, 8 heads of 128: 36 us; K and V by turns: 46)
+  const bool is_v = id >= pages / 2;
+  const int64_t part = is_v ? id - pages / 2 : id;
+  const int P = c.page_len, split = int(part % r.splits);
   Kv4Span sp;
-  if (!kv4_span(c, a, int(id / 2 / r.splits), &sp, P)) return;
+  if (!kv4_span(c, a, int(part / r.splits), &sp, P)) return;
   const Kv8Page L(c);
   const int tph = P * HD / 32, th = t % tph, abreast = NT / tph;      // threads of a head, heads side by side
   Kv8Mine me;
