@@ -106,14 +106,14 @@ __device__ __forceinline__ void kv8_rotate(const Kv8Point& t, float& a, float& b
   a = x;
 }
 
-// cos and sin to fp32's last bit (within 2^-24.9 of 1)
-__device__ __forceinline__ float2 kv8_turn_fast(uint64_t phase, int pos) {
+// cos and sin to fp32's last bit (within 2^-24.9 of 1); `circle`: a copy of the points in shared memory
+__device__ __forceinline__ float2 kv8_turn_fast(const Kv8Point* circle, uint64_t phase, int pos) {
   const uint64_t turn = phase * uint64_t(uint32_t(pos));
   const uint32_t i = uint32_t((turn + (1ull << 55)) >> 56) & 255u;
   constexpr float k = float(6.283185307179586477 * 0x1p-32);
   const float r = float(int32_t(uint32_t(turn >> 32) - (i << 24))) * k, q = r * r;
   const float s = fmaf(r * q, -1.f / 6.f, r), m = q * fmaf(q, 1.f / 24.f, -0.5f);
-  const float4 at = *reinterpret_cast<const float4*>(&kKv8Circle.p[i]);
+  const float4 at = *reinterpret_cast<const float4*>(&circle[i]);
   return make_float2(at.x + fmaf(at.x, m, fmaf(-at.z, s, at.y)), at.z + fmaf(at.z, m, fmaf(at.x, s, at.w)));
 }
 
@@ -225,6 +225,7 @@ struct Kv8AppendShared {
   uint64_t phase[HD / 2];
   int exp[2][NT / 32];
   uint32_t lo[2][kGroups * HD / 2], hi[2][kGroups * HD / 2];   // f16 pairs
+  Kv8Point circle[256];
   uint32_t later[NT / 32][32];                      // a warp's keys to be formed again: step, lane, position of eight
 };
 extern __shared__ __align__(16) float kv8_turns[];   // [position of the page][pair / 2]: cos of both pairs, sin of both
@@ -590,8 +591,11 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) k_kv8_append(Kv4 c, Kv4
                                                                                          const T* q) {
   __shared__ Kv8AppendShared<HD, NT> sh;
   const int t = threadIdx.x;
-  if (r.on)
+  if (r.on) {
     for (int i = t; i < HD / 2; i += NT) sh.phase[i] = r.phase[i];
+    // (lookups that differ by lane, 16 a thread, take 8000 cycles a CTA out of global memory)
+    for (int i = t; i < 256; i += NT) sh.circle[i] = kKv8Circle.p[i];
+  }
   kv4_dependent();
   if (kv4_check_rows(c, a)) return;
   const int64_t id = int64_t(blockIdx.x) - a.checks, pages = int64_t(a.units) * r.splits * 2;
@@ -622,14 +626,14 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) k_kv8_append(Kv4 c, Kv4
   const int g = split * r.per * abreast + t / tph;
   const int left = (c.n_kv - split * r.per * abreast + abreast - 1) / abreast, steps = left < r.per ? left : r.per;
   const T* src = (is_v ? v : k) + int64_t(sp.row - sp.first + me.p0) * a.row_stride + me.d0;
+  const int page = c.table[int64_t(sp.s) * c.max_pages + sp.p0 / P];
   uint32_t raw[Kv8Raw<T>::kWords];                                    // (on the way while the page is looked up)
   if (is_v) kv8_load<T, true>(me, src + int64_t(g) * a.head_stride, g < c.n_kv, raw);
   else kv8_load<T, false>(me, src + int64_t(g) * a.head_stride, g < c.n_kv, raw);
-  const int page = c.table[int64_t(sp.s) * c.max_pages + sp.p0 / P];
   if (!is_v && r.on) {
     __syncthreads();   // the phases
     for (int i = t + sp.first * (HD / 2); i < sp.last * (HD / 2); i += NT) {
-      const float2 z = kv8_turn_fast(sh.phase[i % (HD / 2)], sp.p0 + i / (HD / 2));
+      const float2 z = kv8_turn_fast(sh.circle, sh.phase[i % (HD / 2)], sp.p0 + i / (HD / 2));
       kv8_turns[(i >> 1) * 4 + (i & 1)] = z.x;
       kv8_turns[(i >> 1) * 4 + (i & 1) + 2] = z.y;
     }
