@@ -107,8 +107,7 @@ __device__ __forceinline__ void kv8_rotate(const Kv8Point& t, float& a, float& b
 }
 
 // cos and sin to fp32's last bit (within 2^-24.9 of 1); `circle`: a copy of the points in shared memory
-__device__ __forceinline__ float2 kv8_turn_fast(const Kv8Point* circle, uint64_t phase, int pos) {
-  const uint64_t turn = phase * uint64_t(uint32_t(pos));
+__device__ __forceinline__ float2 kv8_turn_fast(const Kv8Point* circle, uint64_t turn) {
   const uint32_t i = uint32_t((turn + (1ull << 55)) >> 56) & 255u;
   constexpr float k = float(6.283185307179586477 * 0x1p-32);
   const float r = float(int32_t(uint32_t(turn >> 32) - (i << 24))) * k, q = r * r;
@@ -119,16 +118,21 @@ __device__ __forceinline__ float2 kv8_turn_fast(const Kv8Point* circle, uint64_t
 
 // ------------------------------------------------------------ append, read --
 //
-// append: a CTA takes the K or the V of one page of one sequence, the rows that fall on its positions, for
-// several kv heads one after the other, the next one's rows on the way; the page's exponent needs all rows of a head before the
-// first code.  A thread has 32 values: of K 4 dimensions of 8 positions (cos and sin of the page's positions stand in
-// shared memory for all heads, and four threads exchange their codes for runs of 16), of V 2 dimensions of 16 positions (a run each).
-//   A key is rotated in fp32, which is off by less than d = 1.25 2^-22 (|x| + |y|) of its pair (kUnsure).  Where x + d and x - d have
-// different codes (about one value in 10^4), the warp puts the key on a list and forms it again to 2^-45 when all heads are through,
-// one key a lane, in place of 1000 cycles and more that the other warps would wait for at the next head's barrier; where
-// the largest magnitude of a warp lies that near to where the exponent changes, the list is full or there is one head only, it
-// does so at once.
-// read: a warp handles K or V of 16 positions of one sequence and kv head.
+// append: a CTA takes the K or the V of one page of one sequence, the rows that fall on its positions, for several kv heads
+// one after the other, the next one's rows on the way; the page's exponent needs all rows of a head before the first code.  A
+// thread has 32 values: of K 4 dimensions of 8 positions (cos and sin of the page's positions stand in shared memory for
+// all heads, and four threads exchange their codes for runs of 16), of V 2 dimensions of 16 positions (a run each).
+//   A key is rotated in fp32, which is off by less than d = 1.25 2^-22 (|x| + |y|) of its pair (kUnsure).  Where x + d and
+// x - d have different codes (about one value in 10^4), the warp puts the key on a list and forms it again to 2^-45 when all
+// heads are through, one key a lane, in place of 1000 cycles and more that the other warps would wait for at the next head's
+// barrier; where the largest magnitude of a warp lies that near to where the exponent changes, the list is full or there is one
+// head only, it does so at once.
+//   What bounds it: 2 x 20011 f16 rows, 8 heads of 128, pages of 64 (247 MB in and out): 82 us, 3.0 TB/s.  A page's K takes a CTA
+// 37,000 cycles, 8000 of them before the first head (its rows and page looked up, cos and sin), V 24,500; while V pages are
+// stored, memory is the bound (6 TB/s of reads and writes), while K pages are, instructions and a barrier a head; and 626 pages are
+// little more than two rounds of 304 CTAs.  (More rows on the way, four heads by cp.async: 85; 3 CTAs an SM, 80 registers, spills: no gain;
+// 16 positions of a head in a warp, the first form: 199.)  1 token: 4.5 us, a launch and five dependent reads.
+// read: a warp handles K or V of 16 positions of one sequence and kv head; 2 x 20011 f16 rows: 40.6 us, 6.0 TB/s.
 
 struct Kv8Rot {
   uint64_t phase[64];   // turns per position, as 64-bit fractions
@@ -257,8 +261,7 @@ __device__ __forceinline__ uint32_t kv8_exact_codes(const T* from, bool turned, 
     kv8_rotate(kv8_turn(phase[0], pos), y.x, y.y);
     kv8_rotate(kv8_turn(phase[1], pos), y.z, y.w);
   }
-  auto held = [&](float x) { return kv8_held(x) ? x * up : NAN; };
-  return kv8_code4(held(y.x), held(y.y), held(y.z), held(y.w));
+  return kv8_code4(kv8_scaled(y.x, up), kv8_scaled(y.y, up), kv8_scaled(y.z, up), kv8_scaled(y.w, up));
 }
 
 template <class T> struct Kv8Raw;   // what a thread has of a head as it comes: 8 times 4 (K) or 16 times 2 (V) elements
@@ -632,10 +635,17 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) k_kv8_append(Kv4 c, Kv4
   else kv8_load<T, false>(me, src + int64_t(g) * a.head_stride, g < c.n_kv, raw);
   if (!is_v && r.on) {
     __syncthreads();   // the phases
-    for (int i = t + sp.first * (HD / 2); i < sp.last * (HD / 2); i += NT) {
-      const float2 z = kv8_turn_fast(sh.circle, sh.phase[i % (HD / 2)], sp.p0 + i / (HD / 2));
-      kv8_turns[(i >> 1) * 4 + (i & 1)] = z.x;
-      kv8_turns[(i >> 1) * 4 + (i & 1) + 2] = z.y;
+    constexpr int kSide = NT / (HD / 2);                               // positions side by side
+    const int pair = t % (HD / 2);
+    const uint64_t phase = sh.phase[pair], step = phase * kSide;
+    int p = sp.first + t / (HD / 2);
+    uint64_t turn = phase * uint64_t(uint32_t(sp.p0 + p));
+    float* to = kv8_turns + (pair >> 1) * 4 + (pair & 1);
+#pragma unroll 4
+    for (; p < sp.last; p += kSide, turn += step) {
+      const float2 z = kv8_turn_fast(sh.circle, turn);
+      to[p * HD] = z.x;
+      to[p * HD + 2] = z.y;
     }
     __syncthreads();
   }

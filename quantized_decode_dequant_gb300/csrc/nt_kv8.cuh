@@ -9,9 +9,8 @@
 namespace nt {
 
 constexpr int kKv8MaxGroup = 16;                   // query heads per kv head
-constexpr int kKv8MinExp = -100, kKv8MaxExp = 100;
+constexpr int kKv8MinExp = -100;
 constexpr float kKv8Most = 448.f * 0x1p100f;       // largest magnitude that can be held
-constexpr uint32_t kKv8Nan = 0x7f;                 // the code NaN (0xff too)
 
 // Offsets inside a page.  Per kv head: K codes, V codes; behind all of them per kv head
 // the exponents (16 bytes, two used) and the bounds lo [hd], hi [hd].
@@ -53,7 +52,7 @@ __device__ __forceinline__ uint32_t kv8_code2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// the same for a page of exponent e (up = 2^-e)
+// what is coded of a value in a page of exponent e (up = 2^-e)
 __device__ __forceinline__ float kv8_scaled(float x, float up) { return kv8_held(x) ? x * up : NAN; }
 __device__ __forceinline__ float2 kv8_value2(uint32_t codes) {
   uint32_t h;
