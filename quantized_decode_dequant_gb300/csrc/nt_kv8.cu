@@ -29,6 +29,7 @@ nt_status kv8_check(const nt_kv8_cache* c, const char* who, bool pointers, Kv4* 
 struct __align__(16) Kv8Point {
   float c, cl, s, sl;   // cos, sin: the sums of two terms
 };
+// (`circle` below: a copy of the points in shared memory)
 struct Kv8Circle {
   Kv8Point p[256];
 };
@@ -62,7 +63,7 @@ __device__ __forceinline__ float kv8_rest(float a, float b, float hi) {
   const float bb = __fsub_rn(hi, a);
   return __fadd_rn(__fsub_rn(a, __fsub_rn(hi, bb)), __fsub_rn(b, bb));
 }
-__device__ __forceinline__ Kv8Point kv8_turn(uint64_t phase, int pos) {
+__device__ __forceinline__ Kv8Point kv8_turn(const Kv8Point* circle, uint64_t phase, int pos) {
   const uint64_t turn = phase * uint64_t(uint32_t(pos));
   const uint32_t i = uint32_t((turn + (1ull << 55)) >> 56) & 255u;
   const int64_t rest = int64_t(turn - (uint64_t(i) << 56));                  // in [-2^55, 2^55)
@@ -75,7 +76,7 @@ __device__ __forceinline__ Kv8Point kv8_turn(uint64_t phase, int pos) {
   // sin r and cos r - 1
   const float s = r, sl = __fsub_rn(rl, __fmul_rn(__fmul_rn(q, r), __fmaf_rn(q, -1.f / 120.f, 1.f / 6.f)));
   const float m = -0.5f * q, ml = __fmaf_rn(__fmul_rn(q, q), __fmaf_rn(q, -1.f / 720.f, 1.f / 24.f), -0.5f * ql);
-  const float4 at = *reinterpret_cast<const float4*>(&kKv8Circle.p[i]);
+  const float4 at = *reinterpret_cast<const float4*>(&circle[i]);
   const float C = at.x, Cl = at.y, S = at.z, Sl = at.w;
   auto times = [](float x, float xl, float y, float yl, float& p) {          // (x + xl) (y + yl) = p + the rest
     p = __fmul_rn(x, y);
@@ -106,7 +107,7 @@ __device__ __forceinline__ void kv8_rotate(const Kv8Point& t, float& a, float& b
   a = x;
 }
 
-// cos and sin to fp32's last bit (within 2^-24.9 of 1); `circle`: a copy of the points in shared memory
+// cos and sin to fp32's last bit (within 2^-24.9 of 1)
 __device__ __forceinline__ float2 kv8_turn_fast(const Kv8Point* circle, uint64_t turn) {
   const uint32_t i = uint32_t((turn + (1ull << 55)) >> 56) & 255u;
   constexpr float k = float(6.283185307179586477 * 0x1p-32);
@@ -137,6 +138,7 @@ __device__ __forceinline__ float2 kv8_turn_fast(const Kv8Point* circle, uint64_t
 struct Kv8Rot {
   uint64_t phase[64];   // turns per position, as 64-bit fractions
   int32_t on, heads;
+  int32_t q_heads;      // that a warp rotates, a multiple of 4
   int32_t splits, per;  // CTAs that share a page's kv heads, and heads (times those side by side) that each takes
   int64_t q_stride, out_stride;
   float* out;
@@ -147,7 +149,10 @@ struct Kv8Rot {
 // 128 a CTA: 500 rows 7.7, 9.5, 13.4, 20; 2000 rows 13.2, 10.7, 13.3, 21; 8000 rows 37, 28.5, 27.0, 27.9; 2 x 20011 rows
 // 173, 122, 98, 88; 64 sequences of 1 row 22, 16.6, 14.2, 19.8.)
 constexpr int kKv8AppendCtas = 3 * 152;
-constexpr int kKv8QHeads = 4;   // heads that a warp rotates
+// Query heads that a warp rotates at its row's position (whose cos and sin cost as much as 4 heads): 16 or 8 where that leaves as many warps as
+// this, else 4.  (us with 4, 8 and 16, heads of 128 in fp32: 100 rows of 32 heads 6.5, 6.1, 6.2; 500 of 64 12.5, 11.5, 11.9; 2000 of
+// 32 30, 27.7, 26.5; 9000 of 64 213, 180, 159.)
+constexpr int kKv8QWarps16 = 152 * 16, kKv8QWarps8 = 152;
 
 template <class T> struct Kv8Quad;   // four elements of a source
 template <> struct Kv8Quad<float> {
@@ -185,25 +190,32 @@ __device__ __forceinline__ int kv8_row_pos(const Kv4& c, const Kv4Rows& a, int r
 }
 
 template <int HD, class T>
-__device__ __forceinline__ void kv8_rotate_q(const Kv4& c, const Kv4Rows& a, const Kv8Rot& r, const uint64_t* phase, const T* q,
-                                             int64_t id) {
-  constexpr int kLanes = HD / 4;           // of a head
-  const int lane = threadIdx.x & 31, groups = (r.heads + kKv8QHeads - 1) / kKv8QHeads;
+__device__ __forceinline__ void kv8_rotate_q(const Kv4& c, const Kv4Rows& a, const Kv8Rot& r, const Kv8Point* circle, const uint64_t* phase,
+                                             const T* q, int64_t id) {
+  constexpr int kLanes = HD / 4, kSide = 32 / kLanes, kFew = 4 / kSide;   // lanes of a head, heads side by side, on the way together
+  const int lane = threadIdx.x & 31, groups = (r.heads + r.q_heads - 1) / r.q_heads;
   const int64_t unit = id * (blockDim.x / 32) + (threadIdx.x >> 5);
   if (unit >= int64_t(a.n_rows) * groups) return;
-  const int row = int(unit / groups), h0 = int(unit % groups) * kKv8QHeads;
+  const int row = int(unit / groups), h0 = int(unit % groups) * r.q_heads, h1 = min(h0 + r.q_heads, r.heads);
   const int pos = kv8_row_pos(c, a, row);
   if (pos < 0) return;
   const int i = lane % kLanes;
-  const Kv8Point t0 = kv8_turn(phase[2 * i], pos), t1 = kv8_turn(phase[2 * i + 1], pos);
+  const Kv8Point t0 = kv8_turn(circle, phase[2 * i], pos), t1 = kv8_turn(circle, phase[2 * i + 1], pos);
+  const T* from = q + int64_t(row) * r.q_stride + 4 * i;
+  float* to = r.out + int64_t(row) * r.out_stride + 4 * i;
+#pragma unroll 1
+  for (int h = h0 + lane / kLanes; h < h1; h += 4) {
+    float4 x[kFew];
 #pragma unroll
-  for (int y = 0; y < kKv8QHeads; y += 32 / kLanes) {
-    const int h = h0 + y + lane / kLanes;
-    if (h >= r.heads) break;
-    float4 x = Kv8Quad<T>::get(q + int64_t(row) * r.q_stride + h * HD + 4 * i);
-    kv8_rotate(t0, x.x, x.y);
-    kv8_rotate(t1, x.z, x.w);
-    *reinterpret_cast<float4*>(r.out + int64_t(row) * r.out_stride + h * HD + 4 * i) = x;
+    for (int y = 0; y < kFew; y++)
+      if (h + y * kSide < h1) x[y] = Kv8Quad<T>::get(from + (h + y * kSide) * HD);
+#pragma unroll
+    for (int y = 0; y < kFew; y++) {
+      if (h + y * kSide >= h1) break;
+      kv8_rotate(t0, x[y].x, x[y].y);
+      kv8_rotate(t1, x[y].z, x[y].w);
+      *reinterpret_cast<float4*>(to + (h + y * kSide) * HD) = x[y];
+    }
   }
 }
 
@@ -236,15 +248,16 @@ extern __shared__ __align__(16) float kv8_turns[];   // [position of the page][p
 
 // Keys of the positions in `which` (of 8; 4 dimensions each) to 2^-45, into out [8][4].
 template <class T>
-__device__ __noinline__ void kv8_exact_keys(const T* from, int64_t row_stride, uint32_t which, bool turned, const uint64_t* phase, int pos0,
+__device__ __noinline__ void kv8_exact_keys(const T* from, int64_t row_stride, uint32_t which, bool turned, const Kv8Point* circle,
+                                            const uint64_t* phase, int pos0,
                                             float* out) {
 #pragma unroll 1
   for (int i = 0; i < 8; i++) {
     if (!(which >> i & 1u)) continue;
     float4 y = Kv8Quad<T>::get(from + i * row_stride);
     if (turned) {
-      kv8_rotate(kv8_turn(phase[0], pos0 + i), y.x, y.y);
-      kv8_rotate(kv8_turn(phase[1], pos0 + i), y.z, y.w);
+      kv8_rotate(kv8_turn(circle, phase[0], pos0 + i), y.x, y.y);
+      kv8_rotate(kv8_turn(circle, phase[1], pos0 + i), y.z, y.w);
     }
     out[4 * i] = kv8_held(y.x) ? y.x : NAN;
     out[4 * i + 1] = kv8_held(y.y) ? y.y : NAN;
@@ -255,11 +268,12 @@ __device__ __noinline__ void kv8_exact_keys(const T* from, int64_t row_stride, u
 
 // The key quad at `from` to 2^-45, as codes.
 template <class T>
-__device__ __forceinline__ uint32_t kv8_exact_codes(const T* from, bool turned, const uint64_t* phase, int pos, float up) {
+__device__ __forceinline__ uint32_t kv8_exact_codes(const T* from, bool turned, const Kv8Point* circle, const uint64_t* phase, int pos,
+                                                    float up) {
   float4 y = Kv8Quad<T>::get(from);
   if (turned) {
-    kv8_rotate(kv8_turn(phase[0], pos), y.x, y.y);
-    kv8_rotate(kv8_turn(phase[1], pos), y.z, y.w);
+    kv8_rotate(kv8_turn(circle, phase[0], pos), y.x, y.y);
+    kv8_rotate(kv8_turn(circle, phase[1], pos), y.z, y.w);
   }
   return kv8_code4(kv8_scaled(y.x, up), kv8_scaled(y.y, up), kv8_scaled(y.z, up), kv8_scaled(y.w, up));
 }
@@ -463,7 +477,7 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
         float y[32];
 #pragma unroll
         for (int i = 0; i < 32; i++) y[i] = 0.f;
-        kv8_exact_keys(from, me.row_stride, on ? me.live : 0u, turned, sh.phase + me.d0 / 2, me.pos0, y);
+        kv8_exact_keys(from, me.row_stride, on ? me.live : 0u, turned, sh.circle, sh.phase + me.d0 / 2, me.pos0, y);
 #pragma unroll
         for (int i = 0; i < 32; i++) x[i] = y[i];
       }
@@ -528,7 +542,7 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
         } else {
           const uint32_t again_in = __reduce_or_sync(0xffffffffu, differ);
           float y[32];
-          kv8_exact_keys(from, me.row_stride, on ? me.live & again_in : 0u, turned, sh.phase + me.d0 / 2, me.pos0, y);
+          kv8_exact_keys(from, me.row_stride, on ? me.live & again_in : 0u, turned, sh.circle, sh.phase + me.d0 / 2, me.pos0, y);
 #pragma unroll
           for (int i = 0; i < 8; i++)
             if (on && (me.live & again_in) >> i & 1u) w[i] = kv8_code4(y[4 * i] * up, y[4 * i + 1] * up, y[4 * i + 2] * up, y[4 * i + 3] * up);
@@ -566,7 +580,7 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
     const int d1 = 4 * (th1 % (HD / 4)), p1 = 8 * (th1 / (HD / 4)) + int(what & 7u);
     const T* from = src + int64_t(p1 - me.p0) * me.row_stride + (d1 - me.d0) + int64_t(g1) * head_stride;
     const int e = *reinterpret_cast<const int8_t*>(me.base + L.exps(g1));
-    const uint32_t w = kv8_exact_codes(from, turned, sh.phase + d1 / 2, me.pos0 - me.p0 + p1, kv8_exp2i(-e));
+    const uint32_t w = kv8_exact_codes(from, turned, sh.circle, sh.phase + d1 / 2, me.pos0 - me.p0 + p1, kv8_exp2i(-e));
     *reinterpret_cast<uint32_t*>(me.base + L.k(g1) + kv8_k_at(HD, p1, d1 >> 4) + (d1 & 15)) = w;
     uint32_t y[2], least = 0u, most = 0u;
     kv8_half4(w, y[0], y[1]);
@@ -604,7 +618,7 @@ __global__ void __launch_bounds__(NT, NT == 512 ? 1 : 2) k_kv8_append(Kv4 c, Kv4
   const int64_t id = int64_t(blockIdx.x) - a.checks, pages = int64_t(a.units) * r.splits * 2;
   if (id >= pages) {
     __syncthreads();
-    kv8_rotate_q<HD, T>(c, a, r, sh.phase, q, id - pages);
+    kv8_rotate_q<HD, T>(c, a, r, sh.circle, sh.phase, q, id - pages);
     return;
   }
   // K first: a CTA of it takes longer (16000 f16 rows, 8 heads of 128: 36 us; K and V by turns: 46)
@@ -890,7 +904,9 @@ nt_status nt_kv8_append(const nt_kv8_cache* c, int32_t layer, int32_t n, const i
         kv4_overlap(dev_seq, dev_seq ? int64_t(n) * 4 : 0, dev_q_out, ob) ||
         kv4_overlap(dev_begin, dev_begin ? int64_t(n) * 4 + 4 : 0, dev_q_out, ob))
       return bad("q_out overlaps another buffer");
-    const int64_t warps = int64_t(n_rows) * ((n_heads + kKv8QHeads - 1) / kKv8QHeads), of_cta = kv8_append_threads(k) / 32;
+    auto with = [&](int heads) { return int64_t(n_rows) * ((n_heads + heads - 1) / heads); };
+    r.q_heads = with(16) >= kKv8QWarps16 ? 16 : with(8) >= kKv8QWarps8 ? 8 : 4;
+    const int64_t warps = with(r.q_heads), of_cta = kv8_append_threads(k) / 32;
     q_ctas = (warps + of_cta - 1) / of_cta;
   }
   const int threads = kv8_append_threads(k), abreast = threads * 32 / (k.page_len * k.hd), steps = (k.n_kv + abreast - 1) / abreast;

@@ -253,6 +253,26 @@ def test_queries_are_rotated_beside_the_keys(nt, hd, heads, half):
         np.testing.assert_array_equal(tq.cpu().numpy(), got[:, :heads * hd].reshape(q.shape))
 
 
+@pytest.mark.parametrize("hd,heads,rows_each", [(64, 17, 1300), (128, 16, 1250), (128, 9, 100), (64, 24, 60)])
+def test_queries_of_many_rows(nt, hd, heads, rows_each):
+    """Rows enough for a warp to take 8 or 16 heads, the last ones not full."""
+    import torch
+    rng = np.random.default_rng(39)
+    ref = R.RefCache(1, 1, hd, 128, 24, 2, 12)
+    ref.hold([rows_each, rows_each + 7])
+    dev, freq, n = Dev(nt, ref), freqs(hd), 2 * rows_each
+    k = torch.zeros(n, 1, hd, device="cuda")
+    q = torch.from_numpy(rng.standard_normal((n, heads, hd)).astype(np.float32)).cuda()
+    out = torch.full((n + 1, heads * hd), 9.0, device="cuda")
+    dev.append(k, k, [0, rows_each, n], freq=freq, q=q, q_out=out[:n])
+    pos = np.concatenate([np.arange(rows_each), np.arange(7, rows_each + 7)])
+    want = R.rotate(q.cpu().numpy(), pos, freq)
+    big = np.abs(q.cpu().numpy()).reshape(n, heads, -1, 2).sum(-1).repeat(2, -1)
+    # one rounding of fp32 on either side, and 2^-45 of the products
+    assert (np.abs(out[:n].cpu().numpy().reshape(want.shape) - want.astype(np.float64)) <= 2 * U * np.abs(want) + 2.0 ** -40 * big).all()
+    assert (out[n] == 9).all() and int(dev.error.cpu()[0]) == 0
+
+
 @pytest.mark.parametrize("sign", [1, -1])
 def test_rotation_at_far_positions(nt, sign):
     """Positions up to 2^31 - 257 without their pages: a table row whose last page is there is enough."""
