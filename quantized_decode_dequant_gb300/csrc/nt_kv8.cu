@@ -128,11 +128,12 @@ __device__ __forceinline__ float2 kv8_turn_fast(const Kv8Point* circle, uint64_t
 // heads are through, one key a lane, in place of 1000 cycles and more that the other warps would wait for at the next head's
 // barrier; where the largest magnitude of a warp lies that near to where the exponent changes, the list is full or there is one
 // head only, it does so at once.
-//   What bounds it: 2 x 20011 f16 rows, 8 heads of 128, pages of 64 (247 MB in and out): 81 us, 3.0 TB/s.  A page's K takes a CTA
-// 37,000 cycles, 8000 of them before the first head (its rows and page looked up, cos and sin), V 24,500; while V pages are
-// stored, memory is the bound (6 TB/s of reads and writes), while K pages are, instructions and a barrier a head; and 626 pages are
-// little more than two rounds of 304 CTAs.  (More rows on the way, four heads by cp.async: 85 where it was 83.5; 3 CTAs an SM, 80 registers, spills: no gain;
-// 16 positions of a head in a warp, the first form: 199.)  1 token: 4.5 us, a launch and five dependent reads.
+//   What bounds it: 2 x 20011 f16 rows, 8 heads of 128, pages of 64 (247 MB in and out): 81 us, 3.0 TB/s.  A page's K takes a
+// CTA 37,000 cycles, 8000 of them before the first head (its rows and page looked up, cos and sin), V 24,500; while V pages
+// are stored, memory is the bound (6 TB/s of reads and writes), while K pages are, instructions and a barrier a head; and 626
+// pages are little more than two rounds of 304 CTAs.  (More rows on the way, four heads by cp.async: 85 where it was 83.5;
+// 3 CTAs an SM, 80 registers, spills: no gain; 16 positions of a head in a warp, the first form: 199.)  1 token: 4.5 us, a
+// launch and five dependent reads.
 // read: a warp handles K or V of 16 positions of one sequence and kv head; 2 x 20011 f16 rows: 40.6 us, 6.0 TB/s.
 
 struct Kv8Rot {
