@@ -133,7 +133,7 @@ __device__ __forceinline__ void kv8_pick(const uint32_t* keys, int m, int k, int
     found = s_in == left;
   }
   const int ties = found ? m : left;                     // of those equal to base, how many are taken
-  int taken = 0, equal = 0;                              // of the places before this round's
+  int taken = 0, equal = 0;                              // of the places before this pass over them
   for (int j0 = 0; j0 < m; j0 += NT * per) {
     if (m > chunk) get(j0);
     int over = 0, same = 0;
