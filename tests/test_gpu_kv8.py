@@ -202,6 +202,35 @@ def test_a_page_begun_anew_forgets_its_exponent_and_bounds(nt):
     dev.check()
 
 
+@pytest.mark.parametrize("half", [False, True])
+@pytest.mark.parametrize("hd,kv,page_len,S", [(64, 11, 32, 2), (128, 9, 64, 2), (128, 3, 128, 2), (64, 1, 16, 2), (64, 11, 32, 40), (128, 9, 64, 40),
+                                              (128, 3, 128, 60), (64, 20, 16, 50)])
+def test_keys_between_two_codes(nt, hd, kv, page_len, S, half):
+    """Keys half way between codes where the rotation leaves them (position 0), or far fewer bits long than their pair's other
+    half, zeros of both signs: more of them than are put off, in pages begun, gone on with and ended in the middle; with few
+    sequences a head in each CTA, with many several."""
+    import torch
+    rng = np.random.default_rng(40)
+    n = page_len + 5
+    ref = R.RefCache(2, kv, hd, page_len, 2 * S, S, 2)
+    dev, freq = Dev(nt, ref), freqs(hd)
+    half_way = (1 + (2 * rng.integers(0, 8, (2, S * n, kv, hd)) + 1) / 16) * 2.0 ** rng.integers(-6, 5, (2, S * n, kv, hd))
+    x = (half_way * rng.choice([-1, 1], half_way.shape)).astype(np.float32)
+    x[:, :, 0, 1::2] *= np.float32(2.0 ** -9)                  # (cos of a small angle is 1, and the sum nearly half way)
+    x[0, :, kv // 2] = rng.choice([0.0, -0.0], (S * n, hd))
+    x[0, rng.integers(0, S * n, n)] = -0.0
+    k, v = layout(torch, x, "rows", half)
+    for first, last in ((0, 1), (1, page_len - 3), (page_len - 3, n)):
+        r = last - first
+        dev.extend(range(S), [r] * S)
+        ref.extend(list(range(S)), [r] * S)
+        rows_of = (np.arange(S)[:, None] * n + np.arange(first, last)).reshape(-1)
+        begin = [r * i for i in range(S + 1)]
+        dev.append(k[rows_of].contiguous(), v[rows_of].contiguous(), begin, layer=1, freq=freq)
+        store(ref, x[:, rows_of], begin, range(S), layer=1, freq=freq)
+        dev.check()
+
+
 @pytest.mark.parametrize("rotated", [False, True])
 def test_values_that_cannot_be_held(nt, rotated):
     import torch
