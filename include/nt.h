@@ -655,7 +655,7 @@ nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, i
  * not above the one before it, or behind a negative one, gives NaN in that entry's and kv
  * head's outputs and sets NT_KV4_BAD_PAGE.  No place at all, or no position, gives zeros.
  * Statistics and sums are fp32; codes enter exactly, q with about 24 bits and the
- * softmax weights to 2^-28 of a head's largest.  Any 1 to 16 query heads per kv head
+ * softmax weights to 2^-25 of a head's largest, whatever the values' exponents.  Any 1 to 16 query heads per kv head
  * (NT_E_UNSUPPORTED beyond). */
 nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
                            const int32_t* dev_ctx, int32_t n_select, const int32_t* dev_pages, const float* dev_q,

@@ -12,7 +12,9 @@
 // digit is its own code and an and and a shift make four of them.  Every product is exact; the tensor cores add
 // with 2^-25 of the largest product dropped, and truncate sums, so a tile's outputs
 // are taken out of tensor memory and added in registers.
-//   A key's exponent multiplies its scores, a value's its weight: powers of two.  The weights are
+//   A key's exponent multiplies its scores, a value's its weight: powers of two.  What a value's exponent lies below the largest of
+// a product its weight loses in bits, so a product takes pages whose values' exponents are at most 4 apart, and a tile
+// with others several products, in each of which the other pages' weights are zero.  The weights are
 // 2^(score - m), m the head's largest score of the first tile, moved only where a later one passes it by
 // 2^3.9.  log2(e) / sqrt(hd) is multiplied into q, so that what brings a score to the exponent is a power of two
 // and the maximum and the weights see the same number however large it is.
@@ -34,6 +36,7 @@ constexpr int kKv8Batch = 512;          // entries of a launch: their first tile
 constexpr int kKv8MaxCtas = 304;        // two per SM; the workspace holds two partial results of each
 constexpr int kKv8Tile = 128;
 constexpr int kKv8MaxCluster = 16;
+constexpr int kKv8Apart = 4;            // exponents of the values of a product: at most this far apart
 
 struct Kv8AttnArgs {
   int32_t layer, n, G, k;
@@ -84,6 +87,7 @@ struct Kv8AttnCfg {
   static constexpr int kBars = (kInfo + 4 * E + 7) / 8 * 8;         // full [H], empty [H], scores, taken, weights, outputs
   static constexpr int kTmem = kBars + 8 * (2 * H + 4);
   static constexpr int kSegs = kTmem + 4;                           // items whose q is there
+  static constexpr int kMore = kTmem + 8;                           // another product of the same tile's values comes behind this one
   static constexpr int kSmem = kTmem + 16;
   static_assert(kSmem <= 113 * 1024, "two CTAs an SM");
   // tensor memory: scores, outputs (twice, so that a tile's can be taken while the next one's are formed, gained nothing)
@@ -207,6 +211,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   int2* entry = reinterpret_cast<int2*>(sm + Cfg::kEntry);
   volatile int* info = reinterpret_cast<volatile int*>(sm + Cfg::kInfo);
   volatile int* segs_ready = reinterpret_cast<volatile int*>(sm + Cfg::kSegs);
+  volatile int* more = reinterpret_cast<volatile int*>(sm + Cfg::kMore);
   const volatile uint32_t* tensor_memory = reinterpret_cast<const volatile uint32_t*>(sm + Cfg::kTmem);
   const uint32_t full = smu + Cfg::kBars, empty = full + 8 * H, bar_s = empty + 8 * H, bar_taken = bar_s + 8,
                  bar_p = bar_taken + 8, bar_o = bar_p + 8;
@@ -222,7 +227,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     kv4_bar_init(bar_p, 4);
     kv4_bar_init(bar_o);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    *segs_ready = 0;
+    *segs_ready = *more = 0;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // (tensor memory only now: a kernel that this one waits for could want it on this SM; and the right to take it goes on at
@@ -446,6 +451,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
               moved = true;
             }
           } else if (kv8_bar_test(bar_p, uint32_t(weighed) & 1u)) {
+            const bool last = !*more;
             kv8_tc_after();
             if (kv8_elect()) {
               const uint32_t v0 = smu + slot * Cfg::kSlot, p0 = smu + Cfg::kP;
@@ -454,12 +460,14 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
                 kv8_mma(tmem + Cfg::kColO, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
                         kv8_desc(p0 + kk * 4 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
               kv8_commit(bar_o);
-              kv8_commit(empty + 8 * slot);
+              if (last) kv8_commit(empty + 8 * slot);
             }
             __syncwarp();
-            has_v = false;
             weighed++;
-            np++;
+            if (last) {
+              has_v = false;
+              np++;
+            }
             moved = true;
           }
         }
@@ -608,7 +616,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         const int word = info[no % E], live = word & (Cfg::kLacks - 1);
         if (word & Cfg::kLacks) poison = true;
         if (live == 0 || fail) {
-          if (kv8_any(fail)) dead = kv8_any(fail);     // (as many barriers as a tile with scores has)
+          if (kv8_any(fail)) dead = kv8_any(fail) && kv8_any(fail);     // (as many barriers as a tile with scores has)
           poison = poison || dead;
           __syncwarp();
           if (lane == 0) kv4_bar_arrive(bar_taken);
@@ -646,9 +654,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             if (b == kParts - 1) {
               const int of = t < live ? t >> lg : 0, ek = exps[16 * of], ev = exps[16 * of + 1];
               vmax = __reduce_max_sync(0xffffffffu, (lane & 7) << lg < live ? int(exps[16 * (lane & 7) + 1]) : -128);
-              const int dv = 28 + ev - vmax;
               fk = kv8_exp2i(ek);
-              fv = dv < -126 ? 0.f : kv8_exp2i(dv);
+              fv = ev < vmax - kKv8Apart ? 0.f : kv8_exp2i(28 + ev - vmax);
             }
             kv8_tc_wait(r);
             if (b == 0) {
@@ -682,8 +689,24 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             most = fmaxf(most, p[h]);
           }
         };
+        auto weigh = [&]() {                           // the weights times fv as digits, and the product begun
+#pragma unroll
+          for (int h = 0; h < HB; h += 2) {
+            uint32_t u[2];
+#pragma unroll
+            for (int y = 0; y < 2; y++) u[y] = __float2uint_rn(p[h + y] * fv);
+            *reinterpret_cast<uint4*>(my_p + h * 64) =
+                make_uint4(u[0] & 0x0f0f0f0fu, (u[0] >> 4) & 0x0f0f0f0fu, u[1] & 0x0f0f0f0fu, (u[1] >> 4) & 0x0f0f0f0fu);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          kv8_tc_before();
+          __syncwarp();
+          if (lane == 0) kv4_bar_arrive(bar_p);
+          out_scale = kv8_exp2i(vmax - 19);            // digits are 2^-9 of themselves, weights 2^28
+          pending = 1;
+        };
         weights();
-        if (kv8_any(!(most <= 15.f) || fail)) {
+        if (kv8_any(!(most <= 15.f) || fail || fv == 0.f)) {
           // A weight may have passed 2^3.9 (at first all are infinite): the maxima over the tile's positions.
           fail = !await() || fail;
           take();
@@ -694,7 +717,8 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             const float top = kv8_join(x, [](float u, float v) { return fmaxf(u, v); });
             if (lane % (32 / HB) == 0) red[warp * HB + kv8_joined<HB>(lane)] = top;
           }
-          dead = kv8_any(fail);
+          const bool apart = kv8_any(fail || fv == 0.f);
+          dead = apart && kv8_any(fail);
 #pragma unroll
           for (int h = 0; h < HB; h++) {
             const float top = fmaxf(fmaxf(red[h], red[HB + h]), fmaxf(red[2 * HB + h], red[3 * HB + h])) * cs[h];
@@ -708,26 +732,26 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             continue;
           }
           weights();
+          // Values too small for a product with the largest ones: a product for all but the smallest.
+          while (apart) {
+            const int8_t* exps = reinterpret_cast<const int8_t*>(sm + Cfg::kExps + no % E * 8 * 16);
+            const int ev = exps[16 * (t < live ? t >> lg : 0) + 1], page = exps[16 * ((lane & 7) << lg < live ? lane & 7 : 0) + 1];
+            const int below = vmax - kKv8Apart, next = __reduce_max_sync(0xffffffffu, page < below ? page : -129);
+            if (next == -129) break;
+            if (t == 0) *more = 1;
+            weigh();
+            if (!await()) poison = true;
+            take();
+            if (t == 0) *more = 0;
+            vmax = next;
+            fv = ev >= below || ev < vmax - kKv8Apart ? 0.f : kv8_exp2i(28 + ev - vmax);
+          }
         }
-        if (!await()) poison = true;                   // (the last tile's products have read the weights before)
+        if (!await()) poison = true;                   // (the last product has read its weights)
         take();
 #pragma unroll
-        for (int h = 0; h < HB; h += 2) {
-          uint32_t u[2];
-#pragma unroll
-          for (int y = 0; y < 2; y++) {
-            l[h + y] += p[h + y];
-            u[y] = __float2uint_rn(p[h + y] * fv);
-          }
-          *reinterpret_cast<uint4*>(my_p + h * 64) =
-              make_uint4(u[0] & 0x0f0f0f0fu, (u[0] >> 4) & 0x0f0f0f0fu, u[1] & 0x0f0f0f0fu, (u[1] >> 4) & 0x0f0f0f0fu);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        kv8_tc_before();
-        __syncwarp();
-        if (lane == 0) kv4_bar_arrive(bar_p);
-        out_scale = kv8_exp2i(vmax - 19);              // digits are 2^-9 of themselves, weights 2^28
-        pending = 1;
+        for (int h = 0; h < HB; h++) l[h] += p[h];
+        weigh();
       }
       // ---- the segment's end, behind the next one's q
       if (x + count < c1) {

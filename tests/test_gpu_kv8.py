@@ -630,6 +630,55 @@ def test_exponents_of_every_size(nt):
     check_attention(dev, rng, q=(0.2 * rng.standard_normal((3, 4, 64))).astype(np.float32))
 
 
+# (kv heads, query heads, hd, page_len, columns of the table, length): a cluster per item, then tiles shared out
+APART = [(2, 4, 64, 16, 9, 129), (1, 8, 128, 32, 20, 600), (2, 32, 64, 64, 12, 700), (1, 2, 128, 64, 2, 128), (1, 2, 64, 128, 5, 600),
+         (1, 8, 128, 16, 2000, 900), (2, 4, 64, 32, 1000, 3000), (1, 16, 128, 64, 800, 1500), (2, 2, 64, 16, 700, 128),
+         (1, 5, 128, 128, 500, 1000)]
+
+
+@pytest.mark.parametrize("gap", [3, 4, 5, 8, 12, 16, 24, 32, 60, 120])
+@pytest.mark.parametrize("kv,heads,hd,page_len,columns,n", APART)
+def test_pages_whose_values_differ_by_many_powers_of_two(nt, kv, heads, hd, page_len, columns, n, gap):
+    """Every third page's values are 2^gap larger, some 2^(gap / 2), and their scores so far below the others' that they add less
+    than e^-25: the outputs are the small values' mean, to fp32's accuracy.
+
+    Allowed, relative to a head's outputs: the values have mean zero and the weights' errors know nothing of them, so relative
+    errors e of the weights move out = sum w V by e |V| w, independent from position to position: in the mean square by the
+    root mean square of e times |out|.  e is the scores' error, 12 U of their size |q||k| (24 bits of q, the losses of 4
+    instructions, 2^-25 and 2^-23 of the largest product each, and the fp32 factors), 2^-22 of the exponential, and 2^-25 of
+    the head's largest weight for the digits (2^-29 and exponents up to 4 apart), which is 2^-25 sqrt(n / sum w^2) of out, w
+    relative to the largest; a sum of 128 loses 2^-23 of itself in each of 4 instructions and U in each fp32 addition."""
+    import torch
+    rng = np.random.default_rng([41, gap, hd, heads])
+    held = -(-n // page_len)
+    ref = R.RefCache(1, kv, hd, page_len, held + 1, 1, columns)
+    ref.randomize(rng)
+    ref.hold([n], rng)
+    d, t = np.arange(hd), np.arange(page_len)[:, None]
+    for j in range(held):
+        row, up = ref.pool[0, ref.table[0, j]], gap if j % 3 == 1 else gap // 2 if j % 5 == 2 else 0
+        for g in range(kv):
+            c = R.code(rng.standard_normal((page_len, hd)) * 0.3 * (d > 0) + (d == 0) * (-8 if up else 0))
+            row[ref.k_at(g, t, d)] = c
+            row[ref.v_at(g, t, d)] = R.code(rng.standard_normal((page_len, hd)) * 100)
+            row[ref.exp_at(g, 0)], row[ref.exp_at(g, 1)] = 0, np.int8(up - min(gap, 60)).view(np.uint8)
+    q = rng.standard_normal((1, heads, hd)).astype(np.float32)
+    q[..., 0] = (gap * 0.6931 + 25) / 8 * hd ** 0.5          # (e^-25 2^-gap)
+    got = Dev(nt, ref, heads).attention(torch.from_numpy(q).cuda()).cpu().numpy()[0]
+    G = heads // kv
+    for h in range(heads):
+        k, v = ref.kv(0, 0, h // G)
+        x = q[0, h].astype(np.float64)
+        s = k @ x / hd ** 0.5
+        w = np.exp(s - s.max())
+        want = R.attend(x[None], k, v)[0][0]
+        dots = (np.abs(k) @ np.abs(x))[w > 1e-12].max() / hd ** 0.5
+        e = 12 * U * dots + 2.0 ** -22 + 2.0 ** -25 * (n / (w * w).sum()) ** 0.5
+        limit = e + 4 * 2.0 ** -23 + (n / 128 + 8) ** 0.5 * U
+        rel = np.linalg.norm(got[h] - want) / np.linalg.norm(want)
+        assert rel <= limit, (h, rel, limit)
+
+
 def test_one_strong_position_far_from_the_start(nt):
     """The reference of the weights has to move: scores rise along the sequence, and one position outweighs the rest."""
     rng = np.random.default_rng(17)
