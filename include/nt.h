@@ -654,8 +654,10 @@ nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, i
  * first min(m, n_select) places are looked at (no more can be right); one of them that is m or more,
  * not above the one before it, or behind a negative one, gives NaN in that entry's and kv
  * head's outputs and sets NT_KV4_BAD_PAGE.  No place at all, or no position, gives zeros.
- * Statistics and sums are fp32; codes enter exactly, q with about 24 bits and the
- * softmax weights to 2^-25 of a head's largest, whatever the values' exponents.  Any 1 to 16 query heads per kv head
+ * Statistics and sums are fp32; codes enter exactly, q with about 24 bits.  A softmax weight is
+ * held to 2^-25 of its head's largest, or, where its value's exponent is more than 4 above those of the tiles of 128
+ * positions before or lies that far from others of its own tile, to 2^-25 of the largest weight that goes with values of its
+ * size.  What is lost counts in the divisor: n weights below 2^-29 of the largest may take up to n 2^-29 of the outputs.  Any 1 to 16 query heads per kv head
  * (NT_E_UNSUPPORTED beyond). */
 nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
                            const int32_t* dev_ctx, int32_t n_select, const int32_t* dev_pages, const float* dev_q,

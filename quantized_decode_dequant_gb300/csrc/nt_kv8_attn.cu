@@ -14,7 +14,8 @@
 // are taken out of tensor memory and added in registers.
 //   A key's exponent multiplies its scores, a value's its weight: powers of two.  What a value's exponent lies below the largest of
 // a product its weight loses in bits, so a product takes pages whose values' exponents are at most 4 apart, and a tile
-// with others several products, in each of which the other pages' weights are zero.  The weights are
+// with others several products, in each of which the other pages' weights are zero.  In these products, and where a tile's values are
+// larger than those of a tile before, low weights may count as much as the head's largest: they are brought up to 1.  The weights are
 // 2^(score - m), m the head's largest score of the first tile, moved only where a later one passes it by
 // 2^3.9.  log2(e) / sqrt(hd) is multiplied into q, so that what brings a score to the exponent is a power of two
 // and the maximum and the weights see the same number however large it is.
@@ -79,7 +80,9 @@ struct Kv8AttnCfg {
   static constexpr int kQ = kExps + E * 8 * 16;
   static constexpr int kP = kQ + NS * HD;
   static constexpr int kRed = kP + 16 * kPStep;                      // [4][HB] of the warps, twice: maxima, sums; [2][HB] scales of q
-  static constexpr int kPrefix = kRed + 10 * HB * 4;
+  static constexpr int kTops = kRed + 10 * HB * 4;                   // [2][4][HB] maxima over the positions of a product
+  static constexpr int kLows = kTops + 8 * HB * 4;                   // [4] of each warp, see vlow
+  static constexpr int kPrefix = kLows + 16;
   static constexpr int kEntry = kPrefix + (kKv8Batch + 4) * 4;
   static constexpr int kSums = kEntry + kKv8Batch * 8;
   static constexpr int kInfo = kSums + 32;                          // [E]: positions of the tile, and kLacks: behind them a page is not there
@@ -483,13 +486,15 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
     const uint32_t mine = uint32_t(32 * warp) << 16;   // this warp's rows of tensor memory
     float* red = reinterpret_cast<float*>(sm + Cfg::kRed);
     uint8_t* my_p = sm + Cfg::kP + (t >> 3) * Cfg::kPStep + (t & 7) * 16;
-    float O[HB], l[HB], mref[HB], cs[HB];
+    float O[HB], l[HB], mref[HB], css[HB];
     uint32_t ps = 0, po = 0;
     int no = 0, segs = 0;                              // tiles; items whose q was prepared
     bool dead = false;
     // outputs of the last tile with scores: none under way, under way, there; their scale
     int pending = 0;
     float out_scale = 0.f;
+    // of the item's tiles so far: the smallest of their largest value exponents
+    volatile int* vlow = reinterpret_cast<volatile int*>(sm + Cfg::kLows) + warp;
     auto await = [&]() -> bool {                       // false: they never came
       if (pending != 1) return true;
       pending = 2;
@@ -499,12 +504,17 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       return ok;
     };
     constexpr int kTake = HB < 4 ? HB : 4;             // heads taken together
+    const uint64_t k16 = kv8_pack(16.f, 16.f), k65536 = kv8_pack(65536.f, 65536.f);
+    auto output = [&](const uint32_t* r) {             // out of the sums of a head's digits 0, 2, 4, 6, 1, 3, 5, 7
+      auto two = [&](int i) { return kv8_pack(__uint_as_float(r[i]), __uint_as_float(r[i + 1])); };
+      const float2 v = kv8_unpack(kv8_fma2(kv8_fma2(two(6), k16, two(2)), k65536, kv8_fma2(two(4), k16, two(0))));
+      return fmaf(v.y, 256.f, v.x);
+    };
     auto take = [&]() {                                // adds them to the sums
       if (pending != 2) return;
       pending = 0;
       const uint32_t from = tmem + mine + Cfg::kColO;
       if (HD == 128 || warp < 2) {
-        const uint64_t k16 = kv8_pack(16.f, 16.f), k65536 = kv8_pack(65536.f, 65536.f);
 #pragma unroll
         for (int b = 0; b < HB / kTake; b++) {
           uint32_t r[8 * kTake];
@@ -512,11 +522,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           for (int y = 0; y < kTake / 2; y++) kv8_tc_ld16(from + 8 * kTake * b + 16 * y, r + 16 * y);
           kv8_tc_wait(r);
 #pragma unroll
-          for (int h = 0; h < kTake; h++) {            // a head's digits 0, 2, 4, 6, 1, 3, 5, 7
-            auto two = [&](int i) { return kv8_pack(__uint_as_float(r[8 * h + i]), __uint_as_float(r[8 * h + i + 1])); };
-            const float2 v = kv8_unpack(kv8_fma2(kv8_fma2(two(6), k16, two(2)), k65536, kv8_fma2(two(4), k16, two(0))));
-            O[kTake * b + h] = fmaf(fmaf(v.y, 256.f, v.x), out_scale, O[kTake * b + h]);
-          }
+          for (int h = 0; h < kTake; h++) O[kTake * b + h] = fmaf(output(r + 8 * h), out_scale, O[kTake * b + h]);
         }
       }
       kv8_tc_before();
@@ -601,12 +607,15 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       at = next;
       const int count = segment(x, at);
       bool poison = dead;
+      auto cs = [&](int h) { return HB == 16 ? scales[odd * HB + h] : css[h]; };   // (16 more registers are not there)
 #pragma unroll
       for (int h = 0; h < HB; h++) {
-        cs[h] = scales[odd * HB + h];
+        css[h] = scales[odd * HB + h];
         O[h] = l[h] = 0.f;
         mref[h] = -3e38f;
       }
+      if (lane == 0) *vlow = 127;
+      __syncwarp();
 #pragma unroll 1
       for (int i = 0; i < count; i++, no++) {
         if (dead) continue;
@@ -652,10 +661,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
 #pragma unroll
             for (int y = 0; y < kCols / 16; y++) kv8_tc_ld16(tmem + mine + Cfg::kColS + b * kCols + 16 * y, r + 16 * y);
             if (b == kParts - 1) {
-              const int of = t < live ? t >> lg : 0, ek = exps[16 * of], ev = exps[16 * of + 1];
+              const int of = t < live ? t >> lg : 0, ek = exps[16 * of], ev = exps[16 * of + 1], low = *vlow;
               vmax = __reduce_max_sync(0xffffffffu, (lane & 7) << lg < live ? int(exps[16 * (lane & 7) + 1]) : -128);
               fk = kv8_exp2i(ek);
-              fv = ev < vmax - kKv8Apart ? 0.f : kv8_exp2i(28 + ev - vmax);
+              fv = ev < vmax - kKv8Apart || vmax > low + kKv8Apart ? 0.f : kv8_exp2i(28 + ev - vmax);
+              *vlow = min(vmax, low);
             }
             kv8_tc_wait(r);
             if (b == 0) {
@@ -685,19 +695,15 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           most = 0.f;
 #pragma unroll
           for (int h = 0; h < HB; h++) {
-            p[h] = kv8_ex2(fmaf(s[h], cs[h], -mref[h]));
+            p[h] = kv8_ex2(fmaf(s[h], cs(h), -mref[h]));
             most = fmaxf(most, p[h]);
           }
         };
-        auto weigh = [&]() {                           // the weights times fv as digits, and the product begun
-#pragma unroll
-          for (int h = 0; h < HB; h += 2) {
-            uint32_t u[2];
-#pragma unroll
-            for (int y = 0; y < 2; y++) u[y] = __float2uint_rn(p[h + y] * fv);
-            *reinterpret_cast<uint4*>(my_p + h * 64) =
-                make_uint4(u[0] & 0x0f0f0f0fu, (u[0] >> 4) & 0x0f0f0f0fu, u[1] & 0x0f0f0f0fu, (u[1] >> 4) & 0x0f0f0f0fu);
-          }
+        auto digits = [&](int h, uint32_t u0, uint32_t u1) {   // of two heads' weights times 2^28
+          *reinterpret_cast<uint4*>(my_p + h * 64) =
+              make_uint4(u0 & 0x0f0f0f0fu, (u0 >> 4) & 0x0f0f0f0fu, u1 & 0x0f0f0f0fu, (u1 >> 4) & 0x0f0f0f0fu);
+        };
+        auto multiply = [&]() {                        // the product with these digits
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           kv8_tc_before();
           __syncwarp();
@@ -721,7 +727,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           dead = apart && kv8_any(fail);
 #pragma unroll
           for (int h = 0; h < HB; h++) {
-            const float top = fmaxf(fmaxf(red[h], red[HB + h]), fmaxf(red[2 * HB + h], red[3 * HB + h])) * cs[h];
+            const float top = fmaxf(fmaxf(red[h], red[HB + h]), fmaxf(red[2 * HB + h], red[3 * HB + h])) * cs(h);
             const float to = top - mref[h] > 3.f ? top : mref[h], f = kv8_ex2(mref[h] - to);
             mref[h] = to;
             l[h] *= f;
@@ -731,27 +737,88 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             poison = true;
             continue;
           }
-          weights();
-          // Values too small for a product with the largest ones: a product for all but the smallest.
-          while (apart) {
+          if (apart) {
+            // Values too small for a product with the tile's largest, or larger than those of the tiles before: a product for those that go
+            // together, the largest first, with the weights of a head brought up to 1 where all are lower.  (Rare: little code, few registers; the
+            // arrays are in local memory.)
+            float x[HB], o[HB], sum[HB];
+#pragma unroll
+            for (int h = 0; h < HB; h++) {
+              x[h] = fmaf(s[h], cs(h), -mref[h]);
+              o[h] = O[h];
+              sum[h] = l[h];
+            }
             const int8_t* exps = reinterpret_cast<const int8_t*>(sm + Cfg::kExps + no % E * 8 * 16);
             const int ev = exps[16 * (t < live ? t >> lg : 0) + 1], page = exps[16 * ((lane & 7) << lg < live ? lane & 7 : 0) + 1];
-            const int below = vmax - kKv8Apart, next = __reduce_max_sync(0xffffffffu, page < below ? page : -129);
-            if (next == -129) break;
-            if (t == 0) *more = 1;
-            weigh();
-            if (!await()) poison = true;
-            take();
-            if (t == 0) *more = 0;
-            vmax = next;
-            fv = ev >= below || ev < vmax - kKv8Apart ? 0.f : kv8_exp2i(28 + ev - vmax);
+            float* tops = reinterpret_cast<float*>(sm + Cfg::kTops);
+#pragma unroll 1
+            for (int next = vmax, above = 128, other = 4 * HB; next > -129; tops += other, other = -other) {
+              vmax = next;
+              const int least = vmax - kKv8Apart;
+              const bool in = ev < above && ev >= least;
+              fv = in ? kv8_exp2i(28 + ev - vmax) : 0.f;
+              above = least;
+              next = __reduce_max_sync(0xffffffffu, page < least ? page : -129);
+              float most_of = -INFINITY, up = 0.f;       // of head `lane`
+#pragma unroll 1
+              for (int h = 0; h < HB; h++) {
+                float y = in ? x[h] : -INFINITY;
+#pragma unroll
+                for (int z = 16; z; z >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
+                if (lane == h) most_of = y;
+              }
+              if (lane < HB) tops[warp * HB + lane] = most_of;
+              kv8_any(false);
+              if (lane < HB) {
+                const float y = fmaxf(fmaxf(tops[lane], tops[HB + lane]), fmaxf(tops[2 * HB + lane], tops[3 * HB + lane]));
+                up = fminf(fmaxf(floorf(-y), 0.f), 126.f);
+              }
+              __syncwarp();
+#pragma unroll 1
+              for (int h = 0; h < HB; h += 2) {
+                uint32_t u[2];
+#pragma unroll
+                for (int y = 0; y < 2; y++) {
+                  const float z = __shfl_sync(0xffffffffu, up, h + y), w = in ? kv8_ex2(x[h + y] + z) : 0.f;
+                  sum[h + y] = fmaf(w, kv8_exp2i(-int(z)), sum[h + y]);
+                  u[y] = __float2uint_rn(w * fv);
+                }
+                digits(h, u[0], u[1]);
+              }
+              if (t == 0) *more = next > -129;
+              multiply();
+              if (!await()) poison = true;
+              pending = 0;
+#pragma unroll 1
+              for (int h = 0; h < HB && (HD == 128 || warp < 2); h += 2) {
+                uint32_t r[16];
+                kv8_tc_ld16(tmem + mine + Cfg::kColO + 8 * h, r);
+                kv8_tc_wait(r);
+#pragma unroll
+                for (int y = 0; y < 2; y++)
+                  o[h + y] = fmaf(output(r + 8 * y), out_scale * kv8_exp2i(-int(__shfl_sync(0xffffffffu, up, h + y))), o[h + y]);
+              }
+              kv8_tc_before();
+            }
+            if (lane == 0 && vmax < *vlow) *vlow = vmax;
+#pragma unroll
+            for (int h = 0; h < HB; h++) {
+              O[h] = o[h];
+              l[h] = sum[h];
+            }
+            continue;
           }
+          weights();
         }
         if (!await()) poison = true;                   // (the last product has read its weights)
         take();
 #pragma unroll
-        for (int h = 0; h < HB; h++) l[h] += p[h];
-        weigh();
+        for (int h = 0; h < HB; h += 2) {
+          l[h] += p[h];
+          l[h + 1] += p[h + 1];
+          digits(h, __float2uint_rn(p[h] * fv), __float2uint_rn(p[h + 1] * fv));
+        }
+        multiply();
       }
       // ---- the segment's end, behind the next one's q
       if (x + count < c1) {

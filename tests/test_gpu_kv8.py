@@ -679,6 +679,103 @@ def test_pages_whose_values_differ_by_many_powers_of_two(nt, kv, heads, hd, page
         assert rel <= limit, (h, rel, limit)
 
 
+@pytest.mark.parametrize("bits", [6.6, 11.5, 19.3, 22.4, 26.4, 29.2, 33.5, 45.3, 70.7, 95.2])
+@pytest.mark.parametrize("kv,heads,hd,page_len,columns,n", [
+    (1, 2, 128, 64, 20, 1200), (2, 16, 64, 16, 40, 600), (1, 16, 128, 32, 8, 250), (1, 4, 64, 128, 3, 300), (1, 8, 128, 64, 2048, 131072),
+    (1, 4, 64, 16, 2000, 30000), (2, 32, 128, 128, 400, 5000)])
+def test_many_low_weights_beside_a_large_one(nt, kv, heads, hd, page_len, columns, n, bits):
+    """One position near the start has the largest score of all heads, the others' weights lie about 2^bits below, but their values
+    are larger by as much as they are too few: the outputs are made of both parts, to fp32's accuracy.
+
+    Allowed, relative to a head's outputs: the others' common score is off by 12 U of its size, their weights by 2^-22 for the
+    exponential, and for the digits by 2^-25 where their values are more than 2^4 larger, else by 2^-29 of the largest weight,
+    rounded each its own way (3 sigma of n uniform errors); twice that, since the outputs may be smaller than the sum of their two
+    parts; a sum of 128 loses 2^-23 of itself in each of 4 instructions, and an fp32 addition U in the mean square, the
+    sum of the weights as well."""
+    import torch
+    rng = np.random.default_rng([42, int(bits), hd, heads])
+    held = -(-n // page_len)
+    ref = R.RefCache(1, kv, hd, page_len, held, 1, columns)
+    ref.hold([n], rng)
+    up = int(np.clip(round(bits - np.log2(n)), -40, 90))
+    d, t = np.arange(hd), np.arange(page_len)[:, None]
+    for j in range(held):
+        row = ref.pool[0, ref.table[0, j]]
+        for g in range(kv):
+            k = np.where(d == 0, -8.0, 0.1 * rng.standard_normal((page_len, hd)))
+            v = 100 + 30 * rng.standard_normal((page_len, hd)) * (d % 2) - 200 * (d % 3 == 0)
+            if j == 0:                                       # (no other position of its page: its values' exponent is its own)
+                k[1:, 0], k[0] = -100, 0
+                v[0] = 100 * rng.standard_normal(hd)
+            row[ref.k_at(g, t, d)], row[ref.v_at(g, t, d)] = R.code(k), R.code(v)
+            row[ref.exp_at(g, 0)], row[ref.exp_at(g, 1)] = 0, np.int8(up if j else 0).view(np.uint8)
+    q = (0.1 * rng.standard_normal((1, heads, hd))).astype(np.float32)
+    q[..., 0] = (bits + np.linspace(-0.7, 0.7, heads)) * 0.6931 / 8 * hd ** 0.5
+    got = Dev(nt, ref, heads).attention(torch.from_numpy(q).cuda()).cpu().numpy()[0]
+    G = heads // kv
+    for h in range(heads):
+        k, v = ref.kv(0, 0, h // G)
+        x = q[0, h].astype(np.float64)
+        want, alone = R.attend(x[None], k, v)[0][0], v[0]
+        digits = 2.0 ** -25 if up > 4 else 3 * 2.0 ** (bits + 1 - 29) / (3 * n) ** 0.5
+        limit = 2 * (12 * U * (bits + 1) * 0.6931 + 2.0 ** -22 + digits) + 8 * 2.0 ** -23 + 2 * (n / 128 + 8) ** 0.5 * U
+        rel = np.linalg.norm(got[h] - want) / np.linalg.norm(want)
+        assert rel <= limit, (h, rel, limit)
+        assert up < 0 or np.linalg.norm(alone - want) > 1000 * limit * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("larger", [8, 16, 24, 32])
+@pytest.mark.parametrize("nats", [20, 50, 80])
+@pytest.mark.parametrize("page_len,columns", [(16, 8), (32, 4), (64, 2), (16, 900), (32, 900), (64, 900)])
+def test_large_values_with_low_weights_in_the_same_tile(nt, page_len, columns, nats, larger):
+    """Two kinds of pages in one tile: the ones' scores lie 20 to 80 nats below, their values are 2^larger larger, so that they are
+    everything, nothing or something between.  Limits as in test_many_low_weights_beside_a_large_one."""
+    import torch
+    rng = np.random.default_rng([43, nats, larger])
+    hd, heads, n = 128, 8, 128
+    ref = R.RefCache(1, 1, hd, page_len, n // page_len, 1, columns)
+    ref.hold([n], rng)
+    d, t = np.arange(hd), np.arange(page_len)[:, None]
+    for j in range(n // page_len):
+        row = ref.pool[0, ref.table[0, j]]
+        row[ref.k_at(0, t, d)] = R.code(np.where(d == 0, -8.0 * (j % 2), 0.1 * rng.standard_normal((page_len, hd))))
+        row[ref.v_at(0, t, d)] = R.code(100 + 30 * rng.standard_normal((page_len, hd)) - 200 * (d % (2 + j % 2) == 0))
+        row[ref.exp_at(0, 0)], row[ref.exp_at(0, 1)] = 0, larger * (j % 2)
+    q = (0.1 * rng.standard_normal((1, heads, hd))).astype(np.float32)
+    q[..., 0] = (nats + np.linspace(-3, 3, heads)) / 8 * hd ** 0.5
+    got = Dev(nt, ref, heads).attention(torch.from_numpy(q).cuda()).cpu().numpy()[0]
+    k, v = ref.kv(0, 0, 0)
+    for h in range(heads):
+        want = R.attend(q[0, h][None].astype(np.float64), k, v)[0][0]
+        limit = 2 * (12 * U * (nats + 4) + 2.0 ** -22 + 2.0 ** -25) + 8 * 2.0 ** -23 + 2 * 3 * U
+        rel = np.linalg.norm(got[h] - want) / np.linalg.norm(want)
+        assert rel <= limit, (h, rel, limit)
+
+
+def test_weights_that_are_nothing_beside_the_largest(nt):
+    """Values alike, one large weight and 131071 that lie 2^29.4 below, of which no digit is left: the outputs lose what the
+    interface says, n 2^-29 of the largest weight, and no more."""
+    import torch
+    rng = np.random.default_rng(44)
+    hd, n = 128, 131072
+    ref = R.RefCache(1, 1, hd, 64, n // 64, 1, n // 64)
+    ref.randomize(rng)
+    ref.hold([n], rng)
+    d, t = np.arange(hd), np.arange(64)[:, None]
+    for j in range(n // 64):
+        row = ref.pool[0, ref.table[0, j]]
+        row[ref.k_at(0, t, d)] = R.code(np.where((t == 0) & (j == 0) & (d == 0), 8.0, 0.0))
+        row[ref.v_at(0, t, d)] = R.code(100 + 10 * rng.standard_normal((64, hd)))
+        row[ref.exp_at(0, 0)] = row[ref.exp_at(0, 1)] = 0
+    q = np.zeros((1, 8, hd), np.float32)
+    q[..., 0] = 29.4 * 0.6931472 / 8 * hd ** 0.5
+    got = Dev(nt, ref, 8).attention(torch.from_numpy(q).cuda()).cpu().numpy()[0]
+    k, v = ref.kv(0, 0, 0)
+    want = R.attend(q[0].astype(np.float64), k, v)[0]
+    rel = np.linalg.norm(got - want, axis=1) / np.linalg.norm(want, axis=1)
+    assert (rel <= n * 2.0 ** -29 + 1e-5).all()
+
+
 def test_one_strong_position_far_from_the_start(nt):
     """The reference of the weights has to move: scores rise along the sequence, and one position outweighs the rest."""
     rng = np.random.default_rng(17)
