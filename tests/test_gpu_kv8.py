@@ -478,6 +478,87 @@ def test_attention_over_many_tiles(nt, hd, kv, heads, page_len, lens):
     assert np.isfinite(got).all()
 
 
+def rel_limit(k, q, n, spread):
+    """What |got - want| / |want| over a head's outputs may be for values of mean zero that the weights' errors know nothing of:
+    relative errors e of the weights move out = sum w V by sum w e (V - out), in the mean square by the root mean square of e
+    times |out|.  e has
+    - the scores' error: 2^-24 of sum |q||k| for q's six terms (four bits each); in each of the hd / 32 instructions 33 products
+      that lose up to 2^-25 of the largest, half of it in the mean, and a sum truncated at 2^-23, which is half the final one in
+      the mean; 4 U of |s| for the scale, the sum of the terms and the exponent, U of the exponent's argument,
+    - 2^-22 of the exponential,
+    - 2^-29 of the head's largest weight, 2^spread times that where the exponents of the tile's values are so far apart.
+    A tile's sum is truncated in 4 instructions, at 2^-23 of itself each, and goes through at most n / 128 / 8 + 16 additions
+    that round to nearest, each its own way."""
+    hd = k.shape[1]
+    s, big = k @ q / hd ** 0.5, (np.abs(k) * np.abs(q)).max(1) / hd ** 0.5
+    w = np.exp(s - s.max())
+    ds = U * (np.abs(k) @ np.abs(q)) / hd ** 0.5 + hd / 32 * (33 / 2 * 2.0 ** -25 * big + 2.0 ** -23 * np.abs(s) / 2)
+    ds += 4 * U * np.abs(s) + U * np.abs(s - s.max())
+    e = (ds * ds * w * w).sum() / (w * w).sum()
+    return e ** 0.5 + 2.0 ** -22 + 2.0 ** (spread - 29) * (n / (w * w).sum()) ** 0.5 + 4 * 2.0 ** -23 + (n / 1024 + 16) ** 0.5 * U
+
+
+def in_terms(q, terms):
+    """q as so many e4m3 terms, each a sixteenth of the one before."""
+    up = 2.0 ** (7 - np.floor(np.log2(np.abs(q).max())))
+    rest, out = q * up, 0.0
+    for i in range(terms):
+        t = R.NUMBER[R.code(rest)]
+        out, rest = out + t * 16.0 ** -i, (rest - t) * 16
+    return out / up
+
+
+# (kv heads, query heads, hd, page_len, columns of the table, lengths, size of q): a cluster per item, then tiles shared out
+WHOLE = [
+    (8, 64, 128, 64, 66, [4161], 1.0), (8, 128, 128, 32, 132, [4161], 1.0), (2, 4, 64, 16, 60, [900, 129, 1, 700], 1.0),
+    (1, 2, 128, 128, 30, [3001], 2.0), (4, 64, 64, 64, 40, [2500], 1.0), (8, 32, 128, 64, 141, [9001], 1.0),
+    (1, 8, 128, 64, 2049, [131077], 1.0), (1, 16, 128, 64, 2049, [131077], 1.0), (1, 4, 128, 32, 4097, [131077], 2.0),
+    (1, 2, 128, 128, 1025, [131077], 1.0), (1, 8, 64, 16, 8193, [131077], 1.0), (1, 16, 64, 64, 2049, [131077, 40001], 1.0),
+    (3, 12, 128, 64, 400, [20011, 2047, 25000, 1], 1.0)]
+
+
+@pytest.mark.parametrize("kv,heads,hd,page_len,columns,lens,size", WHOLE)
+def test_attention_as_a_whole_misses_nothing(nt, kv, heads, hd, page_len, columns, lens, size):
+    """Weights of similar size, so that every position counts: a position left out anywhere, q in fewer terms or weights in fewer
+    bits show at several times what is allowed."""
+    import torch
+    rng = np.random.default_rng([45, kv, heads, hd, lens[0]])
+    P = sum(-(-x // page_len) for x in lens)
+    ref = R.RefCache(1, kv, hd, page_len, P, len(lens), columns)
+    c = rng.integers(0, 254, ref.pool.shape, np.uint8)
+    ref.pool[:] = c + (c >= 127)
+    at = [ref.exp_at(g, 0) for g in range(kv)]
+    for a in at:
+        ref.pool[..., a:a + 2] = rng.integers(-9, -6, ref.pool.shape[:2] + (2,)).astype(np.int8).view(np.uint8)
+    ref.hold(lens, rng)
+    q = (rng.standard_normal((len(lens), heads, hd)) * size).astype(np.float32)
+    dev = Dev(nt, ref, heads)
+    got = dev.attention(torch.from_numpy(q).cuda()).cpu().numpy()
+    assert int(dev.error.cpu()[0]) == 0
+    G, worst, seen = heads // kv, 0.0, {}
+    for i, n in enumerate(lens):
+        for g in range(kv):
+            k, v = ref.kv(0, i, g)
+            for h in range(g * G, (g + 1) * G):
+                x = q[i, h].astype(np.float64)
+                w = np.exp(k @ x / hd ** 0.5 - 2 * size)
+                want, limit = w @ v / w.sum(), rel_limit(k, x, n, 2)
+                norm = np.linalg.norm(want)
+                rel = np.linalg.norm(got[i, h] - want) / norm
+                assert rel <= limit, (n, h, rel, limit)
+                worst = max(worst, rel / limit)
+                if h % G == 0 and n > 2000:
+                    for lost in (0, n // 3, n - 1):
+                        assert np.linalg.norm((v[lost] - want) * w[lost] / (w.sum() - w[lost])) > 3 * limit * norm, (n, lost)
+                    x3 = in_terms(x, 3)
+                    w3 = np.exp(k @ x3 / hd ** 0.5 - 2 * size)
+                    few = np.rint(w / w.max() * 2.0 ** 16)
+                    for name, other in (("terms", w3 @ v / w3.sum()), ("bits", few @ v / few.sum())):
+                        seen[name] = min(seen.get(name, np.inf), np.linalg.norm(other - want) / norm / limit)
+    assert all(x > 2 for x in seen.values()), seen
+    print(f"kv {kv} heads {heads} hd {hd} page {page_len} lengths {lens}: {worst:.2f} of the limit {limit:.1e}; {seen}")
+
+
 def test_what_lies_behind_the_end_is_never_looked_at(nt):
     """The last page's other positions and all free pages hold NaN codes and the largest exponents."""
     rng = np.random.default_rng(12)
