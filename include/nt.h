@@ -580,8 +580,8 @@ typedef struct {
 nt_status nt_kv8_pool_bytes(const nt_kv8_cache* c, size_t* page_bytes, size_t* pool_bytes);
 
 /* Bytes of a workspace that serves every call below on this cache with at most n
- * listed sequences, and nt_kv8_select and nt_attention_kv8 with n_heads query heads.
- * Its contents on entry do not matter. */
+ * listed sequences (65536 for any larger n: no call takes more), and nt_kv8_select and
+ * nt_attention_kv8 with n_heads query heads.  Its contents on entry do not matter. */
 nt_status nt_kv8_workspace_bytes(const nt_kv8_cache* c, int32_t n_heads, int32_t n, size_t* bytes);
 
 /* The page operators, as nt_kv4_extend, nt_kv4_fork, nt_kv4_free, nt_kv4_copy_pages

@@ -812,6 +812,7 @@ nt_status nt_kv8_workspace_bytes(const nt_kv8_cache* c, int32_t n_heads, int32_t
   if (!bytes) return fail(NT_E_INVAL, "nt_kv8_workspace_bytes: NULL argument");
   if (n < 0 || n_heads < 1) return fail(NT_E_INVAL, "nt_kv8_workspace_bytes: n or n_heads out of range");
   if (n_heads % k.n_kv) return fail(NT_E_INVAL, "nt_kv8_workspace_bytes: n_heads must be a multiple of n_kv_heads");
+  n = n < kKv4MaxSeqs ? n : kKv4MaxSeqs;   // (no call takes more, and the sizes fit 64 bits)
   const size_t w[3] = {kv4_ws(k, n).bytes, kv8_select_ws_bytes(k, n), kv8_attn_ws_bytes(k.hd)};
   *bytes = w[0] > w[1] ? w[0] : w[1];
   if (w[2] > *bytes) *bytes = w[2];

@@ -123,6 +123,17 @@ def test_sizes(built):
     assert lib.nt_kv8_workspace_bytes(cache(), 8, 4, None) == nt.NT_E_INVAL
 
 
+def test_workspace_of_any_number_of_sequences(built):
+    """No call takes more than 65536 sequences, so more need no more; the largest sizes do not wrap round."""
+    for kw in (dict(), dict(n_kv_heads=256, page_len=16, max_pages=(1 << 27) - 16), dict(n_kv_heads=65535, page_len=16, max_pages=(1 << 27) - 16)):
+        c = cache(**kw)
+        most = nt.nt_kv8_workspace_bytes(c, c.n_kv_heads, 65536)
+        assert most >= 65536 * c.n_kv_heads * c.max_pages * 4
+        for n in (65537, 1 << 20, 1 << 28, (1 << 31) - 1):
+            assert nt.nt_kv8_workspace_bytes(c, c.n_kv_heads, n) == most
+        assert nt.nt_kv8_workspace_bytes(c, c.n_kv_heads, 1000) < most
+
+
 A, B, CTX, WS, Q, O, K, V = (1 << 24, (1 << 24) + 4096, (1 << 24) + 8192, 1 << 25, 1 << 28, 1 << 29, 1 << 30, 1 << 31)
 FREQ = [1.0 / (i + 1) for i in range(32)]
 
