@@ -267,4 +267,18 @@ __device__ __forceinline__ bool kv4_bar_wait(uint32_t bar, uint32_t parity) {
   return false;
 }
 
+// ---- tcgen05
+__device__ __forceinline__ void kv4_tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// One thread of a converged warp.  elect.sync, not a test of the thread's number: behind it the compiler knows that one thread
+// runs, and issues a product in 9 cycles instead of 45.
+__device__ __forceinline__ bool kv4_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void kv4_tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void kv4_tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
 }  // namespace nt

@@ -88,9 +88,6 @@ __device__ __forceinline__ void kv4_tc_mma(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
       : "memory");
 }
-__device__ __forceinline__ void kv4_tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
 // 16 rows x 64 columns: lane (gi, tg) has columns 4 i + tg of rows gi (r[2 i]) and gi + 8 (r[2 i + 1])
 __device__ __forceinline__ void kv4_tc_st16(uint32_t a, const uint32_t (&r)[32]) {
   asm volatile(
@@ -122,15 +119,6 @@ __device__ __forceinline__ void kv4_tc_ld16(uint32_t a, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
-// One thread of a converged warp.  elect.sync, not a test of the thread's number: behind it the compiler knows that one thread
-// runs, and issues a product in 9 cycles instead of 45.
-__device__ __forceinline__ bool kv4_elect() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void kv4_tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void kv4_tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // Barrier of a group's 128 threads; whether any of them says so.
 template <int THREADS>
 __device__ __forceinline__ bool kv4_group_any(int id, bool p) {

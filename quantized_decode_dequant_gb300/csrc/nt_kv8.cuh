@@ -46,6 +46,16 @@ __device__ __forceinline__ int kv8_exponent(float top) {
 }
 __device__ __forceinline__ bool kv8_held(float x) { return fabsf(x) <= kKv8Most; }   // (not NaN)
 
+// Sequence of entry i (seq0 + i where none are listed) and the positions that it sees (-1 and none: cannot be read, the bit in *bad).
+__device__ __forceinline__ int2 kv8_entry(const Kv4& c, const int32_t* seq, const int32_t* ctx, int seq0, int i, uint32_t* bad) {
+  const int s = seq ? seq[i] : seq0 + i;
+  *bad = NT_KV4_BAD_SEQ;
+  if (s < 0 || s >= c.max_seqs) return make_int2(-1, 0);
+  const int len = c.len[s], n = ctx ? ctx[i] : len;
+  *bad = len < 0 || len > c.capacity() || n < 0 || n > len ? NT_KV4_BAD_LEN : 0;
+  return make_int2(*bad ? -1 : s, *bad ? 0 : n);
+}
+
 // Codes of two values, the first in the low byte.
 __device__ __forceinline__ uint32_t kv8_code2(float lo, float hi) {
   uint16_t r;

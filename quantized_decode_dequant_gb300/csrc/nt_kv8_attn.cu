@@ -116,9 +116,6 @@ __device__ __forceinline__ void kv8_mma(uint32_t d, uint64_t a, uint64_t b, uint
       "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add))
       : "memory");
 }
-__device__ __forceinline__ void kv8_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
 // this lane's row, 16 columns; awaited by kv8_tc_wait
 __device__ __forceinline__ void kv8_tc_ld16(uint32_t a, uint32_t* r) {
   asm volatile(
@@ -133,14 +130,6 @@ __device__ __forceinline__ void kv8_tc_wait(uint32_t (&r)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < N; i++) asm volatile("" : "+r"(r[i]));
-}
-__device__ __forceinline__ void kv8_tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void kv8_tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// One thread of a converged warp, known as such to the compiler.
-__device__ __forceinline__ bool kv8_elect() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r;
 }
 // (by a whole warp, the same for all of it)
 __device__ __forceinline__ bool kv8_bar_test(uint32_t bar, uint32_t parity) {
@@ -184,16 +173,6 @@ __device__ __forceinline__ float kv8_join(float (&x)[N], F f) {
 }
 template <int N>
 __device__ __forceinline__ int kv8_joined(int lane) { return lane / (32 / N); }
-
-// Sequence and positions of listed entry e (0 positions and *bad where it cannot be read).
-__device__ __forceinline__ int2 kv8_attn_entry(const Kv4& c, const Kv8AttnArgs& a, int e, uint32_t* bad) {
-  const int s = a.seq ? a.seq[e] : a.seq0 + e;
-  *bad = NT_KV4_BAD_SEQ;
-  if (s < 0 || s >= c.max_seqs) return make_int2(-1, 0);
-  const int len = c.len[s], n = a.ctx ? a.ctx[e] : len;
-  *bad = len < 0 || len > c.capacity() || n < 0 || n > len ? NT_KV4_BAD_LEN : 0;
-  return make_int2(*bad ? -1 : s, *bad ? 0 : n);
-}
 
 // Where a CTA is in the row of all tiles: tile ti of nt of kv head g of entry e.
 struct Kv8At {
@@ -250,12 +229,12 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
   int total = 0;
   if (CL) {
     uint32_t bad;
-    only = kv8_attn_entry(c, a, int(blockIdx.y) / c.n_kv, &bad);
+    only = kv8_entry(c, a.seq, a.ctx, a.seq0, int(blockIdx.y) / c.n_kv, &bad);
     if (bad && blockIdx.x == 0 && t == 0) kv4_flag(c, bad);
     total = tiles(only.y);
-    kv8_tc_before();
+    kv4_tc_before();
     __syncthreads();
-    kv8_tc_after();
+    kv4_tc_after();
   } else {
     int* sums = reinterpret_cast<int*>(sm + Cfg::kSums);
     int run = 0;
@@ -264,7 +243,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       int mine = 0;
       if (e < n) {
         uint32_t bad;
-        const int2 sl = kv8_attn_entry(c, a, e, &bad);
+        const int2 sl = kv8_entry(c, a.seq, a.ctx, a.seq0, e, &bad);
         if (bad && blockIdx.x == 0) kv4_flag(c, bad);
         entry[e] = sl;
         mine = tiles(sl.y) * c.n_kv;
@@ -289,9 +268,9 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       __syncthreads();
     }
     if (t == 0) prefix[n] = run;
-    kv8_tc_before();
+    kv4_tc_before();
     __syncthreads();
-    kv8_tc_after();
+    kv4_tc_after();
   }
   const uint32_t tmem = *tensor_memory;
   asm volatile("griddepcontrol.launch_dependents;");
@@ -421,14 +400,14 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         if (!has_k) has_k = kv8_bar_test(full + 8 * slot, uint32_t(2 * ns / H) & 1u);
         if (ok && has_k && (ns == 0 || kv8_bar_test(bar_taken, uint32_t(ns - 1) & 1u))) {
           if (info[ns % E] & (Cfg::kLacks - 1)) {
-            kv8_tc_after();
-            if (kv8_elect()) {
+            kv4_tc_after();
+            if (kv4_elect()) {
               const uint32_t k0 = smu + slot * Cfg::kSlot, q0 = smu + Cfg::kQ;
 #pragma unroll
               for (int kk = 0; kk < HD / 32; kk++)
                 kv8_mma(tmem + Cfg::kColS, kv8_desc(k0 + kk * 256, 128, 8 * HD), kv8_desc(q0 + kk * 256, 128, 8 * HD), kIdescS, kk > 0);
-              kv8_commit(bar_s);
-              kv8_commit(empty + 8 * slot);
+              kv4_tc_commit(bar_s);
+              kv4_tc_commit(empty + 8 * slot);
             }
           } else if (lane == 0) {                      // nothing to multiply: the tile goes the same way
             kv4_bar_arrive(bar_s);
@@ -455,15 +434,15 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             }
           } else if (kv8_bar_test(bar_p, uint32_t(weighed) & 1u)) {
             const bool last = !*more;
-            kv8_tc_after();
-            if (kv8_elect()) {
+            kv4_tc_after();
+            if (kv4_elect()) {
               const uint32_t v0 = smu + slot * Cfg::kSlot, p0 = smu + Cfg::kP;
 #pragma unroll
               for (int kk = 0; kk < kKv8Tile / 32; kk++)
                 kv8_mma(tmem + Cfg::kColO, kv8_desc(v0 + kk * 32 * HD, 16 * HD, 128),
                         kv8_desc(p0 + kk * 4 * Cfg::kPStep, Cfg::kPStep, 128), kIdescO, kk > 0);
-              kv8_commit(bar_o);
-              if (last) kv8_commit(empty + 8 * slot);
+              kv4_tc_commit(bar_o);
+              if (last) kv4_tc_commit(empty + 8 * slot);
             }
             __syncwarp();
             weighed++;
@@ -500,7 +479,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       pending = 2;
       const bool ok = __all_sync(0xffffffffu, kv4_bar_wait(bar_o, po));
       po ^= 1u;
-      kv8_tc_after();
+      kv4_tc_after();
       return ok;
     };
     constexpr int kTake = HB < 4 ? HB : 4;             // heads taken together
@@ -525,7 +504,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           for (int h = 0; h < kTake; h++) O[kTake * b + h] = fmaf(output(r + 8 * h), out_scale, O[kTake * b + h]);
         }
       }
-      kv8_tc_before();
+      kv4_tc_before();
     };
 
     // The q of the item at `at` into shared memory, scaled so that its largest element is in [2^7, 2^8), in six terms; a warp takes every fourth
@@ -631,7 +610,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
           if (lane == 0) kv4_bar_arrive(bar_taken);
           continue;
         }
-        kv8_tc_after();
+        kv4_tc_after();
         if (live < kKv8Tile) {   // values behind the end: zeros, whatever the page holds there
           const int vfill = 2 * no + 1;
           fail = !__all_sync(0xffffffffu, kv4_bar_wait(full + 8 * (vfill % H), uint32_t(vfill / H) & 1u)) || fail;
@@ -669,7 +648,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
             }
             kv8_tc_wait(r);
             if (b == 0) {
-              kv8_tc_before();
+              kv4_tc_before();
               __syncwarp();
               if (lane == 0) kv4_bar_arrive(bar_taken);
             }
@@ -705,7 +684,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         };
         auto multiply = [&]() {                        // the product with these digits
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          kv8_tc_before();
+          kv4_tc_before();
           __syncwarp();
           if (lane == 0) kv4_bar_arrive(bar_p);
           out_scale = kv8_exp2i(vmax - 19);            // digits are 2^-9 of themselves, weights 2^28
@@ -798,7 +777,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
                 for (int y = 0; y < 2; y++)
                   o[h + y] = fmaf(output(r + 8 * y), out_scale * kv8_exp2i(-int(__shfl_sync(0xffffffffu, up, h + y))), o[h + y]);
               }
-              kv8_tc_before();
+              kv4_tc_before();
             }
             if (lane == 0 && vmax < *vlow) *vlow = vmax;
 #pragma unroll
@@ -867,11 +846,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       if (t < HB) reinterpret_cast<float2*>(to + HB * HD)[t] = make_float2(-3e38f, 0.f);
     }
   }
-  kv8_tc_before();
+  kv4_tc_before();
   if (CL) asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   else __syncthreads();
   if (warp == 5) {
-    kv8_tc_after();
+    kv4_tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(Cfg::kCols));
   }
   if (CL) {

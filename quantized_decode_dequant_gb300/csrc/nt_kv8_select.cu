@@ -28,16 +28,6 @@ struct Kv8SelectArgs {
 __host__ __device__ __forceinline__ int64_t kv8_key_stride(const Kv4& k) { return (int64_t(k.max_pages) + 3) / 4 * 4; }
 size_t kv8_select_ws_bytes(const Kv4& k, int64_t n) { return size_t(n) * k.n_kv * kv8_key_stride(k) * 4; }
 
-// Sequence of entry i and the positions that it sees (-1: cannot be read, the bit in *bad).
-__device__ __forceinline__ int2 kv8_entry(const Kv4& c, const int32_t* seq, const int32_t* ctx, int seq0, int i, uint32_t* bad) {
-  const int s = seq ? seq[i] : seq0 + i;
-  *bad = NT_KV4_BAD_SEQ;
-  if (s < 0 || s >= c.max_seqs) return make_int2(-1, 0);
-  const int len = c.len[s], n = ctx ? ctx[i] : len;
-  *bad = len < 0 || len > c.capacity() || n < 0 || n > len ? NT_KV4_BAD_LEN : 0;
-  return make_int2(*bad ? -1 : s, *bad ? 0 : n);
-}
-
 constexpr int kKv8SelectThreads = 256;
 constexpr int kKv8ScorePages = 16;   // of a warp at a time
 constexpr int kKv8PickBins = 1024;
