@@ -29,7 +29,6 @@ nt_status kv8_check(const nt_kv8_cache* c, const char* who, bool pointers, Kv4* 
 struct __align__(16) Kv8Point {
   float c, cl, s, sl;   // cos, sin: the sums of two terms
 };
-// (`circle` below: a copy of the points in shared memory)
 struct Kv8Circle {
   Kv8Point p[256];
 };
@@ -56,7 +55,7 @@ constexpr Kv8Circle kv8_circle() {
   }
   return t;
 }
-__device__ constexpr Kv8Circle kKv8Circle = kv8_circle();
+__device__ constexpr Kv8Circle kKv8Circle = kv8_circle();   // (kernels look points up in a copy in shared memory, `circle`)
 
 // a + b in two terms (a in hi already: hi = a + b rounded)
 __device__ __forceinline__ float kv8_rest(float a, float b, float hi) {
@@ -107,7 +106,9 @@ __device__ __forceinline__ void kv8_rotate(const Kv8Point& t, float& a, float& b
   a = x;
 }
 
-// cos and sin to fp32's last bit (within 2^-24.9 of 1)
+// cos and sin in fp32, off by less than 2^-24.8 (of 1).  In units of 2^-25: the last addition rounds (1); the angle r, at most
+// pi / 256, loses the turn's lower half, 2 pi 2^-32 (0.05); rounding r, its factor and sin r, and the two inner sums of at most 2^-6 each,
+// 2^-31 (0.08 in all); cos r - 1, the series' next terms and the points' second terms are below 2^-36.  1.13, 2^-24.82.
 __device__ __forceinline__ float2 kv8_turn_fast(const Kv8Point* circle, uint64_t turn) {
   const uint32_t i = uint32_t((turn + (1ull << 55)) >> 56) & 255u;
   constexpr float k = float(6.283185307179586477 * 0x1p-32);
@@ -222,7 +223,7 @@ __device__ __forceinline__ void kv8_rotate_q(const Kv4& c, const Kv4Rows& a, con
 
 // Error of a rotated key in fp32, relative to S = |x| + |y| of its pair, in units of 2^-24: cos and sin are off by 2^-24.8, which (|a| +
 // |b|) <= sqrt(2) S multiplies (0.82); the first product rounds (|b| <= S: 1), the multiply-add (1), and the key that the format defines is rounded to
-// fp32 once itself (1); forming x 2^-e -+ d rounds (1).  4.82 2^-24 in all.
+// fp32 once itself (1); forming x 2^-e -+ d rounds (1).  4.82 2^-24 in all, where kUnsure is 5.
 constexpr float kUnsure = 0x1.4p-22f;
 
 // What the threads of an append know of their page.
@@ -328,11 +329,11 @@ __device__ __forceinline__ void kv8_load(const Kv8Mine& me, const T* from, bool 
   }
 }
 
-// Exponent that a warp's values need; an infinity or what lies beyond the largest that can be held is the caller's affair first.
+// Largest magnitude of a warp's values, NaN passed over (infinities and what lies beyond the largest that can be held are the caller's affair).
 __device__ __forceinline__ float kv8_largest(const float (&x)[32]) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));   // (a NaN is passed over)
+  for (int i = 0; i < 32; i += 2) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(x[i + 1])));
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
 
@@ -506,61 +507,61 @@ __device__ __forceinline__ void kv8_append_page(const Kv4& c, const Kv8Page& L, 
       uint32_t lo[2] = {0x7c007c00u, 0x7c007c00u}, hi[2] = {0xfc00fc00u, 0xfc00fc00u};   // bounds of this thread's positions
       uint32_t w[8] = {}, mine = me.live;                              // mine: of whose keys the codes are right
       if (busy) {
-      uint32_t z[8], differ = 0u;                                      // codes of a position's 4 dimensions, of x - d and x + d
-      const uint64_t up2 = kv8_pack(up, up), off = kv8_pack(up * kUnsure, up * kUnsure), minus = kv8_pack(up * -kUnsure, up * -kUnsure);
-      if (exact) {
+        uint32_t z[8], differ = 0u;                                      // codes of a position's 4 dimensions, of x - d and x + d
+        const uint64_t up2 = kv8_pack(up, up), off = kv8_pack(up * kUnsure, up * kUnsure), minus = kv8_pack(up * -kUnsure, up * -kUnsure);
+        if (exact) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) w[i] = z[i] = kv8_code4(x[4 * i] * up, x[4 * i + 1] * up, x[4 * i + 2] * up, x[4 * i + 3] * up);
-      } else {
+          for (int i = 0; i < 8; i++) w[i] = z[i] = kv8_code4(x[4 * i] * up, x[4 * i + 1] * up, x[4 * i + 2] * up, x[4 * i + 3] * up);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const uint64_t x02 = kv8_pack(x[4 * i], x[4 * i + 2]), x13 = kv8_pack(x[4 * i + 1], x[4 * i + 3]);
+            const uint64_t size = kv8_pack(fabsf(x[4 * i]) + fabsf(x[4 * i + 1]), fabsf(x[4 * i + 2]) + fabsf(x[4 * i + 3]));
+            const uint64_t d = kv8_mul2(size, off), md = kv8_mul2(size, minus);
+            const float2 l02 = kv8_unpack(kv8_fma2(x02, up2, md)), l13 = kv8_unpack(kv8_fma2(x13, up2, md));
+            const float2 h02 = kv8_unpack(kv8_fma2(x02, up2, d)), h13 = kv8_unpack(kv8_fma2(x13, up2, d));
+            w[i] = kv8_code4(l02.x, l13.x, l02.y, l13.y);
+            z[i] = kv8_code4(h02.x, h13.x, h02.y, h13.y);
+            differ |= w[i] ^ z[i];
+          }
+          if (differ) {
+            differ = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; i++) differ |= uint32_t(w[i] != z[i]) << i;
+          }
+        }
+        differ &= on ? me.live : 0u;                                     // (a zero of no row may differ in its sign)
+        if (__any_sync(0xffffffffu, differ != 0u)) {
+          const int more = __reduce_add_sync(0xffffffffu, __popc(differ));
+          if (steps > 1 && later + more <= 32) {
+            mine &= ~differ;
+#pragma unroll 1
+            for (int i = 0; i < 8; i++) {
+              const uint32_t m = __ballot_sync(0xffffffffu, differ >> i & 1u);
+              if (differ >> i & 1u) sh.later[t >> 5][later + __popc(m & ((1u << lane) - 1u))] = uint32_t(step << 8 | lane << 3 | i);
+              later += __popc(m);
+            }
+          } else {
+            const uint32_t again_in = __reduce_or_sync(0xffffffffu, differ);
+            float y[32];
+            kv8_exact_keys(from, me.row_stride, on ? me.live & again_in : 0u, turned, sh.circle, sh.phase + me.d0 / 2, me.pos0, y);
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+              if (on && (me.live & again_in) >> i & 1u) w[i] = kv8_code4(y[4 * i] * up, y[4 * i + 1] * up, y[4 * i + 2] * up, y[4 * i + 3] * up);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          const uint64_t x02 = kv8_pack(x[4 * i], x[4 * i + 2]), x13 = kv8_pack(x[4 * i + 1], x[4 * i + 3]);
-          const uint64_t size = kv8_pack(fabsf(x[4 * i]) + fabsf(x[4 * i + 1]), fabsf(x[4 * i + 2]) + fabsf(x[4 * i + 3]));
-          const uint64_t d = kv8_mul2(size, off), md = kv8_mul2(size, minus);
-          const float2 l02 = kv8_unpack(kv8_fma2(x02, up2, md)), l13 = kv8_unpack(kv8_fma2(x13, up2, md));
-          const float2 h02 = kv8_unpack(kv8_fma2(x02, up2, d)), h13 = kv8_unpack(kv8_fma2(x13, up2, d));
-          w[i] = kv8_code4(l02.x, l13.x, l02.y, l13.y);
-          z[i] = kv8_code4(h02.x, h13.x, h02.y, h13.y);
-          differ |= w[i] ^ z[i];
-        }
-        if (differ) {
-          differ = 0u;
+          uint32_t y[2];
+          kv8_half4(w[i], y[0], y[1]);
+          if (mine >> i & 1u) {
 #pragma unroll
-          for (int i = 0; i < 8; i++) differ |= uint32_t(w[i] != z[i]) << i;
-        }
-      }
-      differ &= on ? me.live : 0u;                                     // (a zero of no row may differ in its sign)
-      if (__any_sync(0xffffffffu, differ != 0u)) {
-        const int more = __reduce_add_sync(0xffffffffu, __popc(differ));
-        if (steps > 1 && later + more <= 32) {
-          mine &= ~differ;
-#pragma unroll 1
-          for (int i = 0; i < 8; i++) {
-            const uint32_t m = __ballot_sync(0xffffffffu, differ >> i & 1u);
-            if (differ >> i & 1u) sh.later[t >> 5][later + __popc(m & ((1u << lane) - 1u))] = uint32_t(step << 8 | lane << 3 | i);
-            later += __popc(m);
-          }
-        } else {
-          const uint32_t again_in = __reduce_or_sync(0xffffffffu, differ);
-          float y[32];
-          kv8_exact_keys(from, me.row_stride, on ? me.live & again_in : 0u, turned, sh.circle, sh.phase + me.d0 / 2, me.pos0, y);
-#pragma unroll
-          for (int i = 0; i < 8; i++)
-            if (on && (me.live & again_in) >> i & 1u) w[i] = kv8_code4(y[4 * i] * up, y[4 * i + 1] * up, y[4 * i + 2] * up, y[4 * i + 3] * up);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        uint32_t y[2];
-        kv8_half4(w[i], y[0], y[1]);
-        if (mine >> i & 1u) {
-#pragma unroll
-          for (int j = 0; j < 2; j++) {
-            lo[j] = kv8_min2(lo[j], y[j]);
-            hi[j] = kv8_max2(hi[j], y[j]);
+            for (int j = 0; j < 2; j++) {
+              lo[j] = kv8_min2(lo[j], y[j]);
+              hi[j] = kv8_max2(hi[j], y[j]);
+            }
           }
         }
-      }
       }
       const int group = t / (HD / 4);
       *reinterpret_cast<uint2*>(&sh.lo[buf][group * (HD / 2) + me.d0 / 2]) = make_uint2(lo[0], lo[1]);
