@@ -13,7 +13,7 @@
 // with 2^-25 of the largest product dropped, and truncate sums, so a tile's outputs
 // are taken out of tensor memory and added in registers.
 //   A key's exponent multiplies its scores, a value's its weight: powers of two.  What a value's exponent lies below the largest of
-// a product its weight loses in bits, so a product takes pages whose values' exponents are at most 4 apart, and a tile
+// a product its weight loses in bits, so a product takes pages whose values' exponents are at most 7 apart, and a tile
 // with others several products, in each of which the other pages' weights are zero.  In these products, and where a tile's values are
 // larger than those of a tile before, low weights may count as much as the head's largest: they are brought up to 1.  The weights are
 // 2^(score - m), m the head's largest score of the first tile, moved only where a later one passes it by
@@ -37,7 +37,10 @@ constexpr int kKv8Batch = 512;          // entries of a launch: their first tile
 constexpr int kKv8MaxCtas = 304;        // two per SM; the workspace holds two partial results of each
 constexpr int kKv8Tile = 128;
 constexpr int kKv8MaxCluster = 16;
-constexpr int kKv8Apart = 4;            // exponents of the values of a product: at most this far apart
+// Exponents of the values of a product: at most so far apart; largest ones of a tile: at most so far above a tile's before, else the
+// tile goes the rare path.  (131077 positions, 64/8 heads, us, exponents within +-2 of their own as a model's vary: apart by 4, pages of 64 65
+// and of 16 142; by 7 48.6 and 49.9, as with like ones.  All tiles on the rare path, half of the pages 2^10 larger: 148 and 203.)
+constexpr int kKv8Apart = 7, kKv8Above = 4;
 
 struct Kv8AttnArgs {
   int32_t layer, n, G, k;
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
               const int of = t < live ? t >> lg : 0, ek = exps[16 * of], ev = exps[16 * of + 1], low = *vlow;
               vmax = __reduce_max_sync(0xffffffffu, (lane & 7) << lg < live ? int(exps[16 * (lane & 7) + 1]) : -128);
               fk = kv8_exp2i(ek);
-              fv = ev < vmax - kKv8Apart || vmax > low + kKv8Apart ? 0.f : kv8_exp2i(28 + ev - vmax);
+              fv = ev < vmax - kKv8Apart || vmax > low + kKv8Above ? 0.f : kv8_exp2i(28 + ev - vmax);
               *vlow = min(vmax, low);
             }
             kv8_tc_wait(r);
@@ -738,22 +741,22 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
               fv = in ? kv8_exp2i(28 + ev - vmax) : 0.f;
               above = least;
               next = __reduce_max_sync(0xffffffffu, page < least ? page : -129);
-              float most_of = -INFINITY, up = 0.f;       // of head `lane`
-#pragma unroll 1
+              float up = 0.f;                            // of head `lane`
+              int largest = 0;
+              auto ordered = [](int y) { return y ^ (y >> 31 & 0x7fffffff); };   // numbers' bits in the order of whole numbers
+#pragma unroll 2
               for (int h = 0; h < HB; h++) {
-                float y = in ? x[h] : -INFINITY;
-#pragma unroll
-                for (int z = 16; z; z >>= 1) y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, z));
-                if (lane == h) most_of = y;
+                const int y = __reduce_max_sync(0xffffffffu, ordered(__float_as_int(in ? x[h] : -INFINITY)));
+                if (lane == h) largest = y;
               }
-              if (lane < HB) tops[warp * HB + lane] = most_of;
+              if (lane < HB) tops[warp * HB + lane] = __int_as_float(ordered(largest));
               kv8_any(false);
               if (lane < HB) {
                 const float y = fmaxf(fmaxf(tops[lane], tops[HB + lane]), fmaxf(tops[2 * HB + lane], tops[3 * HB + lane]));
                 up = fminf(fmaxf(floorf(-y), 0.f), 126.f);
               }
               __syncwarp();
-#pragma unroll 1
+#pragma unroll 2
               for (int h = 0; h < HB; h += 2) {
                 uint32_t u[2];
 #pragma unroll
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
               multiply();
               if (!await()) poison = true;
               pending = 0;
-#pragma unroll 1
+#pragma unroll 2
               for (int h = 0; h < HB && (HD == 128 || warp < 2); h += 2) {
                 uint32_t r[16];
                 kv8_tc_ld16(tmem + mine + Cfg::kColO + 8 * h, r);

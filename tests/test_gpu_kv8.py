@@ -726,8 +726,8 @@ def test_pages_whose_values_differ_by_many_powers_of_two(nt, kv, heads, hd, page
     Allowed, relative to a head's outputs: the values have mean zero and the weights' errors know nothing of them, so relative
     errors e of the weights move out = sum w V by e |V| w, independent from position to position: in the mean square by the
     root mean square of e times |out|.  e is the scores' error, 12 U of their size |q||k| (24 bits of q, the losses of 4
-    instructions, 2^-25 and 2^-23 of the largest product each, and the fp32 factors), 2^-22 of the exponential, and 2^-25 of
-    the head's largest weight for the digits (2^-29 and exponents up to 4 apart), which is 2^-25 sqrt(n / sum w^2) of out, w
+    instructions, 2^-25 and 2^-23 of the largest product each, and the fp32 factors), 2^-22 of the exponential, and 2^-22 of
+    the head's largest weight for the digits (2^-29 and exponents up to 7 apart), which is 2^-22 sqrt(n / sum w^2) of out, w
     relative to the largest; a sum of 128 loses 2^-23 of itself in each of 4 instructions and U in each fp32 addition."""
     import torch
     rng = np.random.default_rng([41, gap, hd, heads])
@@ -754,7 +754,7 @@ def test_pages_whose_values_differ_by_many_powers_of_two(nt, kv, heads, hd, page
         w = np.exp(s - s.max())
         want = R.attend(x[None], k, v)[0][0]
         dots = (np.abs(k) @ np.abs(x))[w > 1e-12].max() / hd ** 0.5
-        e = 12 * U * dots + 2.0 ** -22 + 2.0 ** -25 * (n / (w * w).sum()) ** 0.5
+        e = 12 * U * dots + 2.0 ** -22 + 2.0 ** -22 * (n / (w * w).sum()) ** 0.5
         limit = e + 4 * 2.0 ** -23 + (n / 128 + 8) ** 0.5 * U
         rel = np.linalg.norm(got[h] - want) / np.linalg.norm(want)
         assert rel <= limit, (h, rel, limit)
