@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
       at = next;
       const int count = segment(x, at);
       bool poison = dead;
-      auto cs = [&](int h) { return HB == 16 ? scales[odd * HB + h] : css[h]; };   // (16 more registers are not there)
+      auto cs = [&](int h) { return HB == 16 && HD == 128 ? scales[odd * HB + h] : css[h]; };   // (16 more registers are not there)
 #pragma unroll
       for (int h = 0; h < HB; h++) {
         css[h] = scales[odd * HB + h];
@@ -796,11 +796,11 @@ __global__ void __launch_bounds__(Kv8AttnCfg<HD, HB>::kThreads, 2) k_kv8_attn(Kv
         take();
 #pragma unroll
         for (int h = 0; h < HB; h += 2) {
-          l[h] += p[h];
-          l[h + 1] += p[h + 1];
           digits(h, __float2uint_rn(p[h] * fv), __float2uint_rn(p[h + 1] * fv));
         }
         multiply();
+#pragma unroll
+        for (int h = 0; h < HB; h++) l[h] += p[h];
       }
       // ---- the segment's end, behind the next one's q
       if (x + count < c1) {
