@@ -655,10 +655,12 @@ nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, i
  * not above the one before it, or behind a negative one, gives NaN in that entry's and kv
  * head's outputs and sets NT_KV4_BAD_PAGE.  No place at all, or no position, gives zeros.
  * Statistics and sums are fp32; codes enter exactly, q with about 24 bits.  A softmax weight is
- * held to 2^-29 of its head's largest where the values of its tile (128 positions) have one exponent, to 2^-22 where their exponents lie
- * up to 7 apart.  Where they lie further apart, or the largest is more than 4 above that of a tile before, it is held to that
- * share of the largest weight of the tile that goes with values of like size (and the tile takes about three times as long).
- * What a weight loses still counts in the divisor: n weights below 2^-29 of the largest may take up to n 2^-29 of the outputs.  Any 1 to 16 query heads per kv head
+ * held to 2^-28 of its head's largest where the values of its tile (128 positions) have one
+ * exponent, to 2^-21 where their exponents lie up to 7 apart.  Where they lie further apart, or
+ * the largest is more than 4 above that of a tile before, it is held to that share of the largest
+ * weight of the tile that goes with values of like size (and the tile takes about three times as
+ * long).  Below that a weight is kept or dropped by turns, so that the sum of many holds: n of
+ * them are off by about sqrt(n) 2^-29, not by n.  Any 1 to 16 query heads per kv head
  * (NT_E_UNSUPPORTED beyond). */
 nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
                            const int32_t* dev_ctx, int32_t n_select, const int32_t* dev_pages, const float* dev_q,
