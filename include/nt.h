@@ -659,8 +659,9 @@ nt_status nt_kv8_select(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, i
  * exponent, to 2^-21 where their exponents lie up to 7 apart.  Where they lie further apart, or
  * the largest is more than 4 above that of a tile before, it is held to that share of the largest
  * weight of the tile that goes with values of like size (and the tile takes about three times as
- * long).  Below that a weight is kept or dropped by turns, so that the sum of many holds: n of
- * them are off by about sqrt(n) 2^-29, not by n.  Any 1 to 16 query heads per kv head
+ * long for two sizes, longer for more).  Below that a weight is kept or dropped by turns, so that
+ * the sum of many holds: n of them are off by about sqrt(n) 2^-29, not by n.  Any 1 to 16 query
+ * heads per kv head
  * (NT_E_UNSUPPORTED beyond). */
 nt_status nt_attention_kv8(const nt_kv8_cache* c, int32_t layer, int32_t n_heads, int32_t n, const int32_t* dev_seq,
                            const int32_t* dev_ctx, int32_t n_select, const int32_t* dev_pages, const float* dev_q,

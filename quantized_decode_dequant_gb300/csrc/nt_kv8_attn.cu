@@ -25,9 +25,9 @@
 // Else the tiles of all items in a row go evenly to the CTAs, two per SM; an item that is cut leaves partial results for a
 // second launch.  In a CTA one warp copies, one starts products, four have a position (then a dimension) per thread.
 //
-// What bounds it: memory while it streams.  1 sequence of 131077 positions, 64/8 heads of 128, 268 MB: 47.9 us, of which 43
-// at 6.1 TB/s, the start 2, the second launch 3; 56 ragged ones, 32/8, 520 MB: 90.9; 1 with 128/8 heads: 52.6 (instructions:
-// a tile takes a CTA 1600 cycles with 8 heads a kv head).  1 of 4161: 7.9 us, a chain of length, page, tile
+// What bounds it: memory while it streams.  1 sequence of 131077 positions, 64/8 heads of 128, 268 MB: 48.5 us, of which 43
+// at 6.1 TB/s, the start 2, the second launch 3; 56 ragged ones, 32/8, 520 MB: 91.2; 1 with 128/8 heads: 52.2 (instructions:
+// a tile takes a CTA 1800 cycles with 8 heads a kv head where it comes out of L2, 1500 with 4).  1 of 4161: 8.0 us, a chain of length, page, tile
 // and q (3900 cycles to the first scores), then the cluster's merge.
 #include "nt_kv8.cuh"
 

@@ -8,8 +8,8 @@
 // |lo|, |hi| <= 127 stay below 2^24.
 //
 // What bounds it: for one long sequence latency (2049 pages, 8 kv heads, 4.5 MB: 8.0 us, of which the choice of 64 is 3.9 and
-// a launch, the table and the bounds one after the other the rest); for many, reads of 272 bytes scattered over the pool
-// (24 x 30k positions, 25 MB: 13.8 us, 1.8 TB/s).
+// a launch, the table and the bounds one after the other the rest); for many, reads of 272 bytes, which eight
+// clusters make of a page's 2176 since an item is one kv head (24 x 30k positions, 25 MB: 13.8 us, 1.8 TB/s).
 #include "nt_kv8.cuh"
 
 namespace nt {
